@@ -67,7 +67,7 @@ enum {                               /* bits of the device status word */
     MOE_DEV_TIMEOUT = 4              /* a bounded pipeline wait expired (about 1 s) */
 };
 enum { MOE_SCORING_SOFTMAX = 0, MOE_SCORING_SIGMOID = 1 };
-enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP8_BLOCK128 = 1 };
+enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP8_BLOCK128 = 1, MOE_DTYPE_MXFP4 = 2 };  /* MXFP4: moe_layer_few only */
 enum { MOE_OUT_F32 = 0, MOE_OUT_BF16 = 1 };
 enum { MOE_ACT_IDENTITY = 0, MOE_ACT_SILU_MUL = 1 };
 /* Layout of an expert weight tensor W [groups, N, K] (w13, w2):
@@ -409,6 +409,101 @@ MOE_API int moe_combine(const moe_config *cfg, int32_t T, const void *y, const i
 MOE_API int moe_workspace_size(const moe_config *cfg, size_t *bytes /* host */);
 MOE_API int moe_layer_forward(const moe_config *cfg, const moe_weights *w, int32_t T, const void *x,
                       void *out, int32_t out_dtype, void *ws, size_t ws_bytes, void *stream);
+
+/* ---- the whole layer for a few tokens ---------------------------------------------
+ * moe_layer_forward's layer for 1 to moe_layer_few_max_tokens() (16) tokens in
+ * two kernels: the gate logits (with the quantisation of x), then selection,
+ * both expert products and the combine in one persistent kernel that streams
+ * each chosen expert's weights once.  The same definition, step by step:
+ * routing ids and weights are moe_route's, bit for bit; x and h are quantised
+ * in the same places; sums are fp32 in another order, so outputs agree within
+ * the layer's tolerance and not bit for bit (a sum that lies on a rounding
+ * boundary of h may take the neighbouring code).  Outputs do not depend on
+ * timing.
+ *   cfg        as for moe_layer_forward, max_tokens 0..16 (else
+ *              MOE_ERR_UNSUPPORTED_SHAPE); dtype may also be
+ *              MOE_DTYPE_MXFP4: x and h are then quantised to MXFP4 (blocks of
+ *              32, below) and w13 / w2 are MXFP4
+ *   w          expert_layout must be MOE_LAYOUT_TILES (else
+ *              MOE_ERR_INVALID_ARG): w13 and w2 from moe_pack_expert_weights,
+ *              with the fp32 block scales in FP8; MXFP4 takes codes and scale
+ *              bytes (in the w13_scales / w2_scales pointers) from
+ *              moe_mx4_pack_weights
+ *   x bf16 [T, H], out fp32 or bf16 [T, H], 0 <= T <= max_tokens
+ *   ws         scratch of moe_layer_few_workspace_size bytes, 16-byte aligned,
+ *              one call at a time; needs no initialisation
+ * A token none of whose choices is valid gets its shared experts alone, or
+ * zeros.  The device status word is the first word of ws
+ * (moe_get_device_status). */
+MOE_API int32_t moe_layer_few_max_tokens(void);
+MOE_API int moe_layer_few_workspace_size(const moe_config *cfg, size_t *bytes /* host */);
+MOE_API int moe_layer_few(const moe_config *cfg, const moe_weights *w, int32_t T, const void *x,
+                          void *out, int32_t out_dtype, void *ws, size_t ws_bytes, void *stream);
+/* Byte offsets inside that workspace (host): topk_ids int32 [T, k] (physical,
+ * -1 where a choice was invalid) and topk_w fp32 [T, k] are what a caller may
+ * want to read; the rest are intermediates. */
+typedef struct moe_few_layout {
+    size_t status, sched, logits, topk_ids, topk_w, x16, xs, h16, hs, y, total;
+} moe_few_layout;
+MOE_API int moe_layer_few_layout(const moe_config *cfg, moe_few_layout *layout /* host */);
+
+/* ---- MXFP4 -------------------------------------------------------------------------
+ * Microscaled four-bit floating point (OCP MX, e2m1 elements): 32 consecutive
+ * elements of a row share a power of two.  With m the block's largest
+ * magnitude, e = max(floor(log2 m) - 2, -127) (0 for a block of zeros);
+ *   code  = e2m1(v / 2^e), round to nearest even, saturating at 6
+ *   scale byte = e + 127.
+ * A block holding an infinity or a NaN has the byte 255 and zero codes, and
+ * reads back as NaN.
+ *   codes  [rows, cols/2] bytes, the even element in the low four bits
+ *   scales [rows, cols/32] bytes
+ * cols a multiple of 32 (else MOE_ERR_UNSUPPORTED_SHAPE); rows may be 0; in /
+ * out fp32 or bf16 (MOE_OUT_*), pointers 16-byte aligned (scales: any). */
+MOE_API int moe_mx4_quantize(int32_t rows, int32_t cols, const void *in, int32_t in_dtype,
+                             void *codes, void *scales, void *stream);
+MOE_API int moe_mx4_dequantize(int32_t rows, int32_t cols, const void *codes, const void *scales,
+                               void *out, int32_t out_dtype, void *stream);
+
+/* Expert weights W [groups, n_out, k_dim] in MXFP4, row-major, into the tiles
+ * that the products and moe_layer_few read (same sizes, device, caller-owned,
+ * no overlap): tile (g, n/128, k/128) holds 128 rows of 64 bytes, 16-byte
+ * chunk c of row r at chunk position c ^ ((r/2) mod 4) (the 64-byte swizzle);
+ * its 512 scale bytes are at byte (r mod 32)*16 + (r/32)*4 + j for block j of
+ * row r, the order the tensor cores take them in.  n_out and k_dim multiples
+ * of 128. */
+MOE_API int moe_mx4_pack_weights(int32_t groups, int32_t n_out, int32_t k_dim, const void *codes,
+                                 const void *scales, void *codes_tiled, void *scales_tiled,
+                                 void *stream);
+
+/* ---- norms around a block ------------------------------------------------------------
+ * One pass over T rows of `hidden` elements:
+ *   n  = w_post ? norm(y) * w_post (+ b_post) : y
+ *   r' = residual_scale * residual + branch_scale * gate * n
+ *   x  = norm(r') * w_pre (+ b_pre)
+ * with norm(v) = v / sqrt(mean(v^2) + eps) (MOE_NORM_RMS) or the same of v -
+ * mean(v) (MOE_NORM_LAYER): the norm after a block, its gate and residual
+ * scale, and the norm before the next one.  fp32 inside; x is formed from the
+ * unrounded r'.
+ *   y            [T, hidden] (y_dtype) the block's output, or NULL: r' =
+ *                residual_scale * residual (a first pre-norm; gate and w_post
+ *                must then be NULL)
+ *   residual     [T, hidden] (residual_dtype); residual_out the same type, may
+ *                be `residual` itself, or NULL (not written)
+ *   gate         by gate_mode: none, [hidden], [T], or [T, hidden]
+ *   w_*, b_*, gate  param_dtype; b_* may be NULL; w_post NULL: no post-norm
+ *   x_out        bf16 [T, hidden], or NULL (then w_pre, b_pre must be NULL)
+ * hidden a multiple of 8, at most 16384; dtypes MOE_OUT_*; eps >= 0; other
+ * outputs must not overlap any input. */
+enum { MOE_NORM_RMS = 0, MOE_NORM_LAYER = 1 };
+enum { MOE_GATE_NONE = 0, MOE_GATE_FEATURE = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 };
+typedef struct moe_norm {
+    int32_t hidden, kind, y_dtype, residual_dtype, param_dtype, gate_mode;
+    float eps, residual_scale, branch_scale;
+} moe_norm;
+MOE_API int moe_block_norm(const moe_norm *d, int32_t T, const void *y, const void *residual,
+                           const void *gate, const void *w_post, const void *b_post,
+                           const void *w_pre, const void *b_pre, void *residual_out, void *x_out,
+                           void *stream);
 
 /* Byte offsets of the intermediates inside the layer workspace (host), for
  * callers that want to read routing results or rows per expert.  gate_up is

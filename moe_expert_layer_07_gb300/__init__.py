@@ -24,10 +24,15 @@ __all__ = ["Config", "Weights", "WsLayout", "lib", "make_config", "route", "rout
            "expert_ffn", "experts_forward", "expert_ffn_sched_bytes", "pack_expert_weights", "LAYOUT_ROWS",
            "LAYOUT_TILES",
            "SOFTMAX", "SIGMOID", "BF16", "FP8", "OUT_F32", "OUT_BF16", "ACT_IDENTITY",
-           "ACT_SILU_MUL"]
+           "ACT_SILU_MUL",
+           # what stands around the layer (block.py)
+           "MXFP4", "FewTokenLayer", "FewLayout", "layer_few", "layer_few_max_tokens",
+           "layer_few_workspace_size", "layer_few_layout", "mx4_quantize", "mx4_dequantize",
+           "pack_mx4_weights", "Norm", "block_norm", "NORM_RMS", "NORM_LAYER", "GATE_NONE",
+           "GATE_FEATURE", "GATE_TOKEN", "GATE_FULL"]
 
 SOFTMAX, SIGMOID = 0, 1
-BF16, FP8 = 0, 1
+BF16, FP8, MXFP4 = 0, 1, 2   # MXFP4: the few-token layer only
 OUT_F32, OUT_BF16 = 0, 1
 ACT_IDENTITY, ACT_SILU_MUL = 0, 1
 DEV_BAD_EXPERT_ID, DEV_BAD_OFFSETS, DEV_TIMEOUT = 1, 2, 4
@@ -113,7 +118,7 @@ def lib():
             raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
                               "(there is no non-CUDA fallback)")
         L = ctypes.CDLL(LIB_PATH)
-        for name, args in _SIGS.items():
+        for name, args in {**_SIGS, **block._SIGS}.items():
             fn = getattr(L, name)
             fn.argtypes = args
             fn.restype = ctypes.c_int
@@ -650,3 +655,10 @@ class ExpertRebalancer:
         """Device time of the last re-layout (waits for it)."""
         self._events[1].synchronize()
         return self._events[0].elapsed_time(self._events[1])
+
+
+from . import block  # noqa: E402  (needs the names above)
+from .block import (GATE_FEATURE, GATE_FULL, GATE_NONE, GATE_TOKEN, NORM_LAYER,  # noqa: E402
+                    NORM_RMS, FewLayout, FewTokenLayer, Norm, block_norm, layer_few,
+                    layer_few_layout, layer_few_max_tokens, layer_few_workspace_size,
+                    mx4_dequantize, mx4_quantize, pack_mx4_weights)

@@ -1,0 +1,256 @@
+"""Binding of what stands around the layer: the few-token layer, MXFP4 and the
+norms before and after a block (declared in include/moe_gb300.h).
+
+Argument marshalling only, as in the package's __init__: shapes and types are
+read off the tensors and checked against each other here, everything else by
+the library.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import (LAYOUT_ROWS, LAYOUT_TILES, MXFP4, OUT_BF16, OUT_F32, Config, Weights,
+               _check, _CP, _I, _P, _ptr, _stream, get_device_status, lib, make_config,
+               pack_expert_weights)
+
+NORM_RMS, NORM_LAYER = 0, 1
+GATE_NONE, GATE_FEATURE, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
+
+
+class FewLayout(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in
+                ("status", "sched", "logits", "topk_ids", "topk_w", "x16", "xs", "h16", "hs", "y",
+                 "total")]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("hidden", "kind", "y_dtype", "residual_dtype", "param_dtype", "gate_mode")] + \
+               [(n, ctypes.c_float) for n in ("eps", "residual_scale", "branch_scale")]
+
+
+_SIGS = {
+    "moe_layer_few_max_tokens": [],
+    "moe_layer_few_workspace_size": [_CP, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_layer_few_layout": [_CP, ctypes.POINTER(FewLayout)],
+    "moe_layer_few": [_CP, ctypes.POINTER(Weights), _I, _P, _P, _I, _P, ctypes.c_size_t, _P],
+    "moe_mx4_quantize": [_I, _I, _P, _I, _P, _P, _P],
+    "moe_mx4_dequantize": [_I, _I, _P, _P, _P, _I, _P],
+    "moe_mx4_pack_weights": [_I, _I, _I, _P, _P, _P, _P, _P],
+    "moe_block_norm": [ctypes.POINTER(Norm), _I] + [_P] * 10,
+}
+
+
+def _out_type(t) -> int:
+    """MOE_OUT_* of a tensor."""
+    import torch
+    if t.dtype == torch.float32:
+        return OUT_F32
+    if t.dtype == torch.bfloat16:
+        return OUT_BF16
+    raise TypeError(f"expected a float32 or bfloat16 tensor, got {t.dtype}")
+
+
+def _dense(t, shape, name):
+    """t itself, once it is a contiguous device tensor of this shape."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor")
+    return t
+
+
+def _bytes(t, name):
+    import torch
+    if t.dtype != torch.uint8:
+        raise TypeError(f"{name}: expected a uint8 tensor, got {t.dtype}")
+    return t
+
+
+# ---- MXFP4 ------------------------------------------------------------------------------
+
+
+def mx4_quantize(x, codes=None, scales=None, stream=None):
+    """x fp32 or bf16 [..., cols] -> (codes uint8 [..., cols/2], scales uint8 [..., cols/32])."""
+    import torch
+    cols = x.shape[-1]
+    lead = tuple(x.shape[:-1])
+    _dense(x, x.shape, "x")
+    if codes is None:
+        codes = torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty(lead + (cols // 32,), dtype=torch.uint8, device=x.device)
+    _bytes(_dense(codes, lead + (cols // 2,), "codes"), "codes")
+    _bytes(_dense(scales, lead + (cols // 32,), "scales"), "scales")
+    rows = x.numel() // cols if cols else 0
+    _check(lib().moe_mx4_quantize(rows, cols, _ptr(x), _out_type(x), _ptr(codes), _ptr(scales),
+                                  _stream(stream)), "moe_mx4_quantize")
+    return codes, scales
+
+
+def mx4_dequantize(codes, scales, out=None, stream=None):
+    """The values [..., cols] (a new bf16 tensor unless `out`, fp32 or bf16, is given)."""
+    import torch
+    cols = codes.shape[-1] * 2
+    lead = tuple(codes.shape[:-1])
+    _bytes(_dense(codes, codes.shape, "codes"), "codes")
+    _bytes(_dense(scales, lead + (cols // 32,), "scales"), "scales")
+    if out is None:
+        out = torch.empty(lead + (cols,), dtype=torch.bfloat16, device=codes.device)
+    _dense(out, lead + (cols,), "out")
+    rows = codes.numel() * 2 // cols if cols else 0
+    _check(lib().moe_mx4_dequantize(rows, cols, _ptr(codes), _ptr(scales), _ptr(out),
+                                    _out_type(out), _stream(stream)), "moe_mx4_dequantize")
+    return out
+
+
+def pack_mx4_weights(codes, scales, stream=None):
+    """Row-major MXFP4 weights (codes [G, N, K/2], scales [G, N, K/32]) -> new tensors of the
+    same shapes in the tile layout that the products and the few-token layer read."""
+    import torch
+    G, N, half = codes.shape
+    K = 2 * half
+    _bytes(_dense(codes, (G, N, half), "codes"), "codes")
+    _bytes(_dense(scales, (G, N, K // 32), "scales"), "scales")
+    w, ws = torch.empty_like(codes), torch.empty_like(scales)
+    _check(lib().moe_mx4_pack_weights(G, N, K, _ptr(codes), _ptr(scales), _ptr(w), _ptr(ws),
+                                      _stream(stream)), "moe_mx4_pack_weights")
+    return w, ws
+
+
+# ---- the layer for a few tokens ------------------------------------------------------------
+
+
+def layer_few_max_tokens() -> int:
+    return int(lib().moe_layer_few_max_tokens())
+
+
+def layer_few_workspace_size(cfg: Config) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_layer_few_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "moe_layer_few_workspace_size")
+    return n.value
+
+
+def layer_few_layout(cfg: Config) -> FewLayout:
+    L = FewLayout()
+    _check(lib().moe_layer_few_layout(ctypes.byref(cfg), ctypes.byref(L)), "moe_layer_few_layout")
+    return L
+
+
+def layer_few(cfg: Config, weights: Weights, T, x, out, out_dtype, ws, ws_bytes, stream=None):
+    _check(lib().moe_layer_few(ctypes.byref(cfg), ctypes.byref(weights), T, _ptr(x), _ptr(out),
+                               out_dtype, _ptr(ws), ws_bytes, _stream(stream)), "moe_layer_few")
+
+
+class FewTokenLayer:
+    """The MoE layer for 1 to 16 tokens a call, in two kernels.
+
+    weights as MoELayer's; for a shape whose dtype is "mxfp4", w13 / w13_s and
+    w2 / w2_s are MXFP4 codes and scale bytes as mx4_quantize gives them.
+    Row-major expert weights are packed into tiles once.  An MoELayer may be
+    passed in their place: its (packed) weights are then shared, also after it
+    gets new ones (rebalancing).
+    """
+
+    def __init__(self, shape, weights, max_tokens: int | None = None, log2phys=None):
+        import torch
+        n = layer_few_max_tokens() if max_tokens is None else max_tokens
+        self.shape = shape
+        self.cfg = make_config(shape, n)
+        if shape.dtype == "mxfp4":
+            self.cfg.dtype = MXFP4
+        self._layer = weights if not isinstance(weights, dict) else None
+        if self._layer is not None:
+            if self._layer.expert_layout != LAYOUT_TILES:
+                raise ValueError("the layer's expert weights are not packed into tiles")
+            device = self._layer.ws.device
+        else:
+            keep = {k: weights.get(k) for k in ("wg", "e_bias", "logit_offset", "w13", "w13_s",
+                                                "w2", "w2_s", "expert_layout")}
+            if keep["expert_layout"] in (None, LAYOUT_ROWS):
+                for key in ("w13", "w2"):
+                    if self.cfg.dtype == MXFP4:
+                        keep[key], keep[key + "_s"] = pack_mx4_weights(keep[key], keep[key + "_s"])
+                    else:
+                        keep[key] = pack_expert_weights(self.cfg, keep[key])
+            device = keep["w13"].device
+            keep["log2phys"] = None if log2phys is None else torch.as_tensor(
+                log2phys, dtype=torch.int32, device=device)
+            self._keep = keep
+            self._weights = Weights(
+                w_gate=_ptr(keep["wg"]), e_bias=_ptr(keep["e_bias"]),
+                logit_offset=_ptr(keep["logit_offset"]), log2phys=_ptr(keep["log2phys"]),
+                w13=_ptr(keep["w13"]), w13_scales=_ptr(keep["w13_s"]), w2=_ptr(keep["w2"]),
+                w2_scales=_ptr(keep["w2_s"]), expert_layout=LAYOUT_TILES)
+        self.layout = layer_few_layout(self.cfg)
+        self.ws_bytes = self.layout.total
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+
+    @property
+    def weights(self) -> Weights:
+        return self._layer.weights if self._layer is not None else self._weights
+
+    def forward(self, x, out, out_dtype=OUT_F32, T=None, stream=None):
+        """x bf16 [T, H] and out [T, H] (fp32 or bf16) device tensors."""
+        T = x.shape[0] if T is None else T
+        layer_few(self.cfg, self.weights, T, x, out, out_dtype, self.ws, self.ws_bytes, stream)
+        return out
+
+    def view(self, name, dtype, shape):
+        """A tensor view of one part of the workspace (topk_ids, topk_w, ...)."""
+        import math
+        import torch
+        off = getattr(self.layout, name)
+        nbytes = math.prod(shape) * torch.empty((), dtype=dtype).element_size()
+        return self.ws[off:off + nbytes].view(dtype).view(*shape)
+
+    def status(self) -> int:
+        return get_device_status(self.ws)
+
+
+# ---- norms around a block ----------------------------------------------------------------
+
+
+def block_norm(residual, y=None, residual_out=None, x_out=None, w_post=None, b_post=None,
+               w_pre=None, b_pre=None, gate=None, residual_scale=1.0, branch_scale=1.0, eps=1e-6,
+               kind=NORM_RMS, stream=None):
+    """The norm after a block, its gate and residual scale, and the norm before the next one:
+
+        n = norm(y) w_post + b_post           (y itself without w_post)
+        residual_out = residual_scale residual + branch_scale gate n
+        x_out = norm(residual_out) w_pre + b_pre
+
+    residual, y [T, H] fp32 or bf16; residual_out of residual's type (may be it), or None; x_out
+    bf16, or None; gate [H], [T] or [T, H] (for T == H a one-dimensional gate is by feature)."""
+    import torch
+    T, H = residual.shape
+    params = [t for t in (w_post, b_post, w_pre, b_pre, gate) if t is not None]
+    ptype = _out_type(params[0]) if params else OUT_BF16
+    for name, t, shape in (("residual", residual, (T, H)), ("y", y, (T, H)),
+                           ("residual_out", residual_out, (T, H)), ("x_out", x_out, (T, H)),
+                           ("w_post", w_post, (H,)), ("b_post", b_post, (H,)),
+                           ("w_pre", w_pre, (H,)), ("b_pre", b_pre, (H,))):
+        if t is not None:
+            _dense(t, shape, name)
+    if any(_out_type(t) != ptype for t in params):
+        raise TypeError("norm weights, biases and gate must share one type")
+    if residual_out is not None and residual_out.dtype != residual.dtype:
+        raise TypeError("residual_out must have residual's type")
+    if x_out is not None and x_out.dtype != torch.bfloat16:
+        raise TypeError("x_out must be bfloat16")
+    mode = GATE_NONE
+    if gate is not None:
+        mode = {(H,): GATE_FEATURE, (T, H): GATE_FULL}.get(
+            tuple(gate.shape), GATE_TOKEN if tuple(gate.shape) == (T,) else None)
+        if mode is None:
+            raise ValueError(f"gate: expected shape ({H},), ({T},) or ({T}, {H}), "
+                             f"got {tuple(gate.shape)}")
+        _dense(gate, gate.shape, "gate")
+    d = Norm(hidden=H, kind=kind, y_dtype=OUT_F32 if y is None else _out_type(y),
+             residual_dtype=_out_type(residual), param_dtype=ptype, gate_mode=mode, eps=eps,
+             residual_scale=residual_scale, branch_scale=branch_scale)
+    _check(lib().moe_block_norm(ctypes.byref(d), T, _ptr(y), _ptr(residual), _ptr(gate),
+                                _ptr(w_post), _ptr(b_post), _ptr(w_pre), _ptr(b_pre),
+                                _ptr(residual_out), _ptr(x_out), _stream(stream)),
+           "moe_block_norm")

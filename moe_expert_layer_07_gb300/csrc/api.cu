@@ -2,26 +2,14 @@
 // device status.  Every entry point validates before enqueuing anything and
 // never synchronises the host (except moe_get_device_status, which exists to).
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <cstdio>
 #include <mutex>
 
 #include "internal.h"
+#include "range.h"
 
 namespace moe {
-
-namespace {
-// An NVTX range around each entry point (and each step of the layer call),
-// so that a profiler's timeline names the library's calls; without a tool
-// attached a push/pop is a call to an empty function.
-struct Range {
-    explicit Range(const char *name) { nvtxRangePushA(name); }
-    ~Range() { nvtxRangePop(); }
-    Range(const Range &) = delete;
-    Range &operator=(const Range &) = delete;
-};
-}  // namespace
 
 namespace {
 thread_local char g_error_detail[256] = "";

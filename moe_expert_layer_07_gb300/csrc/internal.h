@@ -110,6 +110,24 @@ int launch_combine(const moe_config *cfg, int T, const void *y, const int32_t *r
                    const float *topk_w, const int32_t *offsets, void *out, int out_dtype,
                    cudaStream_t s);
 
+// The whole layer for a few tokens (few.cu); its workspace's layout.
+constexpr int kFewMaxTokens = 16;
+void few_layout(const moe_config *cfg, moe_few_layout *L);
+int launch_layer_few(const moe_config *cfg, const moe_weights *w, int T, const void *x, void *out,
+                     int out_dtype, void *ws, cudaStream_t s);
+// MXFP4 (mx4.cu)
+int launch_mx4_quantize(int64_t rows, int64_t cols, const void *in, bool f32, void *codes,
+                        void *scales, cudaStream_t s);
+int launch_mx4_dequantize(int64_t rows, int64_t cols, const void *codes, const void *scales,
+                          void *out, bool f32, cudaStream_t s);
+int launch_mx4_pack(int64_t groups, int64_t n_out, int64_t k_dim, const void *codes,
+                    const void *scales, void *codes_t, void *scales_t, cudaStream_t s);
+// Norms around a block (norm.cu)
+int launch_block_norm(const moe_norm *d, int T, const void *y, const void *residual,
+                      const void *gate, const void *w_post, const void *b_post,
+                      const void *w_pre, const void *b_pre, void *residual_out, void *x_out,
+                      cudaStream_t s);
+
 // Programmatic dependent launch: `kernel` may start while the previous
 // kernel in the stream drains.  Every CTA of such a kernel executes
 // pdl_wait() (griddepcontrol.wait) before it reads data that an earlier
