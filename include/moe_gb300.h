@@ -475,6 +475,34 @@ MOE_API int moe_mx4_pack_weights(int32_t groups, int32_t n_out, int32_t k_dim, c
                                  const void *scales, void *codes_tiled, void *scales_tiled,
                                  void *stream);
 
+/* Grouped products of MXFP4 rows and MXFP4 weights, as moe_grouped_gemm's:
+ * for every group g and row r in [expert_offsets[g], expert_offsets[g+1])
+ *   C[r, n] = sum_k A[r, k] W[g, n, k],
+ * each operand's value its code times its block's scale, products and sums
+ * in fp32 (the tensor cores' four-bit kind; the scales are powers of two).
+ *   a, a_scales  codes [rows, k_dim/2] and scale bytes [rows, k_dim/32], as
+ *                moe_mx4_quantize gives them
+ *   w, w_scales  [groups, n_out, k_dim] in tiles (moe_mx4_pack_weights)
+ *   expert_offsets device int32 [groups + 1], as in moe_grouped_gemm; rows
+ *                outside every group are not written, a table that is not
+ *                non-decreasing within [0, rows] sets MOE_DEV_BAD_OFFSETS and
+ *                nothing is computed
+ *   c            fp32 or bf16 (MOE_OUT_*) [rows, n_out]
+ * n_out and k_dim multiples of 128, groups <= 1024, pointers 16-byte aligned.
+ * The SwiGLU form takes W13 [groups, 2*inter, k_dim] (gate rows, then up rows)
+ * and writes h = silu(g) * u, formed in fp32, as MXFP4: codes [rows, inter/2],
+ * scale bytes [rows, inter/32]; inter a multiple of 128. */
+MOE_API int moe_mx4_grouped_gemm(int32_t groups, int32_t n_out, int32_t k_dim, int32_t rows,
+                                 const void *a, const void *a_scales,
+                                 const int32_t *expert_offsets, const void *w_tiled,
+                                 const void *w_scales_tiled, void *c, int32_t c_dtype,
+                                 int32_t *dev_status, void *stream);
+MOE_API int moe_mx4_grouped_gemm_swiglu(int32_t groups, int32_t inter, int32_t k_dim, int32_t rows,
+                                        const void *a, const void *a_scales,
+                                        const int32_t *expert_offsets, const void *w13_tiled,
+                                        const void *w13_scales_tiled, void *h, void *h_scales,
+                                        int32_t *dev_status, void *stream);
+
 /* ---- norms around a block ------------------------------------------------------------
  * One pass over T rows of `hidden` elements:
  *   n  = w_post ? norm(y) * w_post (+ b_post) : y

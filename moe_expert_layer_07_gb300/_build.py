@@ -19,7 +19,8 @@ LIB = os.path.join(HERE, "libmoe_gb300.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "route.cu", "quant.cu", "permute.cu", "gemm.cu", "gemm_wide.cu", "combine.cu",
            "selftest.cu", "stream_read.cu", "permute_static.cu", "rebalance.cu", "ffn.cu", "pack.cu",
-           "api_block.cu", "few.cu", "mx4.cu", "norm.cu", "balance.cpp"]
+           "api_block.cu", "few.cu", "mx4.cu", "mx4_gemm.cu",
+           "norm.cu", "balance.cpp"]
 
 
 def _nvcc() -> str:

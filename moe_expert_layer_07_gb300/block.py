@@ -37,6 +37,8 @@ _SIGS = {
     "moe_mx4_quantize": [_I, _I, _P, _I, _P, _P, _P],
     "moe_mx4_dequantize": [_I, _I, _P, _P, _P, _I, _P],
     "moe_mx4_pack_weights": [_I, _I, _I, _P, _P, _P, _P, _P],
+    "moe_mx4_grouped_gemm": [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _I, _P, _P],
+    "moe_mx4_grouped_gemm_swiglu": [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P],
     "moe_block_norm": [ctypes.POINTER(Norm), _I] + [_P] * 10,
 }
 
@@ -116,6 +118,24 @@ def pack_mx4_weights(codes, scales, stream=None):
     _check(lib().moe_mx4_pack_weights(G, N, K, _ptr(codes), _ptr(scales), _ptr(w), _ptr(ws),
                                       _stream(stream)), "moe_mx4_pack_weights")
     return w, ws
+
+
+def mx4_grouped_gemm(groups, n_out, k_dim, rows, a, a_scales, expert_offsets, w, w_scales, c,
+                     c_dtype, status=None, stream=None):
+    """C[r] = A[r] W[g]^T for the rows of each group; w, w_scales from pack_mx4_weights."""
+    _check(lib().moe_mx4_grouped_gemm(groups, n_out, k_dim, rows, _ptr(a), _ptr(a_scales),
+                                      _ptr(expert_offsets), _ptr(w), _ptr(w_scales), _ptr(c),
+                                      c_dtype, _ptr(status), _stream(stream)),
+           "moe_mx4_grouped_gemm")
+
+
+def mx4_grouped_gemm_swiglu(groups, inter, k_dim, rows, a, a_scales, expert_offsets, w13,
+                            w13_scales, h, h_scales, status=None, stream=None):
+    """The gate/up product with SwiGLU, h in MXFP4 (codes [rows, inter/2], scales [rows, inter/32])."""
+    _check(lib().moe_mx4_grouped_gemm_swiglu(groups, inter, k_dim, rows, _ptr(a), _ptr(a_scales),
+                                             _ptr(expert_offsets), _ptr(w13), _ptr(w13_scales),
+                                             _ptr(h), _ptr(h_scales), _ptr(status),
+                                             _stream(stream)), "moe_mx4_grouped_gemm_swiglu")
 
 
 # ---- the layer for a few tokens ------------------------------------------------------------

@@ -21,6 +21,15 @@ int check_few(const moe_config *cfg) {
     return c.max_tokens > kFewMaxTokens ? MOE_ERR_UNSUPPORTED_SHAPE : MOE_OK;
 }
 
+int check_mx4_gemm(int32_t groups, int32_t n_out, int32_t k_dim, int32_t rows) {
+    if (groups <= 0 || n_out <= 0 || k_dim <= 0 || rows < 0) return MOE_ERR_INVALID_ARG;
+    if (groups > 1024 || n_out % 128 || k_dim % 128) return MOE_ERR_UNSUPPORTED_SHAPE;
+    // tiles are counted in 32 bits
+    if (((int64_t)n_out + 255) / 256 * (groups + (int64_t)rows / 128 + 1) > INT32_MAX)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
 bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     const uint8_t *p = static_cast<const uint8_t *>(a), *q = static_cast<const uint8_t *>(b);
     return p && q && p < q + nb && q < p + na;
@@ -113,6 +122,41 @@ int moe_mx4_pack_weights(int32_t groups, int32_t n_out, int32_t k_dim, const voi
         return MOE_ERR_INVALID_ARG;
     return launch_mx4_pack(groups, n_out, k_dim, codes, scales, codes_tiled, scales_tiled,
                            static_cast<cudaStream_t>(stream));
+}
+
+int moe_mx4_grouped_gemm(int32_t groups, int32_t n_out, int32_t k_dim, int32_t rows, const void *a,
+                         const void *a_scales, const int32_t *expert_offsets, const void *w_tiled,
+                         const void *w_scales_tiled, void *c, int32_t c_dtype, int32_t *dev_status,
+                         void *stream) {
+    Range range("moe_mx4_grouped_gemm");
+    if (!is_float_type(c_dtype)) return MOE_ERR_INVALID_ARG;
+    if (int rc = check_mx4_gemm(groups, n_out, k_dim, rows)) return rc;
+    if (rows == 0) return MOE_OK;
+    if (!a || !a_scales || !expert_offsets || !w_tiled || !w_scales_tiled || !c)
+        return MOE_ERR_INVALID_ARG;
+    if (!al16(a) || !al16(a_scales) || !al16(w_tiled) || !al16(w_scales_tiled) || !al16(c))
+        return MOE_ERR_INVALID_ARG;
+    return launch_mx4_gemm(groups, n_out, k_dim, rows, a, a_scales, expert_offsets, w_tiled,
+                           w_scales_tiled, c, c_dtype, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+int moe_mx4_grouped_gemm_swiglu(int32_t groups, int32_t inter, int32_t k_dim, int32_t rows,
+                                const void *a, const void *a_scales, const int32_t *expert_offsets,
+                                const void *w13_tiled, const void *w13_scales_tiled, void *h,
+                                void *h_scales, int32_t *dev_status, void *stream) {
+    Range range("moe_mx4_grouped_gemm_swiglu");
+    if (inter <= 0 || inter > INT32_MAX / 2) return MOE_ERR_INVALID_ARG;
+    if (int rc = check_mx4_gemm(groups, 2 * inter, k_dim, rows)) return rc;
+    if (inter % 128) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (rows == 0) return MOE_OK;
+    if (!a || !a_scales || !expert_offsets || !w13_tiled || !w13_scales_tiled || !h || !h_scales)
+        return MOE_ERR_INVALID_ARG;
+    if (!al16(a) || !al16(a_scales) || !al16(w13_tiled) || !al16(w13_scales_tiled) || !al16(h) ||
+        !al16(h_scales))
+        return MOE_ERR_INVALID_ARG;
+    return launch_mx4_gemm_swiglu(groups, inter, k_dim, rows, a, a_scales, expert_offsets, w13_tiled,
+                                  w13_scales_tiled, h, h_scales, dev_status,
+                                  static_cast<cudaStream_t>(stream));
 }
 
 int moe_block_norm(const moe_norm *d, int32_t T, const void *y, const void *residual,

@@ -682,7 +682,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // and the encoder costs about as much host time as a kernel launch.
 // Direct-mapped; a colliding key replaces the entry.
 namespace {
-enum TmType : uint32_t { kTmU8 = 1, kTmBf16 = 2, kTmF32 = 4 };
+// element size in the low byte; kTmU8Sw64: bytes in boxes of 64, 64-byte swizzle
+enum TmType : uint32_t { kTmU8 = 1, kTmBf16 = 2, kTmF32 = 4, kTmU8Sw64 = 0x101 };
 struct TmKey {
     uint64_t base, inner, outer;
     uint32_t box_rows, type;
@@ -723,16 +724,18 @@ bool encode_rows(CUtensorMap *m, const void *base, TmType type, uint64_t inner, 
     }
     auto enc = tensor_map_encoder();
     if (!enc) return false;
-    const uint32_t esize = (uint32_t)type;
+    const uint32_t esize = (uint32_t)type & 0xffu;
+    const bool sw64 = type == kTmU8Sw64;
     cuuint64_t dims[2] = {inner, outer};
     cuuint64_t strides[1] = {inner * esize};
-    cuuint32_t box[2] = {128 / esize, box_rows};
+    cuuint32_t box[2] = {(sw64 ? 64 : 128) / esize, box_rows};
     cuuint32_t estr[2] = {1, 1};
-    const CUtensorMapDataType dt = type == kTmU8     ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+    const CUtensorMapDataType dt = esize == 1        ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : type == kTmBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
     CUresult r = enc(m, dt, 2, const_cast<void *>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     sw64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return false;
     std::lock_guard<std::mutex> lock(g_tm_mutex);
@@ -742,6 +745,11 @@ bool encode_rows(CUtensorMap *m, const void *base, TmType type, uint64_t inner, 
     return true;
 }
 }  // namespace
+
+bool encode_2d_sw64(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer,
+                    uint32_t box_rows) {
+    return encode_rows(m, base, kTmU8Sw64, inner, outer, box_rows);
+}
 
 // Row-major [outer, inner] matrix, box of 128 bytes x box_rows, 128-byte swizzle.
 bool encode_2d(CUtensorMap *m, const void *base, bool fp8, uint64_t inner, uint64_t outer,

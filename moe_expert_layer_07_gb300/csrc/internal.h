@@ -122,6 +122,14 @@ int launch_mx4_dequantize(int64_t rows, int64_t cols, const void *codes, const v
                           void *out, bool f32, cudaStream_t s);
 int launch_mx4_pack(int64_t groups, int64_t n_out, int64_t k_dim, const void *codes,
                     const void *scales, void *codes_t, void *scales_t, cudaStream_t s);
+// MXFP4 grouped products (mx4_gemm.cu), weights in tiles
+int launch_mx4_gemm(int groups, int n_out, int k_dim, int rows, const void *a, const void *a_scales,
+                    const int32_t *offsets, const void *w, const void *w_scales, void *c, int c_dtype,
+                    int32_t *status, cudaStream_t s);
+int launch_mx4_gemm_swiglu(int groups, int inter, int k_dim, int rows, const void *a,
+                           const void *a_scales, const int32_t *offsets, const void *w13,
+                           const void *w13_scales, void *h, void *h_scales, int32_t *status,
+                           cudaStream_t s);
 // Norms around a block (norm.cu)
 int launch_block_norm(const moe_norm *d, int T, const void *y, const void *residual,
                       const void *gate, const void *w_post, const void *b_post,
