@@ -19,8 +19,7 @@ GATE_NONE, GATE_FEATURE, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 
 class FewLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in
-                ("status", "sched", "logits", "topk_ids", "topk_w", "x16", "xs", "h16", "hs", "y",
-                 "total")]
+                ("status", "sched", "score", "select", "topk_ids", "topk_w", "x16", "h16", "y", "total")]
 
 
 class Norm(ctypes.Structure):

@@ -55,23 +55,26 @@ constexpr int kMaxSlots = kMaxT * 16;                   // routed slots
 constexpr int kMaxRows = kMaxSlots + kMaxT * kMaxShared;
 constexpr int kMaxGroups = kMaxSlots + kMaxShared;      // groups with rows
 
+// The token side of the scaled types, x and h: segments of 128 values of a
+// row, each code kept as the fp16 number it stands for before its scale (256
+// bytes), then the segment's scale (fp32, FP8) or four scale bytes (MXFP4).
+// Such a segment is one bulk copy.
+constexpr int kSegment = 272;
+
 enum { DT_BF16 = MOE_DTYPE_BF16, DT_FP8 = MOE_DTYPE_FP8_BLOCK128, DT_MX4 = MOE_DTYPE_MXFP4 };
 
 struct FewArgs {
     int T, H, I, E, S, k, out_bf16;
-    const uint16_t *x;          // bf16 [T, H]
     const uint8_t *w13, *w2;
     const void *w13_s, *w2_s;
-    const float *logits;
+    const float *score, *select;   // [T, E]
     int32_t *ids;
     float *wts;
-    const uint16_t *x16;        // what the products read: bf16 x, or fp16 code values
-    const void *xs;             // fp32 [T, H/128] (FP8) or scale bytes [T, H/32] (MXFP4)
-    uint16_t *h16;
-    void *hs;
-    float *y;                   // [rows, H]
+    const uint8_t *xrows;          // bf16 [T, H], or segments [T, H/128]
+    uint8_t *hrows;                // bf16 [rows, I], or segments [rows, I/128]
+    float *y;                      // [rows, H]
     void *out;
-    int32_t *sched;             // unit counter | h_done[kMaxGroups] | col_done[H/128]
+    int32_t *sched;                // unit counter | h_done[kMaxGroups] | col_done[H/128]
     int32_t *status;
 };
 
@@ -84,9 +87,9 @@ struct RouteArgs {
     int T, H, E, sched_ints, logit_blocks, dtype;
     const uint16_t *x, *wg;
     const float *offset;
-    float *logits;
-    uint16_t *x16;
-    void *xs;
+    SelectArgs sel;
+    float *score, *select;   // [T, E]: SelectArgs' scores (softmax: logits), what it compares
+    uint8_t *x16;
     int32_t *sched, *status;
     const uint8_t *pf[2];       // weights to bring into L2 (the shared experts')
     size_t pf_bytes[2];
@@ -150,11 +153,11 @@ __device__ __forceinline__ uint2 fp8_as_half4(float a, float b, float c, float d
 }
 
 // One 256-column segment of a token's row, quantised as the layer does
-// (quant_row_segment's arithmetic, or mx4.cu's), each code kept as the fp16
-// number it stands for before its scale.
+// (quant_row_segment's arithmetic, or mx4.cu's) into segments of 128 values.
 __device__ __forceinline__ void quant_segment(const RouteArgs &a, int t, int seg, int lane) {
     const int col = seg * 256 + lane * 8;
     const bool active = col < a.H;
+    uint8_t *seg_at = a.x16 + ((size_t)t * (a.H / 128) + col / 128) * kSegment;
     float f[8] = {};
     if (active) bf8(__ldg(reinterpret_cast<const uint4 *>(a.x + (size_t)t * a.H + col)), f);
     uint32_t m = 0;
@@ -172,8 +175,7 @@ __device__ __forceinline__ void quant_segment(const RouteArgs &a, int t, int seg
         for (int j = 0; j < 8; ++j) f[j] = __fdiv_rn(f[j], sc);
         const uint2 p = fp8_as_half4(f[0], f[1], f[2], f[3]), q = fp8_as_half4(f[4], f[5], f[6], f[7]);
         o = make_uint4(p.x, p.y, q.x, q.y);
-        if (active && (lane & 15) == 0)
-            static_cast<float *>(a.xs)[(size_t)t * (a.H / 128) + col / 128] = sc;
+        if (active && (lane & 15) == 0) *reinterpret_cast<float *>(seg_at + 256) = sc;
     } else {
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
@@ -181,10 +183,9 @@ __device__ __forceinline__ void quant_segment(const RouteArgs &a, int t, int seg
         uint32_t h[4];
         mx4_half8(mx4_codes8(f, byte), h);
         o = make_uint4(h[0], h[1], h[2], h[3]);
-        if (active && (lane & 3) == 0)
-            static_cast<uint8_t *>(a.xs)[(size_t)t * (a.H / 32) + col / 32] = (uint8_t)byte;
+        if (active && (lane & 3) == 0) seg_at[256 + col % 128 / 32] = (uint8_t)byte;
     }
-    if (active) *reinterpret_cast<uint4 *>(a.x16 + (size_t)t * a.H + col) = o;
+    if (active) *reinterpret_cast<uint4 *>(seg_at + col % 128 * 2) = o;
 }
 
 __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const RouteArgs a) {
@@ -219,56 +220,176 @@ __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const RouteArg
         float v = acc[t];
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
-        if (lane == t && t < nt)
-            a.logits[(size_t)(t0 + t) * a.E + e] = a.offset ? __fadd_rn(v, a.offset[e]) : v;
+        if (lane == t) acc[0] = a.offset ? __fadd_rn(v, a.offset[e]) : v;
+    }
+    if (lane < nt) {
+        const size_t at = (size_t)(t0 + lane) * a.E + e;
+        float s, c;
+        expert_scores(a.sel, e, true, acc[0], s, c);
+        a.score[at] = s;
+        a.select[at] = c;
     }
 }
 
 // ---- kernel 2 ---------------------------------------------------------------
 
-constexpr int kConsumers = 8;                         // consumer warps
-constexpr int kFfnThreads = (kConsumers + 1) * 32;    // and the producer's
+constexpr int kConsumers = 8;     // warps that multiply: 16 weight rows of a tile each
+constexpr int kProducer = kConsumers, kTokens = kProducer + 1, kFirstPublisher = kTokens + 1;
+constexpr int kPublishers = 4;
+constexpr int kWarps = kFirstPublisher + kPublishers;
+constexpr int kFfnThreads = kWarps * 32;
+constexpr int kUnitSlots = 8;     // units announced ahead
 
-template <int DT>
+template <int DT, int NT>
 struct Traits {
     // K elements of one tile, bytes of its codes and of its scales in a stage
     static constexpr int kKT = DT == DT_BF16 ? 64 : 128;
     static constexpr int kTile = DT == DT_MX4 ? 8192 : 16384;
     static constexpr int kScale = DT == DT_MX4 ? 512 : 0;
-    static constexpr int kStage = 2 * (kTile + kScale);
-    static constexpr int kStages = DT == DT_MX4 ? 11 : 6;
-    static constexpr int kBWords = DT == DT_BF16 ? 8 : 16;   // B words a lane holds for a tile
+    static constexpr int kSlot = kTile + kScale;
+    // the token side of one tile of K: 8 NT rows.  The pitch spreads the reads
+    // of a quarter warp (two rows, four chunks each) over all banks.
+    static constexpr int kCopy = DT == DT_BF16 ? 128 : kSegment;
+    static constexpr int kPitch = DT == DT_BF16 ? 192 : DT == DT_FP8 ? 272 : 320;
+    static constexpr int kTokOff = 2 * kSlot;
+    static constexpr int kTokHalf = 8 * NT * kPitch;
+    static constexpr int kWsOff = kTokOff + 2 * kTokHalf;   // FP8: the tiles' two scales
+    static constexpr int kStage = (kWsOff + 16 + 127) / 128 * 128;
+    static constexpr int kBWords = DT == DT_BF16 ? 8 : 16;  // B words a lane holds for a tile
 };
 
+template <int NT>
 struct FewShared {   // after the ring
     uint64_t full[16], empty[16];
-    uint64_t unit_full[2], unit_empty[2];
-    uint64_t sync;
-    int32_t unit[2];
+    uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
+    uint64_t res_full[2], res_empty[2], pub_sync;
+    int32_t unit[kUnitSlots];
     int abort, last, n_groups;
-    int32_t ids[kMaxSlots], slot_row[kMaxSlots], first_id[kMaxSlots];
+    int32_t ids[kMaxSlots];
     float wts[kMaxSlots];
-    int32_t group_id[kMaxGroups], group_row[kMaxGroups], group_n[kMaxGroups];
-    int32_t row_tok[kMaxRows];
-    alignas(16) float h[kMaxT][132];   // 128 features of a token; the pitch keeps the stores conflict-free
+    int16_t slot_row[kMaxSlots], first_id[kMaxSlots];
+    int16_t group_id[kMaxGroups], group_row[kMaxGroups];
+    uint8_t group_n[kMaxGroups], row_tok[kMaxRows];
+    // a unit's 128 results of each token; the pitch keeps the stores conflict-free
+    alignas(16) float res[2][8 * NT][132];
 };
 
-template <int PL>
-__device__ __noinline__ void select_tokens(const SelectArgs &a, float *sh, int warp, int lane) {
-    float *l = sh + warp * 3 * PL * 32, *s = l + PL * 32, *sel = s + PL * 32;
-    for (int t = warp; t < a.T; t += kConsumers) {
-        for (int e = lane; e < PL * 32; e += 32) {
-            const bool ok = e < a.E;
-            const float lv = ok ? a.logits[(size_t)t * a.E + e] : 0.0f;
-            float sv, selv;
-            expert_scores(a, e, ok, lv, sv, selv);
-            l[e] = lv;
-            s[e] = sv;
-            sel[e] = selv;
+// Ring stages: what fits beside FewShared in the 227 KB a CTA can have.
+template <int DT, int NT>
+struct Ring {
+    static constexpr int kFit = (227 * 1024 - (int)sizeof(FewShared<NT>)) / Traits<DT, NT>::kStage;
+    static constexpr int kStages = kFit < 16 ? kFit : 16;
+    static constexpr int kBytes = kStages * Traits<DT, NT>::kStage + (int)sizeof(FewShared<NT>);
+};
+static_assert(Ring<DT_FP8, 1>::kStages == 5 && Ring<DT_FP8, 2>::kStages == 5 &&
+              Ring<DT_MX4, 2>::kStages >= 7, "depth of the rings");
+
+// Order-preserving integers of the selection values: larger is better, 0 is
+// not selectable (NaN and minus infinity, as warp_select treats them); the two
+// zeros are equal.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    if (!(v >= -FLT_MAX)) return 0u;
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return (u >> 31) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return k == 0u ? -FLT_MAX : __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k);
+}
+
+// warp_select's choice and weights (the same bits) in rolled loops over shared
+// memory: every CTA runs this once, with a cold instruction cache, where
+// warp_select's unrolled registers took 15 us of 84 (one token, 256 experts)
+// and this takes 2.  key, score: this warp's rows of E; ids, wts: the token's
+// top_k.
+__device__ __noinline__ void few_select(const SelectArgs &a, int lane, uint32_t *key, const float *score,
+                                        int32_t *ids, float *wts) {
+    if (a.groups > 1) {
+        const int gs = a.E / a.groups;
+        float sum = 0.0f;
+        if (lane < a.groups) {   // lane g: the sum of group g's best, best first
+            uint32_t pk = 0xffffffffu;
+            int pi = -1;
+            for (int r = 0; r < a.topn; ++r) {
+                uint32_t bk = 0;
+                int bi = INT_MAX;
+#pragma unroll 4
+                for (int e = lane * gs; e < (lane + 1) * gs; ++e) {
+                    const uint32_t k = key[e];
+                    if ((k < pk || (k == pk && e > pi)) && k > bk) bk = k, bi = e;
+                }
+                sum = r == 0 ? key_value(bk) : __fadd_rn(sum, key_value(bk));
+                pk = bk;
+                pi = bi;
+            }
         }
+        const uint32_t gk = lane < a.groups ? order_key(sum) : 0u;
+        int rank = 0;
+        for (int g = 0; g < a.groups; ++g) {
+            const uint32_t o = __shfl_sync(0xffffffffu, gk, g);
+            rank += o > gk || (o == gk && g < lane);
+        }
+        const uint32_t kept = __ballot_sync(0xffffffffu, gk != 0u && rank < a.topk_groups);
         __syncwarp();
-        warp_select<PL>(a, t, lane, l, s, sel);
+        for (int e = lane; e < a.E; e += 32)
+            if (!((kept >> (e / gs)) & 1u)) key[e] = 0u;
         __syncwarp();
+    }
+    uint32_t pk = 0xffffffffu;
+    int pi = -1, my_id = 0;
+    for (int j = 0; j < a.k; ++j) {   // the next one in (value, index) order
+        uint32_t bk = 0;
+        int bi = INT_MAX;
+#pragma unroll 4
+        for (int e = lane; e < a.E; e += 32) {
+            const uint32_t k = key[e];
+            if ((k < pk || (k == pk && e > pi)) && k > bk) bk = k, bi = e;
+        }
+        pk = __reduce_max_sync(0xffffffffu, bk);
+        if (pk == 0u) {   // fewer candidates than k
+            if (lane == 0 && a.status) atomicOr(a.status, MOE_DEV_BAD_EXPERT_ID);
+            return;
+        }
+        pi = (int)__reduce_min_sync(0xffffffffu, (uint32_t)(bk == pk ? bi : INT_MAX));
+        if (lane == j) my_id = pi;
+    }
+    const float mine = score[my_id];
+    float w = 0.0f;
+    if (a.sigmoid) {
+        float total = 0.0f;
+        for (int j = 0; j < a.k; ++j) total = __fadd_rn(total, __shfl_sync(0xffffffffu, mine, j));
+        w = a.norm ? __fmul_rn(__fdiv_rn(mine, total), a.scaling) : __fmul_rn(mine, a.scaling);
+    } else {
+        float m = -FLT_MAX;
+        for (int e = lane; e < a.E; e += 32) m = fmaxf(m, score[e]);
+        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        auto ex = [&](float lv) -> double {   // as warp_select's
+            const float d = __fsub_rn(lv, m);
+            const float bb = __fsub_rn(d, lv);
+            const float e = __fadd_rn(__fsub_rn(lv, __fsub_rn(d, bb)), __fsub_rn(-m, bb));
+            const double x = (double)expf(d);
+            return fma(x, (double)e, x);
+        };
+        const double mex = ex(mine);
+        double denom = 0.0;
+        if (a.norm) {
+            for (int j = 0; j < a.k; ++j) denom += __shfl_sync(0xffffffffu, mex, j);
+        } else {
+            for (int e = lane; e < a.E; e += 32) denom += ex(score[e]);
+            for (int o = 16; o >= 1; o >>= 1) denom += __shfl_xor_sync(0xffffffffu, denom, o);
+        }
+        w = (float)(mex / denom * (double)a.scaling);
+    }
+    if (lane < a.k) {
+        int id = my_id;
+        if (a.log2phys) {
+            id = a.log2phys[my_id];
+            if (id < 0 || id >= a.E) {
+                if (a.status) atomicOr(a.status, MOE_DEV_BAD_EXPERT_ID);
+                id = -1;
+            }
+        }
+        ids[lane] = id;
+        wts[lane] = w;
     }
 }
 
@@ -290,71 +411,62 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ void e4m3_half4(uint32_t codes, uint32_t &lo, uint32_t &hi) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
         "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(lo), "=r"(hi)
+        : "=&r"(lo), "=&r"(hi)
         : "r"(codes));
 }
 
 // What a lane holds of the token side for one tile of K: the words of column
 // g of each n-tile, and (scaled types) the scales of columns 2t and 2t+1.
+// Columns past the group's rows hold what the stage held before; their
+// results are not used.
 template <int DT, int NT>
 struct TokenSide {
-    uint32_t b[NT][Traits<DT>::kBWords];
+    uint32_t b[NT][Traits<DT, NT>::kBWords];
     float s[NT][2];        // FP8
     uint32_t s4[NT][2];    // MXFP4: four scale bytes, one for each 32 of K
 };
 
-template <int DT, int NT, bool FRESH>   // FRESH: written during this kernel (past L1)
-__device__ __forceinline__ void load_tokens(TokenSide<DT, NT> &f, const uint16_t *const (&row)[NT],
-                                            const uint8_t *const (&srow)[NT][2], int kb, int t) {
-    using TR = Traits<DT>;
-    auto ld = [](const uint16_t *p) {
-        return FRESH ? __ldcg(reinterpret_cast<const uint4 *>(p))
-                     : *reinterpret_cast<const uint4 *>(p);
+template <int DT, int NT>
+__device__ __forceinline__ void load_tokens(TokenSide<DT, NT> &f, const uint8_t *rows, int g, int t) {
+    using TR = Traits<DT, NT>;
+    auto put = [](uint32_t *d, const uint8_t *p) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
     };
-    auto put = [](uint32_t *d, const uint4 v) { d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w; };
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const uint16_t *p = row[n];
-        if (p) {
-            p += (size_t)kb * TR::kKT;
-            if (DT == DT_FP8) {
+        const uint8_t *p = rows + (8 * n + g) * TR::kPitch;
+        if (DT == DT_FP8) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    put(&f.b[n][8 * h], ld(p + (t + 4 * h) * 16));
-                    put(&f.b[n][8 * h + 4], ld(p + (t + 4 * h) * 16 + 8));
-                }
-            } else if (DT == DT_BF16) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) put(&f.b[n][4 * h], ld(p + (t + 4 * h) * 8));
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) put(&f.b[n][4 * q], ld(p + q * 32 + t * 8));
+            for (int h = 0; h < 2; ++h) {
+                put(&f.b[n][8 * h], p + (t + 4 * h) * 32);
+                put(&f.b[n][8 * h + 4], p + (t + 4 * h) * 32 + 16);
             }
+        } else if (DT == DT_BF16) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) put(&f.b[n][4 * h], p + (t + 4 * h) * 16);
         } else {
 #pragma unroll
-            for (int i = 0; i < TR::kBWords; ++i) f.b[n][i] = 0;
+            for (int q = 0; q < 4; ++q) put(&f.b[n][4 * q], p + q * 64 + t * 16);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            if (DT == DT_FP8) {
-                const float *q = reinterpret_cast<const float *>(srow[n][i]) + kb;
-                f.s[n][i] = srow[n][i] ? (FRESH ? __ldcg(q) : *q) : 0.0f;
-            } else if (DT == DT_MX4) {
-                const uint32_t *q = reinterpret_cast<const uint32_t *>(srow[n][i]) + kb;
-                f.s4[n][i] = srow[n][i] ? (FRESH ? __ldcg(q) : *q) : 0x7f7f7f7fu;
-            }
+            const uint8_t *s = rows + (8 * n + 2 * t + i) * TR::kPitch + 256;
+            if (DT == DT_FP8) f.s[n][i] = *reinterpret_cast<const float *>(s);
+            else if (DT == DT_MX4) f.s4[n][i] = *reinterpret_cast<const uint32_t *>(s);
         }
     }
 }
 
 // acc += (16 weight rows of a tile in shared memory) x (the token side).
 // ra: this lane's first row of the tile (the second is ra + 8); ws: the
-// tile's scale (FP8); scales: its scale bytes in shared memory (MXFP4).
+// tile's scale (FP8).
 template <int DT, int NT>
 __device__ __forceinline__ void tile_product(float (&acc)[NT][4], const uint8_t *tile, int ra, int t,
                                              const TokenSide<DT, NT> &f, float ws, bool second) {
+    using TR = Traits<DT, NT>;
     if (DT == DT_MX4) {
-        const uint8_t *scales = tile + Traits<DT>::kTile;
+        const uint8_t *scales = tile + TR::kTile;
         const uint32_t sa4 = *reinterpret_cast<const uint32_t *>(scales + (ra & 31) * 16 + (ra >> 5) * 4);
         const int rb = ra + 8;
         const uint32_t sb4 = *reinterpret_cast<const uint32_t *>(scales + (rb & 31) * 16 + (rb >> 5) * 4);
@@ -407,8 +519,8 @@ __device__ __forceinline__ void tile_product(float (&acc)[NT][4], const uint8_t 
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     if (!n || second)
-                        mma_f16(part[n], a0, b0, a2, b2, f.b[n][8 * h + 2 * j],
-                                f.b[n][8 * h + 2 * j + 1]);
+                        mma_f16(part[n], a0, b0, a2, b2, f.b[n][(8 * h + 2 * j) % TR::kBWords],
+                                f.b[n][(8 * h + 2 * j + 1) % TR::kBWords]);
             }
         }
     }
@@ -427,21 +539,26 @@ __device__ __forceinline__ void tile_product(float (&acc)[NT][4], const uint8_t 
 template <int DT, int NT>
 __global__ void __launch_bounds__(kFfnThreads, 1)
     few_ffn_kernel(const FewArgs a, const SelectArgs sel) {
-    using TR = Traits<DT>;
+    using TR = Traits<DT, NT>;
+    constexpr int kStages = Ring<DT, NT>::kStages;
     extern __shared__ __align__(1024) uint8_t ring[];
-    FewShared &sh = *reinterpret_cast<FewShared *>(ring + TR::kStages * TR::kStage);
+    FewShared<NT> &sh = *reinterpret_cast<FewShared<NT> *>(ring + kStages * TR::kStage);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < TR::kStages; ++s) {
-            ptx::mbar_init(ptx::smem_u32(&sh.full[s]), 1);
+        for (int s = 0; s < kStages; ++s) {
+            ptx::mbar_init(ptx::smem_u32(&sh.full[s]), 2);   // the weights' thread, the tokens' warp
             ptx::mbar_init(ptx::smem_u32(&sh.empty[s]), kConsumers);
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < kUnitSlots; ++s) {
             ptx::mbar_init(ptx::smem_u32(&sh.unit_full[s]), 1);
-            ptx::mbar_init(ptx::smem_u32(&sh.unit_empty[s]), kConsumers);
+            ptx::mbar_init(ptx::smem_u32(&sh.unit_empty[s]), kWarps - 1);
         }
-        ptx::mbar_init(ptx::smem_u32(&sh.sync), kConsumers);
+        for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(ptx::smem_u32(&sh.res_full[s]), kConsumers);
+            ptx::mbar_init(ptx::smem_u32(&sh.res_empty[s]), kPublishers);
+        }
+        ptx::mbar_init(ptx::smem_u32(&sh.pub_sync), kPublishers);
         ptx::fence_mbar_init();
         sh.abort = 0;
         sh.n_groups = 0;
@@ -449,22 +566,28 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     const int slots = a.T * a.k;
     for (int i = threadIdx.x; i < slots; i += kFfnThreads) sh.ids[i] = -1;
     ptx::pdl_launch_dependents();
-    ptx::pdl_wait();   // logits, quantised x, counters
+    ptx::pdl_wait();   // scores, quantised x, counters
     __syncthreads();
 
-    // ---- selection, by every CTA for itself (scores where the ring will be) ----
-    if (warp < kConsumers) {
-        SelectArgs s = sel;
-        s.ids = sh.ids;
-        s.w = sh.wts;
-        float *buf = reinterpret_cast<float *>(ring);
-        if (s.E <= 32) select_tokens<1>(s, buf, warp, lane);
-        else if (s.E <= 64) select_tokens<2>(s, buf, warp, lane);
-        else if (s.E <= 128) select_tokens<4>(s, buf, warp, lane);
-        else if (s.E <= 256) select_tokens<8>(s, buf, warp, lane);
-        else if (s.E <= 512) select_tokens<16>(s, buf, warp, lane);
-        else select_tokens<32>(s, buf, warp, lane);
+    // ---- selection, by every CTA for itself -------------------------------------
+    int next = 0;
+    if (warp == kProducer && lane == 0) next = atomicAdd(a.sched, 1);   // the first unit
+    {   // keys and scores of a token where the ring will be
+        uint32_t *keys = reinterpret_cast<uint32_t *>(ring);
+        float *scores = reinterpret_cast<float *>(ring) + a.T * a.E;
+        for (int t = warp; t < a.T; t += kWarps) {
+            uint32_t *key = keys + t * a.E;
+            float *score = scores + t * a.E;
+#pragma unroll 4
+            for (int e = lane; e < a.E; e += 32) {
+                key[e] = order_key(a.select[(size_t)t * a.E + e]);
+                score[e] = a.score[(size_t)t * a.E + e];
+            }
+            __syncwarp();
+            few_select(sel, lane, key, score, sh.ids + t * a.k, sh.wts + t * a.k);
+        }
     }
+    ptx::fence_proxy_async_shared();   // copies write there from here on
     __syncthreads();
 
     // ---- groups with rows: shared experts, then the chosen ones by id ----------
@@ -481,7 +604,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         const int row = id >= 0 ? a.S * a.T + before + rank : -1;
         if (id >= 0) sh.row_tok[row] = i / a.k;
         sh.slot_row[i] = row;
-        sh.first_id[i] = id >= 0 && rank == 0 ? id : INT_MAX;
+        sh.first_id[i] = id >= 0 && rank == 0 ? id : INT16_MAX;
         if (blockIdx.x == 0) {
             a.ids[i] = id;
             a.wts[i] = id >= 0 ? sh.wts[i] : 0.0f;
@@ -490,7 +613,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     __syncthreads();
     for (int i = threadIdx.x; i < slots; i += kFfnThreads) {
         const int id = sh.first_id[i];
-        if (id == INT_MAX) continue;
+        if (id == INT16_MAX) continue;
         int place = a.S, n = 0;   // distinct chosen experts below; this one's rows
         for (int j = 0; j < slots; ++j) {
             place += sh.first_id[j] < id;
@@ -507,7 +630,6 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         sh.group_row[threadIdx.x] = threadIdx.x * a.T;
         sh.group_n[threadIdx.x] = a.T;
     }
-    ptx::fence_proxy_async_shared();   // the scores' place is written by copies from here on
     __syncthreads();
 
     const int nG = sh.n_groups + a.S;
@@ -527,236 +649,247 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         return;
     }
 
-    if (warp == kConsumers) {
-        // ---- producer ------------------------------------------------------------
+    // What a unit number stands for.
+    struct Unit {
+        bool gu;
+        int gi, tile, kb, steps;   // gate/up: a stage is one K tile of both blocks; down: two K tiles
+    };
+    auto unit_of = [&](int u) {
+        Unit r;
+        r.gu = u < u1;
+        const int v = r.gu ? u : u - u1, per = r.gu ? mt1 : nb2;
+        r.gi = v / per;
+        r.tile = v % per;
+        r.kb = r.gu ? kb1 : kb2;
+        r.steps = r.gu ? r.kb : (r.kb + 1) / 2;
+        return r;
+    };
+    // The it-th unit of this CTA (-1: no more), as every warp but the producer
+    // reads it; -2 after a wait that gave up.
+    auto take_unit = [&](int it) {
+        const int slot = it % kUnitSlots;
+        const bool ok = ptx::wait_bounded(ptx::smem_u32(&sh.unit_full[slot]), (it / kUnitSlots) & 1,
+                                          abort_flag, a.status, MOE_DEV_TIMEOUT);
+        if (!__all_sync(0xffffffffu, ok)) return -2;
+        const int u = *reinterpret_cast<volatile int32_t *>(&sh.unit[slot]);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.unit_empty[slot]));
+        return u;
+    };
+
+    if (warp == kProducer) {
+        // ---- weights -------------------------------------------------------------
         if (lane) return;
         const uint64_t policy = ptx::policy_evict_first();
         int issued = 0;
         bool ok = true;
-        int next = atomicAdd(a.sched, 1);
         for (int it = 0; ok; ++it) {
-            const int u = next;
-            const int slot = it & 1;
-            if (!ptx::wait_bounded(ptx::smem_u32(&sh.unit_empty[slot]), ((it >> 1) & 1) ^ 1,
+            const int u = next, slot = it % kUnitSlots;
+            if (!ptx::wait_bounded(ptx::smem_u32(&sh.unit_empty[slot]), ((it / kUnitSlots) & 1) ^ 1,
                                    abort_flag, a.status, MOE_DEV_TIMEOUT))
                 break;
             sh.unit[slot] = u < units ? u : -1;
             ptx::mbar_arrive(ptx::smem_u32(&sh.unit_full[slot]));
             if (u >= units) break;
-            next = atomicAdd(a.sched, 1);
-            const bool gu = u < u1;
-            const int v = gu ? u : u - u1, per = gu ? mt1 : nb2;
-            const int gi = v / per, tile = v % per, kb = gu ? kb1 : kb2;
-            const size_t g = sh.group_id[gi];
+            const Unit un = unit_of(u);
+            const size_t g = sh.group_id[un.gi];
             // tiles of a block of 128 weight rows are consecutive along K
-            const size_t b0 = gu ? (g * 2 * mt1 + tile) * kb : (g * nb2 + tile) * kb;
-            const size_t b1 = b0 + (size_t)mt1 * kb;   // the matching up rows
-            const uint8_t *w = gu ? a.w13 : a.w2;
-            const uint8_t *ws = static_cast<const uint8_t *>(gu ? a.w13_s : a.w2_s);
-            const int steps = gu ? kb : (kb + 1) / 2;
-            for (int s = 0; s < steps; ++s) {
-                const int st = issued % TR::kStages;
+            const size_t b0 = un.gu ? (g * 2 * mt1 + un.tile) * un.kb : (g * nb2 + un.tile) * un.kb;
+            const size_t b1 = b0 + (size_t)mt1 * un.kb;   // the matching up rows
+            const uint8_t *w = un.gu ? a.w13 : a.w2;
+            const uint8_t *ws = static_cast<const uint8_t *>(un.gu ? a.w13_s : a.w2_s);
+            for (int s = 0; s < un.steps; ++s) {
+                const int st = issued % kStages;
                 const uint32_t full = ptx::smem_u32(&sh.full[st]);
-                if (!ptx::wait_bounded(ptx::smem_u32(&sh.empty[st]), ((issued / TR::kStages) & 1) ^ 1,
+                if (!ptx::wait_bounded(ptx::smem_u32(&sh.empty[st]), ((issued / kStages) & 1) ^ 1,
                                        abort_flag, a.status, MOE_DEV_TIMEOUT)) {
                     ok = false;
                     break;
                 }
                 const uint32_t dst = ptx::smem_u32(ring + st * TR::kStage);
-                constexpr uint32_t kSlot = TR::kTile + TR::kScale;
-                const size_t i0 = gu ? b0 + s : b0 + 2 * s, i1 = gu ? b1 + s : i0 + 1;
-                const bool two = gu || 2 * s + 1 < kb;
-                ptx::mbar_arrive_expect_tx(full, two ? 2 * kSlot : kSlot);
+                const size_t i0 = un.gu ? b0 + s : b0 + 2 * s, i1 = un.gu ? b1 + s : i0 + 1;
+                const bool two = un.gu || 2 * s + 1 < un.kb;
+                ptx::mbar_arrive_expect_tx(full, two ? 2 * TR::kSlot : TR::kSlot);
                 ptx::bulk_load(dst, w + i0 * TR::kTile, TR::kTile, full, policy);
                 if (TR::kScale) ptx::bulk_load(dst + TR::kTile, ws + i0 * TR::kScale, TR::kScale, full, policy);
                 if (two) {
-                    ptx::bulk_load(dst + kSlot, w + i1 * TR::kTile, TR::kTile, full, policy);
+                    ptx::bulk_load(dst + TR::kSlot, w + i1 * TR::kTile, TR::kTile, full, policy);
                     if (TR::kScale)
-                        ptx::bulk_load(dst + kSlot + TR::kTile, ws + i1 * TR::kScale, TR::kScale, full, policy);
+                        ptx::bulk_load(dst + TR::kSlot + TR::kTile, ws + i1 * TR::kScale, TR::kScale, full, policy);
                 }
                 ++issued;
             }
+            // claimed only now: a unit claimed ahead would wait behind this one
+            // while another CTA is idle.  The ring covers the counter's latency.
+            next = atomicAdd(a.sched, 1);
         }
         // no copy may still be writing when the CTA's shared memory is given up
-        for (int i = max(0, issued - TR::kStages); i < issued; ++i)
-            ptx::wait_drain(ptx::smem_u32(&sh.full[i % TR::kStages]), (i / TR::kStages) & 1);
+        for (int i = max(0, issued - kStages); i < issued; ++i)
+            ptx::wait_drain(ptx::smem_u32(&sh.full[i % kStages]), (i / kStages) & 1);
         return;
     }
 
-    // ---- consumers -----------------------------------------------------------------
-    const int g8 = lane >> 2, t4 = lane & 3;
-    const int ra = warp * 16 + ((g8 >> 1) | ((g8 & 1) << 2));   // this lane's rows ra, ra + 8
-    uint32_t sync_parity = 0;
-    auto consumer_sync = [&]() -> bool {   // all consumer warps; bounded
-        __syncwarp();
-        const uint32_t bar = ptx::smem_u32(&sh.sync);
-        if (lane == 0) ptx::mbar_arrive(bar);
-        const bool ok = ptx::wait_bounded(bar, sync_parity, abort_flag, a.status, MOE_DEV_TIMEOUT);
-        sync_parity ^= 1;
-        return __all_sync(0xffffffffu, ok);
-    };
-    int stage = 0;   // stages consumed so far
-    bool ok = true;
-    for (int it = 0; ok; ++it) {
-        const int slot = it & 1;
-        ok = ptx::wait_bounded(ptx::smem_u32(&sh.unit_full[slot]), (it >> 1) & 1, abort_flag, a.status,
-                               MOE_DEV_TIMEOUT);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        const int u = *reinterpret_cast<volatile int32_t *>(&sh.unit[slot]);
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.unit_empty[slot]));
-        if (u < 0) break;
-        const bool gu = u < u1;
-        const int v = gu ? u : u - u1, per = gu ? mt1 : nb2;
-        const int gi = v / per, tile = v % per, kb = gu ? kb1 : kb2;
-        const int g = sh.group_id[gi], row0 = sh.group_row[gi], n = sh.group_n[gi];
-        const bool second = NT > 1 && n > 8;
-
-        // the token side's rows: column 8 j + g8 of the MMA, scales of 2 t4 (+1)
-        const uint16_t *rows[NT];
-        const uint8_t *srows[NT][2];
-        const uint16_t *src = gu ? a.x16 : a.h16;
-        const uint8_t *ssrc = static_cast<const uint8_t *>(gu ? a.xs : a.hs);
-        const int K = gu ? a.H : a.I, spitch = K / 32;   // bytes of scales a row, FP8 too
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            auto at = [&](int c) { return gu ? sh.row_tok[row0 + c] : row0 + c; };
-            rows[j] = 8 * j + g8 < n ? src + (size_t)at(8 * j + g8) * K : nullptr;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int c = 8 * j + 2 * t4 + i;
-                srows[j][i] = DT != DT_BF16 && c < n ? ssrc + (size_t)at(c) * spitch : nullptr;
-            }
-        }
-        // FP8: the weight scales of the unit's row blocks, K block i in lane i mod 32
-        float wsc[2][2] = {};
-        if (DT == DT_FP8) {
-            const float *s0 = static_cast<const float *>(gu ? a.w13_s : a.w2_s) +
-                              (gu ? ((size_t)g * 2 * mt1 + tile) * kb : ((size_t)g * nb2 + tile) * kb);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (lane + 32 * i < kb) {
-                    wsc[0][i] = __ldg(s0 + lane + 32 * i);
-                    if (gu) wsc[1][i] = __ldg(s0 + (size_t)mt1 * kb + lane + 32 * i);
-                }
-        }
-        if (!gu) {   // the group's h: all its units, from whichever CTAs
-            ok = lane ? true
-                      : ptx::wait_flag_geq(h_done + gi, mt1, abort_flag, a.status, MOE_DEV_TIMEOUT);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-        }
-        float acc[2][NT][4] = {};
-        TokenSide<DT, NT> cur, nxt;
-        auto load = [&](TokenSide<DT, NT> &f, int i) {
-            if (gu) load_tokens<DT, NT, false>(f, rows, srows, i, t4);
-            else load_tokens<DT, NT, true>(f, rows, srows, i, t4);
-        };
-        load(cur, 0);
-        for (int i = 0; i < kb; ++i) {
-            if (i + 1 < kb) load(nxt, i + 1);
-            const int st = stage % TR::kStages;
-            const int half = gu ? 0 : i & 1;   // a down stage holds two K tiles
-            if (half == 0) {
-                ok = ptx::wait_bounded(ptx::smem_u32(&sh.full[st]), (stage / TR::kStages) & 1, abort_flag,
-                                       a.status, MOE_DEV_TIMEOUT);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
-            }
-            constexpr int kSlot = TR::kTile + TR::kScale;
-            const uint8_t *base = ring + st * TR::kStage;
-            float w0 = 0.0f, w1 = 0.0f;
+    if (warp == kTokens) {
+        // ---- the token side: x, or h once it is complete ------------------------------
+        const uint64_t policy = ptx::policy_evict_last();
+        ptx::fence_proxy_async_global();   // x's segments were written by another kernel
+        int stage = 0;
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            const int u = take_unit(it);
+            if (u < 0) break;
+            const Unit un = unit_of(u);
+            const int g = sh.group_id[un.gi], row0 = sh.group_row[un.gi], n = sh.group_n[un.gi];
+            // FP8: the weight scales of the unit's row blocks, K tile i in lane i mod 32
+            float wsc[2][2] = {};
             if (DT == DT_FP8) {
-                w0 = __shfl_sync(0xffffffffu, i < 32 ? wsc[0][0] : wsc[0][1], i & 31);
-                w1 = __shfl_sync(0xffffffffu, i < 32 ? wsc[1][0] : wsc[1][1], i & 31);
+                const float *s0 = static_cast<const float *>(un.gu ? a.w13_s : a.w2_s) +
+                                  (un.gu ? ((size_t)g * 2 * mt1 + un.tile) * un.kb
+                                         : ((size_t)g * nb2 + un.tile) * un.kb);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (lane + 32 * i < un.kb) {
+                        wsc[0][i] = __ldg(s0 + lane + 32 * i);
+                        if (un.gu) wsc[1][i] = __ldg(s0 + (size_t)mt1 * un.kb + lane + 32 * i);
+                    }
             }
-            tile_product<DT, NT>(acc[0], base + half * kSlot, ra, t4, cur, w0, second);
-            if (gu) tile_product<DT, NT>(acc[1], base + kSlot, ra, t4, cur, w1, second);
-            if (gu || half == 1 || i + 1 == kb) {
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.empty[st]));
-                ++stage;
+            if (!un.gu) {   // all units of the group's h, from whichever CTAs
+                ok = lane ? true
+                          : ptx::wait_flag_geq(h_done + un.gi, mt1, abort_flag, a.status, MOE_DEV_TIMEOUT);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ptx::fence_proxy_async_global();
             }
-            cur = nxt;
+            // this lane copies row `lane` (its segment of each K tile is contiguous)
+            const int r = lane % (8 * NT), half = lane / (8 * NT);
+            const uint8_t *src = nullptr;
+            if (r < n && half < 2)
+                src = un.gu ? a.xrows + (size_t)sh.row_tok[row0 + r] * un.kb * TR::kCopy
+                            : a.hrows + (size_t)(row0 + r) * un.kb * TR::kCopy;
+            for (int s = 0; s < un.steps; ++s, ++stage) {
+                const int st = stage % kStages;
+                const uint32_t full = ptx::smem_u32(&sh.full[st]);
+                ok = ptx::wait_bounded(ptx::smem_u32(&sh.empty[st]), ((stage / kStages) & 1) ^ 1, abort_flag,
+                                       a.status, MOE_DEV_TIMEOUT);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                uint8_t *base = ring + st * TR::kStage;
+                const int k0 = un.gu ? s : 2 * s, nk = un.gu ? 1 : min(2, un.kb - k0);
+                if (DT == DT_FP8) {
+                    const int k1 = un.gu ? k0 : min(k0 + 1, un.kb - 1);
+                    const float w0 = __shfl_sync(0xffffffffu, k0 < 32 ? wsc[0][0] : wsc[0][1], k0 & 31);
+                    const float o0 = __shfl_sync(0xffffffffu, k1 < 32 ? wsc[0][0] : wsc[0][1], k1 & 31);
+                    const float o1 = __shfl_sync(0xffffffffu, k1 < 32 ? wsc[1][0] : wsc[1][1], k1 & 31);
+                    if (lane == 0)
+                        *reinterpret_cast<float2 *>(base + TR::kWsOff) = make_float2(w0, un.gu ? o1 : o0);
+                }
+                if (lane == 0) ptx::mbar_arrive_expect_tx(full, n * nk * TR::kCopy);
+                __syncwarp();   // the bytes are announced before any copy lands
+                if (src && half < nk)
+                    ptx::bulk_load(ptx::smem_u32(base + TR::kTokOff + half * TR::kTokHalf + r * TR::kPitch),
+                                   src + (size_t)(k0 + half) * TR::kCopy, TR::kCopy, full, policy);
+            }
         }
-        if (!ok) break;
+        if (lane == 0)   // as the producer: no copy may outlive the CTA
+            for (int i = max(0, stage - kStages); i < stage; ++i)
+                ptx::wait_drain(ptx::smem_u32(&sh.full[i % kStages]), (i / kStages) & 1);
+        return;
+    }
 
-        if (gu) {
-            // h = silu(gate) up: to shared memory, then quantised by token
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = 8 * j + 2 * t4 + (i & 1);
-                    if (c < n) sh.h[c][ra + (i & 2) * 4] = silu_mul(acc[0][j][i], acc[1][j][i]);
-                }
-            if (!(ok = consumer_sync())) break;
-            for (int c = warp; c < n; c += kConsumers) {
-                const float4 q = *reinterpret_cast<const float4 *>(&sh.h[c][lane * 4]);
-                uint2 o;
+    if (warp >= kFirstPublisher) {
+        // ---- results: h to its format and to memory, y to memory, the combine --------
+        const int pw = warp - kFirstPublisher;
+        uint32_t parity = 0;
+        auto pub_sync = [&]() -> bool {   // all publishers; bounded
+            __syncwarp();
+            const uint32_t bar = ptx::smem_u32(&sh.pub_sync);
+            if (lane == 0) ptx::mbar_arrive(bar);
+            const bool ok = ptx::wait_bounded(bar, parity, abort_flag, a.status, MOE_DEV_TIMEOUT);
+            parity ^= 1;
+            return __all_sync(0xffffffffu, ok);
+        };
+        for (int it = 0;; ++it) {
+            const int u = take_unit(it);
+            if (u < 0) break;
+            const Unit un = unit_of(u);
+            const int row0 = sh.group_row[un.gi], n = sh.group_n[un.gi], buf = it & 1;
+            const bool ok = ptx::wait_bounded(ptx::smem_u32(&sh.res_full[buf]), (it >> 1) & 1, abort_flag,
+                                              a.status, MOE_DEV_TIMEOUT);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            for (int c = pw; c < n; c += kPublishers) {
+                const float4 q = *reinterpret_cast<const float4 *>(&sh.res[buf][c][lane * 4]);
                 const size_t row = row0 + c;
-                if (DT == DT_BF16) {
+                if (!un.gu) {
+                    *reinterpret_cast<float4 *>(a.y + row * a.H + un.tile * 128 + lane * 4) = q;
+                } else if (DT == DT_BF16) {
                     __nv_bfloat162 b0 = __floats2bfloat162_rn(q.x, q.y), b1 = __floats2bfloat162_rn(q.z, q.w);
-                    o = make_uint2(*reinterpret_cast<uint32_t *>(&b0), *reinterpret_cast<uint32_t *>(&b1));
-                } else if (DT == DT_FP8) {
-                    float m = fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)), fmaxf(fabsf(q.z), fabsf(q.w)));
-#pragma unroll
-                    for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                    const float sc = fp8_group_scale(m), inv = fp8_group_inv(sc);
-                    o = fp8_as_half4(__fmul_rn(q.x, inv), __fmul_rn(q.y, inv), __fmul_rn(q.z, inv),
-                                     __fmul_rn(q.w, inv));
-                    if (lane == 0) static_cast<float *>(a.hs)[row * mt1 + tile] = sc;
+                    *reinterpret_cast<uint2 *>(a.hrows + (row * a.I + un.tile * 128 + lane * 4) * 2) =
+                        make_uint2(*reinterpret_cast<uint32_t *>(&b0), *reinterpret_cast<uint32_t *>(&b1));
                 } else {
-                    uint32_t m = max(max(__float_as_uint(q.x) & 0x7fffffffu, __float_as_uint(q.y) & 0x7fffffffu),
-                                     max(__float_as_uint(q.z) & 0x7fffffffu, __float_as_uint(q.w) & 0x7fffffffu));
+                    uint8_t *seg = a.hrows + (row * mt1 + un.tile) * kSegment;
+                    uint2 o;
+                    if (DT == DT_FP8) {
+                        float m = fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)), fmaxf(fabsf(q.z), fabsf(q.w)));
 #pragma unroll
-                    for (int d = 4; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-                    const uint32_t byte = mx4_scale_byte(m);
-                    o = byte == 255u ? make_uint2(0u, 0u)
-                                     : mx4_as_half4(q.x, q.y, q.z, q.w, mx4_inv_scale(byte));
-                    if ((lane & 7) == 0)
-                        static_cast<uint8_t *>(a.hs)[row * (a.I / 32) + tile * 4 + lane / 8] = (uint8_t)byte;
+                        for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                        const float sc = fp8_group_scale(m), inv = fp8_group_inv(sc);
+                        o = fp8_as_half4(__fmul_rn(q.x, inv), __fmul_rn(q.y, inv), __fmul_rn(q.z, inv),
+                                         __fmul_rn(q.w, inv));
+                        if (lane == 0) *reinterpret_cast<float *>(seg + 256) = sc;
+                    } else {
+                        uint32_t m = max(max(__float_as_uint(q.x) & 0x7fffffffu, __float_as_uint(q.y) & 0x7fffffffu),
+                                         max(__float_as_uint(q.z) & 0x7fffffffu, __float_as_uint(q.w) & 0x7fffffffu));
+#pragma unroll
+                        for (int d = 4; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+                        const uint32_t byte = mx4_scale_byte(m);
+                        o = byte == 255u ? make_uint2(0u, 0u)
+                                         : mx4_as_half4(q.x, q.y, q.z, q.w, mx4_inv_scale(byte));
+                        if ((lane & 7) == 0) seg[256 + lane / 8] = (uint8_t)byte;
+                    }
+                    *reinterpret_cast<uint2 *>(seg + lane * 8) = o;
                 }
-                *reinterpret_cast<uint2 *>(a.h16 + row * a.I + tile * 128 + lane * 4) = o;
             }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.res_empty[buf]));
+            if (un.gu) ptx::fence_proxy_async_global();   // h is read by copies
             __threadfence();
-            if (!(ok = consumer_sync())) break;   // every warp's rows are out; sh.h is free
-            if (threadIdx.x == 0) ptx::red_release_gpu_add(h_done + gi, 1);
-        } else {
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = 8 * j + 2 * t4 + (i & 1);
-                    if (c < n) a.y[(size_t)(row0 + c) * a.H + tile * 128 + ra + (i & 2) * 4] = acc[0][j][i];
-                }
-            __threadfence();
-            if (!(ok = consumer_sync())) break;
-            if (threadIdx.x == 0) {
-                sh.last = atomicAdd(col_done + tile, 1) == nG - 1;
+            if (!pub_sync()) break;   // every publisher's rows are out
+            if (un.gu) {
+                if (pw == 0 && lane == 0) ptx::red_release_gpu_add(h_done + un.gi, 1);
+                continue;
+            }
+            if (pw == 0 && lane == 0) {
+                sh.last = atomicAdd(col_done + un.tile, 1) == nG - 1;
                 __threadfence();
             }
-            if (!(ok = consumer_sync())) break;
-            if (!sh.last) continue;
+            if (!pub_sync()) break;
+            if (!*reinterpret_cast<volatile int *>(&sh.last)) continue;
             // all groups' rows of these columns are there: the combine
-            for (int i = threadIdx.x; i < a.T * 32; i += kConsumers * 32) {
+            for (int i = pw * 32 + lane; i < a.T * 32; i += kPublishers * 32) {
                 const int t = i >> 5;
-                const size_t col = tile * 128 + (i & 31) * 4;
+                const size_t col = un.tile * 128 + (i & 31) * 4;
                 float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                const float *y = a.y + col;
                 for (int s = 0; s < a.S; ++s) {
-                    const float4 r = __ldcg(reinterpret_cast<const float4 *>(a.y + (size_t)(s * a.T + t) * a.H + col));
+                    const float4 r = __ldcg(reinterpret_cast<const float4 *>(y + (size_t)(s * a.T + t) * a.H));
                     o.x = __fadd_rn(o.x, r.x), o.y = __fadd_rn(o.y, r.y);
                     o.z = __fadd_rn(o.z, r.z), o.w = __fadd_rn(o.w, r.w);
                 }
-                for (int j = 0; j < a.k; ++j) {
-                    const int row = sh.slot_row[t * a.k + j];
-                    if (row < 0) continue;
-                    const float w = sh.wts[t * a.k + j];
-                    const float4 r = __ldcg(reinterpret_cast<const float4 *>(a.y + (size_t)row * a.H + col));
-                    o.x = fmaf(w, r.x, o.x), o.y = fmaf(w, r.y, o.y);
-                    o.z = fmaf(w, r.z, o.z), o.w = fmaf(w, r.w, o.w);
+                for (int j0 = 0; j0 < a.k; j0 += 8) {   // eight rows' loads, then their sums in order
+                    float4 r[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int row = j0 + j < a.k ? sh.slot_row[t * a.k + j0 + j] : -1;
+                        r[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (row >= 0) r[j] = __ldcg(reinterpret_cast<const float4 *>(y + (size_t)row * a.H));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if (j0 + j >= a.k || sh.slot_row[t * a.k + j0 + j] < 0) continue;
+                        const float w = sh.wts[t * a.k + j0 + j];
+                        o.x = fmaf(w, r[j].x, o.x), o.y = fmaf(w, r[j].y, o.y);
+                        o.z = fmaf(w, r[j].z, o.z), o.w = fmaf(w, r[j].w, o.w);
+                    }
                 }
                 const size_t at = (size_t)t * a.H + col;
                 if (a.out_bf16) {
@@ -768,13 +901,65 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 }
             }
         }
+        return;
+    }
+
+    // ---- products -------------------------------------------------------------------
+    const int g8 = lane >> 2, t4 = lane & 3;
+    const int ra = warp * 16 + ((g8 >> 1) | ((g8 & 1) << 2));   // this lane's rows ra, ra + 8
+    int stage = 0;   // stages consumed so far
+    bool ok = true;
+    for (int it = 0; ok; ++it) {
+        const int u = take_unit(it);
+        if (u < 0) break;
+        const Unit un = unit_of(u);
+        const int n = sh.group_n[un.gi];
+        const bool second = NT > 1 && n > 8;
+        float acc[2][NT][4] = {};
+        for (int s = 0; s < un.steps; ++s, ++stage) {
+            const int st = stage % kStages;
+            ok = ptx::wait_bounded(ptx::smem_u32(&sh.full[st]), (stage / kStages) & 1, abort_flag, a.status,
+                                   MOE_DEV_TIMEOUT);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint8_t *base = ring + st * TR::kStage;
+            float2 ws = make_float2(0.0f, 0.0f);
+            if (DT == DT_FP8) ws = *reinterpret_cast<const float2 *>(base + TR::kWsOff);
+            TokenSide<DT, NT> f;
+            load_tokens<DT, NT>(f, base + TR::kTokOff, g8, t4);
+            tile_product<DT, NT>(acc[0], base, ra, t4, f, ws.x, second);
+            if (un.gu) {
+                tile_product<DT, NT>(acc[1], base + TR::kSlot, ra, t4, f, ws.y, second);
+            } else if (2 * s + 1 < un.kb) {
+                load_tokens<DT, NT>(f, base + TR::kTokOff + TR::kTokHalf, g8, t4);
+                tile_product<DT, NT>(acc[0], base + TR::kSlot, ra, t4, f, ws.y, second);
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.empty[st]));
+        }
+        if (!ok) break;
+        const int buf = it & 1;
+        ok = ptx::wait_bounded(ptx::smem_u32(&sh.res_empty[buf]), ((it >> 1) & 1) ^ 1, abort_flag, a.status,
+                               MOE_DEV_TIMEOUT);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = 8 * j + 2 * t4 + (i & 1);
+                if (c < n)
+                    sh.res[buf][c][ra + (i & 2) * 4] =
+                        un.gu ? silu_mul(acc[0][j][i], acc[1][j][i]) : acc[0][j][i];
+            }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.res_full[buf]));
     }
 }
 
 template <int DT, int NT>
 int launch_ffn(const FewArgs &a, const SelectArgs &sel, cudaStream_t s) {
-    using TR = Traits<DT>;
-    const int smem = TR::kStages * TR::kStage + (int)sizeof(FewShared);
+    constexpr int smem = Ring<DT, NT>::kBytes;
     static std::once_flag once[64];
     static int rc[64];
     int dev = 0;
@@ -796,7 +981,7 @@ int sched_ints(const moe_config *c) { return 1 + kMaxGroups + c->hidden / 128; }
 void few_layout(const moe_config *c, moe_few_layout *L) {
     const int64_t T = c->max_tokens, H = c->hidden, I = c->inter, k = c->top_k;
     const int64_t R = T * (k + c->num_shared);
-    const bool bf = c->dtype == MOE_DTYPE_BF16, fp8 = c->dtype == MOE_DTYPE_FP8_BLOCK128;
+    const bool bf = c->dtype == MOE_DTYPE_BF16;
     size_t off = 0;
     auto take = [&](int64_t bytes) {
         const size_t o = off;
@@ -805,13 +990,12 @@ void few_layout(const moe_config *c, moe_few_layout *L) {
     };
     L->status = take(4);
     L->sched = take(4 * (int64_t)sched_ints(c));
-    L->logits = take(4 * T * c->num_experts);
+    L->score = take(4 * T * c->num_experts);
+    L->select = take(4 * T * c->num_experts);
     L->topk_ids = take(4 * T * k);
     L->topk_w = take(4 * T * k);
-    L->x16 = take(bf ? 0 : 2 * T * H);
-    L->xs = take(bf ? 0 : fp8 ? 4 * T * (H / 128) : T * (H / 32));
-    L->h16 = take(2 * R * I);
-    L->hs = take(bf ? 0 : fp8 ? 4 * R * (I / 128) : R * (I / 32));
+    L->x16 = take(bf ? 0 : T * (H / 128) * kSegment);
+    L->h16 = take(bf ? 2 * R * I : R * (I / 128) * kSegment);
     L->y = take(4 * R * H);
     L->total = off;
 }
@@ -823,27 +1007,6 @@ int launch_layer_few(const moe_config *c, const moe_weights *w, int T, const voi
     uint8_t *b = static_cast<uint8_t *>(ws);
     const int H = c->hidden, E = c->num_experts, S = c->num_shared;
 
-    RouteArgs r = {};
-    r.T = T;
-    r.H = H;
-    r.E = E;
-    r.sched_ints = sched_ints(c);
-    r.dtype = c->dtype;
-    r.x = static_cast<const uint16_t *>(x);
-    r.wg = static_cast<const uint16_t *>(w->w_gate);
-    r.offset = w->logit_offset;
-    r.logits = reinterpret_cast<float *>(b + L.logits);
-    r.x16 = reinterpret_cast<uint16_t *>(b + L.x16);
-    r.xs = b + L.xs;
-    r.sched = reinterpret_cast<int32_t *>(b + L.sched);
-    r.status = reinterpret_cast<int32_t *>(b + L.status);
-    const int64_t warps = (int64_t)E * ceil_div(T, kTokChunk);
-    r.logit_blocks = (int)ceil_div(warps, kRouteThreads / 32);
-    const int64_t qwarps = c->dtype == MOE_DTYPE_BF16 ? 0 : (int64_t)T * ceil_div(H, 256);
-    const int64_t blocks = r.logit_blocks + ceil_div(qwarps, kRouteThreads / 32);
-    if (int rc = launch_dependent(few_route_kernel, dim3((unsigned)blocks), dim3(kRouteThreads), 0, s, r))
-        return rc;
-
     SelectArgs sel = {};
     sel.T = T;
     sel.E = E;
@@ -854,10 +1017,31 @@ int launch_layer_few(const moe_config *c, const moe_weights *w, int T, const voi
     sel.sigmoid = c->scoring == MOE_SCORING_SIGMOID;
     sel.norm = c->norm_topk;
     sel.scaling = c->routed_scaling;
-    sel.logits = r.logits;
     sel.bias = w->e_bias;
     sel.log2phys = w->log2phys;
-    sel.status = r.status;
+    sel.status = reinterpret_cast<int32_t *>(b + L.status);
+
+    RouteArgs r = {};
+    r.T = T;
+    r.H = H;
+    r.E = E;
+    r.sched_ints = sched_ints(c);
+    r.dtype = c->dtype;
+    r.x = static_cast<const uint16_t *>(x);
+    r.wg = static_cast<const uint16_t *>(w->w_gate);
+    r.offset = w->logit_offset;
+    r.sel = sel;
+    r.score = reinterpret_cast<float *>(b + L.score);
+    r.select = reinterpret_cast<float *>(b + L.select);
+    r.x16 = b + L.x16;
+    r.sched = reinterpret_cast<int32_t *>(b + L.sched);
+    r.status = sel.status;
+    const int64_t warps = (int64_t)E * ceil_div(T, kTokChunk);
+    r.logit_blocks = (int)ceil_div(warps, kRouteThreads / 32);
+    const int64_t qwarps = c->dtype == MOE_DTYPE_BF16 ? 0 : (int64_t)T * ceil_div(H, 256);
+    const int64_t blocks = r.logit_blocks + ceil_div(qwarps, kRouteThreads / 32);
+    if (int rc = launch_dependent(few_route_kernel, dim3((unsigned)blocks), dim3(kRouteThreads), 0, s, r))
+        return rc;
 
     FewArgs a = {};
     a.T = T;
@@ -867,18 +1051,16 @@ int launch_layer_few(const moe_config *c, const moe_weights *w, int T, const voi
     a.S = S;
     a.k = c->top_k;
     a.out_bf16 = out_dtype == MOE_OUT_BF16;
-    a.x = r.x;
     a.w13 = static_cast<const uint8_t *>(w->w13);
     a.w2 = static_cast<const uint8_t *>(w->w2);
     a.w13_s = w->w13_scales;
     a.w2_s = w->w2_scales;
-    a.logits = r.logits;
+    a.score = r.score;
+    a.select = r.select;
     a.ids = reinterpret_cast<int32_t *>(b + L.topk_ids);
     a.wts = reinterpret_cast<float *>(b + L.topk_w);
-    a.x16 = c->dtype == MOE_DTYPE_BF16 ? r.x : r.x16;
-    a.xs = r.xs;
-    a.h16 = reinterpret_cast<uint16_t *>(b + L.h16);
-    a.hs = b + L.hs;
+    a.xrows = c->dtype == MOE_DTYPE_BF16 ? static_cast<const uint8_t *>(x) : r.x16;
+    a.hrows = b + L.h16;
     a.y = reinterpret_cast<float *>(b + L.y);
     a.out = out;
     a.sched = r.sched;

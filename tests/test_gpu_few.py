@@ -89,11 +89,14 @@ def _stored_h(shape, layer, R):
     I = shape.inter
     if shape.dtype == "bf16":
         return layer.view("h16", torch.bfloat16, (R, I)).double()
-    v = layer.view("h16", torch.float16, (R, I)).double()
+    # segments of 128 values: fp16 code values, then the scale (fp32) or four scale bytes
+    seg = layer.view("h16", torch.uint8, (R, I // 128, 272))
+    v = seg[..., :256].contiguous().view(torch.float16).double()
     if shape.dtype == "fp8":
-        return v * layer.view("hs", torch.float32, (R, I // 128)).double().repeat_interleave(128, 1)
-    s = layer.view("hs", torch.uint8, (R, I // 32)).double()
-    return v * torch.exp2(s - 127).repeat_interleave(32, 1)
+        s = seg[..., 256:260].contiguous().view(torch.float32).double()
+        return (v * s).reshape(R, I)
+    s = torch.exp2(seg[..., 256:260].double() - 127).repeat_interleave(32, -1)
+    return (v * s).reshape(R, I)
 
 
 def _check(shape, w, values, layer, out_dtype=torch.float32, T=None, log2phys=None):
