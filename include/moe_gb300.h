@@ -443,7 +443,7 @@ MOE_API int moe_layer_few(const moe_config *cfg, const moe_weights *w, int32_t T
  * -1 where a choice was invalid) and topk_w fp32 [T, k] are what a caller may
  * want to read; the rest are intermediates. */
 typedef struct moe_few_layout {
-    size_t status, sched, score, select, topk_ids, topk_w, x16, h16, y, total;
+    size_t status, sched, score, select, topk_ids, topk_w, x, x_scales, h, h_scales, y, total;
 } moe_few_layout;
 MOE_API int moe_layer_few_layout(const moe_config *cfg, moe_few_layout *layout /* host */);
 

@@ -19,7 +19,8 @@ GATE_NONE, GATE_FEATURE, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 
 class FewLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in
-                ("status", "sched", "score", "select", "topk_ids", "topk_w", "x16", "h16", "y", "total")]
+                ("status", "sched", "score", "select", "topk_ids", "topk_w", "x", "x_scales", "h",
+                 "h_scales", "y", "total")]
 
 
 class Norm(ctypes.Structure):

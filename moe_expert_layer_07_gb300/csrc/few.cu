@@ -34,6 +34,7 @@
 // reads 16 bytes of a weight row at a time (the order of K inside a product is
 // free as long as both sides agree), rows 0, 4, 1, 5, ... of eight in MMA
 // order, which makes the reads conflict-free on the swizzled tiles.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -45,6 +46,7 @@
 #include "numerics.cuh"
 #include "ptx.cuh"
 #include "route_select.cuh"
+#include "tma_host.h"
 
 namespace moe {
 namespace {
@@ -55,13 +57,18 @@ constexpr int kMaxSlots = kMaxT * 16;                   // routed slots
 constexpr int kMaxRows = kMaxSlots + kMaxT * kMaxShared;
 constexpr int kMaxGroups = kMaxSlots + kMaxShared;      // groups with rows
 
-// The token side of the scaled types, x and h: segments of 128 values of a
-// row, each code kept as the fp16 number it stands for before its scale (256
-// bytes), then the segment's scale (fp32, FP8) or four scale bytes (MXFP4).
-// Such a segment is one bulk copy.
-constexpr int kSegment = 272;
-
 enum { DT_BF16 = MOE_DTYPE_BF16, DT_FP8 = MOE_DTYPE_FP8_BLOCK128, DT_MX4 = MOE_DTYPE_MXFP4 };
+
+// The token side, x and h.
+//  BF16   rows as they are.
+//  FP8    segments of 128 values of a row: each code kept as the fp16 number it
+//         stands for before its scale (256 bytes), then the fp32 scale.  Such a
+//         segment is one bulk copy.
+//  MXFP4  packed codes, row-major; scale bytes as [K tile][row][16] with a
+//         row's four of the tile in front, which is how the scales' copy to
+//         tensor memory takes 32 rows (16 of them matter here).
+constexpr int kSegment = 272;
+constexpr int kScaleRow = 16;
 
 struct FewArgs {
     int T, H, I, E, S, k, out_bf16;
@@ -70,8 +77,11 @@ struct FewArgs {
     const float *score, *select;   // [T, E]
     int32_t *ids;
     float *wts;
-    const uint8_t *xrows;          // bf16 [T, H], or segments [T, H/128]
-    uint8_t *hrows;                // bf16 [rows, I], or segments [rows, I/128]
+    const uint8_t *xrows;          // bf16 [T, H], or segments [T, H/128] (FP8)
+    uint8_t *hrows;                // bf16 [rows, I], segments [rows, I/128], or codes [rows, I/2]
+    const uint8_t *xs;             // MXFP4: [H/128][16][kScaleRow]
+    uint8_t *hs;                   // MXFP4: [I/128][hs_rows][kScaleRow]
+    int hs_rows;
     float *y;                      // [rows, H]
     void *out;
     int32_t *sched;                // unit counter | h_done[kMaxGroups] | col_done[H/128]
@@ -89,7 +99,7 @@ struct RouteArgs {
     const float *offset;
     SelectArgs sel;
     float *score, *select;   // [T, E]: SelectArgs' scores (softmax: logits), what it compares
-    uint8_t *x16;
+    uint8_t *xq, *xs;
     int32_t *sched, *status;
     const uint8_t *pf[2];       // weights to bring into L2 (the shared experts')
     size_t pf_bytes[2];
@@ -153,17 +163,12 @@ __device__ __forceinline__ uint2 fp8_as_half4(float a, float b, float c, float d
 }
 
 // One 256-column segment of a token's row, quantised as the layer does
-// (quant_row_segment's arithmetic, or mx4.cu's) into segments of 128 values.
+// (quant_row_segment's arithmetic, or mx4.cu's).
 __device__ __forceinline__ void quant_segment(const RouteArgs &a, int t, int seg, int lane) {
     const int col = seg * 256 + lane * 8;
     const bool active = col < a.H;
-    uint8_t *seg_at = a.x16 + ((size_t)t * (a.H / 128) + col / 128) * kSegment;
     float f[8] = {};
     if (active) bf8(__ldg(reinterpret_cast<const uint4 *>(a.x + (size_t)t * a.H + col)), f);
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
-    uint4 o;
     if (a.dtype == DT_FP8) {
         float amax = 0.0f;
 #pragma unroll
@@ -174,18 +179,20 @@ __device__ __forceinline__ void quant_segment(const RouteArgs &a, int t, int seg
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = __fdiv_rn(f[j], sc);
         const uint2 p = fp8_as_half4(f[0], f[1], f[2], f[3]), q = fp8_as_half4(f[4], f[5], f[6], f[7]);
-        o = make_uint4(p.x, p.y, q.x, q.y);
-        if (active && (lane & 15) == 0) *reinterpret_cast<float *>(seg_at + 256) = sc;
+        uint8_t *at = a.xq + ((size_t)t * (a.H / 128) + col / 128) * kSegment;
+        if (active) *reinterpret_cast<uint4 *>(at + col % 128 * 2) = make_uint4(p.x, p.y, q.x, q.y);
+        if (active && (lane & 15) == 0) *reinterpret_cast<float *>(at + 256) = sc;
     } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const uint32_t byte = mx4_scale_byte(m);
-        uint32_t h[4];
-        mx4_half8(mx4_codes8(f, byte), h);
-        o = make_uint4(h[0], h[1], h[2], h[3]);
-        if (active && (lane & 3) == 0) seg_at[256 + col % 128 / 32] = (uint8_t)byte;
+        if (active) *reinterpret_cast<uint32_t *>(a.xq + ((size_t)t * a.H + col) / 2) = mx4_codes8(f, byte);
+        if (active && (lane & 3) == 0)
+            a.xs[((size_t)(col / 128) * kMaxT + t) * kScaleRow + col % 128 / 32] = (uint8_t)byte;
     }
-    if (active) *reinterpret_cast<uint4 *>(seg_at + col % 128 * 2) = o;
 }
 
 __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const RouteArgs a) {
@@ -242,27 +249,44 @@ constexpr int kUnitSlots = 8;     // units announced ahead
 
 template <int DT, int NT>
 struct Traits {
-    // K elements of one tile, bytes of its codes and of its scales in a stage
+    // K elements of one tile, bytes of its codes; a stage holds two tiles
     static constexpr int kKT = DT == DT_BF16 ? 64 : 128;
-    static constexpr int kTile = DT == DT_MX4 ? 8192 : 16384;
-    static constexpr int kScale = DT == DT_MX4 ? 512 : 0;
-    static constexpr int kSlot = kTile + kScale;
+    static constexpr int kTile = 16384;
     // the token side of one tile of K: 8 NT rows.  The pitch spreads the reads
     // of a quarter warp (two rows, four chunks each) over all banks.
     static constexpr int kCopy = DT == DT_BF16 ? 128 : kSegment;
-    static constexpr int kPitch = DT == DT_BF16 ? 192 : DT == DT_FP8 ? 272 : 320;
-    static constexpr int kTokOff = 2 * kSlot;
+    static constexpr int kPitch = DT == DT_BF16 ? 192 : 272;
+    static constexpr int kTokOff = 2 * kTile;
     static constexpr int kTokHalf = 8 * NT * kPitch;
     static constexpr int kWsOff = kTokOff + 2 * kTokHalf;   // FP8: the tiles' two scales
     static constexpr int kStage = (kWsOff + 16 + 127) / 128 * 128;
     static constexpr int kBWords = DT == DT_BF16 ? 8 : 16;  // B words a lane holds for a tile
+    static constexpr int kScale = 0, kScaleOff = 0;
+    static constexpr int kMultipliers = kConsumers;         // warps that release a stage
+    static constexpr int kReaders = kWarps - 1;             // warps that read a unit's number
+};
+template <int NT>
+struct Traits<DT_MX4, NT> {
+    static constexpr int kKT = 128;
+    static constexpr int kTile = 8192, kScale = 512;
+    static constexpr int kTokBytes = 16 * 64, kTokScale = 16 * kScaleRow;
+    static constexpr int kTokOff = 2 * kTile, kScaleOff = kTokOff + 2 * kTokBytes;
+    static constexpr int kTokScaleOff = kScaleOff + 2 * kScale;
+    static constexpr int kStage = kTokScaleOff + 2 * 512;
+    static constexpr int kCopy = 0, kPitch = 0, kTokHalf = 0, kWsOff = 0, kBWords = 1;
+    static constexpr int kMultipliers = 1;                  // the MMAs' commit
+    static constexpr int kReaders = 1 + 1 + kPublishers;
+    // tensor memory: two accumulators of gate and up (16 token columns each),
+    // then for each stage the scales of two weight and two token tiles
+    static constexpr int kTmemCols = 256, kSfCol = 64, kSfStage = 16;
 };
 
 template <int NT>
 struct FewShared {   // after the ring
     uint64_t full[16], empty[16];
     uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
-    uint64_t res_full[2], res_empty[2], pub_sync;
+    uint64_t res_full[2], res_empty[2], pub_sync, drain;
+    uint32_t tmem_slot;
     int32_t unit[kUnitSlots];
     int abort, last, n_groups;
     int32_t ids[kMaxSlots];
@@ -277,12 +301,13 @@ struct FewShared {   // after the ring
 // Ring stages: what fits beside FewShared in the 227 KB a CTA can have.
 template <int DT, int NT>
 struct Ring {
-    static constexpr int kFit = (227 * 1024 - (int)sizeof(FewShared<NT>)) / Traits<DT, NT>::kStage;
-    static constexpr int kStages = kFit < 16 ? kFit : 16;
-    static constexpr int kBytes = kStages * Traits<DT, NT>::kStage + (int)sizeof(FewShared<NT>);
+    static constexpr int kAlign = DT == DT_MX4 ? 1024 : 128;
+    static constexpr int kStages =
+        (227 * 1024 - kAlign - (int)sizeof(FewShared<NT>)) / Traits<DT, NT>::kStage;
+    static constexpr int kBytes = kAlign + kStages * Traits<DT, NT>::kStage + (int)sizeof(FewShared<NT>);
 };
 static_assert(Ring<DT_FP8, 1>::kStages == 5 && Ring<DT_FP8, 2>::kStages == 5 &&
-              Ring<DT_MX4, 2>::kStages >= 7, "depth of the rings");
+              Ring<DT_MX4, 2>::kStages >= 9 && Ring<DT_MX4, 1>::kStages <= 12, "depth of the rings");
 
 // Order-preserving integers of the selection values: larger is better, 0 is
 // not selectable (NaN and minus infinity, as warp_select treats them); the two
@@ -416,14 +441,13 @@ __device__ __forceinline__ void e4m3_half4(uint32_t codes, uint32_t &lo, uint32_
 }
 
 // What a lane holds of the token side for one tile of K: the words of column
-// g of each n-tile, and (scaled types) the scales of columns 2t and 2t+1.
+// g of each n-tile, and (FP8) the scales of columns 2t and 2t+1.
 // Columns past the group's rows hold what the stage held before; their
 // results are not used.
 template <int DT, int NT>
 struct TokenSide {
     uint32_t b[NT][Traits<DT, NT>::kBWords];
-    float s[NT][2];        // FP8
-    uint32_t s4[NT][2];    // MXFP4: four scale bytes, one for each 32 of K
+    float s[NT][2];   // FP8
 };
 
 template <int DT, int NT>
@@ -442,18 +466,14 @@ __device__ __forceinline__ void load_tokens(TokenSide<DT, NT> &f, const uint8_t 
                 put(&f.b[n][8 * h], p + (t + 4 * h) * 32);
                 put(&f.b[n][8 * h + 4], p + (t + 4 * h) * 32 + 16);
             }
-        } else if (DT == DT_BF16) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) put(&f.b[n][4 * h], p + (t + 4 * h) * 16);
         } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) put(&f.b[n][4 * q], p + q * 64 + t * 16);
+            for (int h = 0; h < 2; ++h) put(&f.b[n][4 * h], p + (t + 4 * h) * 16);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint8_t *s = rows + (8 * n + 2 * t + i) * TR::kPitch + 256;
-            if (DT == DT_FP8) f.s[n][i] = *reinterpret_cast<const float *>(s);
-            else if (DT == DT_MX4) f.s4[n][i] = *reinterpret_cast<const uint32_t *>(s);
+            if (DT == DT_FP8)
+                f.s[n][i] = *reinterpret_cast<const float *>(rows + (8 * n + 2 * t + i) * TR::kPitch + 256);
         }
     }
 }
@@ -465,35 +485,6 @@ template <int DT, int NT>
 __device__ __forceinline__ void tile_product(float (&acc)[NT][4], const uint8_t *tile, int ra, int t,
                                              const TokenSide<DT, NT> &f, float ws, bool second) {
     using TR = Traits<DT, NT>;
-    if (DT == DT_MX4) {
-        const uint8_t *scales = tile + TR::kTile;
-        const uint32_t sa4 = *reinterpret_cast<const uint32_t *>(scales + (ra & 31) * 16 + (ra >> 5) * 4);
-        const int rb = ra + 8;
-        const uint32_t sb4 = *reinterpret_cast<const uint32_t *>(scales + (rb & 31) * 16 + (rb >> 5) * 4);
-        const int sw = (ra >> 1) & 3;   // the swizzle of both rows
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint8_t *p = tile + ra * 64 + ((q ^ sw) << 4) + t * 4;
-            uint32_t a[4], b[4];
-            mx4_half8(*reinterpret_cast<const uint32_t *>(p), a);
-            mx4_half8(*reinterpret_cast<const uint32_t *>(p + 8 * 64), b);
-            const float wa = mx4_scale((sa4 >> (8 * q)) & 255u), wb = mx4_scale((sb4 >> (8 * q)) & 255u);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (n && !second) continue;
-                float part[4] = {};
-                mma_f16(part, a[0], b[0], a[1], b[1], f.b[n][4 * q], f.b[n][4 * q + 1]);
-                mma_f16(part, a[2], b[2], a[3], b[3], f.b[n][4 * q + 2], f.b[n][4 * q + 3]);
-                const float x0 = mx4_scale((f.s4[n][0] >> (8 * q)) & 255u);
-                const float x1 = mx4_scale((f.s4[n][1] >> (8 * q)) & 255u);
-                acc[n][0] = fmaf(part[0] * wa, x0, acc[n][0]);
-                acc[n][1] = fmaf(part[1] * wa, x1, acc[n][1]);
-                acc[n][2] = fmaf(part[2] * wb, x0, acc[n][2]);
-                acc[n][3] = fmaf(part[3] * wb, x1, acc[n][3]);
-            }
-        }
-        return;
-    }
     float part[NT][4] = {};
     const int sw = ra & 7;
 #pragma unroll
@@ -536,32 +527,60 @@ __device__ __forceinline__ void tile_product(float (&acc)[NT][4], const uint8_t 
     }
 }
 
+// MXFP4: 128 weight rows x 64 of K against 16 token rows, scale bytes sf and
+// sf + 1 (mx4_gemm.cu has the same product for many rows).
+__host__ __device__ constexpr uint32_t few_idesc_mxf4(int sf) {
+    return ((uint32_t)sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(16 >> 3) << 17) | (1u << 23) |
+           ((uint32_t)(128 >> 4) << 24) | ((uint32_t)sf << 29);
+}
+__device__ __forceinline__ void mma_tile_mxf4(uint32_t d, uint32_t weights, uint32_t tokens, uint32_t sfw,
+                                              uint32_t sft, bool accumulate) {
+    const uint64_t wd = ptx::sdesc_k_sw64(weights), td = ptx::sdesc_k_sw64(tokens);
+    ptx::mma_mxf4(d, wd, td, few_idesc_mxf4(0), sfw, sft, accumulate);
+    ptx::mma_mxf4(d, wd + 2, td + 2, few_idesc_mxf4(2), sfw, sft, 1);
+}
+
 template <int DT, int NT>
 __global__ void __launch_bounds__(kFfnThreads, 1)
-    few_ffn_kernel(const FewArgs a, const SelectArgs sel) {
+    few_ffn_kernel(const FewArgs a, const SelectArgs sel, const __grid_constant__ CUtensorMap tmX,
+                   const __grid_constant__ CUtensorMap tmH) {
     using TR = Traits<DT, NT>;
+    constexpr bool MX4 = DT == DT_MX4;
     constexpr int kStages = Ring<DT, NT>::kStages;
-    extern __shared__ __align__(1024) uint8_t ring[];
+    extern __shared__ uint8_t dsmem[];
+    uint8_t *ring = dsmem + (-ptx::smem_u32(dsmem) & (Ring<DT, NT>::kAlign - 1));
     FewShared<NT> &sh = *reinterpret_cast<FewShared<NT> *>(ring + kStages * TR::kStage);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(ptx::smem_u32(&sh.full[s]), 2);   // the weights' thread, the tokens' warp
-            ptx::mbar_init(ptx::smem_u32(&sh.empty[s]), kConsumers);
+            ptx::mbar_init(ptx::smem_u32(&sh.empty[s]), TR::kMultipliers);
         }
         for (int s = 0; s < kUnitSlots; ++s) {
             ptx::mbar_init(ptx::smem_u32(&sh.unit_full[s]), 1);
-            ptx::mbar_init(ptx::smem_u32(&sh.unit_empty[s]), kWarps - 1);
+            ptx::mbar_init(ptx::smem_u32(&sh.unit_empty[s]), TR::kReaders);
         }
         for (int s = 0; s < 2; ++s) {
-            ptx::mbar_init(ptx::smem_u32(&sh.res_full[s]), kConsumers);
+            ptx::mbar_init(ptx::smem_u32(&sh.res_full[s]), TR::kMultipliers);
             ptx::mbar_init(ptx::smem_u32(&sh.res_empty[s]), kPublishers);
         }
         ptx::mbar_init(ptx::smem_u32(&sh.pub_sync), kPublishers);
+        ptx::mbar_init(ptx::smem_u32(&sh.drain), 1);
         ptx::fence_mbar_init();
         sh.abort = 0;
         sh.n_groups = 0;
+    }
+    if constexpr (MX4) {
+        if (warp == 0) {
+            ptx::tmem_alloc(ptx::smem_u32(&sh.tmem_slot), TR::kTmemCols);
+            ptx::tmem_relinquish();
+        }
+        if (warp == kTokens && lane == 0) {
+            ptx::tma_prefetch_desc(&tmX);
+            ptx::tma_prefetch_desc(&tmH);
+        }
+        ptx::tc_fence_before();   // the address is read after the barriers below
     }
     const int slots = a.T * a.k;
     for (int i = threadIdx.x; i < slots; i += kFfnThreads) sh.ids[i] = -1;
@@ -632,10 +651,15 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     }
     __syncthreads();
 
+    uint32_t tmem = 0;
+    if constexpr (MX4) {
+        ptx::tc_fence_after();
+        tmem = sh.tmem_slot;
+    }
     const int nG = sh.n_groups + a.S;
     const int mt1 = a.I / 128, nb2 = a.H / 128;                  // tiles of 128 weight rows
     const int kb1 = a.H / TR::kKT, kb2 = a.I / TR::kKT;          // tiles along K
-    const int u1 = nG * mt1, units = u1 + nG * nb2;
+    const int u1 = nG * mt1, units = u1 + nG * nb2;              // no groups: no units
     int32_t *h_done = a.sched + 1, *col_done = h_done + kMaxGroups;
     volatile int *abort_flag = &sh.abort;
 
@@ -646,7 +670,6 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             if (a.out_bf16) static_cast<uint16_t *>(a.out)[i] = 0;
             else static_cast<float *>(a.out)[i] = 0.0f;
         }
-        return;
     }
 
     // What a unit number stands for.
@@ -677,9 +700,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         return u;
     };
 
-    if (warp == kProducer) {
+    if (warp == kProducer && lane == 0) {
         // ---- weights -------------------------------------------------------------
-        if (lane) return;
         const uint64_t policy = ptx::policy_evict_first();
         int issued = 0;
         bool ok = true;
@@ -709,13 +731,14 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 const uint32_t dst = ptx::smem_u32(ring + st * TR::kStage);
                 const size_t i0 = un.gu ? b0 + s : b0 + 2 * s, i1 = un.gu ? b1 + s : i0 + 1;
                 const bool two = un.gu || 2 * s + 1 < un.kb;
-                ptx::mbar_arrive_expect_tx(full, two ? 2 * TR::kSlot : TR::kSlot);
+                ptx::mbar_arrive_expect_tx(full, (two ? 2 : 1) * (TR::kTile + TR::kScale));
                 ptx::bulk_load(dst, w + i0 * TR::kTile, TR::kTile, full, policy);
-                if (TR::kScale) ptx::bulk_load(dst + TR::kTile, ws + i0 * TR::kScale, TR::kScale, full, policy);
-                if (two) {
-                    ptx::bulk_load(dst + TR::kSlot, w + i1 * TR::kTile, TR::kTile, full, policy);
-                    if (TR::kScale)
-                        ptx::bulk_load(dst + TR::kSlot + TR::kTile, ws + i1 * TR::kScale, TR::kScale, full, policy);
+                if (two) ptx::bulk_load(dst + TR::kTile, w + i1 * TR::kTile, TR::kTile, full, policy);
+                if constexpr (MX4) {
+                    ptx::bulk_load(dst + TR::kScaleOff, ws + i0 * TR::kScale, TR::kScale, full, policy);
+                    if (two)
+                        ptx::bulk_load(dst + TR::kScaleOff + TR::kScale, ws + i1 * TR::kScale, TR::kScale, full,
+                                       policy);
                 }
                 ++issued;
             }
@@ -726,10 +749,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         // no copy may still be writing when the CTA's shared memory is given up
         for (int i = max(0, issued - kStages); i < issued; ++i)
             ptx::wait_drain(ptx::smem_u32(&sh.full[i % kStages]), (i / kStages) & 1);
-        return;
-    }
-
-    if (warp == kTokens) {
+    } else if (warp == kTokens) {
         // ---- the token side: x, or h once it is complete ------------------------------
         const uint64_t policy = ptx::policy_evict_last();
         ptx::fence_proxy_async_global();   // x's segments were written by another kernel
@@ -775,6 +795,22 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 if (!ok) break;
                 uint8_t *base = ring + st * TR::kStage;
                 const int k0 = un.gu ? s : 2 * s, nk = un.gu ? 1 : min(2, un.kb - k0);
+                if constexpr (MX4) {
+                    // 16 rows whatever the group's: x's are all tokens, h's
+                    // begin at the group's first (rows past its last are not used)
+                    if (lane == 0) {
+                        const uint32_t dst = ptx::smem_u32(base);
+                        ptx::mbar_arrive_expect_tx(full, nk * (TR::kTokBytes + TR::kTokScale));
+                        for (int k = 0; k < nk; ++k) {
+                            ptx::tma_load_2d(dst + TR::kTokOff + k * TR::kTokBytes, un.gu ? &tmX : &tmH,
+                                             (k0 + k) * 64, un.gu ? 0 : row0, full, policy);
+                            const uint8_t *ts = un.gu ? a.xs + (size_t)(k0 + k) * kMaxT * kScaleRow
+                                                      : a.hs + ((size_t)(k0 + k) * a.hs_rows + row0) * kScaleRow;
+                            ptx::bulk_load(dst + TR::kTokScaleOff + k * 512, ts, TR::kTokScale, full, policy);
+                        }
+                    }
+                    continue;
+                }
                 if (DT == DT_FP8) {
                     const int k1 = un.gu ? k0 : min(k0 + 1, un.kb - 1);
                     const float w0 = __shfl_sync(0xffffffffu, k0 < 32 ? wsc[0][0] : wsc[0][1], k0 & 31);
@@ -793,10 +829,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         if (lane == 0)   // as the producer: no copy may outlive the CTA
             for (int i = max(0, stage - kStages); i < stage; ++i)
                 ptx::wait_drain(ptx::smem_u32(&sh.full[i % kStages]), (i / kStages) & 1);
-        return;
-    }
-
-    if (warp >= kFirstPublisher) {
+    } else if (warp >= kFirstPublisher) {
         // ---- results: h to its format and to memory, y to memory, the combine --------
         const int pw = warp - kFirstPublisher;
         uint32_t parity = 0;
@@ -816,7 +849,53 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             const bool ok = ptx::wait_bounded(ptx::smem_u32(&sh.res_full[buf]), (it >> 1) & 1, abort_flag,
                                               a.status, MOE_DEV_TIMEOUT);
             if (!__all_sync(0xffffffffu, ok)) break;
-            for (int c = pw; c < n; c += kPublishers) {
+            if constexpr (MX4) {
+                // this warp's lane quarter of tensor memory: 32 of the 128 rows,
+                // for gate/up one block of h's scales
+                const int q = warp & 3, m = 32 * q + lane;
+                const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * 32;
+                uint32_t d[16], up[16];
+                ptx::tc_fence_after();
+                ptx::tmem_ld16(acc, d);
+                if (un.gu) ptx::tmem_ld16(acc + 16, up);
+                ptx::tmem_wait_ld(d);
+                ptx::tmem_wait_ld(up);
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.res_empty[buf]));
+                if (un.gu) {
+#pragma unroll
+                    for (int c = 0; c < 8 * NT; ++c)
+                        sh.res[0][c][m] = silu_mul(__uint_as_float(d[c]), __uint_as_float(up[c]));
+                    __syncwarp();
+                    for (int i0 = 0; i0 < n; i0 += 8) {   // eight rows, four lanes each
+                        const int i = i0 + (lane >> 2), ch = lane & 3;
+                        const size_t row = row0 + min(i, n - 1);
+                        const float *p = &sh.res[0][sh.row_tok[row]][32 * q + 8 * ch];
+                        float f[8];
+                        *reinterpret_cast<float4 *>(f) = *reinterpret_cast<const float4 *>(p);
+                        *reinterpret_cast<float4 *>(f + 4) = *reinterpret_cast<const float4 *>(p + 4);
+                        uint32_t mx = 0;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) mx = max(mx, __float_as_uint(f[j]) & 0x7fffffffu);
+                        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                        const uint32_t byte = mx4_scale_byte(mx);
+                        if (i < n) {
+                            *reinterpret_cast<uint32_t *>(a.hrows + (row * a.I + un.tile * 128 + 32 * q + 8 * ch) / 2) =
+                                mx4_codes8(f, byte);
+                            if (ch == 0)
+                                a.hs[((size_t)un.tile * a.hs_rows + row) * kScaleRow + q] = (uint8_t)byte;
+                        }
+                    }
+                    __syncwarp();   // res is rewritten by the next unit
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 8 * NT; ++c)
+                        if (c < n) a.y[(size_t)(row0 + c) * a.H + un.tile * 128 + m] = __uint_as_float(d[c]);
+                }
+            }
+            for (int c = pw; !MX4 && c < n; c += kPublishers) {
                 const float4 q = *reinterpret_cast<const float4 *>(&sh.res[buf][c][lane * 4]);
                 const size_t row = row0 + c;
                 if (!un.gu) {
@@ -827,30 +906,20 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                         make_uint2(*reinterpret_cast<uint32_t *>(&b0), *reinterpret_cast<uint32_t *>(&b1));
                 } else {
                     uint8_t *seg = a.hrows + (row * mt1 + un.tile) * kSegment;
-                    uint2 o;
-                    if (DT == DT_FP8) {
-                        float m = fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)), fmaxf(fabsf(q.z), fabsf(q.w)));
+                    float m = fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)), fmaxf(fabsf(q.z), fabsf(q.w)));
 #pragma unroll
-                        for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                        const float sc = fp8_group_scale(m), inv = fp8_group_inv(sc);
-                        o = fp8_as_half4(__fmul_rn(q.x, inv), __fmul_rn(q.y, inv), __fmul_rn(q.z, inv),
-                                         __fmul_rn(q.w, inv));
-                        if (lane == 0) *reinterpret_cast<float *>(seg + 256) = sc;
-                    } else {
-                        uint32_t m = max(max(__float_as_uint(q.x) & 0x7fffffffu, __float_as_uint(q.y) & 0x7fffffffu),
-                                         max(__float_as_uint(q.z) & 0x7fffffffu, __float_as_uint(q.w) & 0x7fffffffu));
-#pragma unroll
-                        for (int d = 4; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-                        const uint32_t byte = mx4_scale_byte(m);
-                        o = byte == 255u ? make_uint2(0u, 0u)
-                                         : mx4_as_half4(q.x, q.y, q.z, q.w, mx4_inv_scale(byte));
-                        if ((lane & 7) == 0) seg[256 + lane / 8] = (uint8_t)byte;
-                    }
+                    for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                    const float sc = fp8_group_scale(m), inv = fp8_group_inv(sc);
+                    const uint2 o = fp8_as_half4(__fmul_rn(q.x, inv), __fmul_rn(q.y, inv),
+                                                 __fmul_rn(q.z, inv), __fmul_rn(q.w, inv));
+                    if (lane == 0) *reinterpret_cast<float *>(seg + 256) = sc;
                     *reinterpret_cast<uint2 *>(seg + lane * 8) = o;
                 }
             }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.res_empty[buf]));
+            if (!MX4) {
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.res_empty[buf]));
+            }
             if (un.gu) ptx::fence_proxy_async_global();   // h is read by copies
             __threadfence();
             if (!pub_sync()) break;   // every publisher's rows are out
@@ -901,64 +970,130 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 }
             }
         }
-        return;
-    }
-
-    // ---- products -------------------------------------------------------------------
-    const int g8 = lane >> 2, t4 = lane & 3;
-    const int ra = warp * 16 + ((g8 >> 1) | ((g8 & 1) << 2));   // this lane's rows ra, ra + 8
-    int stage = 0;   // stages consumed so far
-    bool ok = true;
-    for (int it = 0; ok; ++it) {
-        const int u = take_unit(it);
-        if (u < 0) break;
-        const Unit un = unit_of(u);
-        const int n = sh.group_n[un.gi];
-        const bool second = NT > 1 && n > 8;
-        float acc[2][NT][4] = {};
-        for (int s = 0; s < un.steps; ++s, ++stage) {
-            const int st = stage % kStages;
-            ok = ptx::wait_bounded(ptx::smem_u32(&sh.full[st]), (stage / kStages) & 1, abort_flag, a.status,
+    } else if constexpr (MX4) {
+        // ---- products (MXFP4): one thread issues them -------------------------------
+        if (warp == 0) {
+            int stage = 0;
+            bool ok = true;
+            for (int it = 0; ok; ++it) {
+                const int u = take_unit(it);
+                if (u < 0) break;
+                const Unit un = unit_of(u);
+                const int buf = it & 1;
+                if (lane == 0) {
+                    ok = ptx::wait_bounded(ptx::smem_u32(&sh.res_empty[buf]), ((it >> 1) & 1) ^ 1, abort_flag,
+                                           a.status, MOE_DEV_TIMEOUT);
+                    ptx::tc_fence_after();
+                    const uint32_t acc = tmem + buf * 32;
+                    for (int s = 0; ok && s < un.steps; ++s) {
+                        const int st = (stage + s) % kStages;
+                        ok = ptx::wait_bounded(ptx::smem_u32(&sh.full[st]), ((stage + s) / kStages) & 1,
+                                               abort_flag, a.status, MOE_DEV_TIMEOUT);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        const uint32_t base = ptx::smem_u32(ring + st * TR::kStage);
+                        const uint32_t sf = tmem + TR::kSfCol + st * TR::kSfStage;
+                        const bool two = un.gu || 2 * s + 1 < un.kb;
+                        ptx::tmem_copy_scales(sf, ptx::sdesc_scales(base + TR::kScaleOff));
+                        ptx::tmem_copy_scales(sf + 8, ptx::sdesc_scales(base + TR::kTokScaleOff));
+                        mma_tile_mxf4(acc, base, base + TR::kTokOff, sf, sf + 8, s > 0);
+                        if (two) {
+                            // gate/up: the up rows against the same tokens, into
+                            // the other accumulator; down: the next tile of K
+                            const int k = un.gu ? 0 : 1;
+                            ptx::tmem_copy_scales(sf + 4, ptx::sdesc_scales(base + TR::kScaleOff + TR::kScale));
+                            if (k)
+                                ptx::tmem_copy_scales(sf + 12, ptx::sdesc_scales(base + TR::kTokScaleOff + 512));
+                            mma_tile_mxf4(un.gu ? acc + 16 : acc, base + TR::kTile,
+                                          base + TR::kTokOff + k * TR::kTokBytes, sf + 4, sf + 8 + 4 * k,
+                                          un.gu ? s > 0 : true);
+                        }
+                        ptx::mma_commit(ptx::smem_u32(&sh.empty[st]));
+                    }
+                    if (ok) ptx::mma_commit(ptx::smem_u32(&sh.res_full[buf]));
+                }
+                stage += un.steps;
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+            }
+            if (lane == 0) {   // every product has landed before the columns are given up
+                ptx::mma_commit(ptx::smem_u32(&sh.drain));
+                ptx::wait_drain(ptx::smem_u32(&sh.drain), 0);
+            }
+        }
+    } else if (warp < kConsumers) {
+        // ---- products ---------------------------------------------------------------
+        const int g8 = lane >> 2, t4 = lane & 3;
+        const int ra = warp * 16 + ((g8 >> 1) | ((g8 & 1) << 2));   // this lane's rows ra, ra + 8
+        int stage = 0;   // stages consumed so far
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+            const int u = take_unit(it);
+            if (u < 0) break;
+            const Unit un = unit_of(u);
+            const int n = sh.group_n[un.gi];
+            const bool second = NT > 1 && n > 8;
+            float acc[2][NT][4] = {};
+            for (int s = 0; s < un.steps; ++s, ++stage) {
+                const int st = stage % kStages;
+                ok = ptx::wait_bounded(ptx::smem_u32(&sh.full[st]), (stage / kStages) & 1, abort_flag, a.status,
+                                       MOE_DEV_TIMEOUT);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const uint8_t *base = ring + st * TR::kStage;
+                float2 ws = make_float2(0.0f, 0.0f);
+                if (DT == DT_FP8) ws = *reinterpret_cast<const float2 *>(base + TR::kWsOff);
+                TokenSide<DT, NT> f;
+                load_tokens<DT, NT>(f, base + TR::kTokOff, g8, t4);
+                tile_product<DT, NT>(acc[0], base, ra, t4, f, ws.x, second);
+                if (un.gu) {
+                    tile_product<DT, NT>(acc[1], base + TR::kTile, ra, t4, f, ws.y, second);
+                } else if (2 * s + 1 < un.kb) {
+                    load_tokens<DT, NT>(f, base + TR::kTokOff + TR::kTokHalf, g8, t4);
+                    tile_product<DT, NT>(acc[0], base + TR::kTile, ra, t4, f, ws.y, second);
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.empty[st]));
+            }
+            if (!ok) break;
+            const int buf = it & 1;
+            ok = ptx::wait_bounded(ptx::smem_u32(&sh.res_empty[buf]), ((it >> 1) & 1) ^ 1, abort_flag, a.status,
                                    MOE_DEV_TIMEOUT);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            const uint8_t *base = ring + st * TR::kStage;
-            float2 ws = make_float2(0.0f, 0.0f);
-            if (DT == DT_FP8) ws = *reinterpret_cast<const float2 *>(base + TR::kWsOff);
-            TokenSide<DT, NT> f;
-            load_tokens<DT, NT>(f, base + TR::kTokOff, g8, t4);
-            tile_product<DT, NT>(acc[0], base, ra, t4, f, ws.x, second);
-            if (un.gu) {
-                tile_product<DT, NT>(acc[1], base + TR::kSlot, ra, t4, f, ws.y, second);
-            } else if (2 * s + 1 < un.kb) {
-                load_tokens<DT, NT>(f, base + TR::kTokOff + TR::kTokHalf, g8, t4);
-                tile_product<DT, NT>(acc[0], base + TR::kSlot, ra, t4, f, ws.y, second);
-            }
+    #pragma unroll
+            for (int j = 0; j < NT; ++j)
+    #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = 8 * j + 2 * t4 + (i & 1);
+                    if (c < n)
+                        sh.res[buf][c][ra + (i & 2) * 4] =
+                            un.gu ? silu_mul(acc[0][j][i], acc[1][j][i]) : acc[0][j][i];
+                }
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.empty[st]));
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.res_full[buf]));
         }
-        if (!ok) break;
-        const int buf = it & 1;
-        ok = ptx::wait_bounded(ptx::smem_u32(&sh.res_empty[buf]), ((it >> 1) & 1) ^ 1, abort_flag, a.status,
-                               MOE_DEV_TIMEOUT);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int c = 8 * j + 2 * t4 + (i & 1);
-                if (c < n)
-                    sh.res[buf][c][ra + (i & 2) * 4] =
-                        un.gu ? silu_mul(acc[0][j][i], acc[1][j][i]) : acc[0][j][i];
-            }
+    }
+
+    if constexpr (MX4) {
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.res_full[buf]));
+        ptx::tc_fence_before();
+        __syncthreads();
+        if (warp == 0) {
+            ptx::tc_fence_after();
+            ptx::tmem_dealloc(tmem, TR::kTmemCols);
+        }
     }
 }
 
 template <int DT, int NT>
 int launch_ffn(const FewArgs &a, const SelectArgs &sel, cudaStream_t s) {
+    CUtensorMap tmX = {}, tmH = {};
+    if (DT == DT_MX4) {
+        const int rows = a.T * (a.k + a.S);
+        if (!encode_2d_sw64(&tmX, a.xrows, (uint64_t)a.H / 2, (uint64_t)a.T, 16) ||
+            !encode_2d_sw64(&tmH, a.hrows, (uint64_t)a.I / 2, (uint64_t)rows, 16))
+            return cuda_fail("cuTensorMapEncodeTiled (token rows)");
+    }
     constexpr int smem = Ring<DT, NT>::kBytes;
     static std::once_flag once[64];
     static int rc[64];
@@ -971,7 +1106,7 @@ int launch_ffn(const FewArgs &a, const SelectArgs &sel, cudaStream_t s) {
     });
     if (rc[dev]) return cuda_fail("cudaFuncSetAttribute", (cudaError_t)rc[dev]);
     return launch_dependent(few_ffn_kernel<DT, NT>, dim3(sm_count()), dim3(kFfnThreads), smem, s, a,
-                            sel);
+                            sel, tmX, tmH);
 }
 
 int sched_ints(const moe_config *c) { return 1 + kMaxGroups + c->hidden / 128; }
@@ -981,7 +1116,7 @@ int sched_ints(const moe_config *c) { return 1 + kMaxGroups + c->hidden / 128; }
 void few_layout(const moe_config *c, moe_few_layout *L) {
     const int64_t T = c->max_tokens, H = c->hidden, I = c->inter, k = c->top_k;
     const int64_t R = T * (k + c->num_shared);
-    const bool bf = c->dtype == MOE_DTYPE_BF16;
+    const bool bf = c->dtype == MOE_DTYPE_BF16, mx4 = c->dtype == MOE_DTYPE_MXFP4;
     size_t off = 0;
     auto take = [&](int64_t bytes) {
         const size_t o = off;
@@ -994,8 +1129,11 @@ void few_layout(const moe_config *c, moe_few_layout *L) {
     L->select = take(4 * T * c->num_experts);
     L->topk_ids = take(4 * T * k);
     L->topk_w = take(4 * T * k);
-    L->x16 = take(bf ? 0 : T * (H / 128) * kSegment);
-    L->h16 = take(bf ? 2 * R * I : R * (I / 128) * kSegment);
+    L->x = take(bf ? 0 : mx4 ? T * H / 2 : T * (H / 128) * kSegment);
+    L->x_scales = take(mx4 ? H / 128 * kMaxT * kScaleRow : 0);
+    L->h = take(bf ? 2 * R * I : mx4 ? R * I / 2 : R * (I / 128) * kSegment);
+    // a box of 16 rows may begin at any row
+    L->h_scales = take(mx4 ? I / 128 * (R + kMaxT) * kScaleRow : 0);
     L->y = take(4 * R * H);
     L->total = off;
 }
@@ -1033,7 +1171,8 @@ int launch_layer_few(const moe_config *c, const moe_weights *w, int T, const voi
     r.sel = sel;
     r.score = reinterpret_cast<float *>(b + L.score);
     r.select = reinterpret_cast<float *>(b + L.select);
-    r.x16 = b + L.x16;
+    r.xq = b + L.x;
+    r.xs = b + L.x_scales;
     r.sched = reinterpret_cast<int32_t *>(b + L.sched);
     r.status = sel.status;
     const int64_t warps = (int64_t)E * ceil_div(T, kTokChunk);
@@ -1059,8 +1198,11 @@ int launch_layer_few(const moe_config *c, const moe_weights *w, int T, const voi
     a.select = r.select;
     a.ids = reinterpret_cast<int32_t *>(b + L.topk_ids);
     a.wts = reinterpret_cast<float *>(b + L.topk_w);
-    a.xrows = c->dtype == MOE_DTYPE_BF16 ? static_cast<const uint8_t *>(x) : r.x16;
-    a.hrows = b + L.h16;
+    a.xrows = c->dtype == MOE_DTYPE_BF16 ? static_cast<const uint8_t *>(x) : r.xq;
+    a.hrows = b + L.h;
+    a.xs = r.xs;
+    a.hs = b + L.h_scales;
+    a.hs_rows = c->max_tokens * (c->top_k + S) + kMaxT;
     a.y = reinterpret_cast<float *>(b + L.y);
     a.out = out;
     a.sched = r.sched;

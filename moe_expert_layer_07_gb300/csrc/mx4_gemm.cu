@@ -71,32 +71,6 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(int sf) {
            ((uint32_t)(kTM >> 4) << 24) | ((uint32_t)sf << 29);
 }
 
-// K-major tile with rows of 64 bytes and 64-byte swizzle: 8-row groups 512
-// bytes apart
-__device__ __forceinline__ uint64_t sdesc_k_sw64(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(512 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)4 << 61);
-}
-// 32 rows of 16 bytes, no swizzle: 8-row groups 128 bytes apart
-__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(128 >> 4) << 32) |
-           ((uint64_t)1 << 46);
-}
-__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t sdesc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
-                 : "memory");
-}
-__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
-}
-
 struct Tile {
     int g, nt, row0, nvalid;
 };

@@ -88,15 +88,16 @@ def _nearest_error(shape, h):
 def _stored_h(shape, layer, R):
     I = shape.inter
     if shape.dtype == "bf16":
-        return layer.view("h16", torch.bfloat16, (R, I)).double()
-    # segments of 128 values: fp16 code values, then the scale (fp32) or four scale bytes
-    seg = layer.view("h16", torch.uint8, (R, I // 128, 272))
-    v = seg[..., :256].contiguous().view(torch.float16).double()
-    if shape.dtype == "fp8":
-        s = seg[..., 256:260].contiguous().view(torch.float32).double()
-        return (v * s).reshape(R, I)
-    s = torch.exp2(seg[..., 256:260].double() - 127).repeat_interleave(32, -1)
-    return (v * s).reshape(R, I)
+        return layer.view("h", torch.bfloat16, (R, I)).double()
+    if shape.dtype == "fp8":   # segments of 128 values: fp16 code values, then the fp32 scale
+        seg = layer.view("h", torch.uint8, (R, I // 128, 272))
+        v = seg[..., :256].contiguous().view(torch.float16).double()
+        return (v * seg[..., 256:260].contiguous().view(torch.float32).double()).reshape(R, I)
+    codes = layer.view("h", torch.uint8, (R, I // 2)).cpu().numpy()
+    most = layer.cfg.max_tokens * (shape.top_k + shape.num_shared) + 16
+    s = layer.view("h_scales", torch.uint8, (I // 128, most, 16))[:, :R, :4]
+    s = s.permute(1, 0, 2).reshape(R, I // 32).cpu().numpy()
+    return torch.tensor(mx4.dequantize(codes, s), device="cuda")
 
 
 def _check(shape, w, values, layer, out_dtype=torch.float32, T=None, log2phys=None):
