@@ -261,7 +261,7 @@ struct Traits {
     static constexpr int kWsOff = kTokOff + 2 * kTokHalf;   // FP8: the tiles' two scales
     static constexpr int kStage = (kWsOff + 16 + 127) / 128 * 128;
     static constexpr int kBWords = DT == DT_BF16 ? 8 : 16;  // B words a lane holds for a tile
-    static constexpr int kScale = 0, kScaleOff = 0;
+    static constexpr int kTiles = 2, kScale = 0, kScaleOff = 0;
     static constexpr int kMultipliers = kConsumers;         // warps that release a stage
     static constexpr int kReaders = kWarps - 1;             // warps that read a unit's number
 };
@@ -269,16 +269,17 @@ template <int NT>
 struct Traits<DT_MX4, NT> {
     static constexpr int kKT = 128;
     static constexpr int kTile = 8192, kScale = 512;
+    static constexpr int kTiles = 4;                        // two of gate and of up, or four of W2
     static constexpr int kTokBytes = 16 * 64, kTokScale = 16 * kScaleRow;
-    static constexpr int kTokOff = 2 * kTile, kScaleOff = kTokOff + 2 * kTokBytes;
-    static constexpr int kTokScaleOff = kScaleOff + 2 * kScale;
-    static constexpr int kStage = kTokScaleOff + 2 * 512;
+    static constexpr int kTokOff = kTiles * kTile, kScaleOff = kTokOff + kTiles * kTokBytes;
+    static constexpr int kTokScaleOff = kScaleOff + kTiles * kScale;
+    static constexpr int kStage = kTokScaleOff + kTiles * 512;
     static constexpr int kCopy = 0, kPitch = 0, kTokHalf = 0, kWsOff = 0, kBWords = 1;
     static constexpr int kMultipliers = 1;                  // the MMAs' commit
     static constexpr int kReaders = 1 + 1 + kPublishers;
     // tensor memory: two accumulators of gate and up (16 token columns each),
-    // then for each stage the scales of two weight and two token tiles
-    static constexpr int kTmemCols = 256, kSfCol = 64, kSfStage = 16;
+    // then for each stage the scales of four weight and four token tiles
+    static constexpr int kTmemCols = 256, kSfCol = 64, kSfStage = 32;
 };
 
 template <int NT>
@@ -307,7 +308,7 @@ struct Ring {
     static constexpr int kBytes = kAlign + kStages * Traits<DT, NT>::kStage + (int)sizeof(FewShared<NT>);
 };
 static_assert(Ring<DT_FP8, 1>::kStages == 5 && Ring<DT_FP8, 2>::kStages == 5 &&
-              Ring<DT_MX4, 2>::kStages >= 9 && Ring<DT_MX4, 1>::kStages <= 12, "depth of the rings");
+              Ring<DT_MX4, 1>::kStages == 5 && Ring<DT_MX4, 2>::kStages == 5, "depth of the rings");
 
 // Order-preserving integers of the selection values: larger is better, 0 is
 // not selectable (NaN and minus infinity, as warp_select treats them); the two
@@ -675,7 +676,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     // What a unit number stands for.
     struct Unit {
         bool gu;
-        int gi, tile, kb, steps;   // gate/up: a stage is one K tile of both blocks; down: two K tiles
+        int gi, tile, kb, steps, per;   // a stage takes `per` tiles along K (gate/up: of both blocks)
     };
     auto unit_of = [&](int u) {
         Unit r;
@@ -684,7 +685,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         r.gi = v / per;
         r.tile = v % per;
         r.kb = r.gu ? kb1 : kb2;
-        r.steps = r.gu ? r.kb : (r.kb + 1) / 2;
+        r.per = r.gu ? TR::kTiles / 2 : TR::kTiles;
+        r.steps = (r.kb + r.per - 1) / r.per;
         return r;
     };
     // The it-th unit of this CTA (-1: no more), as every warp but the producer
@@ -729,16 +731,16 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                     break;
                 }
                 const uint32_t dst = ptx::smem_u32(ring + st * TR::kStage);
-                const size_t i0 = un.gu ? b0 + s : b0 + 2 * s, i1 = un.gu ? b1 + s : i0 + 1;
-                const bool two = un.gu || 2 * s + 1 < un.kb;
-                ptx::mbar_arrive_expect_tx(full, (two ? 2 : 1) * (TR::kTile + TR::kScale));
-                ptx::bulk_load(dst, w + i0 * TR::kTile, TR::kTile, full, policy);
-                if (two) ptx::bulk_load(dst + TR::kTile, w + i1 * TR::kTile, TR::kTile, full, policy);
-                if constexpr (MX4) {
-                    ptx::bulk_load(dst + TR::kScaleOff, ws + i0 * TR::kScale, TR::kScale, full, policy);
-                    if (two)
-                        ptx::bulk_load(dst + TR::kScaleOff + TR::kScale, ws + i1 * TR::kScale, TR::kScale, full,
-                                       policy);
+                // `nk` tiles of a row block are consecutive: one copy
+                const int k0 = s * un.per, nk = min(un.per, un.kb - k0);
+                ptx::mbar_arrive_expect_tx(full, (un.gu ? 2 : 1) * nk * (TR::kTile + TR::kScale));
+                for (int h = 0; h < (un.gu ? 2 : 1); ++h) {   // up in the second half of the stage
+                    const size_t i = (h ? b1 : b0) + k0;
+                    const uint32_t at = h * (TR::kTiles / 2);
+                    ptx::bulk_load(dst + at * TR::kTile, w + i * TR::kTile, nk * TR::kTile, full, policy);
+                    if constexpr (MX4)
+                        ptx::bulk_load(dst + TR::kScaleOff + at * TR::kScale, ws + i * TR::kScale, nk * TR::kScale,
+                                       full, policy);
                 }
                 ++issued;
             }
@@ -794,7 +796,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 uint8_t *base = ring + st * TR::kStage;
-                const int k0 = un.gu ? s : 2 * s, nk = un.gu ? 1 : min(2, un.kb - k0);
+                const int k0 = s * un.per, nk = min(un.per, un.kb - k0);
                 if constexpr (MX4) {
                     // 16 rows whatever the group's: x's are all tokens, h's
                     // begin at the group's first (rows past its last are not used)
@@ -993,20 +995,23 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                         ptx::tc_fence_after();
                         const uint32_t base = ptx::smem_u32(ring + st * TR::kStage);
                         const uint32_t sf = tmem + TR::kSfCol + st * TR::kSfStage;
-                        const bool two = un.gu || 2 * s + 1 < un.kb;
-                        ptx::tmem_copy_scales(sf, ptx::sdesc_scales(base + TR::kScaleOff));
-                        ptx::tmem_copy_scales(sf + 8, ptx::sdesc_scales(base + TR::kTokScaleOff));
-                        mma_tile_mxf4(acc, base, base + TR::kTokOff, sf, sf + 8, s > 0);
-                        if (two) {
-                            // gate/up: the up rows against the same tokens, into
-                            // the other accumulator; down: the next tile of K
-                            const int k = un.gu ? 0 : 1;
-                            ptx::tmem_copy_scales(sf + 4, ptx::sdesc_scales(base + TR::kScaleOff + TR::kScale));
-                            if (k)
-                                ptx::tmem_copy_scales(sf + 12, ptx::sdesc_scales(base + TR::kTokScaleOff + 512));
-                            mma_tile_mxf4(un.gu ? acc + 16 : acc, base + TR::kTile,
-                                          base + TR::kTokOff + k * TR::kTokBytes, sf + 4, sf + 8 + 4 * k,
-                                          un.gu ? s > 0 : true);
+                        const int nk = min(un.per, un.kb - s * un.per);
+                        // scales of all tiles first: a product waits for the
+                        // copies in front of it
+                        for (int k = 0; k < nk; ++k) {
+                            ptx::tmem_copy_scales(sf + 4 * k, ptx::sdesc_scales(base + TR::kScaleOff + k * TR::kScale));
+                            ptx::tmem_copy_scales(sf + 16 + 4 * k,
+                                                  ptx::sdesc_scales(base + TR::kTokScaleOff + k * 512));
+                            if (un.gu)
+                                ptx::tmem_copy_scales(
+                                    sf + 4 * (k + 2), ptx::sdesc_scales(base + TR::kScaleOff + (k + 2) * TR::kScale));
+                        }
+                        for (int k = 0; k < nk; ++k) {
+                            const uint32_t tok = base + TR::kTokOff + k * TR::kTokBytes;
+                            mma_tile_mxf4(acc, base + k * TR::kTile, tok, sf + 4 * k, sf + 16 + 4 * k, s + k > 0);
+                            if (un.gu)   // the up rows against the same tokens
+                                mma_tile_mxf4(acc + 16, base + (k + 2) * TR::kTile, tok, sf + 4 * (k + 2),
+                                              sf + 16 + 4 * k, s + k > 0);
                         }
                         ptx::mma_commit(ptx::smem_u32(&sh.empty[st]));
                     }
