@@ -84,7 +84,7 @@ struct FewArgs {
     int hs_rows;
     float *y;                      // [rows, H]
     void *out;
-    int32_t *sched;                // unit counter | h_done[kMaxGroups] | col_done[H/128]
+    int32_t *sched;                // unit counter | h_done[kMaxGroups] | col_done[H/128][kPublishers]
     int32_t *status;
 };
 
@@ -276,7 +276,8 @@ struct Traits<DT_MX4, NT> {
     static constexpr int kStage = kTokScaleOff + kTiles * 512;
     static constexpr int kCopy = 0, kPitch = 0, kTokHalf = 0, kWsOff = 0, kBWords = 1;
     static constexpr int kMultipliers = 1;                  // the MMAs' commit
-    static constexpr int kReaders = 1 + 1 + kPublishers;
+    static constexpr int kScalers = 4;                      // warps 4..7: a lane quarter each
+    static constexpr int kReaders = 1 + kScalers + 1 + kPublishers;
     // tensor memory: two accumulators of gate and up (16 token columns each),
     // then for each stage the scales of four weight and four token tiles
     static constexpr int kTmemCols = 256, kSfCol = 64, kSfStage = 32;
@@ -284,12 +285,12 @@ struct Traits<DT_MX4, NT> {
 
 template <int NT>
 struct FewShared {   // after the ring
-    uint64_t full[16], empty[16];
+    uint64_t full[16], empty[16], sf_full[16];
     uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
-    uint64_t res_full[2], res_empty[2], pub_sync, drain;
+    uint64_t res_full[2], res_empty[2], drain;
     uint32_t tmem_slot;
     int32_t unit[kUnitSlots];
-    int abort, last, n_groups;
+    int abort, n_groups;
     int32_t ids[kMaxSlots];
     float wts[kMaxSlots];
     int16_t slot_row[kMaxSlots], first_id[kMaxSlots];
@@ -557,6 +558,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(ptx::smem_u32(&sh.full[s]), 2);   // the weights' thread, the tokens' warp
             ptx::mbar_init(ptx::smem_u32(&sh.empty[s]), TR::kMultipliers);
+            if constexpr (MX4) ptx::mbar_init(ptx::smem_u32(&sh.sf_full[s]), TR::kScalers);
         }
         for (int s = 0; s < kUnitSlots; ++s) {
             ptx::mbar_init(ptx::smem_u32(&sh.unit_full[s]), 1);
@@ -566,7 +568,6 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             ptx::mbar_init(ptx::smem_u32(&sh.res_full[s]), TR::kMultipliers);
             ptx::mbar_init(ptx::smem_u32(&sh.res_empty[s]), kPublishers);
         }
-        ptx::mbar_init(ptx::smem_u32(&sh.pub_sync), kPublishers);
         ptx::mbar_init(ptx::smem_u32(&sh.drain), 1);
         ptx::fence_mbar_init();
         sh.abort = 0;
@@ -777,7 +778,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             }
             if (!un.gu) {   // all units of the group's h, from whichever CTAs
                 ok = lane ? true
-                          : ptx::wait_flag_geq(h_done + un.gi, mt1, abort_flag, a.status, MOE_DEV_TIMEOUT);
+                          : ptx::wait_flag_geq(h_done + un.gi, mt1 * kPublishers, abort_flag, a.status, MOE_DEV_TIMEOUT);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 ptx::fence_proxy_async_global();
@@ -834,14 +835,56 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     } else if (warp >= kFirstPublisher) {
         // ---- results: h to its format and to memory, y to memory, the combine --------
         const int pw = warp - kFirstPublisher;
-        uint32_t parity = 0;
-        auto pub_sync = [&]() -> bool {   // all publishers; bounded
-            __syncwarp();
-            const uint32_t bar = ptx::smem_u32(&sh.pub_sync);
-            if (lane == 0) ptx::mbar_arrive(bar);
-            const bool ok = ptx::wait_bounded(bar, parity, abort_flag, a.status, MOE_DEV_TIMEOUT);
-            parity ^= 1;
-            return __all_sync(0xffffffffu, ok);
+        // Each of the four warps finishes a unit for itself: no barrier among
+        // them.  In a down unit warp quarter `q` has 32 of the 128 columns.
+        const int q = MX4 ? warp & 3 : pw;   // MXFP4: the lane quarter the warp can read
+        // Combines columns [32 q, 32 q + 32) of a tile for all tokens: lane
+        // i = (token, four columns).
+        auto combine = [&](int tile) {
+            for (int i = lane; i < a.T * 8; i += 32) {
+                const int t = i >> 3;
+                const size_t col = tile * 128 + 32 * q + (i & 7) * 4;
+                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                const float *y = a.y + col;
+                for (int s = 0; s < a.S; ++s) {
+                    const float4 r = __ldcg(reinterpret_cast<const float4 *>(y + (size_t)(s * a.T + t) * a.H));
+                    o.x = __fadd_rn(o.x, r.x), o.y = __fadd_rn(o.y, r.y);
+                    o.z = __fadd_rn(o.z, r.z), o.w = __fadd_rn(o.w, r.w);
+                }
+                for (int j0 = 0; j0 < a.k; j0 += 8) {   // eight rows' loads, then their sums in order
+                    float4 r[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int row = j0 + j < a.k ? sh.slot_row[t * a.k + j0 + j] : -1;
+                        r[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (row >= 0) r[j] = __ldcg(reinterpret_cast<const float4 *>(y + (size_t)row * a.H));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if (j0 + j >= a.k || sh.slot_row[t * a.k + j0 + j] < 0) continue;
+                        const float w = sh.wts[t * a.k + j0 + j];
+                        o.x = fmaf(w, r[j].x, o.x), o.y = fmaf(w, r[j].y, o.y);
+                        o.z = fmaf(w, r[j].z, o.z), o.w = fmaf(w, r[j].w, o.w);
+                    }
+                }
+                const size_t at = (size_t)t * a.H + col;
+                if (a.out_bf16) {
+                    __nv_bfloat162 b0 = __floats2bfloat162_rn(o.x, o.y), b1 = __floats2bfloat162_rn(o.z, o.w);
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
+                        make_uint2(*reinterpret_cast<uint32_t *>(&b0), *reinterpret_cast<uint32_t *>(&b1));
+                } else {
+                    *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = o;
+                }
+            }
+        };
+        // A down unit's count comes back while the next unit is worked on.
+        int pending = -1, before = 0;
+        auto finish_pending = [&]() {
+            if (pending >= 0 && __shfl_sync(0xffffffffu, before, 0) == nG - 1) {
+                __threadfence();   // all groups' rows of these columns are there
+                combine(pending);
+            }
+            pending = -1;
         };
         for (int it = 0;; ++it) {
             const int u = take_unit(it);
@@ -854,7 +897,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             if constexpr (MX4) {
                 // this warp's lane quarter of tensor memory: 32 of the 128 rows,
                 // for gate/up one block of h's scales
-                const int q = warp & 3, m = 32 * q + lane;
+                const int m = 32 * q + lane;
                 const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + buf * 32;
                 uint32_t d[16], up[16];
                 ptx::tc_fence_after();
@@ -897,81 +940,46 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                         if (c < n) a.y[(size_t)(row0 + c) * a.H + un.tile * 128 + m] = __uint_as_float(d[c]);
                 }
             }
-            for (int c = pw; !MX4 && c < n; c += kPublishers) {
-                const float4 q = *reinterpret_cast<const float4 *>(&sh.res[buf][c][lane * 4]);
-                const size_t row = row0 + c;
-                if (!un.gu) {
-                    *reinterpret_cast<float4 *>(a.y + row * a.H + un.tile * 128 + lane * 4) = q;
-                } else if (DT == DT_BF16) {
-                    __nv_bfloat162 b0 = __floats2bfloat162_rn(q.x, q.y), b1 = __floats2bfloat162_rn(q.z, q.w);
-                    *reinterpret_cast<uint2 *>(a.hrows + (row * a.I + un.tile * 128 + lane * 4) * 2) =
-                        make_uint2(*reinterpret_cast<uint32_t *>(&b0), *reinterpret_cast<uint32_t *>(&b1));
-                } else {
-                    uint8_t *seg = a.hrows + (row * mt1 + un.tile) * kSegment;
-                    float m = fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)), fmaxf(fabsf(q.z), fabsf(q.w)));
+            if constexpr (!MX4) {
+                if (un.gu) {
+                    for (int c = pw; c < n; c += kPublishers) {
+                        const float4 v = *reinterpret_cast<const float4 *>(&sh.res[buf][c][lane * 4]);
+                        const size_t row = row0 + c;
+                        if (DT == DT_BF16) {
+                            __nv_bfloat162 b0 = __floats2bfloat162_rn(v.x, v.y), b1 = __floats2bfloat162_rn(v.z, v.w);
+                            *reinterpret_cast<uint2 *>(a.hrows + (row * a.I + un.tile * 128 + lane * 4) * 2) =
+                                make_uint2(*reinterpret_cast<uint32_t *>(&b0), *reinterpret_cast<uint32_t *>(&b1));
+                        } else {
+                            uint8_t *seg = a.hrows + (row * mt1 + un.tile) * kSegment;
+                            float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
-                    for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                    const float sc = fp8_group_scale(m), inv = fp8_group_inv(sc);
-                    const uint2 o = fp8_as_half4(__fmul_rn(q.x, inv), __fmul_rn(q.y, inv),
-                                                 __fmul_rn(q.z, inv), __fmul_rn(q.w, inv));
-                    if (lane == 0) *reinterpret_cast<float *>(seg + 256) = sc;
-                    *reinterpret_cast<uint2 *>(seg + lane * 8) = o;
+                            for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                            const float sc = fp8_group_scale(m), inv = fp8_group_inv(sc);
+                            const uint2 o = fp8_as_half4(__fmul_rn(v.x, inv), __fmul_rn(v.y, inv),
+                                                         __fmul_rn(v.z, inv), __fmul_rn(v.w, inv));
+                            if (lane == 0) *reinterpret_cast<float *>(seg + 256) = sc;
+                            *reinterpret_cast<uint2 *>(seg + lane * 8) = o;
+                        }
+                    }
+                } else {
+                    for (int c = 0; c < n; ++c)
+                        a.y[(size_t)(row0 + c) * a.H + un.tile * 128 + 32 * q + lane] = sh.res[buf][c][32 * q + lane];
                 }
-            }
-            if (!MX4) {
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.res_empty[buf]));
             }
             if (un.gu) ptx::fence_proxy_async_global();   // h is read by copies
             __threadfence();
-            if (!pub_sync()) break;   // every publisher's rows are out
+            __syncwarp();
+            finish_pending();
             if (un.gu) {
-                if (pw == 0 && lane == 0) ptx::red_release_gpu_add(h_done + un.gi, 1);
-                continue;
-            }
-            if (pw == 0 && lane == 0) {
-                sh.last = atomicAdd(col_done + un.tile, 1) == nG - 1;
-                __threadfence();
-            }
-            if (!pub_sync()) break;
-            if (!*reinterpret_cast<volatile int *>(&sh.last)) continue;
-            // all groups' rows of these columns are there: the combine
-            for (int i = pw * 32 + lane; i < a.T * 32; i += kPublishers * 32) {
-                const int t = i >> 5;
-                const size_t col = un.tile * 128 + (i & 31) * 4;
-                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                const float *y = a.y + col;
-                for (int s = 0; s < a.S; ++s) {
-                    const float4 r = __ldcg(reinterpret_cast<const float4 *>(y + (size_t)(s * a.T + t) * a.H));
-                    o.x = __fadd_rn(o.x, r.x), o.y = __fadd_rn(o.y, r.y);
-                    o.z = __fadd_rn(o.z, r.z), o.w = __fadd_rn(o.w, r.w);
-                }
-                for (int j0 = 0; j0 < a.k; j0 += 8) {   // eight rows' loads, then their sums in order
-                    float4 r[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int row = j0 + j < a.k ? sh.slot_row[t * a.k + j0 + j] : -1;
-                        r[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (row >= 0) r[j] = __ldcg(reinterpret_cast<const float4 *>(y + (size_t)row * a.H));
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        if (j0 + j >= a.k || sh.slot_row[t * a.k + j0 + j] < 0) continue;
-                        const float w = sh.wts[t * a.k + j0 + j];
-                        o.x = fmaf(w, r[j].x, o.x), o.y = fmaf(w, r[j].y, o.y);
-                        o.z = fmaf(w, r[j].z, o.z), o.w = fmaf(w, r[j].w, o.w);
-                    }
-                }
-                const size_t at = (size_t)t * a.H + col;
-                if (a.out_bf16) {
-                    __nv_bfloat162 b0 = __floats2bfloat162_rn(o.x, o.y), b1 = __floats2bfloat162_rn(o.z, o.w);
-                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
-                        make_uint2(*reinterpret_cast<uint32_t *>(&b0), *reinterpret_cast<uint32_t *>(&b1));
-                } else {
-                    *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = o;
-                }
+                if (lane == 0) ptx::red_release_gpu_add(h_done + un.gi, 1);
+            } else {
+                if (lane == 0) before = atomicAdd(col_done + un.tile * kPublishers + q, 1);
+                pending = un.tile;
             }
         }
+        finish_pending();
     } else if constexpr (MX4) {
         // ---- products (MXFP4): one thread issues them -------------------------------
         if (warp == 0) {
@@ -989,23 +997,13 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                     const uint32_t acc = tmem + buf * 32;
                     for (int s = 0; ok && s < un.steps; ++s) {
                         const int st = (stage + s) % kStages;
-                        ok = ptx::wait_bounded(ptx::smem_u32(&sh.full[st]), ((stage + s) / kStages) & 1,
+                        ok = ptx::wait_bounded(ptx::smem_u32(&sh.sf_full[st]), ((stage + s) / kStages) & 1,
                                                abort_flag, a.status, MOE_DEV_TIMEOUT);
                         if (!ok) break;
                         ptx::tc_fence_after();
                         const uint32_t base = ptx::smem_u32(ring + st * TR::kStage);
                         const uint32_t sf = tmem + TR::kSfCol + st * TR::kSfStage;
                         const int nk = min(un.per, un.kb - s * un.per);
-                        // scales of all tiles first: a product waits for the
-                        // copies in front of it
-                        for (int k = 0; k < nk; ++k) {
-                            ptx::tmem_copy_scales(sf + 4 * k, ptx::sdesc_scales(base + TR::kScaleOff + k * TR::kScale));
-                            ptx::tmem_copy_scales(sf + 16 + 4 * k,
-                                                  ptx::sdesc_scales(base + TR::kTokScaleOff + k * 512));
-                            if (un.gu)
-                                ptx::tmem_copy_scales(
-                                    sf + 4 * (k + 2), ptx::sdesc_scales(base + TR::kScaleOff + (k + 2) * TR::kScale));
-                        }
                         for (int k = 0; k < nk; ++k) {
                             const uint32_t tok = base + TR::kTokOff + k * TR::kTokBytes;
                             mma_tile_mxf4(acc, base + k * TR::kTile, tok, sf + 4 * k, sf + 16 + 4 * k, s + k > 0);
@@ -1023,6 +1021,39 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             if (lane == 0) {   // every product has landed before the columns are given up
                 ptx::mma_commit(ptx::smem_u32(&sh.drain));
                 ptx::wait_drain(ptx::smem_u32(&sh.drain), 0);
+            }
+        } else if (warp >= kConsumers - TR::kScalers && warp < kConsumers) {
+            // ---- scales to tensor memory: each of these warps writes its lane
+            // quarter.  The tensor pipe's own copies (tcgen05.cp) took about 100
+            // cycles each in line with products of about 118, three to every four.
+            const uint32_t quarter = (uint32_t)(warp & 3) << 21;   // lane 32 (warp & 3)
+            int stage = 0;
+            bool ok = true;
+            for (int it = 0; ok; ++it) {
+                const int u = take_unit(it);
+                if (u < 0) break;
+                const Unit un = unit_of(u);
+                for (int s = 0; s < un.steps; ++s, ++stage) {
+                    const int st = stage % kStages;
+                    ok = ptx::wait_bounded(ptx::smem_u32(&sh.full[st]), (stage / kStages) & 1, abort_flag,
+                                           a.status, MOE_DEV_TIMEOUT);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint8_t *base = ring + st * TR::kStage;
+                    const uint32_t sf = tmem + quarter + TR::kSfCol + st * TR::kSfStage;
+                    const int nk = min(un.per, un.kb - s * un.per);
+#pragma unroll
+                    for (int k = 0; k < TR::kTiles; ++k)   // a slot without a tile: not used
+                        ptx::tmem_st4(sf + 4 * k, *reinterpret_cast<const uint4 *>(
+                                                      base + TR::kScaleOff + k * TR::kScale + lane * 16));
+                    for (int k = 0; k < nk; ++k)
+                        ptx::tmem_st1(sf + 16 + 4 * k, *reinterpret_cast<const uint32_t *>(
+                                                           base + TR::kTokScaleOff + k * 512 + lane * 16));
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.sf_full[st]));
+                }
             }
         }
     } else if (warp < kConsumers) {
@@ -1114,7 +1145,7 @@ int launch_ffn(const FewArgs &a, const SelectArgs &sel, cudaStream_t s) {
                             sel, tmX, tmH);
 }
 
-int sched_ints(const moe_config *c) { return 1 + kMaxGroups + c->hidden / 128; }
+int sched_ints(const moe_config *c) { return 1 + kMaxGroups + c->hidden / 128 * kPublishers; }
 
 }  // namespace
 
