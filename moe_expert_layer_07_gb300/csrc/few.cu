@@ -101,8 +101,6 @@ struct RouteArgs {
     float *score, *select;   // [T, E]: SelectArgs' scores (softmax: logits), what it compares
     uint8_t *xq, *xs;
     int32_t *sched, *status;
-    const uint8_t *pf[2];       // weights to bring into L2 (the shared experts')
-    size_t pf_bytes[2];
 };
 
 __device__ __forceinline__ void bf8(const uint4 &a, float (&f)[8]) {
@@ -198,22 +196,17 @@ __device__ __forceinline__ void quant_segment(const RouteArgs &a, int t, int seg
 __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const RouteArgs a) {
     ptx::pdl_launch_dependents();
     const int gtid = blockIdx.x * kRouteThreads + threadIdx.x, nthreads = gridDim.x * kRouteThreads;
-#pragma unroll
-    for (int p = 0; p < 2; ++p)   // a hint: 16 KB for each thread that takes part
-        for (size_t o = (size_t)gtid * 16384; o < a.pf_bytes[p]; o += (size_t)nthreads * 16384)
-            ptx::prefetch_l2(a.pf[p] + o, (uint32_t)min((size_t)16384, a.pf_bytes[p] - o));
+    const int lane = threadIdx.x & 31, warp = gtid >> 5;
+    const int chunks = (a.T + kTokChunk - 1) / kTokChunk;
+    const int e = warp / chunks, t0 = warp % chunks * kTokChunk;
     ptx::pdl_wait();   // x, and the last call's use of the workspace
-    const int lane = threadIdx.x & 31;
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
     for (int i = gtid; i < a.sched_ints; i += nthreads) a.sched[i] = 0;
-    const int warp = (blockIdx.x * kRouteThreads + threadIdx.x) >> 5;
     if ((int)blockIdx.x >= a.logit_blocks) {
         const int q = warp - a.logit_blocks * (kRouteThreads / 32), segs = (a.H + 255) / 256;
         if (q < a.T * segs) quant_segment(a, q / segs, q % segs, lane);
         return;
     }
-    const int chunks = (a.T + kTokChunk - 1) / kTokChunk;
-    const int e = warp / chunks, t0 = warp % chunks * kTokChunk;
     if (e >= a.E) return;
     const int nt = min(kTokChunk, a.T - t0);
     const uint16_t *w = a.wg + (size_t)e * a.H, *x = a.x + (size_t)t0 * a.H;
@@ -323,13 +316,60 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return k == 0u ? -FLT_MAX : __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k);
 }
 
-// warp_select's choice and weights (the same bits) in rolled loops over shared
-// memory: every CTA runs this once, with a cold instruction cache, where
-// warp_select's unrolled registers took 15 us of 84 (one token, 256 experts)
-// and this takes 2.  key, score: this warp's rows of E; ids, wts: the token's
-// top_k.
-__device__ __noinline__ void few_select(const SelectArgs &a, int lane, uint32_t *key, const float *score,
-                                        int32_t *ids, float *wts) {
+// The top_k of a token in order, lane j keeping the j-th's index; false if
+// there are fewer candidates.  Experts e = 32 q + lane in registers, groups (if
+// any) of 32: a group is one register of the warp, and one reduction each
+// gives its best.
+__device__ __forceinline__ bool choose_in_registers(const SelectArgs &a, int lane, const uint32_t *key,
+                                                    int &my_id) {
+    uint32_t k[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) k[q] = 32 * q + lane < a.E ? key[32 * q + lane] : 0u;
+    if (a.groups > 1) {
+        uint32_t left[8], gk[8];
+        float sum[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) left[q] = k[q];
+        for (int r = 0; r < a.topn; ++r) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const uint32_t m = __reduce_max_sync(0xffffffffu, left[q]);
+                const uint32_t at = __ballot_sync(0xffffffffu, left[q] == m);
+                if (lane == __ffs(at) - 1) left[q] = 0u;
+                sum[q] = r == 0 ? key_value(m) : __fadd_rn(sum[q], key_value(m));
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) gk[q] = q < a.groups ? order_key(sum[q]) : 0u;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            int rank = 0;
+#pragma unroll
+            for (int o = 0; o < 8; ++o) rank += gk[o] > gk[q] || (gk[o] == gk[q] && o < q);
+            if (gk[q] == 0u || rank >= a.topk_groups) k[q] = 0u;
+        }
+    }
+    for (int j = 0; j < a.k; ++j) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) best = max(best, k[q]);
+        const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+        if (m == 0u) return false;
+        int at = INT_MAX;
+#pragma unroll
+        for (int q = 7; q >= 0; --q)
+            if (k[q] == m) at = 32 * q + lane;
+        const int id = (int)__reduce_min_sync(0xffffffffu, (uint32_t)at);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (32 * q + lane == id) k[q] = 0u;
+        if (lane == j) my_id = id;
+    }
+    return true;
+}
+
+// The same for any number and size of groups, in loops over shared memory.
+__device__ __noinline__ bool choose_in_memory(const SelectArgs &a, int lane, uint32_t *key, int &my_id) {
     if (a.groups > 1) {
         const int gs = a.E / a.groups;
         float sum = 0.0f;
@@ -362,22 +402,33 @@ __device__ __noinline__ void few_select(const SelectArgs &a, int lane, uint32_t 
         __syncwarp();
     }
     uint32_t pk = 0xffffffffu;
-    int pi = -1, my_id = 0;
+    int pi = -1;
     for (int j = 0; j < a.k; ++j) {   // the next one in (value, index) order
         uint32_t bk = 0;
         int bi = INT_MAX;
-#pragma unroll 4
         for (int e = lane; e < a.E; e += 32) {
             const uint32_t k = key[e];
             if ((k < pk || (k == pk && e > pi)) && k > bk) bk = k, bi = e;
         }
         pk = __reduce_max_sync(0xffffffffu, bk);
-        if (pk == 0u) {   // fewer candidates than k
-            if (lane == 0 && a.status) atomicOr(a.status, MOE_DEV_BAD_EXPERT_ID);
-            return;
-        }
+        if (pk == 0u) return false;
         pi = (int)__reduce_min_sync(0xffffffffu, (uint32_t)(bk == pk ? bi : INT_MAX));
         if (lane == j) my_id = pi;
+    }
+    return true;
+}
+
+// warp_select's choice and weights (the same bits).  Every CTA runs this once,
+// with a cold instruction cache: warp_select's unrolled shuffles took 15 us of
+// the 84 that one token of the 256-expert layer took.  key, score: this warp's
+// rows of E in shared memory; ids, wts: the token's top_k.
+__device__ __noinline__ void few_select(const SelectArgs &a, int lane, uint32_t *key, const float *score,
+                                        int32_t *ids, float *wts) {
+    int my_id = 0;
+    const bool regs = a.E <= 256 && (a.groups == 1 || a.E == 32 * a.groups);
+    if (!(regs ? choose_in_registers(a, lane, key, my_id) : choose_in_memory(a, lane, key, my_id))) {
+        if (lane == 0 && a.status) atomicOr(a.status, MOE_DEV_BAD_EXPERT_ID);   // fewer candidates than k
+        return;
     }
     const float mine = score[my_id];
     float w = 0.0f;

@@ -146,6 +146,18 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
                  "l"(reinterpret_cast<uint64_t>(src))
                  : "memory");
 }
+// 16 bytes past L1, in groups: cp_async_wait<N> waits until at most N of this
+// thread's newest groups are still on their way.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src))
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 // The mbarrier receives one arrival once this thread's earlier cp.async
 // copies have landed (the arrival counts toward the barrier's init count).
 __device__ __forceinline__ void cp_async_mbar_arrive(uint32_t bar) {
