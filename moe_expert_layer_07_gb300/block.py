@@ -9,6 +9,8 @@ from __future__ import annotations
 
 import ctypes
 
+import torch
+
 from . import (LAYOUT_ROWS, LAYOUT_TILES, MXFP4, OUT_BF16, OUT_F32, Config, Weights,
                _check, _CP, _I, _P, _ptr, _stream, get_device_status, lib, make_config,
                pack_expert_weights)
@@ -45,28 +47,27 @@ _SIGS = {
 
 def _out_type(t) -> int:
     """MOE_OUT_* of a tensor."""
-    import torch
-    if t.dtype == torch.float32:
-        return OUT_F32
-    if t.dtype == torch.bfloat16:
+    d = t.dtype
+    if d is torch.bfloat16:
         return OUT_BF16
-    raise TypeError(f"expected a float32 or bfloat16 tensor, got {t.dtype}")
+    if d is torch.float32:
+        return OUT_F32
+    raise TypeError(f"expected a float32 or bfloat16 tensor, got {d}")
 
 
 def _dense(t, shape, name):
     """t itself, once it is a contiguous device tensor of this shape."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous CUDA tensor")
     return t
 
 
-def _bytes(t, name):
-    import torch
-    if t.dtype != torch.uint8:
+def _bytes(t, shape, name):
+    if t.dtype is not torch.uint8:
         raise TypeError(f"{name}: expected a uint8 tensor, got {t.dtype}")
-    return t
+    return _dense(t, shape, name)
 
 
 # ---- MXFP4 ------------------------------------------------------------------------------
@@ -74,46 +75,47 @@ def _bytes(t, name):
 
 def mx4_quantize(x, codes=None, scales=None, stream=None):
     """x fp32 or bf16 [..., cols] -> (codes uint8 [..., cols/2], scales uint8 [..., cols/32])."""
-    import torch
-    cols = x.shape[-1]
-    lead = tuple(x.shape[:-1])
-    _dense(x, x.shape, "x")
+    shape = x.shape
+    lead, cols = shape[:-1], shape[-1]
+    kind = _out_type(_dense(x, shape, "x"))
+    ctail, stail = lead + (cols // 2,), lead + (cols // 32,)
     if codes is None:
-        codes = torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=x.device)
+        codes = torch.empty(ctail, dtype=torch.uint8, device=x.device)
     if scales is None:
-        scales = torch.empty(lead + (cols // 32,), dtype=torch.uint8, device=x.device)
-    _bytes(_dense(codes, lead + (cols // 2,), "codes"), "codes")
-    _bytes(_dense(scales, lead + (cols // 32,), "scales"), "scales")
-    rows = x.numel() // cols if cols else 0
-    _check(lib().moe_mx4_quantize(rows, cols, _ptr(x), _out_type(x), _ptr(codes), _ptr(scales),
-                                  _stream(stream)), "moe_mx4_quantize")
+        scales = torch.empty(stail, dtype=torch.uint8, device=x.device)
+    _bytes(codes, ctail, "codes")
+    _bytes(scales, stail, "scales")
+    rc = lib().moe_mx4_quantize(x.numel() // cols if cols else 0, cols, x.data_ptr(), kind,
+                                codes.data_ptr(), scales.data_ptr(), _stream(stream))
+    if rc:
+        _check(rc, "moe_mx4_quantize")
     return codes, scales
 
 
 def mx4_dequantize(codes, scales, out=None, stream=None):
     """The values [..., cols] (a new bf16 tensor unless `out`, fp32 or bf16, is given)."""
-    import torch
-    cols = codes.shape[-1] * 2
-    lead = tuple(codes.shape[:-1])
-    _bytes(_dense(codes, codes.shape, "codes"), "codes")
-    _bytes(_dense(scales, lead + (cols // 32,), "scales"), "scales")
+    shape = codes.shape
+    lead, half = shape[:-1], shape[-1]
+    cols = 2 * half
+    _bytes(codes, shape, "codes")
+    _bytes(scales, lead + (cols // 32,), "scales")
     if out is None:
         out = torch.empty(lead + (cols,), dtype=torch.bfloat16, device=codes.device)
     _dense(out, lead + (cols,), "out")
-    rows = codes.numel() * 2 // cols if cols else 0
-    _check(lib().moe_mx4_dequantize(rows, cols, _ptr(codes), _ptr(scales), _ptr(out),
-                                    _out_type(out), _stream(stream)), "moe_mx4_dequantize")
+    rc = lib().moe_mx4_dequantize(codes.numel() // half if half else 0, cols, codes.data_ptr(),
+                                  scales.data_ptr(), out.data_ptr(), _out_type(out), _stream(stream))
+    if rc:
+        _check(rc, "moe_mx4_dequantize")
     return out
 
 
 def pack_mx4_weights(codes, scales, stream=None):
     """Row-major MXFP4 weights (codes [G, N, K/2], scales [G, N, K/32]) -> new tensors of the
     same shapes in the tile layout that the products and the few-token layer read."""
-    import torch
     G, N, half = codes.shape
     K = 2 * half
-    _bytes(_dense(codes, (G, N, half), "codes"), "codes")
-    _bytes(_dense(scales, (G, N, K // 32), "scales"), "scales")
+    _bytes(codes, (G, N, half), "codes")
+    _bytes(scales, (G, N, K // 32), "scales")
     w, ws = torch.empty_like(codes), torch.empty_like(scales)
     _check(lib().moe_mx4_pack_weights(G, N, K, _ptr(codes), _ptr(scales), _ptr(w), _ptr(ws),
                                       _stream(stream)), "moe_mx4_pack_weights")
@@ -174,7 +176,6 @@ class FewTokenLayer:
     """
 
     def __init__(self, shape, weights, max_tokens: int | None = None, log2phys=None):
-        import torch
         n = layer_few_max_tokens() if max_tokens is None else max_tokens
         self.shape = shape
         self.cfg = make_config(shape, n)
@@ -220,7 +221,6 @@ class FewTokenLayer:
     def view(self, name, dtype, shape):
         """A tensor view of one part of the workspace (topk_ids, topk_w, ...)."""
         import math
-        import torch
         off = getattr(self.layout, name)
         nbytes = math.prod(shape) * torch.empty((), dtype=dtype).element_size()
         return self.ws[off:off + nbytes].view(dtype).view(*shape)
@@ -243,34 +243,42 @@ def block_norm(residual, y=None, residual_out=None, x_out=None, w_post=None, b_p
 
     residual, y [T, H] fp32 or bf16; residual_out of residual's type (may be it), or None; x_out
     bf16, or None; gate [H], [T] or [T, H] (for T == H a one-dimensional gate is by feature)."""
-    import torch
-    T, H = residual.shape
-    params = [t for t in (w_post, b_post, w_pre, b_pre, gate) if t is not None]
-    ptype = _out_type(params[0]) if params else OUT_BF16
-    for name, t, shape in (("residual", residual, (T, H)), ("y", y, (T, H)),
-                           ("residual_out", residual_out, (T, H)), ("x_out", x_out, (T, H)),
-                           ("w_post", w_post, (H,)), ("b_post", b_post, (H,)),
-                           ("w_pre", w_pre, (H,)), ("b_pre", b_pre, (H,))):
-        if t is not None:
-            _dense(t, shape, name)
-    if any(_out_type(t) != ptype for t in params):
-        raise TypeError("norm weights, biases and gate must share one type")
-    if residual_out is not None and residual_out.dtype != residual.dtype:
+    shape = residual.shape
+    T, H = shape
+    rtype = _out_type(_dense(residual, shape, "residual"))
+    ytype = OUT_F32
+    if y is not None:
+        ytype = _out_type(_dense(y, shape, "y"))
+    if residual_out is not None and _out_type(_dense(residual_out, shape, "residual_out")) != rtype:
         raise TypeError("residual_out must have residual's type")
-    if x_out is not None and x_out.dtype != torch.bfloat16:
+    if x_out is not None and _out_type(_dense(x_out, shape, "x_out")) != OUT_BF16:
         raise TypeError("x_out must be bfloat16")
-    mode = GATE_NONE
+    mode, ptype = GATE_NONE, None
     if gate is not None:
-        mode = {(H,): GATE_FEATURE, (T, H): GATE_FULL}.get(
-            tuple(gate.shape), GATE_TOKEN if tuple(gate.shape) == (T,) else None)
-        if mode is None:
-            raise ValueError(f"gate: expected shape ({H},), ({T},) or ({T}, {H}), "
-                             f"got {tuple(gate.shape)}")
-        _dense(gate, gate.shape, "gate")
-    d = Norm(hidden=H, kind=kind, y_dtype=OUT_F32 if y is None else _out_type(y),
-             residual_dtype=_out_type(residual), param_dtype=ptype, gate_mode=mode, eps=eps,
-             residual_scale=residual_scale, branch_scale=branch_scale)
-    _check(lib().moe_block_norm(ctypes.byref(d), T, _ptr(y), _ptr(residual), _ptr(gate),
-                                _ptr(w_post), _ptr(b_post), _ptr(w_pre), _ptr(b_pre),
-                                _ptr(residual_out), _ptr(x_out), _stream(stream)),
-           "moe_block_norm")
+        g = gate.shape
+        mode = GATE_FEATURE if g == (H,) else GATE_TOKEN if g == (T,) else GATE_FULL
+        _dense(gate, g if mode != GATE_FULL else shape, "gate")
+        ptype = _out_type(gate)
+    row = (H,)
+    for name, t in (("w_post", w_post), ("b_post", b_post), ("w_pre", w_pre), ("b_pre", b_pre)):
+        if t is not None:
+            kind_t = _out_type(_dense(t, row, name))
+            if ptype is None:
+                ptype = kind_t
+            elif kind_t != ptype:
+                raise TypeError("norm weights, biases and gate must share one type")
+    key = (H, kind, ytype, rtype, OUT_BF16 if ptype is None else ptype, mode, eps, residual_scale,
+           branch_scale)
+    d = _NORMS.get(key)   # descriptions are plain values: made once each
+    if d is None:
+        if len(_NORMS) >= 256:
+            _NORMS.clear()
+        d = _NORMS[key] = Norm(*key)
+    rc = lib().moe_block_norm(d, T, _ptr(y), residual.data_ptr(), _ptr(gate), _ptr(w_post),
+                              _ptr(b_post), _ptr(w_pre), _ptr(b_pre), _ptr(residual_out),
+                              _ptr(x_out), _stream(stream))
+    if rc:
+        _check(rc, "moe_block_norm")
+
+
+_NORMS: dict = {}
