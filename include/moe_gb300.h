@@ -488,7 +488,8 @@ MOE_API int moe_mx4_pack_weights(int32_t groups, int32_t n_out, int32_t k_dim, c
  *                non-decreasing within [0, rows] sets MOE_DEV_BAD_OFFSETS and
  *                nothing is computed
  *   c            fp32 or bf16 (MOE_OUT_*) [rows, n_out]
- * n_out and k_dim multiples of 128, groups <= 1024, pointers 16-byte aligned.
+ * n_out and k_dim multiples of 128, groups <= 1024; c (h below) 32-byte
+ * aligned, the other pointers 16.
  * The SwiGLU form takes W13 [groups, 2*inter, k_dim] (gate rows, then up rows)
  * and writes h = silu(g) * u, formed in fp32, as MXFP4: codes [rows, inter/2],
  * scale bytes [rows, inter/32]; inter a multiple of 128. */

@@ -9,6 +9,9 @@ namespace {
 
 bool al16(const void *p) { return p == nullptr || aligned16(p); }
 
+// products write 32 bytes at a time
+bool al32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 bool is_float_type(int32_t d) { return d == MOE_OUT_F32 || d == MOE_OUT_BF16; }
 
 // check_config, with MXFP4 as a third dtype (its shape rules are BF16's) and
@@ -134,7 +137,7 @@ int moe_mx4_grouped_gemm(int32_t groups, int32_t n_out, int32_t k_dim, int32_t r
     if (rows == 0) return MOE_OK;
     if (!a || !a_scales || !expert_offsets || !w_tiled || !w_scales_tiled || !c)
         return MOE_ERR_INVALID_ARG;
-    if (!al16(a) || !al16(a_scales) || !al16(w_tiled) || !al16(w_scales_tiled) || !al16(c))
+    if (!al16(a) || !al16(a_scales) || !al16(w_tiled) || !al16(w_scales_tiled) || !al32(c))
         return MOE_ERR_INVALID_ARG;
     return launch_mx4_gemm(groups, n_out, k_dim, rows, a, a_scales, expert_offsets, w_tiled,
                            w_scales_tiled, c, c_dtype, dev_status, static_cast<cudaStream_t>(stream));
@@ -151,7 +154,7 @@ int moe_mx4_grouped_gemm_swiglu(int32_t groups, int32_t inter, int32_t k_dim, in
     if (rows == 0) return MOE_OK;
     if (!a || !a_scales || !expert_offsets || !w13_tiled || !w13_scales_tiled || !h || !h_scales)
         return MOE_ERR_INVALID_ARG;
-    if (!al16(a) || !al16(a_scales) || !al16(w13_tiled) || !al16(w13_scales_tiled) || !al16(h) ||
+    if (!al16(a) || !al16(a_scales) || !al16(w13_tiled) || !al16(w13_scales_tiled) || !al32(h) ||
         !al16(h_scales))
         return MOE_ERR_INVALID_ARG;
     return launch_mx4_gemm_swiglu(groups, inter, k_dim, rows, a, a_scales, expert_offsets, w13_tiled,

@@ -8,14 +8,21 @@
 //
 // One persistent CTA per SM takes tiles of 128 token rows (M) x 256 weight
 // rows (N, two blocks of 128).  A stage of the ring holds 256 of K: the token
-// rows' codes (TMA boxes of 64 bytes, 64-byte swizzle), four weight tiles (8
-// KB bulk copies, stored pre-swizzled) with their scale bytes (512-byte bulk
-// copies, stored in the order tensor memory wants), and the token rows' scale
-// bytes, which come row-major from global memory and are put in that order by
-// four warps, one for each ring slot: a warp's lane L holds rows L, L+32,
-// L+64, L+96, whose four words of four scales are one 16-byte chunk.  The MMA
-// thread copies scales to tensor memory (tcgen05.cp, 32 lanes x 16 bytes,
-// repeated for the four lane quarters) in front of the products that use them.
+// rows' codes (TMA boxes of 128 bytes a row, 128-byte swizzle), four weight
+// tiles (8 KB bulk copies, stored pre-swizzled), the weights' scale bytes
+// (stored in the order tensor memory wants), and the token rows' scale bytes,
+// which come row-major from global memory and are put in that order: a warp's
+// lane L holds rows L, L+32, L+64, L+96, whose four words of four scales are
+// one 16-byte chunk, to be repeated in the four lane quarters.
+//
+// What bounds it: weights read once for few rows (decode: 254 MB of down
+// products in 43 us, 87% of the copy rate), the tensor pipe for many: 8192 x
+// 7168 x 7168 takes 176 us, 4.8 PFLOP/s, about 500 of a stage's 1000 cycles in
+// products (with neither products nor scales it takes 148).  On the way there,
+// same product: 267 us -> 253 waits that let the hardware hold the thread; ->
+// 234 one copy for both K blocks' scale bytes; -> 199 a warp for each ring
+// slot to issue its copies; -> 176 scales stored to tensor memory by warps
+// instead of tcgen05.cp.
 //
 // The hardware applies the scales, so nothing is promoted on the way and an
 // accumulator runs over all of K; the epilogue sees each output once.
@@ -39,19 +46,18 @@ constexpr int kStages = 4;
 constexpr int kTileBytes = 128 * 64;                     // 128 rows x 128 of K
 constexpr int kAOff = 0, kBOff = 2 * kTileBytes;         // B: [K block][weight block]
 constexpr int kSAOff = kBOff + 4 * kTileBytes;           // scales of the token rows, 512 each
-constexpr int kSBOff = kSAOff + 2 * 512;                 // of the weights: [K block][weight block]
+constexpr int kSBOff = kSAOff + 2 * 512;                 // of the weights: [weight block][K block]
 constexpr int kStageBytes = kSBOff + 4 * 512;
-constexpr int kScaleWarps = 4, kEpiWarps = 8;
-constexpr int kFirstScaleWarp = 2, kFirstEpiWarp = kFirstScaleWarp + kScaleWarps;
+constexpr int kSlotWarps = 4, kEpiWarps = 8;
+constexpr int kMmaWarp = 0, kFirstSlotWarp = 1, kFirstSfWarp = kFirstSlotWarp + kSlotWarps;
+constexpr int kSfWarps = 4, kFirstEpiWarp = kFirstSfWarp + kSfWarps;
 constexpr int kThreads = (kFirstEpiWarp + kEpiWarps) * 32;
 constexpr int kMaxGroups = 1024;
 constexpr int kSmemBytes = kStages * kStageBytes + 1024;
 // tensor memory: the accumulator, then for each ring slot and K block the
 // scales of the token rows (4 columns) and of the weight rows (8)
 constexpr int kTmemCols = 512, kSfCol = kTN, kSfStage = 2 * (4 + 8);
-static_assert(kScaleWarps == kStages, "scale warp i serves ring slot i");
-static_assert(kSfCol + kStages * kSfStage <= kTmemCols, "tensor memory columns");
-static_assert(kStageBytes % 1024 == 0, "stages keep the swizzle's alignment");
+static_assert(kSlotWarps == kStages, "slot warp i serves ring slot i");
 
 struct Mx4Args {
     int groups, n_out, k_dim, rows;
@@ -96,24 +102,11 @@ __device__ __forceinline__ Tile decode(int t, int G, const int *s_tiles, const i
     return w;
 }
 
-// 16 fp32 columns of a row to C
-__device__ __forceinline__ void store16(const Mx4Args &a, size_t row, int col, const uint32_t (&r)[16]) {
-    const size_t at = row * a.n_out + col;
-    if (a.c_bf16) {
-        uint32_t w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-            w[j] = *reinterpret_cast<uint32_t *>(&b);
-        }
-        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.c) + at);
-        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        o[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else {
-        uint4 *o = reinterpret_cast<uint4 *>(static_cast<float *>(a.c) + at);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-    }
+// 32 bytes, one sector, in one store
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 
 template <bool SW>
@@ -122,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const Mx4Args args) {
     using namespace ptx;
     extern __shared__ uint8_t dsmem[];
-    __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages], acc_full, acc_empty, drain_bar;
+    __shared__ __align__(8) uint64_t full_bar[kStages], sf_bar[kStages], empty_bar[kStages], acc_full, acc_empty, drain_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int s_abort, s_bad;
     __shared__ int s_off[kMaxGroups + 1], s_tiles[kMaxGroups + 1];
@@ -137,7 +130,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(smem_u32(&full_bar[s]), 2);   // the copies' thread and the scale warp
+            mbar_init(smem_u32(&full_bar[s]), 1);
+            mbar_init(smem_u32(&sf_bar[s]), kSfWarps);
             mbar_init(smem_u32(&empty_bar[s]), 1);
         }
         mbar_init(smem_u32(&acc_full), 1);
@@ -147,11 +141,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_bad = 0;
         fence_mbar_init();
     }
-    if (warp == 1) {
+    if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
         tmem_relinquish();
     }
-    if (warp == 0 && lane == 0) {
+    if (warp == kFirstSlotWarp && lane == 0) {
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmA32);
     }
@@ -192,52 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (s_bad && threadIdx.x == 0 && blockIdx.x == 0 && args.status)
         atomicOr(args.status, MOE_DEV_BAD_OFFSETS);
 
-    if (warp == 0) {
-        // ---- copies ---------------------------------------------------------------
-        if (lane == 0) {
-            const uint64_t pol_w = policy_evict_normal(), pol_a = policy_evict_last();
-            uint32_t it = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-                const Tile tl = decode(t, G, s_tiles, s_off);
-                const size_t b0 = (size_t)tl.g * nblocks + (SW ? tl.nt : 2 * tl.nt);
-                const size_t b1 = SW ? b0 + NT : b0 + 1;
-                const int nb = SW || 2 * tl.nt + 1 < nblocks ? 2 : 1;
-                const bool wide = tl.nvalid > 96;   // one box of 128 rows, else boxes of 32
-                const int boxes = wide ? 1 : (tl.nvalid + 31) / 32;
-                const uint32_t abytes = (wide ? 128 : boxes * 32) * 64;
-                for (int s = 0; s < steps; ++s, ++it) {
-                    const uint32_t slot = it % kStages;
-                    if (!wait_bounded(smem_u32(&empty_bar[slot]), ((it / kStages) & 1) ^ 1u, abort_flag,
-                                      args.status, MOE_DEV_TIMEOUT)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t base = smem_base + slot * kStageBytes, fb = smem_u32(&full_bar[slot]);
-                    const int nk = min(2, KB - 2 * s);
-                    mbar_arrive_expect_tx(fb, nk * (abytes + nb * (kTileBytes + 512)));
-                    for (int k = 0; k < nk; ++k) {
-                        const int kb = 2 * s + k;
-                        for (int q = 0; q < boxes; ++q)
-                            tma_load_2d(base + kAOff + k * kTileBytes + q * 32 * 64, wide ? &tmA : &tmA32,
-                                        kb * 64, tl.row0 + q * 32, fb, pol_a);
-                        for (int n = 0; n < nb; ++n) {
-                            const size_t tile = (n ? b1 : b0) * KB + kb;
-                            bulk_load(base + kBOff + (2 * k + n) * kTileBytes, args.w + tile * kTileBytes,
-                                      kTileBytes, fb, pol_w);
-                            bulk_load(base + kSBOff + (2 * k + n) * 512, args.w_scales + tile * 512, 512, fb,
-                                      pol_w);
-                        }
-                    }
-                }
-            }
-            // copies in flight have to land before the CTA gives up its memory
-            if (!ok)
-                for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-                    wait_drain(smem_u32(&full_bar[i % kStages]), (i / kStages) & 1);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
+    if (warp == kMmaWarp) {
         // ---- products --------------------------------------------------------------
         if (lane == 0) {
             uint32_t it = 0, tiles = 0;
@@ -249,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 for (int s = 0; s < steps; ++s, ++it) {
                     const uint32_t slot = it % kStages;
-                    if (!wait_bounded(smem_u32(&full_bar[slot]), (it / kStages) & 1, abort_flag, args.status,
+                    if (!wait_bounded(smem_u32(&sf_bar[slot]), (it / kStages) & 1, abort_flag, args.status,
                                       MOE_DEV_TIMEOUT)) {
                         ok = false;
                         break;
@@ -260,10 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int nk = min(2, KB - 2 * s);
                     for (int k = 0; k < nk; ++k) {
                         const uint32_t sfa = sf + k * 12, sfb = sfa + 4;
-                        tmem_copy_scales(sfa, sdesc_scales(base + kSAOff + k * 512));
-                        tmem_copy_scales(sfb, sdesc_scales(base + kSBOff + 2 * k * 512));
-                        tmem_copy_scales(sfb + 4, sdesc_scales(base + kSBOff + (2 * k + 1) * 512));
-                        const uint64_t ad = sdesc_k_sw64(base + kAOff + k * kTileBytes);
+                        const uint64_t ad = sdesc_k_sw128(base + kAOff) + 4 * k;
                         const uint64_t bd = sdesc_k_sw64(base + kBOff + 2 * k * kTileBytes);
                         mma_mxf4(tmem, ad, bd, idesc_mxf4(0), sfa, sfb, s + k > 0);
                         mma_mxf4(tmem, ad + 2, bd + 2, idesc_mxf4(2), sfa, sfb, 1);
@@ -276,41 +222,100 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_drain(smem_u32(&drain_bar), 0);
         }
         __syncwarp();
-    } else if (warp < kFirstEpiWarp) {
-        // ---- scales of the token rows ------------------------------------------------
-        const uint32_t mine = warp - kFirstScaleWarp;   // this warp's ring slot
+    } else if (warp < kFirstSfWarp) {
+        // ---- operands: one warp for each ring slot -----------------------------------
+        // Lane 0 issues the slot's copies; the warp puts the token rows' scale
+        // bytes, loaded before the slot is free, into their place.  (One thread
+        // issuing every slot's copies kept the products waiting.)
+        const uint32_t mine = warp - kFirstSlotWarp;
         uint8_t *smem = dsmem + (smem_base - smem_u32(dsmem));
+        const uint32_t base = smem_base + mine * kStageBytes, fb = smem_u32(&full_bar[mine]);
         const size_t pitch = args.k_dim / 32;
-        uint32_t it = 0;
+        const uint64_t pol_w = policy_evict_normal(), pol_a = policy_evict_last();
+        const int tiles = total > (int)blockIdx.x ? (total - (int)blockIdx.x - 1) / (int)gridDim.x + 1 : 0;
+        const int stages = tiles * steps;   // in 32 bits: checked by the entry point
+        int at = -1;                        // the tile that `tl` describes
+        Tile tl = {};
+        uint32_t used = 0;                  // stages of this slot so far
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-            const Tile tl = decode(t, G, s_tiles, s_off);
-            for (int s = 0; s < steps; ++s, ++it) {
-                if (it % kStages != mine) continue;
-                const int nk = min(2, KB - 2 * s);
+        for (int it = 0; it < stages; ++it) {
+            if (it % kStages == (int)mine) {
+                const int j = it / steps, s = it - j * steps;
+                if (j != at) {
+                    at = j;
+                    tl = decode(blockIdx.x + j * gridDim.x, G, s_tiles, s_off);
+                }
+                const int nb = SW || 2 * tl.nt + 1 < nblocks ? 2 : 1, nk = min(2, KB - 2 * s);
+                const bool wide = tl.nvalid > 32;   // boxes of 64 rows, or one of 32
+                const int boxes = wide ? (tl.nvalid + 63) / 64 : 1;
                 uint32_t v[2][4];
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int r = lane + 32 * j;
-                        v[k][j] = 0x7f7f7f7fu;
+                    for (int q = 0; q < 4; ++q) {
+                        const int r = lane + 32 * q;
+                        v[k][q] = 0x7f7f7f7fu;
                         if (k < nk && r < tl.nvalid)
-                            v[k][j] = __ldg(reinterpret_cast<const uint32_t *>(
+                            v[k][q] = __ldg(reinterpret_cast<const uint32_t *>(
                                 args.a_scales + (size_t)(tl.row0 + r) * pitch + (2 * s + k) * 4));
                     }
-                ok = wait_bounded(smem_u32(&empty_bar[mine]), ((it / kStages) & 1) ^ 1u, abort_flag,
-                                  args.status, MOE_DEV_TIMEOUT);
+                ok = wait_bounded(smem_u32(&empty_bar[mine]), (used & 1) ^ 1u, abort_flag, args.status,
+                                  MOE_DEV_TIMEOUT);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
+                ++used;
+                if (lane == 0) {
+                    mbar_expect_tx(fb, (wide ? boxes * 64 : 32) * 128 + nk * nb * (kTileBytes + 512));
+                    for (int n = 0; n < nb; ++n) {
+                        const size_t block = (size_t)tl.g * nblocks + (SW ? tl.nt + n * NT : 2 * tl.nt + n);
+                        const size_t tile = block * KB + 2 * s;
+                        for (int k = 0; k < nk; ++k)
+                            bulk_load(base + kBOff + (2 * k + n) * kTileBytes, args.w + (tile + k) * kTileBytes,
+                                      kTileBytes, fb, pol_w);
+                        bulk_load(base + kSBOff + 2 * n * 512, args.w_scales + tile * 512, nk * 512, fb, pol_w);
+                    }
+                    for (int q = 0; q < boxes; ++q)
+                        tma_load_2d(base + kAOff + q * 64 * 128, wide ? &tmA : &tmA32, s * 128,
+                                    tl.row0 + q * 64, fb, pol_a);
+                }
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
                     *reinterpret_cast<uint4 *>(smem + mine * kStageBytes + kSAOff + k * 512 + lane * 16) =
                         make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
-                fence_proxy_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&full_bar[mine]));
+                if (lane == 0) mbar_arrive(fb);
             }
+        }
+        // copies in flight have to land before the CTA gives up its memory
+        if (!ok && used) wait_drain(fb, (used - 1) & 1);
+    } else if (warp < kFirstEpiWarp) {
+        // ---- scales to tensor memory: each warp to its lane quarter ----------------------
+        // The tensor pipe's own copies (tcgen05.cp) run in line with the
+        // products, about 100 cycles each and six a stage.
+        const uint8_t *smem = dsmem + (smem_base - smem_u32(dsmem));
+        const uint32_t sf0 = tmem + ((uint32_t)(warp & 3) << 21) + kSfCol;   // lane 32 (warp & 3)
+        const int tiles = total > (int)blockIdx.x ? (total - (int)blockIdx.x - 1) / (int)gridDim.x + 1 : 0;
+        bool ok = true;
+        for (int it = 0; it < tiles * steps; ++it) {
+            const uint32_t slot = it % kStages;
+            ok = wait_bounded(smem_u32(&full_bar[slot]), (it / kStages) & 1, abort_flag,
+                              args.status, MOE_DEV_TIMEOUT);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint8_t *sc = smem + slot * kStageBytes + kSAOff + lane * 16;
+            const uint32_t sf = sf0 + slot * kSfStage;
+            // a K block: token rows, first and second weight block; what a
+            // short stage leaves in place of one is not used
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                tmem_st4(sf + 12 * k, *reinterpret_cast<const uint4 *>(sc + k * 512));
+                tmem_st4(sf + 12 * k + 4, *reinterpret_cast<const uint4 *>(sc + 1024 + k * 512));
+                tmem_st4(sf + 12 * k + 8, *reinterpret_cast<const uint4 *>(sc + 2048 + k * 512));
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sf_bar[slot]));
         }
     } else {
         // ---- epilogue ------------------------------------------------------------------
@@ -326,63 +331,98 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const bool valid = m < tl.nvalid;
             const size_t row = tl.row0 + m;
+            // The accumulator is given back as soon as this warp's part of it
+            // is in registers: the next tile's products run under the rest.
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&acc_empty));
+            };
             if (SW) {
-                uint16_t sc = 0;
+                float h[64];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    uint32_t g[16], u[16];
+                    tmem_ld16(lane_base + half * 64 + p * 16, g);
+                    tmem_ld16(lane_base + 128 + half * 64 + p * 16, u);
+                    tmem_wait_ld(g);
+                    tmem_wait_ld(u);
+                    if (p == 3) release();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        h[16 * p + j] = silu_mul(__uint_as_float(g[j]), __uint_as_float(u[j]));
+                }
+                uint32_t o[8], sc = 0;
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {   // 32 features, one block of scales
-                    float h[32];
                     uint32_t amax = 0;
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        uint32_t g[16], u[16];
-                        const uint32_t col = half * 64 + b * 32 + p * 16;
-                        tmem_ld16(lane_base + col, g);
-                        tmem_ld16(lane_base + 128 + col, u);
-                        tmem_wait_ld(g);
-                        tmem_wait_ld(u);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float v = silu_mul(__uint_as_float(g[j]), __uint_as_float(u[j]));
-                            h[16 * p + j] = v;
-                            amax = max(amax, __float_as_uint(v) & 0x7fffffffu);
-                        }
-                    }
+                    for (int j = 0; j < 32; ++j) amax = max(amax, __float_as_uint(h[32 * b + j]) & 0x7fffffffu);
                     const uint32_t byte = mx4_scale_byte(amax);
-                    sc |= (uint16_t)(byte << (8 * b));
-                    uint32_t o[4];
+                    sc |= byte << (8 * b);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         float v[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = h[8 * j + i];
-                        o[j] = mx4_codes8(v, byte);
+                        for (int i = 0; i < 8; ++i) v[i] = h[32 * b + 8 * j + i];
+                        o[4 * b + j] = mx4_codes8(v, byte);
                     }
-                    if (valid)
-                        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(args.c) + row * (args.n_out / 4) +
-                                                   tl.nt * 64 + half * 32 + b * 16) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
                 }
-                if (valid)
-                    *reinterpret_cast<uint16_t *>(args.h_scales + row * (args.n_out / 64) + tl.nt * 4 +
-                                                  half * 2) = sc;
-            } else if (2 * tl.nt + half < nblocks) {
-#pragma unroll 2
+                if (valid) {
+                    store32(static_cast<uint8_t *>(args.c) + row * (args.n_out / 4) + tl.nt * 64 + half * 32, o);
+                    *reinterpret_cast<uint16_t *>(args.h_scales + row * (args.n_out / 64) + tl.nt * 4 + half * 2) =
+                        (uint16_t)sc;
+                }
+            } else if (2 * tl.nt + half >= nblocks) {
+                release();   // no second weight block
+            } else if (args.c_bf16) {
+                uint32_t w[64];
+#pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     uint32_t r[16];
                     tmem_ld16(lane_base + half * 128 + j * 16, r);
                     tmem_wait_ld(r);
-                    if (valid) store16(args, row, tl.nt * kTN + half * 128 + j * 16, r);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        __nv_bfloat162 b =
+                            __floats2bfloat162_rn(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                        w[8 * j + i] = *reinterpret_cast<uint32_t *>(&b);
+                    }
+                }
+                release();
+                uint16_t *o = static_cast<uint16_t *>(args.c) + row * args.n_out + tl.nt * kTN + half * 128;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = w[8 * j + i];
+                    if (valid) store32(o + 16 * j, v);
+                }
+            } else {
+                float *o = static_cast<float *>(args.c) + row * args.n_out + tl.nt * kTN + half * 128;
+#pragma unroll
+                for (int q4 = 0; q4 < 2; ++q4) {   // 64 columns at a time
+                    uint32_t r[4][16];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) tmem_ld16(lane_base + half * 128 + q4 * 64 + j * 16, r[j]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) tmem_wait_ld(r[j]);
+                    if (q4 == 1) release();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = r[j >> 1][8 * (j & 1) + i];
+                        if (valid) store32(o + q4 * 64 + 8 * j, v);
+                    }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&acc_empty));
         }
     }
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
@@ -401,8 +441,8 @@ int launch(const Mx4Args &args, const void *a, cudaStream_t s) {
     });
     if (rc[dev]) return cuda_fail("cudaFuncSetAttribute", (cudaError_t)rc[dev]);
     CUtensorMap tmA, tmA32;
-    if (!encode_2d_sw64(&tmA, a, (uint64_t)args.k_dim / 2, (uint64_t)args.rows, 128) ||
-        !encode_2d_sw64(&tmA32, a, (uint64_t)args.k_dim / 2, (uint64_t)args.rows, 32))
+    if (!encode_2d(&tmA, a, true, (uint64_t)args.k_dim / 2, (uint64_t)args.rows, 64) ||
+        !encode_2d(&tmA32, a, true, (uint64_t)args.k_dim / 2, (uint64_t)args.rows, 32))
         return cuda_fail("cuTensorMapEncodeTiled (activations)");
     const int64_t nt = ceil_div(args.n_out, kTN);
     const int64_t bound = nt * (args.groups + ceil_div(args.rows, kTM));
