@@ -26,7 +26,7 @@ __all__ = ["Config", "Weights", "WsLayout", "lib", "make_config", "route", "rout
            "SOFTMAX", "SIGMOID", "BF16", "FP8", "OUT_F32", "OUT_BF16", "ACT_IDENTITY",
            "ACT_SILU_MUL",
            # what stands around the layer (block.py)
-           "MXFP4", "FewTokenLayer", "FewLayout", "layer_few", "layer_few_max_tokens",
+           "MXFP4", "FewTokenLayer", "FewLayout", "Mx4MoELayer", "MoEBlock", "layer_few", "layer_few_max_tokens",
            "layer_few_workspace_size", "layer_few_layout", "mx4_quantize", "mx4_dequantize",
            "pack_mx4_weights", "mx4_grouped_gemm", "mx4_grouped_gemm_swiglu", "Norm", "block_norm", "NORM_RMS", "NORM_LAYER", "GATE_NONE",
            "GATE_FEATURE", "GATE_TOKEN", "GATE_FULL"]
@@ -659,7 +659,8 @@ class ExpertRebalancer:
 
 from . import block  # noqa: E402  (needs the names above)
 from .block import (GATE_FEATURE, GATE_FULL, GATE_NONE, GATE_TOKEN, NORM_LAYER,  # noqa: E402
-                    NORM_RMS, FewLayout, FewTokenLayer, Norm, block_norm, layer_few,
+                    NORM_RMS, FewLayout, FewTokenLayer, MoEBlock, Mx4MoELayer, Norm, block_norm,
+                    layer_few,
                     layer_few_layout, layer_few_max_tokens, layer_few_workspace_size,
                     mx4_dequantize, mx4_grouped_gemm, mx4_grouped_gemm_swiglu, mx4_quantize,
                     pack_mx4_weights)

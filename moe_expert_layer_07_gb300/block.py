@@ -207,6 +207,7 @@ class FewTokenLayer:
         self.layout = layer_few_layout(self.cfg)
         self.ws_bytes = self.layout.total
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        self.ws[:4].zero_()   # status() before the first call
 
     @property
     def weights(self) -> Weights:
@@ -282,3 +283,97 @@ def block_norm(residual, y=None, residual_out=None, x_out=None, w_post=None, b_p
 
 
 _NORMS: dict = {}
+
+
+# ---- a decoder's MoE block ------------------------------------------------------------------
+
+
+class Mx4MoELayer:
+    """The MoE layer with MXFP4 experts, for any number of tokens.
+
+    weights as FewTokenLayer's (MXFP4 codes and scale bytes, row-major), packed
+    once.  Up to layer_few_max_tokens() tokens take the few-token kernels; more
+    go through routing, the dispatch of bf16 rows, their quantisation, the
+    grouped products and the combine.  Both quantise x and h in the same places.
+    """
+
+    def __init__(self, shape, weights: dict, max_tokens: int, log2phys=None):
+        from . import permute_workspace_size
+        self.shape = shape
+        self.few = FewTokenLayer(shape, weights, log2phys=log2phys)
+        self._keep = k = self.few._keep
+        self.cfg = make_config(shape, max_tokens)   # routing and dispatch: bf16 rows
+        self.groups = G = shape.num_experts + shape.num_shared
+        T, H, I, dev = max_tokens, shape.hidden, shape.inter, k["w13"].device
+        R = T * (shape.top_k + shape.num_shared)
+
+        def buf(*size, dtype=torch.uint8):
+            return torch.empty(*size, dtype=dtype, device=dev)
+        i32, f32 = torch.int32, torch.float32
+        self.status_word = torch.zeros(1, dtype=i32, device=dev)
+        self.logits = buf(T, shape.num_experts, dtype=f32)
+        self.ids, self.wts = buf(T, shape.top_k, dtype=i32), buf(T, shape.top_k, dtype=f32)
+        self.offsets, self.src = buf(G + 1, dtype=i32), buf(R, dtype=i32)
+        self.row_of_slot = buf(T, shape.top_k, dtype=i32)
+        self.perm_bytes = permute_workspace_size(self.cfg, T)
+        self.perm_ws = buf(max(1, self.perm_bytes))
+        self.xp = buf(R, H, dtype=torch.bfloat16)
+        self.xq, self.xs = buf(R, H // 2), buf(R, H // 32)
+        self.h, self.hs = buf(R, I // 2), buf(R, I // 32)
+        self.y = buf(R, H, dtype=f32)
+
+    def forward(self, x, out, out_dtype=OUT_F32, stream=None):
+        """x bf16 [T, H] and out [T, H] (fp32 or bf16) device tensors."""
+        from . import combine, permute, route
+        T, s, k = x.shape[0], self.shape, self._keep
+        if T <= self.few.cfg.max_tokens:
+            return self.few.forward(x, out, out_dtype, stream=stream)
+        if T > self.cfg.max_tokens:
+            raise ValueError(f"{T} tokens, and buffers for {self.cfg.max_tokens}")
+        rows = T * (s.top_k + s.num_shared)
+        st = self.status_word
+        route(self.cfg, T, x, k["wg"], k["e_bias"], k["logit_offset"], k["log2phys"], self.logits,
+              self.ids, self.wts, st, stream)
+        permute(self.cfg, T, self.ids, x, None, self.offsets, self.src, self.row_of_slot, self.xp,
+                None, self.perm_ws, self.perm_bytes, st, stream)
+        mx4_quantize(self.xp[:rows], self.xq[:rows], self.xs[:rows], stream)
+        mx4_grouped_gemm_swiglu(self.groups, s.inter, s.hidden, rows, self.xq, self.xs, self.offsets,
+                                k["w13"], k["w13_s"], self.h, self.hs, st, stream)
+        mx4_grouped_gemm(self.groups, s.hidden, s.inter, rows, self.h, self.hs, self.offsets,
+                         k["w2"], k["w2_s"], self.y, OUT_F32, st, stream)
+        combine(self.cfg, T, self.y, self.row_of_slot, self.wts, self.offsets, out, out_dtype, stream)
+        return out
+
+    def status(self) -> int:
+        """The device status of the calls so far (both paths)."""
+        return self.few.status() | int(self.status_word)
+
+
+class MoEBlock:
+    """x = norm(r) w_pre;  y = layer(x);  r = residual_scale r + branch_scale gate norm(y) w_post.
+
+    layer: an MoELayer, a FewTokenLayer or an Mx4MoELayer.  With `few` (a
+    FewTokenLayer) calls of few tokens go there.  w_post and gate may be None.
+    """
+
+    def __init__(self, layer, w_pre, w_post=None, gate=None, residual_scale=1.0, branch_scale=1.0,
+                 eps=1e-6, kind=NORM_RMS, few: FewTokenLayer | None = None):
+        self.layer, self.few = layer, few
+        self.w_pre, self.w_post, self.gate = w_pre, w_post, gate
+        self.scales = dict(residual_scale=residual_scale, branch_scale=branch_scale)
+        self.norm = dict(eps=eps, kind=kind)
+
+    def pre(self, residual, x, stream=None):
+        """x = norm(residual) w_pre, where no earlier block wrote it."""
+        block_norm(residual, x_out=x, w_pre=self.w_pre, stream=stream, **self.norm)
+        return x
+
+    def forward(self, residual, x, y, w_next=None, x_next=None, stream=None):
+        """residual fp32 or bf16 [T, H], updated in place; x bf16 [T, H] the normed input (from
+        `pre`, or the block before); y bf16 [T, H] is scratch.  With w_next the next block's
+        norm is part of the same pass, into x_next (may be x)."""
+        few = self.few is not None and x.shape[0] <= self.few.cfg.max_tokens
+        (self.few if few else self.layer).forward(x, y, OUT_BF16, stream=stream)
+        block_norm(residual, y=y, residual_out=residual, x_out=x_next, w_post=self.w_post,
+                   w_pre=w_next, gate=self.gate, stream=stream, **self.scales, **self.norm)
+        return residual
