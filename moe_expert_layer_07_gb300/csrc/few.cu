@@ -60,7 +60,11 @@ constexpr int kMaxGroups = kMaxSlots + kMaxShared;      // groups with rows
 enum { DT_BF16 = MOE_DTYPE_BF16, DT_FP8 = MOE_DTYPE_FP8_BLOCK128, DT_MX4 = MOE_DTYPE_MXFP4 };
 
 // The token side, x and h.
-//  BF16   rows as they are.
+//  BF16   x's rows as they are; h in two bf16 parts, h = hi + lo to 17 bits, 64
+//         values of hi and then of lo: the products run twice over the same
+//         weights, which are what the time goes into.  (One part, as the large
+//         batches' kernel keeps, made the output's error 2.3e-3 where its own
+//         rounding to bf16 makes 1.7e-3.)
 //  FP8    segments of 128 values of a row: each code kept as the fp16 number it
 //         stands for before its scale (256 bytes), then the fp32 scale.  Such a
 //         segment is one bulk copy.
@@ -78,7 +82,7 @@ struct FewArgs {
     int32_t *ids;
     float *wts;
     const uint8_t *xrows;          // bf16 [T, H], or segments [T, H/128] (FP8)
-    uint8_t *hrows;                // bf16 [rows, I], segments [rows, I/128], or codes [rows, I/2]
+    uint8_t *hrows;                // [rows, I/64][hi, lo][64] (BF16), segments [rows, I/128], or codes [rows, I/2]
     const uint8_t *xs;             // MXFP4: [H/128][16][kScaleRow]
     uint8_t *hs;                   // MXFP4: [I/128][hs_rows][kScaleRow]
     int hs_rows;
@@ -247,8 +251,9 @@ struct Traits {
     static constexpr int kTile = 16384;
     // the token side of one tile of K: 8 NT rows.  The pitch spreads the reads
     // of a quarter warp (two rows, four chunks each) over all banks.
-    static constexpr int kCopy = DT == DT_BF16 ? 128 : kSegment;
-    static constexpr int kPitch = DT == DT_BF16 ? 192 : 272;
+    static constexpr int kCopyX = DT == DT_BF16 ? 128 : kSegment;   // of one row of x, of h
+    static constexpr int kCopyH = DT == DT_BF16 ? 256 : kSegment;
+    static constexpr int kPitch = DT == DT_BF16 ? 320 : 272;
     static constexpr int kTokOff = 2 * kTile;
     static constexpr int kTokHalf = 8 * NT * kPitch;
     static constexpr int kWsOff = kTokOff + 2 * kTokHalf;   // FP8: the tiles' two scales
@@ -267,7 +272,7 @@ struct Traits<DT_MX4, NT> {
     static constexpr int kTokOff = kTiles * kTile, kScaleOff = kTokOff + kTiles * kTokBytes;
     static constexpr int kTokScaleOff = kScaleOff + kTiles * kScale;
     static constexpr int kStage = kTokScaleOff + kTiles * 512;
-    static constexpr int kCopy = 0, kPitch = 0, kTokHalf = 0, kWsOff = 0, kBWords = 1;
+    static constexpr int kCopyX = 0, kCopyH = 0, kPitch = 0, kTokHalf = 0, kWsOff = 0, kBWords = 1;
     static constexpr int kMultipliers = 1;                  // the MMAs' commit
     static constexpr int kScalers = 4;                      // warps 4..7: a lane quarter each
     static constexpr int kReaders = 1 + kScalers + 1 + kPublishers;
@@ -552,7 +557,7 @@ __device__ __forceinline__ void tile_product(float (&acc)[NT][4], const uint8_t 
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     if (!n || second)
-                        mma_bf16(acc[n], a[2 * i], b[2 * i], a[2 * i + 1], b[2 * i + 1],
+                        mma_bf16(part[n], a[2 * i], b[2 * i], a[2 * i + 1], b[2 * i + 1],
                                  f.b[n][4 * h + 2 * i], f.b[n][4 * h + 2 * i + 1]);
         } else {
 #pragma unroll
@@ -568,7 +573,14 @@ __device__ __forceinline__ void tile_product(float (&acc)[NT][4], const uint8_t 
             }
         }
     }
-    if (DT == DT_FP8) {
+    // A tile's sums join the unit's outside the tensor cores, whose additions
+    // cut off instead of rounding: over 448 steps of K that had grown to 2.5e-5.
+    if (DT == DT_BF16) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][i] += part[n][i];
+    } else {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const float s0 = __fmul_rn(f.s[n][0], ws), s1 = __fmul_rn(f.s[n][1], ws);
@@ -838,8 +850,9 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             const int r = lane % (8 * NT), half = lane / (8 * NT);
             const uint8_t *src = nullptr;
             if (r < n && half < 2)
-                src = un.gu ? a.xrows + (size_t)sh.row_tok[row0 + r] * un.kb * TR::kCopy
-                            : a.hrows + (size_t)(row0 + r) * un.kb * TR::kCopy;
+                src = un.gu ? a.xrows + (size_t)sh.row_tok[row0 + r] * un.kb * TR::kCopyX
+                            : a.hrows + (size_t)(row0 + r) * un.kb * TR::kCopyH;
+            const uint32_t copy = un.gu ? TR::kCopyX : TR::kCopyH;
             for (int s = 0; s < un.steps; ++s, ++stage) {
                 const int st = stage % kStages;
                 const uint32_t full = ptx::smem_u32(&sh.full[st]);
@@ -873,11 +886,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                     if (lane == 0)
                         *reinterpret_cast<float2 *>(base + TR::kWsOff) = make_float2(w0, un.gu ? o1 : o0);
                 }
-                if (lane == 0) ptx::mbar_arrive_expect_tx(full, n * nk * TR::kCopy);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(full, n * nk * copy);
                 __syncwarp();   // the bytes are announced before any copy lands
                 if (src && half < nk)
                     ptx::bulk_load(ptx::smem_u32(base + TR::kTokOff + half * TR::kTokHalf + r * TR::kPitch),
-                                   src + (size_t)(k0 + half) * TR::kCopy, TR::kCopy, full, policy);
+                                   src + (size_t)(k0 + half) * copy, copy, full, policy);
             }
         }
         if (lane == 0)   // as the producer: no copy may outlive the CTA
@@ -997,9 +1010,16 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                         const float4 v = *reinterpret_cast<const float4 *>(&sh.res[buf][c][lane * 4]);
                         const size_t row = row0 + c;
                         if (DT == DT_BF16) {
-                            __nv_bfloat162 b0 = __floats2bfloat162_rn(v.x, v.y), b1 = __floats2bfloat162_rn(v.z, v.w);
-                            *reinterpret_cast<uint2 *>(a.hrows + (row * a.I + un.tile * 128 + lane * 4) * 2) =
-                                make_uint2(*reinterpret_cast<uint32_t *>(&b0), *reinterpret_cast<uint32_t *>(&b1));
+                            const __nv_bfloat162 b0 = __floats2bfloat162_rn(v.x, v.y),
+                                                 b1 = __floats2bfloat162_rn(v.z, v.w);
+                            const float2 f0 = __bfloat1622float2(b0), f1 = __bfloat1622float2(b1);
+                            const __nv_bfloat162 l0 = __floats2bfloat162_rn(v.x - f0.x, v.y - f0.y),
+                                                 l1 = __floats2bfloat162_rn(v.z - f1.x, v.w - f1.y);
+                            // tile of 64: un.tile * 2 + lane / 16
+                            uint8_t *o = a.hrows + ((row * mt1 + un.tile) * 2 + lane / 16) * TR::kCopyH + lane % 16 * 8;
+                            auto bits = [](const __nv_bfloat162 &b) { return *reinterpret_cast<const uint32_t *>(&b); };
+                            *reinterpret_cast<uint2 *>(o) = make_uint2(bits(b0), bits(b1));
+                            *reinterpret_cast<uint2 *>(o + 128) = make_uint2(bits(l0), bits(l1));
                         } else {
                             uint8_t *seg = a.hrows + (row * mt1 + un.tile) * kSegment;
                             float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
@@ -1132,11 +1152,19 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 TokenSide<DT, NT> f;
                 load_tokens<DT, NT>(f, base + TR::kTokOff, g8, t4);
                 tile_product<DT, NT>(acc[0], base, ra, t4, f, ws.x, second);
+                if (DT == DT_BF16 && !un.gu) {   // h's low part
+                    load_tokens<DT, NT>(f, base + TR::kTokOff + 128, g8, t4);
+                    tile_product<DT, NT>(acc[0], base, ra, t4, f, ws.x, second);
+                }
                 if (un.gu) {
                     tile_product<DT, NT>(acc[1], base + TR::kTile, ra, t4, f, ws.y, second);
                 } else if (2 * s + 1 < un.kb) {
                     load_tokens<DT, NT>(f, base + TR::kTokOff + TR::kTokHalf, g8, t4);
                     tile_product<DT, NT>(acc[0], base + TR::kTile, ra, t4, f, ws.y, second);
+                    if (DT == DT_BF16) {
+                        load_tokens<DT, NT>(f, base + TR::kTokOff + TR::kTokHalf + 128, g8, t4);
+                        tile_product<DT, NT>(acc[0], base + TR::kTile, ra, t4, f, ws.y, second);
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.empty[st]));
@@ -1218,7 +1246,7 @@ void few_layout(const moe_config *c, moe_few_layout *L) {
     L->topk_w = take(4 * T * k);
     L->x = take(bf ? 0 : mx4 ? T * H / 2 : T * (H / 128) * kSegment);
     L->x_scales = take(mx4 ? H / 128 * kMaxT * kScaleRow : 0);
-    L->h = take(bf ? 2 * R * I : mx4 ? R * I / 2 : R * (I / 128) * kSegment);
+    L->h = take(bf ? 4 * R * I : mx4 ? R * I / 2 : R * (I / 128) * kSegment);
     // a box of 16 rows may begin at any row
     L->h_scales = take(mx4 ? I / 128 * (R + kMaxT) * kScaleRow : 0);
     L->y = take(4 * R * H);

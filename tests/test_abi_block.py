@@ -43,9 +43,9 @@ def test_few_workspace(L):
         assert offs == sorted(offs) and all(o % 256 == 0 for o in offs)
         rows = 16 * 9
         assert lay.total - lay.y == rows * cfg.hidden * 4
-    # h: bf16, segments of 128 values and a scale, packed codes
+    # h: two bf16 parts, segments of 128 values and a scale, packed codes
     size = {d: moe.layer_few_layout(_cfg(dtype=d)) for d in (moe.BF16, moe.FP8, moe.MXFP4)}
-    assert size[moe.BF16].h_scales - size[moe.BF16].h == 16 * 9 * 384 * 2
+    assert size[moe.BF16].h_scales - size[moe.BF16].h == 16 * 9 * 384 * 4
     assert size[moe.MXFP4].h_scales - size[moe.MXFP4].h == 16 * 9 * 384 // 2
 
 

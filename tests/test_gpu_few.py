@@ -76,7 +76,8 @@ def _nearest_error(shape, h):
     b = h.view(h.shape[0], -1, n)
     amax = b.abs().amax(-1, keepdim=True).expand_as(b).reshape(h.shape)
     if shape.dtype == "bf16":
-        return (h.bfloat16().double() - h).abs(), amax
+        hi = h.bfloat16().double()   # two parts
+        return (hi + (h - hi).bfloat16().double() - h).abs(), amax
     if shape.dtype == "mxfp4":
         v = torch.tensor(mx4.dequantize(*mx4.quantize(h.cpu().numpy())), device="cuda")
         return (v - h).abs(), amax
@@ -88,7 +89,7 @@ def _nearest_error(shape, h):
 def _stored_h(shape, layer, R):
     I = shape.inter
     if shape.dtype == "bf16":
-        return layer.view("h", torch.bfloat16, (R, I)).double()
+        return layer.view("h", torch.bfloat16, (R, I // 64, 2, 64)).double().sum(2).reshape(R, I)
     if shape.dtype == "fp8":   # segments of 128 values: fp16 code values, then the fp32 scale
         seg = layer.view("h", torch.uint8, (R, I // 128, 272))
         v = seg[..., :256].contiguous().view(torch.float16).double()
