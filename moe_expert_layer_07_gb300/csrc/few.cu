@@ -86,6 +86,7 @@ struct FewArgs {
     const uint8_t *xs;             // MXFP4: [H/128][16][kScaleRow]
     uint8_t *hs;                   // MXFP4: [I/128][hs_rows][kScaleRow]
     int hs_rows;
+    size_t pf_w13, pf_w2, pf_w13_one, pf_w2_one;   // bytes to prefetch; of one expert
     float *y;                      // [rows, H]
     void *out;
     int32_t *sched;                // unit counter | h_done[kMaxGroups] | col_done[H/128][kPublishers]
@@ -243,6 +244,11 @@ constexpr int kPublishers = 4;
 constexpr int kWarps = kFirstPublisher + kPublishers;
 constexpr int kFfnThreads = kWarps * 32;
 constexpr int kUnitSlots = 8;     // units announced ahead
+constexpr int kPrefetchBytes = 8192;
+// The shared experts' part of W13 and of W2 that is fetched ahead, far inside
+// L2 (one token of the 256-expert layer: 76.8 us without, 74.7 with 12 MB,
+// 75.0 with 24; three with MXFP4 experts 102 / 100.4 / 100.7).
+constexpr size_t kPrefetchMost = 24u << 20;
 
 template <int DT, int NT>
 struct Traits {
@@ -321,72 +327,33 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return k == 0u ? -FLT_MAX : __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k);
 }
 
-// The top_k of a token in order, lane j keeping the j-th's index; false if
-// there are fewer candidates.  Experts e = 32 q + lane in registers, groups (if
-// any) of 32: a group is one register of the warp, and one reduction each
-// gives its best.
-__device__ __forceinline__ bool choose_in_registers(const SelectArgs &a, int lane, const uint32_t *key,
-                                                    int &my_id) {
-    uint32_t k[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) k[q] = 32 * q + lane < a.E ? key[32 * q + lane] : 0u;
-    if (a.groups > 1) {
-        uint32_t left[8], gk[8];
-        float sum[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) left[q] = k[q];
-        for (int r = 0; r < a.topn; ++r) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const uint32_t m = __reduce_max_sync(0xffffffffu, left[q]);
-                const uint32_t at = __ballot_sync(0xffffffffu, left[q] == m);
-                if (lane == __ffs(at) - 1) left[q] = 0u;
-                sum[q] = r == 0 ? key_value(m) : __fadd_rn(sum[q], key_value(m));
+// Zeroes the keys of the groups that are not kept.  Lane g scores group g: the
+// sum of its best, best first.
+__device__ __forceinline__ void drop_groups(const SelectArgs &a, int lane, uint32_t *key) {
+    const int gs = a.E / a.groups;
+    float sum = 0.0f;
+    if (lane < a.groups) {
+        const uint32_t *k0 = key + lane * gs;
+        if (a.topn <= 2) {   // the two largest values in one pass
+            uint32_t m1 = 0, m2 = 0;
+            int e = lane % gs;   // lanes start apart: one bank each where gs is a multiple of 32
+#pragma unroll 4
+            for (int i = 0; i < gs; ++i) {
+                const uint32_t k = k0[e];
+                m2 = max(m2, min(m1, k));
+                m1 = max(m1, k);
+                if (++e == gs) e = 0;
             }
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q) gk[q] = q < a.groups ? order_key(sum[q]) : 0u;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            int rank = 0;
-#pragma unroll
-            for (int o = 0; o < 8; ++o) rank += gk[o] > gk[q] || (gk[o] == gk[q] && o < q);
-            if (gk[q] == 0u || rank >= a.topk_groups) k[q] = 0u;
-        }
-    }
-    for (int j = 0; j < a.k; ++j) {
-        uint32_t best = 0;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) best = max(best, k[q]);
-        const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-        if (m == 0u) return false;
-        int at = INT_MAX;
-#pragma unroll
-        for (int q = 7; q >= 0; --q)
-            if (k[q] == m) at = 32 * q + lane;
-        const int id = (int)__reduce_min_sync(0xffffffffu, (uint32_t)at);
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-            if (32 * q + lane == id) k[q] = 0u;
-        if (lane == j) my_id = id;
-    }
-    return true;
-}
-
-// The same for any number and size of groups, in loops over shared memory.
-__device__ __noinline__ bool choose_in_memory(const SelectArgs &a, int lane, uint32_t *key, int &my_id) {
-    if (a.groups > 1) {
-        const int gs = a.E / a.groups;
-        float sum = 0.0f;
-        if (lane < a.groups) {   // lane g: the sum of group g's best, best first
+            sum = key_value(m1);
+            if (a.topn == 2) sum = __fadd_rn(sum, key_value(m2));
+        } else {
             uint32_t pk = 0xffffffffu;
             int pi = -1;
-            for (int r = 0; r < a.topn; ++r) {
+            for (int r = 0; r < a.topn; ++r) {   // the next one in (value, index) order
                 uint32_t bk = 0;
                 int bi = INT_MAX;
-#pragma unroll 4
-                for (int e = lane * gs; e < (lane + 1) * gs; ++e) {
-                    const uint32_t k = key[e];
+                for (int e = 0; e < gs; ++e) {
+                    const uint32_t k = k0[e];
                     if ((k < pk || (k == pk && e > pi)) && k > bk) bk = k, bi = e;
                 }
                 sum = r == 0 ? key_value(bk) : __fadd_rn(sum, key_value(bk));
@@ -394,17 +361,46 @@ __device__ __noinline__ bool choose_in_memory(const SelectArgs &a, int lane, uin
                 pi = bi;
             }
         }
-        const uint32_t gk = lane < a.groups ? order_key(sum) : 0u;
-        int rank = 0;
-        for (int g = 0; g < a.groups; ++g) {
-            const uint32_t o = __shfl_sync(0xffffffffu, gk, g);
-            rank += o > gk || (o == gk && g < lane);
+    }
+    const uint32_t gk = lane < a.groups ? order_key(sum) : 0u;
+    int rank = 0;
+    for (int g = 0; g < a.groups; ++g) {
+        const uint32_t o = __shfl_sync(0xffffffffu, gk, g);
+        rank += o > gk || (o == gk && g < lane);
+    }
+    const uint32_t kept = __ballot_sync(0xffffffffu, gk != 0u && rank < a.topk_groups);
+    __syncwarp();
+    for (int g = 0; g < a.groups; ++g)
+        if (!((kept >> g) & 1u))
+            for (int e = lane; e < gs; e += 32) key[g * gs + e] = 0u;
+    __syncwarp();
+}
+
+// The top_k of a token in order, lane j keeping the j-th's index; false if
+// there are fewer candidates.
+__device__ __forceinline__ bool choose(const SelectArgs &a, int lane, const uint32_t *key, int &my_id) {
+    if (a.E <= 256) {   // experts e = 32 q + lane in registers
+        uint32_t k[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) k[q] = 32 * q + lane < a.E ? key[32 * q + lane] : 0u;
+#pragma unroll 1
+        for (int j = 0; j < a.k; ++j) {
+            uint32_t best = 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) best = max(best, k[q]);
+            const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+            if (m == 0u) return false;
+            int at = INT_MAX;
+#pragma unroll
+            for (int q = 7; q >= 0; --q)
+                if (k[q] == m) at = 32 * q + lane;
+            const int id = (int)__reduce_min_sync(0xffffffffu, (uint32_t)at);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (32 * q + lane == id) k[q] = 0u;
+            if (lane == j) my_id = id;
         }
-        const uint32_t kept = __ballot_sync(0xffffffffu, gk != 0u && rank < a.topk_groups);
-        __syncwarp();
-        for (int e = lane; e < a.E; e += 32)
-            if (!((kept >> (e / gs)) & 1u)) key[e] = 0u;
-        __syncwarp();
+        return true;
     }
     uint32_t pk = 0xffffffffu;
     int pi = -1;
@@ -424,14 +420,15 @@ __device__ __noinline__ bool choose_in_memory(const SelectArgs &a, int lane, uin
 }
 
 // warp_select's choice and weights (the same bits).  Every CTA runs this once,
-// with a cold instruction cache: warp_select's unrolled shuffles took 15 us of
-// the 84 that one token of the 256-expert layer took.  key, score: this warp's
-// rows of E in shared memory; ids, wts: the token's top_k.
+// with a cold instruction cache, so its length counts more than its work:
+// warp_select's unrolled shuffles took 15 us of the 84 that one token of the
+// 256-expert layer took, this takes 3.5.  key, score: this warp's rows of E
+// in shared memory; ids, wts: the token's top_k.
 __device__ __noinline__ void few_select(const SelectArgs &a, int lane, uint32_t *key, const float *score,
                                         int32_t *ids, float *wts) {
+    if (a.groups > 1) drop_groups(a, lane, key);
     int my_id = 0;
-    const bool regs = a.E <= 256 && (a.groups == 1 || a.E == 32 * a.groups);
-    if (!(regs ? choose_in_registers(a, lane, key, my_id) : choose_in_memory(a, lane, key, my_id))) {
+    if (!choose(a, lane, key, my_id)) {
         if (lane == 0 && a.status) atomicOr(a.status, MOE_DEV_BAD_EXPERT_ID);   // fewer candidates than k
         return;
     }
@@ -652,6 +649,17 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();   // scores, quantised x, counters
     __syncthreads();
+
+    // The shared experts' weights are needed whatever the selection says: to L2
+    // while it runs and HBM is idle (a hint; each CTA its part of each block).
+    if (warp == kWarps - 1)
+        for (int p = 0; p < 2; ++p) {
+            const size_t bytes = p ? a.pf_w2 : a.pf_w13;   // of all shared experts, at most kPrefetchMost
+            const uint8_t *w = p ? a.w2 + a.E * (a.pf_w2_one) : a.w13 + a.E * (a.pf_w13_one);
+            for (size_t o = ((size_t)lane * gridDim.x + blockIdx.x) * kPrefetchBytes; o < bytes;
+                 o += (size_t)32 * gridDim.x * kPrefetchBytes)
+                ptx::prefetch_l2(w + o, (uint32_t)min((size_t)kPrefetchBytes, bytes - o));
+        }
 
     // ---- selection, by every CTA for itself -------------------------------------
     int next = 0;
@@ -908,21 +916,28 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             for (int i = lane; i < a.T * 8; i += 32) {
                 const int t = i >> 3;
                 const size_t col = tile * 128 + 32 * q + (i & 7) * 4;
-                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f), sr[kMaxShared], r[8];
                 const float *y = a.y + col;
-                for (int s = 0; s < a.S; ++s) {
-                    const float4 r = __ldcg(reinterpret_cast<const float4 *>(y + (size_t)(s * a.T + t) * a.H));
-                    o.x = __fadd_rn(o.x, r.x), o.y = __fadd_rn(o.y, r.y);
-                    o.z = __fadd_rn(o.z, r.z), o.w = __fadd_rn(o.w, r.w);
-                }
-                for (int j0 = 0; j0 < a.k; j0 += 8) {   // eight rows' loads, then their sums in order
-                    float4 r[8];
+                auto load = [&](int j0) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int row = j0 + j < a.k ? sh.slot_row[t * a.k + j0 + j] : -1;
-                        r[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         if (row >= 0) r[j] = __ldcg(reinterpret_cast<const float4 *>(y + (size_t)row * a.H));
                     }
+                };
+#pragma unroll
+                for (int s = 0; s < kMaxShared; ++s)   // all loads first, then the sums in order
+                    if (s < a.S)
+                        sr[s] = __ldcg(reinterpret_cast<const float4 *>(y + (size_t)(s * a.T + t) * a.H));
+                load(0);
+#pragma unroll
+                for (int s = 0; s < kMaxShared; ++s)
+                    if (s < a.S) {
+                        o.x = __fadd_rn(o.x, sr[s].x), o.y = __fadd_rn(o.y, sr[s].y);
+                        o.z = __fadd_rn(o.z, sr[s].z), o.w = __fadd_rn(o.w, sr[s].w);
+                    }
+                for (int j0 = 0; j0 < a.k; j0 += 8) {
+                    if (j0) load(j0);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         if (j0 + j >= a.k || sh.slot_row[t * a.k + j0 + j] < 0) continue;
@@ -1309,6 +1324,11 @@ int launch_layer_few(const moe_config *c, const moe_weights *w, int T, const voi
     a.w2 = static_cast<const uint8_t *>(w->w2);
     a.w13_s = w->w13_scales;
     a.w2_s = w->w2_scales;
+    const size_t IH = (size_t)c->inter * H;   // elements of W2
+    a.pf_w2_one = c->dtype == MOE_DTYPE_MXFP4 ? IH / 2 : c->dtype == MOE_DTYPE_BF16 ? 2 * IH : IH;
+    a.pf_w13_one = 2 * a.pf_w2_one;
+    a.pf_w13 = std::min(S * a.pf_w13_one, kPrefetchMost);
+    a.pf_w2 = std::min(S * a.pf_w2_one, kPrefetchMost);
     a.score = r.score;
     a.select = r.select;
     a.ids = reinterpret_cast<int32_t *>(b + L.topk_ids);
