@@ -1055,13 +1055,17 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.res_empty[buf]));
             }
             if (un.gu) ptx::fence_proxy_async_global();   // h is read by copies
-            __threadfence();
             __syncwarp();
             finish_pending();
+            // the warp's stores, then (one fence by one lane, after the warp's
+            // barrier) the count
             if (un.gu) {
                 if (lane == 0) ptx::red_release_gpu_add(h_done + un.gi, 1);
             } else {
-                if (lane == 0) before = atomicAdd(col_done + un.tile * kPublishers + q, 1);
+                if (lane == 0) {
+                    __threadfence();
+                    before = atomicAdd(col_done + un.tile * kPublishers + q, 1);
+                }
                 pending = un.tile;
             }
         }
