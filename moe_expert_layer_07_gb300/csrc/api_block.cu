@@ -27,9 +27,9 @@ int check_few(const moe_config *cfg) {
 int check_mx4_gemm(int32_t groups, int32_t n_out, int32_t k_dim, int32_t rows) {
     if (groups <= 0 || n_out <= 0 || k_dim <= 0 || rows < 0) return MOE_ERR_INVALID_ARG;
     if (groups > 1024 || n_out % 128 || k_dim % 128) return MOE_ERR_UNSUPPORTED_SHAPE;
-    // tiles are counted in 32 bits
-    if (((int64_t)n_out + 255) / 256 * (groups + (int64_t)rows / 128 + 1) > INT32_MAX)
-        return MOE_ERR_UNSUPPORTED_SHAPE;
+    // tiles, and a CTA's steps of 256 along K, are counted in 32 bits
+    const int64_t tiles = ((int64_t)n_out + 255) / 256 * (groups + (int64_t)rows / 128 + 1);
+    if (tiles > INT32_MAX || tiles * ((k_dim + 255) / 256) > INT32_MAX) return MOE_ERR_UNSUPPORTED_SHAPE;
     return MOE_OK;
 }
 

@@ -121,7 +121,10 @@ __device__ __forceinline__ void bf8(const uint4 &a, float (&f)[8]) {
 template <int NT>
 __device__ __forceinline__ void gate_dots(const uint16_t *w, const uint16_t *x, int H, int lane,
                                           float (&acc)[kTokChunk]) {
-    constexpr int U = NT == 1 ? 14 : 7;   // loads in flight
+    // Chunks of each row under way.  More of them make the code longer, and cold
+    // instructions cost more than the loads save: 14 for one token was 0.5 us
+    // slower, all 28 of the gate row 3 us.
+    constexpr int U = 7;
     const int n8 = H / 8;
     for (int c0 = lane; c0 < n8; c0 += 32 * U) {
         uint4 wv[U], xv[U][NT];
