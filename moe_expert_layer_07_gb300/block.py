@@ -45,14 +45,15 @@ _SIGS = {
 }
 
 
+_OUT = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+
+
 def _out_type(t) -> int:
     """MOE_OUT_* of a tensor."""
-    d = t.dtype
-    if d is torch.bfloat16:
-        return OUT_BF16
-    if d is torch.float32:
-        return OUT_F32
-    raise TypeError(f"expected a float32 or bfloat16 tensor, got {d}")
+    kind = _OUT.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"expected a float32 or bfloat16 tensor, got {t.dtype}")
+    return kind
 
 
 def _dense(t, shape, name):
@@ -73,20 +74,34 @@ def _bytes(t, shape, name):
 # ---- MXFP4 ------------------------------------------------------------------------------
 
 
+def _mx4_tensors(values, codes, scales):
+    """Checks the three tensors of a quantisation; (rows, cols, type of values)."""
+    shape = values.shape
+    cols = shape[-1]
+    kind = _OUT.get(values.dtype)
+    if kind is None:
+        _out_type(values)
+    # one test of all that holds in a correct call; what failed is looked up after
+    if not (values.is_cuda and codes.is_cuda and scales.is_cuda and values.is_contiguous()
+            and codes.is_contiguous() and scales.is_contiguous() and codes.dtype is torch.uint8
+            and scales.dtype is torch.uint8 and codes.shape[-1] * 2 == cols
+            and scales.shape[-1] == cols // 32 and codes.shape[:-1] == shape[:-1]
+            and scales.shape[:-1] == shape[:-1]):
+        _dense(values, shape, "values")
+        _bytes(codes, shape[:-1] + (cols // 2,), "codes")
+        _bytes(scales, shape[:-1] + (cols // 32,), "scales")
+    return (values.numel() // cols if cols else 0), cols, kind
+
+
 def mx4_quantize(x, codes=None, scales=None, stream=None):
     """x fp32 or bf16 [..., cols] -> (codes uint8 [..., cols/2], scales uint8 [..., cols/32])."""
-    shape = x.shape
-    lead, cols = shape[:-1], shape[-1]
-    kind = _out_type(_dense(x, shape, "x"))
-    ctail, stail = lead + (cols // 2,), lead + (cols // 32,)
     if codes is None:
-        codes = torch.empty(ctail, dtype=torch.uint8, device=x.device)
+        codes = torch.empty(x.shape[:-1] + (x.shape[-1] // 2,), dtype=torch.uint8, device=x.device)
     if scales is None:
-        scales = torch.empty(stail, dtype=torch.uint8, device=x.device)
-    _bytes(codes, ctail, "codes")
-    _bytes(scales, stail, "scales")
-    rc = lib().moe_mx4_quantize(x.numel() // cols if cols else 0, cols, x.data_ptr(), kind,
-                                codes.data_ptr(), scales.data_ptr(), _stream(stream))
+        scales = torch.empty(x.shape[:-1] + (x.shape[-1] // 32,), dtype=torch.uint8, device=x.device)
+    rows, cols, kind = _mx4_tensors(x, codes, scales)
+    rc = lib().moe_mx4_quantize(rows, cols, x.data_ptr(), kind, codes.data_ptr(), scales.data_ptr(),
+                                _stream(stream))
     if rc:
         _check(rc, "moe_mx4_quantize")
     return codes, scales
@@ -94,16 +109,12 @@ def mx4_quantize(x, codes=None, scales=None, stream=None):
 
 def mx4_dequantize(codes, scales, out=None, stream=None):
     """The values [..., cols] (a new bf16 tensor unless `out`, fp32 or bf16, is given)."""
-    shape = codes.shape
-    lead, half = shape[:-1], shape[-1]
-    cols = 2 * half
-    _bytes(codes, shape, "codes")
-    _bytes(scales, lead + (cols // 32,), "scales")
     if out is None:
-        out = torch.empty(lead + (cols,), dtype=torch.bfloat16, device=codes.device)
-    _dense(out, lead + (cols,), "out")
-    rc = lib().moe_mx4_dequantize(codes.numel() // half if half else 0, cols, codes.data_ptr(),
-                                  scales.data_ptr(), out.data_ptr(), _out_type(out), _stream(stream))
+        out = torch.empty(codes.shape[:-1] + (codes.shape[-1] * 2,), dtype=torch.bfloat16,
+                          device=codes.device)
+    rows, cols, kind = _mx4_tensors(out, codes, scales)
+    rc = lib().moe_mx4_dequantize(rows, cols, codes.data_ptr(), scales.data_ptr(), out.data_ptr(),
+                                  kind, _stream(stream))
     if rc:
         _check(rc, "moe_mx4_dequantize")
     return out
@@ -246,40 +257,72 @@ def block_norm(residual, y=None, residual_out=None, x_out=None, w_post=None, b_p
     bf16, or None; gate [H], [T] or [T, H] (for T == H a one-dimensional gate is by feature)."""
     shape = residual.shape
     T, H = shape
-    rtype = _out_type(_dense(residual, shape, "residual"))
-    ytype = OUT_F32
+    out = _OUT.get
+    rtype = out(residual.dtype)
+    ytype = OUT_F32 if y is None else out(y.dtype)
+    # one test of all that holds in a correct call; what failed is looked up after
+    good = rtype is not None and ytype is not None and residual.is_cuda and residual.is_contiguous()
     if y is not None:
-        ytype = _out_type(_dense(y, shape, "y"))
-    if residual_out is not None and _out_type(_dense(residual_out, shape, "residual_out")) != rtype:
-        raise TypeError("residual_out must have residual's type")
-    if x_out is not None and _out_type(_dense(x_out, shape, "x_out")) != OUT_BF16:
-        raise TypeError("x_out must be bfloat16")
-    mode, ptype = GATE_NONE, None
+        good = good and y.shape == shape and y.is_cuda and y.is_contiguous()
+    if residual_out is not None:
+        good = (good and residual_out.shape == shape and residual_out.dtype is residual.dtype
+                and residual_out.is_cuda and residual_out.is_contiguous())
+    if x_out is not None:
+        good = (good and x_out.shape == shape and x_out.dtype is torch.bfloat16 and x_out.is_cuda
+                and x_out.is_contiguous())
+    mode, pdtype, row = GATE_NONE, None, (H,)
+    for t in (w_post, b_post, w_pre, b_pre):
+        if t is not None:
+            if pdtype is None:
+                pdtype = t.dtype
+            good = good and t.shape == row and t.dtype is pdtype and t.is_cuda and t.is_contiguous()
     if gate is not None:
         g = gate.shape
-        mode = GATE_FEATURE if g == (H,) else GATE_TOKEN if g == (T,) else GATE_FULL
-        _dense(gate, g if mode != GATE_FULL else shape, "gate")
-        ptype = _out_type(gate)
-    row = (H,)
-    for name, t in (("w_post", w_post), ("b_post", b_post), ("w_pre", w_pre), ("b_pre", b_pre)):
-        if t is not None:
-            kind_t = _out_type(_dense(t, row, name))
-            if ptype is None:
-                ptype = kind_t
-            elif kind_t != ptype:
-                raise TypeError("norm weights, biases and gate must share one type")
-    key = (H, kind, ytype, rtype, OUT_BF16 if ptype is None else ptype, mode, eps, residual_scale,
-           branch_scale)
+        mode = GATE_FEATURE if g == row else GATE_TOKEN if g == (T,) else GATE_FULL
+        if pdtype is None:
+            pdtype = gate.dtype
+        good = (good and gate.dtype is pdtype and gate.is_cuda and gate.is_contiguous()
+                and (mode != GATE_FULL or g == shape))
+    ptype = OUT_BF16 if pdtype is None else out(pdtype)
+    if not good or ptype is None:
+        _refuse_norm(shape, residual, y, residual_out, x_out, gate, mode,
+                     (("w_post", w_post), ("b_post", b_post), ("w_pre", w_pre), ("b_pre", b_pre)))
+    key = (H, kind, ytype, rtype, ptype, mode, eps, residual_scale, branch_scale)
     d = _NORMS.get(key)   # descriptions are plain values: made once each
     if d is None:
         if len(_NORMS) >= 256:
             _NORMS.clear()
         d = _NORMS[key] = Norm(*key)
-    rc = lib().moe_block_norm(d, T, _ptr(y), residual.data_ptr(), _ptr(gate), _ptr(w_post),
-                              _ptr(b_post), _ptr(w_pre), _ptr(b_pre), _ptr(residual_out),
-                              _ptr(x_out), _stream(stream))
+    rc = lib().moe_block_norm(
+        d, T, None if y is None else y.data_ptr(), residual.data_ptr(),
+        None if gate is None else gate.data_ptr(), None if w_post is None else w_post.data_ptr(),
+        None if b_post is None else b_post.data_ptr(), None if w_pre is None else w_pre.data_ptr(),
+        None if b_pre is None else b_pre.data_ptr(),
+        None if residual_out is None else residual_out.data_ptr(),
+        None if x_out is None else x_out.data_ptr(), _stream(stream))
     if rc:
         _check(rc, "moe_block_norm")
+
+
+def _refuse_norm(shape, residual, y, residual_out, x_out, gate, mode, params):
+    """Raises what is wrong with block_norm's tensors."""
+    for name, t in (("residual", residual), ("y", y), ("residual_out", residual_out),
+                    ("x_out", x_out)):
+        if t is not None:
+            _out_type(_dense(t, shape, name))
+    if residual_out is not None and residual_out.dtype is not residual.dtype:
+        raise TypeError("residual_out must have residual's type")
+    if x_out is not None and x_out.dtype is not torch.bfloat16:
+        raise TypeError("x_out must be bfloat16")
+    types = set()
+    for name, t in params:
+        if t is not None:
+            types.add(_out_type(_dense(t, shape[1:], name)))
+    if gate is not None:
+        types.add(_out_type(_dense(gate, shape if mode == GATE_FULL else gate.shape, "gate")))
+    if len(types) > 1:
+        raise TypeError("norm weights, biases and gate must share one type")
+    raise ValueError("block_norm: unsuitable tensors")
 
 
 _NORMS: dict = {}

@@ -151,5 +151,11 @@ def test_binding_refuses_wrong_tensors():
         moe.block._dense(x, (4, 32), "x")
     with pytest.raises(TypeError):
         moe.block._out_type(x.half())
+    b = torch.zeros(64, dtype=torch.bfloat16)
+    for bad in (dict(residual=x), dict(residual=x, y=x[:2]), dict(residual=x, residual_out=x.bfloat16()),
+                dict(residual=x, x_out=x), dict(residual=x, w_pre=b, gate=b.float()),
+                dict(residual=x, gate=b[:3]), dict(residual=x.half()), dict(residual=x.t())):
+        with pytest.raises((TypeError, ValueError)):
+            moe.block_norm(**bad)
     s = dataclasses.replace(synth.CONFIGS["r1_mini"], dtype="mxfp4")
     assert moe.make_config(s, 4).dtype == moe.BF16         # FewTokenLayer sets its own
