@@ -10,10 +10,18 @@
 //
 // With so few rows an expert's weights are read for one to a few products
 // each, so the time is the weights' bytes over the memory rate: 400 MB, 59 us
-// at the copy rate, for one token of nine 44 MB experts.  Everything else has
-// to hide behind that stream: a producer thread keeps a ring of weight tiles
-// (MOE_LAYOUT_TILES, one bulk copy each) full, and runs ahead into the next
-// unit, and into the down products, while the consumers still wait for h.
+// at the copy rate, for one token of nine 44 MB experts in FP8, where the two
+// kernels take 71.5.  The difference is the first kernel and the selection
+// (about 8 us, in which only the shared experts' weights move, to L2) and the
+// join of the two phases.  In the FFN kernel everything hides behind the
+// stream of weights; its warps are:
+//   producer   keeps a ring of weight tiles (MOE_LAYOUT_TILES, bulk copies)
+//              full, and runs ahead into the next unit, and into the down
+//              products, while the tokens still wait for h
+//   tokens     the other side of the products, x or h, into the same stages
+//   consumers  the products
+//   publishers a unit's results to h or y, and the combine, while the
+//              consumers are in the next unit
 //
 // Units, claimed in order from a counter: for every active group (an expert
 // with rows) and 128 of its features, gate and up (2 x 128 weight rows against
@@ -21,19 +29,21 @@
 // memory); then for every active group and 128 hidden columns, down.  A down
 // unit waits (bounded) until its group's h is complete.  Every unit that is
 // waited for was claimed before by a running CTA, which finishes it without
-// waiting for anyone, so no co-residency is assumed.  The CTA that adds the
-// last group's rows to a block of 128 columns combines them for all tokens, in
-// the combine kernel's order: no atomic sums, the result does not depend on
-// who came when.
+// waiting for anyone, so no co-residency is assumed.  The warp that adds the
+// last group's rows to 32 columns combines them for all tokens, in the combine
+// kernel's order: no atomic sums, the result does not depend on who came when.
 //
-// The products use the warp-wide MMA (m16n8): 16 weight rows of a warp on its
-// M side, up to 8 tokens on N.  tcgen05 would leave its 128-row tile's
+// BF16 and FP8 products use the warp-wide MMA (m16n8): 16 weight rows of a warp
+// on its M side, up to 8 tokens on N.  tcgen05 would leave its 128-row tile's
 // accumulators to be read back and scaled per 128 of K in FP8; here they are
 // already in registers, and the tensor rate does not matter: at 24 bytes of
 // weights a clock and SM the warps' MMA is under a quarter busy.  A thread
 // reads 16 bytes of a weight row at a time (the order of K inside a product is
 // free as long as both sides agree), rows 0, 4, 1, 5, ... of eight in MMA
-// order, which makes the reads conflict-free on the swizzled tiles.
+// order, which makes the reads conflict-free on the swizzled tiles.  MXFP4
+// carries twice the values per byte, whose conversion kept the warps busy for
+// longer than the bytes took to come; there one thread issues tcgen05's
+// block-scaled products, which take codes and scales as they are.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -69,8 +79,8 @@ enum { DT_BF16 = MOE_DTYPE_BF16, DT_FP8 = MOE_DTYPE_FP8_BLOCK128, DT_MX4 = MOE_D
 //         stands for before its scale (256 bytes), then the fp32 scale.  Such a
 //         segment is one bulk copy.
 //  MXFP4  packed codes, row-major; scale bytes as [K tile][row][16] with a
-//         row's four of the tile in front, which is how the scales' copy to
-//         tensor memory takes 32 rows (16 of them matter here).
+//         row's four of the tile in front: tile and row as the boxes of codes,
+//         16 rows from any row one bulk copy (which wants its start aligned).
 constexpr int kSegment = 272;
 constexpr int kScaleRow = 16;
 
@@ -674,7 +684,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     if (warp == kWarps - 1)
         for (int p = 0; p < 2; ++p) {
             const size_t bytes = p ? a.pf_w2 : a.pf_w13;   // of all shared experts, at most kPrefetchMost
-            const uint8_t *w = p ? a.w2 + a.E * (a.pf_w2_one) : a.w13 + a.E * (a.pf_w13_one);
+            const uint8_t *w = p ? a.w2 + a.E * a.pf_w2_one : a.w13 + a.E * a.pf_w13_one;
             for (size_t o = ((size_t)lane * gridDim.x + blockIdx.x) * kPrefetchBytes; o < bytes;
                  o += (size_t)32 * gridDim.x * kPrefetchBytes)
                 ptx::prefetch_l2(w + o, (uint32_t)min((size_t)kPrefetchBytes, bytes - o));
@@ -1213,9 +1223,9 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                                    MOE_DEV_TIMEOUT);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-    #pragma unroll
+#pragma unroll
             for (int j = 0; j < NT; ++j)
-    #pragma unroll
+#pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int c = 8 * j + 2 * t4 + (i & 1);
                     if (c < n)

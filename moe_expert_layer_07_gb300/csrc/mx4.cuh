@@ -58,18 +58,6 @@ __device__ __forceinline__ void mx4_half8(uint32_t codes, uint32_t (&h)[4]) {
         : "=&r"(h[0]), "=&r"(h[1]), "=&r"(h[2]), "=&r"(h[3])
         : "r"(codes));
 }
-// fp16 values of the codes of four values times `inv`
-__device__ __forceinline__ uint2 mx4_as_half4(float a, float b, float c, float d, float inv) {
-    uint2 o;
-    asm("{\n\t.reg .b8 b0, b1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b0, %3, %2;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b1, %5, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t}"
-        : "=&r"(o.x), "=&r"(o.y)
-        : "f"(a * inv), "f"(b * inv), "f"(c * inv), "f"(d * inv));
-    return o;
-}
 __device__ __forceinline__ void mx4_values8(uint32_t codes, float scale, float (&v)[8]) {
     uint32_t h[4];
     mx4_half8(codes, h);

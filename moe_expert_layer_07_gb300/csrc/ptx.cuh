@@ -155,18 +155,6 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
                  "l"(reinterpret_cast<uint64_t>(src))
                  : "memory");
 }
-// 16 bytes past L1, in groups: cp_async_wait<N> waits until at most N of this
-// thread's newest groups are still on their way.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(src))
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 // The mbarrier receives one arrival once this thread's earlier cp.async
 // copies have landed (the arrival counts toward the barrier's init count).
 __device__ __forceinline__ void cp_async_mbar_arrive(uint32_t bar) {
@@ -370,15 +358,6 @@ __device__ __forceinline__ uint64_t sdesc_k_sw128(uint32_t saddr) {
 __device__ __forceinline__ uint64_t sdesc_k_sw64(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(512 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)4 << 61);
-}
-// 32 rows of 16 bytes, no swizzle: 8-row groups 128 bytes apart
-__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(128 >> 4) << 32) |
-           ((uint64_t)1 << 46);
-}
-__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t sdesc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
-                 : "memory");
 }
 __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
