@@ -188,25 +188,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == kMmaWarp) {
         // ---- products --------------------------------------------------------------
-        if (lane == 0) {
-            uint32_t it = 0, tiles = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++tiles) {
-                if (!wait_bounded(smem_u32(&acc_empty), (tiles & 1) ^ 1u, abort_flag, args.status,
-                                  MOE_DEV_TIMEOUT))
-                    break;
+        // The whole warp waits and one thread issues.
+        const bool elected = elect_one();
+        uint32_t it = 0, tiles = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++tiles) {
+            ok = wait_bounded(smem_u32(&acc_empty), (tiles & 1) ^ 1u, abort_flag, args.status,
+                              MOE_DEV_TIMEOUT);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            for (int s = 0; s < steps; ++s, ++it) {
+                const uint32_t slot = it % kStages;
+                ok = wait_bounded(smem_u32(&sf_bar[slot]), (it / kStages) & 1, abort_flag, args.status,
+                                  MOE_DEV_TIMEOUT);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
                 tc_fence_after();
-                for (int s = 0; s < steps; ++s, ++it) {
-                    const uint32_t slot = it % kStages;
-                    if (!wait_bounded(smem_u32(&sf_bar[slot]), (it / kStages) & 1, abort_flag, args.status,
-                                      MOE_DEV_TIMEOUT)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t base = smem_base + slot * kStageBytes;
-                    const uint32_t sf = tmem + kSfCol + slot * kSfStage;
-                    const int nk = min(2, KB - 2 * s);
+                const uint32_t base = smem_base + slot * kStageBytes;
+                const uint32_t sf = tmem + kSfCol + slot * kSfStage;
+                const int nk = min(2, KB - 2 * s);
+                if (elected) {
                     for (int k = 0; k < nk; ++k) {
                         const uint32_t sfa = sf + k * 12, sfb = sfa + 4;
                         const uint64_t ad = sdesc_k_sw128(base + kAOff) + 4 * k;
@@ -215,76 +217,86 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_mxf4(tmem, ad + 2, bd + 2, idesc_mxf4(2), sfa, sfb, 1);
                     }
                     mma_commit(smem_u32(&empty_bar[slot]));
+                    if (s == steps - 1) mma_commit(smem_u32(&acc_full));
                 }
-                if (ok) mma_commit(smem_u32(&acc_full));
+                __syncwarp();
             }
+        }
+        if (elected) {
             mma_commit(smem_u32(&drain_bar));
             wait_drain(smem_u32(&drain_bar), 0);
         }
         __syncwarp();
     } else if (warp < kFirstSfWarp) {
         // ---- operands: one warp for each ring slot -----------------------------------
-        // Lane 0 issues the slot's copies; the warp puts the token rows' scale
-        // bytes, loaded before the slot is free, into their place.  (One thread
-        // issuing every slot's copies kept the products waiting.)
+        // One thread issues the slot's copies; the warp puts the token rows'
+        // scale bytes into their place.  Addresses and scale bytes are there
+        // before the slot is free: from the last product of a stage to the next
+        // one's in its slot everything here is in line.  (One thread issuing
+        // every slot's copies kept the products waiting; with the addresses
+        // formed after the wait, by lane 0, a slot's copies took 1240 cycles to
+        // issue.)
         const uint32_t mine = warp - kFirstSlotWarp;
         uint8_t *smem = dsmem + (smem_base - smem_u32(dsmem));
         const uint32_t base = smem_base + mine * kStageBytes, fb = smem_u32(&full_bar[mine]);
         const size_t pitch = args.k_dim / 32;
         const uint64_t pol_w = policy_evict_normal(), pol_a = policy_evict_last();
-        const int tiles = total > (int)blockIdx.x ? (total - (int)blockIdx.x - 1) / (int)gridDim.x + 1 : 0;
-        const int stages = tiles * steps;   // in 32 bits: checked by the entry point
-        int at = -1;                        // the tile that `tl` describes
-        Tile tl = {};
-        uint32_t used = 0;                  // stages of this slot so far
+        uint32_t used = 0, first = mine;   // stages of this slot so far; its first step in the tile
         bool ok = true;
-        for (int it = 0; it < stages; ++it) {
-            if (it % kStages == (int)mine) {
-                const int j = it / steps, s = it - j * steps;
-                if (j != at) {
-                    at = j;
-                    tl = decode(blockIdx.x + j * gridDim.x, G, s_tiles, s_off);
-                }
-                const int nb = SW || 2 * tl.nt + 1 < nblocks ? 2 : 1, nk = min(2, KB - 2 * s);
-                const bool wide = tl.nvalid > 32;   // boxes of 64 rows, or one of 32
-                const int boxes = wide ? (tl.nvalid + 63) / 64 : 1;
+        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            if ((int)first >= steps) {     // none in this tile
+                first -= steps;
+                continue;
+            }
+            const Tile tl = decode(t, G, s_tiles, s_off);
+            const int nb = SW || 2 * tl.nt + 1 < nblocks ? 2 : 1;
+            const bool wide = tl.nvalid > 32, two = tl.nvalid > 64;   // boxes of 64 rows, or one of 32
+            const uint32_t abytes = (two ? 128 : wide ? 64 : 32) * 128;
+            const CUtensorMap *tma = wide ? &tmA : &tmA32;
+            const size_t w0 = ((size_t)tl.g * nblocks + (SW ? tl.nt : 2 * tl.nt)) * KB;   // tiles
+            const size_t w1 = w0 + (size_t)(SW ? NT : 1) * KB;
+            const uint8_t *rows[4];   // this lane's rows' scale bytes
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                rows[q] = args.a_scales + (size_t)(tl.row0 + min(lane + 32 * q, tl.nvalid - 1)) * pitch;
+            int s = first;
+            for (; s < steps; s += kStages) {
+                const int nk = min(2, KB - 2 * s);
+                const uint8_t *wa = args.w + (w0 + 2 * s) * kTileBytes, *wb = args.w + (w1 + 2 * s) * kTileBytes;
+                const uint8_t *sa = args.w_scales + (w0 + 2 * s) * 512, *sb = args.w_scales + (w1 + 2 * s) * 512;
+                const uint32_t bytes = abytes + nk * nb * (kTileBytes + 512);
                 uint32_t v[2][4];
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int r = lane + 32 * q;
-                        v[k][q] = 0x7f7f7f7fu;
-                        if (k < nk && r < tl.nvalid)
-                            v[k][q] = __ldg(reinterpret_cast<const uint32_t *>(
-                                args.a_scales + (size_t)(tl.row0 + r) * pitch + (2 * s + k) * 4));
-                    }
+                    for (int q = 0; q < 4; ++q)   // rows past the last are the last: not stored
+                        v[k][q] = __ldg(reinterpret_cast<const uint32_t *>(rows[q] + (2 * s + (k < nk ? k : 0)) * 4));
                 ok = wait_bounded(smem_u32(&empty_bar[mine]), (used & 1) ^ 1u, abort_flag, args.status,
                                   MOE_DEV_TIMEOUT);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 ++used;
-                if (lane == 0) {
-                    mbar_expect_tx(fb, (wide ? boxes * 64 : 32) * 128 + nk * nb * (kTileBytes + 512));
-                    for (int n = 0; n < nb; ++n) {
-                        const size_t block = (size_t)tl.g * nblocks + (SW ? tl.nt + n * NT : 2 * tl.nt + n);
-                        const size_t tile = block * KB + 2 * s;
-                        for (int k = 0; k < nk; ++k)
-                            bulk_load(base + kBOff + (2 * k + n) * kTileBytes, args.w + (tile + k) * kTileBytes,
-                                      kTileBytes, fb, pol_w);
-                        bulk_load(base + kSBOff + 2 * n * 512, args.w_scales + tile * 512, nk * 512, fb, pol_w);
+                if (elect_one()) {
+                    mbar_expect_tx(fb, bytes);
+                    bulk_load(base + kBOff, wa, kTileBytes, fb, pol_w);
+                    if (nb > 1) bulk_load(base + kBOff + kTileBytes, wb, kTileBytes, fb, pol_w);
+                    if (nk > 1) {
+                        bulk_load(base + kBOff + 2 * kTileBytes, wa + kTileBytes, kTileBytes, fb, pol_w);
+                        if (nb > 1) bulk_load(base + kBOff + 3 * kTileBytes, wb + kTileBytes, kTileBytes, fb, pol_w);
                     }
-                    for (int q = 0; q < boxes; ++q)
-                        tma_load_2d(base + kAOff + q * 64 * 128, wide ? &tmA : &tmA32, s * 128,
-                                    tl.row0 + q * 64, fb, pol_a);
+                    tma_load_2d(base + kAOff, tma, s * 128, tl.row0, fb, pol_a);
+                    if (two) tma_load_2d(base + kAOff + 64 * 128, tma, s * 128, tl.row0 + 64, fb, pol_a);
+                    bulk_load(base + kSBOff, sa, nk * 512, fb, pol_w);
+                    if (nb > 1) bulk_load(base + kSBOff + 2 * 512, sb, nk * 512, fb, pol_w);
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
                     *reinterpret_cast<uint4 *>(smem + mine * kStageBytes + kSAOff + k * 512 + lane * 16) =
                         make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(fb);
+                if (elect_one()) mbar_arrive(fb);
             }
+            first = s - steps;
         }
         // copies in flight have to land before the CTA gives up its memory
         if (!ok && used) wait_drain(fb, (used - 1) & 1);
@@ -315,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sf_bar[slot]));
+            if (elect_one()) mbar_arrive(smem_u32(&sf_bar[slot]));
         }
     } else {
         // ---- epilogue ------------------------------------------------------------------
