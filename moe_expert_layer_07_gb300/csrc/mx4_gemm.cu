@@ -41,23 +41,32 @@
 namespace moe {
 namespace {
 
-constexpr int kTM = 128, kTN = 256;
-constexpr int kStages = 4;
-constexpr int kTileBytes = 128 * 64;                     // 128 rows x 128 of K
-constexpr int kAOff = 0, kBOff = 2 * kTileBytes;         // B: [K block][weight block]
-constexpr int kSAOff = kBOff + 4 * kTileBytes;           // scales of the token rows, 512 each
-constexpr int kSBOff = kSAOff + 2 * 512;                 // of the weights: [weight block][K block]
-constexpr int kStageBytes = kSBOff + 4 * 512;
-constexpr int kSlotWarps = 4, kEpiWarps = 8;
-constexpr int kMmaWarp = 0, kFirstSlotWarp = 1, kFirstSfWarp = kFirstSlotWarp + kSlotWarps;
-constexpr int kSfWarps = 4, kFirstEpiWarp = kFirstSfWarp + kSfWarps;
-constexpr int kThreads = (kFirstEpiWarp + kEpiWarps) * 32;
+constexpr int kTN = 256;               // columns of a tile: two weight blocks
+constexpr int kTileBytes = 128 * 64;   // 128 rows x 128 of K
 constexpr int kMaxGroups = 1024;
-constexpr int kSmemBytes = kStages * kStageBytes + 1024;
-// tensor memory: the accumulator, then for each ring slot and K block the
-// scales of the token rows (4 columns) and of the weight rows (8)
 constexpr int kTmemCols = 512, kSfCol = kTN, kSfStage = 2 * (4 + 8);
-static_assert(kSlotWarps == kStages, "slot warp i serves ring slot i");
+
+// A ring slot: 128 token rows x 256 of K (this CTA's), then the weights of both
+// blocks ([K block][weight block]) or, in a pair, of this CTA's one; the scales
+// of the token rows and of both weight blocks ([weight block][K block]), 512
+// bytes for a block of 128 rows and of K.
+// Tensor memory: the accumulator, then for each slot and K block the scales of
+// the token rows (4 columns) and of the weight rows (8).
+template <bool SW, bool PAIR>
+struct Shape {
+    static constexpr int kTM = PAIR ? 256 : 128;   // token rows of a tile
+    static constexpr int kBlocks = PAIR ? 1 : 2;   // weight blocks in a CTA's ring
+    static constexpr int kStages = PAIR ? 6 : 4;
+    static constexpr int kAOff = 0, kBOff = 2 * kTileBytes;
+    static constexpr int kSAOff = kBOff + 2 * kBlocks * kTileBytes, kSBOff = kSAOff + 2 * 512;
+    static constexpr int kStageBytes = kSBOff + 4 * 512;
+    static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+    static constexpr int kMmaWarp = 0, kFirstSlotWarp = 1, kSlotWarps = kStages;
+    static constexpr int kFirstSfWarp = kFirstSlotWarp + kSlotWarps, kSfWarps = 4;
+    static constexpr int kFirstEpiWarp = kFirstSfWarp + kSfWarps, kEpiWarps = SW ? 16 : 8;
+    static constexpr int kThreads = (kFirstEpiWarp + kEpiWarps) * 32;
+    static_assert(kSfCol + kStages * kSfStage <= kTmemCols, "tensor memory");
+};
 
 struct Mx4Args {
     int groups, n_out, k_dim, rows;
@@ -72,19 +81,20 @@ struct Mx4Args {
 
 // instruction descriptor: e2m1 x e2m1, ue8m0 scales, K = 64, scale bytes `sf`
 // and `sf` + 1 of each 32-bit column
-__host__ __device__ constexpr uint32_t idesc_mxf4(int sf) {
+__host__ __device__ constexpr uint32_t idesc_mxf4(int rows, int sf) {
     return ((uint32_t)sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kTN >> 3) << 17) | (1u << 23) |
-           ((uint32_t)(kTM >> 4) << 24) | ((uint32_t)sf << 29);
+           ((uint32_t)(rows >> 4) << 24) | ((uint32_t)sf << 29);
 }
 
 struct Tile {
     int g, nt, row0, nvalid;
 };
 
-// Tile t -> (group, column tile, first row, valid rows); s_tiles holds each
-// group's first tile.  Row tiles of one column tile are neighbours, so they
-// share its weights in L2.
-__device__ __forceinline__ Tile decode(int t, int G, const int *s_tiles, const int *s_off) {
+// Tile t -> (group, column tile; this CTA's first row and its valid rows, of the
+// second CTA possibly none); s_tiles holds each group's first tile.  Row tiles
+// of one column tile are neighbours, so they share its weights in L2.
+template <int kTM>
+__device__ __forceinline__ Tile decode(int t, int rank, int G, const int *s_tiles, const int *s_off) {
     int lo = 0, hi = G;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -97,8 +107,9 @@ __device__ __forceinline__ Tile decode(int t, int G, const int *s_tiles, const i
     const int local = t - s_tiles[lo];
     w.nt = local / mtiles;
     const int mt = local - w.nt * mtiles;
-    w.row0 = s_off[lo] + mt * kTM;
-    w.nvalid = min(kTM, rows - mt * kTM);
+    const int r = mt * kTM + rank * 128;
+    w.row0 = s_off[lo] + r;
+    w.nvalid = max(0, min(128, rows - r));
     return w;
 }
 
@@ -109,11 +120,16 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
                  : "memory");
 }
 
-template <bool SW>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool SW, bool PAIR>
+__global__ void __launch_bounds__((Shape<SW, PAIR>::kThreads), 1)
     mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
                     const Mx4Args args) {
     using namespace ptx;
+    using S = Shape<SW, PAIR>;
+    constexpr int kTM = S::kTM, kStages = S::kStages, kStageBytes = S::kStageBytes, kThreads = S::kThreads;
+    constexpr int kAOff = S::kAOff, kBOff = S::kBOff, kSAOff = S::kSAOff, kSBOff = S::kSBOff;
+    constexpr int kMmaWarp = S::kMmaWarp, kFirstSlotWarp = S::kFirstSlotWarp, kFirstSfWarp = S::kFirstSfWarp;
+    constexpr int kFirstEpiWarp = S::kFirstEpiWarp, kCtas = PAIR ? 2 : 1;
     extern __shared__ uint8_t dsmem[];
     __shared__ __align__(8) uint64_t full_bar[kStages], sf_bar[kStages], empty_bar[kStages], acc_full, acc_empty, drain_bar;
     __shared__ uint32_t tmem_slot;
@@ -122,6 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t smem_base = (smem_u32(dsmem) + 1023u) & ~1023u;
+    const int rank = PAIR ? (int)cluster_rank() : 0, pair = blockIdx.x / kCtas, pairs = gridDim.x / kCtas;
     const int G = args.groups;
     const int nblocks = args.n_out / 128;                       // weight blocks of a group
     const int NT = SW ? nblocks / 2 : (nblocks + 1) / 2;        // column tiles
@@ -131,19 +148,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(smem_u32(&full_bar[s]), 1);
-            mbar_init(smem_u32(&sf_bar[s]), kSfWarps);
+            mbar_init(smem_u32(&sf_bar[s]), kCtas * S::kSfWarps);   // of a pair, in its first CTA
             mbar_init(smem_u32(&empty_bar[s]), 1);
         }
         mbar_init(smem_u32(&acc_full), 1);
-        mbar_init(smem_u32(&acc_empty), kEpiWarps);
+        mbar_init(smem_u32(&acc_empty), kCtas * S::kEpiWarps);     // as sf_bar
         mbar_init(smem_u32(&drain_bar), 1);
         s_abort = 0;
         s_bad = 0;
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
-        tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
-        tmem_relinquish();
+        if constexpr (PAIR) {
+            tmem_alloc2(smem_u32(&tmem_slot), kTmemCols);
+            tmem_relinquish2();
+        } else {
+            tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
+            tmem_relinquish();
+        }
     }
     if (warp == kFirstSlotWarp && lane == 0) {
         tma_prefetch_desc(&tmA);
@@ -180,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync();   // both CTAs' barriers are set up
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const int total = s_bad ? 0 : s_tiles[G];
@@ -187,12 +210,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         atomicOr(args.status, MOE_DEV_BAD_OFFSETS);
 
     if (warp == kMmaWarp) {
-        // ---- products --------------------------------------------------------------
+        // ---- products, of both CTAs by the first ---------------------------------------
         // The whole warp waits and one thread issues.
         const bool elected = elect_one();
+        auto commit = [](uint32_t bar, uint16_t ctas) {
+            if constexpr (PAIR) mma_commit2(bar, ctas);
+            else mma_commit(bar);
+        };
         uint32_t it = 0, tiles = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++tiles) {
+        for (int t = pair; t < total && ok && rank == 0; t += pairs, ++tiles) {
             ok = wait_bounded(smem_u32(&acc_empty), (tiles & 1) ^ 1u, abort_flag, args.status,
                               MOE_DEV_TIMEOUT);
             ok = __all_sync(0xffffffffu, ok);
@@ -201,29 +228,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s = 0; s < steps; ++s, ++it) {
                 const uint32_t slot = it % kStages;
                 ok = wait_bounded(smem_u32(&sf_bar[slot]), (it / kStages) & 1, abort_flag, args.status,
-                                  MOE_DEV_TIMEOUT);
+                                        MOE_DEV_TIMEOUT);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t base = smem_base + slot * kStageBytes;
                 const uint32_t sf = tmem + kSfCol + slot * kSfStage;
-                const int nk = min(2, KB - 2 * s);
                 if (elected) {
-                    for (int k = 0; k < nk; ++k) {
-                        const uint32_t sfa = sf + k * 12, sfb = sfa + 4;
-                        const uint64_t ad = sdesc_k_sw128(base + kAOff) + 4 * k;
-                        const uint64_t bd = sdesc_k_sw64(base + kBOff + 2 * k * kTileBytes);
-                        mma_mxf4(tmem, ad, bd, idesc_mxf4(0), sfa, sfb, s + k > 0);
-                        mma_mxf4(tmem, ad + 2, bd + 2, idesc_mxf4(2), sfa, sfb, 1);
+                    const uint64_t ad = sdesc_k_sw128(base + kAOff), bd = sdesc_k_sw64(base + kBOff);
+                    constexpr int kNext = S::kBlocks * kTileBytes / 16;   // the next K block's weights
+                    auto product = [&](uint64_t a, uint64_t b, uint32_t idesc, uint32_t scales, uint32_t add) {
+                        if constexpr (PAIR) mma2_mxf4(tmem, a, b, idesc, scales, scales + 4, add);
+                        else mma_mxf4(tmem, a, b, idesc, scales, scales + 4, add);
+                    };
+                    product(ad, bd, idesc_mxf4(kTM, 0), sf, s > 0);
+                    product(ad + 2, bd + 2, idesc_mxf4(kTM, 2), sf, 1);
+                    if (2 * s + 1 < KB) {
+                        product(ad + 4, bd + kNext, idesc_mxf4(kTM, 0), sf + 12, 1);
+                        product(ad + 6, bd + kNext + 2, idesc_mxf4(kTM, 2), sf + 12, 1);
                     }
-                    mma_commit(smem_u32(&empty_bar[slot]));
-                    if (s == steps - 1) mma_commit(smem_u32(&acc_full));
+                    commit(smem_u32(&empty_bar[slot]), 3);
+                    if (s == steps - 1) commit(smem_u32(&acc_full), 3);
                 }
                 __syncwarp();
             }
         }
-        if (elected) {
-            mma_commit(smem_u32(&drain_bar));
+        if (elected && rank == 0) {
+            commit(smem_u32(&drain_bar), 1);
             wait_drain(smem_u32(&drain_bar), 0);
         }
         __syncwarp();
@@ -243,28 +274,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t pol_w = policy_evict_normal(), pol_a = policy_evict_last();
         uint32_t used = 0, first = mine;   // stages of this slot so far; its first step in the tile
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        for (int t = pair; t < total && ok; t += pairs) {
             if ((int)first >= steps) {     // none in this tile
                 first -= steps;
                 continue;
             }
-            const Tile tl = decode(t, G, s_tiles, s_off);
+            const Tile tl = decode<kTM>(t, rank, G, s_tiles, s_off);
             const int nb = SW || 2 * tl.nt + 1 < nblocks ? 2 : 1;
+            const int copies = PAIR ? rank < nb : nb;                 // weight blocks that this CTA loads
             const bool wide = tl.nvalid > 32, two = tl.nvalid > 64;   // boxes of 64 rows, or one of 32
-            const uint32_t abytes = (two ? 128 : wide ? 64 : 32) * 128;
+            const uint32_t abytes = (two ? 128 : wide ? 64 : tl.nvalid ? 32 : 0) * 128;
+            const int last = s_off[tl.g + 1] - 1;
             const CUtensorMap *tma = wide ? &tmA : &tmA32;
             const size_t w0 = ((size_t)tl.g * nblocks + (SW ? tl.nt : 2 * tl.nt)) * KB;   // tiles
             const size_t w1 = w0 + (size_t)(SW ? NT : 1) * KB;
             const uint8_t *rows[4];   // this lane's rows' scale bytes
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                rows[q] = args.a_scales + (size_t)(tl.row0 + min(lane + 32 * q, tl.nvalid - 1)) * pitch;
+                rows[q] = args.a_scales + (size_t)min(tl.row0 + lane + 32 * q, last) * pitch;
             int s = first;
             for (; s < steps; s += kStages) {
                 const int nk = min(2, KB - 2 * s);
-                const uint8_t *wa = args.w + (w0 + 2 * s) * kTileBytes, *wb = args.w + (w1 + 2 * s) * kTileBytes;
+                const uint8_t *wa = args.w + ((rank ? w1 : w0) + 2 * s) * kTileBytes, *wb = args.w + (w1 + 2 * s) * kTileBytes;
                 const uint8_t *sa = args.w_scales + (w0 + 2 * s) * 512, *sb = args.w_scales + (w1 + 2 * s) * 512;
-                const uint32_t bytes = abytes + nk * nb * (kTileBytes + 512);
+                const uint32_t bytes = abytes + nk * (copies * kTileBytes + nb * 512);
                 uint32_t v[2][4];
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
@@ -278,13 +311,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++used;
                 if (elect_one()) {
                     mbar_expect_tx(fb, bytes);
-                    bulk_load(base + kBOff, wa, kTileBytes, fb, pol_w);
-                    if (nb > 1) bulk_load(base + kBOff + kTileBytes, wb, kTileBytes, fb, pol_w);
-                    if (nk > 1) {
-                        bulk_load(base + kBOff + 2 * kTileBytes, wa + kTileBytes, kTileBytes, fb, pol_w);
-                        if (nb > 1) bulk_load(base + kBOff + 3 * kTileBytes, wb + kTileBytes, kTileBytes, fb, pol_w);
+                    if (PAIR) {   // a block's tiles along K are consecutive
+                        if (copies) bulk_load(base + kBOff, wa, nk * kTileBytes, fb, pol_w);
+                    } else {
+                        bulk_load(base + kBOff, wa, kTileBytes, fb, pol_w);
+                        if (nb > 1) bulk_load(base + kBOff + kTileBytes, wb, kTileBytes, fb, pol_w);
+                        if (nk > 1) {
+                            bulk_load(base + kBOff + 2 * kTileBytes, wa + kTileBytes, kTileBytes, fb, pol_w);
+                            if (nb > 1) bulk_load(base + kBOff + 3 * kTileBytes, wb + kTileBytes, kTileBytes, fb, pol_w);
+                        }
                     }
-                    tma_load_2d(base + kAOff, tma, s * 128, tl.row0, fb, pol_a);
+                    if (tl.nvalid) tma_load_2d(base + kAOff, tma, s * 128, tl.row0, fb, pol_a);
                     if (two) tma_load_2d(base + kAOff + 64 * 128, tma, s * 128, tl.row0 + 64, fb, pol_a);
                     bulk_load(base + kSBOff, sa, nk * 512, fb, pol_w);
                     if (nb > 1) bulk_load(base + kSBOff + 2 * 512, sb, nk * 512, fb, pol_w);
@@ -306,7 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // products, about 100 cycles each and six a stage.
         const uint8_t *smem = dsmem + (smem_base - smem_u32(dsmem));
         const uint32_t sf0 = tmem + ((uint32_t)(warp & 3) << 21) + kSfCol;   // lane 32 (warp & 3)
-        const int tiles = total > (int)blockIdx.x ? (total - (int)blockIdx.x - 1) / (int)gridDim.x + 1 : 0;
+        const int tiles = total > pair ? (total - pair - 1) / pairs + 1 : 0;
+        const uint32_t done = PAIR ? cluster_map(smem_u32(&sf_bar[0]), 0) : smem_u32(&sf_bar[0]);
         bool ok = true;
         for (int it = 0; it < tiles * steps; ++it) {
             const uint32_t slot = it % kStages;
@@ -327,72 +365,79 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (elect_one()) mbar_arrive(smem_u32(&sf_bar[slot]));
+            if (elect_one()) {
+                if constexpr (PAIR) mbar_arrive_cluster(done + slot * 8);
+                else mbar_arrive(done + slot * 8);
+            }
         }
     } else {
         // ---- epilogue ------------------------------------------------------------------
-        const int q = warp & 3, half = (warp - kFirstEpiWarp) >> 2;   // lane quarter, column half
-        const int m = 32 * q + lane;                                  // this thread's row of the tile
+        // A warp has 32 rows (its lane quarter) and 32 features of SwiGLU, or 128
+        // columns.  The accumulator is given back as soon as this warp's part
+        // of it is in registers: the next tile's products run under the rest.
+        const int q = warp & 3, part = (warp - kFirstEpiWarp) >> 2;
+        const int m = 32 * q + lane;   // this thread's row of the tile
         const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
+        const uint32_t given = PAIR ? cluster_map(smem_u32(&acc_empty), 0) : smem_u32(&acc_empty);
         uint32_t tiles = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x, ++tiles) {
-            const Tile tl = decode(t, G, s_tiles, s_off);
+        for (int t = pair; t < total; t += pairs, ++tiles) {
+            const Tile tl = decode<kTM>(t, rank, G, s_tiles, s_off);
             const bool ok = wait_bounded(smem_u32(&acc_full), tiles & 1, abort_flag, args.status,
                                          MOE_DEV_TIMEOUT);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             const bool valid = m < tl.nvalid;
-            const size_t row = tl.row0 + m;
-            // The accumulator is given back as soon as this warp's part of it
-            // is in registers: the next tile's products run under the rest.
+            const size_t row = (size_t)tl.row0 + m;
             auto release = [&]() {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&acc_empty));
-            };
-            if (SW) {
-                float h[64];
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    uint32_t g[16], u[16];
-                    tmem_ld16(lane_base + half * 64 + p * 16, g);
-                    tmem_ld16(lane_base + 128 + half * 64 + p * 16, u);
-                    tmem_wait_ld(g);
-                    tmem_wait_ld(u);
-                    if (p == 3) release();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        h[16 * p + j] = silu_mul(__uint_as_float(g[j]), __uint_as_float(u[j]));
+                if (lane == 0) {
+                    if constexpr (PAIR) mbar_arrive_cluster(given);
+                    else mbar_arrive(given);
                 }
-                uint32_t o[8], sc = 0;
+            };
+            if constexpr (SW) {
+                uint32_t g[2][16], u[2][16];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {   // 32 features, one block of scales
-                    uint32_t amax = 0;
+                for (int p = 0; p < 2; ++p) {
+                    tmem_ld16(lane_base + part * 32 + p * 16, g[p]);
+                    tmem_ld16(lane_base + 128 + part * 32 + p * 16, u[p]);
+                }
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) amax = max(amax, __float_as_uint(h[32 * b + j]) & 0x7fffffffu);
-                    const uint32_t byte = mx4_scale_byte(amax);
-                    sc |= byte << (8 * b);
+                for (int p = 0; p < 2; ++p) {
+                    tmem_wait_ld(g[p]);
+                    tmem_wait_ld(u[p]);
+                }
+                release();
+                float h[32];
+                uint32_t amax = 0;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float v[8];
+                for (int j = 0; j < 32; ++j) {   // a block of scales
+                    h[j] = silu_mul(__uint_as_float(g[j / 16][j % 16]), __uint_as_float(u[j / 16][j % 16]));
+                    amax = max(amax, __float_as_uint(h[j]) & 0x7fffffffu);
+                }
+                const uint32_t byte = mx4_scale_byte(amax);
+                uint32_t o[4];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = h[32 * b + 8 * j + i];
-                        o[4 * b + j] = mx4_codes8(v, byte);
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = h[8 * j + i];
+                    o[j] = mx4_codes8(v, byte);
                 }
                 if (valid) {
-                    store32(static_cast<uint8_t *>(args.c) + row * (args.n_out / 4) + tl.nt * 64 + half * 32, o);
-                    *reinterpret_cast<uint16_t *>(args.h_scales + row * (args.n_out / 64) + tl.nt * 4 + half * 2) =
-                        (uint16_t)sc;
+                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(args.c) + row * (args.n_out / 4) +
+                                               tl.nt * 64 + part * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+                    args.h_scales[row * (args.n_out / 64) + tl.nt * 4 + part] = (uint8_t)byte;
                 }
-            } else if (2 * tl.nt + half >= nblocks) {
+            } else if (2 * tl.nt + part >= nblocks) {
                 release();   // no second weight block
             } else if (args.c_bf16) {
                 uint32_t w[64];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     uint32_t r[16];
-                    tmem_ld16(lane_base + half * 128 + j * 16, r);
+                    tmem_ld16(lane_base + part * 128 + j * 16, r);
                     tmem_wait_ld(r);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -402,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 release();
-                uint16_t *o = static_cast<uint16_t *>(args.c) + row * args.n_out + tl.nt * kTN + half * 128;
+                uint16_t *o = static_cast<uint16_t *>(args.c) + row * args.n_out + tl.nt * kTN + part * 128;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     uint32_t v[8];
@@ -411,12 +456,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (valid) store32(o + 16 * j, v);
                 }
             } else {
-                float *o = static_cast<float *>(args.c) + row * args.n_out + tl.nt * kTN + half * 128;
+                float *o = static_cast<float *>(args.c) + row * args.n_out + tl.nt * kTN + part * 128;
 #pragma unroll
                 for (int q4 = 0; q4 < 2; ++q4) {   // 64 columns at a time
                     uint32_t r[4][16];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) tmem_ld16(lane_base + half * 128 + q4 * 64 + j * 16, r[j]);
+                    for (int j = 0; j < 4; ++j) tmem_ld16(lane_base + part * 128 + q4 * 64 + j * 16, r[j]);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) tmem_wait_ld(r[j]);
                     if (q4 == 1) release();
@@ -432,34 +477,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
+    // neither CTA of a pair leaves while the other's products read its memory
+    // or its arrivals are on their way
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync();
     if (warp == kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        if constexpr (PAIR) tmem_dealloc2(tmem, kTmemCols);
+        else tmem_dealloc(tmem, kTmemCols);
     }
 }
 
-template <bool SW>
+template <bool SW, bool PAIR>
 int launch(const Mx4Args &args, const void *a, cudaStream_t s) {
-    auto kern = mx4_gemm_kernel<SW>;
+    using S = Shape<SW, PAIR>;
+    auto kern = mx4_gemm_kernel<SW, PAIR>;
+    cudaLaunchConfig_t c = {};
+    c.blockDim = dim3(S::kThreads);
+    c.dynamicSmemBytes = S::kSmemBytes;
+    c.stream = s;
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = PAIR ? 2 : 1;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = at;
+
     static std::once_flag once[64];
-    static int rc[64];
+    static int rc[64], clusters[64];   // as many as run at the same time
     int dev = 0;
     MOE_CUDA_TRY(cudaGetDevice(&dev));
     if (dev < 0 || dev >= 64) return cuda_fail("device ordinal beyond 63");
     std::call_once(once[dev], [&] {
-        rc[dev] = (int)cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        rc[dev] = (int)cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
+        clusters[dev] = sm_count();
+        if (!PAIR || rc[dev]) return;
+        cudaLaunchConfig_t q = c;
+        q.gridDim = dim3((unsigned)(sm_count() / 2 * 2));
+        q.numAttrs = 1;
+        rc[dev] = (int)cudaOccupancyMaxActiveClusters(&clusters[dev], kern, &q);
+        if (!rc[dev] && clusters[dev] < 1) rc[dev] = (int)cudaErrorInvalidConfiguration;
     });
-    if (rc[dev]) return cuda_fail("cudaFuncSetAttribute", (cudaError_t)rc[dev]);
+    if (rc[dev]) return cuda_fail("setting up the MXFP4 product", (cudaError_t)rc[dev]);
     CUtensorMap tmA, tmA32;
     if (!encode_2d(&tmA, a, true, (uint64_t)args.k_dim / 2, (uint64_t)args.rows, 64) ||
         !encode_2d(&tmA32, a, true, (uint64_t)args.k_dim / 2, (uint64_t)args.rows, 32))
         return cuda_fail("cuTensorMapEncodeTiled (activations)");
     const int64_t nt = ceil_div(args.n_out, kTN);
-    const int64_t bound = nt * (args.groups + ceil_div(args.rows, kTM));
-    const int grid = (int)std::min<int64_t>((int64_t)sm_count(), bound);
-    return launch_dependent(kern, dim3(grid), dim3(kThreads), kSmemBytes, s, tmA, tmA32, args);
+    const int64_t bound = nt * (args.groups + ceil_div(args.rows, S::kTM));
+    c.gridDim = dim3((PAIR ? 2 : 1) * (unsigned)std::min<int64_t>(clusters[dev], bound));
+    c.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&c, kern, tmA, tmA32, args);
+    return e == cudaSuccess ? MOE_OK : cuda_fail("cudaLaunchKernelEx", e);
+}
+
+template <bool SW>
+int launch(const Mx4Args &args, const void *a, cudaStream_t s) {
+    return args.rows > (int64_t)128 * args.groups ? launch<SW, true>(args, a, s) : launch<SW, false>(args, a, s);
 }
 
 }  // namespace
