@@ -61,7 +61,7 @@ struct Shape {
     static constexpr int kSAOff = kBOff + 2 * kBlocks * kTileBytes, kSBOff = kSAOff + 2 * 512;
     static constexpr int kStageBytes = kSBOff + 4 * 512;
     static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
-    static constexpr int kMmaWarp = 0, kFirstSlotWarp = 1, kSlotWarps = kStages;
+    static constexpr int kMmaWarp = 0, kFirstSlotWarp = 1, kSlotWarps = kStages / 2;   // two slots each
     static constexpr int kFirstSfWarp = kFirstSlotWarp + kSlotWarps, kSfWarps = 4;
     static constexpr int kFirstEpiWarp = kFirstSfWarp + kSfWarps, kEpiWarps = SW ? 16 : 8;
     static constexpr int kThreads = (kFirstEpiWarp + kEpiWarps) * 32;
@@ -259,20 +259,19 @@ __global__ void __launch_bounds__((Shape<SW, PAIR>::kThreads), 1)
         }
         __syncwarp();
     } else if (warp < kFirstSfWarp) {
-        // ---- operands: one warp for each ring slot -----------------------------------
-        // One thread issues the slot's copies; the warp puts the token rows'
+        // ---- operands: each of these warps has two of the ring's slots -----------------
+        // One thread issues a stage's copies; the warp puts the token rows'
         // scale bytes into their place.  Addresses and scale bytes are there
         // before the slot is free: from the last product of a stage to the next
         // one's in its slot everything here is in line.  (One thread issuing
-        // every slot's copies kept the products waiting; with the addresses
-        // formed after the wait, by lane 0, a slot's copies took 1240 cycles to
+        // every stage's copies kept the products waiting; with the addresses
+        // formed after the wait, by lane 0, a stage's copies took 1240 cycles to
         // issue.)
         const uint32_t mine = warp - kFirstSlotWarp;
         uint8_t *smem = dsmem + (smem_base - smem_u32(dsmem));
-        const uint32_t base = smem_base + mine * kStageBytes, fb = smem_u32(&full_bar[mine]);
         const size_t pitch = args.k_dim / 32;
         const uint64_t pol_w = policy_evict_normal(), pol_a = policy_evict_last();
-        uint32_t used = 0, first = mine;   // stages of this slot so far; its first step in the tile
+        uint32_t it = mine, first = mine;   // the stage that is next; its step in the tile
         bool ok = true;
         for (int t = pair; t < total && ok; t += pairs) {
             if ((int)first >= steps) {     // none in this tile
@@ -293,7 +292,9 @@ __global__ void __launch_bounds__((Shape<SW, PAIR>::kThreads), 1)
             for (int q = 0; q < 4; ++q)
                 rows[q] = args.a_scales + (size_t)min(tl.row0 + lane + 32 * q, last) * pitch;
             int s = first;
-            for (; s < steps; s += kStages) {
+            for (; s < steps; s += S::kSlotWarps, it += S::kSlotWarps) {
+                const uint32_t slot = it % kStages, fb = smem_u32(&full_bar[slot]);
+                const uint32_t base = smem_base + slot * kStageBytes;
                 const int nk = min(2, KB - 2 * s);
                 const uint8_t *wa = args.w + ((rank ? w1 : w0) + 2 * s) * kTileBytes, *wb = args.w + (w1 + 2 * s) * kTileBytes;
                 const uint8_t *sa = args.w_scales + (w0 + 2 * s) * 512, *sb = args.w_scales + (w1 + 2 * s) * 512;
@@ -304,11 +305,10 @@ __global__ void __launch_bounds__((Shape<SW, PAIR>::kThreads), 1)
 #pragma unroll
                     for (int q = 0; q < 4; ++q)   // rows past the last are the last: not stored
                         v[k][q] = __ldg(reinterpret_cast<const uint32_t *>(rows[q] + (2 * s + (k < nk ? k : 0)) * 4));
-                ok = wait_bounded(smem_u32(&empty_bar[mine]), (used & 1) ^ 1u, abort_flag, args.status,
+                ok = wait_bounded(smem_u32(&empty_bar[slot]), ((it / kStages) & 1) ^ 1u, abort_flag, args.status,
                                   MOE_DEV_TIMEOUT);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                ++used;
                 if (elect_one()) {
                     mbar_expect_tx(fb, bytes);
                     if (PAIR) {   // a block's tiles along K are consecutive
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__((Shape<SW, PAIR>::kThreads), 1)
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
-                    *reinterpret_cast<uint4 *>(smem + mine * kStageBytes + kSAOff + k * 512 + lane * 16) =
+                    *reinterpret_cast<uint4 *>(smem + slot * kStageBytes + kSAOff + k * 512 + lane * 16) =
                         make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
                 __syncwarp();
                 if (elect_one()) mbar_arrive(fb);
@@ -336,7 +336,8 @@ __global__ void __launch_bounds__((Shape<SW, PAIR>::kThreads), 1)
             first = s - steps;
         }
         // copies in flight have to land before the CTA gives up its memory
-        if (!ok && used) wait_drain(fb, (used - 1) & 1);
+        for (uint32_t i = it > kStages ? it - kStages : mine; !ok && i < it; i += S::kSlotWarps)
+            wait_drain(smem_u32(&full_bar[i % kStages]), (i / kStages) & 1);
     } else if (warp < kFirstEpiWarp) {
         // ---- scales to tensor memory: each warp to its lane quarter ----------------------
         // The tensor pipe's own copies (tcgen05.cp) run in line with the
@@ -435,15 +436,17 @@ __global__ void __launch_bounds__((Shape<SW, PAIR>::kThreads), 1)
             } else if (args.c_bf16) {
                 uint32_t w[64];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    uint32_t r[16];
-                    tmem_ld16(lane_base + part * 128 + j * 16, r);
-                    tmem_wait_ld(r);
+                for (int p = 0; p < 4; ++p) {
+                    uint32_t r[2][16];
+                    tmem_ld16(lane_base + part * 128 + p * 32, r[0]);
+                    tmem_ld16(lane_base + part * 128 + p * 32 + 16, r[1]);
+                    tmem_wait_ld(r[0]);
+                    tmem_wait_ld(r[1]);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        __nv_bfloat162 b =
-                            __floats2bfloat162_rn(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-                        w[8 * j + i] = *reinterpret_cast<uint32_t *>(&b);
+                    for (int i = 0; i < 16; ++i) {
+                        __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[i / 8][2 * i % 16]),
+                                                                 __uint_as_float(r[i / 8][2 * i % 16 + 1]));
+                        w[16 * p + i] = *reinterpret_cast<uint32_t *>(&b);
                     }
                 }
                 release();
