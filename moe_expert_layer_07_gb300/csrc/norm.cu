@@ -63,6 +63,13 @@ struct Raw {
         for (int j = 0; j < (F32 ? 2 : 1); ++j)
             a[j] = static_cast<const uint4 *>(p)[(F32 ? 2 : 1) * i + j];
     }
+    // What a row is read once for, past L1 (16384 bf16 rows of 7168: 151 -> 146
+    // us with its stores; layer norm 207 -> 190).  Not fp32, whose two pieces
+    // share a sector (261 -> 270).
+    __device__ __forceinline__ void load_once(const void *p, size_t i) {
+        if (F32) load(p, i);
+        else a[0] = ptx::load_past_l1(static_cast<const uint4 *>(p) + i);
+    }
     __device__ __forceinline__ void get(F2 (&v)[4]) const {
         if (F32) {
 #pragma unroll
@@ -104,7 +111,7 @@ __device__ __forceinline__ void store8(void *p, size_t i, const F2 (&v)[4]) {
             __nv_bfloat162 b = __floats2bfloat162_rn(lo2(v[j]), hi2(v[j]));
             w[j] = *reinterpret_cast<uint32_t *>(&b);
         }
-        static_cast<uint4 *>(p)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        ptx::store_past_l1(static_cast<uint4 *>(p) + i, make_uint4(w[0], w[1], w[2], w[3]));
     }
 }
 
@@ -187,8 +194,8 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : VPT == 2 ? 512 : 256, VPT ==
     for (int i = 0; i < VPT; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
         if (c < n8) {
-            if (a.y) y[i].load(a.y, base + c);
-            r[i].load(a.r, base + c);
+            if (a.y) y[i].load_once(a.y, base + c);
+            r[i].load_once(a.r, base + c);
         }
     }
     float2 st = make_float2(0.0f, 1.0f);

@@ -161,6 +161,20 @@ __device__ __forceinline__ bool wait_flag_geq(const int32_t *flag, int target,
     }
 }
 
+// ---- 16 bytes that pass by L1 ---------------------------------------------------
+__device__ __forceinline__ uint4 load_past_l1(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+__device__ __forceinline__ void store_past_l1(uint4 *p, const uint4 v) {
+    asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
+}
+
 // ---- cp.async (4-byte global -> shared) ------------------------------------
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst),
