@@ -196,6 +196,9 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : VPT == 2 ? 512 : 256, VPT ==
         if (c < n8) {
             if (a.y) y[i].load_once(a.y, base + c);
             r[i].load_once(a.r, base + c);
+            // wanted after the first reduction (16384 bf16 rows of 7168: 220 -> 184 us)
+            if (a.gate_mode == MOE_GATE_FULL)
+                ptx::prefetch_l2_line(static_cast<const uint4 *>(a.gate) + (base + c) * (a.p_f32 ? 2 : 1));
         }
     }
     float2 st = make_float2(0.0f, 1.0f);

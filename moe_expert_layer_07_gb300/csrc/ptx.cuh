@@ -169,6 +169,9 @@ __device__ __forceinline__ uint4 load_past_l1(const uint4 *p) {
                  : "l"(p));
     return v;
 }
+__device__ __forceinline__ void prefetch_l2_line(const void *p) {   // a hint
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 __device__ __forceinline__ void store_past_l1(uint4 *p, const uint4 v) {
     asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z),
                  "r"(v.w)
