@@ -6,23 +6,32 @@
 // MXFP4 quantisation of h (gate block and up block of the same 128 features
 // in one tile).
 //
-// One persistent CTA per SM takes tiles of 128 token rows (M) x 256 weight
-// rows (N, two blocks of 128).  A stage of the ring holds 256 of K: the token
-// rows' codes (TMA boxes of 128 bytes a row, 128-byte swizzle), four weight
-// tiles (8 KB bulk copies, stored pre-swizzled), the weights' scale bytes
-// (stored in the order tensor memory wants), and the token rows' scale bytes,
-// which come row-major from global memory and are put in that order: a warp's
-// lane L holds rows L, L+32, L+64, L+96, whose four words of four scales are
-// one 16-byte chunk, to be repeated in the four lane quarters.
+// Persistent CTAs, one to an SM, take tiles of 256 weight rows (N, two blocks
+// of 128) and 128 token rows (M), or, in pairs of CTAs (tcgen05 cta_group::2,
+// clusters of two), 256 token rows: each CTA of a pair loads its own 128 token
+// rows and one of the two weight blocks, and the products read both CTAs'
+// shared memory, which takes a third off what an SM has to load for a product.
+// A stage of the ring holds 256 of K: the token rows' codes (TMA boxes of 128
+// bytes a row, 128-byte swizzle), the weight tiles (bulk copies, stored
+// pre-swizzled), the weights' scale bytes (stored in the order tensor memory
+// wants), and the token rows' scale bytes, which come row-major from global
+// memory and are put in that order: a warp's lane L holds rows L, L+32, L+64,
+// L+96, whose four words of four scales are one 16-byte chunk, to be repeated
+// in the four lane quarters.
 //
-// What bounds it: weights read once for few rows (decode: 254 MB of down
-// products in 43 us, 87% of the copy rate), the tensor pipe for many: 8192 x
-// 7168 x 7168 takes 176 us, 4.8 PFLOP/s, about 500 of a stage's 1000 cycles in
-// products (with neither products nor scales it takes 148).  On the way there,
-// same product: 267 us -> 253 waits that let the hardware hold the thread; ->
-// 234 one copy for both K blocks' scale bytes; -> 199 a warp for each ring
-// slot to issue its copies; -> 176 scales stored to tensor memory by warps
-// instead of tcgen05.cp.
+// What bounds it: weights read once for few rows (254 MB of down products for
+// 273 rows in 39 us, 95% of the copy rate); for many, products and the way from
+// one tile to the next, since the accumulator and the scales leave no room in
+// tensor memory for a second accumulator: 8192 x 7168 x 7168 takes 116 us, 7.3
+// PFLOP/s, of which about 640 cycles a stage in products and 2000 a tile where
+// they wait for the epilogue to read it.
+// On the way there, same product: 267 us -> 253 waits that let the hardware
+// hold the thread; -> 234 one copy for both K blocks' scale bytes; -> 199 a
+// warp for each ring slot to issue its copies; -> 176 scales stored to tensor
+// memory by warps instead of tcgen05.cp; -> 164 one elected thread issues, with
+// addresses formed before the slot is free; -> 127 pairs; -> 124 two slots to
+// an operand warp (more registers for the epilogue); -> 121 stores past L1; ->
+// 116 weights that are read again stay in L2.
 //
 // The hardware applies the scales, so nothing is promoted on the way and an
 // accumulator runs over all of K; the epilogue sees each output once.
@@ -540,6 +549,10 @@ int launch(const Mx4Args &args, const void *a, cudaStream_t s) {
     return e == cudaSuccess ? MOE_OK : cuda_fail("cudaLaunchKernelEx", e);
 }
 
+// Pairs where a group has more than one CTA's 128 rows on average: the second
+// CTA's products are wasted on a smaller one.  (CTAs alone / pairs: 273 rows in
+// 33 groups 42 / 52 us, 264 with SwiGLU 82 / 88; 4599 in 33 with SwiGLU 98 / 99;
+// 16411 in 8 groups 124 / 113, 8192 with SwiGLU in 4 95 / 84.)
 template <bool SW>
 int launch(const Mx4Args &args, const void *a, cudaStream_t s) {
     return args.rows > (int64_t)128 * args.groups ? launch<SW, true>(args, a, s) : launch<SW, false>(args, a, s);

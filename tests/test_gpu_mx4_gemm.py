@@ -176,3 +176,38 @@ def test_repeatable(lib):
     for o in c:
         moe.mx4_grouped_gemm(5, 512, 1024, 461, a, a_s, off, wt, wt_s, o, moe.OUT_F32)
     assert torch.equal(*c)
+
+
+# Groups of more than 128 rows on average run on pairs of CTAs, 256 rows to a tile: one row past a
+# CTA's, exactly full tiles, a tile with nothing for the second CTA, an odd number of weight blocks
+# (the second CTA has none) and of K blocks, more tiles than pairs.
+PAIRS = [([129], 128, 128), ([256], 256, 256), ([257, 256, 255, 0], 384, 384), ([700, 1, 0, 300], 640, 1408),
+         ([1300, 20], 1024, 2304), ([6000], 896, 640)]
+
+
+@pytest.mark.parametrize("counts,N,K", PAIRS)
+def test_product_on_pairs(lib, counts, N, K):
+    test_product(lib, counts, N, K)
+
+
+@pytest.mark.parametrize("counts,I,K", [([129], 128, 128), ([257, 256, 255, 0], 384, 384),
+                                        ([700, 1, 0, 300], 640, 1408), ([3000, 130], 1024, 2304)])
+def test_swiglu_on_pairs(lib, counts, I, K):
+    test_swiglu(lib, counts, I, K)
+
+
+def test_each_scale_meets_its_block_on_pairs(lib):
+    """As above with rows, and weight rows, in both CTAs."""
+    K, N, rows = 768, 384, 300
+    one = torch.full((rows, K // 2), 0x22, dtype=torch.uint8, device="cuda")
+    wone = torch.full((1, N, K // 2), 0x22, dtype=torch.uint8, device="cuda")
+    r = torch.arange(rows, device="cuda")[:, None]
+    b = torch.arange(K // 32, device="cuda")[None, :]
+    n = torch.arange(N, device="cuda")[:, None]
+    a_s = (127 + (r * 7 + b * 3) % 5).to(torch.uint8)
+    w_s = (127 - (n * 3 + b * 5) % 7).to(torch.uint8)[None]
+    wt, wt_s = moe.pack_mx4_weights(wone, w_s.contiguous())
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    c = torch.empty(rows, N, device="cuda")
+    moe.mx4_grouped_gemm(1, N, K, rows, one, a_s.contiguous(), off, wt, wt_s, c, moe.OUT_F32)
+    assert torch.equal(c.double(), _values(one, a_s) @ _values(wone[0], w_s[0]).t())
