@@ -344,8 +344,9 @@ __device__ __forceinline__ void cluster_sync() {
 }
 // The address of CTA `rank`'s counterpart of a shared-memory variable, and an
 // arrival on such a barrier.  Waits and arrivals keep their default scope: what
-// they order here are tensor-memory accesses that tcgen05.wait has completed,
-// and a release at cluster scope took 1200 cycles.
+// they order here has completed before: tensor-memory accesses that
+// tcgen05.wait waited for, and copies that have arrived on their own barrier.
+// A release at cluster scope took 1200 cycles.
 __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
