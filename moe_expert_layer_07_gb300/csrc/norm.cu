@@ -269,7 +269,8 @@ int launch_typed(const NormArgs &a, cudaStream_t s) {
     // SM at once to cover one another's reductions, and few threads to reduce
     // over (16384 rows of 7168 bf16: 317 / 190 / 152 us with 1 / 2 / 4 chunks;
     // fp32 rows, whose chunks take twice the registers: 371 / 263 / 326; of
-    // 1024 bf16: 30 / 26 / 28; 65536 rows of 256: 28 / 32 / 36).
+    // 1024 bf16: 30 / 26 / 28; 65536 rows of 256: 28 / 32 / 36; all while bf16
+    // rows went through L1, past it the first is 147 with 4).
     if (n8 > 1024) return launch_rows<8, Y32, R32>(a, s);
     if (a.T <= 2 * sm_count() || n8 <= 64) return launch_rows<1, Y32, R32>(a, s);
     if (n8 <= 512 || Y32 || R32) return launch_rows<2, Y32, R32>(a, s);
