@@ -104,7 +104,8 @@ typedef struct moe_weights {
     const void *w_gate;       /* bf16 [E, H], LOGICAL expert order */
     const float *e_bias;      /* fp32 [E] logical, selection-only bias (sigmoid); NULL = none */
     const float *logit_offset;/* fp32 [E] logical, added to the gate logits; NULL = none */
-    const int32_t *log2phys;  /* int32 [E]: physical slot of each logical expert; NULL = identity */
+    const int32_t *log2phys;  /* int32 [E]: physical slot of each logical expert (two may share
+                                 one); NULL = identity */
     const void *w13;          /* [G, 2I, H]: rows [0, I) gate proj, [I, 2I) up proj; e4m3 or bf16 */
     const float *w13_scales;  /* fp32 [G, 2I/128, H/128], one per 128x128 block (FP8 only) */
     const void *w2;           /* [G, H, I] down proj; e4m3 or bf16 */

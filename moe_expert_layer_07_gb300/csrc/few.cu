@@ -65,7 +65,7 @@ constexpr int kMaxT = kFewMaxTokens;
 constexpr int kMaxShared = 4;
 constexpr int kMaxSlots = kMaxT * 16;                   // routed slots
 constexpr int kMaxRows = kMaxSlots + kMaxT * kMaxShared;
-constexpr int kMaxGroups = kMaxSlots + kMaxShared;      // groups with rows
+constexpr int kMaxGroups = kMaxSlots + kMaxShared;      // groups with rows, each at most 8 NT
 
 enum { DT_BF16 = MOE_DTYPE_BF16, DT_FP8 = MOE_DTYPE_FP8_BLOCK128, DT_MX4 = MOE_DTYPE_MXFP4 };
 
@@ -713,7 +713,9 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
 
     // ---- groups with rows: shared experts, then the chosen ones by id ----------
     // rows: shared expert s of token t at s T + t, then each chosen expert's
-    // tokens in order
+    // tokens in order.  A group takes 8 NT of them: a table log2phys with an
+    // entry twice can give an expert more rows than there are tokens, which
+    // are then further groups of the same weights.
     for (int i = threadIdx.x; i < slots; i += kFfnThreads) {
         const int id = sh.ids[i];
         int before = 0, rank = 0;   // slots of lower experts; of this one in earlier slots
@@ -725,7 +727,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         const int row = id >= 0 ? a.S * a.T + before + rank : -1;
         if (id >= 0) sh.row_tok[row] = i / a.k;
         sh.slot_row[i] = row;
-        sh.first_id[i] = id >= 0 && rank == 0 ? id : INT16_MAX;
+        sh.first_id[i] = id >= 0 && rank % (8 * NT) == 0 ? id : INT16_MAX;   // opens a group
         if (blockIdx.x == 0) {
             a.ids[i] = id;
             a.wts[i] = id >= 0 ? sh.wts[i] : 0.0f;
@@ -735,14 +737,14 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     for (int i = threadIdx.x; i < slots; i += kFfnThreads) {
         const int id = sh.first_id[i];
         if (id == INT16_MAX) continue;
-        int place = a.S, n = 0;   // distinct chosen experts below; this one's rows
+        int place = a.S, n = 0;   // groups of lower experts, or before in this one; rows from here on
         for (int j = 0; j < slots; ++j) {
-            place += sh.first_id[j] < id;
-            n += sh.ids[j] == id;
+            place += sh.first_id[j] < id || (sh.first_id[j] == id && j < i);
+            n += sh.ids[j] == id && j >= i;
         }
         sh.group_id[place] = id;
         sh.group_row[place] = sh.slot_row[i];
-        sh.group_n[place] = n;
+        sh.group_n[place] = min(n, 8 * NT);
         atomicAdd(&sh.n_groups, 1);
     }
     for (int i = threadIdx.x; i < a.S * a.T; i += kFfnThreads) sh.row_tok[i] = i % a.T;

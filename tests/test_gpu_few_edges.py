@@ -1,0 +1,62 @@
+"""The few-token layer where its tables and numbers are unusual."""
+from __future__ import annotations
+
+import dataclasses
+
+import pytest
+import torch
+
+import moe_expert_layer_07_gb300 as moe
+import synth
+
+from _gpu_common import build_library
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = ["bf16", "fp8", "mxfp4"]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    return build_library()
+
+
+def _inputs(shape, seed=0):
+    four = shape.dtype == "mxfp4"
+    w = synth.make_inputs(dataclasses.replace(shape, dtype="bf16") if four else shape, seed=seed,
+                          device="cuda")
+    if four:
+        for key in ("w13", "w2"):
+            w[key], w[key + "_s"] = moe.mx4_quantize(w[key])
+    return w
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,E,k,table", [
+    (1, 8, 3, [5] * 8),                       # one token's choices all on one slot
+    (3, 8, 2, [0, 0, 1, 1, 2, 2, 3, 3]),      # pairs of experts on a slot
+    (8, 8, 2, [7] * 8),                       # 16 rows of one expert, 8 to a group
+    (9, 16, 4, [2] * 12 + [15, 14, 13, 13]),
+    (16, 16, 16, [3] * 16),                   # as many rows of one expert as there can be
+    (16, 16, 16, [1, 0] * 8)])
+def test_experts_that_share_a_slot(lib, dtype, T, E, k, table):
+    """log2phys may name a slot more than once: the same bits as with the slots' weights written out
+    for each logical expert, since a row's products do not depend on the rows beside it."""
+    s = synth.MoEShape("shared slots", tokens=T, hidden=384, inter=256, num_experts=E, num_shared=1,
+                       top_k=k, dtype=dtype)
+    w = _inputs(s, T + k)
+    few = moe.FewTokenLayer(s, w, log2phys=table)
+    few.ws[4:].fill_(0xFF)
+    got = torch.full((T, 384), float("nan"), device="cuda")
+    few.forward(w["x"], got)
+    assert few.status() == 0
+    at = torch.tensor(table + [E], device="cuda")
+    spread = dict(w, **{key: w[key][at].contiguous() for key in ("w13", "w13_s", "w2", "w2_s")
+                        if w[key] is not None})
+    ref = torch.empty_like(got)
+    moe.FewTokenLayer(s, spread).forward(w["x"], ref)
+    assert torch.equal(got, ref)
+    ids = few.view("topk_ids", torch.int32, (T, k))
+    assert bool((ids[..., None] == at[:E].int()).any(-1).all())
