@@ -199,6 +199,12 @@ def make_config(shape, max_tokens: int | None = None) -> Config:
                   routed_scaling=float(shape.routed_scaling))
 
 
+def _bf16_or_fp8(shape):
+    """Refuses a shape whose experts are in a type that MoELayer's kernels do not take."""
+    if shape.dtype == "mxfp4":
+        raise ValueError("experts in MXFP4 belong to FewTokenLayer and Mx4MoELayer")
+
+
 def route(cfg: Config, T, x, w_gate, e_bias, logit_offset, log2phys, logits, topk_ids, topk_w,
           status=None, stream=None):
     _check(lib().moe_route(ctypes.byref(cfg), T, _ptr(x), _ptr(w_gate), _ptr(e_bias),
@@ -292,6 +298,10 @@ def pack_expert_weights(cfg: Config, w, out=None, stream=None):
     import torch
     out = torch.empty_like(w) if out is None else out
     G, N, K = w.shape
+    size = 1 if cfg.dtype == FP8 else 2
+    if w.element_size() != size or out.element_size() != size or out.numel() != w.numel():
+        raise TypeError(f"expected elements of {size} bytes in tensors of one size, got "
+                        f"{w.dtype} {tuple(w.shape)} and {out.dtype} {tuple(out.shape)}")
     _check(lib().moe_pack_expert_weights(ctypes.byref(cfg), G, N, K, _ptr(w), _ptr(out),
                                          _stream(stream)), "moe_pack_expert_weights")
     return out
@@ -462,6 +472,7 @@ class MoELayer:
     def __init__(self, shape, weights: dict, max_tokens: int | None = None, log2phys=None,
                  pack_weights: bool = True):
         import torch
+        _bf16_or_fp8(shape)
         self.cfg = make_config(shape, max_tokens)
         self.shape = shape
         weights = dict(weights)

@@ -158,7 +158,8 @@ class GpuRank:
     def __init__(self, shape, weights: dict, plan: EPPlan, log2phys=None, pack_weights=True,
                  stream=None):
         import torch
-        from . import (LAYOUT_ROWS, LAYOUT_TILES, make_config, pack_expert_weights)
+        from . import (LAYOUT_ROWS, LAYOUT_TILES, _bf16_or_fp8, make_config, pack_expert_weights)
+        _bf16_or_fp8(shape)
         self.shape, self.plan, self.stream = shape, plan, stream
         self.fp8 = shape.dtype == "fp8"
         self.cfg = make_config(shape)
