@@ -3,7 +3,8 @@ norms before and after a block (declared in include/moe_gb300.h).
 
 Argument marshalling only, as in the package's __init__: shapes and types are
 read off the tensors and checked against each other here, everything else by
-the library.
+the library.  Where a call also takes addresses, as the package's calls do, an
+integer is passed on unchecked.
 """
 from __future__ import annotations
 
@@ -71,6 +72,29 @@ def _bytes(t, shape, name):
     return _dense(t, shape, name)
 
 
+def _holds(t, dtype, rows, cols) -> bool:
+    """Whether t has `rows` rows of `cols` elements at least (cols None: `rows` elements in any
+    shape); None and addresses are the library's matter."""
+    if t is None or isinstance(t, int):
+        return True
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        return False
+    if cols is None:
+        return t.numel() >= rows
+    return t.dim() > 0 and t.shape[-1] == cols and t.numel() >= rows * cols
+
+
+def _check_rows(*wanted):
+    """Raises for the first of (name, tensor, type, rows, columns) that does not hold."""
+    for name, t, dtype, rows, cols in wanted:
+        if not _holds(t, dtype, rows, cols):
+            if t.dtype is not dtype:
+                raise TypeError(f"{name}: expected a {dtype} tensor, got {t.dtype}")
+            size = f"{rows} elements" if cols is None else f"{rows} rows of {cols}"
+            raise ValueError(f"{name}: expected a contiguous CUDA tensor of {size} at least, "
+                             f"got {tuple(t.shape)} on {t.device}")
+
+
 # ---- MXFP4 ------------------------------------------------------------------------------
 
 
@@ -133,9 +157,31 @@ def pack_mx4_weights(codes, scales, stream=None):
     return w, ws
 
 
+_C_TYPES = {kind: dtype for dtype, kind in _OUT.items()}
+
+
+def _check_product(groups, n_out, k_dim, rows, a, a_scales, offsets, w, w_scales, status, *outs):
+    """Checks a grouped product's tensors against its sizes."""
+    if rows <= 0:
+        return
+    u8, i32 = torch.uint8, torch.int32
+    _check_rows(("a", a, u8, rows, k_dim // 2), ("a_scales", a_scales, u8, rows, k_dim // 32),
+                ("w", w, u8, groups * n_out, k_dim // 2),
+                ("w_scales", w_scales, u8, groups * n_out, k_dim // 32),
+                ("expert_offsets", offsets, i32, groups + 1, None), ("status", status, i32, 1, None),
+                *outs)
+    for name, t in (("w", w), ("w_scales", w_scales)):
+        if isinstance(t, torch.Tensor) and t.shape[-2:-1] != (n_out,):
+            raise ValueError(f"{name}: expected {n_out} rows a group, got {tuple(t.shape)}")
+
+
 def mx4_grouped_gemm(groups, n_out, k_dim, rows, a, a_scales, expert_offsets, w, w_scales, c,
                      c_dtype, status=None, stream=None):
-    """C[r] = A[r] W[g]^T for the rows of each group; w, w_scales from pack_mx4_weights."""
+    """C[r] = A[r] W[g]^T for the rows of each group; w, w_scales from pack_mx4_weights.
+    a, a_scales and c may have more than `rows` rows; c is of c_dtype."""
+    c_type = _C_TYPES.get(c_dtype) or getattr(c, "dtype", None)   # the library refuses other kinds
+    _check_product(groups, n_out, k_dim, rows, a, a_scales, expert_offsets, w, w_scales,
+                   status, ("c", c, c_type, rows, n_out))
     _check(lib().moe_mx4_grouped_gemm(groups, n_out, k_dim, rows, _ptr(a), _ptr(a_scales),
                                       _ptr(expert_offsets), _ptr(w), _ptr(w_scales), _ptr(c),
                                       c_dtype, _ptr(status), _stream(stream)),
@@ -145,6 +191,9 @@ def mx4_grouped_gemm(groups, n_out, k_dim, rows, a, a_scales, expert_offsets, w,
 def mx4_grouped_gemm_swiglu(groups, inter, k_dim, rows, a, a_scales, expert_offsets, w13,
                             w13_scales, h, h_scales, status=None, stream=None):
     """The gate/up product with SwiGLU, h in MXFP4 (codes [rows, inter/2], scales [rows, inter/32])."""
+    _check_product(groups, 2 * inter, k_dim, rows, a, a_scales, expert_offsets, w13, w13_scales,
+                   status, ("h", h, torch.uint8, rows, inter // 2),
+                   ("h_scales", h_scales, torch.uint8, rows, inter // 32))
     _check(lib().moe_mx4_grouped_gemm_swiglu(groups, inter, k_dim, rows, _ptr(a), _ptr(a_scales),
                                              _ptr(expert_offsets), _ptr(w13), _ptr(w13_scales),
                                              _ptr(h), _ptr(h_scales), _ptr(status),
