@@ -225,6 +225,26 @@ def layer_few(cfg: Config, weights: Weights, T, x, out, out_dtype, ws, ws_bytes,
                                out_dtype, _ptr(ws), ws_bytes, _stream(stream)), "moe_layer_few")
 
 
+def _layer_io(x, out, out_dtype, T, hidden):
+    """MOE_OUT_* of out, once x is bf16 [T, hidden] and out as large."""
+    if isinstance(x, int) or isinstance(out, int):   # addresses
+        return OUT_F32 if out_dtype is None else out_dtype
+    kind = _OUT.get(out.dtype)
+    # one test of all that holds in a correct call; what failed is looked up after
+    if not (kind is not None and x.dtype is torch.bfloat16 and x.is_cuda and out.is_cuda
+            and x.is_contiguous() and out.is_contiguous() and x.dim() == out.dim() == 2
+            and x.shape[1] == out.shape[1] == hidden and x.shape[0] >= T and out.shape[0] >= T):
+        kind = _out_type(out)
+        if x.dim() != 2 or out.dim() != 2:
+            raise ValueError(f"x and out: expected [{T}, {hidden}], got {tuple(x.shape)} and {tuple(out.shape)}")
+        _check_rows(("x", x, torch.bfloat16, T, hidden), ("out", out, out.dtype, T, hidden))
+    if out_dtype is None or out_dtype == kind:
+        return kind
+    if out_dtype in _C_TYPES:
+        raise TypeError(f"out is {out.dtype}, and out_dtype asks for {_C_TYPES[out_dtype]}")
+    return out_dtype   # refused by the library
+
+
 class FewTokenLayer:
     """The MoE layer for 1 to 16 tokens a call, in two kernels.
 
@@ -273,9 +293,11 @@ class FewTokenLayer:
     def weights(self) -> Weights:
         return self._layer.weights if self._layer is not None else self._weights
 
-    def forward(self, x, out, out_dtype=OUT_F32, T=None, stream=None):
-        """x bf16 [T, H] and out [T, H] (fp32 or bf16) device tensors."""
+    def forward(self, x, out, out_dtype=None, T=None, stream=None):
+        """x bf16 [T, H] and out [T, H] (fp32 or bf16) device tensors; out_dtype (OUT_*) may be
+        left to out's type."""
         T = x.shape[0] if T is None else T
+        out_dtype = _layer_io(x, out, out_dtype, T, self.cfg.hidden)
         layer_few(self.cfg, self.weights, T, x, out, out_dtype, self.ws, self.ws_bytes, stream)
         return out
 
@@ -414,14 +436,16 @@ class Mx4MoELayer:
         self.h, self.hs = buf(R, I // 2), buf(R, I // 32)
         self.y = buf(R, H, dtype=f32)
 
-    def forward(self, x, out, out_dtype=OUT_F32, stream=None):
-        """x bf16 [T, H] and out [T, H] (fp32 or bf16) device tensors."""
+    def forward(self, x, out, out_dtype=None, stream=None):
+        """x bf16 [T, H] and out [T, H] (fp32 or bf16) device tensors; out_dtype (OUT_*) may be
+        left to out's type."""
         from . import combine, permute, route
         T, s, k = x.shape[0], self.shape, self._keep
         if T <= self.few.cfg.max_tokens:
             return self.few.forward(x, out, out_dtype, stream=stream)
         if T > self.cfg.max_tokens:
             raise ValueError(f"{T} tokens, and buffers for {self.cfg.max_tokens}")
+        out_dtype = _layer_io(x, out, out_dtype, T, s.hidden)
         rows = T * (s.top_k + s.num_shared)
         st = self.status_word
         route(self.cfg, T, x, k["wg"], k["e_bias"], k["logit_offset"], k["log2phys"], self.logits,

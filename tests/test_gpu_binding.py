@@ -2,10 +2,13 @@
 its bounds, or as another type."""
 from __future__ import annotations
 
+import dataclasses
+
 import pytest
 import torch
 
 import moe_expert_layer_07_gb300 as moe
+import synth
 
 from _gpu_common import build_library
 
@@ -71,3 +74,37 @@ def test_swiglu_tensors(lib):
                       ("h_scales", good["h_scales"][:-1]), ("w13", good["w13"][:, :I].contiguous())):
         with pytest.raises((TypeError, ValueError)):
             call(**{name: bad})
+
+
+def _layer(dtype="bf16", T=20, few=True):
+    shape = synth.MoEShape("io", tokens=T, hidden=256, inter=128, num_experts=4, num_shared=1, top_k=2,
+                           dtype="bf16")
+    w = synth.make_inputs(shape, device="cuda")
+    if dtype == "mxfp4":
+        for key in ("w13", "w2"):
+            w[key], w[key + "_s"] = moe.mx4_quantize(w[key])
+        shape = dataclasses.replace(shape, dtype=dtype)
+    return (moe.FewTokenLayer(shape, w) if few else moe.Mx4MoELayer(shape, w, T)), w["x"]
+
+
+@pytest.mark.parametrize("kind,T", [("few", 3), ("mxfp4", 3), ("mxfp4", 20)])
+def test_layer_input_and_output(lib, kind, T):
+    layer, x = _layer("mxfp4" if kind == "mxfp4" else "bf16", few=kind == "few")
+    x = x[:T].contiguous()
+    f32, bf = _empty(T, 256, dtype=torch.float32), _empty(T, 256, dtype=torch.bfloat16)
+    assert layer.forward(x, f32) is f32 and layer.forward(x, bf) is bf      # out's own type
+    assert torch.equal(f32.bfloat16(), bf)
+    layer.forward(x, bf, moe.OUT_BF16)
+    guarded = torch.full((T + 2, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    layer.forward(x, guarded[1:-1])
+    assert torch.equal(guarded[1:-1], bf) and bool((guarded[0] == 7).all() & (guarded[-1] == 7).all())
+    for bad in (dict(x=x.float()), dict(x=x.half()), dict(x=x[:, :128].contiguous()), dict(x=x.cpu()),
+                dict(x=torch.cat([x, x], 1)[:, ::2]), dict(out=f32[:-1]), dict(out=f32.half()),
+                dict(out=f32[:, :128].contiguous()), dict(out=_empty(T, 512, dtype=torch.float32)[:, :256]),
+                dict(out=bf, out_dtype=moe.OUT_F32), dict(out=f32, out_dtype=moe.OUT_BF16),
+                dict(x=x.reshape(-1)), dict(out=f32.cpu())):
+        with pytest.raises((TypeError, ValueError)):
+            layer.forward(**{"x": x, "out": f32, **bad})
+    if kind == "few":
+        with pytest.raises(ValueError):
+            layer.forward(x, f32, T=T + 1)
