@@ -250,9 +250,9 @@ class FewTokenLayer:
 
     weights as MoELayer's; for a shape whose dtype is "mxfp4", w13 / w13_s and
     w2 / w2_s are MXFP4 codes and scale bytes as mx4_quantize gives them.
-    Row-major expert weights are packed into tiles once.  An MoELayer may be
-    passed in their place: its (packed) weights are then shared, also after it
-    gets new ones (rebalancing).
+    Row-major expert weights are packed into tiles once.  An MoELayer of the
+    same sizes and type may be passed in their place: its (packed) weights and
+    its log2phys are then shared, also after it gets new ones (rebalancing).
     """
 
     def __init__(self, shape, weights, max_tokens: int | None = None, log2phys=None):
@@ -265,6 +265,11 @@ class FewTokenLayer:
         if self._layer is not None:
             if self._layer.expert_layout != LAYOUT_TILES:
                 raise ValueError("the layer's expert weights are not packed into tiles")
+            if log2phys is not None:
+                raise ValueError("log2phys is the layer's own")
+            for name in ("hidden", "inter", "num_experts", "num_shared", "dtype"):
+                if getattr(self.cfg, name) != getattr(self._layer.cfg, name):
+                    raise ValueError(f"the shape's {name} is not the layer's")
             device = self._layer.ws.device
         else:
             keep = {k: weights.get(k) for k in ("wg", "e_bias", "logit_offset", "w13", "w13_s",

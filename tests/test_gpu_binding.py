@@ -108,3 +108,16 @@ def test_layer_input_and_output(lib, kind, T):
     if kind == "few":
         with pytest.raises(ValueError):
             layer.forward(x, f32, T=T + 1)
+
+
+def test_a_layer_of_other_sizes_or_another_table(lib):
+    shape = synth.MoEShape("w", tokens=4, hidden=256, inter=256, num_experts=4, num_shared=1, top_k=2,
+                           dtype="fp8")
+    big = moe.MoELayer(shape, synth.make_inputs(shape, device="cuda"), log2phys=[1, 0, 3, 2])
+    moe.FewTokenLayer(shape, big)
+    with pytest.raises(ValueError):
+        moe.FewTokenLayer(shape, big, log2phys=[0, 1, 2, 3])
+    for change in (dict(hidden=512), dict(inter=128), dict(num_experts=8), dict(num_shared=0),
+                   dict(dtype="bf16"), dict(dtype="mxfp4")):
+        with pytest.raises(ValueError):
+            moe.FewTokenLayer(dataclasses.replace(shape, **change), big)
