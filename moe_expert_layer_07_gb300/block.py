@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from . import (LAYOUT_ROWS, LAYOUT_TILES, MXFP4, OUT_BF16, OUT_F32, Config, Weights,
+from . import (BF16, LAYOUT_ROWS, LAYOUT_TILES, MXFP4, OUT_BF16, OUT_F32, Config, Weights,
                _check, _CP, _I, _P, _ptr, _stream, get_device_status, lib, make_config,
                pack_expert_weights)
 
@@ -274,6 +274,7 @@ class FewTokenLayer:
         else:
             keep = {k: weights.get(k) for k in ("wg", "e_bias", "logit_offset", "w13", "w13_s",
                                                 "w2", "w2_s", "expert_layout")}
+            self._check_weights(keep)
             if keep["expert_layout"] in (None, LAYOUT_ROWS):
                 for key in ("w13", "w2"):
                     if self.cfg.dtype == MXFP4:
@@ -282,7 +283,9 @@ class FewTokenLayer:
                         keep[key] = pack_expert_weights(self.cfg, keep[key])
             device = keep["w13"].device
             keep["log2phys"] = None if log2phys is None else torch.as_tensor(
-                log2phys, dtype=torch.int32, device=device)
+                log2phys, dtype=torch.int32, device=device).contiguous()
+            if log2phys is not None and keep["log2phys"].numel() != self.cfg.num_experts:
+                raise ValueError("log2phys: expected one entry for each expert")
             self._keep = keep
             self._weights = Weights(
                 w_gate=_ptr(keep["wg"]), e_bias=_ptr(keep["e_bias"]),
@@ -293,6 +296,30 @@ class FewTokenLayer:
         self.ws_bytes = self.layout.total
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
         self.ws[:4].zero_()   # status() before the first call
+
+    def _check_weights(self, weights):
+        """Raises for a weight tensor that is missing, or of another size than the shape says."""
+        c, G = self.cfg, self.cfg.num_experts + self.cfg.num_shared
+        want = {"wg": (2, (c.num_experts, c.hidden)), "e_bias": (4, (c.num_experts,)),
+                "logit_offset": (4, (c.num_experts,))}
+        for key, n, k in (("w13", 2 * c.inter, c.hidden), ("w2", c.hidden, c.inter)):
+            if c.dtype == MXFP4:
+                want[key], want[key + "_s"] = (1, (G, n, k // 2)), (1, (G, n, k // 32))
+            elif c.dtype == BF16:
+                want[key] = (2, (G, n, k))
+            else:
+                want[key], want[key + "_s"] = (1, (G, n, k)), (4, (G, n // 128, k // 128))
+        for key, (size, shape) in want.items():
+            t = weights[key]
+            if t is None and key in ("e_bias", "logit_offset"):
+                continue
+            if t is None:
+                raise ValueError(f"{key} is missing")
+            if t.element_size() != size:
+                raise TypeError(f"{key}: expected elements of {size} bytes, got {t.dtype}")
+            if t.shape != shape or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{key}: expected a contiguous CUDA tensor {shape}, got "
+                                 f"{tuple(t.shape)} on {t.device}")
 
     @property
     def weights(self) -> Weights:

@@ -42,3 +42,11 @@ def test_packing_refuses_elements_of_another_size():
                 moe.pack_expert_weights(cfg, bad)
         with pytest.raises(TypeError):
             moe.pack_expert_weights(cfg, good, out=good[:1])
+
+
+def test_few_token_layer_refuses_weights_of_another_size():
+    four = dataclasses.replace(MX4, dtype="bf16")
+    for shape, w in ((four, _codes(MX4)), (dataclasses.replace(MX4, dtype="fp8"), _codes(MX4)),
+                     (MX4, dict(_codes(MX4), w2=None))):
+        with pytest.raises((TypeError, ValueError)):
+            moe.FewTokenLayer(shape, w)

@@ -110,6 +110,28 @@ def test_layer_input_and_output(lib, kind, T):
             layer.forward(x, f32, T=T + 1)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "mxfp4"])
+def test_weights_of_the_few_token_layer(lib, dtype):
+    shape = synth.MoEShape("w", tokens=4, hidden=256, inter=128, num_experts=4, num_shared=1, top_k=2,
+                           dtype="bf16" if dtype == "mxfp4" else dtype, scoring="sigmoid", bias_std=0.1)
+    w = synth.make_inputs(shape, device="cuda")
+    if dtype == "mxfp4":
+        for key in ("w13", "w2"):
+            w[key], w[key + "_s"] = moe.mx4_quantize(w[key])
+    shape = dataclasses.replace(shape, dtype=dtype)
+    w["logit_offset"] = _empty(4, dtype=torch.float32)
+    moe.FewTokenLayer(shape, w, log2phys=[3, 2, 1, 0])
+    for key, t in w.items():
+        if key == "x" or t is None:
+            continue
+        for bad in (t[:-1], t.double(), t.cpu()):
+            with pytest.raises((TypeError, ValueError)):
+                moe.FewTokenLayer(shape, dict(w, **{key: bad}))
+    for table in ([0, 1, 2], [0] * 5):
+        with pytest.raises(ValueError):
+            moe.FewTokenLayer(shape, w, log2phys=table)
+
+
 def test_a_layer_of_other_sizes_or_another_table(lib):
     shape = synth.MoEShape("w", tokens=4, hidden=256, inter=256, num_experts=4, num_shared=1, top_k=2,
                            dtype="fp8")
