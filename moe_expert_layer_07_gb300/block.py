@@ -445,6 +445,10 @@ class Mx4MoELayer:
 
     def __init__(self, shape, weights: dict, max_tokens: int, log2phys=None):
         from . import permute_workspace_size
+        if shape.dtype != "mxfp4":
+            raise ValueError(f"expected a shape with MXFP4 experts, got {shape.dtype}")
+        if not isinstance(weights, dict):
+            raise TypeError("expected a dict of weights")
         self.shape = shape
         self.few = FewTokenLayer(shape, weights, log2phys=log2phys)
         self._keep = k = self.few._keep

@@ -44,6 +44,15 @@ def test_packing_refuses_elements_of_another_size():
             moe.pack_expert_weights(cfg, good, out=good[:1])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_the_mxfp4_layer_refuses_other_types(dtype):
+    """It took them up to 16 tokens, and read their bytes as codes above."""
+    with pytest.raises(ValueError):
+        moe.Mx4MoELayer(dataclasses.replace(MX4, dtype=dtype), _codes(MX4), 40)
+    with pytest.raises(TypeError):
+        moe.Mx4MoELayer(MX4, object(), 40)
+
+
 def test_few_token_layer_refuses_weights_of_another_size():
     four = dataclasses.replace(MX4, dtype="bf16")
     for shape, w in ((four, _codes(MX4)), (dataclasses.replace(MX4, dtype="fp8"), _codes(MX4)),
