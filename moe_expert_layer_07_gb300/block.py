@@ -460,7 +460,7 @@ class Mx4MoELayer:
         def buf(*size, dtype=torch.uint8):
             return torch.empty(*size, dtype=dtype, device=dev)
         i32, f32 = torch.int32, torch.float32
-        self.status_word = torch.zeros(1, dtype=i32, device=dev)
+        self.status_word = self.few.ws[:4].view(i32)   # one word for both paths
         self.logits = buf(T, shape.num_experts, dtype=f32)
         self.ids, self.wts = buf(T, shape.top_k, dtype=i32), buf(T, shape.top_k, dtype=f32)
         self.offsets, self.src = buf(G + 1, dtype=i32), buf(R, dtype=i32)
@@ -484,6 +484,8 @@ class Mx4MoELayer:
         out_dtype = _layer_io(x, out, out_dtype, T, s.hidden)
         rows = T * (s.top_k + s.num_shared)
         st = self.status_word
+        layer_few(self.few.cfg, self.few.weights, 0, None, None, OUT_F32, self.few.ws,
+                  self.few.ws_bytes, stream)   # no tokens: zeroes the word
         route(self.cfg, T, x, k["wg"], k["e_bias"], k["logit_offset"], k["log2phys"], self.logits,
               self.ids, self.wts, st, stream)
         permute(self.cfg, T, self.ids, x, None, self.offsets, self.src, self.row_of_slot, self.xp,
@@ -497,8 +499,8 @@ class Mx4MoELayer:
         return out
 
     def status(self) -> int:
-        """The device status of the calls so far (both paths)."""
-        return self.few.status() | int(self.status_word)
+        """The device status of the last call, as MoELayer's."""
+        return self.few.status()
 
 
 class MoEBlock:

@@ -60,3 +60,34 @@ def test_experts_that_share_a_slot(lib, dtype, T, E, k, table):
     assert torch.equal(got, ref)
     ids = few.view("topk_ids", torch.int32, (T, k))
     assert bool((ids[..., None] == at[:E].int()).any(-1).all())
+
+
+@pytest.mark.parametrize("T", [4, 40])
+def test_status_of_the_mxfp4_layer_is_the_last_calls(lib, T):
+    """A token of NaN has no expert to go to; the next call starts anew, on each path and after
+    either."""
+    shape = synth.MoEShape("status", tokens=40, hidden=256, inter=128, num_experts=8, num_shared=1,
+                           top_k=2, dtype="mxfp4")
+    w = _inputs(shape)
+    layer = moe.Mx4MoELayer(shape, w, 40)
+    assert layer.status() == 0
+    x, out = w["x"], torch.empty(40, 256, device="cuda")
+    bad = x.clone()
+    bad[1] = float("nan")
+    layer.ids.zero_()
+    for after in (4, 40):
+        layer.forward(bad[:T], out[:T])
+        assert layer.status() == moe.DEV_BAD_EXPERT_ID
+        layer.forward(x[:after], out[:after])
+        assert layer.status() == 0
+        layer.forward(bad[:after], out[:after])
+        layer.forward(x[:T], out[:T])
+        assert layer.status() == 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    layer.forward(bad[:T], out[:T], stream=side)
+    side.synchronize()
+    assert layer.status() == moe.DEV_BAD_EXPERT_ID
+    layer.forward(x[:T], out[:T], stream=side.cuda_stream)
+    side.synchronize()
+    assert layer.status() == 0
