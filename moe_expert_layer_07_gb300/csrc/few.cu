@@ -1059,8 +1059,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                             const __nv_bfloat162 b0 = __floats2bfloat162_rn(v.x, v.y),
                                                  b1 = __floats2bfloat162_rn(v.z, v.w);
                             const float2 f0 = __bfloat1622float2(b0), f1 = __bfloat1622float2(b1);
-                            const __nv_bfloat162 l0 = __floats2bfloat162_rn(v.x - f0.x, v.y - f0.y),
-                                                 l1 = __floats2bfloat162_rn(v.z - f1.x, v.w - f1.y);
+                            // nothing is left of an infinity (inf - inf would add a NaN)
+                            auto left = [](float all, float hi) { return fabsf(hi) <= FLT_MAX ? all - hi : 0.0f; };
+                            const __nv_bfloat162 l0 = __floats2bfloat162_rn(left(v.x, f0.x), left(v.y, f0.y)),
+                                                 l1 = __floats2bfloat162_rn(left(v.z, f1.x), left(v.w, f1.y));
                             // tile of 64: un.tile * 2 + lane / 16
                             uint8_t *o = a.hrows + ((row * mt1 + un.tile) * 2 + lane / 16) * TR::kCopyH + lane % 16 * 8;
                             auto bits = [](const __nv_bfloat162 &b) { return *reinterpret_cast<const uint32_t *>(&b); };

@@ -91,3 +91,32 @@ def test_status_of_the_mxfp4_layer_is_the_last_calls(lib, T):
     layer.forward(x[:T], out[:T], stream=side.cuda_stream)
     side.synchronize()
     assert layer.status() == 0
+
+
+def test_an_overflowing_h_stays_an_infinity(lib):
+    """h beyond bf16's range: the few-token layer, which keeps h in two parts, answers as the layer
+    does.  Token 0's h overflows fp32, token 1's lies between the largest bf16 and the largest fp32
+    number, token 2's is NaN, token 3's an ordinary one."""
+    s = synth.MoEShape("large h", tokens=4, hidden=256, inter=128, num_experts=4, num_shared=0, top_k=1,
+                       dtype="bf16")
+    w = _inputs(s, 1)
+    w["wg"].zero_()
+    w["wg"][torch.arange(4), torch.arange(4)] = 1.0       # token t to expert t
+    w["x"].zero_()
+    w["x"][torch.arange(4), torch.arange(4)] = 1.0
+    w["w13"].zero_()
+    w["w13"][0, :128, 0], w["w13"][0, 128:, 0] = 1e19, 1e20       # h beyond fp32 too
+    w["x"][1, 10] = 1.0                                            # 2^64 (0.9961 + 0.0030) 2^64
+    w["w13"][1, :128, 1], w["w13"][1, 128:, 1], w["w13"][1, 128:, 10] = 2.0 ** 64, 1.8374687e19, 5.534e16
+    w["w13"][2, :128, 2], w["w13"][2, 128:, 2] = float("inf"), 0.0
+    w["w13"][3, :128, 3], w["w13"][3, 128:, 3] = 3.0, 5.0
+    w["w2"][:2] = w["w2"][:2].abs() + 0.01
+    big = moe.MoELayer(s, w)
+    few = moe.FewTokenLayer(s, big)
+    ref, got = torch.empty(4, 256, device="cuda"), torch.empty(4, 256, device="cuda")
+    big.forward(w["x"], ref)
+    few.forward(w["x"], got)
+    assert few.status() == big.status() == 0
+    assert bool((ref[:2] == float("inf")).all()) and torch.equal(got[:2], ref[:2])
+    assert bool(torch.isnan(got[2]).all())
+    assert bool(torch.isfinite(got[3]).all()) and float((got[3] - ref[3]).abs().max()) <= 2e-2 * float(ref[3].abs().max())
