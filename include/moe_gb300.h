@@ -416,7 +416,8 @@ MOE_API int moe_layer_forward(const moe_config *cfg, const moe_weights *w, int32
  * two kernels: the gate logits (with the quantisation of x), then selection,
  * both expert products and the combine in one persistent kernel that streams
  * each chosen expert's weights once.  The same definition, step by step:
- * routing ids and weights are moe_route's, bit for bit; x and h are quantised
+ * routing ids and weights are moe_route's, bit for bit, also with biases of
+ * minus infinity (experts taken out); x and h are quantised
  * in the same places (BF16: h is kept to 17 bits instead of rounded to bf16);
  * sums are fp32 in another order, so outputs agree within the layer's tolerance
  * and not bit for bit (a sum that lies on a rounding boundary of h may take the

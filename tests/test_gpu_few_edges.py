@@ -120,3 +120,40 @@ def test_an_overflowing_h_stays_an_infinity(lib):
     assert bool((ref[:2] == float("inf")).all()) and torch.equal(got[:2], ref[:2])
     assert bool(torch.isnan(got[2]).all())
     assert bool(torch.isfinite(got[3]).all()) and float((got[3] - ref[3]).abs().max()) <= 2e-2 * float(ref[3].abs().max())
+
+
+def _route(s, w):
+    """moe_route's (ids, weights, status)."""
+    cfg = moe.make_config(s, s.tokens)
+    dev = dict(device="cuda")
+    ids = torch.full((s.tokens, s.top_k), -1, dtype=torch.int32, **dev)
+    tw, st = torch.zeros(s.tokens, s.top_k, **dev), torch.zeros(1, dtype=torch.int32, **dev)
+    moe.route(cfg, s.tokens, w["x"], w["wg"], w["e_bias"], None, None,
+              torch.empty(s.tokens, s.num_experts, **dev), ids, tw, st)
+    return ids, tw, int(st)
+
+
+# live experts of each group, the others' bias is minus infinity
+@pytest.mark.parametrize("live", [[16, 16, 1, 1], [16, 1, 0, 1], [2, 1, 1, 0], [1, 1, 1, 1], [0, 0, 3, 0],
+                                  [0, 0, 0, 0], [16, 3, 2, 2]])
+@pytest.mark.parametrize("gs", [16, 32, 64])
+@pytest.mark.parametrize("topn", [1, 2, 4, 5])
+@pytest.mark.parametrize("keep,k", [(2, 2), (3, 1), (4, 4)])
+def test_routing_with_experts_taken_out(lib, live, gs, topn, keep, k):
+    """A bias of minus infinity takes an expert out of the selection; the groups that are kept, the ids,
+    the weights and what is reported are moe_route's."""
+    s = synth.MoEShape("masked", tokens=5, hidden=128, inter=128, num_experts=4 * gs, num_shared=0,
+                       top_k=k, num_groups=4, topk_groups=keep, group_topn=topn, scoring="sigmoid",
+                       norm_topk=True, routed_scaling=2.5, dtype="bf16", bias_std=0.01)
+    w = _inputs(s, gs)
+    bias = torch.full((4, gs), float("-inf"), device="cuda")
+    for g, n in enumerate(live):
+        # groups of few live experts have the best ones, which only the group's score keeps out
+        bias[g, gs // 2 - n // 2:gs // 2 - n // 2 + n] = 0.01 if n == 16 else 1.0
+    w["e_bias"] = bias.reshape(-1).contiguous()
+    ids, tw, st = _route(s, w)
+    few = moe.FewTokenLayer(s, w)
+    few.forward(w["x"], torch.empty(5, 128, device="cuda"))
+    assert few.status() == st
+    assert torch.equal(few.view("topk_ids", torch.int32, (5, k)), ids)
+    assert torch.equal(few.view("topk_w", torch.float32, (5, k)), tw)
