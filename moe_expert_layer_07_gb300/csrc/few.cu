@@ -883,6 +883,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                           : ptx::wait_flag_geq(h_done + un.gi, mt1 * kPublishers, abort_flag, a.status, MOE_DEV_TIMEOUT);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
+                __syncwarp();   // what lane 0 has acquired, for every lane (the vote orders no memory)
                 ptx::fence_proxy_async_global();
             }
             // this lane copies row `lane` (its segment of each K tile is contiguous)
@@ -991,7 +992,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         int pending = -1, before = 0;
         auto finish_pending = [&]() {
             if (pending >= 0 && __shfl_sync(0xffffffffu, before, 0) == nG - 1) {
-                __threadfence();   // all groups' rows of these columns are there
+                // all groups' rows of these columns are there: for lane 0 by its
+                // fence after the count, for the others by the barrier (the
+                // shuffle orders no memory)
+                __threadfence();
+                __syncwarp();
                 combine(pending);
             }
             pending = -1;
