@@ -1167,6 +1167,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                                            a.status, MOE_DEV_TIMEOUT);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
+                    ptx::tc_fence_after();   // the products that read these columns before are done
                     const uint8_t *base = ring + st * TR::kStage;
                     const uint32_t sf = tmem + quarter + TR::kSfCol + st * TR::kSfStage;
                     const int nk = min(un.per, un.kb - s * un.per);
