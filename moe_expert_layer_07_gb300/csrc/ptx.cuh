@@ -74,24 +74,42 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// A wait that gives up: after `limit_ns` (or, as a backstop should the
-// timer stall, 2^26 polls) it raises the CTA's abort flag, records
-// `timeout_bit` in the device status word and returns false.  It also
-// returns false as soon as another warp of the CTA has aborted.
+// How long a wait has taken.  It is over after its limit by the timer or,
+// should the timer stall, after kStalledPolls polls in which the timer did not
+// move: at most 2.6 s (each poll may be held for kSuspendNs), at least some
+// milliseconds, far longer than the timer's step.
 constexpr uint64_t kWaitLimitNs = 1000000000ull;   // one second
-constexpr uint32_t kWaitMaxPolls = 1u << 26;
+constexpr uint32_t kStalledPolls = 1u << 17;
+static_assert((uint64_t)kStalledPolls * kSuspendNs <= 3 * kWaitLimitNs, "a stalled timer bounds a wait too");
+struct WaitClock {
+    uint64_t t0, last;
+    uint32_t still;   // polls since the timer moved
+    __device__ __forceinline__ WaitClock() : t0(globaltimer()), last(t0), still(0) {}
+    // `polls` more have been made
+    __device__ __forceinline__ bool over(uint64_t limit_ns, uint32_t polls) {
+        const uint64_t now = globaltimer();
+        still = now == last ? still + polls : 0;
+        last = now;
+        return now - t0 > limit_ns || still >= kStalledPolls;
+    }
+};
 
+// A wait that gives up: after `limit_ns` it raises the CTA's abort flag,
+// records `timeout_bit` in the device status word and returns false.  It also
+// returns false when another warp of the CTA has aborted.  Timer and flag are
+// looked at every 64 polls, which may take 64 kSuspendNs, 1.3 ms: a limit is
+// passed, or an abort seen late, by that much at most.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity,
                                              volatile int *abort_flag, int32_t *status,
                                              int32_t timeout_bit,
                                              uint64_t limit_ns = kWaitLimitNs) {
     if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer();
+    WaitClock clock;
     for (uint32_t it = 1;; ++it) {
         if (mbar_try_wait(bar, parity)) return true;
         if ((it & 63u) == 0) {
             if (*abort_flag) return false;
-            if (globaltimer() - t0 > limit_ns || it >= kWaitMaxPolls) {
+            if (clock.over(limit_ns, 64)) {
                 if (mbar_try_wait(bar, parity)) return true;   // completed meanwhile
                 *abort_flag = 1;
                 if (status) atomicOr(status, timeout_bit);
@@ -103,10 +121,9 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity,
 
 // Teardown wait: ignores the abort flag, still bounded.
 __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
-    const uint64_t t0 = globaltimer();
-    for (uint32_t it = 0; !mbar_try_wait(bar, parity); ++it) {
-        if (globaltimer() - t0 > kWaitLimitNs || it >= kWaitMaxPolls) return false;
-    }
+    WaitClock clock;
+    while (!mbar_try_wait(bar, parity))
+        if (clock.over(kWaitLimitNs, 1)) return false;
     return true;
 }
 
@@ -124,8 +141,6 @@ __device__ __forceinline__ float ld_relaxed_gpu_f32(const float *p) {
 __device__ __forceinline__ void red_release_gpu_add(int32_t *p, int v) {
     asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
-// Orders this thread's generic-proxy global accesses with async-proxy (TMA)
-// accesses to global memory.
 // Two independent IEEE fp32 FMAs in one instruction (the bits of two fmaf).
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t d;
@@ -138,6 +153,8 @@ __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
     return d;
 }
 
+// Orders this thread's generic-proxy global accesses with async-proxy (TMA)
+// accesses to global memory.
 __device__ __forceinline__ void fence_proxy_async_global() {
     asm volatile("fence.proxy.async.global;" ::: "memory");
 }
@@ -147,12 +164,12 @@ __device__ __forceinline__ bool wait_flag_geq(const int32_t *flag, int target,
                                               volatile int *abort_flag, int32_t *status,
                                               int32_t timeout_bit) {
     if (ld_acquire_gpu(flag) >= target) return true;
-    const uint64_t t0 = globaltimer();
-    for (uint32_t it = 1;; ++it) {
+    WaitClock clock;
+    for (;;) {
         __nanosleep(64);
         if (ld_acquire_gpu(flag) >= target) return true;
         if (*abort_flag) return false;
-        if (globaltimer() - t0 > kWaitLimitNs || it >= kWaitMaxPolls) {
+        if (clock.over(kWaitLimitNs, 1)) {
             if (ld_acquire_gpu(flag) >= target) return true;
             *abort_flag = 1;
             if (status) atomicOr(status, timeout_bit);
