@@ -360,8 +360,9 @@ __global__ void __launch_bounds__((Shape<SW, PAIR>::kThreads), 1)
             }
             first = s - steps;
         }
-        // copies in flight have to land before the CTA gives up its memory
-        for (uint32_t i = it > kStages ? it - kStages : mine; !ok && i < it; i += S::kSlotWarps)
+        // copies in flight have to land before the CTA gives up its memory, also
+        // where another warp gives up after this one's last copies
+        for (uint32_t i = it > kStages ? it - kStages : mine; i < it; i += S::kSlotWarps)
             wait_drain(smem_u32(&full_bar[i % kStages]), (i / kStages) & 1);
     } else if (warp < kFirstEpiWarp) {
         // ---- scales to tensor memory: each warp to its lane quarter ----------------------
