@@ -278,7 +278,7 @@ struct Traits {
     static constexpr int kWsOff = kTokOff + 2 * kTokHalf;   // FP8: the tiles' two scales
     static constexpr int kStage = (kWsOff + 16 + 127) / 128 * 128;
     static constexpr int kBWords = DT == DT_BF16 ? 8 : 16;  // B words a lane holds for a tile
-    static constexpr int kTiles = 2, kScale = 0, kScaleOff = 0;
+    static constexpr int kTiles = 2, kScale = 0;
     static constexpr int kMultipliers = kConsumers;         // warps that release a stage
     static constexpr int kReaders = kWarps - 1;             // warps that read a unit's number
 };
@@ -291,7 +291,7 @@ struct Traits<DT_MX4, NT> {
     static constexpr int kTokOff = kTiles * kTile, kScaleOff = kTokOff + kTiles * kTokBytes;
     static constexpr int kTokScaleOff = kScaleOff + kTiles * kScale;
     static constexpr int kStage = kTokScaleOff + kTiles * 512;
-    static constexpr int kCopyX = 0, kCopyH = 0, kPitch = 0, kTokHalf = 0, kWsOff = 0, kBWords = 1;
+    static constexpr int kCopyX = 0, kCopyH = 0, kPitch = 0, kTokHalf = 0, kWsOff = 0;
     static constexpr int kMultipliers = 1;                  // the MMAs' commit
     static constexpr int kScalers = 4;                      // warps 4..7: a lane quarter each
     static constexpr int kReaders = 1 + kScalers + 1 + kPublishers;
