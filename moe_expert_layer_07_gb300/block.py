@@ -508,6 +508,7 @@ class MoEBlock:
 
     layer: an MoELayer, a FewTokenLayer or an Mx4MoELayer.  With `few` (a
     FewTokenLayer) calls of few tokens go there.  w_post and gate may be None.
+    kind may be NORM_LAYER; norms with biases are block_norm's alone.
     """
 
     def __init__(self, layer, w_pre, w_post=None, gate=None, residual_scale=1.0, branch_scale=1.0,

@@ -11,7 +11,8 @@
 // With so few rows an expert's weights are read for one to a few products
 // each, so the time is the weights' bytes over the memory rate: 400 MB, 59 us
 // at the copy rate, for one token of nine 44 MB experts in FP8, where the two
-// kernels take 71.5.  The difference is the first kernel and the selection
+// kernels take 69 to 73 (graph replays 69.2 / 70.9 / 71.2 on three GPUs, calls
+// from Python in a row 73.2).  The difference is the first kernel and the selection
 // (about 8 us, in which only the shared experts' weights move, to L2) and the
 // join of the two phases.  In the FFN kernel everything hides behind the
 // stream of weights; its warps are:

@@ -36,7 +36,9 @@
 // one tile to the next, since the accumulator and the scales leave no room in
 // tensor memory for a second accumulator: 8192 x 7168 x 7168 takes 116 us, 7.3
 // PFLOP/s, of which about 640 cycles a stage in products and 2000 a tile where
-// they wait for the epilogue to read it.
+// they wait for the epilogue to read it.  fp32 C, twice the bytes to store, on
+// one GPU with bf16 C beside it: 273 rows 38.3 / 37.6 us, 16411 rows of K 2048 in
+// 8 groups 129 / 99 (80 at the copy rate), 8192 x 7168 x 7168 133 / 116.
 // On the way there, same product: 267 us -> 253 waits that let the hardware
 // hold the thread; -> 234 one copy for both K blocks' scale bytes; -> 199 a
 // warp for each ring slot to issue its copies; -> 176 scales stored to tensor
