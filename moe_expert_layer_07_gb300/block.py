@@ -160,6 +160,25 @@ def pack_mx4_weights(codes, scales, stream=None):
 _C_TYPES = {kind: dtype for dtype, kind in _OUT.items()}
 
 
+def _product_fits(groups, n_out, k_dim, rows, a, a_scales, offsets, w, w_scales, status) -> bool:
+    """All that holds of a correct product's operands in one test; False also for what
+    _check_product would let pass (addresses, weights in other shapes of the same size)."""
+    u8, i32 = torch.uint8, torch.int32
+    try:
+        return (a.dtype is u8 and a_scales.dtype is u8 and w.dtype is u8 and w_scales.dtype is u8
+                and offsets.dtype is i32 and a.is_cuda and a_scales.is_cuda and w.is_cuda
+                and w_scales.is_cuda and offsets.is_cuda and a.is_contiguous()
+                and a_scales.is_contiguous() and w.is_contiguous() and w_scales.is_contiguous()
+                and offsets.is_contiguous() and w.shape == (groups, n_out, k_dim // 2)
+                and w_scales.shape == (groups, n_out, k_dim // 32) and a.shape[-1] == k_dim // 2
+                and a_scales.shape[-1] == k_dim // 32 and a.nbytes >= rows * (k_dim // 2)
+                and a_scales.nbytes >= rows * (k_dim // 32) and offsets.nbytes > 4 * groups
+                and (status is None or status.dtype is i32 and status.is_cuda
+                     and status.is_contiguous() and status.nbytes >= 4))
+    except (AttributeError, IndexError):
+        return False
+
+
 def _check_product(groups, n_out, k_dim, rows, a, a_scales, offsets, w, w_scales, status, *outs):
     """Checks a grouped product's tensors against its sizes."""
     if rows <= 0:
@@ -180,8 +199,10 @@ def mx4_grouped_gemm(groups, n_out, k_dim, rows, a, a_scales, expert_offsets, w,
     """C[r] = A[r] W[g]^T for the rows of each group; w, w_scales from pack_mx4_weights.
     a, a_scales and c may have more than `rows` rows; c is of c_dtype."""
     c_type = _C_TYPES.get(c_dtype) or getattr(c, "dtype", None)   # the library refuses other kinds
-    _check_product(groups, n_out, k_dim, rows, a, a_scales, expert_offsets, w, w_scales,
-                   status, ("c", c, c_type, rows, n_out))
+    if not (_product_fits(groups, n_out, k_dim, rows, a, a_scales, expert_offsets, w, w_scales, status)
+            and _holds(c, c_type, rows, n_out)):
+        _check_product(groups, n_out, k_dim, rows, a, a_scales, expert_offsets, w, w_scales,
+                       status, ("c", c, c_type, rows, n_out))
     _check(lib().moe_mx4_grouped_gemm(groups, n_out, k_dim, rows, _ptr(a), _ptr(a_scales),
                                       _ptr(expert_offsets), _ptr(w), _ptr(w_scales), _ptr(c),
                                       c_dtype, _ptr(status), _stream(stream)),
@@ -191,9 +212,12 @@ def mx4_grouped_gemm(groups, n_out, k_dim, rows, a, a_scales, expert_offsets, w,
 def mx4_grouped_gemm_swiglu(groups, inter, k_dim, rows, a, a_scales, expert_offsets, w13,
                             w13_scales, h, h_scales, status=None, stream=None):
     """The gate/up product with SwiGLU, h in MXFP4 (codes [rows, inter/2], scales [rows, inter/32])."""
-    _check_product(groups, 2 * inter, k_dim, rows, a, a_scales, expert_offsets, w13, w13_scales,
-                   status, ("h", h, torch.uint8, rows, inter // 2),
-                   ("h_scales", h_scales, torch.uint8, rows, inter // 32))
+    u8 = torch.uint8
+    if not (_product_fits(groups, 2 * inter, k_dim, rows, a, a_scales, expert_offsets, w13, w13_scales,
+                          status)
+            and _holds(h, u8, rows, inter // 2) and _holds(h_scales, u8, rows, inter // 32)):
+        _check_product(groups, 2 * inter, k_dim, rows, a, a_scales, expert_offsets, w13, w13_scales,
+                       status, ("h", h, u8, rows, inter // 2), ("h_scales", h_scales, u8, rows, inter // 32))
     _check(lib().moe_mx4_grouped_gemm_swiglu(groups, inter, k_dim, rows, _ptr(a), _ptr(a_scales),
                                              _ptr(expert_offsets), _ptr(w13), _ptr(w13_scales),
                                              _ptr(h), _ptr(h_scales), _ptr(status),
