@@ -64,7 +64,9 @@ enum {
 enum {                               /* bits of the device status word */
     MOE_DEV_BAD_EXPERT_ID = 1,       /* a topk id / log2phys entry outside [0, E) */
     MOE_DEV_BAD_OFFSETS = 2,         /* expert_offsets not non-decreasing within [0, rows] */
-    MOE_DEV_TIMEOUT = 4              /* a bounded pipeline wait expired (about 1 s) */
+    MOE_DEV_TIMEOUT = 4,             /* a bounded pipeline wait expired (about 1 s) */
+    MOE_DEV_BAD_INDEX = 8,           /* a page, slot, position or length outside its range */
+    MOE_DEV_NO_ROOM = 16             /* too few free pages, table columns or token rows */
 };
 enum { MOE_SCORING_SOFTMAX = 0, MOE_SCORING_SIGMOID = 1 };
 enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP8_BLOCK128 = 1, MOE_DTYPE_MXFP4 = 2 };  /* MXFP4: moe_layer_few only */
@@ -536,6 +538,149 @@ MOE_API int moe_block_norm(const moe_norm *d, int32_t T, const void *y, const vo
                            const void *gate, const void *w_post, const void *b_post,
                            const void *w_pre, const void *b_pre, void *residual_out, void *x_out,
                            void *stream);
+
+/* ---- a cache of keys and values in four bits --------------------------------------------
+ * Attention's half of a decoder layer, next to the MoE half above: tables of a
+ * paged cache, the norm and rotation of queries and keys with the cache's
+ * write, and attention that reads it.
+ *
+ * The cache holds each token's keys and values of kv_heads heads of `dim`
+ * channels in MXFP4 (blocks of 32 channels, as moe_mx4_quantize), in pages of
+ * `page` tokens.  Token slot s is row s mod page of page s / page.
+ *   codes   [pages, 2, kv_heads, page, dim/2]   (keys, then values)
+ *   scales  [pages, 2, kv_heads, page, dim/32]
+ * dim 64 or 128; page 16, 32, 64 or 128; kv_heads 1..256; pages * page below
+ * 2^31 (byte offsets are 64 bits).  A page's rows that no token was written to
+ * may hold anything. */
+typedef struct moe_cache4 {
+    void *codes, *scales;
+    int32_t pages, kv_heads, page, dim;
+} moe_cache4;
+
+/* Tables of one step, from the requests' lengths: request b holds held[b]
+ * tokens and gets new_tokens[b] more (0: none).  Its page i covers its tokens
+ * [i page, (i+1) page); the pages that it lacks are taken from a ring of free
+ * ones, request after request.
+ *   requests    B, 0..16384
+ *   held, new_tokens  int32 [B], >= 0
+ *   free_pages  int32 [free_count]: a ring; free_range int64 [2] = {next, end}:
+ *               entries next .. end-1 (each mod free_count) are free.  A caller
+ *               gives pages back by writing them behind `end`.
+ *   table       int32 [B, max_pages], the first ceil(held[b]/page) entries of a
+ *               row as earlier steps left them; the new pages' entries are
+ *               written, all others left alone
+ *   lengths     int32 [B], written: held + new_tokens (may be `held`)
+ *   starts      int32 [B+1], written: first token row of each request
+ *   slots       int32 [max_tokens], written: the slot of each token row, -1
+ *               behind the last one
+ *   positions   int32 [max_tokens], written: its position, 0 behind the last
+ *   free_out    int64 [2], written: free_range after the step (may be it)
+ * A step that cannot be made whole is not made: a negative length or a page
+ * id below 0 that a token needs sets MOE_DEV_BAD_INDEX; too few free pages,
+ * table columns or token rows MOE_DEV_NO_ROOM; then lengths = held, starts,
+ * and positions are 0, slots -1, free_out = free_range and the table is as it
+ * was.  (An id below 0 is looked at where tokens join a request's last held
+ * page.)  One launch; nothing else may overlap. */
+MOE_API int moe_cache_tables(int32_t requests, int32_t page, const int32_t *held,
+                             const int32_t *new_tokens, const int32_t *free_pages,
+                             int32_t free_count, const int64_t *free_range, int32_t *table,
+                             int32_t max_pages, int32_t *lengths, int32_t *starts, int32_t *slots,
+                             int32_t *positions, int32_t max_tokens, int64_t *free_out,
+                             int32_t *dev_status, void *stream);
+
+/* Norm of queries and keys for each head and the rotation by the token's
+ * position, in one pass, with the cache's write: for each head v of a row
+ *   n = v / sqrt(mean(v^2) + eps) * w           (v itself without w)
+ * and the first rope_dim channels of n turned by the token's angles,
+ *   MOE_ROPE_HALVES  channels i and i + rope_dim/2 as a pair (i < rope_dim/2)
+ *   MOE_ROPE_PAIRS   channels 2i and 2i + 1
+ *   a, b -> a cos_i - b sin_i, b cos_i + a sin_i
+ * fp32 from load to store, each output rounded once.
+ *   qkv         bf16 [T, qkv_stride]: q_heads, then kv_heads of keys, then
+ *               kv_heads of values, `dim` channels each (dim 64 or 128;
+ *               qkv_stride a multiple of 8)
+ *   positions   int32 [T]; cos_sin fp32 [max_positions, rope_dim]: cosines of
+ *               the rope_dim/2 angles, then sines; both may be NULL with rope_dim 0
+ *   w_q, w_k    [dim] of param_dtype (MOE_OUT_*), or NULL
+ *   q_out       bf16 [T, q_heads, dim]; k_out bf16 [T, kv_heads, dim] or NULL
+ *   cache, slots  NULL, or the keys (after all this) and the values of row t
+ *               go to slot slots[t] (int32 [T]; -1: nowhere), in four bits.
+ *               Slots of one call are distinct.
+ * rope_dim a multiple of 16, 0..dim.  A position outside [0, max_positions) or a
+ * slot outside [-1, pages * page) sets MOE_DEV_BAD_INDEX; of such a row nothing
+ * is written.  Outputs must not overlap inputs. */
+enum { MOE_ROPE_HALVES = 0, MOE_ROPE_PAIRS = 1 };
+typedef struct moe_qk_rope {
+    int32_t q_heads, kv_heads, dim, rope_dim, style, param_dtype, max_positions, qkv_stride;
+    float eps;
+} moe_qk_rope;
+MOE_API int moe_qk_norm_rope(const moe_qk_rope *d, int32_t T, const void *qkv,
+                             const int32_t *positions, const float *cos_sin, const void *w_q,
+                             const void *w_k, void *q_out, void *k_out, const moe_cache4 *cache,
+                             const int32_t *slots, int32_t *dev_status, void *stream);
+
+/* The values that n slots of a cache hold: k, v bf16 [n, kv_heads, dim] (either
+ * may be NULL).  Rows of slot -1 are left as they were; other slots outside
+ * the cache set MOE_DEV_BAD_INDEX and leave theirs too. */
+MOE_API int moe_cache_read(const moe_cache4 *cache, int32_t n, const int32_t *slots, void *k, void *v,
+                           int32_t *dev_status, void *stream);
+
+/* Attention over the cache.  Request b's query rows are starts[b] ..
+ * starts[b+1]-1 of q, its last tokens: row i of n stands at position
+ * p = lengths[b] - n + i and sees the cached tokens j <= p (with a window,
+ * j > p - window):
+ *   o = sum_j softmax_j(scale q . k_j) v_j
+ * for each query head, with keys and values of KV head
+ * head / (q_heads / kv_heads); decode steps, drafted tokens and chunks of
+ * prompts in one call.
+ *   q, out     bf16 [rows, q_heads, dim] (out may be q); out fp32 with out_dtype
+ *              MOE_OUT_F32
+ *   lse        fp32 [rows, q_heads] or NULL: the natural logarithm of
+ *              sum_j exp(scale q . k_j)
+ *   table      int32 [requests, max_pages]; lengths int32 [requests];
+ *              starts int32 [requests + 1] (moe_cache_tables' outputs)
+ * A row that sees nothing (its position is negative) gets zeros and an lse of
+ * -infinity.  Rows outside every request are left as they were.  starts that
+ * decrease or leave [0, rows], lengths outside [0, max_pages * page] and page
+ * ids outside [0, pages) set MOE_DEV_BAD_INDEX: such a request is not computed,
+ * the tokens of such a page are not seen.
+ * Scores and sums are fp32; probabilities are rounded to fp16 before the sum of
+ * the values (relative 2^-11 each).  Values of a channel block whose scale is
+ * below 2^-22 of the largest that the row's tokens have there count as zero.
+ *   desc.max_q    the most query rows of one request, and
+ *   desc.max_len  the longest request: what the kernels and the workspace are
+ *                 chosen by; larger ones on the device are computed all the same
+ *   ws         moe_cache_attention_workspace_size bytes, 16-byte aligned; one call
+ *              at a time; needs no initialisation
+ * requests 0..4096, rows * q_heads below 2^31, q_heads a multiple of kv_heads. */
+typedef struct moe_cache_attn {
+    int32_t requests, rows, q_heads, max_pages, max_q, max_len, window;   /* window 0: none */
+    float scale;
+} moe_cache_attn;
+MOE_API int moe_cache_attention_workspace_size(const moe_cache_attn *d, const moe_cache4 *cache,
+                                               size_t *bytes /* host */);
+MOE_API int moe_cache_attention(const moe_cache_attn *d, const moe_cache4 *cache, const void *q,
+                                const int32_t *table, const int32_t *lengths, const int32_t *starts,
+                                void *out, int32_t out_dtype, float *lse, void *ws, size_t ws_bytes,
+                                int32_t *dev_status, void *stream);
+
+/* Products of 1 to 16 rows with weights in four bits and activations in bf16:
+ *   y[t, n] = sum_k x[t, k] W[n, k],   y fp32 or bf16 [T, n_out] (out_dtype)
+ *   MOE_W4_MX   W in MXFP4: codes [n_out, k_dim/2] and scale bytes
+ *               [n_out, k_dim/32] as moe_mx4_quantize gives them (row-major)
+ *   MOE_W4_INT  W[n, k] = scale[n, k/group] (code - zero[n, k/group]), codes 0..15
+ *               (even k in the low four bits), scales bf16 or fp32 (scale_dtype),
+ *               zero points uint8 0..15 or NULL (8); group 32, 64 or 128
+ * fp32 accumulation.  x is taken as fp16 times a power of two for each row:
+ * values below 2^-38 of a row's largest lose bits.  n_out any, k_dim a multiple of
+ * the group (of 32 for MXFP4), at most 32768; x and codes 16-byte aligned. */
+enum { MOE_W4_MX = 0, MOE_W4_INT = 1 };
+typedef struct moe_w4 {
+    int32_t n_out, k_dim, kind, group, scale_dtype;
+} moe_w4;
+MOE_API int moe_w4_matvec(const moe_w4 *d, int32_t T, const void *x, const void *codes,
+                          const void *scales, const void *zeros, void *y, int32_t out_dtype,
+                          void *stream);
 
 /* Byte offsets of the intermediates inside the layer workspace (host), for
  * callers that want to read routing results or rows per expert.  gate_up is

@@ -29,13 +29,16 @@ __all__ = ["Config", "Weights", "WsLayout", "lib", "make_config", "route", "rout
            "MXFP4", "FewTokenLayer", "FewLayout", "Mx4MoELayer", "MoEBlock", "layer_few", "layer_few_max_tokens",
            "layer_few_workspace_size", "layer_few_layout", "mx4_quantize", "mx4_dequantize",
            "pack_mx4_weights", "mx4_grouped_gemm", "mx4_grouped_gemm_swiglu", "Norm", "block_norm", "NORM_RMS", "NORM_LAYER", "GATE_NONE",
-           "GATE_FEATURE", "GATE_TOKEN", "GATE_FULL"]
+           "GATE_FEATURE", "GATE_TOKEN", "GATE_FULL",
+           # attention over a cache in four bits (attention.py)
+           "Cache4", "CacheAttention", "cache_tables", "cache_read", "qk_norm_rope", "rope_table",
+           "w4_matvec", "ROPE_HALVES", "ROPE_PAIRS"]
 
 SOFTMAX, SIGMOID = 0, 1
 BF16, FP8, MXFP4 = 0, 1, 2   # MXFP4: the few-token layer only
 OUT_F32, OUT_BF16 = 0, 1
 ACT_IDENTITY, ACT_SILU_MUL = 0, 1
-DEV_BAD_EXPERT_ID, DEV_BAD_OFFSETS, DEV_TIMEOUT = 1, 2, 4
+DEV_BAD_EXPERT_ID, DEV_BAD_OFFSETS, DEV_TIMEOUT, DEV_BAD_INDEX, DEV_NO_ROOM = 1, 2, 4, 8, 16
 LAYOUT_ROWS, LAYOUT_TILES = 0, 1
 
 
@@ -118,7 +121,7 @@ def lib():
             raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
                               "(there is no non-CUDA fallback)")
         L = ctypes.CDLL(LIB_PATH)
-        for name, args in {**_SIGS, **block._SIGS}.items():
+        for name, args in {**_SIGS, **block._SIGS, **attention._SIGS}.items():
             fn = getattr(L, name)
             fn.argtypes = args
             fn.restype = ctypes.c_int
@@ -678,3 +681,6 @@ from .block import (GATE_FEATURE, GATE_FULL, GATE_NONE, GATE_TOKEN, NORM_LAYER, 
                     layer_few_layout, layer_few_max_tokens, layer_few_workspace_size,
                     mx4_dequantize, mx4_grouped_gemm, mx4_grouped_gemm_swiglu, mx4_quantize,
                     pack_mx4_weights)
+from . import attention  # noqa: E402
+from .attention import (ROPE_HALVES, ROPE_PAIRS, Cache4, CacheAttention, cache_read,  # noqa: E402
+                        cache_tables, qk_norm_rope, rope_table, w4_matvec)

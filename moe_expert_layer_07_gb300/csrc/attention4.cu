@@ -1,0 +1,726 @@
+// Attention of few query rows over the four-bit cache:
+//   o = sum_j softmax_j(scale q . k_j) v_j
+//
+// One pass over the tokens with a running maximum m and sum l for each row:
+//   s = scale log2(e) q . k,  p = 2^(s - m),  l += p,  o += p v
+// Rows are the query heads of one KV head, for one or more query tokens; 8, 16
+// or 32 of them are the N side of the tensor cores' mma.sync m16n8k16, tokens
+// (for S^T = K Q^T) and channels (for O^T = V^T P^T) the M side, so that a key
+// or value is unpacked once for all rows and no row of a product is wasted when
+// there are eight.  tcgen05 would need both operands in shared memory, 16 bits
+// wide: 176 bytes a clock of an SM at the cache's full rate, where it has 128.
+//
+// Four-bit codes become fp16 with cvt (two an instruction), unscaled.  The
+// keys' scales are powers of two for 32 channels: they multiply the fp32
+// product of each block.  The values' scales multiply P: 2^(e - E + 7) with E
+// the largest exponent that the warp has met in the channel block, so that p up
+// to 2^8 times it fits fp16; what lies 22 binades below counts as zero.  m is
+// raised only when a score passes it by 8 (in log2), E when an exponent passes
+// it; then o is scaled.  q is fp16 times a power of two for each row: bf16
+// values have no more bits, and what is 2^-38 of the row's largest is lost.
+//
+// A warp works alone: it copies tiles of 16 tokens (keys, values and scales, 2176
+// bytes at 128 channels) into a ring of its own with cp.async and has its own m,
+// l and o; ldmatrix gives both operands in the order of the products, the
+// values transposed in units of four codes.  Shared memory holds 16-byte pieces
+// exchanged within rows so that ldmatrix meets no bank twice.
+//
+// Work is cut into units of 128 tokens (eight warps) of a request, KV head and
+// group of rows; a CTA takes as many neighbouring units as any other, whatever
+// the requests' lengths.  A request that is cut between CTAs leaves partial
+// results in the workspace (at most two a CTA), which a second kernel joins.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "attention4.cuh"
+#include "mx4.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = kAttnWarps * 32;
+constexpr float kLazy = 8.0f;      // how far scores may pass the maximum
+constexpr int kVBias = 7;          // P is scaled by 2^(e - E + kVBias)
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src))
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transposed8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+    const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Stands for the scale byte 255 (NaN) in a half word: very small, so that it
+// scales to zero, and known again by with_nans.
+constexpr uint32_t kNan = 0x8000u;
+
+// P times a scale, NaN where the scale is and P is not zero.
+__device__ __noinline__ uint32_t with_nans(uint32_t scaled, uint32_t p, uint32_t e) {
+    if ((e & 0xffffu) == kNan && (p & 0x7fffu)) scaled |= 0x7fffu;
+    if (e >> 16 == kNan && (p & 0x7fff0000u)) scaled |= 0x7fff0000u;
+    return scaled;
+}
+
+template <int D, int NQ>
+struct Shape {
+    static constexpr int kBlocks = D / 32;              // channel blocks
+    static constexpr int kRow = D / 2;                  // bytes of a token's codes
+    static constexpr int kCodes = kAttnTile * kRow;     // of a tile's keys or values
+    static constexpr int kScales = kAttnTile * kBlocks;
+    static constexpr int kStage = 2 * (kCodes + kScales);
+    static constexpr int kStages = D == 128 ? 4 : 6;
+    static constexpr int kRows = 8 * NQ;
+    static constexpr int kRing = kAttnWarps * kStages * kStage;
+    // queries in the order of the products, then what rows and warps exchange
+    static constexpr int kQBytes = D / 16 * NQ * 32 * 8;
+    static constexpr int kSmem = kRing + kQBytes + (kRows + 2 * kAttnWarps * kRows) * 4;
+    static_assert(kAttnWarps * 8 * D * 4 <= kRing, "the warps' sums are exchanged where the ring was");
+};
+
+// 16-byte piece c of a tile's row r: where it lies in the row.
+template <int D>
+__device__ __forceinline__ int swizzled(int r, int c) {
+    return D == 128 ? c ^ ((r >> 1) & 3) : c ^ ((r >> 2) & 1);
+}
+
+// The first unit of each request (s_first[B]: all units), by the whole CTA.
+__device__ __forceinline__ void plan_units(const AttnArgs &a, int rows_at_once, int *s_first, int *s_warp) {
+    int before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        int units = 0;
+        if (b < a.B) {
+            const AttnRequest r = attn_request(a, b);
+            const int tiles = (int)(((int64_t)r.n * a.G + rows_at_once - 1) / rows_at_once);
+            const int64_t want = (int64_t)a.Hk * tiles * max(1, (r.len - r.lo + kAttnChunk - 1) / kAttnChunk);
+            // all requests together stay within 32 bits
+            units = want <= INT32_MAX / a.B ? (int)want : 0;
+            if ((r.bad || units != want) && blockIdx.x == 0 && a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
+        }
+        int v = units;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += x;
+        }
+        __syncthreads();
+        if (lane == 31) s_warp[warp] = v;
+        __syncthreads();
+        int sum = before;
+        for (int w = 0; w < kAttnWarps; ++w) {
+            if (w < warp) v += s_warp[w];
+            sum += s_warp[w];
+        }
+        if (b < a.B) s_first[b] = before + v - units;
+        before = sum;
+    }
+    if (threadIdx.x == 0) s_first[a.B] = before;
+    __syncthreads();
+}
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(const AttnArgs a) {
+    using S = Shape<D, NQ>;
+    constexpr int kBlocks = S::kBlocks;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int s_warp[kAttnWarps];
+    uint2 *s_q = reinterpret_cast<uint2 *>(smem + S::kRing);                 // [k step][8 rows][lane]
+    float *s_mult = reinterpret_cast<float *>(smem + S::kRing + S::kQBytes);   // [rows]
+    float *s_top = s_mult + S::kRows, *s_sum = s_top + kAttnWarps * S::kRows;  // [warp][rows]
+    int *s_first = reinterpret_cast<int *>(smem + S::kSmem);                 // [requests + 1]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    ptx::pdl_launch_dependents();
+    ptx::pdl_wait();
+    plan_units(a, S::kRows, s_first, s_warp);
+    const int all = s_first[a.B], per = max(1, (all + (int)gridDim.x - 1) / (int)gridDim.x);
+    if (blockIdx.x == 0) {
+        for (int b = tid; b <= a.B; b += kThreads) a.plan[b] = s_first[b];
+        if (tid == 0) a.plan[a.B + 1] = per;
+    }
+    int u = min(all, (int)blockIdx.x * per);
+    const int u_end = min(all, u + per);
+    uint8_t *ring = smem + warp * S::kStages * S::kStage;
+    const uint32_t ring_addr = ptx::smem_u32(ring);
+
+    while (u < u_end) {
+        // ---- the piece: request b, KV head h, row group qt, units c0 .. c1-1 of `chunks`
+        int lo_b = 0, hi_b = a.B;
+        while (hi_b - lo_b > 1) {
+            const int mid = (lo_b + hi_b) >> 1;
+            if (s_first[mid] <= u) lo_b = mid;
+            else hi_b = mid;
+        }
+        const int b = lo_b;
+        const AttnRequest r = attn_request(a, b);
+        const int chunks = max(1, (r.len - r.lo + kAttnChunk - 1) / kAttnChunk);
+        const int tiles_q = (int)(((int64_t)r.n * a.G + S::kRows - 1) / S::kRows);
+        const int local = u - s_first[b], piece = local / chunks, c0 = local - piece * chunks;
+        const int c1 = min(chunks, c0 + u_end - u);
+        const int h = piece / tiles_q, qt = piece - h * tiles_q;
+        u += c1 - c0;
+        const int pos0 = r.len - r.n;                     // position of the request's first row
+        const int rowbase = qt * S::kRows;                // (query token, head) rows, token-major
+        const int nrows = min(S::kRows, r.n * a.G - rowbase);
+        const int pos_lo = pos0 + rowbase / a.G, pos_hi = pos0 + (rowbase + nrows - 1) / a.G;
+        const int t_end = min(r.lo + c1 * kAttnChunk, pos_hi + 1);   // tokens seen by any of these rows
+        const int t_begin = r.lo + c0 * kAttnChunk;
+
+        // ---- this warp's tiles: t_begin + 16 (warp + 8 i)
+        const int first_tile = t_begin + warp * kAttnTile;
+        const int ntiles = first_tile < t_end ? (t_end - first_tile + kAttnChunk - 1) / kAttnChunk : 0;
+        int ids = -1;   // lane i: the page of the warp's tile 32 k + i
+        auto load_ids = [&](int i0) {
+            const int64_t t = first_tile + (int64_t)(i0 + lane) * kAttnChunk;
+            ids = -1;
+            if (t < t_end) {
+                ids = a.table[(int64_t)b * a.max_pages + (t >> a.page_shift)];
+                if (ids < 0 || ids >= a.pages) {
+                    if (a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
+                    ids = -1;
+                }
+            }
+        };
+        // Copies tile i into its slot of the ring; a page that is not there
+        // leaves the slot as it is (its tokens are not seen).
+        auto fetch = [&](int i) {
+            if (i < ntiles) {
+                if ((i & 31) == 0) load_ids(i);
+                const int id = __shfl_sync(0xffffffffu, ids, i & 31);
+                if (id >= 0) {
+                    const int t = first_tile + i * kAttnChunk;
+                    const int64_t page_row = ((int64_t)id * 2 * a.Hk + h) << a.page_shift;
+                    const int64_t row = page_row + (t & ((1 << a.page_shift) - 1));
+                    const int64_t kv = (int64_t)a.Hk << a.page_shift;   // rows from keys to values
+                    const uint32_t slot = ring_addr + (i % S::kStages) * S::kStage;
+                    constexpr int kPieces = S::kCodes / 16, kInRow = S::kRow / 16;
+#pragma unroll
+                    for (int j = 0; j < 2 * kPieces; j += 32) {
+                        const int p = j + lane, v = p / kPieces, q = p % kPieces;
+                        const int tr = q / kInRow, tc = q % kInRow;
+                        cp_async16(slot + v * S::kCodes + tr * S::kRow + swizzled<D>(tr, tc) * 16,
+                                   a.codes + (row + v * kv) * S::kRow + q * 16);
+                    }
+                    constexpr int kScalePieces = S::kScales / 16;
+                    if (lane < 2 * kScalePieces) {
+                        const int v = lane / kScalePieces, q = lane % kScalePieces;
+                        cp_async16(slot + 2 * S::kCodes + v * S::kScales + q * 16,
+                                   a.scales + (row + v * kv) * kBlocks + q * 16);
+                    }
+                }
+            }
+            cp_async_commit();
+        };
+        int seen_id = -1;   // as `ids`, for the tile that is computed
+#pragma unroll
+        for (int i = 0; i < S::kStages - 1; ++i) fetch(i);
+
+        // ---- queries: fp16 in the order of the products, a power of two for each row
+        for (int rr = warp; rr < S::kRows; rr += kAttnWarps) {
+            float v[D / 32];
+            float amax = 0.0f;
+            const bool there = rr < nrows;
+            const int row = rowbase + rr;
+            if (there) {
+                const int64_t at = ((int64_t)(r.row0 + row / a.G) * a.Hq + h * a.G + row % a.G) * D;
+                if (D == 128) {
+                    const uint2 w = reinterpret_cast<const uint2 *>(a.q + at)[lane];
+                    v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
+                    v[2 % (D / 32)] = __uint_as_float(w.y << 16), v[3 % (D / 32)] = __uint_as_float(w.y & 0xffff0000u);
+                } else {
+                    const uint32_t w = reinterpret_cast<const uint32_t *>(a.q + at)[lane];
+                    v[0] = __uint_as_float(w << 16), v[1] = __uint_as_float(w & 0xffff0000u);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) v[j] = 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) amax = fmaxf(amax, fabsf(v[j]));
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            // amax 2^up in [2^14, 2^15); the exponent is held where 2^up is a number
+            const int ex = (int)(__float_as_uint(amax) >> 23);
+            const int up = 14 + 127 - min(max(ex, 27), 254);
+            const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) v[j] *= f;
+            if (lane == 0) s_mult[rr] = a.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
+            // Channel 32 b + 8 c + 4 s + {0,1 | 2,3} of row (nq, g) is word {0 | 1} of
+            // lane (g, c) in step 2 b + s
+            const int nq = rr >> 3, lg = rr & 7;
+            uint32_t *dst = reinterpret_cast<uint32_t *>(s_q);
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                const int ch = lane * (D / 32) + 2 * j;
+                const int blk = ch >> 5, cc = (ch >> 3) & 3, st = (ch >> 2) & 1, word = (ch >> 1) & 1;
+                dst[(((2 * blk + st) * NQ + nq) * 32 + lg * 4 + cc) * 2 + word] = half2_bits(v[2 * j], v[2 * j + 1]);
+            }
+        }
+        __syncthreads();
+
+        // ---- the pass over the tokens
+        uint2 qf[NQ <= 2 ? D / 16 : 1][NQ];
+        if (NQ <= 2)
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) qf[k][n] = s_q[(k * NQ + n) * 32 + lane];
+        float mult[NQ][2], top[NQ][2], sum[NQ][2];
+        int last[NQ][2];   // position of this lane's two rows (columns of the products)
+        float o[2 * kBlocks][NQ][4];
+        uint32_t vbias[kBlocks];   // kVBias + 15 - E in both halves
+        int vmax[kBlocks];         // E
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int rr = 8 * n + 2 * c + j;
+                mult[n][j] = s_mult[rr];
+                top[n][j] = -INFINITY;
+                sum[n][j] = 0.0f;
+                last[n][j] = pos0 + (rowbase + min(rr, nrows - 1)) / a.G;
+            }
+#pragma unroll
+        for (int m = 0; m < 2 * kBlocks; ++m)
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[m][n][j] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k) vmax[k] = 0, vbias[k] = (uint32_t)(15 + kVBias) * 0x10001u;
+        // ldmatrix rows of this lane: row lane % 8 (+ 8 for the odd matrices) of pieces
+        // (blocks) 2 x + lane / 16
+        const int mrow = (lane & 7) + ((lane >> 3) & 1) * 8, mblk = lane >> 4;
+
+        for (int i = 0; i < ntiles; ++i) {
+            // ids moves on to the next 32 tiles while up to kStages - 1 of the old
+            // ones are still to be computed: validity is kept apart
+            if ((i & 31) == 0) {
+                const int64_t t = first_tile + (int64_t)(i + lane) * kAttnChunk;
+                seen_id = t < t_end ? a.table[(int64_t)b * a.max_pages + (t >> a.page_shift)] : -1;
+            }
+            cp_async_wait<S::kStages - 2>();
+            __syncwarp();
+            fetch(i + S::kStages - 1);   // into the slot of the tile before
+            const int id = __shfl_sync(0xffffffffu, seen_id, i & 31);
+            if (id < 0 || id >= a.pages) continue;
+            const int t0 = first_tile + i * kAttnChunk;
+            const uint32_t slot = ring_addr + (i % S::kStages) * S::kStage;
+            const uint8_t *sc = ring + (i % S::kStages) * S::kStage + 2 * S::kCodes;
+            // S^T = K Q^T
+            float s[NQ][4];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[n][j] = 0.0f;
+            uint32_t ks0, ks1;   // scale bytes of tokens g and g + 8
+            if (kBlocks == 4) {
+                ks0 = reinterpret_cast<const uint32_t *>(sc)[g];
+                ks1 = reinterpret_cast<const uint32_t *>(sc)[g + 8];
+            } else {
+                ks0 = reinterpret_cast<const uint16_t *>(sc)[g];
+                ks1 = reinterpret_cast<const uint16_t *>(sc)[g + 8];
+            }
+#pragma unroll
+            for (int x = 0; x < kBlocks / 2; ++x) {
+                uint32_t w[4];   // tokens 0-7 and 8-15 of block 2 x, then of block 2 x + 1
+                ldm4(slot + mrow * S::kRow + swizzled<D>(mrow, 2 * x + mblk) * 16, w);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int k = 2 * x + y;
+                    uint32_t k0[4], k1[4];
+                    mx4_half8(w[2 * y], k0);
+                    mx4_half8(w[2 * y + 1], k1);
+                    // 2^(byte - 127); byte 0 (2^-127) counts as zero, 255 as infinity: its
+                    // codes are zero, and zero times it NaN
+                    const float f0 = __uint_as_float((ks0 >> (8 * k) & 0xffu) << 23);
+                    const float f1 = __uint_as_float((ks1 >> (8 * k) & 0xffu) << 23);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        const uint2 qa = NQ <= 2 ? qf[NQ <= 2 ? 2 * k : 0][n] : s_q[(2 * k * NQ + n) * 32 + lane];
+                        const uint2 qb = NQ <= 2 ? qf[NQ <= 2 ? 2 * k + 1 : 0][n]
+                                                 : s_q[((2 * k + 1) * NQ + n) * 32 + lane];
+                        mma16816(d, k0[0], k1[0], k0[1], k1[1], qa.x, qa.y);
+                        mma16816(d, k0[2], k1[2], k0[3], k1[3], qb.x, qb.y);
+                        s[n][0] = fmaf(d[0], f0, s[n][0]);
+                        s[n][1] = fmaf(d[1], f0, s[n][1]);
+                        s[n][2] = fmaf(d[2], f1, s[n][2]);
+                        s[n][3] = fmaf(d[3], f1, s[n][3]);
+                    }
+                }
+            }
+            // scale and mask; rows: tokens t0 + g and t0 + g + 8
+            const bool edge = t0 + kAttnTile - 1 > pos_lo || (a.window && t0 <= pos_hi - a.window);
+            bool over = false;
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float v = s[n][j] * mult[n][j & 1];
+                    if (edge) {
+                        const int t = t0 + g + (j >> 1) * 8, p = last[n][j & 1];
+                        if (t > p || (a.window && t <= p - a.window)) v = -INFINITY;
+                    }
+                    s[n][j] = v;
+                    over |= v > top[n][j & 1] + kLazy;
+                }
+            if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float v = fmaxf(s[n][j], s[n][j + 2]);
+#pragma unroll
+                        for (int x = 4; x <= 16; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
+                        v = fmaxf(v, top[n][j]);
+                        const float f = v == top[n][j] ? 1.0f : ex2(top[n][j] - v);
+                        top[n][j] = v;
+                        sum[n][j] *= f;
+#pragma unroll
+                        for (int m = 0; m < 2 * kBlocks; ++m) o[m][n][j] *= f, o[m][n][j + 2] *= f;
+                    }
+            }
+            // P^T, transposed into the order of the second product
+            uint32_t pt[NQ][2];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                float p[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float m = top[n][j & 1];
+                    p[j] = ex2(s[n][j] - (m == -INFINITY ? 0.0f : m));
+                    sum[n][j & 1] += p[j];
+                }
+                pt[n][0] = transposed8(half2_bits(p[0], p[1]));
+                pt[n][1] = transposed8(half2_bits(p[2], p[3]));
+            }
+            // the values' scales of tokens 2c, 2c+1 and 2c+8, 2c+9, for each block
+            const uint8_t *sv = sc + S::kScales;
+            uint32_t e[kBlocks][2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                uint32_t w0, w1;
+                if (kBlocks == 4) {
+                    const uint2 w = reinterpret_cast<const uint2 *>(sv)[c + 4 * x];
+                    w0 = w.x, w1 = w.y;
+                } else {
+                    w0 = reinterpret_cast<const uint32_t *>(sv)[c + 4 * x];
+                    w1 = w0 >> 16;
+                }
+                if (edge) {   // what no row sees, written to or not
+                    const int t = t0 + 2 * c + 8 * x, seen = a.window ? pos_lo - a.window : -1;
+                    if (t > pos_hi || t <= seen) w0 = 0;
+                    if (t + 1 > pos_hi || t + 1 <= seen) w1 = 0;
+                }
+#pragma unroll
+                for (int k = 0; k < kBlocks; ++k)
+                    e[k][x] = __byte_perm(w0, w1, k | (k + 4) << 8) & 0x00ff00ffu;
+            }
+            bool grown = false, nans = false;   // nans: a value that is NaN, in this tile
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k) {
+                const uint32_t m = __vmaxs2(e[k][0], e[k][1]);
+                grown |= max((int)(m & 0xffffu), (int)(m >> 16)) > vmax[k];
+            }
+            if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+                for (int k = 0; k < kBlocks; ++k) {
+                    int v = vmax[k];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t lo = e[k][x] & 0xffffu, hi = e[k][x] >> 16;
+                        if (lo == 255u) nans = true, lo = kNan;
+                        else v = max(v, (int)lo);
+                        if (hi == 255u) nans = true, hi = kNan;
+                        else v = max(v, (int)hi);
+                        e[k][x] = lo | hi << 16;
+                    }
+                    v = max(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                    v = max(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                    if (v != vmax[k]) {
+                        const float f = ex2((float)(vmax[k] - v));
+                        vmax[k] = v;
+                        vbias[k] = (uint32_t)((15 + kVBias - v) & 0xffff) * 0x10001u;
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) o[2 * k][n][j] *= f, o[2 * k + 1][n][j] *= f;
+                    }
+                }
+            }
+            // O^T += V^T P^T
+#pragma unroll
+            for (int x = 0; x < kBlocks / 2; ++x) {
+                uint32_t w[4];
+                ldm4_trans(slot + S::kCodes + mrow * S::kRow + swizzled<D>(mrow, 2 * x + mblk) * 16, w);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int k = 2 * x + y;
+                    // codes of channels 4g .. 4g+3 of block k: of token 2c in the low half
+                    // of the word, of token 2c + 1 in the high half (+ 8 in the second word)
+                    uint32_t v0[4], v1[4];
+                    mx4_half8(w[2 * y], v0);
+                    mx4_half8(w[2 * y + 1], v1);
+                    const uint32_t f0 = __viaddmax_s16x2_relu(e[k][0], vbias[k], 0u) << 10;
+                    const uint32_t f1 = __viaddmax_s16x2_relu(e[k][1], vbias[k], 0u) << 10;
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        uint32_t b0 = mul_half2(pt[n][0], f0), b1 = mul_half2(pt[n][1], f1);
+                        if (nans) {   // NaN for the rows that see it
+                            b0 = with_nans(b0, pt[n][0], e[k][0]);
+                            b1 = with_nans(b1, pt[n][1], e[k][1]);
+                        }
+                        mma16816(o[2 * k][n], __byte_perm(v0[0], v0[2], 0x5410), __byte_perm(v0[0], v0[2], 0x7632),
+                                 __byte_perm(v1[0], v1[2], 0x5410), __byte_perm(v1[0], v1[2], 0x7632), b0, b1);
+                        mma16816(o[2 * k + 1][n], __byte_perm(v0[1], v0[3], 0x5410),
+                                 __byte_perm(v0[1], v0[3], 0x7632), __byte_perm(v1[1], v1[3], 0x5410),
+                                 __byte_perm(v1[1], v1[3], 0x7632), b0, b1);
+                    }
+                }
+            }
+        }
+
+        // ---- the warps' results together
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int x = 4; x <= 16; x <<= 1) sum[n][j] += __shfl_xor_sync(0xffffffffu, sum[n][j], x);
+                if (g == 0) {
+                    s_top[warp * S::kRows + 8 * n + 2 * c + j] = top[n][j];
+                    s_sum[warp * S::kRows + 8 * n + 2 * c + j] = sum[n][j];
+                }
+            }
+        cp_async_wait<0>();
+        __syncthreads();   // the ring is free, and the maxima are there
+        const bool whole = c0 == 0 && c1 == chunks;
+        float *part = a.part + (int64_t)(2 * blockIdx.x + (c0 == 0 ? 1 : 0)) * S::kRows * (D + 2);
+        float *s_o = reinterpret_cast<float *>(smem);   // [warp][8 rows][D]
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int rr = 8 * n + 2 * c + j;
+                float m = s_top[rr];
+#pragma unroll
+                for (int w = 1; w < kAttnWarps; ++w) m = fmaxf(m, s_top[w * S::kRows + rr]);
+                const float f = top[n][j] == m ? 1.0f : ex2(top[n][j] - m);
+#pragma unroll
+                for (int k = 0; k < kBlocks; ++k) {
+                    // 2^(E - 127 - kVBias)
+                    const float fe = f * (mx4_scale((uint32_t)vmax[k]) * exp2f(-kVBias));
+                    *reinterpret_cast<float4 *>(s_o + ((warp * 8 + 2 * c + j) * D + 32 * k + 4 * g)) =
+                        make_float4(o[2 * k][n][j] * fe, o[2 * k][n][j + 2] * fe, o[2 * k + 1][n][j] * fe,
+                                    o[2 * k + 1][n][j + 2] * fe);
+                }
+            }
+            __syncthreads();
+            for (int x = tid; x < 8 * D / 4; x += kThreads) {
+                const int rr = 8 * n + x / (D / 4), col = x % (D / 4) * 4;
+                float m = s_top[rr], l = 0.0f;
+#pragma unroll
+                for (int w = 1; w < kAttnWarps; ++w) m = fmaxf(m, s_top[w * S::kRows + rr]);
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < kAttnWarps; ++w) {
+                    const float tw = s_top[w * S::kRows + rr];
+                    l += s_sum[w * S::kRows + rr] * (tw == m ? 1.0f : ex2(tw - m));
+                    const float4 y = *reinterpret_cast<const float4 *>(s_o + (w * 8 + x / (D / 4)) * D + col);
+                    v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+                }
+                if (!whole) {
+                    *reinterpret_cast<float4 *>(part + rr * D + col) = v;
+                    if (col == 0) part[S::kRows * D + rr] = m, part[S::kRows * (D + 1) + rr] = l;
+                } else if (rr < nrows) {
+                    const int row = rowbase + rr;
+                    const int64_t at = (int64_t)(r.row0 + row / a.G) * a.Hq + h * a.G + row % a.G;
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // a row that sees nothing
+                    if (a.out_bf16) {
+                        const __nv_bfloat162 y0 = __floats2bfloat162_rn(v.x * inv, v.y * inv);
+                        const __nv_bfloat162 y1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at * D + col) =
+                            make_uint2(*reinterpret_cast<const uint32_t *>(&y0), *reinterpret_cast<const uint32_t *>(&y1));
+                    } else {
+                        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at * D + col) =
+                            make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                    }
+                    if (a.lse && col == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// Joins the pieces of rows that were cut: one warp a query row and head.
+template <int D>
+__global__ void __launch_bounds__(256) attention4_join_kernel(const AttnArgs a, int rows_at_once) {
+    ptx::pdl_launch_dependents();
+    ptx::pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    if (i >= (int64_t)a.rows * a.Hq) return;
+    const int row = (int)(i / a.Hq), head = (int)(i - (int64_t)row * a.Hq);
+    // the request that the row belongs to, if any
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.starts[mid] <= row) lo = mid;
+        else hi = mid;
+    }
+    const AttnRequest r = attn_request(a, lo);
+    if (row < r.row0 || row >= r.row0 + r.n || a.plan[lo] == a.plan[lo + 1]) return;
+    const int per = a.plan[a.B + 1];
+    const int chunks = max(1, (r.len - r.lo + kAttnChunk - 1) / kAttnChunk);
+    const int tiles_q = (int)(((int64_t)r.n * a.G + rows_at_once - 1) / rows_at_once);
+    const int h = head / a.G, flat = (row - r.row0) * a.G + head % a.G;
+    const int qt = flat / rows_at_once, rr = flat - qt * rows_at_once;
+    const int u0 = a.plan[lo] + (h * tiles_q + qt) * chunks;
+    const int k0 = u0 / per, k1 = (u0 + chunks - 1) / per;
+    if (k0 == k1) return;   // one CTA had all of it
+    const int64_t size = (int64_t)rows_at_once * (D + 2);
+    float m = -INFINITY;
+    for (int k = k0 + lane; k <= k1; k += 32)
+        m = fmaxf(m, a.part[(2 * k + (k == k0)) * size + rows_at_once * D + rr]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.0f;
+    float v[D / 32];
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) v[j] = 0.0f;
+#pragma unroll 4
+    for (int k = k0; k <= k1; ++k) {
+        const float *p = a.part + (2 * k + (k == k0)) * size;
+        const float top = p[rows_at_once * D + rr];
+        const float f = top == m ? 1.0f : ex2(top - m);
+        l += f * p[rows_at_once * (D + 1) + rr];
+        if (D == 128) {
+            const float4 y = reinterpret_cast<const float4 *>(p + rr * D)[lane];
+            v[0] += f * y.x, v[1] += f * y.y, v[2 % (D / 32)] += f * y.z, v[3 % (D / 32)] += f * y.w;
+        } else {
+            const float2 y = reinterpret_cast<const float2 *>(p + rr * D)[lane];
+            v[0] += f * y.x, v[1] += f * y.y;
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int j = 0; j < D / 32; j += 2) {
+        const int64_t at = i * D + lane * (D / 32) + j;
+        if (a.out_bf16)
+            *reinterpret_cast<__nv_bfloat162 *>(static_cast<uint16_t *>(a.out) + at) =
+                __floats2bfloat162_rn(v[j] * inv, v[j + 1] * inv);
+        else *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + at) = make_float2(v[j] * inv, v[j + 1] * inv);
+    }
+    if (a.lse && lane == 0) a.lse[i] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
+}
+
+// Groups of eight rows that a warp takes at once: as many as the largest request
+// needs for its rows, four at most.
+int rows8(const moe_cache_attn *d, const moe_cache4 *cache) {
+    const int64_t rows = (int64_t)std::max(1, d->max_q) * (d->q_heads / cache->kv_heads);
+    return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+}
+
+template <int D, int NQ>
+int launch(const AttnArgs &a0, cudaStream_t s) {
+    using S = Shape<D, NQ>;
+    AttnArgs a = a0;
+    const int smem = S::kSmem + (a.B + 1) * 4;
+    MOE_CUDA_TRY(cudaFuncSetAttribute(attention4_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    if (int rc = launch_dependent(attention4_kernel<D, NQ>, dim3(a.ctas), dim3(kThreads), smem, s, (const AttnArgs)a))
+        return rc;
+    const int64_t warps = (int64_t)a.rows * a.Hq;
+    return launch_dependent(attention4_join_kernel<D>, dim3((unsigned)ceil_div(warps, 8)), dim3(256), 0, s,
+                            (const AttnArgs)a, (int)S::kRows);
+}
+
+int ctas_of(int nq) { return sm_count() * (nq == 4 ? 1 : 2); }
+
+}  // namespace
+
+size_t attention4_plan_bytes(const moe_cache_attn *d) { return align_up(sizeof(int32_t) * (d->requests + 2)); }
+
+size_t attention4_workspace(const moe_cache_attn *d, const moe_cache4 *cache) {
+    const int nq = rows8(d, cache);
+    return attention4_plan_bytes(d) + align_up(sizeof(float) * 2 * (size_t)ctas_of(nq) * 8 * nq * (cache->dim + 2));
+}
+
+int launch_attention4(const moe_cache_attn *d, const moe_cache4 *cache, const void *q, const int32_t *table,
+                      const int32_t *lengths, const int32_t *starts, void *out, int out_dtype, float *lse,
+                      void *ws, int32_t *status, cudaStream_t s) {
+    AttnArgs a;
+    a.q = static_cast<const uint16_t *>(q);
+    a.codes = static_cast<const uint8_t *>(cache->codes);
+    a.scales = static_cast<const uint8_t *>(cache->scales);
+    a.table = table;
+    a.lengths = lengths;
+    a.starts = starts;
+    a.out = out;
+    a.lse = lse;
+    a.status = status;
+    a.plan = static_cast<int32_t *>(ws);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + attention4_plan_bytes(d));
+    a.B = d->requests;
+    a.rows = d->rows;
+    a.Hq = d->q_heads;
+    a.Hk = cache->kv_heads;
+    a.G = a.Hq / a.Hk;
+    a.max_pages = d->max_pages;
+    a.pages = cache->pages;
+    a.page_shift = 0;
+    while ((1 << a.page_shift) < cache->page) ++a.page_shift;
+    a.window = d->window;
+    a.out_bf16 = out_dtype == MOE_OUT_BF16;
+    a.scale_log2 = d->scale * 1.44269504f;
+    const int nq = rows8(d, cache);
+    a.ctas = ctas_of(nq);
+    if (cache->dim == 64) return nq == 1 ? launch<64, 1>(a, s) : nq == 2 ? launch<64, 2>(a, s) : launch<64, 4>(a, s);
+    return nq == 1 ? launch<128, 1>(a, s) : nq == 2 ? launch<128, 2>(a, s) : launch<128, 4>(a, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,50 @@
+// What the attention kernels over the four-bit cache share: the work list of a
+// call, and where the results of a piece of a request are kept.
+#pragma once
+
+#include <stdint.h>
+
+#include "internal.h"
+
+namespace moe {
+
+constexpr int kAttnMaxRequests = 4096;
+constexpr int kAttnTile = 16;      // tokens of a tile
+constexpr int kAttnWarps = 8;
+constexpr int kAttnChunk = kAttnTile * kAttnWarps;   // tokens of a unit of work
+
+struct AttnArgs {
+    const uint16_t *q;
+    const uint8_t *codes, *scales;
+    const int32_t *table, *lengths, *starts;
+    void *out;
+    float *lse;
+    int32_t *status;
+    // partial results, two to a CTA: weighted sums [rows, D], then top and sum of each row
+    float *part;
+    int32_t *plan;   // [requests + 1]: first unit of each request, then units a CTA
+    int B, rows, Hq, Hk, G, max_pages, pages, page_shift, window, out_bf16, ctas;
+    float scale_log2;
+};
+
+// Request b of the call: its query rows and the tokens that they see.
+struct AttnRequest {
+    int row0, n, len;      // n = 0 where there is nothing to compute
+    int lo;                // first token seen by any row, a multiple of the tile
+    bool bad;
+};
+
+__device__ __forceinline__ AttnRequest attn_request(const AttnArgs &a, int b) {
+    AttnRequest r;
+    r.row0 = a.starts[b];
+    const int end = a.starts[b + 1];
+    r.len = a.lengths[b];
+    r.bad = r.row0 < 0 || end < r.row0 || end > a.rows || r.len < 0 ||
+            r.len > (int64_t)a.max_pages << a.page_shift || r.len > INT32_MAX - 1024;
+    r.n = r.bad ? 0 : end - r.row0;
+    const int first = r.len - r.n;   // position of the first row; may be negative
+    r.lo = a.window && first >= a.window ? (first - a.window + 1) / kAttnTile * kAttnTile : 0;
+    return r;
+}
+
+}  // namespace moe

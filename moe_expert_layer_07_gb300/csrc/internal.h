@@ -136,6 +136,26 @@ int launch_block_norm(const moe_norm *d, int T, const void *y, const void *resid
                       const void *w_pre, const void *b_pre, void *residual_out, void *x_out,
                       cudaStream_t s);
 
+// The cache in four bits (cache.cu), what comes before its attention (qk_rope.cu),
+// attention (attention4.cu) and products with four-bit weights (matvec4.cu)
+int launch_cache_tables(int B, int page, const int32_t *held, const int32_t *fresh,
+                        const int32_t *free_pages, int free_count, const int64_t *free_range,
+                        int32_t *table, int max_pages, int32_t *lengths, int32_t *starts,
+                        int32_t *slots, int32_t *positions, int max_tokens, int64_t *free_out,
+                        int32_t *status, cudaStream_t s);
+int launch_cache_read(const moe_cache4 *cache, int n, const int32_t *slots, void *k, void *v,
+                      int32_t *status, cudaStream_t s);
+int launch_qk_norm_rope(const moe_qk_rope *d, int T, const void *qkv, const int32_t *positions,
+                        const float *cos_sin, const void *w_q, const void *w_k, void *q_out,
+                        void *k_out, const moe_cache4 *cache, const int32_t *slots, int32_t *status,
+                        cudaStream_t s);
+size_t attention4_workspace(const moe_cache_attn *d, const moe_cache4 *cache);
+int launch_attention4(const moe_cache_attn *d, const moe_cache4 *cache, const void *q, const int32_t *table,
+                      const int32_t *lengths, const int32_t *starts, void *out, int out_dtype, float *lse,
+                      void *ws, int32_t *status, cudaStream_t s);
+int launch_w4_matvec(const moe_w4 *d, int T, const void *x, const void *codes, const void *scales,
+                     const void *zeros, void *y, int out_dtype, cudaStream_t s);
+
 // Programmatic dependent launch: `kernel` may start while the previous
 // kernel in the stream drains.  Every CTA of such a kernel executes
 // pdl_wait() (griddepcontrol.wait) before it reads data that an earlier
