@@ -42,6 +42,9 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = kAttnWarps * 32;
+// What the beginning and end of a piece cost, in units: queries, the first tiles'
+// way from memory, the warps' sums.
+constexpr int kPieceUnits = 4;
 constexpr float kLazy = 8.0f;      // how far scores may pass the maximum
 constexpr int kVBias = 7;          // P is scaled by 2^(e - E + kVBias)
 
@@ -83,6 +86,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// d = the product alone
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
@@ -93,14 +104,33 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
 }
 
 // Stands for the scale byte 255 (NaN) in a half word: very small, so that it
-// scales to zero, and known again by with_nans.
+// scales to zero, and known again by sees_nan.
 constexpr uint32_t kNan = 0x8000u;
 
-// P times a scale, NaN where the scale is and P is not zero.
-__device__ __noinline__ uint32_t with_nans(uint32_t scaled, uint32_t p, uint32_t e) {
-    if ((e & 0xffffu) == kNan && (p & 0x7fffu)) scaled |= 0x7fffu;
-    if (e >> 16 == kNan && (p & 0x7fff0000u)) scaled |= 0x7fff0000u;
-    return scaled;
+// Whether a pair of probabilities gives weight to a value that is NaN.
+__device__ __forceinline__ bool sees_nan(uint32_t p, uint32_t e) {
+    return ((e & 0xffffu) == kNan && (p & 0x7fffu)) || (e >> 16 == kNan && (p & 0x7fff0000u));
+}
+
+// N words of shared memory, as bits or as floats.
+__device__ __forceinline__ void put(uint32_t &v, uint32_t w) { v = w; }
+__device__ __forceinline__ void put(float &v, uint32_t w) { v = __uint_as_float(w); }
+template <int N, typename T>
+__device__ __forceinline__ void load_blocks(T (&v)[N], const T *p) {
+    if (N == 4) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(p);
+        put(v[0], w.x), put(v[1], w.y), put(v[2 % N], w.z), put(v[3 % N], w.w);
+    } else {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p);
+        put(v[0], w.x), put(v[1], w.y);
+    }
+}
+
+// A word of eight codes, of channels 0 .. 3 for one token and for the next, in the
+// order that gives pairs of tokens: channels 0, 2, 1, 3.
+__device__ __forceinline__ uint32_t token_pairs(uint32_t w) {
+    const uint32_t x = (w ^ (w >> 12)) & 0x0000f0f0u;
+    return w ^ x ^ (x << 12);
 }
 
 template <int D, int NQ>
@@ -110,18 +140,22 @@ struct Shape {
     static constexpr int kCodes = kAttnTile * kRow;     // of a tile's keys or values
     static constexpr int kScales = kAttnTile * kBlocks;
     static constexpr int kStage = 2 * (kCodes + kScales);
-    static constexpr int kStages = D == 128 ? 4 : 6;
+    static constexpr int kStages = D == 128 ? 4 : 8;
     static constexpr int kRows = 8 * NQ;
     static constexpr int kRing = kAttnWarps * kStages * kStage;
     // queries in the order of the products, then what rows and warps exchange
     static constexpr int kQBytes = D / 16 * NQ * 32 * 8;
-    static constexpr int kSmem = kRing + kQBytes + (kRows + 2 * kAttnWarps * kRows) * 4;
+    // a warp's scales of a tile: the keys' in fp32, the values' (and what is NaN of
+    // them) for pairs of tokens
+    static constexpr int kScaleBytes = kAttnTile * kBlocks * 4 + 2 * (kAttnTile / 2) * kBlocks * 4;
+    static constexpr int kScaleAt = kRing + kQBytes;
+    static constexpr int kSmem = kScaleAt + kAttnWarps * kScaleBytes + (kRows + 2 * kAttnWarps * kRows) * 4;
     static_assert(kAttnWarps * 8 * D * 4 <= kRing, "the warps' sums are exchanged where the ring was");
 };
 
 // 16-byte piece c of a tile's row r: where it lies in the row.
 template <int D>
-__device__ __forceinline__ int swizzled(int r, int c) {
+__host__ __device__ constexpr int swizzled(int r, int c) {
     return D == 128 ? c ^ ((r >> 1) & 3) : c ^ ((r >> 2) & 1);
 }
 
@@ -134,7 +168,7 @@ __device__ __forceinline__ void plan_units(const AttnArgs &a, int rows_at_once, 
         if (b < a.B) {
             const AttnRequest r = attn_request(a, b);
             const int tiles = (int)(((int64_t)r.n * a.G + rows_at_once - 1) / rows_at_once);
-            const int64_t want = (int64_t)a.Hk * tiles * max(1, (r.len - r.lo + kAttnChunk - 1) / kAttnChunk);
+            const int64_t want = (int64_t)a.Hk * tiles * (attn_chunks(r) + kPieceUnits);
             // all requests together stay within 32 bits
             units = want <= INT32_MAX / a.B ? (int)want : 0;
             if ((r.bad || units != want) && blockIdx.x == 0 && a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
@@ -168,7 +202,10 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_warp[kAttnWarps];
     uint2 *s_q = reinterpret_cast<uint2 *>(smem + S::kRing);                 // [k step][8 rows][lane]
-    float *s_mult = reinterpret_cast<float *>(smem + S::kRing + S::kQBytes);   // [rows]
+    float *s_ks = reinterpret_cast<float *>(smem + S::kScaleAt + (threadIdx.x >> 5) * S::kScaleBytes);   // [token][block]
+    uint32_t *s_vs = reinterpret_cast<uint32_t *>(s_ks) + kAttnTile * kBlocks;                           // [pair][block]
+    uint32_t *s_ve = s_vs + kAttnTile / 2 * kBlocks;
+    float *s_mult = reinterpret_cast<float *>(smem + S::kScaleAt + kAttnWarps * S::kScaleBytes);   // [rows]
     float *s_top = s_mult + S::kRows, *s_sum = s_top + kAttnWarps * S::kRows;  // [warp][rows]
     int *s_first = reinterpret_cast<int *>(smem + S::kSmem);                 // [requests + 1]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
@@ -195,12 +232,14 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
         }
         const int b = lo_b;
         const AttnRequest r = attn_request(a, b);
-        const int chunks = max(1, (r.len - r.lo + kAttnChunk - 1) / kAttnChunk);
+        const int chunks = attn_chunks(r);
         const int tiles_q = (int)(((int64_t)r.n * a.G + S::kRows - 1) / S::kRows);
-        const int local = u - s_first[b], piece = local / chunks, c0 = local - piece * chunks;
-        const int c1 = min(chunks, c0 + u_end - u);
+        const int local = u - s_first[b], piece = local / (chunks + kPieceUnits);
+        const int x0 = local - piece * (chunks + kPieceUnits), x1 = min(chunks + kPieceUnits, x0 + u_end - u);
+        const int c0 = max(0, x0 - kPieceUnits), c1 = max(0, x1 - kPieceUnits);
         const int h = piece / tiles_q, qt = piece - h * tiles_q;
-        u += c1 - c0;
+        u += x1 - x0;
+        if (c0 == c1) continue;
         const int pos0 = r.len - r.n;                     // position of the request's first row
         const int rowbase = qt * S::kRows;                // (query token, head) rows, token-major
         const int nrows = min(S::kRows, r.n * a.G - rowbase);
@@ -211,49 +250,52 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
         // ---- this warp's tiles: t_begin + 16 (warp + 8 i)
         const int first_tile = t_begin + warp * kAttnTile;
         const int ntiles = first_tile < t_end ? (t_end - first_tile + kAttnChunk - 1) / kAttnChunk : 0;
-        int ids = -1;   // lane i: the page of the warp's tile 32 k + i
-        auto load_ids = [&](int i0) {
-            const int64_t t = first_tile + (int64_t)(i0 + lane) * kAttnChunk;
-            ids = -1;
-            if (t < t_end) {
-                ids = a.table[(int64_t)b * a.max_pages + (t >> a.page_shift)];
-                if (ids < 0 || ids >= a.pages) {
-                    if (a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
-                    ids = -1;
-                }
-            }
-        };
+        int ids = -1;         // lane i: the page of the warp's tile 32 k + i
+        uint32_t there = 0;   // bit 0: the tile last fetched has a page, bit 1: the one before, ...
+        constexpr int kPieces = S::kCodes / 16, kInRow = S::kRow / 16;   // 16-byte pieces of a tile and of a row
+        constexpr int kScalePieces = S::kScales / 16;
+        // where this lane's pieces come from (in page 0) and go to (in a slot)
+        const int64_t kv_rows = (int64_t)a.Hk << a.page_shift, page_rows = 2 * kv_rows;
+        const uint8_t *src_k = a.codes + ((int64_t)h << a.page_shift) * S::kRow + (lane % kPieces) * 16;
+        const uint8_t *src_v = src_k + kv_rows * S::kRow;
+        const uint8_t *src_s = a.scales + (((int64_t)h << a.page_shift) + (lane / kScalePieces) * kv_rows) * kBlocks +
+                               lane % kScalePieces * 16;
+        const int piece_row = lane / kInRow, in_page = (1 << a.page_shift) - 1;
+        const uint32_t dst = ring_addr + piece_row * S::kRow + swizzled<D>(piece_row, lane % kInRow) * 16;
+        static_assert(swizzled<D>(0, 1) == swizzled<D>(32 / kInRow, 1), "the pieces 32 apart lie alike");
         // Copies tile i into its slot of the ring; a page that is not there
         // leaves the slot as it is (its tokens are not seen).
         auto fetch = [&](int i) {
+            there <<= 1;
             if (i < ntiles) {
-                if ((i & 31) == 0) load_ids(i);
+                if ((i & 31) == 0) {
+                    const int64_t t = first_tile + (int64_t)(i + lane) * kAttnChunk;
+                    ids = -1;
+                    if (t < t_end) {
+                        ids = a.table[(int64_t)b * a.max_pages + (t >> a.page_shift)];
+                        if (ids < 0 || ids >= a.pages) {
+                            if (a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
+                            ids = -1;
+                        }
+                    }
+                }
                 const int id = __shfl_sync(0xffffffffu, ids, i & 31);
                 if (id >= 0) {
-                    const int t = first_tile + i * kAttnChunk;
-                    const int64_t page_row = ((int64_t)id * 2 * a.Hk + h) << a.page_shift;
-                    const int64_t row = page_row + (t & ((1 << a.page_shift) - 1));
-                    const int64_t kv = (int64_t)a.Hk << a.page_shift;   // rows from keys to values
-                    const uint32_t slot = ring_addr + (i % S::kStages) * S::kStage;
-                    constexpr int kPieces = S::kCodes / 16, kInRow = S::kRow / 16;
+                    there |= 1u;
+                    const int64_t row = id * page_rows + ((first_tile + i * kAttnChunk) & in_page);
+                    const uint32_t at = (i & (S::kStages - 1)) * S::kStage;
+                    const int64_t off = row * S::kRow;
 #pragma unroll
-                    for (int j = 0; j < 2 * kPieces; j += 32) {
-                        const int p = j + lane, v = p / kPieces, q = p % kPieces;
-                        const int tr = q / kInRow, tc = q % kInRow;
-                        cp_async16(slot + v * S::kCodes + tr * S::kRow + swizzled<D>(tr, tc) * 16,
-                                   a.codes + (row + v * kv) * S::kRow + q * 16);
+                    for (int j = 0; j < kPieces; j += 32) {
+                        cp_async16(dst + at + j * 16, src_k + off + j * 16);
+                        cp_async16(dst + at + S::kCodes + j * 16, src_v + off + j * 16);
                     }
-                    constexpr int kScalePieces = S::kScales / 16;
-                    if (lane < 2 * kScalePieces) {
-                        const int v = lane / kScalePieces, q = lane % kScalePieces;
-                        cp_async16(slot + 2 * S::kCodes + v * S::kScales + q * 16,
-                                   a.scales + (row + v * kv) * kBlocks + q * 16);
-                    }
+                    if (lane < 2 * kScalePieces)
+                        cp_async16(ring_addr + at + 2 * S::kCodes + lane * 16, src_s + row * kBlocks);
                 }
             }
             cp_async_commit();
         };
-        int seen_id = -1;   // as `ids`, for the tile that is computed
 #pragma unroll
         for (int i = 0; i < S::kStages - 1; ++i) fetch(i);
 
@@ -302,8 +344,8 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
         __syncthreads();
 
         // ---- the pass over the tokens
-        uint2 qf[NQ <= 2 ? D / 16 : 1][NQ];
-        if (NQ <= 2)
+        uint2 qf[NQ == 1 ? D / 16 : 1][NQ];
+        if (NQ == 1)
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
 #pragma unroll
@@ -311,8 +353,8 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
         float mult[NQ][2], top[NQ][2], sum[NQ][2];
         int last[NQ][2];   // position of this lane's two rows (columns of the products)
         float o[2 * kBlocks][NQ][4];
-        uint32_t vbias[kBlocks];   // kVBias + 15 - E in both halves
-        int vmax[kBlocks];         // E
+        float ref[NQ][2];          // top, or 0 before there is one
+        int vmax = 0;              // E of block lane % kBlocks
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -320,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
                 const int rr = 8 * n + 2 * c + j;
                 mult[n][j] = s_mult[rr];
                 top[n][j] = -INFINITY;
+                ref[n][j] = 0.0f;
                 sum[n][j] = 0.0f;
                 last[n][j] = pos0 + (rowbase + min(rr, nrows - 1)) / a.G;
             }
@@ -329,41 +372,66 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[m][n][j] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kBlocks; ++k) vmax[k] = 0, vbias[k] = (uint32_t)(15 + kVBias) * 0x10001u;
         // ldmatrix rows of this lane: row lane % 8 (+ 8 for the odd matrices) of pieces
         // (blocks) 2 x + lane / 16
         const int mrow = (lane & 7) + ((lane >> 3) & 1) * 8, mblk = lane >> 4;
 
         for (int i = 0; i < ntiles; ++i) {
-            // ids moves on to the next 32 tiles while up to kStages - 1 of the old
-            // ones are still to be computed: validity is kept apart
-            if ((i & 31) == 0) {
-                const int64_t t = first_tile + (int64_t)(i + lane) * kAttnChunk;
-                seen_id = t < t_end ? a.table[(int64_t)b * a.max_pages + (t >> a.page_shift)] : -1;
-            }
             cp_async_wait<S::kStages - 2>();
             __syncwarp();
             fetch(i + S::kStages - 1);   // into the slot of the tile before
-            const int id = __shfl_sync(0xffffffffu, seen_id, i & 31);
-            if (id < 0 || id >= a.pages) continue;
+            if (!(there >> (S::kStages - 1) & 1u)) continue;
             const int t0 = first_tile + i * kAttnChunk;
-            const uint32_t slot = ring_addr + (i % S::kStages) * S::kStage;
-            const uint8_t *sc = ring + (i % S::kStages) * S::kStage + 2 * S::kCodes;
+            const uint32_t slot = ring_addr + (i & (S::kStages - 1)) * S::kStage;
+            const uint8_t *sc = ring + (i & (S::kStages - 1)) * S::kStage + 2 * S::kCodes;
+            const bool edge = t0 + kAttnTile - 1 > pos_lo || (a.window && t0 <= pos_hi - a.window);
+            // Scales, each formed by one lane.  Keys: 2^(byte - 127) in fp32; byte 0 (2^-127) counts as
+            // zero, 255 as infinity: its codes are zero, and zero times it NaN.
+            bool nans = false;   // a value that is NaN, in this tile
+            {
+                if (kBlocks == 4) {
+                    const uint32_t w = reinterpret_cast<const uint16_t *>(sc)[lane];
+                    reinterpret_cast<uint2 *>(s_ks)[lane] = make_uint2((w & 0xffu) << 23, w >> 8 << 23);
+                } else {
+                    s_ks[lane] = __uint_as_float((uint32_t)sc[lane] << 23);
+                }
+                // values: tokens 2 p and 2 p + 1 of block k
+                const int p = (lane / kBlocks) & 7, k = lane % kBlocks;
+                const uint8_t *sv = sc + S::kScales + 2 * p * kBlocks + k;
+                uint32_t e0 = sv[0], e1 = sv[kBlocks];
+                if (edge) {   // what no row sees, written to or not
+                    const int t = t0 + 2 * p, seen = a.window ? pos_lo - a.window : -1;
+                    if (t > pos_hi || t <= seen) e0 = 0;
+                    if (t + 1 > pos_hi || t + 1 <= seen) e1 = 0;
+                }
+                if (__any_sync(0xffffffffu, (int)max(e0, e1) > vmax)) {
+                    if (e0 == 255u) nans = true, e0 = kNan;
+                    if (e1 == 255u) nans = true, e1 = kNan;
+                    nans = __any_sync(0xffffffffu, nans);
+                    if (nans) s_ve[p * kBlocks + k] = e0 | e1 << 16;
+                    int v = max(vmax, max(e0 == kNan ? 0 : (int)e0, e1 == kNan ? 0 : (int)e1));
+#pragma unroll
+                    for (int x = kBlocks; x <= 16; x <<= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, x));
+                    const float f = ex2((float)(vmax - v));
+                    vmax = v;
+#pragma unroll
+                    for (int m = 0; m < kBlocks; ++m) {
+                        const float fm = __shfl_sync(0xffffffffu, f, m);
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) o[2 * m][n][j] *= fm, o[2 * m + 1][n][j] *= fm;
+                    }
+                }
+                const uint32_t bias = (uint32_t)((15 + kVBias - vmax) & 0xffff) * 0x10001u;
+                s_vs[p * kBlocks + k] = __viaddmax_s16x2_relu(e0 | e1 << 16, bias, 0u) << 10;
+                __syncwarp();
+            }
             // S^T = K Q^T
             float s[NQ][4];
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[n][j] = 0.0f;
-            uint32_t ks0, ks1;   // scale bytes of tokens g and g + 8
-            if (kBlocks == 4) {
-                ks0 = reinterpret_cast<const uint32_t *>(sc)[g];
-                ks1 = reinterpret_cast<const uint32_t *>(sc)[g + 8];
-            } else {
-                ks0 = reinterpret_cast<const uint16_t *>(sc)[g];
-                ks1 = reinterpret_cast<const uint16_t *>(sc)[g + 8];
-            }
+            float ks0[kBlocks], ks1[kBlocks];   // of tokens g and g + 8
+            load_blocks<kBlocks>(ks0, s_ks + g * kBlocks);
+            load_blocks<kBlocks>(ks1, s_ks + (g + 8) * kBlocks);
 #pragma unroll
             for (int x = 0; x < kBlocks / 2; ++x) {
                 uint32_t w[4];   // tokens 0-7 and 8-15 of block 2 x, then of block 2 x + 1
@@ -374,27 +442,23 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
                     uint32_t k0[4], k1[4];
                     mx4_half8(w[2 * y], k0);
                     mx4_half8(w[2 * y + 1], k1);
-                    // 2^(byte - 127); byte 0 (2^-127) counts as zero, 255 as infinity: its
-                    // codes are zero, and zero times it NaN
-                    const float f0 = __uint_as_float((ks0 >> (8 * k) & 0xffu) << 23);
-                    const float f1 = __uint_as_float((ks1 >> (8 * k) & 0xffu) << 23);
+                    const float f0 = ks0[k], f1 = ks1[k];
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
-                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        const uint2 qa = NQ <= 2 ? qf[NQ <= 2 ? 2 * k : 0][n] : s_q[(2 * k * NQ + n) * 32 + lane];
-                        const uint2 qb = NQ <= 2 ? qf[NQ <= 2 ? 2 * k + 1 : 0][n]
+                        float d[4];
+                        const uint2 qa = NQ == 1 ? qf[NQ == 1 ? 2 * k : 0][n] : s_q[(2 * k * NQ + n) * 32 + lane];
+                        const uint2 qb = NQ == 1 ? qf[NQ == 1 ? 2 * k + 1 : 0][n]
                                                  : s_q[((2 * k + 1) * NQ + n) * 32 + lane];
-                        mma16816(d, k0[0], k1[0], k0[1], k1[1], qa.x, qa.y);
+                        mma16816_first(d, k0[0], k1[0], k0[1], k1[1], qa.x, qa.y);
                         mma16816(d, k0[2], k1[2], k0[3], k1[3], qb.x, qb.y);
-                        s[n][0] = fmaf(d[0], f0, s[n][0]);
-                        s[n][1] = fmaf(d[1], f0, s[n][1]);
-                        s[n][2] = fmaf(d[2], f1, s[n][2]);
-                        s[n][3] = fmaf(d[3], f1, s[n][3]);
+                        s[n][0] = k ? fmaf(d[0], f0, s[n][0]) : d[0] * f0;
+                        s[n][1] = k ? fmaf(d[1], f0, s[n][1]) : d[1] * f0;
+                        s[n][2] = k ? fmaf(d[2], f1, s[n][2]) : d[2] * f1;
+                        s[n][3] = k ? fmaf(d[3], f1, s[n][3]) : d[3] * f1;
                     }
                 }
             }
             // scale and mask; rows: tokens t0 + g and t0 + g + 8
-            const bool edge = t0 + kAttnTile - 1 > pos_lo || (a.window && t0 <= pos_hi - a.window);
             bool over = false;
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
@@ -419,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
                         v = fmaxf(v, top[n][j]);
                         const float f = v == top[n][j] ? 1.0f : ex2(top[n][j] - v);
                         top[n][j] = v;
+                        ref[n][j] = v == -INFINITY ? 0.0f : v;
                         sum[n][j] *= f;
 #pragma unroll
                         for (int m = 0; m < 2 * kBlocks; ++m) o[m][n][j] *= f, o[m][n][j + 2] *= f;
@@ -431,67 +496,16 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
                 float p[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float m = top[n][j & 1];
-                    p[j] = ex2(s[n][j] - (m == -INFINITY ? 0.0f : m));
+                    p[j] = ex2(s[n][j] - ref[n][j & 1]);
                     sum[n][j & 1] += p[j];
                 }
                 pt[n][0] = transposed8(half2_bits(p[0], p[1]));
                 pt[n][1] = transposed8(half2_bits(p[2], p[3]));
             }
-            // the values' scales of tokens 2c, 2c+1 and 2c+8, 2c+9, for each block
-            const uint8_t *sv = sc + S::kScales;
-            uint32_t e[kBlocks][2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                uint32_t w0, w1;
-                if (kBlocks == 4) {
-                    const uint2 w = reinterpret_cast<const uint2 *>(sv)[c + 4 * x];
-                    w0 = w.x, w1 = w.y;
-                } else {
-                    w0 = reinterpret_cast<const uint32_t *>(sv)[c + 4 * x];
-                    w1 = w0 >> 16;
-                }
-                if (edge) {   // what no row sees, written to or not
-                    const int t = t0 + 2 * c + 8 * x, seen = a.window ? pos_lo - a.window : -1;
-                    if (t > pos_hi || t <= seen) w0 = 0;
-                    if (t + 1 > pos_hi || t + 1 <= seen) w1 = 0;
-                }
-#pragma unroll
-                for (int k = 0; k < kBlocks; ++k)
-                    e[k][x] = __byte_perm(w0, w1, k | (k + 4) << 8) & 0x00ff00ffu;
-            }
-            bool grown = false, nans = false;   // nans: a value that is NaN, in this tile
-#pragma unroll
-            for (int k = 0; k < kBlocks; ++k) {
-                const uint32_t m = __vmaxs2(e[k][0], e[k][1]);
-                grown |= max((int)(m & 0xffffu), (int)(m >> 16)) > vmax[k];
-            }
-            if (__any_sync(0xffffffffu, grown)) {
-#pragma unroll
-                for (int k = 0; k < kBlocks; ++k) {
-                    int v = vmax[k];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        uint32_t lo = e[k][x] & 0xffffu, hi = e[k][x] >> 16;
-                        if (lo == 255u) nans = true, lo = kNan;
-                        else v = max(v, (int)lo);
-                        if (hi == 255u) nans = true, hi = kNan;
-                        else v = max(v, (int)hi);
-                        e[k][x] = lo | hi << 16;
-                    }
-                    v = max(v, __shfl_xor_sync(0xffffffffu, v, 1));
-                    v = max(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                    if (v != vmax[k]) {
-                        const float f = ex2((float)(vmax[k] - v));
-                        vmax[k] = v;
-                        vbias[k] = (uint32_t)((15 + kVBias - v) & 0xffff) * 0x10001u;
-#pragma unroll
-                        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) o[2 * k][n][j] *= f, o[2 * k + 1][n][j] *= f;
-                    }
-                }
-            }
+            // the values' scales of tokens 2c, 2c+1 and 2c+8, 2c+9
+            uint32_t vs0[kBlocks], vs1[kBlocks];
+            load_blocks<kBlocks>(vs0, s_vs + c * kBlocks);
+            load_blocks<kBlocks>(vs1, s_vs + (c + 4) * kBlocks);
             // O^T += V^T P^T
 #pragma unroll
             for (int x = 0; x < kBlocks / 2; ++x) {
@@ -503,24 +517,29 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
                     // codes of channels 4g .. 4g+3 of block k: of token 2c in the low half
                     // of the word, of token 2c + 1 in the high half (+ 8 in the second word)
                     uint32_t v0[4], v1[4];
-                    mx4_half8(w[2 * y], v0);
-                    mx4_half8(w[2 * y + 1], v1);
-                    const uint32_t f0 = __viaddmax_s16x2_relu(e[k][0], vbias[k], 0u) << 10;
-                    const uint32_t f1 = __viaddmax_s16x2_relu(e[k][1], vbias[k], 0u) << 10;
+                    mx4_half8(token_pairs(w[2 * y]), v0);
+                    mx4_half8(token_pairs(w[2 * y + 1]), v1);
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
-                        uint32_t b0 = mul_half2(pt[n][0], f0), b1 = mul_half2(pt[n][1], f1);
-                        if (nans) {   // NaN for the rows that see it
-                            b0 = with_nans(b0, pt[n][0], e[k][0]);
-                            b1 = with_nans(b1, pt[n][1], e[k][1]);
-                        }
-                        mma16816(o[2 * k][n], __byte_perm(v0[0], v0[2], 0x5410), __byte_perm(v0[0], v0[2], 0x7632),
-                                 __byte_perm(v1[0], v1[2], 0x5410), __byte_perm(v1[0], v1[2], 0x7632), b0, b1);
-                        mma16816(o[2 * k + 1][n], __byte_perm(v0[1], v0[3], 0x5410),
-                                 __byte_perm(v0[1], v0[3], 0x7632), __byte_perm(v1[1], v1[3], 0x5410),
-                                 __byte_perm(v1[1], v1[3], 0x7632), b0, b1);
+                        const uint32_t b0 = mul_half2(pt[n][0], vs0[k]), b1 = mul_half2(pt[n][1], vs1[k]);
+                        mma16816(o[2 * k][n], v0[0], v0[2], v1[0], v1[2], b0, b1);       // channels 4g, 4g + 1
+                        mma16816(o[2 * k + 1][n], v0[1], v0[3], v1[1], v1[3], b0, b1);   // 4g + 2, 4g + 3
                     }
                 }
+            }
+            if (nans) {   // NaN for the rows that see it, in its block
+#pragma unroll
+                for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        const bool hit = sees_nan(pt[n][0], s_ve[c * kBlocks + k]) ||
+                                         sees_nan(pt[n][1], s_ve[(c + 4) * kBlocks + k]);
+                        const uint32_t lanes = __ballot_sync(0xffffffffu, hit);   // four lanes to row g
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            if (lanes >> (8 * c + 4 * j) & 15u)
+                                o[2 * k][n][j] = o[2 * k][n][j + 2] = o[2 * k + 1][n][j] = o[2 * k + 1][n][j + 2] = NAN;
+                    }
             }
         }
 
@@ -553,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
 #pragma unroll
                 for (int k = 0; k < kBlocks; ++k) {
                     // 2^(E - 127 - kVBias)
-                    const float fe = f * (mx4_scale((uint32_t)vmax[k]) * exp2f(-kVBias));
+                    const float fe = f * (mx4_scale((uint32_t)__shfl_sync(0xffffffffu, vmax, k)) * exp2f(-kVBias));
                     *reinterpret_cast<float4 *>(s_o + ((warp * 8 + 2 * c + j) * D + 32 * k + 4 * g)) =
                         make_float4(o[2 * k][n][j] * fe, o[2 * k][n][j + 2] * fe, o[2 * k + 1][n][j] * fe,
                                     o[2 * k + 1][n][j + 2] * fe);
@@ -616,11 +635,11 @@ __global__ void __launch_bounds__(256) attention4_join_kernel(const AttnArgs a, 
     const AttnRequest r = attn_request(a, lo);
     if (row < r.row0 || row >= r.row0 + r.n || a.plan[lo] == a.plan[lo + 1]) return;
     const int per = a.plan[a.B + 1];
-    const int chunks = max(1, (r.len - r.lo + kAttnChunk - 1) / kAttnChunk);
+    const int chunks = attn_chunks(r);
     const int tiles_q = (int)(((int64_t)r.n * a.G + rows_at_once - 1) / rows_at_once);
     const int h = head / a.G, flat = (row - r.row0) * a.G + head % a.G;
     const int qt = flat / rows_at_once, rr = flat - qt * rows_at_once;
-    const int u0 = a.plan[lo] + (h * tiles_q + qt) * chunks;
+    const int u0 = a.plan[lo] + (h * tiles_q + qt) * (chunks + kPieceUnits) + kPieceUnits;
     const int k0 = u0 / per, k1 = (u0 + chunks - 1) / per;
     if (k0 == k1) return;   // one CTA had all of it
     const int64_t size = (int64_t)rows_at_once * (D + 2);

@@ -47,4 +47,9 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnArgs &a, int b) {
     return r;
 }
 
+// Units of work over the request's tokens, for one KV head and group of rows.
+__device__ __forceinline__ int attn_chunks(const AttnRequest &r) {
+    return max(1, (r.len - r.lo + kAttnChunk - 1) / kAttnChunk);
+}
+
 }  // namespace moe
