@@ -103,13 +103,12 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Stands for the scale byte 255 (NaN) in a half word: very small, so that it
-// scales to zero, and known again by sees_nan.
+// Scale of a value that is NaN, for a start: minus zero.
 constexpr uint32_t kNan = 0x8000u;
 
 // Whether a pair of probabilities gives weight to a value that is NaN.
-__device__ __forceinline__ bool sees_nan(uint32_t p, uint32_t e) {
-    return ((e & 0xffffu) == kNan && (p & 0x7fffu)) || (e >> 16 == kNan && (p & 0x7fff0000u));
+__device__ __forceinline__ bool sees_nan(uint32_t p, uint32_t scales) {
+    return ((scales & 0xffffu) == kNan && (p & 0x7fffu)) || (scales >> 16 == kNan && (p & 0x7fff0000u));
 }
 
 // N words of shared memory, as bits or as floats.
@@ -140,14 +139,15 @@ struct Shape {
     static constexpr int kCodes = kAttnTile * kRow;     // of a tile's keys or values
     static constexpr int kScales = kAttnTile * kBlocks;
     static constexpr int kStage = 2 * (kCodes + kScales);
-    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr int kTiles = NQ == 1 ? 2 : 1;      // tiles of a warp at a time
+    static constexpr int kStages = (D == 128 ? 3 : 7) + kTiles;
     static constexpr int kRows = 8 * NQ;
     static constexpr int kRing = kAttnWarps * kStages * kStage;
     // queries in the order of the products, then what rows and warps exchange
     static constexpr int kQBytes = D / 16 * NQ * 32 * 8;
-    // a warp's scales of a tile: the keys' in fp32, the values' (and what is NaN of
-    // them) for pairs of tokens
-    static constexpr int kScaleBytes = kAttnTile * kBlocks * 4 + 2 * (kAttnTile / 2) * kBlocks * 4;
+    // a warp's scales: the keys' in fp32, the values' for pairs of tokens
+    static constexpr int kScaleWords = (kAttnTile + kAttnTile / 2) * kBlocks;   // of a tile
+    static constexpr int kScaleBytes = kTiles * kScaleWords * 4;
     static constexpr int kScaleAt = kRing + kQBytes;
     static constexpr int kSmem = kScaleAt + kAttnWarps * kScaleBytes + (kRows + 2 * kAttnWarps * kRows) * 4;
     static_assert(kAttnWarps * 8 * D * 4 <= kRing, "the warps' sums are exchanged where the ring was");
@@ -198,13 +198,12 @@ __device__ __forceinline__ void plan_units(const AttnArgs &a, int rows_at_once, 
 template <int D, int NQ>
 __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(const AttnArgs a) {
     using S = Shape<D, NQ>;
-    constexpr int kBlocks = S::kBlocks;
+    constexpr int kBlocks = S::kBlocks, kTiles = S::kTiles;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_warp[kAttnWarps];
     uint2 *s_q = reinterpret_cast<uint2 *>(smem + S::kRing);                 // [k step][8 rows][lane]
     float *s_ks = reinterpret_cast<float *>(smem + S::kScaleAt + (threadIdx.x >> 5) * S::kScaleBytes);   // [token][block]
     uint32_t *s_vs = reinterpret_cast<uint32_t *>(s_ks) + kAttnTile * kBlocks;                           // [pair][block]
-    uint32_t *s_ve = s_vs + kAttnTile / 2 * kBlocks;
     float *s_mult = reinterpret_cast<float *>(smem + S::kScaleAt + kAttnWarps * S::kScaleBytes);   // [rows]
     float *s_top = s_mult + S::kRows, *s_sum = s_top + kAttnWarps * S::kRows;  // [warp][rows]
     int *s_first = reinterpret_cast<int *>(smem + S::kSmem);                 // [requests + 1]
@@ -252,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
         const int ntiles = first_tile < t_end ? (t_end - first_tile + kAttnChunk - 1) / kAttnChunk : 0;
         int ids = -1;         // lane i: the page of the warp's tile 32 k + i
         uint32_t there = 0;   // bit 0: the tile last fetched has a page, bit 1: the one before, ...
+        uint32_t to = 0;      // the slot that the next tile goes to
         constexpr int kPieces = S::kCodes / 16, kInRow = S::kRow / 16;   // 16-byte pieces of a tile and of a row
         constexpr int kScalePieces = S::kScales / 16;
         // where this lane's pieces come from (in page 0) and go to (in a slot)
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
                 if (id >= 0) {
                     there |= 1u;
                     const int64_t row = id * page_rows + ((first_tile + i * kAttnChunk) & in_page);
-                    const uint32_t at = (i & (S::kStages - 1)) * S::kStage;
+                    const uint32_t at = to;
                     const int64_t off = row * S::kRow;
 #pragma unroll
                     for (int j = 0; j < kPieces; j += 32) {
@@ -295,9 +295,10 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
                 }
             }
             cp_async_commit();
+            to = to == (S::kStages - 1) * S::kStage ? 0 : to + S::kStage;
         };
 #pragma unroll
-        for (int i = 0; i < S::kStages - 1; ++i) fetch(i);
+        for (int i = 0; i < S::kStages - kTiles; ++i) fetch(i);
 
         // ---- queries: fp16 in the order of the products, a power of two for each row
         for (int rr = warp; rr < S::kRows; rr += kAttnWarps) {
@@ -350,10 +351,10 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
             for (int k = 0; k < D / 16; ++k)
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) qf[k][n] = s_q[(k * NQ + n) * 32 + lane];
-        float mult[NQ][2], top[NQ][2], sum[NQ][2];
+        float mult[NQ][2], ref[NQ][2], sum[NQ][2];   // ref: m, 0 before there is one
         int last[NQ][2];   // position of this lane's two rows (columns of the products)
         float o[2 * kBlocks][NQ][4];
-        float ref[NQ][2];          // top, or 0 before there is one
+        float pass[NQ][2];         // what may pass m: kLazy, or nothing before there is an m
         int vmax = 0;              // E of block lane % kBlocks
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
             for (int j = 0; j < 2; ++j) {
                 const int rr = 8 * n + 2 * c + j;
                 mult[n][j] = s_mult[rr];
-                top[n][j] = -INFINITY;
+                pass[n][j] = -INFINITY;
                 ref[n][j] = 0.0f;
                 sum[n][j] = 0.0f;
                 last[n][j] = pos0 + (rowbase + min(rr, nrows - 1)) / a.G;
@@ -376,170 +377,226 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
         // (blocks) 2 x + lane / 16
         const int mrow = (lane & 7) + ((lane >> 3) & 1) * 8, mblk = lane >> 4;
 
-        for (int i = 0; i < ntiles; ++i) {
-            cp_async_wait<S::kStages - 2>();
+        uint32_t from = 0;   // the slot of tile i
+        for (int i = 0; i < ntiles; i += kTiles) {
+            cp_async_wait<S::kStages - 2 * kTiles>();
             __syncwarp();
-            fetch(i + S::kStages - 1);   // into the slot of the tile before
-            if (!(there >> (S::kStages - 1) & 1u)) continue;
-            const int t0 = first_tile + i * kAttnChunk;
-            const uint32_t slot = ring_addr + (i & (S::kStages - 1)) * S::kStage;
-            const uint8_t *sc = ring + (i & (S::kStages - 1)) * S::kStage + 2 * S::kCodes;
-            const bool edge = t0 + kAttnTile - 1 > pos_lo || (a.window && t0 <= pos_hi - a.window);
+#pragma unroll
+            for (int u = 0; u < kTiles; ++u) fetch(i + S::kStages - kTiles + u);   // into the slots of the tiles before
+            uint32_t slot[kTiles];
+#pragma unroll
+            for (int u = 0; u < kTiles; ++u) {
+                slot[u] = from;
+                from = from == (S::kStages - 1) * S::kStage ? 0 : from + S::kStage;
+            }
+            // which of the tiles are there: all of them, but for the last round and bad pages
+            const uint32_t have = there >> (S::kStages - kTiles);
+            if ((have & ((1u << kTiles) - 1)) == 0) continue;
+            const int t0 = first_tile + i * kAttnChunk;   // tile u: t0 + u kAttnChunk
+            const bool edge = t0 + (kTiles - 1) * kAttnChunk + kAttnTile - 1 > pos_lo ||
+                              (a.window && t0 <= pos_hi - a.window) || (~have & ((1u << kTiles) - 1));
             // Scales, each formed by one lane.  Keys: 2^(byte - 127) in fp32; byte 0 (2^-127) counts as
             // zero, 255 as infinity: its codes are zero, and zero times it NaN.
-            bool nans = false;   // a value that is NaN, in this tile
-            {
+            const int vp = (lane / kBlocks) & 7, vk = lane % kBlocks;   // values: tokens 2 vp, 2 vp + 1 of block vk
+            uint32_t e[kTiles];
+            int emax = 0;
+#pragma unroll
+            for (int u = 0; u < kTiles; ++u) {
+                const uint8_t *sc = ring + slot[u] + 2 * S::kCodes;
                 if (kBlocks == 4) {
                     const uint32_t w = reinterpret_cast<const uint16_t *>(sc)[lane];
-                    reinterpret_cast<uint2 *>(s_ks)[lane] = make_uint2((w & 0xffu) << 23, w >> 8 << 23);
+                    reinterpret_cast<uint2 *>(s_ks + u * S::kScaleWords)[lane] = make_uint2((w & 0xffu) << 23, w >> 8 << 23);
                 } else {
-                    s_ks[lane] = __uint_as_float((uint32_t)sc[lane] << 23);
+                    s_ks[u * S::kScaleWords + lane] = __uint_as_float((uint32_t)sc[lane] << 23);
                 }
-                // values: tokens 2 p and 2 p + 1 of block k
-                const int p = (lane / kBlocks) & 7, k = lane % kBlocks;
-                const uint8_t *sv = sc + S::kScales + 2 * p * kBlocks + k;
+                const uint8_t *sv = sc + S::kScales + 2 * vp * kBlocks + vk;
                 uint32_t e0 = sv[0], e1 = sv[kBlocks];
                 if (edge) {   // what no row sees, written to or not
-                    const int t = t0 + 2 * p, seen = a.window ? pos_lo - a.window : -1;
-                    if (t > pos_hi || t <= seen) e0 = 0;
-                    if (t + 1 > pos_hi || t + 1 <= seen) e1 = 0;
+                    const int t = t0 + u * kAttnChunk + 2 * vp, seen = a.window ? pos_lo - a.window : -1;
+                    const bool gone = !(have >> (kTiles - 1 - u) & 1u);
+                    if (gone || t > pos_hi || t <= seen) e0 = 0;
+                    if (gone || t + 1 > pos_hi || t + 1 <= seen) e1 = 0;
                 }
-                if (__any_sync(0xffffffffu, (int)max(e0, e1) > vmax)) {
-                    if (e0 == 255u) nans = true, e0 = kNan;
-                    if (e1 == 255u) nans = true, e1 = kNan;
-                    nans = __any_sync(0xffffffffu, nans);
-                    if (nans) s_ve[p * kBlocks + k] = e0 | e1 << 16;
-                    int v = max(vmax, max(e0 == kNan ? 0 : (int)e0, e1 == kNan ? 0 : (int)e1));
+                e[u] = e0 | e1 << 16;
+                emax = max(emax, (int)max(e0, e1));
+            }
+            bool nans = false;   // a value that is NaN, in these tiles
+            uint32_t nan_bits[kTiles];
 #pragma unroll
-                    for (int x = kBlocks; x <= 16; x <<= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, x));
-                    const float f = ex2((float)(vmax - v));
-                    vmax = v;
+            for (int u = 0; u < kTiles; ++u) nan_bits[u] = 0;
+            if (__any_sync(0xffffffffu, emax > vmax)) {
+                int v = vmax;
 #pragma unroll
-                    for (int m = 0; m < kBlocks; ++m) {
-                        const float fm = __shfl_sync(0xffffffffu, f, m);
-#pragma unroll
-                        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) o[2 * m][n][j] *= fm, o[2 * m + 1][n][j] *= fm;
-                    }
+                for (int u = 0; u < kTiles; ++u) {
+                    uint32_t e0 = e[u] & 0xffffu, e1 = e[u] >> 16;
+                    if (e0 == 255u) nan_bits[u] |= kNan, e0 = 0;
+                    if (e1 == 255u) nan_bits[u] |= kNan << 16, e1 = 0;
+                    nans |= nan_bits[u] != 0;
+                    e[u] = e0 | e1 << 16;
+                    v = max(v, (int)max(e0, e1));
                 }
+                nans = __any_sync(0xffffffffu, nans);
+#pragma unroll
+                for (int x = kBlocks; x <= 16; x <<= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, x));
+                const float f = ex2((float)(vmax - v));
+                vmax = v;
+#pragma unroll
+                for (int m = 0; m < kBlocks; ++m) {
+                    const float fm = __shfl_sync(0xffffffffu, f, m);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[2 * m][n][j] *= fm, o[2 * m + 1][n][j] *= fm;
+                }
+            }
+            {
                 const uint32_t bias = (uint32_t)((15 + kVBias - vmax) & 0xffff) * 0x10001u;
-                s_vs[p * kBlocks + k] = __viaddmax_s16x2_relu(e0 | e1 << 16, bias, 0u) << 10;
-                __syncwarp();
+#pragma unroll
+                for (int u = 0; u < kTiles; ++u) {
+                    uint32_t f = __viaddmax_s16x2_relu(e[u], bias, 0u) << 10;
+                    if (nans) f = (f & ~((nan_bits[u] >> 15) * 0xffffu)) | nan_bits[u];
+                    s_vs[u * S::kScaleWords + vp * kBlocks + vk] = f;
+                }
             }
+            __syncwarp();
             // S^T = K Q^T
-            float s[NQ][4];
-            float ks0[kBlocks], ks1[kBlocks];   // of tokens g and g + 8
-            load_blocks<kBlocks>(ks0, s_ks + g * kBlocks);
-            load_blocks<kBlocks>(ks1, s_ks + (g + 8) * kBlocks);
+            float s[kTiles][NQ][4];
 #pragma unroll
-            for (int x = 0; x < kBlocks / 2; ++x) {
-                uint32_t w[4];   // tokens 0-7 and 8-15 of block 2 x, then of block 2 x + 1
-                ldm4(slot + mrow * S::kRow + swizzled<D>(mrow, 2 * x + mblk) * 16, w);
+            for (int u = 0; u < kTiles; ++u) {
+                float ks0[kBlocks], ks1[kBlocks];   // of tokens g and g + 8
+                load_blocks<kBlocks>(ks0, s_ks + u * S::kScaleWords + g * kBlocks);
+                load_blocks<kBlocks>(ks1, s_ks + u * S::kScaleWords + (g + 8) * kBlocks);
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const int k = 2 * x + y;
-                    uint32_t k0[4], k1[4];
-                    mx4_half8(w[2 * y], k0);
-                    mx4_half8(w[2 * y + 1], k1);
-                    const float f0 = ks0[k], f1 = ks1[k];
+                for (int x = 0; x < kBlocks / 2; ++x) {
+                    uint32_t w[4];   // tokens 0-7 and 8-15 of block 2 x, then of block 2 x + 1
+                    ldm4(ring_addr + slot[u] + mrow * S::kRow + swizzled<D>(mrow, 2 * x + mblk) * 16, w);
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
-                        float d[4];
-                        const uint2 qa = NQ == 1 ? qf[NQ == 1 ? 2 * k : 0][n] : s_q[(2 * k * NQ + n) * 32 + lane];
-                        const uint2 qb = NQ == 1 ? qf[NQ == 1 ? 2 * k + 1 : 0][n]
-                                                 : s_q[((2 * k + 1) * NQ + n) * 32 + lane];
-                        mma16816_first(d, k0[0], k1[0], k0[1], k1[1], qa.x, qa.y);
-                        mma16816(d, k0[2], k1[2], k0[3], k1[3], qb.x, qb.y);
-                        s[n][0] = k ? fmaf(d[0], f0, s[n][0]) : d[0] * f0;
-                        s[n][1] = k ? fmaf(d[1], f0, s[n][1]) : d[1] * f0;
-                        s[n][2] = k ? fmaf(d[2], f1, s[n][2]) : d[2] * f1;
-                        s[n][3] = k ? fmaf(d[3], f1, s[n][3]) : d[3] * f1;
+                    for (int y = 0; y < 2; ++y) {
+                        const int k = 2 * x + y;
+                        uint32_t k0[4], k1[4];
+                        mx4_half8(w[2 * y], k0);
+                        mx4_half8(w[2 * y + 1], k1);
+                        const float f0 = ks0[k], f1 = ks1[k];
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) {
+                            float d[4];
+                            const uint2 qa = NQ == 1 ? qf[NQ == 1 ? 2 * k : 0][n] : s_q[(2 * k * NQ + n) * 32 + lane];
+                            const uint2 qb = NQ == 1 ? qf[NQ == 1 ? 2 * k + 1 : 0][n]
+                                                     : s_q[((2 * k + 1) * NQ + n) * 32 + lane];
+                            mma16816_first(d, k0[0], k1[0], k0[1], k1[1], qa.x, qa.y);
+                            mma16816(d, k0[2], k1[2], k0[3], k1[3], qb.x, qb.y);
+                            s[u][n][0] = k ? fmaf(d[0], f0, s[u][n][0]) : d[0] * f0;
+                            s[u][n][1] = k ? fmaf(d[1], f0, s[u][n][1]) : d[1] * f0;
+                            s[u][n][2] = k ? fmaf(d[2], f1, s[u][n][2]) : d[2] * f1;
+                            s[u][n][3] = k ? fmaf(d[3], f1, s[u][n][3]) : d[3] * f1;
+                        }
                     }
                 }
             }
-            // scale and mask; rows: tokens t0 + g and t0 + g + 8
+            // scores past the maximum, masked; rows of s: tokens t0 + g and t0 + g + 8
             bool over = false;
+#pragma unroll
+            for (int u = 0; u < kTiles; ++u)
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[u][n][j] = fmaf(s[u][n][j], mult[n][j & 1], -ref[n][j & 1]);
+            if (edge) {
+#pragma unroll
+                for (int u = 0; u < kTiles; ++u)
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int t = t0 + u * kAttnChunk + g + (j >> 1) * 8, p = last[n][j & 1];
+                            if (t > p || (a.window && t <= p - a.window) || !(have >> (kTiles - 1 - u) & 1u))
+                                s[u][n][j] = -INFINITY;
+                        }
+            }
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float v = s[n][j] * mult[n][j & 1];
-                    if (edge) {
-                        const int t = t0 + g + (j >> 1) * 8, p = last[n][j & 1];
-                        if (t > p || (a.window && t <= p - a.window)) v = -INFINITY;
-                    }
-                    s[n][j] = v;
-                    over |= v > top[n][j & 1] + kLazy;
+                for (int j = 0; j < 2; ++j) {
+                    float v = fmaxf(s[0][n][j], s[0][n][j + 2]);
+#pragma unroll
+                    for (int u = 1; u < kTiles; ++u) v = fmaxf(v, fmaxf(s[u][n][j], s[u][n][j + 2]));
+                    over |= v > pass[n][j];
                 }
             if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float v = fmaxf(s[n][j], s[n][j + 2]);
+                        float v = fmaxf(s[0][n][j], s[0][n][j + 2]);
+#pragma unroll
+                        for (int u = 1; u < kTiles; ++u) v = fmaxf(v, fmaxf(s[u][n][j], s[u][n][j + 2]));
 #pragma unroll
                         for (int x = 4; x <= 16; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
-                        v = fmaxf(v, top[n][j]);
-                        const float f = v == top[n][j] ? 1.0f : ex2(top[n][j] - v);
-                        top[n][j] = v;
-                        ref[n][j] = v == -INFINITY ? 0.0f : v;
+                        // how far m moves
+                        const float up = v == -INFINITY ? 0.0f : pass[n][j] == -INFINITY ? v : fmaxf(v, 0.0f);
+                        const float f = ex2(-up);
+                        if (v != -INFINITY) pass[n][j] = kLazy;
+                        ref[n][j] += up;
                         sum[n][j] *= f;
+#pragma unroll
+                        for (int u = 0; u < kTiles; ++u) s[u][n][j] -= up, s[u][n][j + 2] -= up;
 #pragma unroll
                         for (int m = 0; m < 2 * kBlocks; ++m) o[m][n][j] *= f, o[m][n][j + 2] *= f;
                     }
             }
-            // P^T, transposed into the order of the second product
-            uint32_t pt[NQ][2];
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                float p[4];
+            for (int u = 0; u < kTiles; ++u) {
+                // P^T, transposed into the order of the second product
+                uint32_t pt[NQ][2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    p[j] = ex2(s[n][j] - ref[n][j & 1]);
-                    sum[n][j & 1] += p[j];
+                for (int n = 0; n < NQ; ++n) {
+                    float p[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        p[j] = ex2(s[u][n][j]);
+                        sum[n][j & 1] += p[j];
+                    }
+                    pt[n][0] = transposed8(half2_bits(p[0], p[1]));
+                    pt[n][1] = transposed8(half2_bits(p[2], p[3]));
                 }
-                pt[n][0] = transposed8(half2_bits(p[0], p[1]));
-                pt[n][1] = transposed8(half2_bits(p[2], p[3]));
-            }
-            // the values' scales of tokens 2c, 2c+1 and 2c+8, 2c+9
-            uint32_t vs0[kBlocks], vs1[kBlocks];
-            load_blocks<kBlocks>(vs0, s_vs + c * kBlocks);
-            load_blocks<kBlocks>(vs1, s_vs + (c + 4) * kBlocks);
-            // O^T += V^T P^T
+                // the values' scales of tokens 2c, 2c+1 and 2c+8, 2c+9
+                uint32_t vs0[kBlocks], vs1[kBlocks];
+                load_blocks<kBlocks>(vs0, s_vs + u * S::kScaleWords + c * kBlocks);
+                load_blocks<kBlocks>(vs1, s_vs + u * S::kScaleWords + (c + 4) * kBlocks);
+                // O^T += V^T P^T
 #pragma unroll
-            for (int x = 0; x < kBlocks / 2; ++x) {
-                uint32_t w[4];
-                ldm4_trans(slot + S::kCodes + mrow * S::kRow + swizzled<D>(mrow, 2 * x + mblk) * 16, w);
+                for (int x = 0; x < kBlocks / 2; ++x) {
+                    uint32_t w[4];
+                    ldm4_trans(ring_addr + slot[u] + S::kCodes + mrow * S::kRow + swizzled<D>(mrow, 2 * x + mblk) * 16, w);
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const int k = 2 * x + y;
-                    // codes of channels 4g .. 4g+3 of block k: of token 2c in the low half
-                    // of the word, of token 2c + 1 in the high half (+ 8 in the second word)
-                    uint32_t v0[4], v1[4];
-                    mx4_half8(token_pairs(w[2 * y]), v0);
-                    mx4_half8(token_pairs(w[2 * y + 1]), v1);
+                    for (int y = 0; y < 2; ++y) {
+                        const int k = 2 * x + y;
+                        // codes of channels 4g .. 4g+3 of block k: of token 2c in the low half
+                        // of the word, of token 2c + 1 in the high half (+ 8 in the second word)
+                        uint32_t v0[4], v1[4];
+                        mx4_half8(token_pairs(w[2 * y]), v0);
+                        mx4_half8(token_pairs(w[2 * y + 1]), v1);
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
-                        const uint32_t b0 = mul_half2(pt[n][0], vs0[k]), b1 = mul_half2(pt[n][1], vs1[k]);
-                        mma16816(o[2 * k][n], v0[0], v0[2], v1[0], v1[2], b0, b1);       // channels 4g, 4g + 1
-                        mma16816(o[2 * k + 1][n], v0[1], v0[3], v1[1], v1[3], b0, b1);   // 4g + 2, 4g + 3
+                        for (int n = 0; n < NQ; ++n) {
+                            const uint32_t b0 = mul_half2(pt[n][0], vs0[k]), b1 = mul_half2(pt[n][1], vs1[k]);
+                            mma16816(o[2 * k][n], v0[0], v0[2], v1[0], v1[2], b0, b1);       // channels 4g, 4g + 1
+                            mma16816(o[2 * k + 1][n], v0[1], v0[3], v1[1], v1[3], b0, b1);   // 4g + 2, 4g + 3
+                        }
                     }
                 }
-            }
-            if (nans) {   // NaN for the rows that see it, in its block
+                if (nans) {   // NaN for the rows that see it, in its block
 #pragma unroll
-                for (int k = 0; k < kBlocks; ++k)
+                    for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
-                        const bool hit = sees_nan(pt[n][0], s_ve[c * kBlocks + k]) ||
-                                         sees_nan(pt[n][1], s_ve[(c + 4) * kBlocks + k]);
-                        const uint32_t lanes = __ballot_sync(0xffffffffu, hit);   // four lanes to row g
+                        for (int n = 0; n < NQ; ++n) {
+                            const bool hit = sees_nan(pt[n][0], vs0[k]) || sees_nan(pt[n][1], vs1[k]);
+                            const uint32_t lanes = __ballot_sync(0xffffffffu, hit);   // four lanes to row g
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            if (lanes >> (8 * c + 4 * j) & 15u)
-                                o[2 * k][n][j] = o[2 * k][n][j + 2] = o[2 * k + 1][n][j] = o[2 * k + 1][n][j + 2] = NAN;
-                    }
+                            for (int j = 0; j < 2; ++j)
+                                if (lanes >> (8 * c + 4 * j) & 15u)
+                                    o[2 * k][n][j] = o[2 * k][n][j + 2] = o[2 * k + 1][n][j] = o[2 * k + 1][n][j + 2] = NAN;
+                        }
+                }
             }
         }
 
@@ -551,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
 #pragma unroll
                 for (int x = 4; x <= 16; x <<= 1) sum[n][j] += __shfl_xor_sync(0xffffffffu, sum[n][j], x);
                 if (g == 0) {
-                    s_top[warp * S::kRows + 8 * n + 2 * c + j] = top[n][j];
+                    s_top[warp * S::kRows + 8 * n + 2 * c + j] = pass[n][j] == -INFINITY ? -INFINITY : ref[n][j];
                     s_sum[warp * S::kRows + 8 * n + 2 * c + j] = sum[n][j];
                 }
             }
@@ -568,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
                 float m = s_top[rr];
 #pragma unroll
                 for (int w = 1; w < kAttnWarps; ++w) m = fmaxf(m, s_top[w * S::kRows + rr]);
-                const float f = top[n][j] == m ? 1.0f : ex2(top[n][j] - m);
+                const float mine = s_top[warp * S::kRows + rr], f = mine == m ? 1.0f : ex2(mine - m);
 #pragma unroll
                 for (int k = 0; k < kBlocks; ++k) {
                     // 2^(E - 127 - kVBias)
