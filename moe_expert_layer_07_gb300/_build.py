@@ -20,7 +20,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "route.cu", "quant.cu", "permute.cu", "gemm.cu", "gemm_wide.cu", "combine.cu",
            "selftest.cu", "stream_read.cu", "permute_static.cu", "rebalance.cu", "ffn.cu", "pack.cu",
            "api_block.cu", "few.cu", "mx4.cu", "mx4_gemm.cu",
-           "norm.cu", "api_attention.cu", "cache.cu", "qk_rope.cu", "attention4.cu", "matvec4.cu",
+           "norm.cu", "api_attention.cu", "cache.cu", "qk_rope.cu", "attention4.cu", "attention4_wide.cu", "matvec4.cu",
            "balance.cpp"]
 
 

@@ -170,8 +170,9 @@ __device__ __forceinline__ void plan_units(const AttnArgs &a, int rows_at_once, 
             const int tiles = (int)(((int64_t)r.n * a.G + rows_at_once - 1) / rows_at_once);
             const int64_t want = (int64_t)a.Hk * tiles * (attn_chunks(r) + kPieceUnits);
             // all requests together stay within 32 bits
-            units = want <= INT32_MAX / a.B ? (int)want : 0;
-            if ((r.bad || units != want) && blockIdx.x == 0 && a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
+            const bool few = (int64_t)r.n * a.G <= a.few_rows;   // else another kernel's
+            units = few && want <= INT32_MAX / a.B ? (int)want : 0;
+            if ((r.bad || (few && units != want)) && blockIdx.x == 0 && a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
         }
         int v = units;
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -699,46 +700,24 @@ __global__ void __launch_bounds__(256) attention4_join_kernel(const AttnArgs a, 
     const int u0 = a.plan[lo] + (h * tiles_q + qt) * (chunks + kPieceUnits) + kPieceUnits;
     const int k0 = u0 / per, k1 = (u0 + chunks - 1) / per;
     if (k0 == k1) return;   // one CTA had all of it
-    const int64_t size = (int64_t)rows_at_once * (D + 2);
-    float m = -INFINITY;
-    for (int k = k0 + lane; k <= k1; k += 32)
-        m = fmaxf(m, a.part[(2 * k + (k == k0)) * size + rows_at_once * D + rr]);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.0f;
-    float v[D / 32];
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) v[j] = 0.0f;
-#pragma unroll 4
-    for (int k = k0; k <= k1; ++k) {
-        const float *p = a.part + (2 * k + (k == k0)) * size;
-        const float top = p[rows_at_once * D + rr];
-        const float f = top == m ? 1.0f : ex2(top - m);
-        l += f * p[rows_at_once * (D + 1) + rr];
-        if (D == 128) {
-            const float4 y = reinterpret_cast<const float4 *>(p + rr * D)[lane];
-            v[0] += f * y.x, v[1] += f * y.y, v[2 % (D / 32)] += f * y.z, v[3 % (D / 32)] += f * y.w;
-        } else {
-            const float2 y = reinterpret_cast<const float2 *>(p + rr * D)[lane];
-            v[0] += f * y.x, v[1] += f * y.y;
-        }
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-    for (int j = 0; j < D / 32; j += 2) {
-        const int64_t at = i * D + lane * (D / 32) + j;
-        if (a.out_bf16)
-            *reinterpret_cast<__nv_bfloat162 *>(static_cast<uint16_t *>(a.out) + at) =
-                __floats2bfloat162_rn(v[j] * inv, v[j + 1] * inv);
-        else *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + at) = make_float2(v[j] * inv, v[j + 1] * inv);
-    }
-    if (a.lse && lane == 0) a.lse[i] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
+    attn_join<D>(a, rows_at_once, rr, i, k0, k1, lane);
 }
 
+// Requests of at most this many rows are this file's where the call also has larger
+// ones.
+constexpr int kFewRows = 32;
+
+int64_t most_rows(const moe_cache_attn *d, const moe_cache4 *cache) {
+    return (int64_t)std::max(1, d->max_q) * (d->q_heads / cache->kv_heads);
+}
+
+bool has_wide(const moe_cache_attn *d, const moe_cache4 *cache) { return most_rows(d, cache) > kFewRows; }
+
 // Groups of eight rows that a warp takes at once: as many as the largest request
-// needs for its rows, four at most.
+// needs for its rows, four at most; where larger ones go elsewhere, as many as a
+// query token needs.
 int rows8(const moe_cache_attn *d, const moe_cache4 *cache) {
-    const int64_t rows = (int64_t)std::max(1, d->max_q) * (d->q_heads / cache->kv_heads);
+    const int64_t rows = has_wide(d, cache) ? d->q_heads / cache->kv_heads : most_rows(d, cache);
     return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
 }
 
@@ -759,11 +738,15 @@ int ctas_of(int nq) { return sm_count() * (nq == 4 ? 1 : 2); }
 
 }  // namespace
 
-size_t attention4_plan_bytes(const moe_cache_attn *d) { return align_up(sizeof(int32_t) * (d->requests + 2)); }
+static size_t attention4_plan_bytes(const moe_cache_attn *d) { return align_up(sizeof(int32_t) * (d->requests + 2)); }
 
-size_t attention4_workspace(const moe_cache_attn *d, const moe_cache4 *cache) {
+static size_t attention4_few_workspace(const moe_cache_attn *d, const moe_cache4 *cache) {
     const int nq = rows8(d, cache);
     return attention4_plan_bytes(d) + align_up(sizeof(float) * 2 * (size_t)ctas_of(nq) * 8 * nq * (cache->dim + 2));
+}
+
+size_t attention4_workspace(const moe_cache_attn *d, const moe_cache4 *cache) {
+    return attention4_few_workspace(d, cache) + (has_wide(d, cache) ? attention4_wide_workspace(d, cache) : 0);
 }
 
 int launch_attention4(const moe_cache_attn *d, const moe_cache4 *cache, const void *q, const int32_t *table,
@@ -794,9 +777,15 @@ int launch_attention4(const moe_cache_attn *d, const moe_cache4 *cache, const vo
     a.out_bf16 = out_dtype == MOE_OUT_BF16;
     a.scale_log2 = d->scale * 1.44269504f;
     const int nq = rows8(d, cache);
+    const bool wide = has_wide(d, cache);
+    a.few_rows = wide ? kFewRows : INT32_MAX;
     a.ctas = ctas_of(nq);
-    if (cache->dim == 64) return nq == 1 ? launch<64, 1>(a, s) : nq == 2 ? launch<64, 2>(a, s) : launch<64, 4>(a, s);
-    return nq == 1 ? launch<128, 1>(a, s) : nq == 2 ? launch<128, 2>(a, s) : launch<128, 4>(a, s);
+    if (int rc = cache->dim == 64 ? nq == 1 ? launch<64, 1>(a, s) : nq == 2 ? launch<64, 2>(a, s) : launch<64, 4>(a, s)
+                 : nq == 1 ? launch<128, 1>(a, s) : nq == 2 ? launch<128, 2>(a, s) : launch<128, 4>(a, s))
+        return rc;
+    if (!wide) return MOE_OK;
+    return launch_attention4_wide(a, d, cache, kFewRows,
+                                  static_cast<uint8_t *>(ws) + attention4_few_workspace(d, cache), s);
 }
 
 }  // namespace moe

@@ -1,0 +1,777 @@
+// Attention of many query rows over the four-bit cache (chunks of prompts), on
+// the tensor cores' fifth-generation kinds:
+//   S = Q K^T,  P = 2^(S - m),  O += P V,  o = O / sum P
+//
+// A CTA takes 256 rows (query heads of one KV head, query tokens one after the
+// other) as two tiles of 128, and passes over the keys and values in tiles of
+// 128 tokens.  tcgen05.mma (fp16 operands, fp32 in tensor memory): S from Q and
+// K in shared memory; O from P, which a tile's softmax leaves in tensor memory
+// where S was, and V in shared memory with channels contiguous.  While one
+// tile's softmax works on its S the products of the other are under way:
+//   QK0 QK1 PV0 | QK0 PV1 QK1 PV0 | QK0 PV1 QK1 ...
+// Warps 0-3 and 4-7 are the softmax of tile 0 and 1, a thread to a row; warps
+// 8-11 unpack keys and values; warp 12 issues the products.
+//
+// Four-bit codes become fp16 (cvt) times 2^(e - E + 13), E the largest exponent
+// of the tile's keys, or that the piece has met in its values; what lies 28
+// binades below E counts as zero.  Keys: 2^E goes into the row's factor.
+// Values: where E grows, O is scaled when P is made.  q is fp16 times a power of
+// two for each row.  m is raised only where a score passes it by 8 (in log2), so
+// S is read once and O hardly ever.  A value that is NaN counts as zero in the
+// products; rows that give it weight remember its block.
+//
+// Work: one unit for each tile of tokens that a group of 256 rows sees (causal:
+// fewer for earlier rows) and some for its beginning and end; each CTA takes as
+// many neighbouring units as any other.  Rows cut between CTAs leave partial
+// results, at most two groups a CTA, which a last kernel joins.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "attention4.cuh"
+#include "mx4.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+using namespace ptx;
+
+constexpr int kWideRows = 256, kM = 128, kTok = 128;
+constexpr int kSoftWarps = 8, kUnpackWarps = 4, kMmaWarp = kSoftWarps + kUnpackWarps;
+// Registers a thread, by warpgroups (the last has the products' warp and three idle
+// ones): together no more than the 512 x 128 that the block starts with.
+constexpr int kWideThreads = 512, kSoftRegs = 176, kUnpackRegs = 112, kMmaRegs = 40;
+static_assert(2 * kSoftRegs + kUnpackRegs + kMmaRegs <= 4 * 128, "registers");
+constexpr int kStages = 2, kInfos = 4;
+constexpr int kTmemCols = 512;
+constexpr int kPieceTiles = 2;     // what the beginning and end of a piece cost, in tiles
+constexpr float kLazy = 8.0f;
+constexpr int kBias = 13;
+
+struct WideArgs {
+    AttnArgs a;
+    int few_rows, max_entries;
+    int64_t *units;        // [entries + 1]: units before each (request, group of rows), of one head
+    int64_t *per;          // units a CTA
+    int32_t *entry_request, *first_entry;   // [entries], [requests + 1]
+};
+
+__device__ __forceinline__ float ex2w(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+    const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// fp16 operands, K-major; B with channels contiguous where `mn`
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool mn) {
+    return (1u << 4) | ((uint32_t)mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// V: rows of 128 bytes (64 channels of a token), 128-byte swizzle; eight tokens 1024 bytes,
+// the next 64 channels kTok rows on
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kTok * 128 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// A group of rows of a request: what it sees, in tiles.
+struct RowGroup {
+    int rowbase, nrows, pos_lo, pos_hi, lo, tiles;
+};
+__device__ __forceinline__ RowGroup row_group(const AttnArgs &a, const AttnRequest &r, int qt) {
+    RowGroup w;
+    w.rowbase = qt * kWideRows;
+    w.nrows = (int)min((int64_t)kWideRows, (int64_t)r.n * a.G - w.rowbase);
+    w.pos_lo = r.len - r.n + w.rowbase / a.G;
+    w.pos_hi = r.len - r.n + (w.rowbase + w.nrows - 1) / a.G;
+    w.lo = a.window && w.pos_lo >= a.window ? (w.pos_lo - a.window + 1) / kAttnTile * kAttnTile : 0;
+    w.tiles = max(1, (w.pos_hi - w.lo + kTok) / kTok);   // pos_hi + 1 tokens
+    return w;
+}
+
+// ---- the work list: one CTA -------------------------------------------------------------
+__device__ __forceinline__ int64_t scan_add(int64_t v, int64_t *sh) {   // inclusive, over 1024 threads
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+    }
+    __syncthreads();
+    if (lane == 31) sh[warp] = v;
+    __syncthreads();
+    int64_t x = sh[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    const int64_t before = __shfl_sync(0xffffffffu, x, max(warp - 1, 0));
+    return v + (warp > 0 ? before : 0);
+}
+
+__global__ void __launch_bounds__(1024) wide_plan_kernel(const WideArgs w, int ctas) {
+    __shared__ int s_first[kAttnMaxRequests + 1];
+    __shared__ int64_t sh[32], s_total;
+    const AttnArgs &a = w.a;
+    const int tid = threadIdx.x;
+    pdl_launch_dependents();
+    pdl_wait();
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 1024) {
+        const int b = b0 + tid;
+        int64_t groups = 0;
+        if (b < a.B) {
+            const AttnRequest r = attn_request(a, b);
+            const int64_t rows = (int64_t)r.n * a.G;
+            if (r.bad && a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
+            if (rows > w.few_rows) groups = (rows + kWideRows - 1) / kWideRows;
+        }
+        const int64_t v = scan_add(groups, sh);
+        if (b < a.B) {
+            // rows that more than one request claims: there is room for as many as there are rows
+            s_first[b] = (int)min(before + v - groups, (int64_t)w.max_entries);
+            w.first_entry[b] = s_first[b];
+        }
+        if (tid == 1023) s_total = v;
+        __syncthreads();
+        before += s_total;
+        __syncthreads();
+    }
+    if (before > w.max_entries && tid == 0 && a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
+    const int entries = (int)min(before, (int64_t)w.max_entries);
+    if (tid == 0) s_first[a.B] = w.first_entry[a.B] = entries;
+    __syncthreads();
+    int64_t units = 0;
+    for (int e0 = 0; e0 < entries; e0 += 1024) {
+        const int e = e0 + tid;
+        int64_t n = 0;
+        if (e < entries) {
+            int lo = 0, hi = a.B;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s_first[mid] <= e) lo = mid;
+                else hi = mid;
+            }
+            w.entry_request[e] = lo;
+            n = row_group(a, attn_request(a, lo), e - s_first[lo]).tiles + kPieceTiles;
+        }
+        const int64_t v = scan_add(n, sh);
+        if (e < entries) w.units[e] = units + v - n;
+        if (tid == 1023) s_total = v;
+        __syncthreads();
+        units += s_total;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        w.units[entries] = units;
+        w.per[0] = max((int64_t)1, (units * a.Hk + ctas - 1) / ctas);
+    }
+}
+
+// ---- pieces -----------------------------------------------------------------------------
+struct Piece {
+    AttnRequest r;
+    RowGroup g;
+    int b, h, c0, c1;
+};
+
+// The piece that unit u belongs to, as far as u_end; u moves past it.  c0 == c1: nothing
+// of it is computed here.
+__device__ __forceinline__ Piece take_piece(const WideArgs &w, int64_t &u, int64_t u_end, int entries, int64_t total) {
+    Piece p;
+    p.h = (int)(u / total);
+    const int64_t local = u - p.h * total;
+    int lo = 0, hi = entries;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (w.units[mid] <= local) lo = mid;
+        else hi = mid;
+    }
+    p.b = w.entry_request[lo];
+    p.r = attn_request(w.a, p.b);
+    p.g = row_group(w.a, p.r, lo - w.first_entry[p.b]);
+    const int x0 = (int)(local - w.units[lo]);
+    const int x1 = (int)min((int64_t)p.g.tiles + kPieceTiles, x0 + u_end - u);
+    p.c0 = max(0, x0 - kPieceTiles);
+    p.c1 = max(0, x1 - kPieceTiles);
+    u += x1 - x0;
+    return p;
+}
+
+struct Info {          // of a tile of tokens, from those who unpack it
+    float ek;          // 2^(E - 127 - kBias) of its keys
+    float grown;       // what O is to be multiplied by before this tile
+    float ev;          // 2^(E - 127 - kBias) of the values so far
+    uint32_t bad;      // bit i: tokens 16 i .. are on a page that is not there
+    uint32_t nan;      // a value of the tile is NaN
+};
+
+template <int D>
+struct WideShape {
+    static constexpr int kHalf = kTok * 128;               // 128 rows of 64 channels
+    static constexpr int kTileBytes = D / 64 * kHalf;      // Q of a tile, K or V of a stage
+    static constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + kStages * kTileBytes;
+    static constexpr int kUsed = kV + kStages * kTileBytes + 1024;
+    // one CTA on an SM: each takes all of the tensor memory
+    static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
+    static constexpr int kO = 2 * kTok;                    // columns: S0, S1, O0, O1
+};
+
+template <int D>
+__global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const WideArgs w) {
+    using S = WideShape<D>;
+    constexpr int kBlocks = D / 32;
+    extern __shared__ uint8_t dsmem[];
+    __shared__ uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], info_full[kInfos];
+    __shared__ uint64_t s_full[2], p_ready[2], q_full, o_full, drain_bar;
+    __shared__ uint64_t e_full[2];
+    __shared__ Info s_info[kInfos];
+    __shared__ uint2 s_nan[kInfos][kTok / 2];        // a byte for each token and channel block
+    __shared__ uint4 s_e[2][kUnpackWarps];           // each warp's largest exponents, bad pages, NaN
+    __shared__ uint32_t tmem_slot;
+    __shared__ int s_abort;
+    const AttnArgs &a = w.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int *abort_flag = &s_abort;
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&k_full[s]), kUnpackWarps);
+            mbar_init(smem_u32(&v_full[s]), kUnpackWarps);
+            mbar_init(smem_u32(&k_empty[s]), 1);
+            mbar_init(smem_u32(&v_empty[s]), 1);
+        }
+        for (int s = 0; s < kInfos; ++s) mbar_init(smem_u32(&info_full[s]), kUnpackWarps);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&e_full[s]), kUnpackWarps);
+            mbar_init(smem_u32(&s_full[s]), 1);
+            mbar_init(smem_u32(&p_ready[s]), 4);
+        }
+        mbar_init(smem_u32(&q_full), kSoftWarps);
+        mbar_init(smem_u32(&o_full), 1);
+        mbar_init(smem_u32(&drain_bar), 1);
+        s_abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const uint32_t base = (smem_u32(dsmem) + 1023u) & ~1023u;
+    uint8_t *smem = dsmem + (base - smem_u32(dsmem));
+    const int entries = w.first_entry[a.B];
+    const int64_t total = w.units[entries], all = total * a.Hk, per = w.per[0];
+    int64_t u = min(all, (int64_t)blockIdx.x * per);
+    const int64_t u_end = min(all, u + per);
+    uint32_t tiles = 0, pieces = 0;   // counted by every role alike
+    bool ok = true;
+    // a wait of a whole warp
+    auto wait = [&](uint64_t &bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_bounded(smem_u32(&bar), parity, abort_flag, a.status, MOE_DEV_TIMEOUT));
+    };
+
+    if (warp < kSoftWarps) {
+        more_registers<kSoftRegs>();
+        // ---- softmax, a thread to a row ---------------------------------------------------
+        const int mt = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + mt * kTok, to = tmem + lanes + S::kO + mt * D;
+        uint32_t mine = 0;   // tiles of this half, of all pieces
+        while (u < u_end && ok) {
+            const Piece p = take_piece(w, u, u_end, entries, total);
+            if (p.c0 == p.c1) continue;
+            const int rr = mt * kM + row, flat = p.g.rowbase + rr;
+            const bool there = rr < p.g.nrows;
+            const int64_t at = (int64_t)(p.r.row0 + flat / a.G) * a.Hq + p.h * a.G + flat % a.G;
+            float mult = 0.0f;
+            {   // the row's query: fp16 times 2^up
+                uint4 raw[D / 8];
+                float amax = 0.0f;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    raw[i] = there ? __ldg(reinterpret_cast<const uint4 *>(a.q + at * D) + i) : make_uint4(0, 0, 0, 0);
+                    const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[j] << 16)), fabsf(__uint_as_float(x[j] & 0xffff0000u))));
+                }
+                const int up = 14 + 127 - min(max((int)(__float_as_uint(amax) >> 23), 27), 254);
+                const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+                mult = a.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
+                uint8_t *q = smem + S::kQ + mt * S::kTileBytes + row * 128;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                    uint32_t y[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        y[j] = half2_of(__uint_as_float(x[j] << 16) * f, __uint_as_float(x[j] & 0xffff0000u) * f);
+                    *reinterpret_cast<uint4 *>(q + (i >> 3) * S::kHalf + (((i & 7) ^ (row & 7)) << 4)) =
+                        make_uint4(y[0], y[1], y[2], y[3]);
+                }
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&q_full));
+            const int pos = p.r.len - p.r.n + (p.g.rowbase + min(rr, p.g.nrows - 1)) / a.G;
+            const bool used = mt == 0 || p.g.nrows > kM;
+            float ref = 0.0f, pass = -INFINITY, sum = 0.0f, ev = 0.0f;
+            uint32_t nans = 0;   // channel blocks that are NaN for this row
+            for (int c = p.c0; c < p.c1; ++c, ++tiles) {
+                if (!used) continue;
+                const uint32_t in = tiles % kInfos;
+                ok = wait(info_full[in], (tiles / kInfos) & 1) && wait(s_full[mt], mine & 1);
+                ++mine;
+                if (!ok) break;
+                tc_fence_after();
+                const Info info = s_info[in];
+                ev = info.ev;
+                const int t0 = p.g.lo + c * kTok;
+                const bool edge = t0 + kTok - 1 > p.g.pos_lo || (a.window && t0 <= p.g.pos_hi - a.window) || info.bad;
+                const int upto = pos - t0, from = a.window ? pos - a.window - t0 : -1;   // columns from < i <= upto
+                const float xs = mult * info.ek;
+                uint32_t pk[kTok / 2];
+                float part, shrink = info.grown;
+                for (int again = 0; again < 2; ++again) {
+                    float top = -INFINITY;
+                    part = 0.0f;
+                    uint32_t r[2][16];
+                    tmem_ld16(ts, r[0]);
+#pragma unroll
+                    for (int q = 0; q < kTok / 16; ++q) {
+                        tmem_wait_ld(r[q & 1]);
+                        if (q + 1 < kTok / 16) tmem_ld16(ts + 16 * (q + 1), r[(q + 1) & 1]);
+                        float x[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] = fmaf(__uint_as_float(r[q & 1][i]), xs, -ref);
+                        if (edge) {
+                            const bool bad = info.bad >> q & 1u;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (bad || 16 * q + i > upto || 16 * q + i <= from) x[i] = -INFINITY;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            top = fmaxf(top, fmaxf(x[i], x[i + 1]));
+                            x[i] = ex2w(x[i]);
+                            x[i + 1] = ex2w(x[i + 1]);
+                            part += x[i] + x[i + 1];
+                            pk[8 * q + i / 2] = half2_of(x[i], x[i + 1]);
+                        }
+                    }
+                    if (again || !__any_sync(0xffffffffu, top > pass)) break;
+                    const float rise = top == -INFINITY ? 0.0f : pass == -INFINITY ? top : fmaxf(top, 0.0f);
+                    if (top != -INFINITY) pass = kLazy;
+                    ref += rise;
+                    const float f = ex2w(-rise);
+                    sum *= f;
+                    shrink *= f;
+                }
+                sum += part;
+                if (c > p.c0 && __any_sync(0xffffffffu, shrink != 1.0f)) {
+#pragma unroll 1
+                    for (int q = 0; q < D / 16; ++q) {
+                        uint32_t r[16];
+                        tmem_ld16(to + 16 * q, r);
+                        tmem_wait_ld(r);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * shrink);
+                        tmem_st16(to + 16 * q, r);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < kTok / 32; ++q) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) r[i] = pk[16 * q + i];
+                    tmem_st16(ts + 16 * q, r);
+                }
+                tmem_wait_st();
+                if (info.nan) {
+#pragma unroll 1
+                    for (int q = 0; q < kTok / 32; ++q) {
+                        uint32_t r[16];
+                        tmem_ld16(ts + 16 * q, r);
+                        tmem_wait_ld(r);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const uint2 n8 = s_nan[in][16 * q + i];
+                            if (r[i] & 0x7fffu) nans |= n8.x;
+                            if (r[i] & 0x7fff0000u) nans |= n8.y;
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&p_ready[mt]));
+            }
+            ok = ok && wait(o_full, pieces & 1);
+            ++pieces;
+            if (!ok) break;
+            tc_fence_after();
+            const bool whole = p.c0 == 0 && p.c1 == p.g.tiles;
+            float *dst = a.part + (int64_t)(2 * blockIdx.x + (p.c0 == 0)) * kWideRows * (D + 2);
+            const float inv = !whole ? ev : sum == 0.0f ? 0.0f : ev / sum;
+            if (!whole) dst[kWideRows * D + rr] = pass == -INFINITY ? -INFINITY : ref, dst[kWideRows * (D + 1) + rr] = sum;
+            else if (there && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.69314718f;
+            if (used) {
+#pragma unroll
+                for (int q = 0; q < D / 16; ++q) {
+                    uint32_t r[16];
+                    tmem_ld16(to + 16 * q, r);
+                    tmem_wait_ld(r);
+                    float x[16];
+                    const bool gone = nans >> (8 * (q / 2)) & 1u;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = gone ? NAN : inv == 0.0f ? 0.0f : __uint_as_float(r[i]) * inv;
+                    if (!there) continue;
+                    if (!whole || !a.out_bf16) {
+                        float4 *o = whole ? reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at * D + 16 * q)
+                                          : reinterpret_cast<float4 *>(dst + (int64_t)rr * D + 16 * q);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    } else {
+                        uint32_t y[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                            y[i] = *reinterpret_cast<const uint32_t *>(&b2);
+                        }
+                        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at * D + 16 * q);
+                        o[0] = make_uint4(y[0], y[1], y[2], y[3]);
+                        o[1] = make_uint4(y[4], y[5], y[6], y[7]);
+                    }
+                }
+            }
+            tc_fence_before();   // O may be written again once the next query is there
+        }
+    } else if (warp < kMmaWarp) {
+        fewer_registers<kUnpackRegs>();
+        // ---- keys and values into shared memory -------------------------------------------
+        // A lane takes 16-byte pieces of codes (32 channels, one scale): eight
+        // neighbouring lanes the same piece of eight tokens, so that stores meet no
+        // bank twice; a warp's 32 tokens in `I` rounds.
+        constexpr int kIn = D / 32, I = kIn, kRoundRows = 32 / kIn;
+        const int dw = warp - kSoftWarps;
+        const int pc = D == 128 ? lane >> 3 : lane >> 3 & 1;
+        const int pr = D == 128 ? lane & 7 : (lane & 7) + (lane >> 4) * 8;
+        const int64_t kv_rows = (int64_t)a.Hk << a.page_shift;
+        const int in_page = (1 << a.page_shift) - 1;
+        while (u < u_end && ok) {
+            const Piece p = take_piece(w, u, u_end, entries, total);
+            if (p.c0 == p.c1) continue;
+            const int32_t *table = a.table + (int64_t)p.b * a.max_pages;
+            uint4 kc[I], vc[I];
+            uint32_t kb[I], vb[I], state[I];   // state: 0 there, 1 nothing to see, 2 no page
+            int ids[I];
+            auto load_ids = [&](int c) {
+#pragma unroll
+                for (int i = 0; i < I; ++i) {
+                    const int t = p.g.lo + c * kTok + 32 * dw + kRoundRows * i + pr;
+                    ids[i] = c < p.c1 && t <= p.g.pos_hi ? __ldg(table + (t >> a.page_shift)) : -2;
+                }
+            };
+            auto load = [&](int c) {
+#pragma unroll
+                for (int i = 0; i < I; ++i) {
+                    const int t = p.g.lo + c * kTok + 32 * dw + kRoundRows * i + pr;
+                    const int id = ids[i];
+                    state[i] = id == -2 ? 1u : id < 0 || id >= a.pages ? 2u : 0u;
+                    kc[i] = vc[i] = make_uint4(0, 0, 0, 0);
+                    kb[i] = vb[i] = 0;
+                    if (state[i] == 0) {
+                        const int64_t r = (((int64_t)id * 2 * a.Hk + p.h) << a.page_shift) + (t & in_page);
+                        kc[i] = __ldg(reinterpret_cast<const uint4 *>(a.codes + r * (D / 2)) + pc);
+                        vc[i] = __ldg(reinterpret_cast<const uint4 *>(a.codes + (r + kv_rows) * (D / 2)) + pc);
+                        kb[i] = __ldg(a.scales + r * kBlocks + pc);
+                        vb[i] = __ldg(a.scales + (r + kv_rows) * kBlocks + pc);
+                    } else if (state[i] == 2 && a.status) {
+                        atomicOr(a.status, MOE_DEV_BAD_INDEX);
+                    }
+                }
+            };
+            load_ids(p.c0);
+            load(p.c0);
+            load_ids(p.c0 + 1);
+            int erun = 0;   // E of the values so far
+            for (int c = p.c0; c < p.c1; ++c, ++tiles) {
+                const uint32_t stage = tiles % kStages, in = tiles % kInfos;
+                uint4 k[I], v[I];
+                uint32_t ke[I], ve[I], bad = 0, nan = 0, mk = 0, mv = 0;
+#pragma unroll
+                for (int i = 0; i < I; ++i) {
+                    k[i] = kc[i], v[i] = vc[i], ke[i] = kb[i], ve[i] = vb[i];
+                    if (state[i] == 2) bad |= 1u << ((32 * dw + kRoundRows * i + pr) >> 4);
+                    if (ke[i] != 255u) mk = max(mk, ke[i]);
+                    if (ve[i] != 255u) mv = max(mv, ve[i]);
+                    else nan = 1;
+                }
+                load(c + 1);        // under way while this tile is unpacked
+                load_ids(c + 2);
+                mk = __reduce_max_sync(0xffffffffu, mk);
+                mv = __reduce_max_sync(0xffffffffu, mv);
+                bad = __reduce_or_sync(0xffffffffu, bad);
+                nan = __reduce_or_sync(0xffffffffu, nan);
+                if (lane == 0) {
+                    s_e[tiles & 1][dw] = make_uint4(mk, mv, bad, nan);
+                    mbar_arrive(smem_u32(&e_full[tiles & 1]));
+                }
+                ok = wait(e_full[tiles & 1], (tiles >> 1) & 1);
+                if (!ok) break;
+                int ek = 0, ev = erun;
+#pragma unroll
+                for (int x = 0; x < kUnpackWarps; ++x) {
+                    const uint4 e = s_e[tiles & 1][x];
+                    ek = max(ek, (int)e.x), ev = max(ev, (int)e.y), bad |= e.z, nan |= e.w;
+                }
+                ok = wait(k_empty[stage], ((tiles / kStages) & 1) ^ 1u);
+                if (!ok) break;
+                if (dw == 0 && lane == 0) {
+                    Info info;
+                    info.ek = ex2w((float)(ek - 127 - kBias));
+                    info.grown = ev == erun || c == p.c0 ? 1.0f : ex2w((float)(erun - ev));
+                    info.ev = ex2w((float)(ev - 127 - kBias));
+                    info.bad = bad, info.nan = nan;
+                    s_info[in] = info;
+                }
+                if (nan)
+#pragma unroll
+                    for (int i = 0; i < I; ++i) {
+                        const int t = 32 * dw + kRoundRows * i + pr;
+                        uint8_t *n = reinterpret_cast<uint8_t *>(s_nan[in]) + 4 * t + pc;
+                        n[0] = ve[i] == 255u;
+                        if (kIn == 2) n[2] = 0;
+                    }
+                erun = ev;
+                // codes of eight channels -> 16 bytes, times 2^(e - E + kBias)
+                auto widen = [&](const uint4 &codes, uint32_t byte, int e, uint8_t *dst, int t, bool keys) {
+                    uint32_t f = (uint32_t)max((int)byte - e + kBias + 15, 0) << 10;
+                    if (byte == 255u) f = keys ? 0x7e00u : 0u;
+                    f *= 0x10001u;
+                    const uint32_t x[4] = {codes.x, codes.y, codes.z, codes.w};
+                    uint8_t *rowp = dst + (pc >> 1) * S::kHalf + t * 128;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t hv[4];
+                        mx4_half8(x[j], hv);
+                        *reinterpret_cast<uint4 *>(rowp + ((((pc & 1) * 4 + j) ^ (t & 7)) << 4)) =
+                            make_uint4(mul_half2(hv[0], f), mul_half2(hv[1], f), mul_half2(hv[2], f), mul_half2(hv[3], f));
+                    }
+                };
+#pragma unroll
+                for (int i = 0; i < I; ++i)
+                    widen(k[i], ke[i], ek, smem + S::kK + stage * S::kTileBytes, 32 * dw + kRoundRows * i + pr, true);
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&info_full[in]));
+                    mbar_arrive(smem_u32(&k_full[stage]));
+                }
+                ok = wait(v_empty[stage], ((tiles / kStages) & 1) ^ 1u);
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < I; ++i)
+                    widen(v[i], ve[i], ev, smem + S::kV + stage * S::kTileBytes, 32 * dw + kRoundRows * i + pr, false);
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&v_full[stage]));
+            }
+        }
+    } else {
+        fewer_registers<kMmaRegs>();
+        // ---- products ---------------------------------------------------------------------
+        if (warp > kMmaWarp) u = u_end;   // idle
+        const bool elected = elect_one();
+        constexpr uint32_t kQK = idesc_f16(kM, kTok, false), kPV = idesc_f16(kM, D, true);
+        uint32_t made[2] = {0, 0};   // P of each half that products have taken
+        while (u < u_end && ok) {
+            const Piece p = take_piece(w, u, u_end, entries, total);
+            if (p.c0 == p.c1) continue;
+            const int n = p.c1 - p.c0, halves = p.g.nrows > kM ? 2 : 1;
+            auto qk = [&](int mt, uint32_t tile, bool last) {
+                const uint32_t stage = tile % kStages;
+                if (elected) {
+                    const uint64_t q = sdesc_k_sw128(base + S::kQ + mt * S::kTileBytes);
+                    const uint64_t k = sdesc_k_sw128(base + S::kK + stage * S::kTileBytes);
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s) {
+                        const uint32_t off = (s >> 2) * (S::kHalf >> 4) + (s & 3) * 2;
+                        mma_f16(tmem + mt * kTok, q + off, k + off, kQK, s > 0);
+                    }
+                    mma_commit(smem_u32(&s_full[mt]));
+                    if (last) mma_commit(smem_u32(&k_empty[stage]));
+                }
+                __syncwarp();
+            };
+            auto pv = [&](int mt, uint32_t tile, bool first, bool last) {
+                const uint32_t stage = tile % kStages;
+                const bool good = wait(v_full[stage], (tile / kStages) & 1) && wait(p_ready[mt], made[mt] & 1);
+                ++made[mt];
+                if (!good) return false;
+                tc_fence_after();
+                if (elected) {
+                    const uint64_t v = sdesc_mn_sw128(base + S::kV + stage * S::kTileBytes);
+#pragma unroll
+                    for (int s = 0; s < kTok / 16; ++s)
+                        mma_f16_ta(tmem + S::kO + mt * D, tmem + mt * kTok + 8 * s, v + s * (2048 >> 4), kPV, !first || s > 0);
+                    if (last) mma_commit(smem_u32(&v_empty[stage]));
+                }
+                __syncwarp();
+                return true;
+            };
+            ok = wait(q_full, pieces & 1);
+            ++pieces;
+            for (int j = 0; j < n && ok; ++j) {
+                const uint32_t tile = tiles + j;
+                ok = wait(k_full[tile % kStages], (tile / kStages) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                qk(0, tile, halves == 1);
+                if (halves == 2) {
+                    if (j > 0) ok = pv(1, tile - 1, j == 1, true);
+                    if (!ok) break;
+                    qk(1, tile, true);
+                }
+                ok = pv(0, tile, j == 0, halves == 1);
+            }
+            if (ok && halves == 2) ok = pv(1, tiles + n - 1, n == 1, true);
+            tiles += n;
+            if (elected && ok) mma_commit(smem_u32(&o_full));
+            __syncwarp();
+        }
+        if (elected && warp == kMmaWarp) {
+            mma_commit(smem_u32(&drain_bar));
+            wait_drain(smem_u32(&drain_bar), 0);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the pieces of rows that were cut: one warp a query row and head.
+template <int D>
+__global__ void __launch_bounds__(256) wide_join_kernel(const WideArgs w) {
+    const AttnArgs &a = w.a;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    if (i >= (int64_t)a.rows * a.Hq) return;
+    const int row = (int)(i / a.Hq), head = (int)(i - (int64_t)row * a.Hq);
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.starts[mid] <= row) lo = mid;
+        else hi = mid;
+    }
+    const AttnRequest r = attn_request(a, lo);
+    if (row < r.row0 || row >= r.row0 + r.n || (int64_t)r.n * a.G <= w.few_rows) return;
+    const int h = head / a.G;
+    const int64_t flat = (int64_t)(row - r.row0) * a.G + head % a.G;
+    const int qt = (int)(flat / kWideRows), rr = (int)(flat - (int64_t)qt * kWideRows);
+    const int entries = w.first_entry[a.B], e = w.first_entry[lo] + qt;
+    if (e >= entries || w.entry_request[e] != lo) return;
+    const int64_t per = w.per[0], u0 = h * w.units[entries] + w.units[e] + kPieceTiles;
+    const int64_t u1 = h * w.units[entries] + w.units[e + 1] - 1;
+    const int k0 = (int)(u0 / per), k1 = (int)(u1 / per);
+    if (k0 == k1) return;   // one CTA had all of it
+    attn_join<D>(a, kWideRows, rr, i, k0, k1, lane);
+}
+
+int entries_bound(const moe_cache_attn *d, int G) {
+    return (int)std::min<int64_t>((int64_t)d->rows * G / kWideRows + std::min(d->requests, d->rows), 1 << 30);
+}
+
+struct WideLayout {
+    size_t units, per, request, first, part, total;
+};
+WideLayout wide_layout(const moe_cache_attn *d, const moe_cache4 *cache) {
+    WideLayout l;
+    const size_t e = (size_t)entries_bound(d, d->q_heads / cache->kv_heads);
+    l.units = 0;
+    l.per = align_up(8 * (e + 1));
+    l.request = l.per + align_up(8);
+    l.first = l.request + align_up(4 * e);
+    l.part = l.first + align_up(4 * ((size_t)d->requests + 1));
+    l.total = l.part + align_up(sizeof(float) * 2 * (size_t)sm_count() * kWideRows * (cache->dim + 2));
+    return l;
+}
+
+template <int D>
+int launch(const WideArgs &w, cudaStream_t s) {
+    const int ctas = sm_count();
+    MOE_CUDA_TRY(cudaFuncSetAttribute(attention4_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      WideShape<D>::kSmem));
+    if (int rc = launch_dependent(wide_plan_kernel, dim3(1), dim3(1024), 0, s, (const WideArgs)w, ctas)) return rc;
+    if (int rc = launch_dependent(attention4_wide_kernel<D>, dim3((unsigned)ctas), dim3(kWideThreads),
+                                  WideShape<D>::kSmem, s, (const WideArgs)w))
+        return rc;
+    const int64_t warps = (int64_t)w.a.rows * w.a.Hq;
+    return launch_dependent(wide_join_kernel<D>, dim3((unsigned)ceil_div(warps, 8)), dim3(256), 0, s, (const WideArgs)w);
+}
+
+}  // namespace
+
+size_t attention4_wide_workspace(const moe_cache_attn *d, const moe_cache4 *cache) {
+    return wide_layout(d, cache).total;
+}
+
+int launch_attention4_wide(const AttnArgs &args, const moe_cache_attn *d, const moe_cache4 *cache, int few_rows,
+                           void *ws, cudaStream_t s) {
+    const WideLayout l = wide_layout(d, cache);
+    uint8_t *p = static_cast<uint8_t *>(ws);
+    WideArgs w;
+    w.a = args;
+    w.a.part = reinterpret_cast<float *>(p + l.part);
+    w.few_rows = few_rows;
+    w.max_entries = entries_bound(d, args.G);
+    w.units = reinterpret_cast<int64_t *>(p + l.units);
+    w.per = reinterpret_cast<int64_t *>(p + l.per);
+    w.entry_request = reinterpret_cast<int32_t *>(p + l.request);
+    w.first_entry = reinterpret_cast<int32_t *>(p + l.first);
+    return cache->dim == 64 ? launch<64>(w, s) : launch<128>(w, s);
+}
+
+}  // namespace moe
