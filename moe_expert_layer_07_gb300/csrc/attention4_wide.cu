@@ -17,7 +17,7 @@
 // binades below E counts as zero.  Keys: 2^E goes into the row's factor.
 // Values: where E grows, O is scaled when P is made.  q is fp16 times a power of
 // two for each row.  m is raised only where a score passes it by 8 (in log2), so
-// S is read once and O hardly ever.  A value that is NaN counts as zero in the
+// S is read once and O hardly ever; it rises by whole powers of two.  A value that is NaN counts as zero in the
 // products; rows that give it weight remember its block.
 //
 // Work: one unit for each tile of tokens that a group of 256 rows sees (causal:
@@ -40,10 +40,7 @@ using namespace ptx;
 
 constexpr int kWideRows = 256, kM = 128, kTok = 128;
 constexpr int kSoftWarps = 8, kUnpackWarps = 4, kMmaWarp = kSoftWarps + kUnpackWarps;
-// Registers a thread, by warpgroups (the last has the products' warp and three idle
-// ones): together no more than the 512 x 128 that the block starts with.
-constexpr int kWideThreads = 512, kSoftRegs = 176, kUnpackRegs = 112, kMmaRegs = 40;
-static_assert(2 * kSoftRegs + kUnpackRegs + kMmaRegs <= 4 * 128, "registers");
+constexpr int kWideThreads = (kMmaWarp + 1) * 32;
 constexpr int kStages = 2, kInfos = 4;
 constexpr int kTmemCols = 512;
 constexpr int kPieceTiles = 2;     // what the beginning and end of a piece cost, in tiles
@@ -78,14 +75,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
-}
-template <int N>
-__device__ __forceinline__ void more_registers() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void fewer_registers() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 // D[tmem] (+)= A[tmem] * B[smem]
 __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
@@ -310,7 +299,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
     };
 
     if (warp < kSoftWarps) {
-        more_registers<kSoftRegs>();
         // ---- softmax, a thread to a row ---------------------------------------------------
         const int mt = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -324,23 +312,24 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             const int64_t at = (int64_t)(p.r.row0 + flat / a.G) * a.Hq + p.h * a.G + flat % a.G;
             float mult = 0.0f;
             {   // the row's query: fp16 times 2^up
-                uint4 raw[D / 8];
-                float amax = 0.0f;
-#pragma unroll
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + at * D);
+                const uint4 none = make_uint4(0, 0, 0, 0);
+                uint32_t most = 0;   // of the magnitudes, as bf16 bits moved up
+#pragma unroll 8
                 for (int i = 0; i < D / 8; ++i) {
-                    raw[i] = there ? __ldg(reinterpret_cast<const uint4 *>(a.q + at * D) + i) : make_uint4(0, 0, 0, 0);
-                    const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                    const uint4 v = there ? __ldg(src + i) : none;
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[j] << 16)), fabsf(__uint_as_float(x[j] & 0xffff0000u))));
+                    for (int j = 0; j < 4; ++j) most = max(most, max(x[j] << 16 & 0x7fff0000u, x[j] & 0x7fff0000u));
                 }
-                const int up = 14 + 127 - min(max((int)(__float_as_uint(amax) >> 23), 27), 254);
+                const int up = 14 + 127 - min(max((int)(most >> 23), 27), 254);
                 const float f = __uint_as_float((uint32_t)(127 + up) << 23);
                 mult = a.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
                 uint8_t *q = smem + S::kQ + mt * S::kTileBytes + row * 128;
-#pragma unroll
+#pragma unroll 4
                 for (int i = 0; i < D / 8; ++i) {
-                    const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                    const uint4 v = there ? __ldg(src + i) : none;
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
                     uint32_t y[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -369,44 +358,73 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 const bool edge = t0 + kTok - 1 > p.g.pos_lo || (a.window && t0 <= p.g.pos_hi - a.window) || info.bad;
                 const int upto = pos - t0, from = a.window ? pos - a.window - t0 : -1;   // columns from < i <= upto
                 const float xs = mult * info.ek;
-                uint32_t pk[kTok / 2];
-                float part, shrink = info.grown;
-                for (int again = 0; again < 2; ++again) {
-                    float top = -INFINITY;
-                    part = 0.0f;
-                    uint32_t r[2][16];
-                    tmem_ld16(ts, r[0]);
+                float shrink = info.grown;
+                // Half of the columns at a time: their P takes the place of a quarter of S
+                // that has been read.
 #pragma unroll
-                    for (int q = 0; q < kTok / 16; ++q) {
-                        tmem_wait_ld(r[q & 1]);
-                        if (q + 1 < kTok / 16) tmem_ld16(ts + 16 * (q + 1), r[(q + 1) & 1]);
-                        float x[16];
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t pk[kTok / 4];
+                    float part;
+#pragma unroll 1
+                    for (int again = 0; again < 2; ++again) {
+                        float top = -INFINITY;
+                        part = 0.0f;
+                        uint32_t r[2][16];
+                        tmem_ld16(ts + half * (kTok / 2), r[0]);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] = fmaf(__uint_as_float(r[q & 1][i]), xs, -ref);
-                        if (edge) {
-                            const bool bad = info.bad >> q & 1u;
+                        for (int q = 0; q < kTok / 32; ++q) {
+                            const int col = half * (kTok / 2) + 16 * q;
+                            tmem_wait_ld(r[q & 1]);
+                            if (q + 1 < kTok / 32) tmem_ld16(ts + col + 16, r[(q + 1) & 1]);
+                            float x[16];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (bad || 16 * q + i > upto || 16 * q + i <= from) x[i] = -INFINITY;
+                            for (int i = 0; i < 16; ++i) x[i] = fmaf(__uint_as_float(r[q & 1][i]), xs, -ref);
+                            if (edge) {
+                                const bool bad = info.bad >> (col >> 4) & 1u;
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    if (bad || col + i > upto || col + i <= from) x[i] = -INFINITY;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                top = fmaxf(top, fmaxf(x[i], x[i + 1]));
+                                x[i] = ex2w(x[i]);
+                                x[i + 1] = ex2w(x[i + 1]);
+                                part += x[i] + x[i + 1];
+                                pk[8 * q + i / 2] = half2_of(x[i], x[i + 1]);
+                            }
                         }
+                        if (again || !__any_sync(0xffffffffu, top > pass)) break;
+                        // m rises by whole powers of two, so that what is scaled stays exact
+                        const float rise = top == -INFINITY ? 0.0f : pass == -INFINITY ? ceilf(top) : fmaxf(ceilf(top), 0.0f);
+                        if (top != -INFINITY) pass = kLazy;
+                        ref += rise;
+                        const float f = ex2w(-rise);
+                        sum *= f;
+                        shrink *= f;
+                        if (half == 1) {   // P of the first half
+                            const uint32_t f2 = half2_of(f, f);
+                            tmem_wait_st();
+#pragma unroll 1
+                            for (int q = 0; q < 2; ++q) {
+                                uint32_t y[16];
+                                tmem_ld16(ts + 16 * q, y);
+                                tmem_wait_ld(y);
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            top = fmaxf(top, fmaxf(x[i], x[i + 1]));
-                            x[i] = ex2w(x[i]);
-                            x[i + 1] = ex2w(x[i + 1]);
-                            part += x[i] + x[i + 1];
-                            pk[8 * q + i / 2] = half2_of(x[i], x[i + 1]);
+                                for (int i = 0; i < 16; ++i) y[i] = mul_half2(y[i], f2);
+                                tmem_st16(ts + 16 * q, y);
+                            }
                         }
                     }
-                    if (again || !__any_sync(0xffffffffu, top > pass)) break;
-                    const float rise = top == -INFINITY ? 0.0f : pass == -INFINITY ? top : fmaxf(top, 0.0f);
-                    if (top != -INFINITY) pass = kLazy;
-                    ref += rise;
-                    const float f = ex2w(-rise);
-                    sum *= f;
-                    shrink *= f;
+                    sum += part;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t y[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) y[i] = pk[16 * q + i];
+                        tmem_st16(ts + half * (kTok / 4) + 16 * q, y);
+                    }
                 }
-                sum += part;
                 if (c > p.c0 && __any_sync(0xffffffffu, shrink != 1.0f)) {
 #pragma unroll 1
                     for (int q = 0; q < D / 16; ++q) {
@@ -417,13 +435,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                         for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * shrink);
                         tmem_st16(to + 16 * q, r);
                     }
-                }
-#pragma unroll
-                for (int q = 0; q < kTok / 32; ++q) {
-                    uint32_t r[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) r[i] = pk[16 * q + i];
-                    tmem_st16(ts + 16 * q, r);
                 }
                 tmem_wait_st();
                 if (info.nan) {
@@ -485,7 +496,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             tc_fence_before();   // O may be written again once the next query is there
         }
     } else if (warp < kMmaWarp) {
-        fewer_registers<kUnpackRegs>();
         // ---- keys and values into shared memory -------------------------------------------
         // A lane takes 16-byte pieces of codes (32 channels, one scale): eight
         // neighbouring lanes the same piece of eight tokens, so that stores meet no
@@ -500,53 +510,65 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             const Piece p = take_piece(w, u, u_end, entries, total);
             if (p.c0 == p.c1) continue;
             const int32_t *table = a.table + (int64_t)p.b * a.max_pages;
+            // What the next tile needs is on its way: pages two tiles ahead, scales one, codes
+            // from when this tile's have been taken.
             uint4 kc[I], vc[I];
-            uint32_t kb[I], vb[I], state[I];   // state: 0 there, 1 nothing to see, 2 no page
-            int ids[I];
-            auto load_ids = [&](int c) {
+            uint32_t kb[I], vb[I];   // scale bytes of this tile; 0 where there is nothing
+            uint32_t kn[I], vn[I];   // of the next
+            int ids[I] = {}, next_ids[I];   // pages of the next tile and of the one behind it; -2: nothing to see
+            auto token = [&](int c, int i) { return p.g.lo + c * kTok + 32 * dw + kRoundRows * i + pr; };
+            auto load_ids = [&](int c, int (&id)[I]) {
 #pragma unroll
                 for (int i = 0; i < I; ++i) {
-                    const int t = p.g.lo + c * kTok + 32 * dw + kRoundRows * i + pr;
-                    ids[i] = c < p.c1 && t <= p.g.pos_hi ? __ldg(table + (t >> a.page_shift)) : -2;
+                    const int t = token(c, i);
+                    id[i] = c < p.c1 && t <= p.g.pos_hi ? __ldg(table + (t >> a.page_shift)) : -2;
                 }
             };
-            auto load = [&](int c) {
+            auto there = [&](int id) { return id >= 0 && id < a.pages; };
+            auto row_of = [&](int c, int i) {
+                return (((int64_t)ids[i] * 2 * a.Hk + p.h) << a.page_shift) + (token(c, i) & in_page);
+            };
+            auto load_codes = [&](int c, uint4 (&x)[I], int64_t rows_on) {
+#pragma unroll
+                for (int i = 0; i < I; ++i)
+                    x[i] = there(ids[i]) ? __ldg(reinterpret_cast<const uint4 *>(a.codes + (row_of(c, i) + rows_on) * (D / 2)) + pc)
+                                         : make_uint4(0, 0, 0, 0);
+            };
+            uint32_t next_lost = 0;   // bit i: tokens 16 i .. of the next tile have no page
+            auto load_scales = [&](int c) {
+                next_lost = 0;
 #pragma unroll
                 for (int i = 0; i < I; ++i) {
-                    const int t = p.g.lo + c * kTok + 32 * dw + kRoundRows * i + pr;
-                    const int id = ids[i];
-                    state[i] = id == -2 ? 1u : id < 0 || id >= a.pages ? 2u : 0u;
-                    kc[i] = vc[i] = make_uint4(0, 0, 0, 0);
-                    kb[i] = vb[i] = 0;
-                    if (state[i] == 0) {
-                        const int64_t r = (((int64_t)id * 2 * a.Hk + p.h) << a.page_shift) + (t & in_page);
-                        kc[i] = __ldg(reinterpret_cast<const uint4 *>(a.codes + r * (D / 2)) + pc);
-                        vc[i] = __ldg(reinterpret_cast<const uint4 *>(a.codes + (r + kv_rows) * (D / 2)) + pc);
-                        kb[i] = __ldg(a.scales + r * kBlocks + pc);
-                        vb[i] = __ldg(a.scales + (r + kv_rows) * kBlocks + pc);
-                    } else if (state[i] == 2 && a.status) {
-                        atomicOr(a.status, MOE_DEV_BAD_INDEX);
+                    kn[i] = vn[i] = 0;
+                    if (there(ids[i])) {
+                        const uint8_t *s = a.scales + row_of(c, i) * kBlocks + pc;
+                        kn[i] = __ldg(s);
+                        vn[i] = __ldg(s + kv_rows * kBlocks);
+                    } else if (ids[i] != -2) {
+                        next_lost |= 1u << ((32 * dw + kRoundRows * i + pr) >> 4);
+                        if (a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
                     }
                 }
             };
-            load_ids(p.c0);
-            load(p.c0);
-            load_ids(p.c0 + 1);
+            load_ids(p.c0, ids);
+            load_ids(p.c0 + 1, next_ids);
+            load_scales(p.c0);
+            load_codes(p.c0, kc, 0);
+            load_codes(p.c0, vc, kv_rows);
             int erun = 0;   // E of the values so far
             for (int c = p.c0; c < p.c1; ++c, ++tiles) {
                 const uint32_t stage = tiles % kStages, in = tiles % kInfos;
-                uint4 k[I], v[I];
-                uint32_t ke[I], ve[I], bad = 0, nan = 0, mk = 0, mv = 0;
+                uint32_t bad = next_lost, nan = 0, mk = 0, mv = 0;
 #pragma unroll
                 for (int i = 0; i < I; ++i) {
-                    k[i] = kc[i], v[i] = vc[i], ke[i] = kb[i], ve[i] = vb[i];
-                    if (state[i] == 2) bad |= 1u << ((32 * dw + kRoundRows * i + pr) >> 4);
-                    if (ke[i] != 255u) mk = max(mk, ke[i]);
-                    if (ve[i] != 255u) mv = max(mv, ve[i]);
+                    kb[i] = kn[i], vb[i] = vn[i];
+                    if (kb[i] != 255u) mk = max(mk, kb[i]);
+                    if (vb[i] != 255u) mv = max(mv, vb[i]);
                     else nan = 1;
+                    ids[i] = next_ids[i];
                 }
-                load(c + 1);        // under way while this tile is unpacked
-                load_ids(c + 2);
+                load_scales(c + 1);
+                load_ids(c + 2, next_ids);
                 mk = __reduce_max_sync(0xffffffffu, mk);
                 mv = __reduce_max_sync(0xffffffffu, mv);
                 bad = __reduce_or_sync(0xffffffffu, bad);
@@ -578,7 +600,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                     for (int i = 0; i < I; ++i) {
                         const int t = 32 * dw + kRoundRows * i + pr;
                         uint8_t *n = reinterpret_cast<uint8_t *>(s_nan[in]) + 4 * t + pc;
-                        n[0] = ve[i] == 255u;
+                        n[0] = vb[i] == 255u;
                         if (kIn == 2) n[2] = 0;
                     }
                 erun = ev;
@@ -599,27 +621,27 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 };
 #pragma unroll
                 for (int i = 0; i < I; ++i)
-                    widen(k[i], ke[i], ek, smem + S::kK + stage * S::kTileBytes, 32 * dw + kRoundRows * i + pr, true);
+                    widen(kc[i], kb[i], ek, smem + S::kK + stage * S::kTileBytes, 32 * dw + kRoundRows * i + pr, true);
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(smem_u32(&info_full[in]));
                     mbar_arrive(smem_u32(&k_full[stage]));
                 }
+                load_codes(c + 1, kc, 0);
                 ok = wait(v_empty[stage], ((tiles / kStages) & 1) ^ 1u);
                 if (!ok) break;
 #pragma unroll
                 for (int i = 0; i < I; ++i)
-                    widen(v[i], ve[i], ev, smem + S::kV + stage * S::kTileBytes, 32 * dw + kRoundRows * i + pr, false);
+                    widen(vc[i], vb[i], ev, smem + S::kV + stage * S::kTileBytes, 32 * dw + kRoundRows * i + pr, false);
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&v_full[stage]));
+                load_codes(c + 1, vc, kv_rows);
             }
         }
     } else {
-        fewer_registers<kMmaRegs>();
         // ---- products ---------------------------------------------------------------------
-        if (warp > kMmaWarp) u = u_end;   // idle
         const bool elected = elect_one();
         constexpr uint32_t kQK = idesc_f16(kM, kTok, false), kPV = idesc_f16(kM, D, true);
         uint32_t made[2] = {0, 0};   // P of each half that products have taken
@@ -678,7 +700,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             if (elected && ok) mma_commit(smem_u32(&o_full));
             __syncwarp();
         }
-        if (elected && warp == kMmaWarp) {
+        if (elected) {
             mma_commit(smem_u32(&drain_bar));
             wait_drain(smem_u32(&drain_bar), 0);
         }
