@@ -76,6 +76,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// Eight columns, there when it returns.
+__device__ __forceinline__ void tmem_get8(uint32_t addr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(addr)
+        : "memory");
+}
+using F2 = uint64_t;   // two fp32 numbers
 // D[tmem] (+)= A[tmem] * B[smem]
 __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -359,42 +374,43 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 const int upto = pos - t0, from = a.window ? pos - a.window - t0 : -1;   // columns from < i <= upto
                 const float xs = mult * info.ek;
                 float shrink = info.grown;
-                // Half of the columns at a time: their P takes the place of a quarter of S
-                // that has been read.
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t pk[kTok / 4];
-                    float part;
+                // 32 columns at a time (a small loop: unrolled, its code did not stay in the
+                // instruction cache): their P takes the place of S that has been read.
+                uint32_t r[2][16];
+                tmem_ld16(ts, r[0]);
+                tmem_ld16(ts + 16, r[1]);
+                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-                    for (int again = 0; again < 2; ++again) {
-                        float top = -INFINITY;
-                        part = 0.0f;
-                        uint32_t r[2][16];
-                        tmem_ld16(ts + half * (kTok / 2), r[0]);
+                for (int q = 0; q < kTok / 32; ++q) {
+                    float x[32];
+                    tmem_wait_ld(r[0]);
+                    tmem_wait_ld(r[1]);
+                    const F2 xs2 = pack2(__float_as_uint(xs), __float_as_uint(xs));
+                    const F2 ref2 = pack2(__float_as_uint(-ref), __float_as_uint(-ref));
 #pragma unroll
-                        for (int q = 0; q < kTok / 32; ++q) {
-                            const int col = half * (kTok / 2) + 16 * q;
-                            tmem_wait_ld(r[q & 1]);
-                            if (q + 1 < kTok / 32) tmem_ld16(ts + col + 16, r[(q + 1) & 1]);
-                            float x[16];
+                    for (int i = 0; i < 32; i += 2) {
+                        const F2 v = fma2(pack2(r[i >> 4][i & 15], r[i >> 4][(i & 15) + 1]), xs2, ref2);
+                        x[i] = __uint_as_float((uint32_t)v), x[i + 1] = __uint_as_float((uint32_t)(v >> 32));
+                    }
+                    if (q + 1 < kTok / 32) {
+                        tmem_ld16(ts + 32 * q + 32, r[0]);
+                        tmem_ld16(ts + 32 * q + 48, r[1]);
+                    }
+                    if (edge) {
+                        const int hi = upto - 32 * q, lo = from - 32 * q;
+                        const uint32_t bad = (info.bad >> 2 * q & 1u ? 0xffffu : 0u) | (info.bad >> 2 * q & 2u ? 0xffff0000u : 0u);
+                        // bit i: column i is seen
+                        uint32_t seen = hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1u;
+                        if (lo >= 0) seen &= lo >= 31 ? 0u : ~((2u << lo) - 1u);
+                        seen &= ~bad;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) x[i] = fmaf(__uint_as_float(r[q & 1][i]), xs, -ref);
-                            if (edge) {
-                                const bool bad = info.bad >> (col >> 4) & 1u;
+                        for (int i = 0; i < 32; ++i)
+                            if (!(seen >> i & 1u)) x[i] = -INFINITY;
+                    }
+                    float top = fmaxf(x[0], x[1]);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    if (bad || col + i > upto || col + i <= from) x[i] = -INFINITY;
-                            }
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                top = fmaxf(top, fmaxf(x[i], x[i + 1]));
-                                x[i] = ex2w(x[i]);
-                                x[i + 1] = ex2w(x[i + 1]);
-                                part += x[i] + x[i + 1];
-                                pk[8 * q + i / 2] = half2_of(x[i], x[i + 1]);
-                            }
-                        }
-                        if (again || !__any_sync(0xffffffffu, top > pass)) break;
+                    for (int i = 2; i < 32; i += 2) top = fmaxf(top, fmaxf(x[i], x[i + 1]));
+                    if (__any_sync(0xffffffffu, top > pass)) {
                         // m rises by whole powers of two, so that what is scaled stays exact
                         const float rise = top == -INFINITY ? 0.0f : pass == -INFINITY ? ceilf(top) : fmaxf(ceilf(top), 0.0f);
                         if (top != -INFINITY) pass = kLazy;
@@ -402,29 +418,32 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                         const float f = ex2w(-rise);
                         sum *= f;
                         shrink *= f;
-                        if (half == 1) {   // P of the first half
-                            const uint32_t f2 = half2_of(f, f);
-                            tmem_wait_st();
-#pragma unroll 1
-                            for (int q = 0; q < 2; ++q) {
-                                uint32_t y[16];
-                                tmem_ld16(ts + 16 * q, y);
-                                tmem_wait_ld(y);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) y[i] = mul_half2(y[i], f2);
-                                tmem_st16(ts + 16 * q, y);
-                            }
+                        for (int i = 0; i < 4; ++i) part[i] *= f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] -= rise;
+                        const uint32_t f2 = half2_of(f, f);
+                        tmem_wait_st();
+#pragma unroll 1
+                        for (int z = 0; z < 2 * q; ++z) {   // P so far
+                            uint32_t y[8];
+                            tmem_get8(ts + 8 * z, y);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) y[i] = mul_half2(y[i], f2);
+                            tmem_st8(ts + 8 * z, y);
                         }
                     }
-                    sum += part;
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t y[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = pk[16 * q + i];
-                        tmem_st16(ts + half * (kTok / 4) + 16 * q, y);
+                    for (int i = 0; i < 32; i += 2) {
+                        x[i] = ex2w(x[i]);
+                        x[i + 1] = ex2w(x[i + 1]);
+                        part[i >> 1 & 3] += x[i] + x[i + 1];
+                        pk[i / 2] = half2_of(x[i], x[i + 1]);
                     }
+                    tmem_st16(ts + 16 * q, pk);
                 }
+                sum += (part[0] + part[1]) + (part[2] + part[3]);
                 if (c > p.c0 && __any_sync(0xffffffffu, shrink != 1.0f)) {
 #pragma unroll 1
                     for (int q = 0; q < D / 16; ++q) {
@@ -515,33 +534,33 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             uint4 kc[I], vc[I];
             uint32_t kb[I], vb[I];   // scale bytes of this tile; 0 where there is nothing
             uint32_t kn[I], vn[I];   // of the next
-            int ids[I] = {}, next_ids[I];   // pages of the next tile and of the one behind it; -2: nothing to see
+            int64_t rows[I];         // cache rows of the next tile's keys; below 0: nothing
+            int ids[I];              // pages of the tile behind it; -2: nothing to see
             auto token = [&](int c, int i) { return p.g.lo + c * kTok + 32 * dw + kRoundRows * i + pr; };
-            auto load_ids = [&](int c, int (&id)[I]) {
+            auto load_ids = [&](int c) {
 #pragma unroll
                 for (int i = 0; i < I; ++i) {
                     const int t = token(c, i);
-                    id[i] = c < p.c1 && t <= p.g.pos_hi ? __ldg(table + (t >> a.page_shift)) : -2;
+                    ids[i] = c < p.c1 && t <= p.g.pos_hi ? __ldg(table + (t >> a.page_shift)) : -2;
                 }
             };
-            auto there = [&](int id) { return id >= 0 && id < a.pages; };
-            auto row_of = [&](int c, int i) {
-                return (((int64_t)ids[i] * 2 * a.Hk + p.h) << a.page_shift) + (token(c, i) & in_page);
-            };
-            auto load_codes = [&](int c, uint4 (&x)[I], int64_t rows_on) {
+            auto load_codes = [&](uint4 (&x)[I], int64_t rows_on) {
 #pragma unroll
                 for (int i = 0; i < I; ++i)
-                    x[i] = there(ids[i]) ? __ldg(reinterpret_cast<const uint4 *>(a.codes + (row_of(c, i) + rows_on) * (D / 2)) + pc)
-                                         : make_uint4(0, 0, 0, 0);
+                    x[i] = rows[i] >= 0 ? __ldg(reinterpret_cast<const uint4 *>(a.codes + (rows[i] + rows_on) * (D / 2)) + pc)
+                                        : make_uint4(0, 0, 0, 0);
             };
             uint32_t next_lost = 0;   // bit i: tokens 16 i .. of the next tile have no page
+            // From the pages of tile c: its rows, and its scales on their way.
             auto load_scales = [&](int c) {
                 next_lost = 0;
 #pragma unroll
                 for (int i = 0; i < I; ++i) {
                     kn[i] = vn[i] = 0;
-                    if (there(ids[i])) {
-                        const uint8_t *s = a.scales + row_of(c, i) * kBlocks + pc;
+                    rows[i] = -1;
+                    if (ids[i] >= 0 && ids[i] < a.pages) {
+                        rows[i] = (((int64_t)ids[i] * 2 * a.Hk + p.h) << a.page_shift) + (token(c, i) & in_page);
+                        const uint8_t *s = a.scales + rows[i] * kBlocks + pc;
                         kn[i] = __ldg(s);
                         vn[i] = __ldg(s + kv_rows * kBlocks);
                     } else if (ids[i] != -2) {
@@ -550,11 +569,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                     }
                 }
             };
-            load_ids(p.c0, ids);
-            load_ids(p.c0 + 1, next_ids);
+            load_ids(p.c0);
             load_scales(p.c0);
-            load_codes(p.c0, kc, 0);
-            load_codes(p.c0, vc, kv_rows);
+            load_ids(p.c0 + 1);
+            load_codes(kc, 0);
+            load_codes(vc, kv_rows);
             int erun = 0;   // E of the values so far
             for (int c = p.c0; c < p.c1; ++c, ++tiles) {
                 const uint32_t stage = tiles % kStages, in = tiles % kInfos;
@@ -565,10 +584,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                     if (kb[i] != 255u) mk = max(mk, kb[i]);
                     if (vb[i] != 255u) mv = max(mv, vb[i]);
                     else nan = 1;
-                    ids[i] = next_ids[i];
                 }
                 load_scales(c + 1);
-                load_ids(c + 2, next_ids);
+                load_ids(c + 2);
                 mk = __reduce_max_sync(0xffffffffu, mk);
                 mv = __reduce_max_sync(0xffffffffu, mv);
                 bad = __reduce_or_sync(0xffffffffu, bad);
@@ -628,7 +646,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                     mbar_arrive(smem_u32(&info_full[in]));
                     mbar_arrive(smem_u32(&k_full[stage]));
                 }
-                load_codes(c + 1, kc, 0);
+                load_codes(kc, 0);
                 ok = wait(v_empty[stage], ((tiles / kStages) & 1) ^ 1u);
                 if (!ok) break;
 #pragma unroll
@@ -637,7 +655,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&v_full[stage]));
-                load_codes(c + 1, vc, kv_rows);
+                load_codes(vc, kv_rows);
             }
         }
     } else {
