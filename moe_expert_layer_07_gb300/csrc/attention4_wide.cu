@@ -91,6 +91,16 @@ __device__ __forceinline__ void tmem_get8(uint32_t addr, uint32_t (&r)[8]) {
         : "memory");
 }
 using F2 = uint64_t;   // two fp32 numbers
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 // D[tmem] (+)= A[tmem] * B[smem]
 __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -213,28 +223,41 @@ struct Piece {
     int b, h, c0, c1;
 };
 
-// The piece that unit u belongs to, as far as u_end; u moves past it.  c0 == c1: nothing
-// of it is computed here.
-__device__ __forceinline__ Piece take_piece(const WideArgs &w, int64_t &u, int64_t u_end, int entries, int64_t total) {
-    Piece p;
-    p.h = (int)(u / total);
-    const int64_t local = u - p.h * total;
-    int lo = 0, hi = entries;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (w.units[mid] <= local) lo = mid;
-        else hi = mid;
+// The pieces of units u .. u_end, one after the other: entry after entry, then
+// the next head's.  Found by a search once.
+struct Walk {
+    int64_t u, u_end;
+    int h, entry, at;   // at: units of the entry that are taken
+    __device__ __forceinline__ void start(const WideArgs &w, int64_t first, int64_t end, int entries, int64_t total) {
+        u = first, u_end = end;
+        if (u >= u_end) return;
+        h = (int)(u / total);
+        const int64_t local = u - h * total;
+        int lo = 0, hi = entries;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (w.units[mid] <= local) lo = mid;
+            else hi = mid;
+        }
+        entry = lo;
+        at = (int)(local - w.units[lo]);
     }
-    p.b = w.entry_request[lo];
-    p.r = attn_request(w.a, p.b);
-    p.g = row_group(w.a, p.r, lo - w.first_entry[p.b]);
-    const int x0 = (int)(local - w.units[lo]);
-    const int x1 = (int)min((int64_t)p.g.tiles + kPieceTiles, x0 + u_end - u);
-    p.c0 = max(0, x0 - kPieceTiles);
-    p.c1 = max(0, x1 - kPieceTiles);
-    u += x1 - x0;
-    return p;
-}
+    // False when there are no more.  c0 == c1: nothing of the piece is computed here.
+    __device__ __forceinline__ bool next(const WideArgs &w, int entries, Piece &p) {
+        if (u >= u_end) return false;
+        p.h = h;
+        p.b = w.entry_request[entry];
+        p.r = attn_request(w.a, p.b);
+        p.g = row_group(w.a, p.r, entry - w.first_entry[p.b]);
+        const int all = p.g.tiles + kPieceTiles, to = (int)min((int64_t)all, at + u_end - u);
+        p.c0 = max(0, at - kPieceTiles);
+        p.c1 = max(0, to - kPieceTiles);
+        u += to - at;
+        at = 0;
+        if (++entry == entries) entry = 0, ++h;
+        return true;
+    }
+};
 
 struct Info {          // of a tile of tokens, from those who unpack it
     float ek;          // 2^(E - 127 - kBias) of its keys
@@ -304,8 +327,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
     uint8_t *smem = dsmem + (base - smem_u32(dsmem));
     const int entries = w.first_entry[a.B];
     const int64_t total = w.units[entries], all = total * a.Hk, per = w.per[0];
-    int64_t u = min(all, (int64_t)blockIdx.x * per);
-    const int64_t u_end = min(all, u + per);
+    Walk walk;
+    walk.start(w, min(all, (int64_t)blockIdx.x * per), min(all, (int64_t)(blockIdx.x + 1) * per), entries, total);
+    Piece p;
     uint32_t tiles = 0, pieces = 0;   // counted by every role alike
     bool ok = true;
     // a wait of a whole warp
@@ -319,8 +343,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + mt * kTok, to = tmem + lanes + S::kO + mt * D;
         uint32_t mine = 0;   // tiles of this half, of all pieces
-        while (u < u_end && ok) {
-            const Piece p = take_piece(w, u, u_end, entries, total);
+        while (ok && walk.next(w, entries, p)) {
             if (p.c0 == p.c1) continue;
             const int rr = mt * kM + row, flat = p.g.rowbase + rr;
             const bool there = rr < p.g.nrows;
@@ -379,7 +402,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 uint32_t r[2][16];
                 tmem_ld16(ts, r[0]);
                 tmem_ld16(ts + 16, r[1]);
-                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                F2 part[2] = {0ull, 0ull};
 #pragma unroll 1
                 for (int q = 0; q < kTok / 32; ++q) {
                     float x[32];
@@ -407,9 +430,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                         for (int i = 0; i < 32; ++i)
                             if (!(seen >> i & 1u)) x[i] = -INFINITY;
                     }
-                    float top = fmaxf(x[0], x[1]);
+                    float t4[4];
 #pragma unroll
-                    for (int i = 2; i < 32; i += 2) top = fmaxf(top, fmaxf(x[i], x[i + 1]));
+                    for (int i = 0; i < 4; ++i) t4[i] = fmaxf(x[i], x[i + 4]);
+#pragma unroll
+                    for (int i = 8; i < 32; i += 8)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) t4[z] = fmaxf(t4[z], fmaxf(x[i + z], x[i + z + 4]));
+                    const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                     if (__any_sync(0xffffffffu, top > pass)) {
                         // m rises by whole powers of two, so that what is scaled stays exact
                         const float rise = top == -INFINITY ? 0.0f : pass == -INFINITY ? ceilf(top) : fmaxf(ceilf(top), 0.0f);
@@ -419,7 +447,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                         sum *= f;
                         shrink *= f;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) part[i] *= f;
+                        for (int i = 0; i < 2; ++i) part[i] = mul2(part[i], pack2(__float_as_uint(f), __float_as_uint(f)));
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[i] -= rise;
                         const uint32_t f2 = half2_of(f, f);
@@ -438,12 +466,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                     for (int i = 0; i < 32; i += 2) {
                         x[i] = ex2w(x[i]);
                         x[i + 1] = ex2w(x[i + 1]);
-                        part[i >> 1 & 3] += x[i] + x[i + 1];
+                        part[i >> 1 & 1] = add2(part[i >> 1 & 1], pack2(__float_as_uint(x[i]), __float_as_uint(x[i + 1])));
                         pk[i / 2] = half2_of(x[i], x[i + 1]);
                     }
                     tmem_st16(ts + 16 * q, pk);
                 }
-                sum += (part[0] + part[1]) + (part[2] + part[3]);
+                part[0] = add2(part[0], part[1]);
+                sum += __uint_as_float((uint32_t)part[0]) + __uint_as_float((uint32_t)(part[0] >> 32));
                 if (c > p.c0 && __any_sync(0xffffffffu, shrink != 1.0f)) {
 #pragma unroll 1
                     for (int q = 0; q < D / 16; ++q) {
@@ -525,12 +554,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
         const int pr = D == 128 ? lane & 7 : (lane & 7) + (lane >> 4) * 8;
         const int64_t kv_rows = (int64_t)a.Hk << a.page_shift;
         const int in_page = (1 << a.page_shift) - 1;
-        while (u < u_end && ok) {
-            const Piece p = take_piece(w, u, u_end, entries, total);
+        while (ok && walk.next(w, entries, p)) {
             if (p.c0 == p.c1) continue;
             const int32_t *table = a.table + (int64_t)p.b * a.max_pages;
-            // What the next tile needs is on its way: pages two tiles ahead, scales one, codes
-            // from when this tile's have been taken.
+            // What the next tile needs is on its way: pages two tiles ahead, scales one, keys
+            // from when this tile's have been taken; values from the tile's own start.  (Loads
+            // issued before older ones are used were waited for with them.)
             uint4 kc[I], vc[I];
             uint32_t kb[I], vb[I];   // scale bytes of this tile; 0 where there is nothing
             uint32_t kn[I], vn[I];   // of the next
@@ -573,11 +602,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             load_scales(p.c0);
             load_ids(p.c0 + 1);
             load_codes(kc, 0);
-            load_codes(vc, kv_rows);
             int erun = 0;   // E of the values so far
             for (int c = p.c0; c < p.c1; ++c, ++tiles) {
                 const uint32_t stage = tiles % kStages, in = tiles % kInfos;
-                uint32_t bad = next_lost, nan = 0, mk = 0, mv = 0;
+                uint32_t bad = next_lost, nan = 0, mk = 0, mv = 0;   // of all the warp's tokens
 #pragma unroll
                 for (int i = 0; i < I; ++i) {
                     kb[i] = kn[i], vb[i] = vn[i];
@@ -585,8 +613,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                     if (vb[i] != 255u) mv = max(mv, vb[i]);
                     else nan = 1;
                 }
-                load_scales(c + 1);
-                load_ids(c + 2);
                 mk = __reduce_max_sync(0xffffffffu, mk);
                 mv = __reduce_max_sync(0xffffffffu, mv);
                 bad = __reduce_or_sync(0xffffffffu, bad);
@@ -595,6 +621,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                     s_e[tiles & 1][dw] = make_uint4(mk, mv, bad, nan);
                     mbar_arrive(smem_u32(&e_full[tiles & 1]));
                 }
+                load_codes(vc, kv_rows);
+                load_scales(c + 1);
+                load_ids(c + 2);
                 ok = wait(e_full[tiles & 1], (tiles >> 1) & 1);
                 if (!ok) break;
                 int ek = 0, ev = erun;
@@ -655,7 +684,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&v_full[stage]));
-                load_codes(vc, kv_rows);
             }
         }
     } else {
@@ -663,8 +691,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
         const bool elected = elect_one();
         constexpr uint32_t kQK = idesc_f16(kM, kTok, false), kPV = idesc_f16(kM, D, true);
         uint32_t made[2] = {0, 0};   // P of each half that products have taken
-        while (u < u_end && ok) {
-            const Piece p = take_piece(w, u, u_end, entries, total);
+        while (ok && walk.next(w, entries, p)) {
             if (p.c0 == p.c1) continue;
             const int n = p.c1 - p.c0, halves = p.g.nrows > kM ? 2 : 1;
             auto qk = [&](int mt, uint32_t tile, bool last) {
