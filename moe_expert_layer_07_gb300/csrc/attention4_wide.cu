@@ -403,21 +403,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 tmem_ld16(ts, r[0]);
                 tmem_ld16(ts + 16, r[1]);
                 F2 part[2] = {0ull, 0ull};
-#pragma unroll 1
-                for (int q = 0; q < kTok / 32; ++q) {
-                    float x[32];
-                    tmem_wait_ld(r[0]);
-                    tmem_wait_ld(r[1]);
+                // scores of 32 columns from r, past m, hidden ones at minus infinity
+                auto scores = [&](int q, float (&x)[32]) {
                     const F2 xs2 = pack2(__float_as_uint(xs), __float_as_uint(xs));
                     const F2 ref2 = pack2(__float_as_uint(-ref), __float_as_uint(-ref));
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
                         const F2 v = fma2(pack2(r[i >> 4][i & 15], r[i >> 4][(i & 15) + 1]), xs2, ref2);
                         x[i] = __uint_as_float((uint32_t)v), x[i + 1] = __uint_as_float((uint32_t)(v >> 32));
-                    }
-                    if (q + 1 < kTok / 32) {
-                        tmem_ld16(ts + 32 * q + 32, r[0]);
-                        tmem_ld16(ts + 32 * q + 48, r[1]);
                     }
                     if (edge) {
                         const int hi = upto - 32 * q, lo = from - 32 * q;
@@ -430,6 +423,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                         for (int i = 0; i < 32; ++i)
                             if (!(seen >> i & 1u)) x[i] = -INFINITY;
                     }
+                };
+                auto largest = [](const float (&x)[32]) {
                     float t4[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) t4[i] = fmaxf(x[i], x[i + 4]);
@@ -437,7 +432,32 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                     for (int i = 8; i < 32; i += 8)
 #pragma unroll
                         for (int z = 0; z < 4; ++z) t4[z] = fmaxf(t4[z], fmaxf(x[i + z], x[i + z + 4]));
-                    const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                    return fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                };
+#pragma unroll 1
+                for (int q = 0; q < kTok / 32; ++q) {
+                    float x[32];
+                    uint32_t pk[16];
+                    tmem_wait_ld(r[0]);
+                    tmem_wait_ld(r[1]);
+                    scores(q, x);
+                    if (q + 1 < kTok / 32) {
+                        tmem_ld16(ts + 32 * q + 32, r[0]);
+                        tmem_ld16(ts + 32 * q + 48, r[1]);
+                    }
+                    // exponentials first: whether m has to rise is known while they are formed
+                    const float top = largest(x);
+                    F2 more[2] = {0ull, 0ull};
+                    auto exponentials = [&]() {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            x[i] = ex2w(x[i]);
+                            x[i + 1] = ex2w(x[i + 1]);
+                            more[i >> 1 & 1] = add2(more[i >> 1 & 1], pack2(__float_as_uint(x[i]), __float_as_uint(x[i + 1])));
+                            pk[i / 2] = half2_of(x[i], x[i + 1]);
+                        }
+                    };
+                    exponentials();
                     if (__any_sync(0xffffffffu, top > pass)) {
                         // m rises by whole powers of two, so that what is scaled stays exact
                         const float rise = top == -INFINITY ? 0.0f : pass == -INFINITY ? ceilf(top) : fmaxf(ceilf(top), 0.0f);
@@ -448,8 +468,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                         shrink *= f;
 #pragma unroll
                         for (int i = 0; i < 2; ++i) part[i] = mul2(part[i], pack2(__float_as_uint(f), __float_as_uint(f)));
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] -= rise;
                         const uint32_t f2 = half2_of(f, f);
                         tmem_wait_st();
 #pragma unroll 1
@@ -460,15 +478,21 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                             for (int i = 0; i < 8; ++i) y[i] = mul_half2(y[i], f2);
                             tmem_st8(ts + 8 * z, y);
                         }
+                        // these columns again, and the next ones' loads
+                        tmem_ld16(ts + 32 * q, r[0]);
+                        tmem_ld16(ts + 32 * q + 16, r[1]);
+                        tmem_wait_ld(r[0]);
+                        tmem_wait_ld(r[1]);
+                        scores(q, x);
+                        more[0] = more[1] = 0ull;
+                        exponentials();
+                        if (q + 1 < kTok / 32) {
+                            tmem_ld16(ts + 32 * q + 32, r[0]);
+                            tmem_ld16(ts + 32 * q + 48, r[1]);
+                        }
                     }
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        x[i] = ex2w(x[i]);
-                        x[i + 1] = ex2w(x[i + 1]);
-                        part[i >> 1 & 1] = add2(part[i >> 1 & 1], pack2(__float_as_uint(x[i]), __float_as_uint(x[i + 1])));
-                        pk[i / 2] = half2_of(x[i], x[i + 1]);
-                    }
+                    part[0] = add2(part[0], more[0]);
+                    part[1] = add2(part[1], more[1]);
                     tmem_st16(ts + 16 * q, pk);
                 }
                 part[0] = add2(part[0], part[1]);
