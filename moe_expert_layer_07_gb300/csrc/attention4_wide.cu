@@ -38,12 +38,12 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kWideRows = 256, kM = 128, kTok = 128;
+constexpr int kWideRows = 256, kM = 128, kTok = 128, kSub = 64;   // tokens of a tile, of a product
 constexpr int kSoftWarps = 8, kUnpackWarps = 4, kMmaWarp = kSoftWarps + kUnpackWarps;
 constexpr int kWideThreads = (kMmaWarp + 1) * 32;
 constexpr int kStages = 2, kInfos = 4;
 constexpr int kTmemCols = 512;
-constexpr int kPieceTiles = 2;     // what the beginning and end of a piece cost, in tiles
+constexpr int kPieceTiles = 4;     // what the beginning and end of a piece cost, in tiles
 constexpr float kLazy = 8.0f;
 constexpr int kBias = 13;
 
@@ -275,7 +275,7 @@ struct WideShape {
     static constexpr int kUsed = kV + kStages * kTileBytes + 1024;
     // one CTA on an SM: each takes all of the tensor memory
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
-    static constexpr int kO = 2 * kTok;                    // columns: S0, S1, O0, O1
+    static constexpr int kO = 4 * kSub;                    // columns: S of both halves, twice each; O of both
 };
 
 template <int D>
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
     constexpr int kBlocks = D / 32;
     extern __shared__ uint8_t dsmem[];
     __shared__ uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], info_full[kInfos];
-    __shared__ uint64_t s_full[2], p_ready[2], q_full, o_full, drain_bar;
+    __shared__ uint64_t s_full[4], p_ready[4], o_done[2], q_full, o_full, drain_bar;   // [half][buffer]
     __shared__ uint64_t e_full[2];
     __shared__ Info s_info[kInfos];
     __shared__ uint2 s_nan[kInfos][kTok / 2];        // a byte for each token and channel block
@@ -305,7 +305,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&e_full[s]), kUnpackWarps);
             mbar_init(smem_u32(&s_full[s]), 1);
+            mbar_init(smem_u32(&s_full[s + 2]), 1);
             mbar_init(smem_u32(&p_ready[s]), 4);
+            mbar_init(smem_u32(&p_ready[s + 2]), 4);
+            mbar_init(smem_u32(&o_done[s]), 1);
         }
         mbar_init(smem_u32(&q_full), kSoftWarps);
         mbar_init(smem_u32(&o_full), 1);
@@ -341,8 +344,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
         // ---- softmax, a thread to a row ---------------------------------------------------
         const int mt = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + mt * kTok, to = tmem + lanes + S::kO + mt * D;
-        uint32_t mine = 0;   // tiles of this half, of all pieces
+        const uint32_t to = tmem + lanes + S::kO + mt * D;
+        uint32_t mine = 0;   // products' tiles of this half, of all pieces
         while (ok && walk.next(w, entries, p)) {
             if (p.c0 == p.c1) continue;
             const int rr = mt * kM + row, flat = p.g.rowbase + rr;
@@ -386,17 +389,22 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             for (int c = p.c0; c < p.c1; ++c, ++tiles) {
                 if (!used) continue;
                 const uint32_t in = tiles % kInfos;
-                ok = wait(info_full[in], (tiles / kInfos) & 1) && wait(s_full[mt], mine & 1);
-                ++mine;
+                ok = wait(info_full[in], (tiles / kInfos) & 1);
                 if (!ok) break;
-                tc_fence_after();
                 const Info info = s_info[in];
                 ev = info.ev;
-                const int t0 = p.g.lo + c * kTok;
-                const bool edge = t0 + kTok - 1 > p.g.pos_lo || (a.window && t0 <= p.g.pos_hi - a.window) || info.bad;
+#pragma unroll 1
+                for (int sub = 0; sub < kTok / kSub && ok; ++sub, ++mine) {
+                const uint32_t ts = tmem + lanes + (2 * mt + sub) * kSub;
+                ok = wait(s_full[2 * mt + sub], (mine >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const int t0 = p.g.lo + c * kTok + sub * kSub;
+                const bool edge = t0 + kSub - 1 > p.g.pos_lo || (a.window && t0 <= p.g.pos_hi - a.window) || info.bad;
                 const int upto = pos - t0, from = a.window ? pos - a.window - t0 : -1;   // columns from < i <= upto
+                const uint32_t lost = info.bad >> 4 * sub;
                 const float xs = mult * info.ek;
-                float shrink = info.grown;
+                float shrink = sub ? 1.0f : info.grown;
                 // 32 columns at a time (a small loop: unrolled, its code did not stay in the
                 // instruction cache): their P takes the place of S that has been read.
                 uint32_t r[2][16];
@@ -414,7 +422,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                     }
                     if (edge) {
                         const int hi = upto - 32 * q, lo = from - 32 * q;
-                        const uint32_t bad = (info.bad >> 2 * q & 1u ? 0xffffu : 0u) | (info.bad >> 2 * q & 2u ? 0xffff0000u : 0u);
+                        const uint32_t bad = (lost >> 2 * q & 1u ? 0xffffu : 0u) | (lost >> 2 * q & 2u ? 0xffff0000u : 0u);
                         // bit i: column i is seen
                         uint32_t seen = hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1u;
                         if (lo >= 0) seen &= lo >= 31 ? 0u : ~((2u << lo) - 1u);
@@ -435,13 +443,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                     return fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                 };
 #pragma unroll 1
-                for (int q = 0; q < kTok / 32; ++q) {
+                for (int q = 0; q < kSub / 32; ++q) {
                     float x[32];
                     uint32_t pk[16];
                     tmem_wait_ld(r[0]);
                     tmem_wait_ld(r[1]);
                     scores(q, x);
-                    if (q + 1 < kTok / 32) {
+                    if (q + 1 < kSub / 32) {
                         tmem_ld16(ts + 32 * q + 32, r[0]);
                         tmem_ld16(ts + 32 * q + 48, r[1]);
                     }
@@ -486,7 +494,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                         scores(q, x);
                         more[0] = more[1] = 0ull;
                         exponentials();
-                        if (q + 1 < kTok / 32) {
+                        if (q + 1 < kSub / 32) {
                             tmem_ld16(ts + 32 * q + 32, r[0]);
                             tmem_ld16(ts + 32 * q + 48, r[1]);
                         }
@@ -497,7 +505,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 }
                 part[0] = add2(part[0], part[1]);
                 sum += __uint_as_float((uint32_t)part[0]) + __uint_as_float((uint32_t)(part[0] >> 32));
-                if (c > p.c0 && __any_sync(0xffffffffu, shrink != 1.0f)) {
+                if ((c > p.c0 || sub) && __any_sync(0xffffffffu, shrink != 1.0f)) {
+                    ok = wait(o_done[mt], (mine - 1) & 1);   // the products before these
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll 1
                     for (int q = 0; q < D / 16; ++q) {
                         uint32_t r[16];
@@ -511,13 +522,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 tmem_wait_st();
                 if (info.nan) {
 #pragma unroll 1
-                    for (int q = 0; q < kTok / 32; ++q) {
+                    for (int q = 0; q < kSub / 32; ++q) {
                         uint32_t r[16];
                         tmem_ld16(ts + 16 * q, r);
                         tmem_wait_ld(r);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const uint2 n8 = s_nan[in][16 * q + i];
+                            const uint2 n8 = s_nan[in][kSub / 2 * sub + 16 * q + i];
                             if (r[i] & 0x7fffu) nans |= n8.x;
                             if (r[i] & 0x7fff0000u) nans |= n8.y;
                         }
@@ -525,7 +536,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&p_ready[mt]));
+                if (lane == 0) mbar_arrive(smem_u32(&p_ready[2 * mt + sub]));
+                }
+                if (!ok) break;
             }
             ok = ok && wait(o_full, pieces & 1);
             ++pieces;
@@ -587,39 +600,51 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             uint4 kc[I], vc[I];
             uint32_t kb[I], vb[I];   // scale bytes of this tile; 0 where there is nothing
             uint32_t kn[I], vn[I];   // of the next
-            int64_t rows[I];         // cache rows of the next tile's keys; below 0: nothing
-            int ids[I];              // pages of the tile behind it; -2: nothing to see
-            auto token = [&](int c, int i) { return p.g.lo + c * kTok + 32 * dw + kRoundRows * i + pr; };
+            int64_t rows[2];         // of the next tile's keys for each 16 tokens: this lane's first; below 0: nothing
+            int ids[2];              // pages of the tile behind it; -2: nothing to see
             auto load_ids = [&](int c) {
 #pragma unroll
-                for (int i = 0; i < I; ++i) {
-                    const int t = token(c, i);
+                for (int i = 0; i < 2; ++i) {
+                    const int t = p.g.lo + c * kTok + 32 * dw + 16 * i;
                     ids[i] = c < p.c1 && t <= p.g.pos_hi ? __ldg(table + (t >> a.page_shift)) : -2;
                 }
             };
+            // rounds of 16 / kRoundRows for each 16 tokens
+            constexpr int kRounds = 16 / kRoundRows;
             auto load_codes = [&](uint4 (&x)[I], int64_t rows_on) {
 #pragma unroll
-                for (int i = 0; i < I; ++i)
-                    x[i] = rows[i] >= 0 ? __ldg(reinterpret_cast<const uint4 *>(a.codes + (rows[i] + rows_on) * (D / 2)) + pc)
-                                        : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < I; ++i) {
+                    const int64_t r = rows[i / kRounds];
+                    x[i] = r >= 0 ? __ldg(reinterpret_cast<const uint4 *>(a.codes + (r + rows_on) * (D / 2)) + pc +
+                                          (i % kRounds) * kRoundRows * (D / 32))
+                                  : make_uint4(0, 0, 0, 0);
+                }
             };
             uint32_t next_lost = 0;   // bit i: tokens 16 i .. of the next tile have no page
+            int next_seen = 0;        // its tokens that rows see
             // From the pages of tile c: its rows, and its scales on their way.
             auto load_scales = [&](int c) {
                 next_lost = 0;
+                const int t0 = p.g.lo + c * kTok;
+                next_seen = p.g.pos_hi + 1 - t0;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    rows[g] = -1;
+                    if (ids[g] >= 0 && ids[g] < a.pages) {
+                        rows[g] = (((int64_t)ids[g] * 2 * a.Hk + p.h) << a.page_shift) + ((t0 + 32 * dw + 16 * g + pr) & in_page);
+                    } else if (ids[g] != -2) {
+                        next_lost |= 1u << (2 * dw + g);
+                        if (a.status && lane == 0) atomicOr(a.status, MOE_DEV_BAD_INDEX);
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < I; ++i) {
                     kn[i] = vn[i] = 0;
-                    rows[i] = -1;
-                    if (ids[i] >= 0 && ids[i] < a.pages) {
-                        rows[i] = (((int64_t)ids[i] * 2 * a.Hk + p.h) << a.page_shift) + (token(c, i) & in_page);
-                        const uint8_t *s = a.scales + rows[i] * kBlocks + pc;
-                        kn[i] = __ldg(s);
-                        vn[i] = __ldg(s + kv_rows * kBlocks);
-                    } else if (ids[i] != -2) {
-                        next_lost |= 1u << ((32 * dw + kRoundRows * i + pr) >> 4);
-                        if (a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
-                    }
+                    const int64_t r = rows[i / kRounds];
+                    if (r < 0) continue;
+                    const uint8_t *s = a.scales + r * kBlocks + pc + (i % kRounds) * kRoundRows * kBlocks;
+                    kn[i] = __ldg(s);
+                    vn[i] = __ldg(s + kv_rows * kBlocks);
                 }
             };
             load_ids(p.c0);
@@ -632,15 +657,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 uint32_t bad = next_lost, nan = 0, mk = 0, mv = 0;   // of all the warp's tokens
 #pragma unroll
                 for (int i = 0; i < I; ++i) {
-                    kb[i] = kn[i], vb[i] = vn[i];
+                    // rows behind the last token may hold anything
+                    const bool seen = 32 * dw + kRoundRows * i + pr < next_seen;
+                    kb[i] = seen ? kn[i] : 0u, vb[i] = seen ? vn[i] : 0u;
                     if (kb[i] != 255u) mk = max(mk, kb[i]);
                     if (vb[i] != 255u) mv = max(mv, vb[i]);
                     else nan = 1;
                 }
                 mk = __reduce_max_sync(0xffffffffu, mk);
                 mv = __reduce_max_sync(0xffffffffu, mv);
-                bad = __reduce_or_sync(0xffffffffu, bad);
-                nan = __reduce_or_sync(0xffffffffu, nan);
+                nan = __any_sync(0xffffffffu, nan);
                 if (lane == 0) {
                     s_e[tiles & 1][dw] = make_uint4(mk, mv, bad, nan);
                     mbar_arrive(smem_u32(&e_full[tiles & 1]));
@@ -713,59 +739,64 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
     } else {
         // ---- products ---------------------------------------------------------------------
         const bool elected = elect_one();
-        constexpr uint32_t kQK = idesc_f16(kM, kTok, false), kPV = idesc_f16(kM, D, true);
+        constexpr uint32_t kQK = idesc_f16(kM, kSub, false), kPV = idesc_f16(kM, D, true);
+        constexpr uint32_t kNext = kSub * 128 >> 4;   // a product's tokens, in a descriptor
         uint32_t made[2] = {0, 0};   // P of each half that products have taken
         while (ok && walk.next(w, entries, p)) {
             if (p.c0 == p.c1) continue;
-            const int n = p.c1 - p.c0, halves = p.g.nrows > kM ? 2 : 1;
-            auto qk = [&](int mt, uint32_t tile, bool last) {
-                const uint32_t stage = tile % kStages;
+            const int n = 2 * (p.c1 - p.c0), halves = p.g.nrows > kM ? 2 : 1;
+            auto qk = [&](int mt, int sub) {
+                const uint32_t stage = (tiles + sub / 2) % kStages, half = sub & 1;
                 if (elected) {
                     const uint64_t q = sdesc_k_sw128(base + S::kQ + mt * S::kTileBytes);
-                    const uint64_t k = sdesc_k_sw128(base + S::kK + stage * S::kTileBytes);
+                    const uint64_t k = sdesc_k_sw128(base + S::kK + stage * S::kTileBytes) + half * kNext;
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s) {
                         const uint32_t off = (s >> 2) * (S::kHalf >> 4) + (s & 3) * 2;
-                        mma_f16(tmem + mt * kTok, q + off, k + off, kQK, s > 0);
+                        mma_f16(tmem + (2 * mt + half) * kSub, q + off, k + off, kQK, s > 0);
                     }
-                    mma_commit(smem_u32(&s_full[mt]));
-                    if (last) mma_commit(smem_u32(&k_empty[stage]));
+                    mma_commit(smem_u32(&s_full[2 * mt + half]));
+                    if (half && mt == halves - 1) mma_commit(smem_u32(&k_empty[stage]));
                 }
                 __syncwarp();
             };
-            auto pv = [&](int mt, uint32_t tile, bool first, bool last) {
-                const uint32_t stage = tile % kStages;
-                const bool good = wait(v_full[stage], (tile / kStages) & 1) && wait(p_ready[mt], made[mt] & 1);
-                ++made[mt];
-                if (!good) return false;
+            auto have_keys = [&](int sub) {
+                const uint32_t tile = tiles + sub / 2;
+                const bool good = wait(k_full[tile % kStages], (tile / kStages) & 1);
                 tc_fence_after();
-                if (elected) {
-                    const uint64_t v = sdesc_mn_sw128(base + S::kV + stage * S::kTileBytes);
-#pragma unroll
-                    for (int s = 0; s < kTok / 16; ++s)
-                        mma_f16_ta(tmem + S::kO + mt * D, tmem + mt * kTok + 8 * s, v + s * (2048 >> 4), kPV, !first || s > 0);
-                    if (last) mma_commit(smem_u32(&v_empty[stage]));
-                }
-                __syncwarp();
-                return true;
+                return good;
             };
-            ok = wait(q_full, pieces & 1);
+            ok = wait(q_full, pieces & 1) && have_keys(0);
             ++pieces;
-            for (int j = 0; j < n && ok; ++j) {
-                const uint32_t tile = tiles + j;
-                ok = wait(k_full[tile % kStages], (tile / kStages) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                qk(0, tile, halves == 1);
-                if (halves == 2) {
-                    if (j > 0) ok = pv(1, tile - 1, j == 1, true);
+            if (!ok) break;
+            for (int sub = 0; sub < 2; ++sub)
+                for (int mt = 0; mt < halves; ++mt) qk(mt, sub);
+            for (int sub = 0; sub < n && ok; ++sub) {
+                const uint32_t tile = tiles + sub / 2, stage = tile % kStages, half = sub & 1;
+                if (!half) ok = wait(v_full[stage], (tile / kStages) & 1);
+                for (int mt = 0; mt < halves && ok; ++mt) {
+                    ok = wait(p_ready[2 * mt + half], (made[mt] >> 1) & 1);
+                    ++made[mt];
                     if (!ok) break;
-                    qk(1, tile, true);
+                    tc_fence_after();
+                    if (elected) {
+                        const uint64_t v = sdesc_mn_sw128(base + S::kV + stage * S::kTileBytes) + half * kNext;
+#pragma unroll
+                        for (int s = 0; s < kSub / 16; ++s)
+                            mma_f16_ta(tmem + S::kO + mt * D, tmem + (2 * mt + half) * kSub + 8 * s, v + s * (2048 >> 4), kPV,
+                                       sub > 0 || s > 0);
+                        mma_commit(smem_u32(&o_done[mt]));
+                        if (half && mt == halves - 1) mma_commit(smem_u32(&v_empty[stage]));
+                    }
+                    __syncwarp();
+                    if (sub + 2 < n) {   // into the S that these products have taken P from
+                        if (!half && mt == 0) ok = have_keys(sub + 2);
+                        if (!ok) break;
+                        qk(mt, sub + 2);
+                    }
                 }
-                ok = pv(0, tile, j == 0, halves == 1);
             }
-            if (ok && halves == 2) ok = pv(1, tiles + n - 1, n == 1, true);
-            tiles += n;
+            tiles += n / 2;
             if (elected && ok) mma_commit(smem_u32(&o_full));
             __syncwarp();
         }
