@@ -196,6 +196,19 @@ __device__ __forceinline__ void plan_units(const AttnArgs &a, int rows_at_once, 
     __syncthreads();
 }
 
+// Four channels of the output, times inv.
+__device__ __forceinline__ void write4(const AttnArgs &a, int64_t at, const float4 v, float inv) {
+    if (a.out_bf16) {
+        const __nv_bfloat162 y0 = __floats2bfloat162_rn(v.x * inv, v.y * inv);
+        const __nv_bfloat162 y1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&y0), *reinterpret_cast<const uint32_t *>(&y1));
+    } else {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) =
+            make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    }
+}
+
 template <int D, int NQ>
 __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(const AttnArgs a) {
     using S = Shape<D, NQ>;
@@ -213,10 +226,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
     ptx::pdl_wait();
     plan_units(a, S::kRows, s_first, s_warp);
     const int all = s_first[a.B], per = max(1, (all + (int)gridDim.x - 1) / (int)gridDim.x);
-    if (blockIdx.x == 0) {
-        for (int b = tid; b <= a.B; b += kThreads) a.plan[b] = s_first[b];
-        if (tid == 0) a.plan[a.B + 1] = per;
-    }
+    if (tid == 0) a.cuts[blockIdx.x].nrows = 0;
     int u = min(all, (int)blockIdx.x * per);
     const int u_end = min(all, u + per);
     uint8_t *ring = smem + warp * S::kStages * S::kStage;
@@ -616,6 +626,11 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
         cp_async_wait<0>();
         __syncthreads();   // the ring is free, and the maxima are there
         const bool whole = c0 == 0 && c1 == chunks;
+        if (tid == 0 && c0 == 0 && !whole) {
+            const int first = s_first[b] + piece * (chunks + kPieceUnits);
+            const AttnCut cut = {r.row0, h * a.G, rowbase, nrows, (first + chunks + kPieceUnits - 1) / per, {}};
+            a.cuts[blockIdx.x] = cut;
+        }
         float *part = a.part + (int64_t)(2 * blockIdx.x + (c0 == 0 ? 1 : 0)) * S::kRows * (D + 2);
         float *s_o = reinterpret_cast<float *>(smem);   // [warp][8 rows][D]
 #pragma unroll
@@ -657,15 +672,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
                     const int row = rowbase + rr;
                     const int64_t at = (int64_t)(r.row0 + row / a.G) * a.Hq + h * a.G + row % a.G;
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // a row that sees nothing
-                    if (a.out_bf16) {
-                        const __nv_bfloat162 y0 = __floats2bfloat162_rn(v.x * inv, v.y * inv);
-                        const __nv_bfloat162 y1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
-                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at * D + col) =
-                            make_uint2(*reinterpret_cast<const uint32_t *>(&y0), *reinterpret_cast<const uint32_t *>(&y1));
-                    } else {
-                        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at * D + col) =
-                            make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-                    }
+                    write4(a, at * D + col, v, inv);
                     if (a.lse && col == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
                 }
             }
@@ -674,33 +681,88 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
     }
 }
 
-// Joins the pieces of rows that were cut: one warp a query row and head.
+// One block: eight rows of what CTA blockIdx.x began.  A warp takes every eighth
+// partial result for all of the rows.
+constexpr int kJoinRows = 8;
+
 template <int D>
 __global__ void __launch_bounds__(256) attention4_join_kernel(const AttnArgs a, int rows_at_once) {
+    constexpr int V = D / 32;   // channels of a lane
+    __shared__ float s_top[8][kJoinRows], s_sum[8][kJoinRows];
+    __shared__ __align__(16) float s_o[8][kJoinRows][D];
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (i >= (int64_t)a.rows * a.Hq) return;
-    const int row = (int)(i / a.Hq), head = (int)(i - (int64_t)row * a.Hq);
-    // the request that the row belongs to, if any
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.starts[mid] <= row) lo = mid;
-        else hi = mid;
+    const int k0 = blockIdx.x, r0 = blockIdx.y * kJoinRows, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const AttnCut cut = a.cuts[k0];
+    if (r0 >= cut.nrows) return;
+    const int parts = cut.last - k0 + 1;
+    const int64_t size = (int64_t)rows_at_once * (D + 2);
+    auto part = [&](int j) { return a.part + (2 * (int64_t)(k0 + j) + (j == 0)) * size; };
+    {   // each row's largest: lane rr + 8 i of a warp takes partial 4 warp + i + 32 n
+        float m = -INFINITY;
+        for (int j = 4 * warp + (lane >> 3); j < parts; j += 32)
+            m = fmaxf(m, part(j)[rows_at_once * D + r0 + (lane & 7)]);
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        if (lane < kJoinRows) s_top[warp][lane] = m;
     }
-    const AttnRequest r = attn_request(a, lo);
-    if (row < r.row0 || row >= r.row0 + r.n || a.plan[lo] == a.plan[lo + 1]) return;
-    const int per = a.plan[a.B + 1];
-    const int chunks = attn_chunks(r);
-    const int tiles_q = (int)(((int64_t)r.n * a.G + rows_at_once - 1) / rows_at_once);
-    const int h = head / a.G, flat = (row - r.row0) * a.G + head % a.G;
-    const int qt = flat / rows_at_once, rr = flat - qt * rows_at_once;
-    const int u0 = a.plan[lo] + (h * tiles_q + qt) * (chunks + kPieceUnits) + kPieceUnits;
-    const int k0 = u0 / per, k1 = (u0 + chunks - 1) / per;
-    if (k0 == k1) return;   // one CTA had all of it
-    attn_join<D>(a, rows_at_once, rr, i, k0, k1, lane);
+    __syncthreads();
+    float top = s_top[0][lane & 7];   // of row lane % 8
+#pragma unroll
+    for (int w = 1; w < 8; ++w) top = fmaxf(top, s_top[w][lane & 7]);
+    float o[kJoinRows][V], sum = 0.0f;
+#pragma unroll
+    for (int rr = 0; rr < kJoinRows; ++rr)
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[rr][j] = 0.0f;
+#pragma unroll 2
+    for (int j = warp; j < parts; j += 8) {
+        const float *p = part(j);
+        const float m = p[rows_at_once * D + r0 + (lane & 7)];
+        const float f = m == top ? 1.0f : ex2(m - top);
+        sum += f * p[rows_at_once * (D + 1) + r0 + (lane & 7)];
+#pragma unroll
+        for (int rr = 0; rr < kJoinRows; ++rr) {
+            const float fr = __shfl_sync(0xffffffffu, f, rr);
+            if (r0 + rr >= cut.nrows) continue;
+            const float *y = p + (int64_t)(r0 + rr) * D + lane * V;
+            if (V == 4) {
+                const float4 q = *reinterpret_cast<const float4 *>(y);
+                o[rr][0] += fr * q.x, o[rr][1] += fr * q.y, o[rr][2 % V] += fr * q.z, o[rr][3 % V] += fr * q.w;
+            } else {
+                const float2 q = *reinterpret_cast<const float2 *>(y);
+                o[rr][0] += fr * q.x, o[rr][1] += fr * q.y;
+            }
+        }
+    }
+    if (lane < kJoinRows) s_sum[warp][lane] = sum;
+#pragma unroll
+    for (int rr = 0; rr < kJoinRows; ++rr)
+#pragma unroll
+        for (int j = 0; j < V; ++j) s_o[warp][rr][lane * V + j] = o[rr][j];
+    __syncthreads();
+    for (int x = tid; x < kJoinRows * D / 4; x += 256) {
+        const int rr = x / (D / 4), col = x % (D / 4) * 4;
+        if (r0 + rr >= cut.nrows) break;
+        float l = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            l += s_sum[w][rr];
+            const float4 y = *reinterpret_cast<const float4 *>(&s_o[w][rr][col]);
+            v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+        }
+        const int row = cut.rowbase + r0 + rr;
+        const int64_t at = (int64_t)(cut.row0 + row / a.G) * a.Hq + cut.head0 + row % a.G;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        write4(a, at * D + col, v, inv);
+        if (a.lse && col == 0) {
+            float m = s_top[0][rr];
+#pragma unroll
+            for (int w = 1; w < 8; ++w) m = fmaxf(m, s_top[w][rr]);
+            a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
+        }
+    }
 }
 
 // Requests of at most this many rows are this file's where the call also has larger
@@ -729,20 +791,22 @@ int launch(const AttnArgs &a0, cudaStream_t s) {
     MOE_CUDA_TRY(cudaFuncSetAttribute(attention4_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     if (int rc = launch_dependent(attention4_kernel<D, NQ>, dim3(a.ctas), dim3(kThreads), smem, s, (const AttnArgs)a))
         return rc;
-    const int64_t warps = (int64_t)a.rows * a.Hq;
-    return launch_dependent(attention4_join_kernel<D>, dim3((unsigned)ceil_div(warps, 8)), dim3(256), 0, s,
-                            (const AttnArgs)a, (int)S::kRows);
+    return launch_attention4_join(a, D, S::kRows, a.ctas, s);
 }
 
 int ctas_of(int nq) { return sm_count() * (nq == 4 ? 1 : 2); }
 
 }  // namespace
 
-static size_t attention4_plan_bytes(const moe_cache_attn *d) { return align_up(sizeof(int32_t) * (d->requests + 2)); }
-
 static size_t attention4_few_workspace(const moe_cache_attn *d, const moe_cache4 *cache) {
     const int nq = rows8(d, cache);
-    return attention4_plan_bytes(d) + align_up(sizeof(float) * 2 * (size_t)ctas_of(nq) * 8 * nq * (cache->dim + 2));
+    return align_up(sizeof(AttnCut) * ctas_of(nq)) + align_up(sizeof(float) * 2 * (size_t)ctas_of(nq) * 8 * nq * (cache->dim + 2));
+}
+
+int launch_attention4_join(const AttnArgs &a, int dim, int rows_at_once, int ctas, cudaStream_t s) {
+    const dim3 grid((unsigned)ctas, (unsigned)(rows_at_once / kJoinRows));
+    if (dim == 64) return launch_dependent(attention4_join_kernel<64>, grid, dim3(256), 0, s, (const AttnArgs)a, rows_at_once);
+    return launch_dependent(attention4_join_kernel<128>, grid, dim3(256), 0, s, (const AttnArgs)a, rows_at_once);
 }
 
 size_t attention4_workspace(const moe_cache_attn *d, const moe_cache4 *cache) {
@@ -762,8 +826,6 @@ int launch_attention4(const moe_cache_attn *d, const moe_cache4 *cache, const vo
     a.out = out;
     a.lse = lse;
     a.status = status;
-    a.plan = static_cast<int32_t *>(ws);
-    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + attention4_plan_bytes(d));
     a.B = d->requests;
     a.rows = d->rows;
     a.Hq = d->q_heads;
@@ -780,6 +842,8 @@ int launch_attention4(const moe_cache_attn *d, const moe_cache4 *cache, const vo
     const bool wide = has_wide(d, cache);
     a.few_rows = wide ? kFewRows : INT32_MAX;
     a.ctas = ctas_of(nq);
+    a.cuts = static_cast<AttnCut *>(ws);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + align_up(sizeof(AttnCut) * a.ctas));
     if (int rc = cache->dim == 64 ? nq == 1 ? launch<64, 1>(a, s) : nq == 2 ? launch<64, 2>(a, s) : launch<64, 4>(a, s)
                  : nq == 1 ? launch<128, 1>(a, s) : nq == 2 ? launch<128, 2>(a, s) : launch<128, 4>(a, s))
         return rc;

@@ -330,6 +330,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
     uint8_t *smem = dsmem + (base - smem_u32(dsmem));
     const int entries = w.first_entry[a.B];
     const int64_t total = w.units[entries], all = total * a.Hk, per = w.per[0];
+    if (tid == 0) a.cuts[blockIdx.x].nrows = 0;
     Walk walk;
     walk.start(w, min(all, (int64_t)blockIdx.x * per), min(all, (int64_t)(blockIdx.x + 1) * per), entries, total);
     Piece p;
@@ -545,6 +546,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             if (!ok) break;
             tc_fence_after();
             const bool whole = p.c0 == 0 && p.c1 == p.g.tiles;
+            if (tid == 0 && p.c0 == 0 && !whole) {   // the CTA's last piece: units to come are those after walk.u
+                const AttnCut cut = {p.r.row0, p.h * a.G, p.g.rowbase, p.g.nrows,
+                                     (int)((walk.u + (p.g.tiles - p.c1) - 1) / per), {}};
+                a.cuts[blockIdx.x] = cut;
+            }
             float *dst = a.part + (int64_t)(2 * blockIdx.x + (p.c0 == 0)) * kWideRows * (D + 2);
             const float inv = !whole ? ev : sum == 0.0f ? 0.0f : ev / sum;
             if (!whole) dst[kWideRows * D + rr] = pass == -INFINITY ? -INFINITY : ref, dst[kWideRows * (D + 1) + rr] = sum;
@@ -812,42 +818,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the pieces of rows that were cut: one warp a query row and head.
-template <int D>
-__global__ void __launch_bounds__(256) wide_join_kernel(const WideArgs w) {
-    const AttnArgs &a = w.a;
-    pdl_launch_dependents();
-    pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (i >= (int64_t)a.rows * a.Hq) return;
-    const int row = (int)(i / a.Hq), head = (int)(i - (int64_t)row * a.Hq);
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.starts[mid] <= row) lo = mid;
-        else hi = mid;
-    }
-    const AttnRequest r = attn_request(a, lo);
-    if (row < r.row0 || row >= r.row0 + r.n || (int64_t)r.n * a.G <= w.few_rows) return;
-    const int h = head / a.G;
-    const int64_t flat = (int64_t)(row - r.row0) * a.G + head % a.G;
-    const int qt = (int)(flat / kWideRows), rr = (int)(flat - (int64_t)qt * kWideRows);
-    const int entries = w.first_entry[a.B], e = w.first_entry[lo] + qt;
-    if (e >= entries || w.entry_request[e] != lo) return;
-    const int64_t per = w.per[0], u0 = h * w.units[entries] + w.units[e] + kPieceTiles;
-    const int64_t u1 = h * w.units[entries] + w.units[e + 1] - 1;
-    const int k0 = (int)(u0 / per), k1 = (int)(u1 / per);
-    if (k0 == k1) return;   // one CTA had all of it
-    attn_join<D>(a, kWideRows, rr, i, k0, k1, lane);
-}
-
 int entries_bound(const moe_cache_attn *d, int G) {
     return (int)std::min<int64_t>((int64_t)d->rows * G / kWideRows + std::min(d->requests, d->rows), 1 << 30);
 }
 
 struct WideLayout {
-    size_t units, per, request, first, part, total;
+    size_t units, per, request, first, cuts, part, total;
 };
 WideLayout wide_layout(const moe_cache_attn *d, const moe_cache4 *cache) {
     WideLayout l;
@@ -856,7 +832,8 @@ WideLayout wide_layout(const moe_cache_attn *d, const moe_cache4 *cache) {
     l.per = align_up(8 * (e + 1));
     l.request = l.per + align_up(8);
     l.first = l.request + align_up(4 * e);
-    l.part = l.first + align_up(4 * ((size_t)d->requests + 1));
+    l.cuts = l.first + align_up(4 * ((size_t)d->requests + 1));
+    l.part = l.cuts + align_up(sizeof(AttnCut) * sm_count());
     l.total = l.part + align_up(sizeof(float) * 2 * (size_t)sm_count() * kWideRows * (cache->dim + 2));
     return l;
 }
@@ -870,8 +847,7 @@ int launch(const WideArgs &w, cudaStream_t s) {
     if (int rc = launch_dependent(attention4_wide_kernel<D>, dim3((unsigned)ctas), dim3(kWideThreads),
                                   WideShape<D>::kSmem, s, (const WideArgs)w))
         return rc;
-    const int64_t warps = (int64_t)w.a.rows * w.a.Hq;
-    return launch_dependent(wide_join_kernel<D>, dim3((unsigned)ceil_div(warps, 8)), dim3(256), 0, s, (const WideArgs)w);
+    return launch_attention4_join(w.a, D, kWideRows, ctas, s);
 }
 
 }  // namespace
@@ -887,6 +863,7 @@ int launch_attention4_wide(const AttnArgs &args, const moe_cache_attn *d, const 
     WideArgs w;
     w.a = args;
     w.a.part = reinterpret_cast<float *>(p + l.part);
+    w.a.cuts = reinterpret_cast<AttnCut *>(p + l.cuts);
     w.few_rows = few_rows;
     w.max_entries = entries_bound(d, args.G);
     w.units = reinterpret_cast<int64_t *>(p + l.units);
