@@ -3,19 +3,20 @@
 // x in bf16, W in MXFP4 or as integers with group scales and zero points.
 //
 // Bound by reading W once: 4.25 bits a weight and more.  A warp takes 16 rows
-// of W by a slice of 128 of K at a time, the M side of mma.sync m16n8k16, with
-// 8 or 16 rows of x as its N side.  A slice of x stays in the warp's registers
+// of W by slices of 128 of K, the M side of mma.sync m16n8k16, with 8 or 16
+// rows of x as its N side.  Its slices of x stay in the warp's registers
 // for all of its rows of W, so x costs nothing per weight: a CTA's warps share
 // K among them, and where K is longer than a CTA's registers hold, the CTAs of a
 // cluster do.  W comes by cp.async through a ring of each warp's own and leaves
-// it by ldmatrix in the order of the products; scales go to registers, the next
-// rows' ahead of their use.
+// it by ldmatrix in the order of the products; the scales of a tile of rows
+// come through the same ring, as the strips of four-byte words that hold them
+// (their rows need not be aligned).
 //
-// Codes become fp16 unscaled (MXFP4: cvt; integers: 1024 + code put together
-// from bits, minus 1024 + zero point, both exact), products of 32 of K are
-// multiplied by the group's scale in fp32.  x is fp16 times a power of two for
-// each row (bf16 values have no more bits; below 2^-38 of a row's largest they
-// lose some).
+// Codes become fp16 unscaled (MXFP4: cvt; integers: 1024 + code or 1024 + 16 code
+// put together from bits, minus the zero point, both exact), products of 32 of K
+// are multiplied by the group's scale in fp32.  x is fp16 times a power of two for
+// each row and warp (bf16 values have no more bits; below 2^-38 of the largest
+// among the warp's they lose some).
 //
 // Sums: the K slices of a warp one after the other, then warps in order, then
 // CTAs in order: the same bits each time.
@@ -33,17 +34,22 @@ namespace {
 
 constexpr int kMaxWarps = 16;
 constexpr int kTileRows = 16, kSlice = 128;
-constexpr int kTileBytes = kTileRows * kSlice / 2;
-constexpr int kRingStages = 4;
+constexpr int kItemBytes = kTileRows * kSlice / 2;
 constexpr int kHold = 16;   // row tiles whose sums a CTA of a cluster holds between exchanges
+// Strips of scales and zero points: bytes of a row of W
+constexpr int kScaleStrip = 32, kZeroStrip = 12;
+
+// A stage of a warp's ring: a tile of 16 rows by the warp's slices, and its strips.
+__host__ __device__ constexpr int stage_bytes(bool ints, int slices) {
+    return slices * kItemBytes + kTileRows * (ints ? kScaleStrip + kZeroStrip : 12) + (ints ? 0 : 64 - 192 % 64) % 64;
+}
 
 struct MatvecArgs {
     const uint16_t *x;
-    const uint8_t *w;
-    const void *scales;
-    const uint8_t *zeros;
+    const uint8_t *w, *scales, *zeros;
     void *y;
-    int T, N, K, slices, warps, per_cta, group_shift, s_f32, out_bf16;
+    int T, N, K, slices, warps, per_cta, stages, group_shift, s_f32, out_bf16;
+    int scale_row, scale_words, zero_words;   // bytes of a row's scales; words of a strip
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
@@ -72,152 +78,141 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c) {
+    const __half2 h = __hfma2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b),
+                              *reinterpret_cast<const __half2 *>(&c));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t add_half2(uint32_t a, uint32_t b) {
+    const __half2 h = __hadd2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Scales of one slice of one row of W: four MXFP4 bytes, or as many group
-// scales (raw bits) and zero points as the slice has.
-struct RawScales {
-    uint32_t s[4];   // MXFP4: s[0] the four bytes; integers: the scale of each block of 32
-    uint32_t z;      // zero points of the four blocks
+// Eight integer codes less their zero point as fp16 pairs (0,4) (1,5) (2,6) (3,7), which x's
+// fragments follow: 1024 + c - (1024 + z), and (1024 + 16 c) / 16 - (64 + z).
+struct Zero {
+    uint32_t one, sixteen;   // -(1024 + z), -(64 + z), twice each
+    __device__ __forceinline__ explicit Zero(uint32_t z)
+        : one((0xe400u + z) * 0x10001u), sixteen((0xd400u + (z << 4)) * 0x10001u) {}
 };
-
-template <bool INT>
-__device__ __forceinline__ RawScales load_scales(const MatvecArgs &a, int n, int slice) {
-    RawScales r;
-    r.z = 0x08080808u;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) r.s[b] = 0;
-    if (n >= a.N) return r;
-    if (!INT) {
-        const uint8_t *p = static_cast<const uint8_t *>(a.scales) + (int64_t)n * (a.K >> 5) + slice * 4;
-        if ((a.K & 127) == 0) {
-            r.s[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
-        } else {
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                if (slice * 4 + b < a.K >> 5) r.s[0] |= (uint32_t)__ldg(p + b) << (8 * b);
-        }
-    } else {
-        const int groups = a.K >> a.group_shift, per = kSlice >> a.group_shift;   // 1, 2 or 4 a slice
-        const int64_t at = (int64_t)n * groups;
-        uint32_t z = 0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            if (b >= per) break;
-            const int gi = slice * per + b;
-            uint32_t v = 0, zero = 8;
-            if (gi < groups) {
-                v = a.s_f32 ? __ldg(static_cast<const uint32_t *>(a.scales) + at + gi)
-                            : (uint32_t)__ldg(static_cast<const uint16_t *>(a.scales) + at + gi) << 16;
-                if (a.zeros) zero = __ldg(a.zeros + at + gi) & 15u;
-            }
-            // to the blocks of 32 that the group has
-            if (per == 4) r.s[b] = v, z |= zero << (8 * b);
-            else if (per == 2) {
-                r.s[2 * b] = r.s[(2 * b + 1) & 3] = v;
-                z |= zero * 0x0101u << (16 * b);
-            } else {
-                r.s[0] = r.s[1] = r.s[2] = r.s[3] = v;
-                z = zero * 0x01010101u;
-            }
-        }
-        r.z = z;
-    }
-    return r;
+__device__ __forceinline__ void widen_ints(uint32_t codes, const Zero &z, uint32_t (&h)[4]) {
+    const uint32_t up = codes >> 8, k = 0x64006400u, sixteenth = 0x2c002c00u;
+    h[0] = add_half2((codes & 0x000f000fu) | k, z.one);
+    h[1] = fma_half2((codes & 0x00f000f0u) | k, sixteenth, z.sixteen);
+    h[2] = add_half2((up & 0x000f000fu) | k, z.one);
+    h[3] = fma_half2((up & 0x00f000f0u) | k, sixteenth, z.sixteen);
 }
 
-// Eight codes of one row (block b) as fp16 pairs (0,1) (2,3) (4,5) (6,7); integers in
-// the order (0,4) (1,5) (2,6) (3,7), which x's fragments follow.
-template <bool INT>
-__device__ __forceinline__ void widen(uint32_t codes, uint32_t z, int b, uint32_t (&h)[4]) {
-    if (!INT) {
-        mx4_half8(codes, h);
-    } else {
-        const uint32_t one = 0x6400u + (z >> (8 * b) & 0xffu);   // 1024 + zero
-        const uint32_t zz = one * 0x10001u;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = sub_half2(((codes >> (4 * j)) & 0x000f000fu) | 0x64006400u, zz);
-    }
+__device__ __forceinline__ void write(const MatvecArgs &a, int t, int n, float v) {
+    if (t >= a.T || n >= a.N) return;
+    if (a.out_bf16) static_cast<__nv_bfloat16 *>(a.y)[(int64_t)t * a.N + n] = __float2bfloat16(v);
+    else static_cast<float *>(a.y)[(int64_t)t * a.N + n] = v;
 }
 
 // NQ: rows of x in eights.  S: slices of a warp.
 template <bool INT, int NQ, int S>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const MatvecArgs a) {
+    constexpr int kStage = stage_bytes(INT, S), kStrips = S * kItemBytes;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float s_up[16];   // what each row of x was multiplied by, undone
-    __shared__ uint32_t s_max[16];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int rank = ptx::cluster_rank();
     const int ranks = a.slices > a.per_cta ? (a.slices + a.per_cta - 1) / a.per_cta : 1;
     const int cluster = blockIdx.x / ranks, clusters = gridDim.x / ranks;
-    const int first_slice = rank * a.per_cta + warp * S;
+    const int first_slice = rank * a.per_cta + warp * S, last_slice = min(a.slices, (rank + 1) * a.per_cta);
     const int tiles = (a.N + kTileRows - 1) / kTileRows;
     const int mine = cluster < tiles ? (tiles - cluster + clusters - 1) / clusters : 0;
-    uint8_t *ring = smem + warp * kRingStages * kTileBytes;
+    uint8_t *ring = smem + warp * a.stages * kStage;
     const uint32_t ring_addr = ptx::smem_u32(ring);
-    float *s_part = reinterpret_cast<float *>(smem + a.warps * kRingStages * kTileBytes);   // [2][warps][NQ * 128]
-    float *s_hold = s_part + 2 * a.warps * NQ * 128;                                         // [kHold][NQ * 128]
-    const int row_bytes = a.K >> 1;
-    // Copies item i (tile i / S, slice i % S) into its slot of the ring
+    float *s_part = reinterpret_cast<float *>(smem + a.warps * a.stages * kStage);   // [2][warps][NQ * 128]
+    float *s_hold = s_part + 2 * a.warps * NQ * 128;                                  // [kHold][NQ * 128]
+    const int row_bytes = a.K >> 1, groups = a.K >> a.group_shift;
+    const int group0 = INT ? first_slice * (kSlice >> a.group_shift) : 0;
+    // A row's scales of this warp's slices begin at this byte of the tensor, its zero points here
+    auto scale_at = [&](int n) {
+        return INT ? ((int64_t)n * groups + group0) * (a.s_f32 ? 4 : 2) : (int64_t)n * (a.K >> 5) + first_slice * 4;
+    };
+    auto zero_at = [&](int n) { return (int64_t)n * groups + group0; };
+    const int64_t scale_end = (int64_t)a.N * a.scale_row, zero_end = (int64_t)a.N * groups;
+    // The words that hold `bytes from `at` on of each row of a tile
+    auto fetch_strip = [&](uint32_t dst, const uint8_t *src, int64_t at, int64_t end, int word) {
+        at = (at & ~(int64_t)3) + 4 * word;
+        if (at < end) cp_async4(dst, src + at, (int)min((int64_t)4, end - at));
+    };
+    uint32_t to = 0, from = 0;   // stages of the ring
     auto fetch = [&](int i) {
-        if (i < mine * S) {
-            const int tile = cluster + i / S * clusters, slice = first_slice + i % S;
-            const uint32_t slot = ring_addr + (i % kRingStages) * kTileBytes;
+        if (i < mine && first_slice < last_slice) {
+            const int n0 = (cluster + i * clusters) * kTileRows;
+            const uint32_t slot = ring_addr + to;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int p = 32 * j + lane, r = p >> 2, q = p & 3;
-                const int n = tile * kTileRows + r;
-                if (n < a.N && slice * 64 + q * 16 < row_bytes)
-                    cp_async16(slot + r * 64 + ((q ^ ((r >> 1) & 3)) << 4),
-                               a.w + (int64_t)n * row_bytes + slice * 64 + q * 16);
+            for (int j = 0; j < 2 * S; ++j) {
+                const int r = (32 * (j & 1) + lane) >> 2, q = lane & 3, at = (first_slice + j / 2) * 64 + q * 16;
+                if (n0 + r < a.N && at < row_bytes)
+                    cp_async16(slot + j / 2 * kItemBytes + r * 64 + ((q ^ ((r >> 1) & 3)) << 4),
+                               a.w + (int64_t)(n0 + r) * row_bytes + at);
+            }
+            const int r = lane & 15, n = n0 + r;
+            if (n < a.N) {
+                if (!INT) {   // three words: the third is needed where rows are not aligned
+                    fetch_strip(slot + kStrips + r * 12 + (lane >> 4) * 4, a.scales, scale_at(n), scale_end, lane >> 4);
+                    if ((a.K & 127) && lane < 16) fetch_strip(slot + kStrips + r * 12 + 8, a.scales, scale_at(n), scale_end, 2);
+                } else {
+                    for (int word = lane >> 4; word < a.scale_words; word += 2)
+                        fetch_strip(slot + kStrips + r * kScaleStrip + word * 4, a.scales, scale_at(n), scale_end, word);
+                    for (int word = lane >> 4; word < a.zero_words; word += 2)
+                        fetch_strip(slot + kStrips + kTileRows * kScaleStrip + r * kZeroStrip + word * 4, a.zeros, zero_at(n),
+                                    zero_end, word);
+                }
             }
         }
         cp_async_commit();
+        to = to == (uint32_t)((a.stages - 1) * kStage) ? 0 : to + kStage;
     };
     ptx::pdl_launch_dependents();
-    // weights are constants of the program; x may be an earlier kernel's
     ptx::pdl_wait();
-#pragma unroll
-    for (int i = 0; i < kRingStages - 1; ++i) fetch(i);
-    // pieces that lie behind K or N are never copied: their scales are zero, and
-    // whatever bits the ring holds there are finite numbers
-    if (tid < 16) s_max[tid] = 0;
-    __syncthreads();
-    // each row's largest magnitude, by each CTA over all of K
-#pragma unroll 4
-    for (int t = 0; t < a.T; ++t) {
-        uint32_t m = 0;
-        const uint4 *row = reinterpret_cast<const uint4 *>(a.x + (int64_t)t * a.K);
-        for (int i = tid; i < a.K / 8; i += a.warps * 32) {
-            const uint4 v = __ldg(row + i);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) m = max(m, max(w[j] << 16 & 0x7fff0000u, w[j] & 0x7fff0000u));
-        }
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0 && m) atomicMax(s_max + t, m);
-    }
-    __syncthreads();
-    // 2^up puts it into [2^14, 2^15); held where 2^up and 2^-up are numbers
-    if (tid < 16) s_up[tid] = __uint_as_float((uint32_t)(min(max((int)(s_max[tid] >> 23), 27), 254) - 14) << 23);
-    __syncthreads();
+    for (int i = 0; i < a.stages - 1; ++i) fetch(i);
+    // Pieces behind N or K are never copied: their products are not used (rows) or
+    // are with x of zero (columns; the ring's bits are finite numbers, and the scales
+    // are taken as zero).
     uint32_t xf[S][8][NQ][2];   // slices, steps of 16, rows of x
+    float down[NQ][2];          // what undoes the powers of two of rows 8 n + 2 c, + 1
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
         const int t = 8 * n + g;
-        const float f = __uint_as_float((254u << 23) - __float_as_uint(s_up[t]));   // 1 / s_up
+        uint4 raw[S][4];
+        uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < S; ++i)
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 const int k = (first_slice + i) * kSlice + 32 * b + 8 * c;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (t < a.T && k < a.K && first_slice + i < (rank + 1) * a.per_cta)
-                    v = __ldg(reinterpret_cast<const uint4 *>(a.x + (int64_t)t * a.K + k));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                raw[i][b] = make_uint4(0, 0, 0, 0);
+                if (t < a.T && k < a.K && first_slice + i < last_slice)
+                    raw[i][b] = __ldg(reinterpret_cast<const uint4 *>(a.x + (int64_t)t * a.K + k));
+            }
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const uint32_t w[4] = {raw[i][b].x, raw[i][b].y, raw[i][b].z, raw[i][b].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m = max(m, max(w[j] << 16 & 0x7fff0000u, w[j] & 0x7fff0000u));
+            }
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        // f = 2^up puts the row's largest into [2^14, 2^15); held where 2^up and 2^-up are numbers
+        const int ex = min(max((int)(m >> 23), 27), 254) - 14;
+        const float f = __uint_as_float((uint32_t)(254 - ex) << 23), un = __uint_as_float((uint32_t)ex << 23);
+        down[n][0] = __shfl_sync(0xffffffffu, un, 8 * c);
+        down[n][1] = __shfl_sync(0xffffffffu, un, 8 * c + 4);
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const uint32_t w[4] = {raw[i][b].x, raw[i][b].y, raw[i][b].z, raw[i][b].w};
                 float e[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -230,24 +225,19 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
             }
     }
     const int mrow = (lane & 7) + ((lane >> 3) & 1) * 8, mblk = lane >> 4;
-    RawScales nx[S][2];
-    auto load_tile_scales = [&](int it) {
-#pragma unroll
-        for (int i = 0; i < S; ++i)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const bool there = it < mine && first_slice + i < min(a.slices, (rank + 1) * a.per_cta);
-                nx[i][r] = load_scales<INT>(a, there ? (cluster + it * clusters) * kTileRows + g + 8 * r : a.N,
-                                            first_slice + i);
-            }
-    };
-    load_tile_scales(0);
+    const int per = kSlice >> a.group_shift;   // groups of a slice: 1, 2 or 4
 
     for (int it = 0; it < mine; ++it) {
-        RawScales cur[S][2];
-#pragma unroll
-        for (int i = 0; i < S; ++i) cur[i][0] = nx[i][0], cur[i][1] = nx[i][1];
-        load_tile_scales(it + 1);
+        // wait for the stage: all but the last stages - 2 fetches
+        if (a.stages == 4) cp_async_wait<2>();
+        else if (a.stages == 5) cp_async_wait<3>();
+        else cp_async_wait<4>();
+        __syncwarp();
+        fetch(it + a.stages - 1);
+        const uint8_t *stage = ring + from;
+        const uint32_t slot = ring_addr + from;
+        from = from == (uint32_t)((a.stages - 1) * kStage) ? 0 : from + kStage;
+        const int n0 = (cluster + it * clusters) * kTileRows;
         float acc[NQ][4];
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
@@ -255,32 +245,66 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
             for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-            const int item = it * S + i;
-            cp_async_wait<kRingStages - 2>();
-            __syncwarp();
-            fetch(item + kRingStages - 1);
-            const uint32_t slot = ring_addr + (item % kRingStages) * kTileBytes;
+            // scales of rows g and g + 8, for the four blocks of 32
+            float sc[2][4];
+            uint32_t zp[2][4];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = g + 8 * r;
+                if (!INT) {
+                    const uint32_t *strip = reinterpret_cast<const uint32_t *>(stage + kStrips + row * 12) + i;
+                    uint32_t w = strip[0];
+                    if (a.K & 127) {
+                        w = __funnelshift_r(w, strip[1], 8 * (((n0 + row) * (a.K >> 5)) & 3));   // 4 first_slice: no matter
+                        if ((first_slice + i) * 4 + 4 > a.K >> 5)   // blocks behind K
+                            w &= (1u << 8 * max(0, (a.K >> 5) - (first_slice + i) * 4)) - 1u;
+                    }
+                    if (first_slice + i >= last_slice) w = 0;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) sc[r][b] = __uint_as_float(w << (23 - 8 * b > 0 ? 23 - 8 * b : 0) >> (b == 3 ? 1 : 0) & 0x7f800000u);
+                } else {
+                    const uint32_t at = (uint32_t)(n0 + row) * groups + group0;   // its low bits
+                    const uint8_t *strip = stage + kStrips + row * kScaleStrip + ((uint32_t)at * (a.s_f32 ? 4 : 2) & 3);
+                    const uint8_t *zs = stage + kStrips + kTileRows * kScaleStrip + row * kZeroStrip + (at & 3);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        if (b == 0 || (b == 2 && per == 2) || per == 4) {
+                            const int gi = i * per + (per == 4 ? b : b >> 1);
+                            const bool there = group0 + gi < groups;
+                            sc[r][b] = !there ? 0.0f
+                                       : a.s_f32 ? reinterpret_cast<const float *>(strip)[gi]
+                                                 : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(strip)[gi] << 16);
+                            zp[r][b] = a.zeros && there ? zs[gi] & 15u : 8u;
+                        } else {
+                            sc[r][b] = sc[r][b - 1], zp[r][b] = zp[r][b - 1];
+                        }
+                    }
+                }
+            }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 uint32_t w[4];
-                ldm4(slot + mrow * 64 + (((2 * x + mblk) ^ ((mrow >> 1) & 3)) << 4), w);
+                ldm4(slot + i * kItemBytes + mrow * 64 + (((2 * x + mblk) ^ ((mrow >> 1) & 3)) << 4), w);
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const int b = 2 * x + y;
                     uint32_t w0[4], w1[4];
-                    widen<INT>(w[2 * y], cur[i][0].z, b, w0);
-                    widen<INT>(w[2 * y + 1], cur[i][1].z, b, w1);
-                    const float f0 = INT ? __uint_as_float(cur[i][0].s[b]) : mx4_scale(cur[i][0].s[0] >> (8 * b) & 0xffu);
-                    const float f1 = INT ? __uint_as_float(cur[i][1].s[b]) : mx4_scale(cur[i][1].s[0] >> (8 * b) & 0xffu);
+                    if (INT) {
+                        widen_ints(w[2 * y], Zero(zp[0][b]), w0);
+                        widen_ints(w[2 * y + 1], Zero(zp[1][b]), w1);
+                    } else {
+                        mx4_half8(w[2 * y], w0);
+                        mx4_half8(w[2 * y + 1], w1);
+                    }
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
                         float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                         mma16816(d, w0[0], w1[0], w0[1], w1[1], xf[i][2 * b][n][0], xf[i][2 * b][n][1]);
                         mma16816(d, w0[2], w1[2], w0[3], w1[3], xf[i][2 * b + 1][n][0], xf[i][2 * b + 1][n][1]);
-                        acc[n][0] = fmaf(d[0], f0, acc[n][0]);
-                        acc[n][1] = fmaf(d[1], f0, acc[n][1]);
-                        acc[n][2] = fmaf(d[2], f1, acc[n][2]);
-                        acc[n][3] = fmaf(d[3], f1, acc[n][3]);
+                        acc[n][0] = fmaf(d[0], sc[0][b], acc[n][0]);
+                        acc[n][1] = fmaf(d[1], sc[0][b], acc[n][1]);
+                        acc[n][2] = fmaf(d[2], sc[1][b], acc[n][2]);
+                        acc[n][3] = fmaf(d[3], sc[1][b], acc[n][3]);
                     }
                 }
             }
@@ -290,22 +314,18 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
             float *p = part + warp * NQ * 128 + 8 * n + 2 * c;
-            *reinterpret_cast<float2 *>(p + g * 8 * NQ) = make_float2(acc[n][0], acc[n][1]);
-            *reinterpret_cast<float2 *>(p + (g + 8) * 8 * NQ) = make_float2(acc[n][2], acc[n][3]);
+            *reinterpret_cast<float2 *>(p + g * 8 * NQ) = make_float2(acc[n][0] * down[n][0], acc[n][1] * down[n][1]);
+            *reinterpret_cast<float2 *>(p + (g + 8) * 8 * NQ) = make_float2(acc[n][2] * down[n][0], acc[n][3] * down[n][1]);
         }
         // one barrier a tile: `part` is written again two tiles on, past the next one
         __syncthreads();
         for (int i = tid; i < NQ * 128; i += a.warps * 32) {
             float v = 0.0f;
-            for (int w = 0; w < a.warps; ++w) v += part[w * NQ * 128 + i];
-            const int t = i & (8 * NQ - 1), n = (cluster + it * clusters) * kTileRows + i / (8 * NQ);
-            if (ranks > 1) {
-                s_hold[(it % kHold) * NQ * 128 + i] = v;
-            } else if (t < a.T && n < a.N) {
-                v *= s_up[t];
-                if (a.out_bf16) static_cast<__nv_bfloat16 *>(a.y)[(int64_t)t * a.N + n] = __float2bfloat16(v);
-                else static_cast<float *>(a.y)[(int64_t)t * a.N + n] = v;
-            }
+#pragma unroll 4
+            for (int q = 0; q < a.warps; ++q) v += part[q * NQ * 128 + i];
+            const int t = i & (8 * NQ - 1), n = n0 + i / (8 * NQ);
+            if (ranks > 1) s_hold[(it % kHold) * NQ * 128 + i] = v;
+            else write(a, t, n, v);
         }
         if (ranks > 1 && (it % kHold == kHold - 1 || it == mine - 1)) {
             // the CTAs' sums together: CTA r finishes its share of what is held
@@ -319,13 +339,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
                     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(ptx::cluster_map(mem + 4 * i, r)));
                     v += p;
                 }
-                const int j = i % (NQ * 128), t = j & (8 * NQ - 1);
-                const int n = (cluster + (base + i / (NQ * 128)) * clusters) * kTileRows + j / (8 * NQ);
-                if (t < a.T && n < a.N) {
-                    v *= s_up[t];
-                    if (a.out_bf16) static_cast<__nv_bfloat16 *>(a.y)[(int64_t)t * a.N + n] = __float2bfloat16(v);
-                    else static_cast<float *>(a.y)[(int64_t)t * a.N + n] = v;
-                }
+                const int j = i % (NQ * 128);
+                write(a, j & (8 * NQ - 1), (cluster + (base + i / (NQ * 128)) * clusters) * kTileRows + j / (8 * NQ), v);
             }
             ptx::cluster_sync();   // nobody reads this CTA's shared memory any more
         }
@@ -334,8 +349,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
 }
 
 template <bool INT, int NQ, int S>
-int launch(const MatvecArgs &a, int ranks, int clusters, cudaStream_t s) {
-    const int smem = a.warps * kRingStages * kTileBytes + (2 * a.warps + kHold) * NQ * 128 * 4;
+int launch(MatvecArgs a, int ranks, int clusters, cudaStream_t s) {
+    // as many stages as an SM's shared memory holds, four to six
+    const int sums = (2 * a.warps + kHold) * NQ * 128 * 4, room = 225 * 1024 - sums;
+    a.stages = std::min(6, room / (a.warps * stage_bytes(INT, S)));
+    const int smem = a.warps * a.stages * stage_bytes(INT, S) + sums;
     MOE_CUDA_TRY(cudaFuncSetAttribute(matvec4_kernel<INT, NQ, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)(ranks * clusters));
@@ -361,7 +379,7 @@ int launch_w4_matvec(const moe_w4 *d, int T, const void *x, const void *codes, c
     MatvecArgs a;
     a.x = static_cast<const uint16_t *>(x);
     a.w = static_cast<const uint8_t *>(codes);
-    a.scales = scales;
+    a.scales = static_cast<const uint8_t *>(scales);
     a.zeros = static_cast<const uint8_t *>(zeros);
     a.y = y;
     a.T = T;
@@ -371,6 +389,7 @@ int launch_w4_matvec(const moe_w4 *d, int T, const void *x, const void *codes, c
     a.group_shift = d->group == 32 ? 5 : d->group == 64 ? 6 : 7;
     a.s_f32 = d->scale_dtype == MOE_OUT_F32;
     a.out_bf16 = out_dtype == MOE_OUT_BF16;
+    a.stages = 0;
     // Slices a warp and CTAs a cluster: x's registers are 16 (8 rows) or 32 a slice
     const int per_warp = a.slices > kMaxWarps ? 2 : 1;
     int ranks = 1;
@@ -378,6 +397,10 @@ int launch_w4_matvec(const moe_w4 *d, int T, const void *x, const void *codes, c
     a.warps = (int)ceil_div(ceil_div(a.slices, ranks), per_warp);
     a.per_cta = a.warps * per_warp;
     ranks = (int)ceil_div(a.slices, a.per_cta);
+    const int groups = a.K / d->group, size = a.s_f32 ? 4 : 2, strip = per_warp * kSlice / d->group;   // a strip's groups
+    a.scale_row = d->kind == MOE_W4_INT ? groups * size : groups;
+    a.scale_words = a.s_f32 ? strip : (strip * 2 + 2 + 3) / 4;
+    a.zero_words = zeros ? (strip + 3 + 3) / 4 : 0;
     const int tiles = (int)ceil_div(a.N, kTileRows);
     const int clusters = std::max(1, std::min(tiles, sm_count() / ranks));
     const bool i = d->kind == MOE_W4_INT, wide = T > 8;
