@@ -24,6 +24,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "mx4.cuh"
@@ -39,6 +40,12 @@ constexpr int kHold = 16;   // row tiles whose sums a CTA of a cluster holds bet
 // Strips of scales and zero points: bytes of a row of W
 constexpr int kScaleStrip = 32, kZeroStrip = 12;
 
+constexpr int kStages = 4;   // what 16 warps' rings, of two slices each, leave room for
+
+// Kinds of weights: MXFP4, integers with one scale for a slice (groups of 128), with
+// more than one (32, 64)
+enum { kMx, kIntSlice, kIntBlocks };
+
 // A stage of a warp's ring: a tile of 16 rows by the warp's slices, and its strips.
 __host__ __device__ constexpr int stage_bytes(bool ints, int slices) {
     return slices * kItemBytes + kTileRows * (ints ? kScaleStrip + kZeroStrip : 12) + (ints ? 0 : 64 - 192 % 64) % 64;
@@ -48,7 +55,7 @@ struct MatvecArgs {
     const uint16_t *x;
     const uint8_t *w, *scales, *zeros;
     void *y;
-    int T, N, K, slices, warps, per_cta, stages, group_shift, s_f32, out_bf16;
+    int T, N, K, slices, warps, per_cta, group_shift, s_f32, out_bf16;
     int scale_row, scale_words, zero_words;   // bytes of a row's scales; words of a strip
 };
 
@@ -73,6 +80,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// d = the product alone
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -114,8 +129,9 @@ __device__ __forceinline__ void write(const MatvecArgs &a, int t, int n, float v
 }
 
 // NQ: rows of x in eights.  S: slices of a warp.
-template <bool INT, int NQ, int S>
+template <int KIND, int NQ, int S>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const MatvecArgs a) {
+    constexpr bool INT = KIND != kMx;
     constexpr int kStage = stage_bytes(INT, S), kStrips = S * kItemBytes;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
@@ -125,55 +141,63 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
     const int first_slice = rank * a.per_cta + warp * S, last_slice = min(a.slices, (rank + 1) * a.per_cta);
     const int tiles = (a.N + kTileRows - 1) / kTileRows;
     const int mine = cluster < tiles ? (tiles - cluster + clusters - 1) / clusters : 0;
-    uint8_t *ring = smem + warp * a.stages * kStage;
+    uint8_t *ring = smem + warp * kStages * kStage;
     const uint32_t ring_addr = ptx::smem_u32(ring);
-    float *s_part = reinterpret_cast<float *>(smem + a.warps * a.stages * kStage);   // [2][warps][NQ * 128]
+    float *s_part = reinterpret_cast<float *>(smem + a.warps * kStages * kStage);   // [2][warps][NQ * 128]
     float *s_hold = s_part + 2 * a.warps * NQ * 128;                                  // [kHold][NQ * 128]
+    float *s_scale = s_hold + kHold * NQ * 128 + warp * (S * 64);                      // MXFP4: [slice][row][block]
     const int row_bytes = a.K >> 1, groups = a.K >> a.group_shift;
     const int group0 = INT ? first_slice * (kSlice >> a.group_shift) : 0;
-    // A row's scales of this warp's slices begin at this byte of the tensor, its zero points here
-    auto scale_at = [&](int n) {
-        return INT ? ((int64_t)n * groups + group0) * (a.s_f32 ? 4 : 2) : (int64_t)n * (a.K >> 5) + first_slice * 4;
-    };
-    auto zero_at = [&](int n) { return (int64_t)n * groups + group0; };
-    const int64_t scale_end = (int64_t)a.N * a.scale_row, zero_end = (int64_t)a.N * groups;
-    // The words that hold `bytes from `at` on of each row of a tile
-    auto fetch_strip = [&](uint32_t dst, const uint8_t *src, int64_t at, int64_t end, int word) {
-        at = (at & ~(int64_t)3) + 4 * word;
-        if (at < end) cp_async4(dst, src + at, (int)min((int64_t)4, end - at));
-    };
-    uint32_t to = 0, from = 0;   // stages of the ring
-    auto fetch = [&](int i) {
-        if (i < mine && first_slice < last_slice) {
-            const int n0 = (cluster + i * clusters) * kTileRows;
-            const uint32_t slot = ring_addr + to;
+    const bool busy = first_slice < last_slice;
+    // What this lane copies of a tile: pieces lane % 4 of rows lane / 4 and 8 more, and
+    // words lane / 16, + 2 .. of the strips of row lane % 16, which begin anywhere in
+    // their first word.
+    const int row_a = lane >> 2, piece = lane & 3, row_s = lane & 15, word0 = lane >> 4;
+    const uint32_t dst = ring_addr + row_a * 64 + ((piece ^ ((row_a >> 1) & 3)) << 4);
+    const uint32_t dst_s = ring_addr + kStrips + row_s * (INT ? kScaleStrip : 12) + word0 * 4;
+    const uint32_t dst_z = ring_addr + kStrips + kTileRows * kScaleStrip + row_s * kZeroStrip + word0 * 4;
+    bool inside[S];
 #pragma unroll
-            for (int j = 0; j < 2 * S; ++j) {
-                const int r = (32 * (j & 1) + lane) >> 2, q = lane & 3, at = (first_slice + j / 2) * 64 + q * 16;
-                if (n0 + r < a.N && at < row_bytes)
-                    cp_async16(slot + j / 2 * kItemBytes + r * 64 + ((q ^ ((r >> 1) & 3)) << 4),
-                               a.w + (int64_t)(n0 + r) * row_bytes + at);
+    for (int i = 0; i < S; ++i) inside[i] = busy && (first_slice + i) * 64 + piece * 16 < row_bytes;
+    int n_next = cluster * kTileRows;   // the next tile to be copied
+    const int64_t step_w = (int64_t)clusters * kTileRows * row_bytes, half_w = (int64_t)8 * row_bytes;
+    const uint8_t *src = a.w + (int64_t)(n_next + row_a) * row_bytes + first_slice * 64 + piece * 16;
+    const int64_t scale_end = (int64_t)a.N * a.scale_row, zero_end = (int64_t)a.N * groups;
+    const int step_s = clusters * kTileRows * a.scale_row, step_z = clusters * kTileRows * groups;
+    int64_t at_s = (int64_t)(n_next + row_s) * a.scale_row + (INT ? group0 * (a.s_f32 ? 4 : 2) : first_slice * 4);
+    int64_t at_z = INT ? (int64_t)(n_next + row_s) * groups + group0 : 0;
+    const int words = INT ? a.scale_words : (a.K & 127) ? 3 : S;
+    uint32_t to = 0, from = 0;   // stages of the ring
+    auto strip = [&](uint32_t to_addr, const uint8_t *base, int64_t at, int64_t end, int count) {
+        at = (at & ~(int64_t)3) + 4 * word0;
+        for (int word = word0; word < count; word += 2, at += 8, to_addr += 8)
+            if (at < end) cp_async4(to_addr, base + at, (int)min((int64_t)4, end - at));
+    };
+    // Copies the next tile into its stage of the ring
+    auto fetch = [&]() {
+        if (busy && n_next < a.N) {
+            const bool lo = n_next + row_a < a.N, hi = n_next + row_a + 8 < a.N;
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                if (lo && inside[i]) cp_async16(dst + to + i * kItemBytes, src + i * 64);
+                if (hi && inside[i]) cp_async16(dst + to + i * kItemBytes + 512, src + half_w + i * 64);
             }
-            const int r = lane & 15, n = n0 + r;
-            if (n < a.N) {
-                if (!INT) {   // three words: the third is needed where rows are not aligned
-                    fetch_strip(slot + kStrips + r * 12 + (lane >> 4) * 4, a.scales, scale_at(n), scale_end, lane >> 4);
-                    if ((a.K & 127) && lane < 16) fetch_strip(slot + kStrips + r * 12 + 8, a.scales, scale_at(n), scale_end, 2);
-                } else {
-                    for (int word = lane >> 4; word < a.scale_words; word += 2)
-                        fetch_strip(slot + kStrips + r * kScaleStrip + word * 4, a.scales, scale_at(n), scale_end, word);
-                    for (int word = lane >> 4; word < a.zero_words; word += 2)
-                        fetch_strip(slot + kStrips + kTileRows * kScaleStrip + r * kZeroStrip + word * 4, a.zeros, zero_at(n),
-                                    zero_end, word);
-                }
+            if (n_next + row_s < a.N) {
+                strip(dst_s + to, a.scales, at_s, scale_end, words);
+                if (INT) strip(dst_z + to, a.zeros, at_z, zero_end, a.zero_words);
             }
+            src += step_w;
+            at_s += step_s;
+            at_z += step_z;
         }
+        n_next += clusters * kTileRows;
         cp_async_commit();
-        to = to == (uint32_t)((a.stages - 1) * kStage) ? 0 : to + kStage;
+        to = to == (kStages - 1) * kStage ? 0 : to + kStage;
     };
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
-    for (int i = 0; i < a.stages - 1; ++i) fetch(i);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch();
     // Pieces behind N or K are never copied: their products are not used (rows) or
     // are with x of zero (columns; the ring's bits are finite numbers, and the scales
     // are taken as zero).
@@ -225,50 +249,60 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
             }
     }
     const int mrow = (lane & 7) + ((lane >> 3) & 1) * 8, mblk = lane >> 4;
-    const int per = kSlice >> a.group_shift;   // groups of a slice: 1, 2 or 4
+
+    const int threads = a.warps * 32;
+    int turn = 0;
 
     for (int it = 0; it < mine; ++it) {
-        // wait for the stage: all but the last stages - 2 fetches
-        if (a.stages == 4) cp_async_wait<2>();
-        else if (a.stages == 5) cp_async_wait<3>();
-        else cp_async_wait<4>();
+        cp_async_wait<kStages - 2>();
         __syncwarp();
-        fetch(it + a.stages - 1);
+        fetch();
         const uint8_t *stage = ring + from;
         const uint32_t slot = ring_addr + from;
-        from = from == (uint32_t)((a.stages - 1) * kStage) ? 0 : from + kStage;
+        from = from == (kStages - 1) * kStage ? 0 : from + kStage;
         const int n0 = (cluster + it * clusters) * kTileRows;
         float acc[NQ][4];
+        if (KIND == kMx) {
+            // Scales as numbers, each formed once: lane (row, half) two blocks of each slice.
+            // 2^(byte - 127); byte 0 (2^-127) counts as zero, 255 as infinity: its codes are
+            // zero, and zero times it NaN.
+            const int row = lane >> 1, half = lane & 1;
 #pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
+            for (int i = 0; i < S; ++i) {
+                const uint32_t *strip = reinterpret_cast<const uint32_t *>(stage + kStrips + row * 12) + i;
+                uint32_t w = strip[0];
+                if (a.K & 127) {
+                    w = __funnelshift_r(w, strip[1], 8 * (((n0 + row) * (a.K >> 5)) & 3));   // 4 first_slice: no matter
+                    if ((first_slice + i) * 4 + 4 > a.K >> 5)   // blocks behind K
+                        w &= (1u << 8 * max(0, (a.K >> 5) - (first_slice + i) * 4)) - 1u;
+                }
+                if (first_slice + i >= last_slice) w = 0;
+                w >>= 16 * half;
+                *reinterpret_cast<float2 *>(s_scale + i * 64 + row * 4 + 2 * half) =
+                    make_float2(__uint_as_float((w & 0xffu) << 23), __uint_as_float((w >> 8 & 0xffu) << 23));
+            }
+            __syncwarp();
+        }
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-            // scales of rows g and g + 8, for the four blocks of 32
-            float sc[2][4];
-            uint32_t zp[2][4];
+            // scales (and zero points) of rows g and g + 8, for the four blocks of 32 or the slice
+            constexpr int kB = KIND == kIntSlice ? 1 : 4;
+            float sc[2][kB];
+            uint32_t zp[2][kB];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int row = g + 8 * r;
-                if (!INT) {
-                    const uint32_t *strip = reinterpret_cast<const uint32_t *>(stage + kStrips + row * 12) + i;
-                    uint32_t w = strip[0];
-                    if (a.K & 127) {
-                        w = __funnelshift_r(w, strip[1], 8 * (((n0 + row) * (a.K >> 5)) & 3));   // 4 first_slice: no matter
-                        if ((first_slice + i) * 4 + 4 > a.K >> 5)   // blocks behind K
-                            w &= (1u << 8 * max(0, (a.K >> 5) - (first_slice + i) * 4)) - 1u;
-                    }
-                    if (first_slice + i >= last_slice) w = 0;
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) sc[r][b] = __uint_as_float(w << (23 - 8 * b > 0 ? 23 - 8 * b : 0) >> (b == 3 ? 1 : 0) & 0x7f800000u);
+                if (KIND == kMx) {
+                    const float4 f = *reinterpret_cast<const float4 *>(s_scale + i * 64 + row * 4);
+                    sc[r][0] = f.x, sc[r][1 % kB] = f.y, sc[r][2 % kB] = f.z, sc[r][3 % kB] = f.w;
                 } else {
                     const uint32_t at = (uint32_t)(n0 + row) * groups + group0;   // its low bits
                     const uint8_t *strip = stage + kStrips + row * kScaleStrip + ((uint32_t)at * (a.s_f32 ? 4 : 2) & 3);
                     const uint8_t *zs = stage + kStrips + kTileRows * kScaleStrip + row * kZeroStrip + (at & 3);
+                    const int per = KIND == kIntSlice ? 1 : kSlice >> a.group_shift;   // groups of a slice: 1, or 2 or 4
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        if (b == 0 || (b == 2 && per == 2) || per == 4) {
+                    for (int b = 0; b < kB; ++b) {
+                        if (b == 0 || b == 2 || per == 4) {
                             const int gi = i * per + (per == 4 ? b : b >> 1);
                             const bool there = group0 + gi < groups;
                             sc[r][b] = !there ? 0.0f
@@ -276,11 +310,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
                                                  : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(strip)[gi] << 16);
                             zp[r][b] = a.zeros && there ? zs[gi] & 15u : 8u;
                         } else {
-                            sc[r][b] = sc[r][b - 1], zp[r][b] = zp[r][b - 1];
+                            sc[r][b] = sc[r][(b + kB - 1) % kB], zp[r][b] = zp[r][(b + kB - 1) % kB];
                         }
                     }
                 }
             }
+            float d[NQ][4];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 uint32_t w[4];
@@ -290,21 +325,23 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
                     const int b = 2 * x + y;
                     uint32_t w0[4], w1[4];
                     if (INT) {
-                        widen_ints(w[2 * y], Zero(zp[0][b]), w0);
-                        widen_ints(w[2 * y + 1], Zero(zp[1][b]), w1);
+                        widen_ints(w[2 * y], Zero(zp[0][b % kB]), w0);
+                        widen_ints(w[2 * y + 1], Zero(zp[1][b % kB]), w1);
                     } else {
                         mx4_half8(w[2 * y], w0);
                         mx4_half8(w[2 * y + 1], w1);
                     }
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
-                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        mma16816(d, w0[0], w1[0], w0[1], w1[1], xf[i][2 * b][n][0], xf[i][2 * b][n][1]);
-                        mma16816(d, w0[2], w1[2], w0[3], w1[3], xf[i][2 * b + 1][n][0], xf[i][2 * b + 1][n][1]);
-                        acc[n][0] = fmaf(d[0], sc[0][b], acc[n][0]);
-                        acc[n][1] = fmaf(d[1], sc[0][b], acc[n][1]);
-                        acc[n][2] = fmaf(d[2], sc[1][b], acc[n][2]);
-                        acc[n][3] = fmaf(d[3], sc[1][b], acc[n][3]);
+                        // one sum for what shares a scale
+                        if (b % (4 / kB) == 0) mma16816_first(d[n], w0[0], w1[0], w0[1], w1[1], xf[i][2 * b][n][0], xf[i][2 * b][n][1]);
+                        else mma16816(d[n], w0[0], w1[0], w0[1], w1[1], xf[i][2 * b][n][0], xf[i][2 * b][n][1]);
+                        mma16816(d[n], w0[2], w1[2], w0[3], w1[3], xf[i][2 * b + 1][n][0], xf[i][2 * b + 1][n][1]);
+                        if (b % (4 / kB) == 4 / kB - 1) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                acc[n][j] = i + b < 4 / kB ? d[n][j] * sc[j >> 1][b % kB] : fmaf(d[n][j], sc[j >> 1][b % kB], acc[n][j]);
+                        }
                     }
                 }
             }
@@ -319,7 +356,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
         }
         // one barrier a tile: `part` is written again two tiles on, past the next one
         __syncthreads();
-        for (int i = tid; i < NQ * 128; i += a.warps * 32) {
+        // other threads each time: they fall behind the rest
+        int i0 = tid - turn;
+        if (i0 < 0) i0 += threads;
+        turn = (turn + NQ * 128) % threads;
+        for (int i = i0; i < NQ * 128; i += threads) {
             float v = 0.0f;
 #pragma unroll 4
             for (int q = 0; q < a.warps; ++q) v += part[q * NQ * 128 + i];
@@ -348,13 +389,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
     cp_async_wait<0>();
 }
 
-template <bool INT, int NQ, int S>
-int launch(MatvecArgs a, int ranks, int clusters, cudaStream_t s) {
-    // as many stages as an SM's shared memory holds, four to six
-    const int sums = (2 * a.warps + kHold) * NQ * 128 * 4, room = 225 * 1024 - sums;
-    a.stages = std::min(6, room / (a.warps * stage_bytes(INT, S)));
-    const int smem = a.warps * a.stages * stage_bytes(INT, S) + sums;
-    MOE_CUDA_TRY(cudaFuncSetAttribute(matvec4_kernel<INT, NQ, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+template <int KIND, int NQ, int S>
+int launch(const MatvecArgs &a, int ranks, int clusters, cudaStream_t s) {
+    const auto kern = matvec4_kernel<KIND, NQ, S>;
+    const int smem = a.warps * kStages * stage_bytes(KIND != kMx, S) + (2 * a.warps + kHold) * NQ * 128 * 4 +
+                     (KIND == kMx ? a.warps * S * 64 * 4 : 0);
+    MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3((unsigned)(ranks * clusters));
     c.blockDim = dim3((unsigned)(a.warps * 32));
@@ -368,7 +408,7 @@ int launch(MatvecArgs a, int ranks, int clusters, cudaStream_t s) {
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     c.attrs = at;
     c.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&c, matvec4_kernel<INT, NQ, S>, (const MatvecArgs)a);
+    const cudaError_t e = cudaLaunchKernelEx(&c, kern, (const MatvecArgs)a);
     return e == cudaSuccess ? MOE_OK : cuda_fail("cudaLaunchKernelEx", e);
 }
 
@@ -389,7 +429,6 @@ int launch_w4_matvec(const moe_w4 *d, int T, const void *x, const void *codes, c
     a.group_shift = d->group == 32 ? 5 : d->group == 64 ? 6 : 7;
     a.s_f32 = d->scale_dtype == MOE_OUT_F32;
     a.out_bf16 = out_dtype == MOE_OUT_BF16;
-    a.stages = 0;
     // Slices a warp and CTAs a cluster: x's registers are 16 (8 rows) or 32 a slice
     const int per_warp = a.slices > kMaxWarps ? 2 : 1;
     int ranks = 1;
@@ -403,13 +442,15 @@ int launch_w4_matvec(const moe_w4 *d, int T, const void *x, const void *codes, c
     a.zero_words = zeros ? (strip + 3 + 3) / 4 : 0;
     const int tiles = (int)ceil_div(a.N, kTileRows);
     const int clusters = std::max(1, std::min(tiles, sm_count() / ranks));
-    const bool i = d->kind == MOE_W4_INT, wide = T > 8;
-    if (per_warp == 1) {
-        if (i) return wide ? launch<true, 2, 1>(a, ranks, clusters, s) : launch<true, 1, 1>(a, ranks, clusters, s);
-        return wide ? launch<false, 2, 1>(a, ranks, clusters, s) : launch<false, 1, 1>(a, ranks, clusters, s);
-    }
-    if (i) return wide ? launch<true, 2, 2>(a, ranks, clusters, s) : launch<true, 1, 2>(a, ranks, clusters, s);
-    return wide ? launch<false, 2, 2>(a, ranks, clusters, s) : launch<false, 1, 2>(a, ranks, clusters, s);
+    const bool wide = T > 8;
+    auto go = [&](auto kind) {
+        constexpr int K = decltype(kind)::value;
+        if (per_warp == 1) return wide ? launch<K, 2, 1>(a, ranks, clusters, s) : launch<K, 1, 1>(a, ranks, clusters, s);
+        return wide ? launch<K, 2, 2>(a, ranks, clusters, s) : launch<K, 1, 2>(a, ranks, clusters, s);
+    };
+    if (d->kind == MOE_W4_MX) return go(std::integral_constant<int, kMx>());
+    if (d->group == kSlice) return go(std::integral_constant<int, kIntSlice>());
+    return go(std::integral_constant<int, kIntBlocks>());
 }
 
 }  // namespace moe
