@@ -37,6 +37,8 @@ constexpr int kMaxWarps = 16;
 constexpr int kTileRows = 16, kSlice = 128;
 constexpr int kItemBytes = kTileRows * kSlice / 2;
 constexpr int kHold = 16;   // row tiles whose sums a CTA of a cluster holds between exchanges
+// Row tiles between two of a CTA's barriers, for 8 and 16 rows of x
+__host__ __device__ constexpr int batch_tiles(int nq) { return 4 / nq; }
 // Strips of scales and zero points: bytes of a row of W
 constexpr int kScaleStrip = 32, kZeroStrip = 12;
 
@@ -132,6 +134,7 @@ __device__ __forceinline__ void write(const MatvecArgs &a, int t, int n, float v
 template <int KIND, int NQ, int S>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const MatvecArgs a) {
     constexpr bool INT = KIND != kMx;
+    constexpr int kBatch = batch_tiles(NQ), kSums = NQ * 128;   // of a tile: [row of W][row of x]
     constexpr int kStage = stage_bytes(INT, S), kStrips = S * kItemBytes;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
@@ -143,9 +146,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
     const int mine = cluster < tiles ? (tiles - cluster + clusters - 1) / clusters : 0;
     uint8_t *ring = smem + warp * kStages * kStage;
     const uint32_t ring_addr = ptx::smem_u32(ring);
-    float *s_part = reinterpret_cast<float *>(smem + a.warps * kStages * kStage);   // [2][warps][NQ * 128]
-    float *s_hold = s_part + 2 * a.warps * NQ * 128;                                  // [kHold][NQ * 128]
-    float *s_scale = s_hold + kHold * NQ * 128 + warp * (S * 64);                      // MXFP4: [slice][row][block]
+    float *s_part = reinterpret_cast<float *>(smem + a.warps * kStages * kStage);   // [warps][kBatch][kSums]
+    float *s_hold = s_part + a.warps * kBatch * kSums;                                // [kHold][kSums]
+    float *s_scale = s_hold + kHold * kSums + warp * (S * 64);                      // MXFP4: [slice][row][block]
     const int row_bytes = a.K >> 1, groups = a.K >> a.group_shift;
     const int group0 = INT ? first_slice * (kSlice >> a.group_shift) : 0;
     const bool busy = first_slice < last_slice;
@@ -250,18 +253,20 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
     }
     const int mrow = (lane & 7) + ((lane >> 3) & 1) * 8, mblk = lane >> 4;
 
-    const int threads = a.warps * 32;
-    int turn = 0;
-
-    for (int it = 0; it < mine; ++it) {
-        cp_async_wait<kStages - 2>();
-        __syncwarp();
-        fetch();
+    for (int it0 = 0; it0 < mine; it0 += kBatch) {
+        const int batch = min(kBatch, mine - it0);
+        float acc[kBatch][NQ][4];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (u >= batch) break;
+            const int it = it0 + u;
+            cp_async_wait<kStages - 2>();
+            __syncwarp();
+            fetch();
         const uint8_t *stage = ring + from;
         const uint32_t slot = ring_addr + from;
         from = from == (kStages - 1) * kStage ? 0 : from + kStage;
         const int n0 = (cluster + it * clusters) * kTileRows;
-        float acc[NQ][4];
         if (KIND == kMx) {
             // Scales as numbers, each formed once: lane (row, half) two blocks of each slice.
             // 2^(byte - 127); byte 0 (2^-127) counts as zero, 255 as infinity: its codes are
@@ -340,48 +345,50 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
                         if (b % (4 / kB) == 4 / kB - 1) {
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                acc[n][j] = i + b < 4 / kB ? d[n][j] * sc[j >> 1][b % kB] : fmaf(d[n][j], sc[j >> 1][b % kB], acc[n][j]);
+                                acc[u][n][j] = i + b < 4 / kB ? d[n][j] * sc[j >> 1][b % kB] : fmaf(d[n][j], sc[j >> 1][b % kB], acc[u][n][j]);
                         }
                     }
                 }
             }
         }
-        // the warps' sums of this tile: [row of W][row of x]
-        float *part = s_part + (it & 1) * a.warps * NQ * 128;
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-            float *p = part + warp * NQ * 128 + 8 * n + 2 * c;
-            *reinterpret_cast<float2 *>(p + g * 8 * NQ) = make_float2(acc[n][0] * down[n][0], acc[n][1] * down[n][1]);
-            *reinterpret_cast<float2 *>(p + (g + 8) * 8 * NQ) = make_float2(acc[n][2] * down[n][0], acc[n][3] * down[n][1]);
         }
-        // one barrier a tile: `part` is written again two tiles on, past the next one
+        // the warps' sums of these tiles
+        if (it0) __syncthreads();   // those of the tiles before have been read
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (u >= batch) break;
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                float *p = s_part + (warp * kBatch + u) * kSums + 8 * n + 2 * c;
+                *reinterpret_cast<float2 *>(p + g * 8 * NQ) = make_float2(acc[u][n][0] * down[n][0], acc[u][n][1] * down[n][1]);
+                *reinterpret_cast<float2 *>(p + (g + 8) * 8 * NQ) = make_float2(acc[u][n][2] * down[n][0], acc[u][n][3] * down[n][1]);
+            }
+        }
         __syncthreads();
-        // other threads each time: they fall behind the rest
-        int i0 = tid - turn;
-        if (i0 < 0) i0 += threads;
-        turn = (turn + NQ * 128) % threads;
-        for (int i = i0; i < NQ * 128; i += threads) {
+        for (int i = tid; i < batch * kSums; i += a.warps * 32) {
             float v = 0.0f;
 #pragma unroll 4
-            for (int q = 0; q < a.warps; ++q) v += part[q * NQ * 128 + i];
-            const int t = i & (8 * NQ - 1), n = n0 + i / (8 * NQ);
-            if (ranks > 1) s_hold[(it % kHold) * NQ * 128 + i] = v;
-            else write(a, t, n, v);
+            for (int q = 0; q < a.warps; ++q) v += s_part[q * kBatch * kSums + i];
+            const int it = it0 + i / kSums, j = i % kSums;
+            if (ranks > 1) s_hold[(it % kHold) * kSums + j] = v;
+            else write(a, j & (8 * NQ - 1), (cluster + it * clusters) * kTileRows + j / (8 * NQ), v);
         }
-        if (ranks > 1 && (it % kHold == kHold - 1 || it == mine - 1)) {
+        static_assert(kHold % kBatch == 0, "a batch is held as a whole");
+        const int last = it0 + batch - 1;
+        if (ranks > 1 && (last % kHold == kHold - 1 || last == mine - 1)) {
             // the CTAs' sums together: CTA r finishes its share of what is held
-            const int held = it % kHold + 1, base = it - it % kHold;
+            const int held = last % kHold + 1, base = last - last % kHold;
             ptx::cluster_sync();
             const uint32_t mem = ptx::smem_u32(s_hold);
-            for (int i = rank * a.warps * 32 + tid; i < held * NQ * 128; i += ranks * a.warps * 32) {
+            for (int i = rank * a.warps * 32 + tid; i < held * kSums; i += ranks * a.warps * 32) {
                 float v = 0.0f;
                 for (int r = 0; r < ranks; ++r) {
                     float p;
                     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(ptx::cluster_map(mem + 4 * i, r)));
                     v += p;
                 }
-                const int j = i % (NQ * 128);
-                write(a, j & (8 * NQ - 1), (cluster + (base + i / (NQ * 128)) * clusters) * kTileRows + j / (8 * NQ), v);
+                const int j = i % kSums;
+                write(a, j & (8 * NQ - 1), (cluster + (base + i / kSums) * clusters) * kTileRows + j / (8 * NQ), v);
             }
             ptx::cluster_sync();   // nobody reads this CTA's shared memory any more
         }
@@ -392,7 +399,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
 template <int KIND, int NQ, int S>
 int launch(const MatvecArgs &a, int ranks, int clusters, cudaStream_t s) {
     const auto kern = matvec4_kernel<KIND, NQ, S>;
-    const int smem = a.warps * kStages * stage_bytes(KIND != kMx, S) + (2 * a.warps + kHold) * NQ * 128 * 4 +
+    const int smem = a.warps * kStages * stage_bytes(KIND != kMx, S) + (a.warps * batch_tiles(NQ) + kHold) * NQ * 128 * 4 +
                      (KIND == kMx ? a.warps * S * 64 * 4 : 0);
     MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     cudaLaunchConfig_t c = {};
