@@ -5,8 +5,8 @@
 //   a, b -> a cos - b sin, b cos + a sin      (the pairs of the first R channels)
 //
 // A head is dim / 8 neighbouring lanes of eight channels: the norm's sum and the
-// block maxima of MXFP4 (32 channels, four lanes) are butterflies over them, and
-// with pairs half a rotation apart the partner's channels are another lane's.
+// block maxima of MXFP4 are butterflies over them.  Where pairs are half a
+// rotation apart a lane takes four channels and their four partners.
 // Everything is fp32 until the one rounding of each output; keys go to four
 // bits from fp32, not by way of bf16.
 //
@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "mx4.cuh"
@@ -32,7 +33,7 @@ struct RopeArgs {
     const float *cos_sin;
     const void *w_q, *w_k;
     uint16_t *q_out, *k_out;
-    uint32_t *codes;
+    uint16_t *codes;
     uint8_t *scales;
     const int32_t *slots;
     int32_t *status;
@@ -41,146 +42,179 @@ struct RopeArgs {
     float eps;
 };
 
-__device__ __forceinline__ void unpack8(const uint4 q, float (&v)[8]) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
+// Pairs of fp32 numbers: the packed instructions do two channels each.
+using F2 = uint64_t;
+__device__ __forceinline__ F2 pair(float lo, float hi) { return ptx::pack2(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ float lo2(F2 v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi2(F2 v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-        w[j] = *reinterpret_cast<const uint32_t *>(&b);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ uint2 load_once(const uint16_t *p) {
+    uint2 v;
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
 }
-
-__device__ __forceinline__ void load_w(const void *w, int f32, int c, float (&v)[8]) {
+// Four channels as two pairs
+__device__ __forceinline__ void unpack4(const uint2 q, F2 (&v)[2]) {
+    v[0] = ptx::pack2(q.x << 16, q.x & 0xffff0000u);
+    v[1] = ptx::pack2(q.y << 16, q.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store4(uint16_t *p, const F2 (&v)[2]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(lo2(v[0]), hi2(v[0])), b = __floats2bfloat162_rn(lo2(v[1]), hi2(v[1]));
+    asm volatile("st.global.L1::no_allocate.v2.b32 [%0], {%1, %2};" ::"l"(p),
+                 "r"(*reinterpret_cast<const uint32_t *>(&a)), "r"(*reinterpret_cast<const uint32_t *>(&b))
+                 : "memory");
+}
+__device__ __forceinline__ void load_w(const void *w, int f32, int ch, F2 (&v)[2]) {
     if (f32) {
-        const float4 a = static_cast<const float4 *>(w)[2 * c], b = static_cast<const float4 *>(w)[2 * c + 1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const float *>(w) + ch);
+        v[0] = ptx::pack2(a.x, a.y), v[1] = ptx::pack2(a.z, a.w);
     } else {
-        unpack8(static_cast<const uint4 *>(w)[c], v);
+        unpack4(*reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(w) + ch), v);
     }
+}
+__device__ __forceinline__ uint32_t magnitude(const F2 (&v)[2]) {   // the largest of four
+    const uint32_t k = 0x7fffffffu;
+    return max(max((uint32_t)v[0] & k, (uint32_t)(v[0] >> 32) & k), max((uint32_t)v[1] & k, (uint32_t)(v[1] >> 32) & k));
 }
 
 // U heads of a thread's own at a time.  D: channels of a head.  PAIRS: neighbours
 // are a pair, else channels R / 2 apart.
 template <int D, bool PAIRS, int U>
-__global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopeArgs a) {
     constexpr int N8 = D / 8, kHeads = kRopeThreads / N8;   // lanes of a head, heads at a time
     const int c = threadIdx.x % N8, g = threadIdx.x / N8;
-    const int lane = threadIdx.x & 31, base = lane & ~(N8 - 1);
     const int64_t t = blockIdx.x;
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
-    const int heads = a.Hq + a.Hk + (a.codes ? a.Hk : 0);
-    const uint4 *row = reinterpret_cast<const uint4 *>(a.qkv + t * a.stride) + c;
+    const int heads = a.Hq + a.Hk + (a.codes ? a.Hk : 0), keyed = a.Hq + a.Hk;
+    // This lane's channels: two fours, of which the second is the first one's partner
+    // where pairs are half a rotation apart (no shuffles); of values eight neighbours.
+    const bool turned = c < a.R / 8, split = !PAIRS && turned;
+    const int ch_a = split ? 4 * c : 8 * c, ch_b = split ? a.R / 2 + 4 * c : 8 * c + 4;
+    const uint16_t *row = a.qkv + t * a.stride;
+    const int first = blockIdx.y * kHeads * U;
+    uint2 raw[U][2];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + u * kHeads + g;
+            raw[u][0] = raw[u][1] = make_uint2(0, 0);
+            if (h < heads) {
+                const uint16_t *p = row + h * D;
+                raw[u][0] = load_once(p + (h < keyed ? ch_a : 8 * c));
+                raw[u][1] = load_once(p + (h < keyed ? ch_b : 8 * c + 4));
+            }
+        }
+    };
+    load(first);   // before what the position is waited for
     const int pos = a.R ? a.positions[t] : 0;
     const int slot = a.codes ? a.slots[t] : -1;
+    F2 wq[2][2], wk[2][2];
+    if (a.w_q) load_w(a.w_q, a.w_f32, ch_a, wq[0]), load_w(a.w_q, a.w_f32, ch_b, wq[1]);
+    if (a.w_k) load_w(a.w_k, a.w_f32, ch_a, wk[0]), load_w(a.w_k, a.w_f32, ch_b, wk[1]);
     if (pos < 0 || (a.R && pos >= a.max_positions) || slot < -1 || slot >= a.slots_in_cache) {
         if (threadIdx.x == 0 && a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
         return;   // the CTA
     }
-    // this lane's angles; past the rotated channels cos 1, sin 0
-    float cs[8], sn[8];
-    const int half = a.R / 16;   // in lanes
-    const bool turned = c < 2 * half;
-    const int partner = base + (c < half ? c + half : c - half);
+    // The angles: halves, of this lane's four pairs; neighbours, of each four's two pairs,
+    // both cosines and (-sin, sin) twice
+    F2 cs[PAIRS ? 4 : 2], sn[PAIRS ? 4 : 2];
     if (turned) {
-        const float *table = a.cos_sin + (int64_t)pos * a.R;
+        const float *table = a.cos_sin + (int64_t)pos * a.R + 4 * c;
+        const uint4 x = *reinterpret_cast<const uint4 *>(table), y = *reinterpret_cast<const uint4 *>(table + a.R / 2);
         if (PAIRS) {
-            const float4 x = *reinterpret_cast<const float4 *>(table + 4 * c);
-            const float4 y = *reinterpret_cast<const float4 *>(table + a.R / 2 + 4 * c);
-            cs[0] = cs[1] = x.x, cs[2] = cs[3] = x.y, cs[4] = cs[5] = x.z, cs[6] = cs[7] = x.w;
-            sn[0] = sn[1] = y.x, sn[2] = sn[3] = y.y, sn[4] = sn[5] = y.z, sn[6] = sn[7] = y.w;
+            const uint32_t neg = 0x80000000u;
+            cs[0] = ptx::pack2(x.x, x.x), cs[1] = ptx::pack2(x.y, x.y);
+            cs[PAIRS ? 2 : 0] = ptx::pack2(x.z, x.z), cs[PAIRS ? 3 : 1] = ptx::pack2(x.w, x.w);
+            sn[0] = ptx::pack2(y.x ^ neg, y.x), sn[1] = ptx::pack2(y.y ^ neg, y.y);
+            sn[PAIRS ? 2 : 0] = ptx::pack2(y.z ^ neg, y.z), sn[PAIRS ? 3 : 1] = ptx::pack2(y.w ^ neg, y.w);
         } else {
-            const int i = 8 * (c < half ? c : c - half);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float4 x = *reinterpret_cast<const float4 *>(table + i + 4 * j);
-                const float4 y = *reinterpret_cast<const float4 *>(table + a.R / 2 + i + 4 * j);
-                cs[4 * j] = x.x, cs[4 * j + 1] = x.y, cs[4 * j + 2] = x.z, cs[4 * j + 3] = x.w;
-                sn[4 * j] = y.x, sn[4 * j + 1] = y.y, sn[4 * j + 2] = y.z, sn[4 * j + 3] = y.w;
-            }
-            if (c < half)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sn[j] = -sn[j];   // a cos - b sin; b cos + a sin
+            cs[0] = ptx::pack2(x.x, x.y), cs[1] = ptx::pack2(x.z, x.w);
+            sn[0] = ptx::pack2(y.x, y.y), sn[1] = ptx::pack2(y.z, y.w);
         }
     }
     const int64_t at = a.codes ? (((int64_t)(slot >> a.page_shift) * 2 * a.Hk) << a.page_shift) +
                                      (slot & ((1 << a.page_shift) - 1))
                                : 0;
     // every thread of a warp goes through the same rounds: shuffles inside
-    for (int h0 = blockIdx.y * kHeads * U; h0 < heads; h0 += gridDim.y * kHeads * U) {
-        uint4 raw[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * kHeads + g;
-            if (h < heads) raw[u] = ptx::load_past_l1(row + (int64_t)h * N8);
-            else raw[u] = make_uint4(0, 0, 0, 0);
-        }
+    for (int h0 = first;;) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int h = h0 + u * kHeads + g;
             if (h0 + u * kHeads >= heads) break;   // the CTA
-            const bool is_v = h >= a.Hq + a.Hk, is_k = !is_v && h >= a.Hq;
-            float v[8];
-            unpack8(raw[u], v);
-            const void *w = is_k ? a.w_k : a.w_q;
-            float sum = 0.0f;
+            const bool is_v = h >= keyed, is_k = !is_v && h >= a.Hq;
+            F2 x[2], y[2];
+            unpack4(raw[u][0], x);
+            unpack4(raw[u][1], y);
+            if (a.w_q || a.w_k) {
+                F2 s2 = mul2(x[0], x[0]);
+                s2 = ptx::fma2(x[1], x[1], s2);
+                s2 = ptx::fma2(y[0], y[0], s2);
+                s2 = ptx::fma2(y[1], y[1], s2);
+                float sum = lo2(s2) + hi2(s2);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
-#pragma unroll
-            for (int o = N8 / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (w && !is_v) {
+                for (int o = N8 / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 const float inv = rsqrtf(sum * (1.0f / D) + a.eps);
-                float wv[8];
-                load_w(w, a.w_f32, c, wv);
+                const F2 i2 = pair(inv, inv);
+                if (h < a.Hq) {
+                    if (a.w_q)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = v[j] * inv * wv[j];
+                        for (int j = 0; j < 2; ++j) x[j] = mul2(mul2(x[j], i2), wq[0][j]), y[j] = mul2(mul2(y[j], i2), wq[1][j]);
+                } else if (is_k && a.w_k) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) x[j] = mul2(mul2(x[j], i2), wk[0][j]), y[j] = mul2(mul2(y[j], i2), wk[1][j]);
+                }
             }
-            if (PAIRS) {
-                if (turned && !is_v)
+            if (turned && !is_v) {
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        const float x = v[j], y = v[j + 1];
-                        v[j] = x * cs[j] - y * sn[j];
-                        v[j + 1] = y * cs[j] + x * sn[j];
+                for (int j = 0; j < 2; ++j) {
+                    if (PAIRS) {
+                        x[j] = ptx::fma2(x[j], cs[j], mul2(pair(hi2(x[j]), lo2(x[j])), sn[j]));
+                        y[j] = ptx::fma2(y[j], cs[PAIRS ? 2 + j : 0], mul2(pair(hi2(y[j]), lo2(y[j])), sn[PAIRS ? 2 + j : 0]));
+                    } else {
+                        const F2 m = mul2(y[j], sn[j]);
+                        y[j] = ptx::fma2(y[j], cs[j], mul2(x[j], sn[j]));
+                        x[j] = ptx::fma2(x[j], cs[j], m ^ 0x8000000080000000ull);
                     }
-            } else if (a.R) {
-                float o[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = __shfl_sync(0xffffffffu, v[j], turned ? partner : lane);
-                if (turned && !is_v)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = fmaf(v[j], cs[j], o[j] * sn[j]);
+                }
             }
-            if (h < a.Hq) {
-                ptx::store_past_l1(reinterpret_cast<uint4 *>(a.q_out + (t * a.Hq + h) * D) + c, pack8(v));
-            } else if (is_k && a.k_out) {
-                ptx::store_past_l1(reinterpret_cast<uint4 *>(a.k_out + (t * a.Hk + h - a.Hq) * D) + c, pack8(v));
-            }
+            uint16_t *dst = h < a.Hq ? a.q_out + (t * a.Hq + h) * D : is_k && a.k_out ? a.k_out + (t * a.Hk + h - a.Hq) * D : nullptr;
+            if (dst) store4(dst + ch_a, x), store4(dst + ch_b, y);
             if (a.codes && h0 + (u + 1) * kHeads > a.Hq) {   // the CTA: some of these heads are cached
-                uint32_t m = 0;
+                // the blocks that this lane's channels are in, and their largest magnitudes
+                const int at_a = is_v ? 8 * c : ch_a, at_b = is_v ? 8 * c + 4 : ch_b;
+                const int blk_a = at_a >> 5, blk_b = at_b >> 5;
+                const uint32_t ma = magnitude(x), mb = magnitude(y);
+                uint32_t byte_a = 0, byte_b = 0, mine = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                if (h >= a.Hq && h < heads && slot >= 0) {
+                for (int b = 0; b < D / 32; ++b) {
+                    uint32_t m = max(blk_a == b ? ma : 0u, blk_b == b ? mb : 0u);
+#pragma unroll
+                    for (int o = N8 / 2; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
                     const uint32_t byte = mx4_scale_byte(m);
+                    if (blk_a == b) byte_a = byte;
+                    if (blk_b == b) byte_b = byte;
+                    if (c == b) mine = byte;
+                }
+                if (h >= a.Hq && h < heads && slot >= 0) {
                     // keys' heads, then values' heads, follow one another in a page
                     const int64_t r = at + ((int64_t)(h - a.Hq) << a.page_shift);
-                    a.codes[r * N8 + c] = mx4_codes8(v, byte);
-                    if ((c & 3) == 0) a.scales[(r * N8 + c) >> 2] = (uint8_t)byte;
+                    const float fa[8] = {lo2(x[0]), hi2(x[0]), lo2(x[1]), hi2(x[1]), 0.0f, 0.0f, 0.0f, 0.0f};
+                    const float fb[8] = {lo2(y[0]), hi2(y[0]), lo2(y[1]), hi2(y[1]), 0.0f, 0.0f, 0.0f, 0.0f};
+                    a.codes[r * (D / 4) + (at_a >> 2)] = (uint16_t)mx4_codes8(fa, byte_a);
+                    a.codes[r * (D / 4) + (at_b >> 2)] = (uint16_t)mx4_codes8(fb, byte_b);
+                    if (c < D / 32) a.scales[r * (D / 32) + c] = (uint8_t)mine;
                 }
             }
         }
+        h0 += gridDim.y * kHeads * U;
+        if (h0 >= heads) break;
+        load(h0);
     }
 }
 
@@ -198,7 +232,7 @@ int launch_qk_norm_rope(const moe_qk_rope *d, int T, const void *qkv, const int3
     a.w_k = w_k;
     a.q_out = static_cast<uint16_t *>(q_out);
     a.k_out = static_cast<uint16_t *>(k_out);
-    a.codes = cache ? static_cast<uint32_t *>(cache->codes) : nullptr;
+    a.codes = cache ? static_cast<uint16_t *>(cache->codes) : nullptr;
     a.scales = cache ? static_cast<uint8_t *>(cache->scales) : nullptr;
     a.slots = slots;
     a.status = status;
@@ -223,13 +257,17 @@ int launch_qk_norm_rope(const moe_qk_rope *d, int T, const void *qkv, const int3
         return launch_dependent(kern, dim3((unsigned)T, spread ? parts : 1u), dim3(kRopeThreads), 0, s,
                                 (const RopeArgs)a);
     };
-    const bool few = (int64_t)T * heads < 64 * sm_count();
-    if (d->dim == 64) {
-        if (pairs) return few ? go(qk_rope_kernel<64, true, 1>, 1) : go(qk_rope_kernel<64, true, 4>, 4);
-        return few ? go(qk_rope_kernel<64, false, 1>, 1) : go(qk_rope_kernel<64, false, 4>, 4);
-    }
-    if (pairs) return few ? go(qk_rope_kernel<128, true, 1>, 1) : go(qk_rope_kernel<128, true, 4>, 4);
-    return few ? go(qk_rope_kernel<128, false, 1>, 1) : go(qk_rope_kernel<128, false, 4>, 4);
+    // Heads of a thread at once: one where there are few rows, else three.
+    const int u = (int64_t)T * heads < 64 * sm_count() ? 1 : 3;
+    auto pick = [&](auto dim, auto p) {
+        constexpr int D = decltype(dim)::value;
+        constexpr bool P = decltype(p)::value;
+        return u == 1 ? go(qk_rope_kernel<D, P, 1>, 1) : go(qk_rope_kernel<D, P, 3>, 3);
+    };
+    using std::integral_constant;
+    if (d->dim == 64)
+        return pairs ? pick(integral_constant<int, 64>(), std::true_type()) : pick(integral_constant<int, 64>(), std::false_type());
+    return pairs ? pick(integral_constant<int, 128>(), std::true_type()) : pick(integral_constant<int, 128>(), std::false_type());
 }
 
 }  // namespace moe
