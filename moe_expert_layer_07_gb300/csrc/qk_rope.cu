@@ -10,9 +10,9 @@
 // Everything is fp32 until the one rounding of each output; keys go to four
 // bits from fp32, not by way of bf16.
 //
-// Bound by memory: a row is read and written once.  A CTA keeps one token's
-// angles in registers over all of the token's heads that it takes, whose loads
-// are under way together.
+// Bound by memory: a row is read and written once.  A warp keeps one token's
+// angles in registers over the heads that it takes, the next ones' loads under
+// way.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -38,7 +38,7 @@ struct RopeArgs {
     const int32_t *slots;
     int32_t *status;
     int64_t stride, slots_in_cache;
-    int Hq, Hk, R, w_f32, max_positions, page_shift;
+    int T, parts, Hq, Hk, R, w_f32, max_positions, page_shift;   // parts: warps that share a row
     float eps;
 };
 
@@ -86,18 +86,20 @@ __device__ __forceinline__ uint32_t magnitude(const F2 (&v)[2]) {   // the large
 // are a pair, else channels R / 2 apart.
 template <int D, bool PAIRS, int U>
 __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopeArgs a) {
-    constexpr int N8 = D / 8, kHeads = kRopeThreads / N8;   // lanes of a head, heads at a time
-    const int c = threadIdx.x % N8, g = threadIdx.x / N8;
-    const int64_t t = blockIdx.x;
+    constexpr int N8 = D / 8, kHeads = 32 / N8;   // lanes of a head, heads of a warp at a time
+    const int lane = threadIdx.x & 31, c = lane % N8, g = lane / N8;
+    const int64_t job = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+    const int64_t t = job / a.parts;
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
+    if (t >= a.T) return;
     const int heads = a.Hq + a.Hk + (a.codes ? a.Hk : 0), keyed = a.Hq + a.Hk;
     // This lane's channels: two fours, of which the second is the first one's partner
     // where pairs are half a rotation apart (no shuffles); of values eight neighbours.
     const bool turned = c < a.R / 8, split = !PAIRS && turned;
     const int ch_a = split ? 4 * c : 8 * c, ch_b = split ? a.R / 2 + 4 * c : 8 * c + 4;
     const uint16_t *row = a.qkv + t * a.stride;
-    const int first = blockIdx.y * kHeads * U;
+    const int first = (int)(job - t * a.parts) * kHeads * U, step = a.parts * kHeads * U;
     uint2 raw[U][2];
     auto load = [&](int h0) {
 #pragma unroll
@@ -118,8 +120,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopeArgs
     if (a.w_q) load_w(a.w_q, a.w_f32, ch_a, wq[0]), load_w(a.w_q, a.w_f32, ch_b, wq[1]);
     if (a.w_k) load_w(a.w_k, a.w_f32, ch_a, wk[0]), load_w(a.w_k, a.w_f32, ch_b, wk[1]);
     if (pos < 0 || (a.R && pos >= a.max_positions) || slot < -1 || slot >= a.slots_in_cache) {
-        if (threadIdx.x == 0 && a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
-        return;   // the CTA
+        if (lane == 0 && a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
+        return;   // the warp
     }
     // The angles: halves, of this lane's four pairs; neighbours, of each four's two pairs,
     // both cosines and (-sin, sin) twice
@@ -142,15 +144,19 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopeArgs
                                      (slot & ((1 << a.page_shift) - 1))
                                : 0;
     // every thread of a warp goes through the same rounds: shuffles inside
-    for (int h0 = first;;) {
+    for (int h0 = first; h0 < heads; h0 += step) {
+        uint2 now[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) now[u][0] = raw[u][0], now[u][1] = raw[u][1];
+        load(h0 + step);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int h = h0 + u * kHeads + g;
-            if (h0 + u * kHeads >= heads) break;   // the CTA
+            if (h0 + u * kHeads >= heads) break;   // the warp
             const bool is_v = h >= keyed, is_k = !is_v && h >= a.Hq;
             F2 x[2], y[2];
-            unpack4(raw[u][0], x);
-            unpack4(raw[u][1], y);
+            unpack4(now[u][0], x);
+            unpack4(now[u][1], y);
             if (a.w_q || a.w_k) {
                 F2 s2 = mul2(x[0], x[0]);
                 s2 = ptx::fma2(x[1], x[1], s2);
@@ -185,7 +191,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopeArgs
             }
             uint16_t *dst = h < a.Hq ? a.q_out + (t * a.Hq + h) * D : is_k && a.k_out ? a.k_out + (t * a.Hk + h - a.Hq) * D : nullptr;
             if (dst) store4(dst + ch_a, x), store4(dst + ch_b, y);
-            if (a.codes && h0 + (u + 1) * kHeads > a.Hq) {   // the CTA: some of these heads are cached
+            if (a.codes && h0 + (u + 1) * kHeads > a.Hq) {   // the warp: some of these heads are cached
                 // the blocks that this lane's channels are in, and their largest magnitudes
                 const int at_a = is_v ? 8 * c : ch_a, at_b = is_v ? 8 * c + 4 : ch_b;
                 const int blk_a = at_a >> 5, blk_b = at_b >> 5;
@@ -212,9 +218,6 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopeArgs
                 }
             }
         }
-        h0 += gridDim.y * kHeads * U;
-        if (h0 >= heads) break;
-        load(h0);
     }
 }
 
@@ -249,20 +252,21 @@ int launch_qk_norm_rope(const moe_qk_rope *d, int T, const void *qkv, const int3
     a.eps = d->eps;
     const int heads = a.Hq + a.Hk + (cache ? a.Hk : 0);
     const bool pairs = d->style == MOE_ROPE_PAIRS;
-    auto go = [&](auto kern, int u) {
-        const int at_once = kRopeThreads / (d->dim / 8) * u;
-        const unsigned parts = (unsigned)std::min<int64_t>(ceil_div(heads, at_once), 65535);
-        // few tokens: each round of heads in a CTA of its own
-        const bool spread = (int64_t)T < 4 * sm_count();
-        return launch_dependent(kern, dim3((unsigned)T, spread ? parts : 1u), dim3(kRopeThreads), 0, s,
+    a.T = T;
+    // As many warps to a row as fill the GPU; where that leaves each a round, one head at
+    // a time.
+    const int at_once = 32 / (d->dim / 8);
+    const int most = (int)ceil_div(heads, at_once);
+    a.parts = (int)std::max<int64_t>(1, std::min<int64_t>(most, (int64_t)sm_count() * 32 / T));
+    const bool one = a.parts * 2 > most;
+    auto go = [&](auto kern) {
+        return launch_dependent(kern, dim3((unsigned)ceil_div((int64_t)T * a.parts, kRopeThreads / 32)), dim3(kRopeThreads), 0, s,
                                 (const RopeArgs)a);
     };
-    // Heads of a thread at once: one where there are few rows, else three.
-    const int u = (int64_t)T * heads < 64 * sm_count() ? 1 : 3;
     auto pick = [&](auto dim, auto p) {
         constexpr int D = decltype(dim)::value;
         constexpr bool P = decltype(p)::value;
-        return u == 1 ? go(qk_rope_kernel<D, P, 1>, 1) : go(qk_rope_kernel<D, P, 3>, 3);
+        return one ? go(qk_rope_kernel<D, P, 1>) : go(qk_rope_kernel<D, P, 2>);
     };
     using std::integral_constant;
     if (d->dim == 64)
