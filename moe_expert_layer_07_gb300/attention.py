@@ -120,9 +120,10 @@ def cache_tables(held, new_tokens, free_pages, free_range, page, table, lengths,
     n, f = slots.shape[0], free_pages.shape[0]
     i64 = torch.int64
     # one test of all that holds in a correct call; what failed is looked up after
-    if not (all(t.dtype is _I32 and t.is_cuda and t.is_contiguous()
-                for t in (held, new_tokens, free_pages, table, lengths, starts, slots, positions))
-            and free_range.dtype is i64 and free_out.dtype is i64 and free_range.is_cuda and free_out.is_cuda
+    good = True
+    for t in (held, new_tokens, free_pages, table, lengths, starts, slots, positions):
+        good = good and t.dtype is _I32 and t.is_cuda and t.is_contiguous()
+    if not (good and free_range.dtype is i64 and free_out.dtype is i64 and free_range.is_cuda and free_out.is_cuda
             and free_range.is_contiguous() and free_out.is_contiguous() and free_range.shape == free_out.shape == (2,)
             and held.shape == new_tokens.shape == lengths.shape == (B,) and table.shape == (B, w)
             and starts.shape == (B + 1,) and slots.shape == positions.shape == (n,)
@@ -155,28 +156,24 @@ def qk_norm_rope(qkv, positions, cos_sin, q_heads, kv_heads, q_out, k_out=None, 
     rot = 0 if cos_sin is None else cos_sin.shape[-1]
     param = w_q if w_q is not None else w_k
     pkind = OUT_BF16 if param is None else _OUT.get(param.dtype)
-    cuda = qkv.is_cuda and q_out.is_cuda
-    if not (cuda and qkv.dtype is _BF16 and q_out.dtype is _BF16 and qkv.dim() == 2 and pkind is not None
-            and qkv.stride(1) == 1 and qkv.shape[1] >= (q_heads + 2 * kv_heads) * dim
-            and q_out.shape == (T, q_heads, dim) and q_out.is_contiguous()):
-        if qkv.dtype is not _BF16:
-            raise TypeError(f"qkv: expected a bfloat16 tensor, got {qkv.dtype}")
-        _typed(q_out, _BF16, (T, q_heads, dim), "q_out")
-        if pkind is None:
-            raise TypeError(f"w_q, w_k: expected float32 or bfloat16 tensors, got {param.dtype}")
-        raise ValueError(f"qkv: expected CUDA rows of {q_heads} + 2 x {kv_heads} heads of {dim}, got {tuple(qkv.shape)}")
-    for name, w in (("w_q", w_q), ("w_k", w_k)):
+    # one test of all that holds in a correct call; what failed is looked up after
+    good = (pkind is not None and qkv.dtype is _BF16 and q_out.dtype is _BF16 and qkv.is_cuda and q_out.is_cuda
+            and qkv.dim() == 2 and qkv.stride(1) == 1 and qkv.shape[1] >= (q_heads + 2 * kv_heads) * dim
+            and q_out.shape == (T, q_heads, dim) and q_out.is_contiguous() and (cache is None) == (slots is None))
+    for w in (w_q, w_k):
         if w is not None:
-            _typed(w, param.dtype, (dim,), name)
+            good = good and w.dtype is param.dtype and w.shape == (dim,) and w.is_cuda and w.is_contiguous()
     if k_out is not None:
-        _typed(k_out, _BF16, (T, kv_heads, dim), "k_out")
+        good = (good and k_out.dtype is _BF16 and k_out.shape == (T, kv_heads, dim) and k_out.is_cuda
+                and k_out.is_contiguous())
     if rot:
-        _typed(cos_sin, torch.float32, (cos_sin.shape[0], rot), "cos_sin")
-        _typed(positions, _I32, (T,), "positions")
-    if (cache is None) != (slots is None):
-        raise ValueError("cache and slots go together")
+        good = (good and cos_sin.dtype is torch.float32 and cos_sin.dim() == 2 and cos_sin.is_cuda
+                and cos_sin.is_contiguous() and positions.dtype is _I32 and positions.shape == (T,)
+                and positions.is_cuda and positions.is_contiguous())
     if slots is not None:
-        _typed(slots, _I32, (T,), "slots")
+        good = good and slots.dtype is _I32 and slots.shape == (T,) and slots.is_cuda and slots.is_contiguous()
+    if not good:
+        _refuse_rope(qkv, positions, cos_sin, rot, q_heads, kv_heads, q_out, k_out, w_q, w_k, param, pkind, cache, slots)
     stride = qkv.stride(0) if T > 1 else qkv.shape[1]
     key = (q_heads, kv_heads, dim, rot, style, pkind, cos_sin.shape[0] if rot else 0, stride, eps)
     d = _ROPES.get(key)   # descriptions are plain values: made once each
@@ -191,6 +188,29 @@ def qk_norm_rope(qkv, positions, cos_sin, q_heads, kv_heads, q_out, k_out=None, 
         _check(rc, "moe_qk_norm_rope")
 
 
+def _refuse_rope(qkv, positions, cos_sin, rot, q_heads, kv_heads, q_out, k_out, w_q, w_k, param, pkind, cache, slots):
+    """Raises what is wrong with qk_norm_rope's tensors."""
+    T, dim = qkv.shape[0], q_out.shape[-1]
+    if qkv.dtype is not _BF16:
+        raise TypeError(f"qkv: expected a bfloat16 tensor, got {qkv.dtype}")
+    _typed(q_out, _BF16, (T, q_heads, dim), "q_out")
+    if pkind is None:
+        raise TypeError(f"w_q, w_k: expected float32 or bfloat16 tensors, got {param.dtype}")
+    for name, w in (("w_q", w_q), ("w_k", w_k)):
+        if w is not None:
+            _typed(w, param.dtype, (dim,), name)
+    if k_out is not None:
+        _typed(k_out, _BF16, (T, kv_heads, dim), "k_out")
+    if rot:
+        _typed(cos_sin, torch.float32, (cos_sin.shape[0], rot), "cos_sin")
+        _typed(positions, _I32, (T,), "positions")
+    if (cache is None) != (slots is None):
+        raise ValueError("cache and slots go together")
+    if slots is not None:
+        _typed(slots, _I32, (T,), "slots")
+    raise ValueError(f"qkv: expected CUDA rows of {q_heads} + 2 x {kv_heads} heads of {dim}, got {tuple(qkv.shape)}")
+
+
 _ROPES: dict = {}
 
 
@@ -198,10 +218,16 @@ def cache_read(cache: Cache4, slots, k=None, v=None, status=None, stream=None):
     """The values in `slots` of the cache: k, v bf16 [n, kv_heads, dim], either may be None.  Rows of
     slot -1 are left as they were."""
     n = slots.shape[0]
-    _typed(slots, _I32, (n,), "slots")
-    for name, t in (("k", k), ("v", v)):
+    shape = (n, cache.kv_heads, cache.dim)
+    good = slots.dtype is _I32 and slots.shape == (n,) and slots.is_cuda and slots.is_contiguous()
+    for t in (k, v):
         if t is not None:
-            _typed(t, _BF16, (n, cache.kv_heads, cache.dim), name)
+            good = good and t.dtype is _BF16 and t.shape == shape and t.is_cuda and t.is_contiguous()
+    if not good:
+        _typed(slots, _I32, (n,), "slots")
+        for name, t in (("k", k), ("v", v)):
+            if t is not None:
+                _typed(t, _BF16, shape, name)
     rc = lib().moe_cache_read(cache.c, n, slots.data_ptr(), _at(k), _at(v), _word(status), _stream(stream))
     if rc:
         _check(rc, "moe_cache_read")

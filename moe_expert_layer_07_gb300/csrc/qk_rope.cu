@@ -253,11 +253,12 @@ int launch_qk_norm_rope(const moe_qk_rope *d, int T, const void *qkv, const int3
     const int heads = a.Hq + a.Hk + (cache ? a.Hk : 0);
     const bool pairs = d->style == MOE_ROPE_PAIRS;
     a.T = T;
-    // As many warps to a row as fill the GPU; where that leaves each a round, one head at
-    // a time.
+    // As many warps to a row as give an SM three times the warps that it holds (5001 rows of
+    // 40 heads of 64: 23 us with one to a row, two of which do not fit at once, 20 with two);
+    // where that leaves each a round, one head at a time.
     const int at_once = 32 / (d->dim / 8);
     const int most = (int)ceil_div(heads, at_once);
-    a.parts = (int)std::max<int64_t>(1, std::min<int64_t>(most, (int64_t)sm_count() * 32 / T));
+    a.parts = (int)std::max<int64_t>(1, std::min<int64_t>(most, (int64_t)sm_count() * 96 / T));
     const bool one = a.parts * 2 > most;
     auto go = [&](auto kern) {
         return launch_dependent(kern, dim3((unsigned)ceil_div((int64_t)T * a.parts, kRopeThreads / 32)), dim3(kRopeThreads), 0, s,
