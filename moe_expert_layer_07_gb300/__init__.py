@@ -31,7 +31,7 @@ __all__ = ["Config", "Weights", "WsLayout", "lib", "make_config", "route", "rout
            "pack_mx4_weights", "mx4_grouped_gemm", "mx4_grouped_gemm_swiglu", "Norm", "block_norm", "NORM_RMS", "NORM_LAYER", "GATE_NONE",
            "GATE_FEATURE", "GATE_TOKEN", "GATE_FULL",
            # attention over a cache in four bits (attention.py)
-           "Cache4", "CacheAttention", "cache_tables", "cache_read", "qk_norm_rope", "rope_table",
+           "Cache4", "CacheAttention", "PageTables", "AttentionBlock", "cache_tables", "cache_read", "qk_norm_rope", "rope_table",
            "w4_matvec", "ROPE_HALVES", "ROPE_PAIRS"]
 
 SOFTMAX, SIGMOID = 0, 1
@@ -682,5 +682,5 @@ from .block import (GATE_FEATURE, GATE_FULL, GATE_NONE, GATE_TOKEN, NORM_LAYER, 
                     mx4_dequantize, mx4_grouped_gemm, mx4_grouped_gemm_swiglu, mx4_quantize,
                     pack_mx4_weights)
 from . import attention  # noqa: E402
-from .attention import (ROPE_HALVES, ROPE_PAIRS, Cache4, CacheAttention, cache_read,  # noqa: E402
-                        cache_tables, qk_norm_rope, rope_table, w4_matvec)
+from .attention import (ROPE_HALVES, ROPE_PAIRS, AttentionBlock, Cache4, CacheAttention,  # noqa: E402
+                        PageTables, cache_read, cache_tables, qk_norm_rope, rope_table, w4_matvec)

@@ -330,3 +330,125 @@ def w4_matvec(x, codes, scales, out, zeros=None, stream=None):
 
 
 _W4S: dict = {}
+
+
+# ---- a decoder's attention block ---------------------------------------------------------------
+
+
+class PageTables:
+    """The tables of a cache's pages for up to `requests` requests, on the GPU: step() takes the
+    requests one step on, in one launch that a CUDA graph can hold.
+
+    lengths int32 [requests], table int32 [requests, max_pages], and of the step: starts
+    [requests + 1], slots and positions [max_tokens].  status: the device status word."""
+
+    def __init__(self, cache: Cache4, requests, max_pages, max_tokens):
+        dev = cache.codes.device
+        zeros = lambda *n: torch.zeros(*n, dtype=_I32, device=dev)  # noqa: E731
+        self.page = cache.page
+        self.lengths, self.table = zeros(requests), zeros(requests, max_pages)
+        self.starts, self.slots, self.positions = zeros(requests + 1), zeros(max_tokens), zeros(max_tokens)
+        self.free_pages = torch.arange(cache.pages, dtype=_I32, device=dev)
+        self.free_range = torch.tensor([0, cache.pages], dtype=torch.int64, device=dev)
+        self.status = zeros(1)
+
+    def step(self, new_tokens, stream=None):
+        """new_tokens int32 [requests]: how many tokens each request gets."""
+        cache_tables(self.lengths, new_tokens, self.free_pages, self.free_range, self.page, self.table,
+                     self.lengths, self.starts, self.slots, self.positions, self.free_range, self.status, stream)
+
+    def release(self, request, length):
+        """Gives the pages of a request that holds `length` tokens back; it holds none then.  On the
+        current stream, between steps."""
+        n = -(-length // self.page)
+        at = (self.free_range[1] + torch.arange(n, device=self.free_pages.device)) % self.free_pages.shape[0]
+        self.free_pages[at] = self.table[request, :n]
+        self.free_range[1] += n
+        self.lengths[request] = 0
+
+
+class AttentionBlock:
+    """q, k, v = x W_qkv;  q, k normed and rotated, k and v into the cache;  o = attention;
+    r = residual_scale r + branch_scale gate norm(o W_o) w_post: the attention half of a decoder
+    layer, beside MoEBlock.
+
+    w_qkv, w_o: MXFP4 (codes [N, K/2], scale bytes [N, K/32], row-major, as mx4_quantize gives them) of
+    [(q_heads + 2 kv_heads) dim, hidden] and [hidden, q_heads dim].  Up to 16 rows are multiplied in bf16
+    (w4_matvec); more, a prompt's, are quantised to MXFP4 themselves (mx4_grouped_gemm on packed
+    copies, made where max_rows is more than 16: both sizes then multiples of 128).  One call at a time."""
+
+    def __init__(self, cache: Cache4, q_heads, hidden, w_qkv, w_o, cos_sin, requests, max_rows, max_pages, max_q=1,
+                 max_len=None, w_q=None, w_k=None, w_pre=None, w_post=None, gate=None, residual_scale=1.0,
+                 branch_scale=1.0, eps=1e-6, kind=NORM_RMS, style=ROPE_HALVES, window=0, scale=None):
+        self.cache, self.q_heads, self.hidden, self.cos_sin = cache, q_heads, hidden, cos_sin
+        self.requests, self.max_rows, self.max_pages = requests, max_rows, max_pages
+        self.plan_args = dict(max_q=max_q, max_len=max_len, window=window, scale=scale)
+        self.w_q, self.w_k, self.w_pre, self.w_post, self.gate = w_q, w_k, w_pre, w_post, gate
+        self.eps, self.kind, self.style = eps, kind, style
+        self.scales = dict(residual_scale=residual_scale, branch_scale=branch_scale)
+        D, n_qkv = cache.dim, (q_heads + 2 * cache.kv_heads) * cache.dim
+        dev = cache.codes.device
+        self.weights, self.sizes = (w_qkv, w_o), ((n_qkv, hidden), (hidden, q_heads * D))
+        for name, (codes, scales), (n, k) in zip(("w_qkv", "w_o"), self.weights, self.sizes):
+            _typed(codes, torch.uint8, (n, k // 2), name)
+            _typed(scales, torch.uint8, (n, k // 32), name)
+        self.packed = None
+        if max_rows > 16:
+            self.packed = [pack_mx4_weights(c[None], s[None]) for c, s in self.weights]
+            k = max(hidden, q_heads * D)
+            self.xq = torch.empty(max_rows * k // 2, dtype=torch.uint8, device=dev)
+            self.xs = torch.empty(max_rows * k // 32, dtype=torch.uint8, device=dev)
+            self.offsets = torch.zeros(2, dtype=_I32, device=dev)
+        self.qkv = torch.empty(max_rows, n_qkv, dtype=_BF16, device=dev)
+        self.q = torch.zeros(max_rows, q_heads, D, dtype=_BF16, device=dev)
+        self.status_word = torch.zeros(1, dtype=_I32, device=dev)
+        self._plans = {}
+
+    def _project(self, which, x, out, stream):
+        (n, k), T = self.sizes[which], x.shape[0]
+        if T <= 16:
+            return w4_matvec(x, *self.weights[which], out, stream=stream)
+        xq, xs = self.xq[:T * k // 2].view(T, k // 2), self.xs[:T * k // 32].view(T, k // 32)
+        mx4_quantize(x, xq, xs, stream)
+        mx4_grouped_gemm(1, n, k, T, xq, xs, self.offsets, *self.packed[which], out, OUT_BF16, self.status_word, stream)
+        return out
+
+    def pre(self, residual, x, stream=None):
+        """x = norm(residual) w_pre, where no earlier block wrote it."""
+        block_norm(residual, x_out=x, w_pre=self.w_pre, eps=self.eps, kind=self.kind, stream=stream)
+        return x
+
+    def forward(self, residual, x, y, tables: PageTables, w_next=None, x_next=None, stream=None):
+        """residual fp32 or bf16 [T, hidden], updated in place; x bf16 [T, hidden] the normed input; y
+        bf16 [T, hidden] is scratch; tables: of this step, with at most T token rows (rows behind the
+        last token go nowhere; what their outputs hold means nothing).  With w_next the next block's
+        norm is part of the last pass, into x_next (may be x)."""
+        T = x.shape[0]
+        if T > self.max_rows:
+            raise ValueError(f"{T} rows, and buffers for {self.max_rows}")
+        if tables.slots.shape[0] < T:
+            raise ValueError(f"{T} rows, and tables for {tables.slots.shape[0]}")
+        plan = self._plans.get(T)
+        if plan is None:
+            plan = self._plans[T] = CacheAttention(self.requests, T, self.q_heads, self.cache, self.max_pages,
+                                                   **self.plan_args)
+        if T > 16:
+            if stream is None:
+                self.offsets[1:].fill_(T)
+            else:
+                with torch.cuda.stream(stream):
+                    self.offsets[1:].fill_(T)
+        qkv, q = self.qkv[:T], self.q[:T]
+        self._project(0, x, qkv, stream)
+        qk_norm_rope(qkv, tables.positions[:T], self.cos_sin, self.q_heads, self.cache.kv_heads, q, w_q=self.w_q,
+                     w_k=self.w_k, cache=self.cache, slots=tables.slots[:T], eps=self.eps, style=self.style,
+                     status=self.status_word, stream=stream)
+        plan.forward(q, tables.table, tables.lengths, tables.starts, q, status=self.status_word, stream=stream)
+        self._project(1, q.view(T, -1), y, stream)
+        block_norm(residual, y=y, residual_out=residual, x_out=x_next, w_post=self.w_post, w_pre=w_next,
+                   gate=self.gate, eps=self.eps, kind=self.kind, stream=stream, **self.scales)
+        return residual
+
+    def status(self) -> int:
+        """The device status bits of the calls so far (waits for them)."""
+        return int(self.status_word)
