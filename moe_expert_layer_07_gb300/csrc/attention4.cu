@@ -545,7 +545,8 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
                         for (int x = 4; x <= 16; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
                         // how far m moves
                         const float up = v == -INFINITY ? 0.0f : pass[n][j] == -INFINITY ? v : fmaxf(v, 0.0f);
-                        const float f = ex2(-up);
+                        // before there is an m there is nothing to scale
+                        const float f = pass[n][j] == -INFINITY ? 1.0f : ex2(-up);
                         if (v != -INFINITY) pass[n][j] = kLazy;
                         ref[n][j] += up;
                         sum[n][j] *= f;

@@ -396,148 +396,150 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 ev = info.ev;
 #pragma unroll 1
                 for (int sub = 0; sub < kTok / kSub && ok; ++sub, ++mine) {
-                const uint32_t ts = tmem + lanes + (2 * mt + sub) * kSub;
-                ok = wait(s_full[2 * mt + sub], (mine >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                const int t0 = p.g.lo + c * kTok + sub * kSub;
-                const bool edge = t0 + kSub - 1 > p.g.pos_lo || (a.window && t0 <= p.g.pos_hi - a.window) || info.bad;
-                const int upto = pos - t0, from = a.window ? pos - a.window - t0 : -1;   // columns from < i <= upto
-                const uint32_t lost = info.bad >> 4 * sub;
-                const float xs = mult * info.ek;
-                float shrink = sub ? 1.0f : info.grown;
-                // 32 columns at a time (a small loop: unrolled, its code did not stay in the
-                // instruction cache): their P takes the place of S that has been read.
-                uint32_t r[2][16];
-                tmem_ld16(ts, r[0]);
-                tmem_ld16(ts + 16, r[1]);
-                F2 part[2] = {0ull, 0ull};
-                // scores of 32 columns from r, past m, hidden ones at minus infinity
-                auto scores = [&](int q, float (&x)[32]) {
-                    const F2 xs2 = pack2(__float_as_uint(xs), __float_as_uint(xs));
-                    const F2 ref2 = pack2(__float_as_uint(-ref), __float_as_uint(-ref));
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const F2 v = fma2(pack2(r[i >> 4][i & 15], r[i >> 4][(i & 15) + 1]), xs2, ref2);
-                        x[i] = __uint_as_float((uint32_t)v), x[i + 1] = __uint_as_float((uint32_t)(v >> 32));
-                    }
-                    if (edge) {
-                        const int hi = upto - 32 * q, lo = from - 32 * q;
-                        const uint32_t bad = (lost >> 2 * q & 1u ? 0xffffu : 0u) | (lost >> 2 * q & 2u ? 0xffff0000u : 0u);
-                        // bit i: column i is seen
-                        uint32_t seen = hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1u;
-                        if (lo >= 0) seen &= lo >= 31 ? 0u : ~((2u << lo) - 1u);
-                        seen &= ~bad;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!(seen >> i & 1u)) x[i] = -INFINITY;
-                    }
-                };
-                auto largest = [](const float (&x)[32]) {
-                    float t4[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) t4[i] = fmaxf(x[i], x[i + 4]);
-#pragma unroll
-                    for (int i = 8; i < 32; i += 8)
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) t4[z] = fmaxf(t4[z], fmaxf(x[i + z], x[i + z + 4]));
-                    return fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-                };
-#pragma unroll 1
-                for (int q = 0; q < kSub / 32; ++q) {
-                    float x[32];
-                    uint32_t pk[16];
-                    tmem_wait_ld(r[0]);
-                    tmem_wait_ld(r[1]);
-                    scores(q, x);
-                    if (q + 1 < kSub / 32) {
-                        tmem_ld16(ts + 32 * q + 32, r[0]);
-                        tmem_ld16(ts + 32 * q + 48, r[1]);
-                    }
-                    // exponentials first: whether m has to rise is known while they are formed
-                    const float top = largest(x);
-                    F2 more[2] = {0ull, 0ull};
-                    auto exponentials = [&]() {
+                    const uint32_t ts = tmem + lanes + (2 * mt + sub) * kSub;
+                    ok = wait(s_full[2 * mt + sub], (mine >> 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const int t0 = p.g.lo + c * kTok + sub * kSub;
+                    const bool edge = t0 + kSub - 1 > p.g.pos_lo || (a.window && t0 <= p.g.pos_hi - a.window) || info.bad;
+                    const int upto = pos - t0, from = a.window ? pos - a.window - t0 : -1;   // columns from < i <= upto
+                    const uint32_t lost = info.bad >> 4 * sub;
+                    const float xs = mult * info.ek;
+                    float shrink = sub ? 1.0f : info.grown;
+                    // 32 columns at a time (a small loop: unrolled, its code did not stay in the
+                    // instruction cache): their P takes the place of S that has been read.
+                    uint32_t r[2][16];
+                    tmem_ld16(ts, r[0]);
+                    tmem_ld16(ts + 16, r[1]);
+                    F2 part[2] = {0ull, 0ull};
+                    // scores of 32 columns from r, past m, hidden ones at minus infinity
+                    auto scores = [&](int q, float (&x)[32]) {
+                        const F2 xs2 = pack2(__float_as_uint(xs), __float_as_uint(xs));
+                        const F2 ref2 = pack2(__float_as_uint(-ref), __float_as_uint(-ref));
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
-                            x[i] = ex2w(x[i]);
-                            x[i + 1] = ex2w(x[i + 1]);
-                            more[i >> 1 & 1] = add2(more[i >> 1 & 1], pack2(__float_as_uint(x[i]), __float_as_uint(x[i + 1])));
-                            pk[i / 2] = half2_of(x[i], x[i + 1]);
+                            const F2 v = fma2(pack2(r[i >> 4][i & 15], r[i >> 4][(i & 15) + 1]), xs2, ref2);
+                            x[i] = __uint_as_float((uint32_t)v), x[i + 1] = __uint_as_float((uint32_t)(v >> 32));
+                        }
+                        if (edge) {
+                            const int hi = upto - 32 * q, lo = from - 32 * q;
+                            const uint32_t bad = (lost >> 2 * q & 1u ? 0xffffu : 0u) | (lost >> 2 * q & 2u ? 0xffff0000u : 0u);
+                            // bit i: column i is seen
+                            uint32_t seen = hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1u;
+                            if (lo >= 0) seen &= lo >= 31 ? 0u : ~((2u << lo) - 1u);
+                            seen &= ~bad;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!(seen >> i & 1u)) x[i] = -INFINITY;
                         }
                     };
-                    exponentials();
-                    if (__any_sync(0xffffffffu, top > pass)) {
-                        // m rises by whole powers of two, so that what is scaled stays exact
-                        const float rise = top == -INFINITY ? 0.0f : pass == -INFINITY ? ceilf(top) : fmaxf(ceilf(top), 0.0f);
-                        if (top != -INFINITY) pass = kLazy;
-                        ref += rise;
-                        const float f = ex2w(-rise);
-                        sum *= f;
-                        shrink *= f;
+                    auto largest = [](const float (&x)[32]) {
+                        float t4[4];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) part[i] = mul2(part[i], pack2(__float_as_uint(f), __float_as_uint(f)));
-                        const uint32_t f2 = half2_of(f, f);
-                        tmem_wait_st();
+                        for (int i = 0; i < 4; ++i) t4[i] = fmaxf(x[i], x[i + 4]);
+#pragma unroll
+                        for (int i = 8; i < 32; i += 8)
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) t4[z] = fmaxf(t4[z], fmaxf(x[i + z], x[i + z + 4]));
+                        return fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                    };
 #pragma unroll 1
-                        for (int z = 0; z < 2 * q; ++z) {   // P so far
-                            uint32_t y[8];
-                            tmem_get8(ts + 8 * z, y);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) y[i] = mul_half2(y[i], f2);
-                            tmem_st8(ts + 8 * z, y);
-                        }
-                        // these columns again, and the next ones' loads
-                        tmem_ld16(ts + 32 * q, r[0]);
-                        tmem_ld16(ts + 32 * q + 16, r[1]);
+                    for (int q = 0; q < kSub / 32; ++q) {
+                        float x[32];
+                        uint32_t pk[16];
                         tmem_wait_ld(r[0]);
                         tmem_wait_ld(r[1]);
                         scores(q, x);
-                        more[0] = more[1] = 0ull;
-                        exponentials();
                         if (q + 1 < kSub / 32) {
                             tmem_ld16(ts + 32 * q + 32, r[0]);
                             tmem_ld16(ts + 32 * q + 48, r[1]);
                         }
-                    }
-                    part[0] = add2(part[0], more[0]);
-                    part[1] = add2(part[1], more[1]);
-                    tmem_st16(ts + 16 * q, pk);
-                }
-                part[0] = add2(part[0], part[1]);
-                sum += __uint_as_float((uint32_t)part[0]) + __uint_as_float((uint32_t)(part[0] >> 32));
-                if ((c > p.c0 || sub) && __any_sync(0xffffffffu, shrink != 1.0f)) {
-                    ok = wait(o_done[mt], (mine - 1) & 1);   // the products before these
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int q = 0; q < D / 16; ++q) {
-                        uint32_t r[16];
-                        tmem_ld16(to + 16 * q, r);
-                        tmem_wait_ld(r);
+                        // exponentials first: whether m has to rise is known while they are formed
+                        const float top = largest(x);
+                        F2 more[2] = {0ull, 0ull};
+                        auto exponentials = [&]() {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * shrink);
-                        tmem_st16(to + 16 * q, r);
-                    }
-                }
-                tmem_wait_st();
-                if (info.nan) {
-#pragma unroll 1
-                    for (int q = 0; q < kSub / 32; ++q) {
-                        uint32_t r[16];
-                        tmem_ld16(ts + 16 * q, r);
-                        tmem_wait_ld(r);
+                            for (int i = 0; i < 32; i += 2) {
+                                x[i] = ex2w(x[i]);
+                                x[i + 1] = ex2w(x[i + 1]);
+                                more[i >> 1 & 1] = add2(more[i >> 1 & 1], pack2(__float_as_uint(x[i]), __float_as_uint(x[i + 1])));
+                                pk[i / 2] = half2_of(x[i], x[i + 1]);
+                            }
+                        };
+                        exponentials();
+                        if (__any_sync(0xffffffffu, top > pass)) {
+                            // m rises by whole powers of two, so that what is scaled stays exact
+                            // before there is an m there is nothing to scale
+                            const bool none = pass == -INFINITY;
+                            const float rise = top == -INFINITY ? 0.0f : none ? ceilf(top) : fmaxf(ceilf(top), 0.0f);
+                            if (top != -INFINITY) pass = kLazy;
+                            ref += rise;
+                            const float f = none ? 1.0f : ex2w(-rise);
+                            sum *= f;
+                            shrink *= f;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const uint2 n8 = s_nan[in][kSub / 2 * sub + 16 * q + i];
-                            if (r[i] & 0x7fffu) nans |= n8.x;
-                            if (r[i] & 0x7fff0000u) nans |= n8.y;
+                            for (int i = 0; i < 2; ++i) part[i] = mul2(part[i], pack2(__float_as_uint(f), __float_as_uint(f)));
+                            const uint32_t f2 = half2_of(f, f);
+                            tmem_wait_st();
+#pragma unroll 1
+                            for (int z = 0; z < 2 * q; ++z) {   // P so far
+                                uint32_t y[8];
+                                tmem_get8(ts + 8 * z, y);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) y[i] = mul_half2(y[i], f2);
+                                tmem_st8(ts + 8 * z, y);
+                            }
+                            // these columns again, and the next ones' loads
+                            tmem_ld16(ts + 32 * q, r[0]);
+                            tmem_ld16(ts + 32 * q + 16, r[1]);
+                            tmem_wait_ld(r[0]);
+                            tmem_wait_ld(r[1]);
+                            scores(q, x);
+                            more[0] = more[1] = 0ull;
+                            exponentials();
+                            if (q + 1 < kSub / 32) {
+                                tmem_ld16(ts + 32 * q + 32, r[0]);
+                                tmem_ld16(ts + 32 * q + 48, r[1]);
+                            }
+                        }
+                        part[0] = add2(part[0], more[0]);
+                        part[1] = add2(part[1], more[1]);
+                        tmem_st16(ts + 16 * q, pk);
+                    }
+                    part[0] = add2(part[0], part[1]);
+                    sum += __uint_as_float((uint32_t)part[0]) + __uint_as_float((uint32_t)(part[0] >> 32));
+                    if ((c > p.c0 || sub) && __any_sync(0xffffffffu, shrink != 1.0f)) {
+                        ok = wait(o_done[mt], (mine - 1) & 1);   // the products before these
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int q = 0; q < D / 16; ++q) {
+                            uint32_t r[16];
+                            tmem_ld16(to + 16 * q, r);
+                            tmem_wait_ld(r);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * shrink);
+                            tmem_st16(to + 16 * q, r);
                         }
                     }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&p_ready[2 * mt + sub]));
+                    tmem_wait_st();
+                    if (info.nan) {
+#pragma unroll 1
+                        for (int q = 0; q < kSub / 32; ++q) {
+                            uint32_t r[16];
+                            tmem_ld16(ts + 16 * q, r);
+                            tmem_wait_ld(r);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const uint2 n8 = s_nan[in][kSub / 2 * sub + 16 * q + i];
+                                if (r[i] & 0x7fffu) nans |= n8.x;
+                                if (r[i] & 0x7fff0000u) nans |= n8.y;
+                            }
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&p_ready[2 * mt + sub]));
                 }
                 if (!ok) break;
             }

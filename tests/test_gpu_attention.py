@@ -236,6 +236,20 @@ def test_large_and_small_scores(lib):
     _run(c, lse=True)
 
 
+@pytest.mark.parametrize("news", [[2], [60]])
+def test_scores_far_below_and_above_zero(lib, news):
+    """All scores of a row at -1000 or 1000: what stands before its first token must not matter."""
+    for sign in (-1.0, 1.0):
+        c = Case([500], news, 8, 2, 128, 16, seed=13)
+        c.cache.codes[:, 0, :, :, :16] = 0x33   # 1.5 each
+        c.cache.codes[:, 0, :, :, 16:] &= 0x11
+        c.cache.scales[:, 0] = 127
+        c.q[..., :32] = sign * 20.0 * c.D ** 0.5
+        c.q[..., 32:] *= 0.1
+        _run(c, lse=True)
+        _run(c, lse=True, window=100)
+
+
 def test_values_of_very_different_sizes(lib):
     """A value 2^15 times the others', wherever it stands: the others still count."""
     for where in (0, 70, 799):
