@@ -8,7 +8,7 @@
 // K in shared memory; O from P, which a tile's softmax leaves in tensor memory
 // where S was, and V in shared memory with channels contiguous.  While one
 // tile's softmax works on its S the products of the other are under way:
-//   QK0 QK1 PV0 | QK0 PV1 QK1 PV0 | QK0 PV1 QK1 ...
+//   QK0 QK1 | PV0 QK0 PV1 QK1 | PV0 QK0 PV1 QK1 ...
 // Warps 0-3 and 4-7 are the softmax of tile 0 and 1, a thread to a row; warps
 // 8-11 unpack keys and values; warp 12 issues the products.
 //
@@ -38,7 +38,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kWideRows = 256, kM = 128, kTok = 128, kSub = 64;   // tokens of a tile, of a product
+constexpr int kWideRows = 256, kM = 128, kTok = 128;
 constexpr int kSoftWarps = 8, kUnpackWarps = 4, kMmaWarp = kSoftWarps + kUnpackWarps;
 constexpr int kWideThreads = (kMmaWarp + 1) * 32;
 constexpr int kStages = 2, kInfos = 4;
@@ -275,7 +275,7 @@ struct WideShape {
     static constexpr int kUsed = kV + kStages * kTileBytes + 1024;
     // one CTA on an SM: each takes all of the tensor memory
     static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
-    static constexpr int kO = 4 * kSub;                    // columns: S of both halves, twice each; O of both
+    static constexpr int kO = 2 * kTok;                    // columns: S of both halves, then O
 };
 
 template <int D>
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
     constexpr int kBlocks = D / 32;
     extern __shared__ uint8_t dsmem[];
     __shared__ uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], info_full[kInfos];
-    __shared__ uint64_t s_full[4], p_ready[4], o_done[2], q_full, o_full, drain_bar;   // [half][buffer]
+    __shared__ uint64_t s_full[2], p_ready[2], q_full, o_full, drain_bar;
     __shared__ uint64_t e_full[2];
     __shared__ Info s_info[kInfos];
     __shared__ uint2 s_nan[kInfos][kTok / 2];        // a byte for each token and channel block
@@ -305,10 +305,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&e_full[s]), kUnpackWarps);
             mbar_init(smem_u32(&s_full[s]), 1);
-            mbar_init(smem_u32(&s_full[s + 2]), 1);
             mbar_init(smem_u32(&p_ready[s]), 4);
-            mbar_init(smem_u32(&p_ready[s + 2]), 4);
-            mbar_init(smem_u32(&o_done[s]), 1);
         }
         mbar_init(smem_u32(&q_full), kSoftWarps);
         mbar_init(smem_u32(&o_full), 1);
@@ -345,7 +342,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
         // ---- softmax, a thread to a row ---------------------------------------------------
         const int mt = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t to = tmem + lanes + S::kO + mt * D;
+        const uint32_t ts = tmem + lanes + mt * kTok, to = tmem + lanes + S::kO + mt * D;
         uint32_t mine = 0;   // products' tiles of this half, of all pieces
         while (ok && walk.next(w, entries, p)) {
             if (p.c0 == p.c1) continue;
@@ -390,158 +387,148 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             for (int c = p.c0; c < p.c1; ++c, ++tiles) {
                 if (!used) continue;
                 const uint32_t in = tiles % kInfos;
-                ok = wait(info_full[in], (tiles / kInfos) & 1);
+                ok = wait(info_full[in], (tiles / kInfos) & 1) && wait(s_full[mt], mine & 1);
+                ++mine;
                 if (!ok) break;
+                tc_fence_after();
                 const Info info = s_info[in];
                 ev = info.ev;
+                const int t0 = p.g.lo + c * kTok;
+                const bool edge = t0 + kTok - 1 > p.g.pos_lo || (a.window && t0 <= p.g.pos_hi - a.window) || info.bad;
+                const int upto = pos - t0, from = a.window ? pos - a.window - t0 : -1;   // columns from < i <= upto
+                const float xs = mult * info.ek;
+                float shrink = info.grown;
+                // 32 columns at a time (a small loop: unrolled, its code did not stay in the
+                // instruction cache): their P takes the place of S that has been read.
+                uint32_t r[2][16];
+                tmem_ld16(ts, r[0]);
+                tmem_ld16(ts + 16, r[1]);
+                F2 part[2] = {0ull, 0ull};
+                // scores of 32 columns from r, past m, hidden ones at minus infinity
+                auto scores = [&](int q, float (&x)[32]) {
+                    const F2 xs2 = pack2(__float_as_uint(xs), __float_as_uint(xs));
+                    const F2 ref2 = pack2(__float_as_uint(-ref), __float_as_uint(-ref));
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const F2 v = fma2(pack2(r[i >> 4][i & 15], r[i >> 4][(i & 15) + 1]), xs2, ref2);
+                        x[i] = __uint_as_float((uint32_t)v), x[i + 1] = __uint_as_float((uint32_t)(v >> 32));
+                    }
+                    if (edge) {
+                        const int hi = upto - 32 * q, lo = from - 32 * q;
+                        const uint32_t bad = (info.bad >> 2 * q & 1u ? 0xffffu : 0u) | (info.bad >> 2 * q & 2u ? 0xffff0000u : 0u);
+                        // bit i: column i is seen
+                        uint32_t seen = hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1u;
+                        if (lo >= 0) seen &= lo >= 31 ? 0u : ~((2u << lo) - 1u);
+                        seen &= ~bad;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(seen >> i & 1u)) x[i] = -INFINITY;
+                    }
+                };
+                auto largest = [](const float (&x)[32]) {
+                    float t4[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) t4[i] = fmaxf(x[i], x[i + 4]);
+#pragma unroll
+                    for (int i = 8; i < 32; i += 8)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) t4[z] = fmaxf(t4[z], fmaxf(x[i + z], x[i + z + 4]));
+                    return fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                };
 #pragma unroll 1
-                for (int sub = 0; sub < kTok / kSub && ok; ++sub, ++mine) {
-                    const uint32_t ts = tmem + lanes + (2 * mt + sub) * kSub;
-                    ok = wait(s_full[2 * mt + sub], (mine >> 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const int t0 = p.g.lo + c * kTok + sub * kSub;
-                    const bool edge = t0 + kSub - 1 > p.g.pos_lo || (a.window && t0 <= p.g.pos_hi - a.window) || info.bad;
-                    const int upto = pos - t0, from = a.window ? pos - a.window - t0 : -1;   // columns from < i <= upto
-                    const uint32_t lost = info.bad >> 4 * sub;
-                    const float xs = mult * info.ek;
-                    float shrink = sub ? 1.0f : info.grown;
-                    // 32 columns at a time (a small loop: unrolled, its code did not stay in the
-                    // instruction cache): their P takes the place of S that has been read.
-                    uint32_t r[2][16];
-                    tmem_ld16(ts, r[0]);
-                    tmem_ld16(ts + 16, r[1]);
-                    F2 part[2] = {0ull, 0ull};
-                    // scores of 32 columns from r, past m, hidden ones at minus infinity
-                    auto scores = [&](int q, float (&x)[32]) {
-                        const F2 xs2 = pack2(__float_as_uint(xs), __float_as_uint(xs));
-                        const F2 ref2 = pack2(__float_as_uint(-ref), __float_as_uint(-ref));
+                for (int q = 0; q < kTok / 32; ++q) {
+                    float x[32];
+                    uint32_t pk[16];
+                    tmem_wait_ld(r[0]);
+                    tmem_wait_ld(r[1]);
+                    scores(q, x);
+                    if (q + 1 < kTok / 32) {
+                        tmem_ld16(ts + 32 * q + 32, r[0]);
+                        tmem_ld16(ts + 32 * q + 48, r[1]);
+                    }
+                    // exponentials first: whether m has to rise is known while they are formed
+                    const float top = largest(x);
+                    F2 more[2] = {0ull, 0ull};
+                    auto exponentials = [&]() {
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
-                            const F2 v = fma2(pack2(r[i >> 4][i & 15], r[i >> 4][(i & 15) + 1]), xs2, ref2);
-                            x[i] = __uint_as_float((uint32_t)v), x[i + 1] = __uint_as_float((uint32_t)(v >> 32));
-                        }
-                        if (edge) {
-                            const int hi = upto - 32 * q, lo = from - 32 * q;
-                            const uint32_t bad = (lost >> 2 * q & 1u ? 0xffffu : 0u) | (lost >> 2 * q & 2u ? 0xffff0000u : 0u);
-                            // bit i: column i is seen
-                            uint32_t seen = hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1u;
-                            if (lo >= 0) seen &= lo >= 31 ? 0u : ~((2u << lo) - 1u);
-                            seen &= ~bad;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (!(seen >> i & 1u)) x[i] = -INFINITY;
+                            x[i] = ex2w(x[i]);
+                            x[i + 1] = ex2w(x[i + 1]);
+                            more[i >> 1 & 1] = add2(more[i >> 1 & 1], pack2(__float_as_uint(x[i]), __float_as_uint(x[i + 1])));
+                            pk[i / 2] = half2_of(x[i], x[i + 1]);
                         }
                     };
-                    auto largest = [](const float (&x)[32]) {
-                        float t4[4];
+                    exponentials();
+                    if (__any_sync(0xffffffffu, top > pass)) {
+                        // m rises by whole powers of two, so that what is scaled stays exact
+                        // before there is an m there is nothing to scale
+                        const bool none = pass == -INFINITY;
+                        const float rise = top == -INFINITY ? 0.0f : none ? ceilf(top) : fmaxf(ceilf(top), 0.0f);
+                        if (top != -INFINITY) pass = kLazy;
+                        ref += rise;
+                        const float f = none ? 1.0f : ex2w(-rise);
+                        sum *= f;
+                        shrink *= f;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) t4[i] = fmaxf(x[i], x[i + 4]);
-#pragma unroll
-                        for (int i = 8; i < 32; i += 8)
-#pragma unroll
-                            for (int z = 0; z < 4; ++z) t4[z] = fmaxf(t4[z], fmaxf(x[i + z], x[i + z + 4]));
-                        return fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-                    };
+                        for (int i = 0; i < 2; ++i) part[i] = mul2(part[i], pack2(__float_as_uint(f), __float_as_uint(f)));
+                        const uint32_t f2 = half2_of(f, f);
+                        tmem_wait_st();
 #pragma unroll 1
-                    for (int q = 0; q < kSub / 32; ++q) {
-                        float x[32];
-                        uint32_t pk[16];
+                        for (int z = 0; z < 2 * q; ++z) {   // P so far
+                            uint32_t y[8];
+                            tmem_get8(ts + 8 * z, y);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) y[i] = mul_half2(y[i], f2);
+                            tmem_st8(ts + 8 * z, y);
+                        }
+                        // these columns again, and the next ones' loads
+                        tmem_ld16(ts + 32 * q, r[0]);
+                        tmem_ld16(ts + 32 * q + 16, r[1]);
                         tmem_wait_ld(r[0]);
                         tmem_wait_ld(r[1]);
                         scores(q, x);
-                        if (q + 1 < kSub / 32) {
+                        more[0] = more[1] = 0ull;
+                        exponentials();
+                        if (q + 1 < kTok / 32) {
                             tmem_ld16(ts + 32 * q + 32, r[0]);
                             tmem_ld16(ts + 32 * q + 48, r[1]);
                         }
-                        // exponentials first: whether m has to rise is known while they are formed
-                        const float top = largest(x);
-                        F2 more[2] = {0ull, 0ull};
-                        auto exponentials = [&]() {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                x[i] = ex2w(x[i]);
-                                x[i + 1] = ex2w(x[i + 1]);
-                                more[i >> 1 & 1] = add2(more[i >> 1 & 1], pack2(__float_as_uint(x[i]), __float_as_uint(x[i + 1])));
-                                pk[i / 2] = half2_of(x[i], x[i + 1]);
-                            }
-                        };
-                        exponentials();
-                        if (__any_sync(0xffffffffu, top > pass)) {
-                            // m rises by whole powers of two, so that what is scaled stays exact
-                            // before there is an m there is nothing to scale
-                            const bool none = pass == -INFINITY;
-                            const float rise = top == -INFINITY ? 0.0f : none ? ceilf(top) : fmaxf(ceilf(top), 0.0f);
-                            if (top != -INFINITY) pass = kLazy;
-                            ref += rise;
-                            const float f = none ? 1.0f : ex2w(-rise);
-                            sum *= f;
-                            shrink *= f;
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) part[i] = mul2(part[i], pack2(__float_as_uint(f), __float_as_uint(f)));
-                            const uint32_t f2 = half2_of(f, f);
-                            tmem_wait_st();
-#pragma unroll 1
-                            for (int z = 0; z < 2 * q; ++z) {   // P so far
-                                uint32_t y[8];
-                                tmem_get8(ts + 8 * z, y);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) y[i] = mul_half2(y[i], f2);
-                                tmem_st8(ts + 8 * z, y);
-                            }
-                            // these columns again, and the next ones' loads
-                            tmem_ld16(ts + 32 * q, r[0]);
-                            tmem_ld16(ts + 32 * q + 16, r[1]);
-                            tmem_wait_ld(r[0]);
-                            tmem_wait_ld(r[1]);
-                            scores(q, x);
-                            more[0] = more[1] = 0ull;
-                            exponentials();
-                            if (q + 1 < kSub / 32) {
-                                tmem_ld16(ts + 32 * q + 32, r[0]);
-                                tmem_ld16(ts + 32 * q + 48, r[1]);
-                            }
-                        }
-                        part[0] = add2(part[0], more[0]);
-                        part[1] = add2(part[1], more[1]);
-                        tmem_st16(ts + 16 * q, pk);
                     }
-                    part[0] = add2(part[0], part[1]);
-                    sum += __uint_as_float((uint32_t)part[0]) + __uint_as_float((uint32_t)(part[0] >> 32));
-                    if ((c > p.c0 || sub) && __any_sync(0xffffffffu, shrink != 1.0f)) {
-                        ok = wait(o_done[mt], (mine - 1) & 1);   // the products before these
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int q = 0; q < D / 16; ++q) {
-                            uint32_t r[16];
-                            tmem_ld16(to + 16 * q, r);
-                            tmem_wait_ld(r);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * shrink);
-                            tmem_st16(to + 16 * q, r);
-                        }
-                    }
-                    tmem_wait_st();
-                    if (info.nan) {
-#pragma unroll 1
-                        for (int q = 0; q < kSub / 32; ++q) {
-                            uint32_t r[16];
-                            tmem_ld16(ts + 16 * q, r);
-                            tmem_wait_ld(r);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const uint2 n8 = s_nan[in][kSub / 2 * sub + 16 * q + i];
-                                if (r[i] & 0x7fffu) nans |= n8.x;
-                                if (r[i] & 0x7fff0000u) nans |= n8.y;
-                            }
-                        }
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&p_ready[2 * mt + sub]));
+                    part[0] = add2(part[0], more[0]);
+                    part[1] = add2(part[1], more[1]);
+                    tmem_st16(ts + 16 * q, pk);
                 }
-                if (!ok) break;
+                part[0] = add2(part[0], part[1]);
+                sum += __uint_as_float((uint32_t)part[0]) + __uint_as_float((uint32_t)(part[0] >> 32));
+                if (c > p.c0 && __any_sync(0xffffffffu, shrink != 1.0f)) {   // S was there: the products before it are done
+#pragma unroll 1
+                    for (int q = 0; q < D / 16; ++q) {
+                        uint32_t r[16];
+                        tmem_ld16(to + 16 * q, r);
+                        tmem_wait_ld(r);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * shrink);
+                        tmem_st16(to + 16 * q, r);
+                    }
+                }
+                tmem_wait_st();
+                if (info.nan) {
+#pragma unroll 1
+                    for (int q = 0; q < kTok / 32; ++q) {
+                        uint32_t r[16];
+                        tmem_ld16(ts + 16 * q, r);
+                        tmem_wait_ld(r);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const uint2 n8 = s_nan[in][16 * q + i];
+                            if (r[i] & 0x7fffu) nans |= n8.x;
+                            if (r[i] & 0x7fff0000u) nans |= n8.y;
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&p_ready[mt]));
             }
             ok = ok && wait(o_full, pieces & 1);
             ++pieces;
@@ -747,64 +734,57 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
     } else {
         // ---- products ---------------------------------------------------------------------
         const bool elected = elect_one();
-        constexpr uint32_t kQK = idesc_f16(kM, kSub, false), kPV = idesc_f16(kM, D, true);
-        constexpr uint32_t kNext = kSub * 128 >> 4;   // a product's tokens, in a descriptor
+        constexpr uint32_t kQK = idesc_f16(kM, kTok, false), kPV = idesc_f16(kM, D, true);
         uint32_t made[2] = {0, 0};   // P of each half that products have taken
         while (ok && walk.next(w, entries, p)) {
             if (p.c0 == p.c1) continue;
-            const int n = 2 * (p.c1 - p.c0), halves = p.g.nrows > kM ? 2 : 1;
-            auto qk = [&](int mt, int sub) {
-                const uint32_t stage = (tiles + sub / 2) % kStages, half = sub & 1;
+            const int n = p.c1 - p.c0, halves = p.g.nrows > kM ? 2 : 1;
+            auto qk = [&](int mt, uint32_t tile) {
+                const uint32_t stage = tile % kStages;
                 if (elected) {
                     const uint64_t q = sdesc_k_sw128(base + S::kQ + mt * S::kTileBytes);
-                    const uint64_t k = sdesc_k_sw128(base + S::kK + stage * S::kTileBytes) + half * kNext;
+                    const uint64_t k = sdesc_k_sw128(base + S::kK + stage * S::kTileBytes);
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s) {
                         const uint32_t off = (s >> 2) * (S::kHalf >> 4) + (s & 3) * 2;
-                        mma_f16(tmem + (2 * mt + half) * kSub, q + off, k + off, kQK, s > 0);
+                        mma_f16(tmem + mt * kTok, q + off, k + off, kQK, s > 0);
                     }
-                    mma_commit(smem_u32(&s_full[2 * mt + half]));
-                    if (half && mt == halves - 1) mma_commit(smem_u32(&k_empty[stage]));
+                    mma_commit(smem_u32(&s_full[mt]));
+                    if (mt == halves - 1) mma_commit(smem_u32(&k_empty[stage]));
                 }
                 __syncwarp();
             };
-            auto have_keys = [&](int sub) {
-                const uint32_t tile = tiles + sub / 2;
+            auto have_keys = [&](uint32_t tile) {
                 const bool good = wait(k_full[tile % kStages], (tile / kStages) & 1);
                 tc_fence_after();
                 return good;
             };
-            ok = wait(q_full, pieces & 1) && have_keys(0);
+            ok = wait(q_full, pieces & 1) && have_keys(tiles);
             ++pieces;
             if (!ok) break;
-            for (int sub = 0; sub < 2; ++sub)
-                for (int mt = 0; mt < halves; ++mt) qk(mt, sub);
-            for (int sub = 0; sub < n && ok; ++sub) {
-                const uint32_t tile = tiles + sub / 2, stage = tile % kStages, half = sub & 1;
-                if (!half) ok = wait(v_full[stage], (tile / kStages) & 1);
+            for (int mt = 0; mt < halves; ++mt) qk(mt, tiles);
+            for (int j = 0; j < n && ok; ++j, ++tiles) {
+                const uint32_t stage = tiles % kStages;
+                ok = wait(v_full[stage], (tiles / kStages) & 1);
                 for (int mt = 0; mt < halves && ok; ++mt) {
-                    ok = wait(p_ready[2 * mt + half], (made[mt] >> 1) & 1);
+                    ok = wait(p_ready[mt], made[mt] & 1);
                     ++made[mt];
                     if (!ok) break;
                     tc_fence_after();
                     if (elected) {
-                        const uint64_t v = sdesc_mn_sw128(base + S::kV + stage * S::kTileBytes) + half * kNext;
+                        const uint64_t v = sdesc_mn_sw128(base + S::kV + stage * S::kTileBytes);
 #pragma unroll
-                        for (int s = 0; s < kSub / 16; ++s)
-                            mma_f16_ta(tmem + S::kO + mt * D, tmem + (2 * mt + half) * kSub + 8 * s, v + s * (2048 >> 4), kPV,
-                                       sub > 0 || s > 0);
-                        mma_commit(smem_u32(&o_done[mt]));
-                        if (half && mt == halves - 1) mma_commit(smem_u32(&v_empty[stage]));
+                        for (int s = 0; s < kTok / 16; ++s)
+                            mma_f16_ta(tmem + S::kO + mt * D, tmem + mt * kTok + 8 * s, v + s * (2048 >> 4), kPV, j > 0 || s > 0);
+                        if (mt == halves - 1) mma_commit(smem_u32(&v_empty[stage]));
                     }
                     __syncwarp();
-                    if (sub + 2 < n) {   // into the S that these products have taken P from
-                        if (!half && mt == 0) ok = have_keys(sub + 2);
-                        if (!ok) break;
-                        qk(mt, sub + 2);
+                    if (j + 1 < n) {   // into S that these products have taken P from
+                        if (mt == 0) ok = have_keys(tiles + 1);
+                        if (ok) qk(mt, tiles + 1);
                     }
                 }
             }
-            tiles += n / 2;
             if (elected && ok) mma_commit(smem_u32(&o_full));
             __syncwarp();
         }
