@@ -671,8 +671,8 @@ MOE_API int moe_cache_attention(const moe_cache_attn *d, const moe_cache4 *cache
  *   MOE_W4_INT  W[n, k] = scale[n, k/group] (code - zero[n, k/group]), codes 0..15
  *               (even k in the low four bits), scales bf16 or fp32 (scale_dtype),
  *               zero points uint8 0..15 or NULL (8); group 32, 64 or 128
- * fp32 accumulation.  x is taken as fp16 times a power of two for each row:
- * values below 2^-38 of a row's largest lose bits.  n_out any, k_dim a multiple of
+ * fp32 accumulation.  x is taken as fp16 times a power of two for each row
+ * (and part of K): each value is off by 2^-29 of a row's largest at most.  n_out any, k_dim a multiple of
  * the group (of 32 for MXFP4), at most 32768; x and codes 16-byte aligned. */
 enum { MOE_W4_MX = 0, MOE_W4_INT = 1 };
 typedef struct moe_w4 {

@@ -15,8 +15,8 @@
 // Codes become fp16 unscaled (MXFP4: cvt; integers: 1024 + code or 1024 + 16 code
 // put together from bits, minus the zero point, both exact), products of 32 of K
 // are multiplied by the group's scale in fp32.  x is fp16 times a power of two for
-// each row and warp (bf16 values have no more bits; below 2^-38 of the largest
-// among the warp's they lose some).
+// each row and warp (bf16 values have no more bits; off by up to 2^-29 of the
+// largest among the warp's where they are as small).
 //
 // Sums: the K slices of a warp one after the other, then warps in order, then
 // CTAs in order: the same bits each time.
@@ -91,10 +91,6 @@ __device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint3
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
                  : "memory");
@@ -122,6 +118,11 @@ __device__ __forceinline__ void widen_ints(uint32_t codes, const Zero &z, uint32
     h[1] = fma_half2((codes & 0x00f000f0u) | k, sixteenth, z.sixteen);
     h[2] = add_half2((up & 0x000f000fu) | k, z.one);
     h[3] = fma_half2((up & 0x00f000f0u) | k, sixteenth, z.sixteen);
+}
+
+// A barrier of the cluster that orders no memory: what was read before it has been used.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void write(const MatvecArgs &a, int t, int n, float v) {
@@ -224,31 +225,43 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
         for (int i = 0; i < S; ++i)
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                const uint32_t w[4] = {raw[i][b].x, raw[i][b].y, raw[i][b].z, raw[i][b].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) m = max(m, max(w[j] << 16 & 0x7fff0000u, w[j] & 0x7fff0000u));
+                const uint4 v = raw[i][b];
+                const uint32_t k = 0x7fff7fffu;   // magnitudes of bf16 pairs order like whole numbers
+                m = __vimax3_s16x2(m, v.x & k, v.y & k);
+                m = __vimax3_s16x2(m, v.z & k, v.w & k);
             }
+        m = max(m & 0xffffu, m >> 16);
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        // f = 2^up puts the row's largest into [2^14, 2^15); held where 2^up and 2^-up are numbers
-        const int ex = min(max((int)(m >> 23), 27), 254) - 14;
-        const float f = __uint_as_float((uint32_t)(254 - ex) << 23), un = __uint_as_float((uint32_t)ex << 23);
+        // 2^(127 - ex) puts the row's largest into [2^14, 2^15), or leaves a tiny row's exponents
+        // as they are
+        const int ex = min(max((int)(m >> 7), 29), 254) - 14;
+        const float un = __uint_as_float((uint32_t)ex << 23);
         down[n][0] = __shfl_sync(0xffffffffu, un, 8 * c);
         down[n][1] = __shfl_sync(0xffffffffu, un, 8 * c + 4);
+        // bf16 to fp16 times that in the bits: the exponent is lowered by ex - 15 (in bf16's
+        // place, with both types' biases); what falls below fp16's smallest is zero, and what
+        // falls among its subnormal numbers off by up to 2^-15
+        const uint32_t lower = (uint32_t)((-(ex - 15) << 7) & 0xffff) * 0x10001u;
+        const bool special = m >= 0x7f80u;   // an infinity or a NaN
 #pragma unroll
         for (int i = 0; i < S; ++i)
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 const uint32_t w[4] = {raw[i][b].x, raw[i][b].y, raw[i][b].z, raw[i][b].w};
-                float e[8];
+                uint32_t h[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    e[2 * j] = __uint_as_float(w[j] << 16) * f;
-                    e[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * f;
+                    h[j] = (__viaddmax_s16x2_relu(w[j] & 0x7fff7fffu, lower, 0u) << 3) | (w[j] & 0x80008000u);
+                    if (special) {
+                        if ((w[j] & 0x7f80u) == 0x7f80u) h[j] |= 0x7c00u | (w[j] & 0x7fu) << 3;
+                        if ((w[j] & 0x7f800000u) == 0x7f800000u) h[j] |= 0x7c000000u | (w[j] & 0x7f0000u) << 3;
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    xf[i][2 * b + j / 2][n][j & 1] = INT ? half2_bits(e[j], e[j + 4]) : half2_bits(e[2 * j], e[2 * j + 1]);
+                    xf[i][2 * b + j / 2][n][j & 1] =
+                        INT ? __byte_perm(h[j / 2], h[2 + j / 2], j & 1 ? 0x7632 : 0x5410) : h[j];
             }
     }
     const int mrow = (lane & 7) + ((lane >> 3) & 1) * 8, mblk = lane >> 4;
@@ -390,7 +403,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
                 const int j = i % kSums;
                 write(a, j & (8 * NQ - 1), (cluster + (base + i / kSums) * clusters) * kTileRows + j / (8 * NQ), v);
             }
-            ptx::cluster_sync();   // nobody reads this CTA's shared memory any more
+            cluster_sync_relaxed();   // nobody reads this CTA's shared memory any more
         }
     }
     cp_async_wait<0>();

@@ -37,7 +37,7 @@ def _projection(x, w, got):
     w64 = torch.tensor(mx4.dequantize(w[0].cpu().numpy(), w[1].cpu().numpy()), device="cuda")
     x64 = x.double() if x.shape[0] <= 16 else _rounded(x)
     ref, size = x64 @ w64.t(), x64.abs() @ w64.abs().t()
-    bound = 2.0 ** -8 * ref.abs() + 2.0 ** -17 * size + 2.0 ** -38 * x64.abs().amax() * w64.abs().sum(1)
+    bound = 2.0 ** -8 * ref.abs() + 2.0 ** -17 * size + 2.0 ** -29 * x64.abs().amax() * w64.abs().sum(1)
     assert bool(((got.double() - ref).abs() <= bound).all())
 
 
