@@ -112,12 +112,25 @@ struct Zero {
     __device__ __forceinline__ explicit Zero(uint32_t z)
         : one((0xe400u + z) * 0x10001u), sixteen((0xd400u + (z << 4)) * 0x10001u) {}
 };
-__device__ __forceinline__ void widen_ints(uint32_t codes, const Zero &z, uint32_t (&h)[4]) {
-    const uint32_t up = codes >> 8, k = 0x64006400u, sixteenth = 0x2c002c00u;
-    h[0] = add_half2((codes & 0x000f000fu) | k, z.one);
-    h[1] = fma_half2((codes & 0x00f000f0u) | k, sixteenth, z.sixteen);
-    h[2] = add_half2((up & 0x000f000fu) | k, z.one);
-    h[3] = fma_half2((up & 0x00f000f0u) | k, sixteenth, z.sixteen);
+// Constants that stay in registers: an instruction has room for one immediate.
+struct IntBits {
+    uint32_t lo, hi, k, sixteenth;
+    __device__ __forceinline__ IntBits() {
+        asm volatile("mov.b32 %0, 0x000f000f;\n\tmov.b32 %1, 0x00f000f0;\n\tmov.b32 %2, 0x64006400;\n\tmov.b32 %3, 0x2c002c00;"
+                     : "=r"(lo), "=r"(hi), "=r"(k), "=r"(sixteenth));
+    }
+};
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ void widen_ints(uint32_t codes, const IntBits &k, const Zero &z, uint32_t (&h)[4]) {
+    const uint32_t up = codes >> 8;
+    h[0] = add_half2(and_or(codes, k.lo, k.k), z.one);
+    h[1] = fma_half2(and_or(codes, k.hi, k.k), k.sixteenth, z.sixteen);
+    h[2] = add_half2(and_or(up, k.lo, k.k), z.one);
+    h[3] = fma_half2(and_or(up, k.hi, k.k), k.sixteenth, z.sixteen);
 }
 
 // A barrier of the cluster that orders no memory: what was read before it has been used.
@@ -166,61 +179,95 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
     int n_next = cluster * kTileRows;   // the next tile to be copied
     const int64_t step_w = (int64_t)clusters * kTileRows * row_bytes, half_w = (int64_t)8 * row_bytes;
     const uint8_t *src = a.w + (int64_t)(n_next + row_a) * row_bytes + first_slice * 64 + piece * 16;
-    const int64_t scale_end = (int64_t)a.N * a.scale_row, zero_end = (int64_t)a.N * groups;
-    const int step_s = clusters * kTileRows * a.scale_row, step_z = clusters * kTileRows * groups;
-    int64_t at_s = (int64_t)(n_next + row_s) * a.scale_row + (INT ? group0 * (a.s_f32 ? 4 : 2) : first_slice * 4);
-    int64_t at_z = INT ? (int64_t)(n_next + row_s) * groups + group0 : 0;
-    const int words = INT ? a.scale_words : (a.K & 127) ? 3 : S;
+    // (Tiles are 16 rows apart and more: where a row's strip begins in its word is the same
+    // for all of them.)
+    const int64_t step_s = (int64_t)clusters * kTileRows * a.scale_row, step_z = (int64_t)clusters * kTileRows * groups;
+    const int64_t at_s = (int64_t)(n_next + row_s) * a.scale_row + (INT ? group0 * (a.s_f32 ? 4 : 2) : first_slice * 4);
+    const int64_t at_z = INT ? (int64_t)(n_next + row_s) * groups + group0 : 0;
+    const uint8_t *src_s = a.scales + (at_s & ~(int64_t)3) + 4 * word0;
+    const uint8_t *src_z = INT ? a.zeros + (at_z & ~(int64_t)3) + 4 * word0 : nullptr;
+    const int words = INT ? a.scale_words : (a.K & 127) ? S + 1 : S;
     uint32_t to = 0, from = 0;   // stages of the ring
-    auto strip = [&](uint32_t to_addr, const uint8_t *base, int64_t at, int64_t end, int count) {
-        at = (at & ~(int64_t)3) + 4 * word0;
-        for (int word = word0; word < count; word += 2, at += 8, to_addr += 8)
-            if (at < end) cp_async4(to_addr, base + at, (int)min((int64_t)4, end - at));
-    };
     // Copies the next tile into its stage of the ring
     auto fetch = [&]() {
         if (busy && n_next < a.N) {
-            const bool lo = n_next + row_a < a.N, hi = n_next + row_a + 8 < a.N;
+            // all rows are there, and so many behind them that no strip's words pass the tensors' ends
+            // (35 bytes of two a row, 11 of one)
+            if (n_next + 3 * kTileRows <= a.N) {
 #pragma unroll
-            for (int i = 0; i < S; ++i) {
-                if (lo && inside[i]) cp_async16(dst + to + i * kItemBytes, src + i * 64);
-                if (hi && inside[i]) cp_async16(dst + to + i * kItemBytes + 512, src + half_w + i * 64);
-            }
-            if (n_next + row_s < a.N) {
-                strip(dst_s + to, a.scales, at_s, scale_end, words);
-                if (INT) strip(dst_z + to, a.zeros, at_z, zero_end, a.zero_words);
+                for (int i = 0; i < S; ++i)
+                    if (inside[i]) {
+                        cp_async16(dst + to + i * kItemBytes, src + i * 64);
+                        cp_async16(dst + to + i * kItemBytes + 512, src + half_w + i * 64);
+                    }
+                if (word0 < words) cp_async4(dst_s + to, src_s, 4);
+                for (int word = 2; word < words; word += 2)
+                    if (word + word0 < words) cp_async4(dst_s + to + 4 * word, src_s + 4 * word, 4);
+                if (INT)
+                    for (int word = 0; word < a.zero_words; word += 2)
+                        if (word + word0 < a.zero_words) cp_async4(dst_z + to + 4 * word, src_z + 4 * word, 4);
+            } else {
+                const bool lo = n_next + row_a < a.N, hi = n_next + row_a + 8 < a.N;
+#pragma unroll 1
+                for (int i = 0; i < S; ++i) {
+                    const bool in = busy && (first_slice + i) * 64 + piece * 16 < row_bytes;
+                    if (lo && in) cp_async16(dst + to + i * kItemBytes, src + i * 64);
+                    if (hi && in) cp_async16(dst + to + i * kItemBytes + 512, src + half_w + i * 64);
+                }
+                if (n_next + row_s < a.N) {   // not past the tensors' ends
+                    const uint8_t *end_s = a.scales + (int64_t)a.N * a.scale_row, *end_z = a.zeros + (int64_t)a.N * groups;
+                    for (int word = 0; word + word0 < words; word += 2)
+                        if (src_s + 4 * word < end_s)
+                            cp_async4(dst_s + to + 4 * word, src_s + 4 * word, (int)min((int64_t)4, (int64_t)(end_s - src_s) - 4 * word));
+                    if (INT)
+                        for (int word = 0; word + word0 < a.zero_words; word += 2)
+                            if (src_z + 4 * word < end_z)
+                                cp_async4(dst_z + to + 4 * word, src_z + 4 * word, (int)min((int64_t)4, (int64_t)(end_z - src_z) - 4 * word));
+                }
             }
             src += step_w;
-            at_s += step_s;
-            at_z += step_z;
+            src_s += step_s;
+            if (INT) src_z += step_z;
         }
         n_next += clusters * kTileRows;
         cp_async_commit();
         to = to == (kStages - 1) * kStage ? 0 : to + kStage;
     };
+    // Where the strips of rows g and g + 8 begin in a stage
+    int strip_s[2], strip_z[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int n = cluster * kTileRows + g + 8 * r;
+        const uint32_t at = (uint32_t)n * groups + group0;   // its low bits
+        strip_s[r] = kStrips + (g + 8 * r) * kScaleStrip + (INT ? (int)(at * (a.s_f32 ? 4 : 2) & 3) : 0);
+        strip_z[r] = kStrips + kTileRows * kScaleStrip + (g + 8 * r) * kZeroStrip + (int)(at & 3);
+    }
+    const IntBits bits;
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
+    uint32_t xf[S][8][NQ][2];   // slices, steps of 16, rows of x
+    float down[NQ][2];          // what undoes the powers of two of rows 8 n + 2 c, + 1
+    uint4 all[NQ][S][4];        // before W: its copies would be waited for in line
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const int t = 8 * n + g, k = (first_slice + i) * kSlice + 32 * b + 8 * c;
+                all[n][i][b] = make_uint4(0, 0, 0, 0);
+                if (t < a.T && k < a.K && first_slice + i < last_slice)
+                    all[n][i][b] = __ldg(reinterpret_cast<const uint4 *>(a.x + (int64_t)t * a.K + k));
+            }
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch();
     // Pieces behind N or K are never copied: their products are not used (rows) or
     // are with x of zero (columns; the ring's bits are finite numbers, and the scales
     // are taken as zero).
-    uint32_t xf[S][8][NQ][2];   // slices, steps of 16, rows of x
-    float down[NQ][2];          // what undoes the powers of two of rows 8 n + 2 c, + 1
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-        const int t = 8 * n + g;
-        uint4 raw[S][4];
+        const uint4 (&raw)[S][4] = all[n];
         uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < S; ++i)
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int k = (first_slice + i) * kSlice + 32 * b + 8 * c;
-                raw[i][b] = make_uint4(0, 0, 0, 0);
-                if (t < a.T && k < a.K && first_slice + i < last_slice)
-                    raw[i][b] = __ldg(reinterpret_cast<const uint4 *>(a.x + (int64_t)t * a.K + k));
-            }
 #pragma unroll
         for (int i = 0; i < S; ++i)
 #pragma unroll
@@ -309,14 +356,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
             uint32_t zp[2][kB];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int row = g + 8 * r;
                 if (KIND == kMx) {
-                    const float4 f = *reinterpret_cast<const float4 *>(s_scale + i * 64 + row * 4);
+                    const float4 f = *reinterpret_cast<const float4 *>(s_scale + i * 64 + (g + 8 * r) * 4);
                     sc[r][0] = f.x, sc[r][1 % kB] = f.y, sc[r][2 % kB] = f.z, sc[r][3 % kB] = f.w;
                 } else {
-                    const uint32_t at = (uint32_t)(n0 + row) * groups + group0;   // its low bits
-                    const uint8_t *strip = stage + kStrips + row * kScaleStrip + ((uint32_t)at * (a.s_f32 ? 4 : 2) & 3);
-                    const uint8_t *zs = stage + kStrips + kTileRows * kScaleStrip + row * kZeroStrip + (at & 3);
+                    const uint8_t *strip = stage + strip_s[r], *zs = stage + strip_z[r];
                     const int per = KIND == kIntSlice ? 1 : kSlice >> a.group_shift;   // groups of a slice: 1, or 2 or 4
 #pragma unroll
                     for (int b = 0; b < kB; ++b) {
@@ -343,8 +387,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
                     const int b = 2 * x + y;
                     uint32_t w0[4], w1[4];
                     if (INT) {
-                        widen_ints(w[2 * y], Zero(zp[0][b % kB]), w0);
-                        widen_ints(w[2 * y + 1], Zero(zp[1][b % kB]), w1);
+                        widen_ints(w[2 * y], bits, Zero(zp[0][b % kB]), w0);
+                        widen_ints(w[2 * y + 1], bits, Zero(zp[1][b % kB]), w1);
                     } else {
                         mx4_half8(w[2 * y], w0);
                         mx4_half8(w[2 * y + 1], w1);
