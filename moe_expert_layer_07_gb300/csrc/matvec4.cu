@@ -290,39 +290,43 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
         // place, with both types' biases); what falls below fp16's smallest is zero, and what
         // falls among its subnormal numbers off by up to 2^-15
         const uint32_t lower = (uint32_t)((-(ex - 15) << 7) & 0xffff) * 0x10001u;
-        const bool special = m >= 0x7f80u;   // an infinity or a NaN
+        auto bits_of = [&](uint32_t w) {
+            return (__viaddmax_s16x2_relu(w & 0x7fff7fffu, lower, 0u) << 3) | (w & 0x80008000u);
+        };
+        auto put = [&](auto convert) {
 #pragma unroll
-        for (int i = 0; i < S; ++i)
+            for (int i = 0; i < S; ++i)
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const uint32_t w[4] = {raw[i][b].x, raw[i][b].y, raw[i][b].z, raw[i][b].w};
-                uint32_t h[4];
+                for (int b = 0; b < 4; ++b) {
+                    const uint32_t h[4] = {convert(raw[i][b].x), convert(raw[i][b].y), convert(raw[i][b].z), convert(raw[i][b].w)};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    h[j] = (__viaddmax_s16x2_relu(w[j] & 0x7fff7fffu, lower, 0u) << 3) | (w[j] & 0x80008000u);
-                    if (special) {
-                        if ((w[j] & 0x7f80u) == 0x7f80u) h[j] |= 0x7c00u | (w[j] & 0x7fu) << 3;
-                        if ((w[j] & 0x7f800000u) == 0x7f800000u) h[j] |= 0x7c000000u | (w[j] & 0x7f0000u) << 3;
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        xf[i][2 * b + j / 2][n][j & 1] =
+                            INT ? __byte_perm(h[j / 2], h[2 + j / 2], j & 1 ? 0x7632 : 0x5410) : h[j];
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    xf[i][2 * b + j / 2][n][j & 1] =
-                        INT ? __byte_perm(h[j / 2], h[2 + j / 2], j & 1 ? 0x7632 : 0x5410) : h[j];
-            }
+        };
+        if (!__any_sync(0xffffffffu, m >= 0x7f80u)) {
+            put(bits_of);
+        } else {   // an infinity or a NaN
+            put([&](uint32_t w) {
+                uint32_t h = bits_of(w);
+                if ((w & 0x7f80u) == 0x7f80u) h |= 0x7c00u | (w & 0x7fu) << 3;
+                if ((w & 0x7f800000u) == 0x7f800000u) h |= 0x7c000000u | (w & 0x7f0000u) << 3;
+                return h;
+            });
+        }
     }
     const int mrow = (lane & 7) + ((lane >> 3) & 1) * 8, mblk = lane >> 4;
 
-    for (int it0 = 0; it0 < mine; it0 += kBatch) {
-        const int batch = min(kBatch, mine - it0);
-        float acc[kBatch][NQ][4];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            if (u >= batch) break;
-            const int it = it0 + u;
-            cp_async_wait<kStages - 2>();
-            __syncwarp();
-            fetch();
+    // (Not unrolled: with two tiles' code in line, the instruction cache was what 16 rows of x
+    // waited for.)
+#pragma unroll 1
+    for (int it = 0; it < mine; ++it) {
+        const int slot_in_batch = it % kBatch;
+        float acc[NQ][4];
+        cp_async_wait<kStages - 2>();
+        __syncwarp();
+        fetch();
         const uint8_t *stage = ring + from;
         const uint32_t slot = ring_addr + from;
         from = from == (kStages - 1) * kStage ? 0 : from + kStage;
@@ -402,39 +406,35 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
                         if (b % (4 / kB) == 4 / kB - 1) {
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                acc[u][n][j] = i + b < 4 / kB ? d[n][j] * sc[j >> 1][b % kB] : fmaf(d[n][j], sc[j >> 1][b % kB], acc[u][n][j]);
+                                acc[n][j] = i + b < 4 / kB ? d[n][j] * sc[j >> 1][b % kB] : fmaf(d[n][j], sc[j >> 1][b % kB], acc[n][j]);
                         }
                     }
                 }
             }
         }
-        }
-        // the warps' sums of these tiles
-        if (it0) __syncthreads();   // those of the tiles before have been read
+        // the warps' sums of a batch of tiles
+        if (slot_in_batch == 0 && it) __syncthreads();   // those of the batch before have been read
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            if (u >= batch) break;
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                float *p = s_part + (warp * kBatch + u) * kSums + 8 * n + 2 * c;
-                *reinterpret_cast<float2 *>(p + g * 8 * NQ) = make_float2(acc[u][n][0] * down[n][0], acc[u][n][1] * down[n][1]);
-                *reinterpret_cast<float2 *>(p + (g + 8) * 8 * NQ) = make_float2(acc[u][n][2] * down[n][0], acc[u][n][3] * down[n][1]);
-            }
+        for (int n = 0; n < NQ; ++n) {
+            float *p = s_part + (warp * kBatch + slot_in_batch) * kSums + 8 * n + 2 * c;
+            *reinterpret_cast<float2 *>(p + g * 8 * NQ) = make_float2(acc[n][0] * down[n][0], acc[n][1] * down[n][1]);
+            *reinterpret_cast<float2 *>(p + (g + 8) * 8 * NQ) = make_float2(acc[n][2] * down[n][0], acc[n][3] * down[n][1]);
         }
+        if (slot_in_batch != kBatch - 1 && it != mine - 1) continue;
+        const int batch = slot_in_batch + 1, it0 = it - slot_in_batch;
         __syncthreads();
         for (int i = tid; i < batch * kSums; i += a.warps * 32) {
             float v = 0.0f;
 #pragma unroll 4
             for (int q = 0; q < a.warps; ++q) v += s_part[q * kBatch * kSums + i];
-            const int it = it0 + i / kSums, j = i % kSums;
-            if (ranks > 1) s_hold[(it % kHold) * kSums + j] = v;
-            else write(a, j & (8 * NQ - 1), (cluster + it * clusters) * kTileRows + j / (8 * NQ), v);
+            const int at = it0 + i / kSums, j = i % kSums;
+            if (ranks > 1) s_hold[(at % kHold) * kSums + j] = v;
+            else write(a, j & (8 * NQ - 1), (cluster + at * clusters) * kTileRows + j / (8 * NQ), v);
         }
         static_assert(kHold % kBatch == 0, "a batch is held as a whole");
-        const int last = it0 + batch - 1;
-        if (ranks > 1 && (last % kHold == kHold - 1 || last == mine - 1)) {
+        if (ranks > 1 && (it % kHold == kHold - 1 || it == mine - 1)) {
             // the CTAs' sums together: CTA r finishes its share of what is held
-            const int held = last % kHold + 1, base = last - last % kHold;
+            const int held = it % kHold + 1, base = it - it % kHold;
             ptx::cluster_sync();
             const uint32_t mem = ptx::smem_u32(s_hold);
             for (int i = rank * a.warps * 32 + tid; i < held * kSums; i += ranks * a.warps * 32) {
