@@ -24,6 +24,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "internal.h"
@@ -36,7 +37,7 @@ namespace {
 constexpr int kMaxWarps = 16;
 constexpr int kTileRows = 16, kSlice = 128;
 constexpr int kItemBytes = kTileRows * kSlice / 2;
-constexpr int kHold = 16;   // row tiles whose sums a CTA of a cluster holds between exchanges
+constexpr int kHold = 16;   // row tiles whose sums the CTAs of a cluster hold between exchanges
 // Row tiles between two of a CTA's barriers, for 8 and 16 rows of x
 __host__ __device__ constexpr int batch_tiles(int nq) { return 4 / nq; }
 // Strips of scales and zero points: bytes of a row of W
@@ -133,10 +134,10 @@ __device__ __forceinline__ void widen_ints(uint32_t codes, const IntBits &k, con
     h[3] = fma_half2(and_or(up, k.hi, k.k), k.sixteenth, z.sixteen);
 }
 
-// A barrier of the cluster that orders no memory: what was read before it has been used.
-__device__ __forceinline__ void cluster_sync_relaxed() {
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
+// The two halves of a barrier of the cluster; relaxed: one that orders no memory.
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void write(const MatvecArgs &a, int t, int n, float v) {
     if (t >= a.T || n >= a.N) return;
@@ -161,8 +162,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
     uint8_t *ring = smem + warp * kStages * kStage;
     const uint32_t ring_addr = ptx::smem_u32(ring);
     float *s_part = reinterpret_cast<float *>(smem + a.warps * kStages * kStage);   // [warps][kBatch][kSums]
-    float *s_hold = s_part + a.warps * kBatch * kSums;                                // [kHold][kSums]
-    float *s_scale = s_hold + kHold * kSums + warp * (S * 64);                      // MXFP4: [slice][row][block]
+    float *s_hold = s_part + a.warps * kBatch * kSums;                                // [ranks][hold_tiles][kSums]
+    const int hold_tiles = (kHold + ranks - 1) / ranks;
+    const uint32_t hold = ptx::smem_u32(s_hold);
+    // MXFP4: [slice][row][block]
+    float *s_scale = s_hold + (ranks > 1 ? ranks * hold_tiles * kSums : 0) + warp * (S * 64);
     const int row_bytes = a.K >> 1, groups = a.K >> a.group_shift;
     const int group0 = INT ? first_slice * (kSlice >> a.group_shift) : 0;
     const bool busy = first_slice < last_slice;
@@ -243,6 +247,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
         strip_z[r] = kStrips + kTileRows * kScaleStrip + (g + 8 * r) * kZeroStrip + (int)(at & 3);
     }
     const IntBits bits;
+    if (ranks > 1) cluster_arrive_relaxed();
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
     uint32_t xf[S][8][NQ][2];   // slices, steps of 16, rows of x
@@ -423,44 +428,57 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
         if (slot_in_batch != kBatch - 1 && it != mine - 1) continue;
         const int batch = slot_in_batch + 1, it0 = it - slot_in_batch;
         __syncthreads();
+        if (ranks > 1 && it0 % kHold == 0) cluster_wait();   // the other CTAs run, and have read what they held
         for (int i = tid; i < batch * kSums; i += a.warps * 32) {
             float v = 0.0f;
 #pragma unroll 4
             for (int q = 0; q < a.warps; ++q) v += s_part[q * kBatch * kSums + i];
-            const int at = it0 + i / kSums, j = i % kSums;
-            if (ranks > 1) s_hold[(at % kHold) * kSums + j] = v;
+            const int at = it0 + i / kSums, j = i % kSums, held = at % kHold;
+            if (ranks > 1)   // to the CTA that adds them up
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(ptx::cluster_map(
+                                 hold + 4 * ((rank * hold_tiles + held / ranks) * kSums + j), held % ranks)), "f"(v) : "memory");
             else write(a, j & (8 * NQ - 1), (cluster + at * clusters) * kTileRows + j / (8 * NQ), v);
         }
         static_assert(kHold % kBatch == 0, "a batch is held as a whole");
         if (ranks > 1 && (it % kHold == kHold - 1 || it == mine - 1)) {
-            // the CTAs' sums together: CTA r finishes its share of what is held
-            const int held = it % kHold + 1, base = it - it % kHold;
+            // the CTAs' sums together: CTA r finishes tiles r, r + ranks .. of what is held
+            const int held = it % kHold + 1, base = it - it % kHold, own = (held - rank + ranks - 1) / ranks;
             ptx::cluster_sync();
-            const uint32_t mem = ptx::smem_u32(s_hold);
-            for (int i = rank * a.warps * 32 + tid; i < held * kSums; i += ranks * a.warps * 32) {
+            for (int i = tid; i < own * kSums; i += a.warps * 32) {
                 float v = 0.0f;
-                for (int r = 0; r < ranks; ++r) {
-                    float p;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(ptx::cluster_map(mem + 4 * i, r)));
-                    v += p;
-                }
-                const int j = i % kSums;
-                write(a, j & (8 * NQ - 1), (cluster + (base + i / kSums) * clusters) * kTileRows + j / (8 * NQ), v);
+                for (int r = 0; r < ranks; ++r) v += s_hold[r * hold_tiles * kSums + i];
+                const int at = base + rank + i / kSums * ranks, j = i % kSums;
+                write(a, j & (8 * NQ - 1), (cluster + at * clusters) * kTileRows + j / (8 * NQ), v);
             }
-            cluster_sync_relaxed();   // nobody reads this CTA's shared memory any more
+            if (it != mine - 1) cluster_arrive();   // they may be overwritten
         }
     }
     cp_async_wait<0>();
 }
 
+// Clusters of c that run at a time on the current device (asked for once each).
+int clusters_at_once(const void *kern, const cudaLaunchConfig_t &c, int ranks) {
+    static std::atomic<int> known[64][9];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+    if ((n = known[dev][ranks].load(std::memory_order_relaxed)) == 0) {
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &c) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            return 1;
+        }
+        known[dev][ranks].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 template <int KIND, int NQ, int S>
-int launch(const MatvecArgs &a, int ranks, int clusters, cudaStream_t s) {
+int launch(const MatvecArgs &a, int ranks, cudaStream_t s) {
     const auto kern = matvec4_kernel<KIND, NQ, S>;
-    const int smem = a.warps * kStages * stage_bytes(KIND != kMx, S) + (a.warps * batch_tiles(NQ) + kHold) * NQ * 128 * 4 +
+    const int hold = ranks > 1 ? ranks * (int)ceil_div(kHold, ranks) : 0;
+    const int smem = a.warps * kStages * stage_bytes(KIND != kMx, S) + (a.warps * batch_tiles(NQ) + hold) * NQ * 128 * 4 +
                      (KIND == kMx ? a.warps * S * 64 * 4 : 0);
     MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     cudaLaunchConfig_t c = {};
-    c.gridDim = dim3((unsigned)(ranks * clusters));
     c.blockDim = dim3((unsigned)(a.warps * 32));
     c.dynamicSmemBytes = smem;
     c.stream = s;
@@ -472,6 +490,13 @@ int launch(const MatvecArgs &a, int ranks, int clusters, cudaStream_t s) {
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     c.attrs = at;
     c.numAttrs = 2;
+    // All clusters at once.  Not every SM has neighbours for one of more than two: 36 of four run, 28
+    // of five, 15 of seven or eight, and a second round of a few takes as long as the first.
+    const int tiles = (int)ceil_div(a.N, kTileRows);
+    int clusters = std::max(1, sm_count() / ranks);
+    c.gridDim = dim3((unsigned)(ranks * clusters));
+    if (ranks > 2) clusters = std::min(clusters, clusters_at_once(reinterpret_cast<const void *>(kern), c, ranks));
+    c.gridDim = dim3((unsigned)(ranks * std::min(tiles, clusters)));
     const cudaError_t e = cudaLaunchKernelEx(&c, kern, (const MatvecArgs)a);
     return e == cudaSuccess ? MOE_OK : cuda_fail("cudaLaunchKernelEx", e);
 }
@@ -496,7 +521,7 @@ int launch_w4_matvec(const moe_w4 *d, int T, const void *x, const void *codes, c
     // Slices a warp and CTAs a cluster: x's registers are 16 (8 rows) or 32 a slice
     const int per_warp = a.slices > kMaxWarps ? 2 : 1;
     int ranks = 1;
-    while (ranks * kMaxWarps * per_warp < a.slices) ranks *= 2;   // 32768 of K: 8
+    while (ranks * kMaxWarps * per_warp < a.slices) ++ranks;   // 32768 of K: 8
     a.warps = (int)ceil_div(ceil_div(a.slices, ranks), per_warp);
     a.per_cta = a.warps * per_warp;
     ranks = (int)ceil_div(a.slices, a.per_cta);
@@ -504,13 +529,11 @@ int launch_w4_matvec(const moe_w4 *d, int T, const void *x, const void *codes, c
     a.scale_row = d->kind == MOE_W4_INT ? groups * size : groups;
     a.scale_words = a.s_f32 ? strip : (strip * 2 + 2 + 3) / 4;
     a.zero_words = zeros ? (strip + 3 + 3) / 4 : 0;
-    const int tiles = (int)ceil_div(a.N, kTileRows);
-    const int clusters = std::max(1, std::min(tiles, sm_count() / ranks));
     const bool wide = T > 8;
     auto go = [&](auto kind) {
         constexpr int K = decltype(kind)::value;
-        if (per_warp == 1) return wide ? launch<K, 2, 1>(a, ranks, clusters, s) : launch<K, 1, 1>(a, ranks, clusters, s);
-        return wide ? launch<K, 2, 2>(a, ranks, clusters, s) : launch<K, 1, 2>(a, ranks, clusters, s);
+        if (per_warp == 1) return wide ? launch<K, 2, 1>(a, ranks, s) : launch<K, 1, 1>(a, ranks, s);
+        return wide ? launch<K, 2, 2>(a, ranks, s) : launch<K, 1, 2>(a, ranks, s);
     };
     if (d->kind == MOE_W4_MX) return go(std::integral_constant<int, kMx>());
     if (d->group == kSlice) return go(std::integral_constant<int, kIntSlice>());
