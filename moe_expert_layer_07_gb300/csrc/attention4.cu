@@ -686,8 +686,8 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
 }
 
 // One block: eight rows of what CTA blockIdx.x began.  A warp takes every eighth
-// partial result for all of the rows.
-constexpr int kJoinRows = 8;
+// partial result for all of the rows, or one row where there are few.
+constexpr int kJoinRows = 8, kShortJoin = 4;
 
 template <int D>
 __global__ void __launch_bounds__(256) attention4_join_kernel(const AttnArgs a, int rows_at_once) {
@@ -702,6 +702,35 @@ __global__ void __launch_bounds__(256) attention4_join_kernel(const AttnArgs a, 
     const int parts = cut.last - k0 + 1;
     const int64_t size = (int64_t)rows_at_once * (D + 2);
     auto part = [&](int j) { return a.part + (2 * (int64_t)(k0 + j) + (j == 0)) * size; };
+    if (parts <= kShortJoin) {   // a warp to a row
+        const int rr = r0 + warp;
+        if (rr >= cut.nrows) return;
+        const float *p = part(min(lane, parts - 1)) + rows_at_once * D + rr;
+        float top = p[0], l = lane < parts ? p[rows_at_once] : 0.0f;
+        const float mine = top;
+        float4 y[kShortJoin];
+#pragma unroll
+        for (int j = 0; j < kShortJoin; ++j)
+            if (j < parts && lane < D / 4) y[j] = *reinterpret_cast<const float4 *>(part(j) + (int64_t)rr * D + 4 * lane);
+#pragma unroll
+        for (int x = 1; x < kShortJoin; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float f = mine == top ? 1.0f : ex2(mine - top);
+        l *= f;
+#pragma unroll
+        for (int x = 1; x < kShortJoin; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < kShortJoin; ++j) {
+            const float fj = __shfl_sync(0xffffffffu, f, j);
+            if (j < parts && lane < D / 4) v.x += fj * y[j].x, v.y += fj * y[j].y, v.z += fj * y[j].z, v.w += fj * y[j].w;
+        }
+        l = __shfl_sync(0xffffffffu, l, 0), top = __shfl_sync(0xffffffffu, top, 0);
+        const int row = cut.rowbase + rr;
+        const int64_t at = (int64_t)(cut.row0 + row / a.G) * a.Hq + cut.head0 + row % a.G;
+        if (lane < D / 4) write4(a, at * D + 4 * lane, v, l == 0.0f ? 0.0f : 1.0f / l);
+        if (a.lse && lane == 0) a.lse[at] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718f;
+        return;
+    }
     {   // each row's largest: lane rr + 8 i of a warp takes partial 4 warp + i + 32 n
         float m = -INFINITY;
         for (int j = 4 * warp + (lane >> 3); j < parts; j += 32)
