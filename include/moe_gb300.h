@@ -579,8 +579,9 @@ typedef struct moe_cache4 {
  * id below 0 that a token needs sets MOE_DEV_BAD_INDEX; too few free pages,
  * table columns or token rows MOE_DEV_NO_ROOM; then lengths = held, starts,
  * and positions are 0, slots -1, free_out = free_range and the table is as it
- * was.  (An id below 0 is looked at where tokens join a request's last held
- * page.)  One launch; nothing else may overlap. */
+ * was.  (Ids are looked at where tokens join a request's last held page.  A free
+ * page whose id is below 0, or so large that its slots pass 32 bits, gives its
+ * tokens the slot -2^31, which is in no cache.)  One launch; nothing else may overlap. */
 MOE_API int moe_cache_tables(int32_t requests, int32_t page, const int32_t *held,
                              const int32_t *new_tokens, const int32_t *free_pages,
                              int32_t free_count, const int64_t *free_range, int32_t *table,
@@ -649,7 +650,9 @@ MOE_API int moe_cache_read(const moe_cache4 *cache, int32_t n, const int32_t *sl
  * below 2^-22 of the largest that the row's tokens have there count as zero.
  *   desc.max_q    the most query rows of one request, and
  *   desc.max_len  the longest request: what the kernels and the workspace are
- *                 chosen by; larger ones on the device are computed all the same
+ *                 chosen by; larger ones on the device are computed all the same,
+ *                 unless their units of work (128 tokens by 8 rows and more) pass
+ *                 2^31 / requests: MOE_DEV_BAD_INDEX, and not computed
  *   ws         moe_cache_attention_workspace_size bytes, 16-byte aligned; one call
  *              at a time; needs no initialisation
  * requests 0..4096, rows * q_heads below 2^31, q_heads a multiple of kv_heads. */
@@ -672,7 +675,7 @@ MOE_API int moe_cache_attention(const moe_cache_attn *d, const moe_cache4 *cache
  *               (even k in the low four bits), scales bf16 or fp32 (scale_dtype),
  *               zero points uint8 0..15 or NULL (8); group 32, 64 or 128
  * fp32 accumulation.  x is taken as fp16 times a power of two for each row
- * (and part of K): each value is off by 2^-29 of a row's largest at most.  n_out any, k_dim a multiple of
+ * (and part of K): each value is off by 2^-29 of a row's largest at most.  n_out up to 2^30, k_dim a multiple of
  * the group (of 32 for MXFP4), at most 32768; x and codes 16-byte aligned. */
 enum { MOE_W4_MX = 0, MOE_W4_INT = 1 };
 typedef struct moe_w4 {

@@ -135,7 +135,7 @@ int moe_w4_matvec(const moe_w4 *d, int32_t T, const void *x, const void *codes, 
     if (d->kind == MOE_W4_INT ? !is_float_type(d->scale_dtype) : zeros != nullptr) return MOE_ERR_INVALID_ARG;
     if (d->group != 32 && (d->kind == MOE_W4_MX || (d->group != 64 && d->group != 128)))
         return MOE_ERR_UNSUPPORTED_SHAPE;
-    if (T > 16 || d->k_dim % d->group || d->k_dim > 32768 || d->n_out > INT32_MAX - 256)
+    if (T > 16 || d->k_dim % d->group || d->k_dim > 32768 || d->n_out > 1 << 30)
         return MOE_ERR_UNSUPPORTED_SHAPE;
     if (T == 0) return MOE_OK;
     if (!x || !codes || !scales || !y) return MOE_ERR_INVALID_ARG;

@@ -821,7 +821,9 @@ int launch(const AttnArgs &a0, cudaStream_t s) {
     using S = Shape<D, NQ>;
     AttnArgs a = a0;
     const int smem = S::kSmem + (a.B + 1) * 4;
-    MOE_CUDA_TRY(cudaFuncSetAttribute(attention4_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    // (the most that any call takes: calls of several threads set the same)
+    MOE_CUDA_TRY(cudaFuncSetAttribute(attention4_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      S::kSmem + (kAttnMaxRequests + 1) * 4));
     if (int rc = launch_dependent(attention4_kernel<D, NQ>, dim3(a.ctas), dim3(kThreads), smem, s, (const AttnArgs)a))
         return rc;
     return launch_attention4_join(a, D, S::kRows, a.ctas, s);
@@ -868,7 +870,8 @@ int launch_attention4(const moe_cache_attn *d, const moe_cache4 *cache, const vo
     a.pages = cache->pages;
     a.page_shift = 0;
     while ((1 << a.page_shift) < cache->page) ++a.page_shift;
-    a.window = d->window;
+    // (a window of all that a request can hold is none)
+    a.window = d->window >= (int64_t)d->max_pages * cache->page ? 0 : d->window;
     a.out_bf16 = out_dtype == MOE_OUT_BF16;
     a.scale_log2 = d->scale * 1.44269504f;
     const int nq = rows8(d, cache);

@@ -22,7 +22,7 @@
 namespace moe {
 namespace {
 
-constexpr int kTabThreads = 1024;
+constexpr int kTabThreads = 1024, kTabMaxRequests = 16384;
 
 struct TabArgs {
     int B, page_shift, free_count, max_pages, max_tokens;
@@ -66,6 +66,9 @@ __device__ __forceinline__ int last_at_most(const int *v, int n, int t) {
     return lo;
 }
 
+// Whether page `id`'s slots are numbers.
+__device__ __forceinline__ bool is_page(int id, int page_shift) { return (unsigned)id <= (unsigned)(INT32_MAX >> page_shift); }
+
 // One cluster.  Shared memory: starts [B + 1], first [B + 1], held [B].
 __global__ void __launch_bounds__(kTabThreads) cache_tables_kernel(const TabArgs a) {
     extern __shared__ int s_tab[];
@@ -91,7 +94,8 @@ __global__ void __launch_bounds__(kTabThreads) cache_tables_kernel(const TabArgs
             want = (held + fresh + page - 1) >> a.page_shift;
             if (want > a.max_pages) full = true;
             // tokens that join the last held page take its id from the table
-            else if (fresh > 0 && (held & (page - 1)) && a.table[(int64_t)b * a.max_pages + had - 1] < 0) bad = true;
+            else if (fresh > 0 && (held & (page - 1)) && !is_page(a.table[(int64_t)b * a.max_pages + had - 1], a.page_shift))
+                bad = true;
         }
         int64_t t = fresh, p = want - had;
         block_scan2(t, p, sh);
@@ -140,7 +144,7 @@ __global__ void __launch_bounds__(kTabThreads) cache_tables_kernel(const TabArgs
             const int i = pos >> a.page_shift, had = (s_held[b] + page - 1) >> a.page_shift;
             const int id = i < had ? a.table[(int64_t)b * a.max_pages + i]
                                    : a.free_pages[((uint64_t)at + s_first[b] + i - had) % F];
-            slot = (int)(((unsigned)id << a.page_shift) + (pos & (page - 1)));
+            slot = is_page(id, a.page_shift) ? (id << a.page_shift) + (pos & (page - 1)) : INT32_MIN;
         }
         a.slots[t] = slot;
         a.positions[t] = pos;
@@ -218,9 +222,9 @@ int launch_cache_tables(int B, int page, const int32_t *held, const int32_t *fre
     a.free_out = free_out;
     a.status = status;
     const size_t smem = sizeof(int) * (3 * (size_t)B + 2);
-    if (smem > 40 * 1024)
+    if (smem > 40 * 1024)   // the most that any call takes: calls of several threads set the same
         MOE_CUDA_TRY(cudaFuncSetAttribute(cache_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          (int)smem));
+                                          (int)sizeof(int) * (3 * kTabMaxRequests + 2)));
     cudaLaunchConfig_t c = {};
     const unsigned ctas = max_tokens > 4 * kTabThreads ? 8 : 1;
     c.gridDim = dim3(ctas);

@@ -474,10 +474,14 @@ int clusters_at_once(const void *kern, const cudaLaunchConfig_t &c, int ranks) {
 template <int KIND, int NQ, int S>
 int launch(const MatvecArgs &a, int ranks, cudaStream_t s) {
     const auto kern = matvec4_kernel<KIND, NQ, S>;
-    const int hold = ranks > 1 ? ranks * (int)ceil_div(kHold, ranks) : 0;
-    const int smem = a.warps * kStages * stage_bytes(KIND != kMx, S) + (a.warps * batch_tiles(NQ) + hold) * NQ * 128 * 4 +
-                     (KIND == kMx ? a.warps * S * 64 * 4 : 0);
-    MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    const int hold = ranks > 1 ? ranks * (int)ceil_div(kHold, ranks) : 0;   // seven ranks: kHold + 5
+    auto bytes = [](int warps, int hold) {
+        return warps * kStages * stage_bytes(KIND != kMx, S) + (warps * batch_tiles(NQ) + hold) * NQ * 128 * 4 +
+               (KIND == kMx ? warps * S * 64 * 4 : 0);
+    };
+    const int smem = bytes(a.warps, hold);
+    // (the most that any call takes: calls of several threads set the same)
+    MOE_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(kMaxWarps, kHold + 5)));
     cudaLaunchConfig_t c = {};
     c.blockDim = dim3((unsigned)(a.warps * 32));
     c.dynamicSmemBytes = smem;

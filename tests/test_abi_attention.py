@@ -133,6 +133,11 @@ def test_w4_refusals(L):
     assert call(kind=1, z=ODD) == -1
 
 
+def test_w4_refuses_more_columns_than_its_counts_hold(L):
+    d = A._W4(n_out=(1 << 30) + 1, k_dim=32, kind=0, group=32, scale_dtype=0)
+    assert L.moe_w4_matvec(d, 1, FAKE, FAKE, FAKE, None, FAKE, 0, None) == -2
+
+
 def test_binding_refuses_wrong_tensors():
     """Shapes, types and places: a tensor on the CPU is not passed on either."""
     u8, i32, bf = torch.uint8, torch.int32, torch.bfloat16
