@@ -7,6 +7,7 @@ against each other here, everything else by the library.
 """
 from __future__ import annotations
 
+import copy
 import ctypes
 
 import torch
@@ -64,10 +65,16 @@ def _typed(t, dtype, shape, name):
     return _dense(t, shape, name)
 
 
-def _word(status):
-    if status is not None and (status.dtype is not _I32 or not status.is_cuda or status.numel() < 1):
-        raise TypeError("status: expected an int32 CUDA tensor")
-    return _at(status)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_ELSEWHERE = "expected tensors of one device, the current one"
+
+
+def _word(status, dev):
+    if status is None:
+        return None
+    if status.dtype is not _I32 or status.numel() < 1 or status.get_device() != dev:
+        raise TypeError("status: expected an int32 CUDA tensor on the others' device")
+    return status.data_ptr()
 
 
 class Cache4:
@@ -94,6 +101,9 @@ class Cache4:
             raise TypeError("codes and scales: expected uint8 tensors")
         _dense(codes, codes.shape, "codes")
         _dense(scales, (pages, 2, kv_heads, page, half // 16), "scales")
+        self.device = codes.get_device()
+        if scales.get_device() != self.device:
+            raise ValueError(_ELSEWHERE)
         self.codes, self.scales = codes, scales
         self.pages, self.page, self.kv_heads, self.dim = pages, page, kv_heads, 2 * half
         self.c = _Cache(codes.data_ptr(), scales.data_ptr(), pages, kv_heads, page, 2 * half)
@@ -120,11 +130,12 @@ def cache_tables(held, new_tokens, free_pages, free_range, page, table, lengths,
     n, f = slots.shape[0], free_pages.shape[0]
     i64 = torch.int64
     # one test of all that holds in a correct call; what failed is looked up after
-    good = True
+    dev = held.get_device()
+    good = dev >= 0
     for t in (held, new_tokens, free_pages, table, lengths, starts, slots, positions):
-        good = good and t.dtype is _I32 and t.is_cuda and t.is_contiguous()
-    if not (good and free_range.dtype is i64 and free_out.dtype is i64 and free_range.is_cuda and free_out.is_cuda
-            and free_range.is_contiguous() and free_out.is_contiguous() and free_range.shape == free_out.shape == (2,)
+        good = good and t.dtype is _I32 and t.get_device() == dev and t.is_contiguous()
+    if not (good and free_range.dtype is i64 and free_out.dtype is i64 and dev == free_range.get_device()
+            and dev == free_out.get_device() and dev == _current_device() and free_range.is_contiguous() and free_out.is_contiguous() and free_range.shape == free_out.shape == (2,)
             and held.shape == new_tokens.shape == lengths.shape == (B,) and table.shape == (B, w)
             and starts.shape == (B + 1,) and slots.shape == positions.shape == (n,)
             and free_pages.shape == (f,)):
@@ -135,10 +146,11 @@ def cache_tables(held, new_tokens, free_pages, free_range, page, table, lengths,
             _typed(t, _I32, shape, name)
         _typed(free_range, i64, (2,), "free_range")
         _typed(free_out, i64, (2,), "free_out")
+        raise ValueError(_ELSEWHERE)
     rc = lib().moe_cache_tables(B, page, held.data_ptr(), new_tokens.data_ptr(), free_pages.data_ptr(), f,
                                 free_range.data_ptr(), table.data_ptr(), w, lengths.data_ptr(),
                                 starts.data_ptr(), slots.data_ptr(), positions.data_ptr(), n,
-                                free_out.data_ptr(), _word(status), _stream(stream))
+                                free_out.data_ptr(), _word(status, dev), _stream(stream))
     if rc:
         _check(rc, "moe_cache_tables")
 
@@ -157,21 +169,23 @@ def qk_norm_rope(qkv, positions, cos_sin, q_heads, kv_heads, q_out, k_out=None, 
     param = w_q if w_q is not None else w_k
     pkind = OUT_BF16 if param is None else _OUT.get(param.dtype)
     # one test of all that holds in a correct call; what failed is looked up after
-    good = (pkind is not None and qkv.dtype is _BF16 and q_out.dtype is _BF16 and qkv.is_cuda and q_out.is_cuda
-            and qkv.dim() == 2 and qkv.stride(1) == 1 and qkv.shape[1] >= (q_heads + 2 * kv_heads) * dim
+    dev = qkv.get_device()
+    good = (pkind is not None and qkv.dtype is _BF16 and q_out.dtype is _BF16 and dev >= 0
+            and q_out.get_device() == dev and dev == _current_device() and qkv.dim() == 2 and qkv.stride(1) == 1 and qkv.shape[1] >= (q_heads + 2 * kv_heads) * dim
             and q_out.shape == (T, q_heads, dim) and q_out.is_contiguous() and (cache is None) == (slots is None))
     for w in (w_q, w_k):
         if w is not None:
-            good = good and w.dtype is param.dtype and w.shape == (dim,) and w.is_cuda and w.is_contiguous()
+            good = good and w.dtype is param.dtype and w.shape == (dim,) and w.get_device() == dev and w.is_contiguous()
     if k_out is not None:
-        good = (good and k_out.dtype is _BF16 and k_out.shape == (T, kv_heads, dim) and k_out.is_cuda
-                and k_out.is_contiguous())
+        good = (good and k_out.dtype is _BF16 and k_out.shape == (T, kv_heads, dim)
+                and k_out.get_device() == dev and k_out.is_contiguous())
     if rot:
-        good = (good and cos_sin.dtype is torch.float32 and cos_sin.dim() == 2 and cos_sin.is_cuda
+        good = (good and cos_sin.dtype is torch.float32 and cos_sin.dim() == 2 and cos_sin.get_device() == dev
                 and cos_sin.is_contiguous() and positions.dtype is _I32 and positions.shape == (T,)
-                and positions.is_cuda and positions.is_contiguous())
+                and positions.get_device() == dev and positions.is_contiguous())
     if slots is not None:
-        good = good and slots.dtype is _I32 and slots.shape == (T,) and slots.is_cuda and slots.is_contiguous()
+        good = (good and slots.dtype is _I32 and slots.shape == (T,) and slots.get_device() == dev
+                and slots.is_contiguous() and cache.device == dev)
     if not good:
         _refuse_rope(qkv, positions, cos_sin, rot, q_heads, kv_heads, q_out, k_out, w_q, w_k, param, pkind, cache, slots)
     stride = qkv.stride(0) if T > 1 else qkv.shape[1]
@@ -183,7 +197,7 @@ def qk_norm_rope(qkv, positions, cos_sin, q_heads, kv_heads, q_out, k_out=None, 
         d = _ROPES[key] = _Rope(*key)
     rc = lib().moe_qk_norm_rope(d, T, qkv.data_ptr(), _at(positions), _at(cos_sin) if rot else None, _at(w_q),
                                 _at(w_k), q_out.data_ptr(), _at(k_out), None if cache is None else cache.c,
-                                _at(slots), _word(status), _stream(stream))
+                                _at(slots), _word(status, dev), _stream(stream))
     if rc:
         _check(rc, "moe_qk_norm_rope")
 
@@ -208,6 +222,8 @@ def _refuse_rope(qkv, positions, cos_sin, rot, q_heads, kv_heads, q_out, k_out, 
         raise ValueError("cache and slots go together")
     if slots is not None:
         _typed(slots, _I32, (T,), "slots")
+    if qkv.is_cuda and qkv.dim() == 2 and qkv.stride(1) == 1 and qkv.shape[1] >= (q_heads + 2 * kv_heads) * dim:
+        raise ValueError(_ELSEWHERE)
     raise ValueError(f"qkv: expected CUDA rows of {q_heads} + 2 x {kv_heads} heads of {dim}, got {tuple(qkv.shape)}")
 
 
@@ -219,16 +235,19 @@ def cache_read(cache: Cache4, slots, k=None, v=None, status=None, stream=None):
     slot -1 are left as they were."""
     n = slots.shape[0]
     shape = (n, cache.kv_heads, cache.dim)
-    good = slots.dtype is _I32 and slots.shape == (n,) and slots.is_cuda and slots.is_contiguous()
+    dev = cache.device
+    good = (slots.dtype is _I32 and slots.shape == (n,) and slots.get_device() == dev and slots.is_contiguous()
+            and dev == _current_device())
     for t in (k, v):
         if t is not None:
-            good = good and t.dtype is _BF16 and t.shape == shape and t.is_cuda and t.is_contiguous()
+            good = good and t.dtype is _BF16 and t.shape == shape and t.get_device() == dev and t.is_contiguous()
     if not good:
         _typed(slots, _I32, (n,), "slots")
         for name, t in (("k", k), ("v", v)):
             if t is not None:
                 _typed(t, _BF16, shape, name)
-    rc = lib().moe_cache_read(cache.c, n, slots.data_ptr(), _at(k), _at(v), _word(status), _stream(stream))
+        raise ValueError(_ELSEWHERE)
+    rc = lib().moe_cache_read(cache.c, n, slots.data_ptr(), _at(k), _at(v), _word(status, dev), _stream(stream))
     if rc:
         _check(rc, "moe_cache_read")
 
@@ -253,22 +272,34 @@ class CacheAttention:
         self.ws_bytes = n.value
         self.ws = torch.empty(max(1, n.value), dtype=torch.uint8, device=cache.codes.device)
 
+    def of_rows(self, rows):
+        """The same for fewer query rows, in the same workspace."""
+        d = self.d
+        if not 0 <= rows <= d.rows:
+            raise ValueError(f"{rows} rows, and a workspace for {d.rows}")
+        other = copy.copy(self)
+        other.d = _Attn(d.requests, rows, d.q_heads, d.max_pages, d.max_q, d.max_len, d.window, d.scale)
+        return other
+
     def forward(self, q, table, lengths, starts, out, lse=None, status=None, stream=None):
         """q bf16 [rows, q_heads, dim], out the same in bf16 (may be q) or fp32; table int32 [requests,
         max_pages], lengths int32 [requests], starts int32 [requests + 1] as cache_tables writes them;
         lse fp32 [rows, q_heads] or None.  Rows behind the last request are left as they were."""
         d, c = self.d, self.cache
+        dev = c.device
         shape = (d.rows, d.q_heads, c.dim)
         kind = _OUT.get(out.dtype)
         # one test of all that holds in a correct call; what failed is looked up after
-        if not (kind is not None and q.dtype is _BF16 and q.shape == out.shape == shape and q.is_cuda and out.is_cuda
+        if not (kind is not None and q.dtype is _BF16 and q.shape == out.shape == shape and q.get_device() == dev
+                and out.get_device() == dev and dev == _current_device()
                 and q.is_contiguous() and out.is_contiguous() and table.dtype is _I32 and lengths.dtype is _I32
-                and starts.dtype is _I32 and table.is_cuda and lengths.is_cuda and starts.is_cuda
+                and starts.dtype is _I32 and table.get_device() == dev and lengths.get_device() == dev
+                and starts.get_device() == dev
                 and table.is_contiguous() and lengths.is_contiguous() and starts.is_contiguous()
                 and table.shape == (d.requests, d.max_pages) and lengths.shape == (d.requests,)
                 and starts.shape == (d.requests + 1,)
-                and (lse is None or lse.dtype is torch.float32 and lse.shape == shape[:2] and lse.is_cuda
-                     and lse.is_contiguous())):
+                and (lse is None or lse.dtype is torch.float32 and lse.shape == shape[:2]
+                     and lse.get_device() == dev and lse.is_contiguous())):
             _typed(q, _BF16, shape, "q")
             if kind is None:
                 raise TypeError(f"out: expected a float32 or bfloat16 tensor, got {out.dtype}")
@@ -276,10 +307,12 @@ class CacheAttention:
             _typed(table, _I32, (d.requests, d.max_pages), "table")
             _typed(lengths, _I32, (d.requests,), "lengths")
             _typed(starts, _I32, (d.requests + 1,), "starts")
-            _typed(lse, torch.float32, shape[:2], "lse")
+            if lse is not None:
+                _typed(lse, torch.float32, shape[:2], "lse")
+            raise ValueError(_ELSEWHERE)
         rc = lib().moe_cache_attention(d, c.c, q.data_ptr(), table.data_ptr(), lengths.data_ptr(),
                                        starts.data_ptr(), out.data_ptr(), kind, _at(lse), self.ws.data_ptr(),
-                                       self.ws_bytes, _word(status), _stream(stream))
+                                       self.ws_bytes, _word(status, dev), _stream(stream))
         if rc:
             _check(rc, "moe_cache_attention")
         return out
@@ -295,13 +328,15 @@ def w4_matvec(x, codes, scales, out, zeros=None, stream=None):
     kind, skind = _OUT.get(out.dtype), _OUT.get(scales.dtype)
     mx = scales.dtype is torch.uint8
     groups = scales.shape[-1]
+    dev = x.get_device()
     if not (kind is not None and (mx or skind is not None) and x.dtype is _BF16 and codes.dtype is torch.uint8
-            and x.is_cuda and codes.is_cuda and scales.is_cuda and out.is_cuda and x.is_contiguous()
+            and dev >= 0 and codes.get_device() == dev and scales.get_device() == dev and out.get_device() == dev
+            and dev == _current_device() and x.is_contiguous()
             and codes.is_contiguous() and scales.is_contiguous() and out.is_contiguous()
             and codes.shape == (N, K // 2) and out.shape == (T, N) and groups and K % groups == 0
             and scales.shape == (N, groups)
             and (zeros is None or not mx and zeros.dtype is torch.uint8 and zeros.shape == scales.shape
-                 and zeros.is_cuda and zeros.is_contiguous())):
+                 and zeros.get_device() == dev and zeros.is_contiguous())):
         _typed(x, _BF16, (T, K), "x")
         _typed(codes, torch.uint8, (N, K // 2), "codes")
         if kind is None:
@@ -316,6 +351,7 @@ def w4_matvec(x, codes, scales, out, zeros=None, stream=None):
             if mx:
                 raise ValueError("MXFP4 has no zero points")
             _typed(zeros, torch.uint8, (N, groups), "zeros")
+        raise ValueError(_ELSEWHERE)
     key = (N, K, W4_MX if mx else W4_INT, K // groups, OUT_F32 if mx else skind)
     d = _W4S.get(key)
     if d is None:
@@ -381,8 +417,8 @@ class AttentionBlock:
                  max_len=None, w_q=None, w_k=None, w_pre=None, w_post=None, gate=None, residual_scale=1.0,
                  branch_scale=1.0, eps=1e-6, kind=NORM_RMS, style=ROPE_HALVES, window=0, scale=None):
         self.cache, self.q_heads, self.hidden, self.cos_sin = cache, q_heads, hidden, cos_sin
-        self.requests, self.max_rows, self.max_pages = requests, max_rows, max_pages
-        self.plan_args = dict(max_q=max_q, max_len=max_len, window=window, scale=scale)
+        self.max_rows = max_rows
+        self.plan = CacheAttention(requests, max_rows, q_heads, cache, max_pages, max_q, max_len, window, scale)
         self.w_q, self.w_k, self.w_pre, self.w_post, self.gate = w_q, w_k, w_pre, w_post, gate
         self.eps, self.kind, self.style = eps, kind, style
         self.scales = dict(residual_scale=residual_scale, branch_scale=branch_scale)
@@ -398,7 +434,8 @@ class AttentionBlock:
             k = max(hidden, q_heads * D)
             self.xq = torch.empty(max_rows * k // 2, dtype=torch.uint8, device=dev)
             self.xs = torch.empty(max_rows * k // 32, dtype=torch.uint8, device=dev)
-            self.offsets = torch.zeros(2, dtype=_I32, device=dev)
+            self.offsets = torch.zeros(max_rows + 1, 4, dtype=_I32, device=dev)   # row T: 0, T
+            self.offsets[:, 1] = torch.arange(max_rows + 1, device=dev)
         self.qkv = torch.empty(max_rows, n_qkv, dtype=_BF16, device=dev)
         self.q = torch.zeros(max_rows, q_heads, D, dtype=_BF16, device=dev)
         self.status_word = torch.zeros(1, dtype=_I32, device=dev)
@@ -410,7 +447,7 @@ class AttentionBlock:
             return w4_matvec(x, *self.weights[which], out, stream=stream)
         xq, xs = self.xq[:T * k // 2].view(T, k // 2), self.xs[:T * k // 32].view(T, k // 32)
         mx4_quantize(x, xq, xs, stream)
-        mx4_grouped_gemm(1, n, k, T, xq, xs, self.offsets, *self.packed[which], out, OUT_BF16, self.status_word, stream)
+        mx4_grouped_gemm(1, n, k, T, xq, xs, self.offsets[T], *self.packed[which], out, OUT_BF16, self.status_word, stream)
         return out
 
     def pre(self, residual, x, stream=None):
@@ -430,14 +467,7 @@ class AttentionBlock:
             raise ValueError(f"{T} rows, and tables for {tables.slots.shape[0]}")
         plan = self._plans.get(T)
         if plan is None:
-            plan = self._plans[T] = CacheAttention(self.requests, T, self.q_heads, self.cache, self.max_pages,
-                                                   **self.plan_args)
-        if T > 16:
-            if stream is None:
-                self.offsets[1:].fill_(T)
-            else:
-                with torch.cuda.stream(stream):
-                    self.offsets[1:].fill_(T)
+            plan = self._plans[T] = self.plan.of_rows(T)
         qkv, q = self.qkv[:T], self.q[:T]
         self._project(0, x, qkv, stream)
         qk_norm_rope(qkv, tables.positions[:T], self.cos_sin, self.q_heads, self.cache.kv_heads, q, w_q=self.w_q,
