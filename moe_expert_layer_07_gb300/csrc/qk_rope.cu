@@ -253,13 +253,20 @@ int launch_qk_norm_rope(const moe_qk_rope *d, int T, const void *qkv, const int3
     const int heads = a.Hq + a.Hk + (cache ? a.Hk : 0);
     const bool pairs = d->style == MOE_ROPE_PAIRS;
     a.T = T;
-    // As many warps to a row as give an SM three times the warps that it holds (5001 rows of
-    // 40 heads of 64: 23 us with one to a row, two of which do not fit at once, 20 with two);
-    // where that leaves each a round, one head at a time.
+    // Warps to a row: what takes the least time where each wave of the warps that run at once takes
+    // 2.5 rounds to begin and end.  (5001 rows of 40 heads of 64: 19.0, 16.8, 17.6 and 25 us with 1,
+    // 2, 3 and 10; 1000 rows: 8.2, 6.4, 5.8, 4.8, 5.9 and 6.5 with 1, 2, 3, 4, 5 and 10.)  Two heads of a
+    // lane's at a time where there are many rounds and waves (8192 rows of 80 heads of 128: 60 us for
+    // 68), one elsewhere (5001 rows: 16.8 for 20.3; 2048 rows of 80 heads of 128: 24.2 for 26.4).
     const int at_once = 32 / (d->dim / 8);
     const int most = (int)ceil_div(heads, at_once);
-    a.parts = (int)std::max<int64_t>(1, std::min<int64_t>(most, (int64_t)sm_count() * 96 / T));
-    const bool one = a.parts * 2 > most;
+    const int64_t warps = (int64_t)sm_count() * 32;
+    int64_t least = INT64_MAX;
+    for (int p = 1; p <= std::min(most, 256); ++p) {
+        const int64_t time = ceil_div((int64_t)T * p, warps) * (2 * ceil_div(most, p) + 5);
+        if (time < least) least = time, a.parts = p;
+    }
+    const bool one = T <= warps || ceil_div(most, a.parts) < 12;
     auto go = [&](auto kern) {
         return launch_dependent(kern, dim3((unsigned)ceil_div((int64_t)T * a.parts, kRopeThreads / 32)), dim3(kRopeThreads), 0, s,
                                 (const RopeArgs)a);
