@@ -69,13 +69,9 @@ __device__ __forceinline__ void store4(uint16_t *p, const F2 (&v)[2]) {
                  "r"(*reinterpret_cast<const uint32_t *>(&a)), "r"(*reinterpret_cast<const uint32_t *>(&b))
                  : "memory");
 }
-__device__ __forceinline__ void load_w(const void *w, int f32, int ch, F2 (&v)[2]) {
-    if (f32) {
-        const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const float *>(w) + ch);
-        v[0] = ptx::pack2(a.x, a.y), v[1] = ptx::pack2(a.z, a.w);
-    } else {
-        unpack4(*reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(w) + ch), v);
-    }
+__device__ __forceinline__ void load_w(const float *w, F2 (&v)[2]) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(w);
+    v[0] = ptx::pack2(a.x, a.y), v[1] = ptx::pack2(a.z, a.w);
 }
 __device__ __forceinline__ uint32_t magnitude(const F2 (&v)[2]) {   // the largest of four
     const uint32_t k = 0x7fffffffu;
@@ -87,21 +83,32 @@ __device__ __forceinline__ uint32_t magnitude(const F2 (&v)[2]) {   // the large
 template <int D, bool PAIRS, int U>
 __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopeArgs a) {
     constexpr int N8 = D / 8, kHeads = 32 / N8;   // lanes of a head, heads of a warp at a time
+    static_assert(kRopeThreads >= 2 * D, "a thread to a weight");
+    __shared__ __align__(16) float s_w[2][D];
     const int lane = threadIdx.x & 31, c = lane % N8, g = lane / N8;
     const int64_t job = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
     const int64_t t = job / a.parts;
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
-    if (t >= a.T) return;
     const int heads = a.Hq + a.Hk + (a.codes ? a.Hk : 0), keyed = a.Hq + a.Hk;
     // This lane's channels: two fours, of which the second is the first one's partner
     // where pairs are half a rotation apart (no shuffles); of values eight neighbours.
     const bool turned = c < a.R / 8, split = !PAIRS && turned;
     const int ch_a = split ? 4 * c : 8 * c, ch_b = split ? a.R / 2 + 4 * c : 8 * c + 4;
-    const uint16_t *row = a.qkv + t * a.stride;
+    const bool there = t < a.T;
+    const uint16_t *row = a.qkv + (there ? t * a.stride : 0);
     const int first = (int)(job - t * a.parts) * kHeads * U, step = a.parts * kHeads * U;
     uint2 raw[U][2];
+    const uint16_t *from_a = row + g * D + ch_a, *from_b = row + g * D + ch_b;
     auto load = [&](int h0) {
+        if (h0 + U * kHeads <= keyed) {   // no values
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                raw[u][0] = load_once(from_a + h0 * D + u * kHeads * D);
+                raw[u][1] = load_once(from_b + h0 * D + u * kHeads * D);
+            }
+            return;
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int h = h0 + u * kHeads + g;
@@ -113,12 +120,17 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopeArgs
             }
         }
     };
-    load(first);   // before what the position is waited for
+    if (there) load(first);   // before what the position is waited for
+    // the norms' weights, where registers would not hold them
+    if (a.w_q || a.w_k) {
+        const int i = threadIdx.x % D, k = threadIdx.x / D;
+        const void *w = k ? a.w_k : a.w_q;
+        if (k < 2 && w) s_w[k][i] = a.w_f32 ? static_cast<const float *>(w)[i] : __uint_as_float((uint32_t)static_cast<const uint16_t *>(w)[i] << 16);
+        __syncthreads();
+    }
+    if (!there) return;
     const int pos = a.R ? a.positions[t] : 0;
     const int slot = a.codes ? a.slots[t] : -1;
-    F2 wq[2][2], wk[2][2];
-    if (a.w_q) load_w(a.w_q, a.w_f32, ch_a, wq[0]), load_w(a.w_q, a.w_f32, ch_b, wq[1]);
-    if (a.w_k) load_w(a.w_k, a.w_f32, ch_a, wk[0]), load_w(a.w_k, a.w_f32, ch_b, wk[1]);
     if (pos < 0 || (a.R && pos >= a.max_positions) || slot < -1 || slot >= a.slots_in_cache) {
         if (lane == 0 && a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
         return;   // the warp
@@ -143,21 +155,19 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopeArgs
     const int64_t at = a.codes ? (((int64_t)(slot >> a.page_shift) * 2 * a.Hk) << a.page_shift) +
                                      (slot & ((1 << a.page_shift) - 1))
                                : 0;
-    // every thread of a warp goes through the same rounds: shuffles inside
-    for (int h0 = first; h0 < heads; h0 += step) {
-        uint2 now[U][2];
-#pragma unroll
-        for (int u = 0; u < U; ++u) now[u][0] = raw[u][0], now[u][1] = raw[u][1];
-        load(h0 + step);
+    uint16_t *const q_row = a.q_out + (t * a.Hq + g) * D;
+    // U heads of this lane's; all of the warp's are queries, or any
+    auto heads_of = [&](int h0, const uint2 (&now)[U][2], auto only_queries) {
+        constexpr bool kQ = decltype(only_queries)::value;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int h = h0 + u * kHeads + g;
-            if (h0 + u * kHeads >= heads) break;   // the warp
-            const bool is_v = h >= keyed, is_k = !is_v && h >= a.Hq;
+            if (!kQ && h0 + u * kHeads >= heads) break;   // the warp
+            const bool is_v = !kQ && h >= keyed, is_k = !kQ && !is_v && h >= a.Hq;
             F2 x[2], y[2];
             unpack4(now[u][0], x);
             unpack4(now[u][1], y);
-            if (a.w_q || a.w_k) {
+            if (a.w_q || (!kQ && a.w_k)) {
                 F2 s2 = mul2(x[0], x[0]);
                 s2 = ptx::fma2(x[1], x[1], s2);
                 s2 = ptx::fma2(y[0], y[0], s2);
@@ -167,13 +177,12 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopeArgs
                 for (int o = N8 / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 const float inv = rsqrtf(sum * (1.0f / D) + a.eps);
                 const F2 i2 = pair(inv, inv);
-                if (h < a.Hq) {
-                    if (a.w_q)
+                const bool of_q = kQ || h < a.Hq;
+                if (!is_v && (of_q ? a.w_q : a.w_k)) {
+                    F2 w[2][2];
+                    load_w(s_w[of_q ? 0 : 1] + ch_a, w[0]), load_w(s_w[of_q ? 0 : 1] + ch_b, w[1]);
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) x[j] = mul2(mul2(x[j], i2), wq[0][j]), y[j] = mul2(mul2(y[j], i2), wq[1][j]);
-                } else if (is_k && a.w_k) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) x[j] = mul2(mul2(x[j], i2), wk[0][j]), y[j] = mul2(mul2(y[j], i2), wk[1][j]);
+                    for (int j = 0; j < 2; ++j) x[j] = mul2(mul2(x[j], i2), w[0][j]), y[j] = mul2(mul2(y[j], i2), w[1][j]);
                 }
             }
             if (turned && !is_v) {
@@ -189,7 +198,12 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopeArgs
                     }
                 }
             }
-            uint16_t *dst = h < a.Hq ? a.q_out + (t * a.Hq + h) * D : is_k && a.k_out ? a.k_out + (t * a.Hk + h - a.Hq) * D : nullptr;
+            if (kQ) {
+                uint16_t *const dst = q_row + h0 * D + u * kHeads * D;
+                store4(dst + ch_a, x), store4(dst + ch_b, y);
+                continue;
+            }
+            uint16_t *dst = h < a.Hq ? q_row + (h0 + u * kHeads) * D : is_k && a.k_out ? a.k_out + (t * a.Hk + h - a.Hq) * D : nullptr;
             if (dst) store4(dst + ch_a, x), store4(dst + ch_b, y);
             if (a.codes && h0 + (u + 1) * kHeads > a.Hq) {   // the warp: some of these heads are cached
                 // the blocks that this lane's channels are in, and their largest magnitudes
@@ -218,6 +232,15 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopeArgs
                 }
             }
         }
+    };
+    // every thread of a warp goes through the same rounds: shuffles inside
+    for (int h0 = first; h0 < heads; h0 += step) {
+        uint2 now[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) now[u][0] = raw[u][0], now[u][1] = raw[u][1];
+        load(h0 + step);
+        if (h0 + U * kHeads <= a.Hq) heads_of(h0, now, std::true_type());
+        else heads_of(h0, now, std::false_type());
     }
 }
 
