@@ -110,8 +110,10 @@ __device__ __forceinline__ uint32_t add_half2(uint32_t a, uint32_t b) {
 // fragments follow: 1024 + c - (1024 + z), and (1024 + 16 c) / 16 - (64 + z).
 struct Zero {
     uint32_t one, sixteen;   // -(1024 + z), -(64 + z), twice each
-    __device__ __forceinline__ explicit Zero(uint32_t z)
-        : one((0xe400u + z) * 0x10001u), sixteen((0xd400u + (z << 4)) * 0x10001u) {}
+    __device__ __forceinline__ Zero(uint32_t z4, int b) {   // byte b of four
+        one = __byte_perm(z4, 0xe4u, 0x4040 + 0x101 * b);
+        sixteen = __byte_perm(z4 << 4, 0xd4u, 0x4040 + 0x101 * b);
+    }
 };
 // Constants that stay in registers: an instruction has room for one immediate.
 struct IntBits {
@@ -205,11 +207,20 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
                         cp_async16(dst + to + i * kItemBytes + 512, src + half_w + i * 64);
                     }
                 if (word0 < words) cp_async4(dst_s + to, src_s, 4);
-                for (int word = 2; word < words; word += 2)
-                    if (word + word0 < words) cp_async4(dst_s + to + 4 * word, src_s + 4 * word, 4);
-                if (INT)
-                    for (int word = 0; word < a.zero_words; word += 2)
+                if (KIND == kIntBlocks) {   // up to 9 words of scales, 3 of zero points
+#pragma unroll
+                    for (int word = 2; word < 10; word += 2)
+                        if (word + word0 < words) cp_async4(dst_s + to + 4 * word, src_s + 4 * word, 4);
+#pragma unroll
+                    for (int word = 0; word < 4; word += 2)
                         if (word + word0 < a.zero_words) cp_async4(dst_z + to + 4 * word, src_z + 4 * word, 4);
+                } else {                    // mostly one, and one
+                    for (int word = 2; word < words; word += 2)
+                        if (word + word0 < words) cp_async4(dst_s + to + 4 * word, src_s + 4 * word, 4);
+                    if (INT)
+                        for (int word = 0; word < a.zero_words; word += 2)
+                            if (word + word0 < a.zero_words) cp_async4(dst_z + to + 4 * word, src_z + 4 * word, 4);
+                }
             } else {
                 const bool lo = n_next + row_a < a.N, hi = n_next + row_a + 8 < a.N;
 #pragma unroll 1
@@ -237,15 +248,20 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
         cp_async_commit();
         to = to == (kStages - 1) * kStage ? 0 : to + kStage;
     };
-    // Where the strips of rows g and g + 8 begin in a stage
-    int strip_s[2], strip_z[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int n = cluster * kTileRows + g + 8 * r;
-        const uint32_t at = (uint32_t)n * groups + group0;   // its low bits
-        strip_s[r] = kStrips + (g + 8 * r) * kScaleStrip + (INT ? (int)(at * (a.s_f32 ? 4 : 2) & 3) : 0);
-        strip_z[r] = kStrips + kTileRows * kScaleStrip + (g + 8 * r) * kZeroStrip + (int)(at & 3);
-    }
+    constexpr int kZeros = kStrips + kTileRows * kScaleStrip;
+    // Where row r's strips begin in a stage
+    auto strip_of = [&](int r, int &scales, int &zeros) {
+        const uint32_t at = (uint32_t)(cluster * kTileRows + r) * groups + group0;   // its low bits
+        scales = kStrips + r * kScaleStrip + (int)(at * (a.s_f32 ? 4 : 2) & 3);
+        zeros = kZeros + r * kZeroStrip + (int)(at & 3);
+    };
+    int strip_s[2], strip_z[2];   // of rows g and g + 8, or of the row whose groups this lane makes numbers of
+    strip_of(KIND == kIntBlocks ? lane >> 1 : g, strip_s[0], strip_z[0]);
+    strip_of(KIND == kIntBlocks ? lane >> 1 : g + 8, strip_s[1], strip_z[1]);
+    auto group_scale = [&](const uint8_t *strip, int gi) {
+        return a.s_f32 ? reinterpret_cast<const float *>(strip)[gi]
+                       : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(strip)[gi] << 16);
+    };
     const IntBits bits;
     if (ranks > 1) cluster_arrive_relaxed();
     ptx::pdl_launch_dependents();
@@ -332,7 +348,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
         cp_async_wait<kStages - 2>();
         __syncwarp();
         fetch();
-        const uint8_t *stage = ring + from;
+        uint8_t *stage = ring + from;
         const uint32_t slot = ring_addr + from;
         from = from == (kStages - 1) * kStage ? 0 : from + kStage;
         const int n0 = (cluster + it * clusters) * kTileRows;
@@ -357,33 +373,48 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
             }
             __syncwarp();
         }
+        if (KIND == kIntBlocks) {
+            // The same for integers, into the strips' places: scales as fp32, zero points as bytes.
+            // (For the one group of a slice it took as long as forming them where they are used.)
+            const int row = lane >> 1, half = lane & 1, per = kSlice >> a.group_shift;   // groups of a slice: 2 or 4
+            float f[S][2];
+            uint32_t z[S][2];
+#pragma unroll
+            for (int i = 0; i < S; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int gi = i * per + (per == 4 ? 2 * half + x : half);
+                    const bool there = group0 + gi < groups;
+                    f[i][x] = there ? group_scale(stage + strip_s[0], gi) : 0.0f;
+                    z[i][x] = a.zeros && there ? stage[strip_z[0] + gi] & 15u : 8u;
+                }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                *reinterpret_cast<float2 *>(stage + kStrips + row * kScaleStrip + 16 * i + 8 * half) = make_float2(f[i][0], f[i][1]);
+                *reinterpret_cast<uint16_t *>(stage + kZeros + row * kZeroStrip + 4 * i + 2 * half) = (uint16_t)(z[i][0] | z[i][1] << 8);
+            }
+            __syncwarp();
+        }
 #pragma unroll
         for (int i = 0; i < S; ++i) {
             // scales (and zero points) of rows g and g + 8, for the four blocks of 32 or the slice
             constexpr int kB = KIND == kIntSlice ? 1 : 4;
             float sc[2][kB];
-            uint32_t zp[2][kB];
+            uint32_t zp[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                if (KIND == kMx) {
-                    const float4 f = *reinterpret_cast<const float4 *>(s_scale + i * 64 + (g + 8 * r) * 4);
-                    sc[r][0] = f.x, sc[r][1 % kB] = f.y, sc[r][2 % kB] = f.z, sc[r][3 % kB] = f.w;
+                const int row = g + 8 * r;
+                if (KIND == kIntSlice) {
+                    const bool there = group0 + i < groups;
+                    sc[r][0] = there ? group_scale(stage + strip_s[r], i) : 0.0f;
+                    zp[r] = a.zeros && there ? stage[strip_z[r] + i] & 15u : 8u;
                 } else {
-                    const uint8_t *strip = stage + strip_s[r], *zs = stage + strip_z[r];
-                    const int per = KIND == kIntSlice ? 1 : kSlice >> a.group_shift;   // groups of a slice: 1, or 2 or 4
-#pragma unroll
-                    for (int b = 0; b < kB; ++b) {
-                        if (b == 0 || b == 2 || per == 4) {
-                            const int gi = i * per + (per == 4 ? b : b >> 1);
-                            const bool there = group0 + gi < groups;
-                            sc[r][b] = !there ? 0.0f
-                                       : a.s_f32 ? reinterpret_cast<const float *>(strip)[gi]
-                                                 : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(strip)[gi] << 16);
-                            zp[r][b] = a.zeros && there ? zs[gi] & 15u : 8u;
-                        } else {
-                            sc[r][b] = sc[r][(b + kB - 1) % kB], zp[r][b] = zp[r][(b + kB - 1) % kB];
-                        }
-                    }
+                    const float *fs = INT ? reinterpret_cast<const float *>(stage + kStrips + row * kScaleStrip) + 4 * i
+                                          : s_scale + i * 64 + row * 4;
+                    const float4 f = *reinterpret_cast<const float4 *>(fs);
+                    sc[r][0] = f.x, sc[r][1 % kB] = f.y, sc[r][2 % kB] = f.z, sc[r][3 % kB] = f.w;
+                    if (INT) zp[r] = *reinterpret_cast<const uint32_t *>(stage + kZeros + row * kZeroStrip + 4 * i);
                 }
             }
             float d[NQ][4];
@@ -396,8 +427,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
                     const int b = 2 * x + y;
                     uint32_t w0[4], w1[4];
                     if (INT) {
-                        widen_ints(w[2 * y], bits, Zero(zp[0][b % kB]), w0);
-                        widen_ints(w[2 * y + 1], bits, Zero(zp[1][b % kB]), w1);
+                        widen_ints(w[2 * y], bits, Zero(zp[0], b % kB), w0);
+                        widen_ints(w[2 * y + 1], bits, Zero(zp[1], b % kB), w1);
                     } else {
                         mx4_half8(w[2 * y], w0);
                         mx4_half8(w[2 * y + 1], w1);
