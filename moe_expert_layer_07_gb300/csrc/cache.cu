@@ -10,7 +10,13 @@
 // Bound by latency: a step's tables are some kilobytes.  Each CTA of one
 // cluster sums all of the requests itself (no sums to pass on) and writes its
 // share of the tokens and pages, after a barrier of the cluster: by then every
-// CTA has read what outputs may replace (held, the free range).
+// CTA has read what outputs may replace (held, the free range).  Eight requests
+// take 4.6 us in a graph (8.3 where each call is the host's), 1000 that decode or have up to 96
+// new tokens 6.4.
+// One CTA up to 4096 token rows, eight above.
+//
+// cache_read: a thread to 16 bytes of output; bound by memory, 3 us for the 5001 rows of 4 heads of
+// 64 that a prompt writes.
 #include <cuda_bf16.h>
 
 #include <algorithm>
