@@ -17,8 +17,8 @@
 // binades below E counts as zero.  Keys: 2^E goes into the row's factor.
 // Values: where E grows, O is scaled when P is made.  q is fp16 times a power of
 // two for each row.  m is raised only where a score passes it by 8 (in log2), so
-// S is read once and O hardly ever; it rises by whole powers of two.  A value that is NaN counts as zero in the
-// products; rows that give it weight remember its block.
+// S is read once and O hardly ever; it rises by whole powers of two.  A value that is
+// NaN counts as zero in the products; rows that give it weight remember its block.
 //
 // Work: one unit for each tile of tokens that a group of 256 rows sees (causal:
 // fewer for earlier rows) and some for its beginning and end; each CTA takes as
@@ -31,7 +31,8 @@
 // one half's S to its P (four rounds of load, exponentials, conversion, store: some
 // 3000 cycles of latency) against 1024 cycles of the other half's products: tensor
 // memory is full (two S of 128 columns, two O), so there is no third tile to work on
-// meanwhile.
+// meanwhile.  (P in shared memory would free S sooner, but with both operands there
+// products of 128 columns read 128 bytes a clock, all that it has.)
 //
 // Tiles of 64 tokens with two S each were slower (products of 64 columns take as long
 // as of 128: 1.50 ms for 1.36), and so were 16 softmax warps with half a row to a thread
