@@ -65,13 +65,13 @@ def _typed(t, dtype, shape, name):
     return _dense(t, shape, name)
 
 
+# torch's raw queries, as in __init__.py; the public ones cost microseconds of a small call
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 _ELSEWHERE = "expected tensors of one device, the current one"
 
 
 def _word(status, dev):
-    if status is None:
-        return None
     if status.dtype is not _I32 or status.numel() < 1 or status.get_device() != dev:
         raise TypeError("status: expected an int32 CUDA tensor on the others' device")
     return status.data_ptr()
@@ -135,7 +135,8 @@ def cache_tables(held, new_tokens, free_pages, free_range, page, table, lengths,
     for t in (held, new_tokens, free_pages, table, lengths, starts, slots, positions):
         good = good and t.dtype is _I32 and t.get_device() == dev and t.is_contiguous()
     if not (good and free_range.dtype is i64 and free_out.dtype is i64 and dev == free_range.get_device()
-            and dev == free_out.get_device() and dev == _current_device() and free_range.is_contiguous() and free_out.is_contiguous() and free_range.shape == free_out.shape == (2,)
+            and dev == free_out.get_device() and dev == _current_device() and free_range.is_contiguous()
+            and free_out.is_contiguous() and free_range.shape == free_out.shape == (2,)
             and held.shape == new_tokens.shape == lengths.shape == (B,) and table.shape == (B, w)
             and starts.shape == (B + 1,) and slots.shape == positions.shape == (n,)
             and free_pages.shape == (f,)):
@@ -147,10 +148,12 @@ def cache_tables(held, new_tokens, free_pages, free_range, page, table, lengths,
         _typed(free_range, i64, (2,), "free_range")
         _typed(free_out, i64, (2,), "free_out")
         raise ValueError(_ELSEWHERE)
+    word = None if status is None else _word(status, dev)
+    s = _raw_stream(dev) if stream is None else _stream(stream)
     rc = lib().moe_cache_tables(B, page, held.data_ptr(), new_tokens.data_ptr(), free_pages.data_ptr(), f,
                                 free_range.data_ptr(), table.data_ptr(), w, lengths.data_ptr(),
                                 starts.data_ptr(), slots.data_ptr(), positions.data_ptr(), n,
-                                free_out.data_ptr(), _word(status, dev), _stream(stream))
+                                free_out.data_ptr(), word, s)
     if rc:
         _check(rc, "moe_cache_tables")
 
@@ -171,11 +174,13 @@ def qk_norm_rope(qkv, positions, cos_sin, q_heads, kv_heads, q_out, k_out=None, 
     # one test of all that holds in a correct call; what failed is looked up after
     dev = qkv.get_device()
     good = (pkind is not None and qkv.dtype is _BF16 and q_out.dtype is _BF16 and dev >= 0
-            and q_out.get_device() == dev and dev == _current_device() and qkv.dim() == 2 and qkv.stride(1) == 1 and qkv.shape[1] >= (q_heads + 2 * kv_heads) * dim
+            and q_out.get_device() == dev and dev == _current_device() and qkv.dim() == 2 and qkv.stride(1) == 1
+            and qkv.shape[1] >= (q_heads + 2 * kv_heads) * dim
             and q_out.shape == (T, q_heads, dim) and q_out.is_contiguous() and (cache is None) == (slots is None))
     for w in (w_q, w_k):
         if w is not None:
-            good = good and w.dtype is param.dtype and w.shape == (dim,) and w.get_device() == dev and w.is_contiguous()
+            good = (good and w.dtype is param.dtype and w.shape == (dim,) and w.get_device() == dev
+                    and w.is_contiguous())
     if k_out is not None:
         good = (good and k_out.dtype is _BF16 and k_out.shape == (T, kv_heads, dim)
                 and k_out.get_device() == dev and k_out.is_contiguous())
@@ -195,9 +200,11 @@ def qk_norm_rope(qkv, positions, cos_sin, q_heads, kv_heads, q_out, k_out=None, 
         if len(_ROPES) >= 256:
             _ROPES.clear()
         d = _ROPES[key] = _Rope(*key)
+    word = None if status is None else _word(status, dev)
+    s = _raw_stream(dev) if stream is None else _stream(stream)
     rc = lib().moe_qk_norm_rope(d, T, qkv.data_ptr(), _at(positions), _at(cos_sin) if rot else None, _at(w_q),
                                 _at(w_k), q_out.data_ptr(), _at(k_out), None if cache is None else cache.c,
-                                _at(slots), _word(status, dev), _stream(stream))
+                                _at(slots), word, s)
     if rc:
         _check(rc, "moe_qk_norm_rope")
 
@@ -247,7 +254,9 @@ def cache_read(cache: Cache4, slots, k=None, v=None, status=None, stream=None):
             if t is not None:
                 _typed(t, _BF16, shape, name)
         raise ValueError(_ELSEWHERE)
-    rc = lib().moe_cache_read(cache.c, n, slots.data_ptr(), _at(k), _at(v), _word(status, dev), _stream(stream))
+    word = None if status is None else _word(status, dev)
+    s = _raw_stream(dev) if stream is None else _stream(stream)
+    rc = lib().moe_cache_read(cache.c, n, slots.data_ptr(), _at(k), _at(v), word, s)
     if rc:
         _check(rc, "moe_cache_read")
 
@@ -310,9 +319,11 @@ class CacheAttention:
             if lse is not None:
                 _typed(lse, torch.float32, shape[:2], "lse")
             raise ValueError(_ELSEWHERE)
+        word = None if status is None else _word(status, dev)
+        s = _raw_stream(dev) if stream is None else _stream(stream)
         rc = lib().moe_cache_attention(d, c.c, q.data_ptr(), table.data_ptr(), lengths.data_ptr(),
                                        starts.data_ptr(), out.data_ptr(), kind, _at(lse), self.ws.data_ptr(),
-                                       self.ws_bytes, _word(status, dev), _stream(stream))
+                                       self.ws_bytes, word, s)
         if rc:
             _check(rc, "moe_cache_attention")
         return out
@@ -358,8 +369,9 @@ def w4_matvec(x, codes, scales, out, zeros=None, stream=None):
         if len(_W4S) >= 256:
             _W4S.clear()
         d = _W4S[key] = _W4(*key)
+    s = _raw_stream(dev) if stream is None else _stream(stream)
     rc = lib().moe_w4_matvec(d, T, x.data_ptr(), codes.data_ptr(), scales.data_ptr(), _at(zeros),
-                             out.data_ptr(), kind, _stream(stream))
+                             out.data_ptr(), kind, s)
     if rc:
         _check(rc, "moe_w4_matvec")
     return out
@@ -447,7 +459,8 @@ class AttentionBlock:
             return w4_matvec(x, *self.weights[which], out, stream=stream)
         xq, xs = self.xq[:T * k // 2].view(T, k // 2), self.xs[:T * k // 32].view(T, k // 32)
         mx4_quantize(x, xq, xs, stream)
-        mx4_grouped_gemm(1, n, k, T, xq, xs, self.offsets[T], *self.packed[which], out, OUT_BF16, self.status_word, stream)
+        mx4_grouped_gemm(1, n, k, T, xq, xs, self.offsets[T], *self.packed[which], out, OUT_BF16, self.status_word,
+                         stream)
         return out
 
     def pre(self, residual, x, stream=None):

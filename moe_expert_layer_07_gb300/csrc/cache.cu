@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kTabThreads) cache_tables_kernel(const TabArgs
     ptx::pdl_wait();
     const int64_t next = a.free_range[0], end = a.free_range[1];
     bool bad = false, full = false;
-    int64_t tokens = 0, pages = 0;   // of the requests before this round
+    int64_t tokens = 0, pages = 0;   // of the requests before these
     for (int b0 = 0; b0 < a.B; b0 += kTabThreads) {
         const int b = b0 + tid;
         int held = 0, fresh = 0, had = 0, want = 0;
