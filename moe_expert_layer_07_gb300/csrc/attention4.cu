@@ -31,8 +31,8 @@
 // results in the workspace (at most two a CTA), which a second kernel joins.
 //
 // Measured (cold): 48 requests of 64 to 16384 tokens, 64 query heads on 8 of 128, 64.2 us (3.5 TB/s
-// of the cache); two of 131073 with three query tokens, 40 heads on 8, 101.6 (2.8 TB/s); one of
-// 4097 tokens 13.7, two thirds of it launches, the way to the first tokens and the join.
+// of the cache); two of 131073 with three query tokens, 40 heads on 8, 98 (2.9 TB/s); one of
+// 4097 tokens 11.4, two thirds of it launches, the way to the first tokens and the join.
 // What bounds the large ones is the unpacking: 370 instructions a warp for 16 tokens
 // of 128 channels, the integer pipe (which converts, at half rate) busy 51%, issue 57%, and
 // 14% of the time CTAs that are done early.
@@ -51,7 +51,7 @@ namespace {
 constexpr int kThreads = kAttnWarps * 32;
 // What the beginning and end of a piece cost, in units: queries, the first tiles'
 // way from memory, the warps' sums.  Measured with 2, 4, 8 and 14: one request of
-// 4097 tokens 16.7, 17.0, 13.7 and 13.7 us, 48 of 64 to 16384 tokens 81, 65.6, 65.9
+// 4097 tokens 16.7, 17.0, 13.7 and 13.7 us (then), 48 of 64 to 16384 tokens 81, 65.6, 65.9
 // and 74 us.
 constexpr int kPieceUnits = 8;
 constexpr float kLazy = 8.0f;      // how far scores may pass the maximum
@@ -692,13 +692,14 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
     }
 }
 
-// One block: eight rows of what CTA blockIdx.x began.  A warp takes every eighth
-// partial result for all of the rows, or one row where there are few (four at most: 48 requests'
-// join 7.5 us -> 6, that of prompts 33 -> 20).
-constexpr int kJoinRows = 8, kShortJoin = 4;
+// One block: eight rows of what CTA blockIdx.x began.  A warp takes one of them, eight
+// partial results on their way at a time; where there are more than 32, every eighth for
+// all of the rows.  (All ways like that: one request 13.9 us for 11.4, two long ones 101.8
+// for 98, 48 requests, mostly of two partial results, 64.3 for 64.9.)
+constexpr int kJoinRows = 8, kShortJoin = 32, kJoinAhead = 8;
 
 template <int D>
-__global__ void __launch_bounds__(256) attention4_join_kernel(const AttnArgs a, int rows_at_once) {
+__global__ void __launch_bounds__(256, 3) attention4_join_kernel(const AttnArgs a, int rows_at_once) {
     constexpr int V = D / 32;   // channels of a lane
     __shared__ float s_top[8][kJoinRows], s_sum[8][kJoinRows];
     __shared__ __align__(16) float s_o[8][kJoinRows][D];
@@ -710,32 +711,39 @@ __global__ void __launch_bounds__(256) attention4_join_kernel(const AttnArgs a, 
     const int parts = cut.last - k0 + 1;
     const int64_t size = (int64_t)rows_at_once * (D + 2);
     auto part = [&](int j) { return a.part + (2 * (int64_t)(k0 + j) + (j == 0)) * size; };
-    if (parts <= kShortJoin) {   // a warp to a row
+    if (parts <= kShortJoin) {   // a warp to a row, a lane to each partial's maximum and sum
         const int rr = r0 + warp;
         if (rr >= cut.nrows) return;
-        const float *p = part(min(lane, parts - 1)) + rows_at_once * D + rr;
-        float top = p[0], l = lane < parts ? p[rows_at_once] : 0.0f;
-        const float mine = top;
-        float4 y[kShortJoin];
+        const bool mine = lane < parts, writes = lane < D / 4;
+        float4 y[kJoinAhead];
+        auto load = [&](int j0) {
 #pragma unroll
-        for (int j = 0; j < kShortJoin; ++j)
-            if (j < parts && lane < D / 4) y[j] = *reinterpret_cast<const float4 *>(part(j) + (int64_t)rr * D + 4 * lane);
+            for (int j = 0; j < kJoinAhead; ++j)
+                if (j0 + j < parts && writes) y[j] = *reinterpret_cast<const float4 *>(part(j0 + j) + (int64_t)rr * D + 4 * lane);
+        };
+        load(0);
+        const float *p = part(mine ? lane : 0) + rows_at_once * D + rr;
+        const float m = mine ? p[0] : -INFINITY;
+        float l = mine ? p[rows_at_once] : 0.0f, top = m;
 #pragma unroll
-        for (int x = 1; x < kShortJoin; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        const float f = mine == top ? 1.0f : ex2(mine - top);
+        for (int x = 1; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float f = m == top ? 1.0f : ex2(m - top);
         l *= f;
 #pragma unroll
-        for (int x = 1; x < kShortJoin; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+        for (int x = 1; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+        for (int j0 = 0; j0 < parts; j0 += kJoinAhead) {
 #pragma unroll
-        for (int j = 0; j < kShortJoin; ++j) {
-            const float fj = __shfl_sync(0xffffffffu, f, j);
-            if (j < parts && lane < D / 4) v.x += fj * y[j].x, v.y += fj * y[j].y, v.z += fj * y[j].z, v.w += fj * y[j].w;
+            for (int j = 0; j < kJoinAhead; ++j) {
+                const float fj = __shfl_sync(0xffffffffu, f, (j0 + j) & 31);
+                if (j0 + j < parts && writes) v.x += fj * y[j].x, v.y += fj * y[j].y, v.z += fj * y[j].z, v.w += fj * y[j].w;
+            }
+            load(j0 + kJoinAhead);
         }
-        l = __shfl_sync(0xffffffffu, l, 0), top = __shfl_sync(0xffffffffu, top, 0);
         const int row = cut.rowbase + rr;
         const int64_t at = (int64_t)(cut.row0 + row / a.G) * a.Hq + cut.head0 + row % a.G;
-        if (lane < D / 4) write4(a, at * D + 4 * lane, v, l == 0.0f ? 0.0f : 1.0f / l);
+        if (writes) write4(a, at * D + 4 * lane, v, l == 0.0f ? 0.0f : 1.0f / l);
         if (a.lse && lane == 0) a.lse[at] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718f;
         return;
     }
