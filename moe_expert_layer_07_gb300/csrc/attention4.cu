@@ -30,9 +30,9 @@
 // the requests' lengths.  A request that is cut between CTAs leaves partial
 // results in the workspace (at most two a CTA), which a second kernel joins.
 //
-// Measured (cold): 48 requests of 64 to 16384 tokens, 64 query heads on 8 of 128, 64.2 us (3.5 TB/s
-// of the cache); two of 131073 with three query tokens, 40 heads on 8, 98 (2.9 TB/s); one of
-// 4097 tokens 11.4, two thirds of it launches, the way to the first tokens and the join.
+// Measured (cold): 48 requests of 64 to 16384 tokens, 64 query heads on 8 of 128, 58.4 us (3.8 TB/s
+// of the cache); two of 131073 with three query tokens, 40 heads on 8, 97.6 (2.9 TB/s); one of
+// 4097 tokens 11.2, two thirds of it launches, the way to the first tokens and the join.
 // What bounds the large ones is the unpacking: 370 instructions a warp for 16 tokens
 // of 128 channels, the integer pipe (which converts, at half rate) busy 51%, issue 57%, and
 // 14% of the time CTAs that are done early.
@@ -50,10 +50,9 @@ namespace {
 
 constexpr int kThreads = kAttnWarps * 32;
 // What the beginning and end of a piece cost, in units: queries, the first tiles'
-// way from memory, the warps' sums.  Measured with 2, 4, 8 and 14: one request of
-// 4097 tokens 16.7, 17.0, 13.7 and 13.7 us (then), 48 of 64 to 16384 tokens 81, 65.6, 65.9
-// and 74 us.
-constexpr int kPieceUnits = 8;
+// way from memory, the warps' sums.  Measured with 3, 4, 5, 6 and 8: 48 requests of 64
+// to 16384 tokens 63.9, 58.4, 58.7, 60.0 and 62.0 us.
+constexpr int kPieceUnits = 4;
 constexpr float kLazy = 8.0f;      // how far scores may pass the maximum
 constexpr int kVBias = 7;          // P is scaled by 2^(e - E + kVBias)
 
@@ -234,35 +233,57 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
     ptx::pdl_launch_dependents();
     ptx::pdl_wait();
     plan_units(a, S::kRows, s_first, s_warp);
-    const int all = s_first[a.B], per = max(1, (all + (int)gridDim.x - 1) / (int)gridDim.x);
+    // (as many units as a warp's tiles at a time: fewer take as long)
+    const int all = s_first[a.B], per = max(S::kTiles, (all + (int)gridDim.x - 1) / (int)gridDim.x);
     if (tid == 0) a.cuts[blockIdx.x].nrows = 0;
     int u = min(all, (int)blockIdx.x * per);
     const int u_end = min(all, u + per);
     uint8_t *ring = smem + warp * S::kStages * S::kStage;
     const uint32_t ring_addr = ptx::smem_u32(ring);
 
-    while (u < u_end) {
-        // ---- the piece: request b, KV head h, row group qt, units c0 .. c1-1 of `chunks`
-        int lo_b = 0, hi_b = a.B;
-        while (hi_b - lo_b > 1) {
-            const int mid = (lo_b + hi_b) >> 1;
-            if (s_first[mid] <= u) lo_b = mid;
-            else hi_b = mid;
+    // The pieces of the CTA's units, one after the other: request b, KV head h, row group
+    // qt, units c0 .. c1-1 of `chunks`.  Found by a search once: the code of a search, and
+    // its divisions, waited 2000 cycles for instructions at each piece.
+    int b = 0, h = 0, qt = 0, x0 = 0, chunks = 0, tiles_q = 0;
+    AttnRequest r = {};
+    auto take = [&]() {
+        r = attn_request(a, b);
+        chunks = attn_chunks(r);
+        tiles_q = (int)(((int64_t)r.n * a.G + S::kRows - 1) / S::kRows);
+    };
+    if (u < u_end) {
+        int hi = a.B;
+        while (hi - b > 1) {
+            const int mid = (b + hi) >> 1;
+            if (s_first[mid] <= u) b = mid;
+            else hi = mid;
         }
-        const int b = lo_b;
-        const AttnRequest r = attn_request(a, b);
-        const int chunks = attn_chunks(r);
-        const int tiles_q = (int)(((int64_t)r.n * a.G + S::kRows - 1) / S::kRows);
+        take();
         const int local = u - s_first[b], piece = local / (chunks + kPieceUnits);
-        const int x0 = local - piece * (chunks + kPieceUnits), x1 = min(chunks + kPieceUnits, x0 + u_end - u);
+        x0 = local - piece * (chunks + kPieceUnits);
+        h = piece / tiles_q, qt = piece - h * tiles_q;
+    }
+    auto advance = [&]() {
+        x0 = 0;
+        if (++qt < tiles_q) return;
+        qt = 0;
+        if (++h < a.Hk) return;
+        h = 0;
+        do ++b;
+        while (s_first[b + 1] <= u);
+        take();
+    };
+    for (; u < u_end; u < u_end ? advance() : void()) {
+        const int x1 = min(chunks + kPieceUnits, x0 + u_end - u), last_unit = u - x0 + chunks + kPieceUnits - 1;
         const int c0 = max(0, x0 - kPieceUnits), c1 = max(0, x1 - kPieceUnits);
-        const int h = piece / tiles_q, qt = piece - h * tiles_q;
         u += x1 - x0;
         if (c0 == c1) continue;
+        // the query token of a row of the request
+        auto token_of = [&](int row) { return r.n == 1 ? 0 : row / a.G; };
         const int pos0 = r.len - r.n;                     // position of the request's first row
         const int rowbase = qt * S::kRows;                // (query token, head) rows, token-major
         const int nrows = min(S::kRows, r.n * a.G - rowbase);
-        const int pos_lo = pos0 + rowbase / a.G, pos_hi = pos0 + (rowbase + nrows - 1) / a.G;
+        const int pos_lo = pos0 + token_of(rowbase), pos_hi = pos0 + token_of(rowbase + nrows - 1);
         const int t_end = min(r.lo + c1 * kAttnChunk, pos_hi + 1);   // tokens seen by any of these rows
         const int t_begin = r.lo + c0 * kAttnChunk;
 
@@ -327,7 +348,8 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
             const int rr = warp + 8 * n, row = rowbase + rr;
             raw[n] = make_uint2(0, 0);
             if (rr < nrows) {
-                const uint16_t *q = a.q + ((int64_t)(r.row0 + row / a.G) * a.Hq + h * a.G + row % a.G) * D;
+                const int token = token_of(row);
+                const uint16_t *q = a.q + ((int64_t)(r.row0 + token) * a.Hq + h * a.G + row - token * a.G) * D;
                 if (D == 128) raw[n] = reinterpret_cast<const uint2 *>(q)[lane];
                 else raw[n].x = reinterpret_cast<const uint32_t *>(q)[lane];
             }
@@ -388,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
                 pass[n][j] = -INFINITY;
                 ref[n][j] = 0.0f;
                 sum[n][j] = 0.0f;
-                last[n][j] = pos0 + (rowbase + min(rr, nrows - 1)) / a.G;
+                last[n][j] = pos0 + token_of(rowbase + min(rr, nrows - 1));
             }
 #pragma unroll
         for (int m = 0; m < 2 * kBlocks; ++m)
@@ -640,8 +662,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
         __syncthreads();   // the ring is free, and the maxima are there
         const bool whole = c0 == 0 && c1 == chunks;
         if (tid == 0 && c0 == 0 && !whole) {
-            const int first = s_first[b] + piece * (chunks + kPieceUnits);
-            const AttnCut cut = {r.row0, h * a.G, rowbase, nrows, (first + chunks + kPieceUnits - 1) / per, {}};
+            const AttnCut cut = {r.row0, h * a.G, rowbase, nrows, last_unit / per, {}};
             a.cuts[blockIdx.x] = cut;
         }
         float *part = a.part + (int64_t)(2 * blockIdx.x + (c0 == 0 ? 1 : 0)) * S::kRows * (D + 2);
@@ -682,8 +703,8 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
                     *reinterpret_cast<float4 *>(part + rr * D + col) = v;
                     if (col == 0) part[S::kRows * D + rr] = m, part[S::kRows * (D + 1) + rr] = l;
                 } else if (rr < nrows) {
-                    const int row = rowbase + rr;
-                    const int64_t at = (int64_t)(r.row0 + row / a.G) * a.Hq + h * a.G + row % a.G;
+                    const int row = rowbase + rr, token = token_of(row);
+                    const int64_t at = (int64_t)(r.row0 + token) * a.Hq + h * a.G + row - token * a.G;
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // a row that sees nothing
                     write4(a, at * D + col, v, inv);
                     if (a.lse && col == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
