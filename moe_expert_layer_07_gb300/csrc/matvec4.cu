@@ -72,6 +72,7 @@ struct MatvecArgs {
     const uint8_t *w, *scales, *zeros;
     void *y;
     int T, N, K, slices, warps, per_cta, group_shift, s_f32, out_bf16;
+    int t_shift;   // T <= 2^t_shift
     int scale_row, scale_words, zero_words;   // bytes of a row's scales; words of a strip
 };
 
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
     const uint32_t ring_addr = ptx::smem_u32(ring);
     float *s_part = reinterpret_cast<float *>(smem + a.warps * kStages * kStage);   // [warps][kBatch][kSums]
     float *s_hold = s_part + a.warps * kBatch * kSums;                                // [ranks][hold_tiles][kSums]
-    const int hold_tiles = (kHold + ranks - 1) / ranks;
+    const int hold_tiles = (kHold + ranks - 1) / ranks, inv_ranks = 256 / ranks + 1;   // exact below kHold, to 8 ranks
     const uint32_t hold = ptx::smem_u32(s_hold);
     // MXFP4: [slice][row][block]
     float *s_scale = s_hold + (ranks > 1 ? ranks * hold_tiles * kSums : 0) + warp * (S * 64);
@@ -473,26 +474,29 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
         const int batch = slot_in_batch + 1, it0 = it - slot_in_batch;
         __syncthreads();
         if (ranks > 1 && it0 % kHold == 0) cluster_wait();   // the other CTAs run, and have read what they held
-        for (int i = tid; i < batch * kSums; i += a.warps * 32) {
+        for (int i = tid; i < batch << (4 + a.t_shift); i += a.warps * 32) {
+            const int t = i & ((1 << a.t_shift) - 1), row = i >> a.t_shift & 15, slot = i >> (4 + a.t_shift), j = row * 8 * NQ + t;
+            const float *p = s_part + slot * kSums + j;
             float v = 0.0f;
 #pragma unroll 4
-            for (int q = 0; q < a.warps; ++q) v += s_part[q * kBatch * kSums + i];
-            const int at = it0 + i / kSums, j = i % kSums, held = at % kHold;
+            for (int q = 0; q < a.warps; ++q) v += p[q * kBatch * kSums];
+            const int at = it0 + slot, held = at % kHold, share = held * inv_ranks >> 8;   // held / ranks
             if (ranks > 1)   // to the CTA that adds them up
                 asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(ptx::cluster_map(
-                                 hold + 4 * ((rank * hold_tiles + held / ranks) * kSums + j), held % ranks)), "f"(v) : "memory");
-            else write(a, j & (8 * NQ - 1), (cluster + at * clusters) * kTileRows + j / (8 * NQ), v);
+                                 hold + 4 * ((rank * hold_tiles + share) * kSums + j), held - share * ranks)), "f"(v) : "memory");
+            else write(a, t, (cluster + at * clusters) * kTileRows + row, v);
         }
         static_assert(kHold % kBatch == 0, "a batch is held as a whole");
         if (ranks > 1 && (it % kHold == kHold - 1 || it == mine - 1)) {
             // the CTAs' sums together: CTA r finishes tiles r, r + ranks .. of what is held
             const int held = it % kHold + 1, base = it - it % kHold, own = (held - rank + ranks - 1) / ranks;
             ptx::cluster_sync();
-            for (int i = tid; i < own * kSums; i += a.warps * 32) {
+            for (int i = tid; i < own << (4 + a.t_shift); i += a.warps * 32) {
+                const int t = i & ((1 << a.t_shift) - 1), row = i >> a.t_shift & 15, slot = i >> (4 + a.t_shift);
+                const float *p = s_hold + slot * kSums + row * 8 * NQ + t;
                 float v = 0.0f;
-                for (int r = 0; r < ranks; ++r) v += s_hold[r * hold_tiles * kSums + i];
-                const int at = base + rank + i / kSums * ranks, j = i % kSums;
-                write(a, j & (8 * NQ - 1), (cluster + at * clusters) * kTileRows + j / (8 * NQ), v);
+                for (int r = 0; r < ranks; ++r) v += p[r * hold_tiles * kSums];
+                write(a, t, (cluster + (base + rank + slot * ranks) * clusters) * kTileRows + row, v);
             }
             if (it != mine - 1) cluster_arrive();   // they may be overwritten
         }
@@ -560,6 +564,7 @@ int launch_w4_matvec(const moe_w4 *d, int T, const void *x, const void *codes, c
     a.zeros = static_cast<const uint8_t *>(zeros);
     a.y = y;
     a.T = T;
+    for (a.t_shift = 0; 1 << a.t_shift < T; ++a.t_shift);
     a.N = d->n_out;
     a.K = d->k_dim;
     a.slices = (int)ceil_div(a.K, kSlice);
