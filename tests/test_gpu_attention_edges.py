@@ -185,3 +185,50 @@ def test_calls_of_several_threads(lib):
     assert not failed, failed
     for i, case in enumerate(cases):
         case.check(outs[i])
+
+
+def _mx4_64(v):
+    """MXFP4 of fp64 values [..., D]: codes [..., D], scale bytes [..., D/32] (no ties among random values)."""
+    b = v.reshape(v.shape[:-1] + (-1, 32))
+    most = b.abs().amax(-1)
+    byte = torch.where(most > 0, (torch.frexp(most).exponent - 1 - 2 + 127).clamp(min=0), 127)
+    y = b.abs() * torch.exp2(127.0 - byte.double()).unsqueeze(-1)
+    mid = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], dtype=torch.float64, device=v.device)
+    codes = torch.searchsorted(mid, y.contiguous()) + 8 * (b < 0)
+    return codes.reshape(v.shape), byte
+
+
+@pytest.mark.parametrize("style", [0, 1])
+@pytest.mark.parametrize("D,R,norm", [(128, 128, True), (64, 32, True), (64, 64, False), (128, 0, True)])
+def test_cached_keys_are_the_codes_of_exact_values(lib, style, D, R, norm):
+    """Not those of values that rounding put on the other side of a border between codes, or of a power of two."""
+    T, Hk = 30000 * 128 // D, 8
+    g = torch.Generator(device="cuda").manual_seed(D + R + style)
+    qkv = torch.randn(T, 3 * Hk * D, device="cuda", generator=g).bfloat16()
+    w = (1 + 0.1 * torch.randn(D, device="cuda", generator=g)).bfloat16() if norm else None
+    pos = torch.randint(1, 8000, (T,), device="cuda", generator=g).to(I32)
+    cs = moe.rope_table(8000, R) if R else None
+    cache = moe.Cache4(-(-T // 64), 64, Hk, D)
+    q = torch.empty(T, Hk, D, dtype=BF, device="cuda")
+    moe.qk_norm_rope(qkv, pos, cs, Hk, Hk, q, w_k=w, cache=cache, slots=torch.arange(T, device="cuda", dtype=I32), style=style)
+    at = torch.arange(T, device="cuda")
+    for h in range(Hk):
+        v = qkv[:, (Hk + h) * D:(Hk + h + 1) * D].double()
+        if norm:
+            v = v / torch.sqrt((v * v).mean(-1, keepdim=True) + 1e-6) * w.double()
+        if R:
+            c, s = cs.double()[pos.long()][:, :R // 2], cs.double()[pos.long()][:, R // 2:]
+            if style == 0:
+                a, b = v[:, :R // 2], v[:, R // 2:R]
+                v = torch.cat([a * c - b * s, b * c + a * s, v[:, R:]], -1)
+            else:
+                a, b = v[:, 0:R:2], v[:, 1:R:2]
+                v = torch.cat([torch.stack([a * c - b * s, b * c + a * s], -1).flatten(1), v[:, R:]], -1)
+        codes, byte = _mx4_64(v)
+        got, scale = cache.codes[at // 64, 0, h, at % 64].long(), cache.scales[at // 64, 0, h, at % 64].long()
+        got = torch.stack([got & 15, got >> 4], -1).flatten(1)
+        assert torch.equal(scale, byte.long())
+        if norm:   # (elsewhere exact ties are possible)
+            assert torch.equal(got, codes)
+        else:
+            assert int((got != codes).sum()) <= 2
