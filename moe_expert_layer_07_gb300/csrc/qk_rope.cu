@@ -222,7 +222,9 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopeArgs
     if (a.w_q || a.w_k) {
         const int i = threadIdx.x % D, k = threadIdx.x / D;
         const void *w = k ? a.w_k : a.w_q;
-        if (k < 2 && w) s_w[k][i] = a.w_f32 ? static_cast<const float *>(w)[i] : __uint_as_float((uint32_t)static_cast<const uint16_t *>(w)[i] << 16);
+        if (k < 2 && w)
+            s_w[k][i] = a.w_f32 ? static_cast<const float *>(w)[i]
+                                : __uint_as_float((uint32_t)static_cast<const uint16_t *>(w)[i] << 16);
         __syncthreads();
     }
     if (!there) return;
@@ -253,48 +255,46 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopeArgs
                                      (slot & ((1 << a.page_shift) - 1))
                                : 0;
     uint16_t *const q_row = a.q_out + (t * a.Hq + g) * D;
-    // A head of this lane's, of queries (or keys) to bf16; QUERIES: all of the warp's are
+    // A head of this lane's, a query (or a key), to bf16; queries: whether all of the warp's are
     auto to_bf16 = [&](int h0, const uint2 (&now)[2], auto queries) {
         constexpr bool kQ = decltype(queries)::value;
-        {
-            const int h = h0 + g;
-            F2 x[2], y[2];
-            unpack4(now[0], x);
-            unpack4(now[1], y);
-            if (a.w_q || (!kQ && a.w_k)) {
-                F2 s2 = mul2(x[0], x[0]);
-                s2 = ptx::fma2(x[1], x[1], s2);
-                s2 = ptx::fma2(y[0], y[0], s2);
-                s2 = ptx::fma2(y[1], y[1], s2);
-                float sum = lo2(s2) + hi2(s2);
+        const int h = h0 + g;
+        F2 x[2], y[2];
+        unpack4(now[0], x);
+        unpack4(now[1], y);
+        if (a.w_q || (!kQ && a.w_k)) {
+            F2 s2 = mul2(x[0], x[0]);
+            s2 = ptx::fma2(x[1], x[1], s2);
+            s2 = ptx::fma2(y[0], y[0], s2);
+            s2 = ptx::fma2(y[1], y[1], s2);
+            float sum = lo2(s2) + hi2(s2);
 #pragma unroll
-                for (int o = N8 / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                const float inv = rsqrtf(sum * (1.0f / D) + a.eps);
-                const F2 i2 = pair(inv, inv);
-                const bool of_q = kQ || h < a.Hq;
-                if (of_q ? a.w_q : a.w_k) {
-                    F2 w[2][2];
-                    load_w(s_w[of_q ? 0 : 1] + ch_a, w[0]), load_w(s_w[of_q ? 0 : 1] + ch_b, w[1]);
+            for (int o = N8 / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const float inv = rsqrtf(sum * (1.0f / D) + a.eps);
+            const F2 i2 = pair(inv, inv);
+            const bool of_q = kQ || h < a.Hq;
+            if (of_q ? a.w_q : a.w_k) {
+                F2 w[2][2];
+                load_w(s_w[of_q ? 0 : 1] + ch_a, w[0]), load_w(s_w[of_q ? 0 : 1] + ch_b, w[1]);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) x[j] = mul2(mul2(x[j], i2), w[0][j]), y[j] = mul2(mul2(y[j], i2), w[1][j]);
-                }
+                for (int j = 0; j < 2; ++j) x[j] = mul2(mul2(x[j], i2), w[0][j]), y[j] = mul2(mul2(y[j], i2), w[1][j]);
             }
-            if (turned) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (PAIRS) {
-                        x[j] = ptx::fma2(x[j], cs[j], mul2(pair(hi2(x[j]), lo2(x[j])), sn[j]));
-                        y[j] = ptx::fma2(y[j], cs[PAIRS ? 2 + j : 0], mul2(pair(hi2(y[j]), lo2(y[j])), sn[PAIRS ? 2 + j : 0]));
-                    } else {
-                        const F2 m = mul2(y[j], sn[j]);
-                        y[j] = ptx::fma2(y[j], cs[j], mul2(x[j], sn[j]));
-                        x[j] = ptx::fma2(x[j], cs[j], m ^ 0x8000000080000000ull);
-                    }
-                }
-            }
-            uint16_t *const dst = kQ || h < a.Hq ? q_row + h0 * D : a.k_out + (t * a.Hk + h - a.Hq) * D;
-            if (kQ || h < heads) store4(dst + ch_a, x), store4(dst + ch_b, y);
         }
+        if (turned) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (PAIRS) {
+                    x[j] = ptx::fma2(x[j], cs[j], mul2(pair(hi2(x[j]), lo2(x[j])), sn[j]));
+                    y[j] = ptx::fma2(y[j], cs[PAIRS ? 2 + j : 0], mul2(pair(hi2(y[j]), lo2(y[j])), sn[PAIRS ? 2 + j : 0]));
+                } else {
+                    const F2 m = mul2(y[j], sn[j]);
+                    y[j] = ptx::fma2(y[j], cs[j], mul2(x[j], sn[j]));
+                    x[j] = ptx::fma2(x[j], cs[j], m ^ 0x8000000080000000ull);
+                }
+            }
+        }
+        uint16_t *const dst = kQ || h < a.Hq ? q_row + h0 * D : a.k_out + (t * a.Hk + h - a.Hq) * D;
+        if (kQ || h < heads) store4(dst + ch_a, x), store4(dst + ch_b, y);
     };
     // Head h of the cache's (below 0: none), keys' heads before values': eight channels of this lane's
     // from 8 c on, or four and four
@@ -311,10 +311,14 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopeArgs
         if (c < D / 32) a.scales[r * (D / 32) + c] = (uint8_t)mine;
     };
     auto encode44 = [&](const float (&v)[8], int h) {
-        const float fa[8] = {v[0], v[1], v[2], v[3], 0.0f, 0.0f, 0.0f, 0.0f}, fb[8] = {v[4], v[5], v[6], v[7], 0.0f, 0.0f, 0.0f, 0.0f};
+        const float fa[8] = {v[0], v[1], v[2], v[3], 0.0f, 0.0f, 0.0f, 0.0f};
+        const float fb[8] = {v[4], v[5], v[6], v[7], 0.0f, 0.0f, 0.0f, 0.0f};
         uint32_t ma = 0, mb = 0, byte_a = 0, byte_b = 0, mine = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ma = max(ma, __float_as_uint(v[i]) & 0x7fffffffu), mb = max(mb, __float_as_uint(v[4 + i]) & 0x7fffffffu);
+        for (int i = 0; i < 4; ++i) {
+            ma = max(ma, __float_as_uint(v[i]) & 0x7fffffffu);
+            mb = max(mb, __float_as_uint(v[4 + i]) & 0x7fffffffu);
+        }
 #pragma unroll
         for (int b = 0; b < D / 32; ++b) {
             uint32_t m = max(ch_a >> 5 == b ? ma : 0u, ch_b >> 5 == b ? mb : 0u);
@@ -364,7 +368,10 @@ __global__ void __launch_bounds__(kRopeThreads, 4) qk_rope_kernel(const RopeArgs
                         store4(dst + ch_a, {v[0], v[1]}), store4(dst + ch_b, {v[2], v[3]});
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) f[2 * i] = to_odd(lo2(v[i]), lo2(lo[i])), f[2 * i + 1] = to_odd(hi2(v[i]), hi2(lo[i]));
+                    for (int i = 0; i < 4; ++i) {
+                        f[2 * i] = to_odd(lo2(v[i]), lo2(lo[i]));
+                        f[2 * i + 1] = to_odd(hi2(v[i]), hi2(lo[i]));
+                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) f[2 * i] = lo2(v[i]), f[2 * i + 1] = hi2(v[i]);
