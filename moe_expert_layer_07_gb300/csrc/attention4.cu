@@ -34,8 +34,8 @@
 // of the cache); two of 131073 with three query tokens, 40 heads on 8, 97.6 (2.9 TB/s); one of
 // 4097 tokens 11.2, two thirds of it launches, the way to the first tokens and the join.
 // What bounds the large ones is the unpacking: 370 instructions a warp for 16 tokens
-// of 128 channels, the integer pipe (which converts, at half rate) busy 51%, issue 57%, and
-// 14% of the time CTAs that are done early.
+// of 128 channels, three quarters of what an SM can issue while it streams (one CTA of an SM
+// is as fast alone as two are together), half of it on the integer pipe, which converts.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -26,7 +26,7 @@
 // results, at most two groups a CTA, which a last kernel joins.
 //
 // Three prompts' chunks of 500 to 4096 tokens onto caches of up to 8192, 64 query
-// heads on 8 of 128: 1343 us, 0.90 PFLOP/s, 47% of what a large library product
+// heads on 8 of 128: 1350 us, 0.89 PFLOP/s, 46% of what a large library product
 // reaches; the tensor pipe is busy 43% of the time.  What bounds it is the way from
 // one half's S to its P (four rounds of load, exponentials, conversion, store: some
 // 3000 cycles of latency) against 1024 cycles of the other half's products: tensor

@@ -5,10 +5,10 @@
 // The least is reading W once, 4.25 bits a weight and more; what bounds it is the
 // instructions around the products (150 to 350 a KB of W and warp) and, for
 // few megabytes, the way in and out: a launch, x, the clusters' sums.  Measured
-// with W of 30 to 40 MB, cold: MXFP4 10240 x 7168, one row 12.6 us (3.1 TB/s),
+// with W of 30 to 40 MB, cold: MXFP4 10240 x 7168, one row 11.8 us (3.3 TB/s),
 // 7168 x 8192 with 16 rows 15.7; integers in groups of 128, 7168 x 8192: one row
-// 11.9, 16 rows 16.9 (1.85 TB/s); in groups of 32: 15.8 and 22.1.  MXFP4 of 65536 x 2048,
-// where a cluster is not needed, one row 19.2 (3.7 TB/s).
+// 11.9, 16 rows 17.0 (1.8 TB/s); in groups of 32: 15.4 and 21.2.  MXFP4 of 65536 x 2048,
+// where a cluster is not needed, one row 18.8 (3.8 TB/s).
 //
 // A warp takes 16 rows
 // of W by slices of 128 of K, the M side of mma.sync m16n8k16, with 8 or 16
@@ -30,8 +30,8 @@
 // CTAs in order: the same bits each time.  Each CTA of a cluster pushes its sums to the
 // one that adds them up (the pull it was before waited for the way there and back).
 //
-// Also measured: two CTAs to an SM with a slice to a warp 26.7 us for the first case's
-// 12.6 (sums of 8 warps' slices twice as often); two tiles' code in line 18.3 for
+// Also measured, each against its time then: two CTAs to an SM with a slice to a warp 26.7 us for
+// the first case's 12.6 (sums of 8 warps' slices twice as often); two tiles' code in line 18.3 for
 // 16.9; integers taken bare as subnormal fp16 with the zero points off the sums 17.9 for 16.9.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
