@@ -57,7 +57,7 @@ constexpr int kSoftWarps = 8, kUnpackWarps = 4, kMmaWarp = kSoftWarps + kUnpackW
 constexpr int kWideThreads = (kMmaWarp + 1) * 32;
 constexpr int kStages = 2, kInfos = 4;
 constexpr int kTmemCols = 512;
-constexpr int kPieceTiles = 4;     // what the beginning and end of a piece cost, in tiles
+constexpr int kPieceTiles = 5;     // what the beginning and end of a piece cost, in tiles
 constexpr float kLazy = 8.0f;
 constexpr int kBias = 13;
 
@@ -357,38 +357,47 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
         const int mt = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + mt * kTok, to = tmem + lanes + S::kO + mt * D;
+        // 16-byte piece p of row r of the warp's 32 in shared memory, queries and then results; kLanes
+        // lanes take a row together
+        constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes;
+        const int sub = lane / kLanes, piece = lane % kLanes;
+        uint8_t *const rows32 = smem + S::kQ + mt * S::kTileBytes + (warp & 3) * 32 * 128;
+        auto tile_piece = [&](int r, int p) { return rows32 + r * 128 + (p >> 3) * S::kHalf + (((p & 7) ^ (r & 7)) << 4); };
         uint32_t mine = 0;   // products' tiles of this half, of all pieces
         while (ok && walk.next(w, entries, p)) {
             if (p.c0 == p.c1) continue;
             const int rr = mt * kM + row, flat = p.g.rowbase + rr;
             const bool there = rr < p.g.nrows;
             const int64_t at = (int64_t)(p.r.row0 + flat / a.G) * a.Hq + p.h * a.G + flat % a.G;
+            const int at_row = there ? (int)at : -1;   // (rows times heads stay within 32 bits)
             float mult = 0.0f;
-            {   // the row's query: fp16 times 2^up
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + at * D);
-                const uint4 none = make_uint4(0, 0, 0, 0);
-                uint32_t most = 0;   // of the magnitudes, as bf16 bits moved up
-#pragma unroll 8
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 v = there ? __ldg(src + i) : none;
-                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+            // The warp's 32 queries, fp16 times 2^up, by kLanes lanes to a row: eight loads of whole rows
+            // on their way.  (A thread to a row took 12000 cycles a piece: 16 bytes of each line at a time.)
+#pragma unroll 1
+            for (int i0 = 0; i0 < kLanes; i0 += 8) {
+                uint4 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int src = __shfl_sync(0xffffffffu, at_row, (i0 + i) * kRowsAtOnce + sub);
+                    v[i] = src >= 0 ? __ldg(reinterpret_cast<const uint4 *>(a.q + (int64_t)src * D) + piece)
+                                    : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    uint32_t most = 0, y[4];   // of the magnitudes, as bf16 bits moved up
 #pragma unroll
                     for (int j = 0; j < 4; ++j) most = max(most, max(x[j] << 16 & 0x7fff0000u, x[j] & 0x7fff0000u));
-                }
-                const int up = 14 + 127 - min(max((int)(most >> 23), 27), 254);
-                const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-                mult = a.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
-                uint8_t *q = smem + S::kQ + mt * S::kTileBytes + row * 128;
-#pragma unroll 4
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 v = there ? __ldg(src + i) : none;
-                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t y[4];
+#pragma unroll
+                    for (int o = kLanes / 2; o >= 1; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+                    const int up = 14 + 127 - min(max((int)(most >> 23), 27), 254);
+                    const float f = __uint_as_float((uint32_t)(127 + up) << 23);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         y[j] = half2_of(__uint_as_float(x[j] << 16) * f, __uint_as_float(x[j] & 0xffff0000u) * f);
-                    *reinterpret_cast<uint4 *>(q + (i >> 3) * S::kHalf + (((i & 7) ^ (row & 7)) << 4)) =
-                        make_uint4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<uint4 *>(tile_piece((i0 + i) * kRowsAtOnce + sub, piece)) = make_uint4(y[0], y[1], y[2], y[3]);
+                    const int own = __shfl_sync(0xffffffffu, up, lane % kRowsAtOnce * kLanes);
+                    if (lane / kRowsAtOnce == i0 + i) mult = a.scale_log2 * __uint_as_float((uint32_t)(127 - own) << 23);
                 }
             }
             fence_proxy_async_shared();
@@ -559,32 +568,49 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             if (!whole) dst[kWideRows * D + rr] = pass == -INFINITY ? -INFINITY : ref, dst[kWideRows * (D + 1) + rr] = sum;
             else if (there && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.69314718f;
             if (used) {
+                // By way of the queries' place (their products are done), so that rows leave whole; fp32 in
+                // two halves.  (A thread to a row: 8000 cycles a piece.)
+                const bool f32 = !whole || !a.out_bf16;
+                const int cols = f32 ? D / 2 : D;
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += cols) {
+#pragma unroll 1
+                    for (int q = 0; q < cols / 16; ++q) {
+                        uint32_t r[16];
+                        tmem_ld16(to + c0 + 16 * q, r);
+                        tmem_wait_ld(r);
+                        float x[16];
+                        const bool gone = nans >> (8 * ((c0 + 16 * q) / 32)) & 1u;
 #pragma unroll
-                for (int q = 0; q < D / 16; ++q) {
-                    uint32_t r[16];
-                    tmem_ld16(to + 16 * q, r);
-                    tmem_wait_ld(r);
-                    float x[16];
-                    const bool gone = nans >> (8 * (q / 2)) & 1u;
+                        for (int i = 0; i < 16; ++i) x[i] = gone ? NAN : inv == 0.0f ? 0.0f : __uint_as_float(r[i]) * inv;
+                        if (f32) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = gone ? NAN : inv == 0.0f ? 0.0f : __uint_as_float(r[i]) * inv;
-                    if (!there) continue;
-                    if (!whole || !a.out_bf16) {
-                        float4 *o = whole ? reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at * D + 16 * q)
-                                          : reinterpret_cast<float4 *>(dst + (int64_t)rr * D + 16 * q);
+                            for (int i = 0; i < 4; ++i)
+                                *reinterpret_cast<float4 *>(tile_piece(lane, 4 * q + i)) =
+                                    make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                        } else {
+                            uint32_t y[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) o[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                    } else {
-                        uint32_t y[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-                            y[i] = *reinterpret_cast<const uint32_t *>(&b2);
+                            for (int i = 0; i < 8; ++i) {
+                                const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                                y[i] = *reinterpret_cast<const uint32_t *>(&b2);
+                            }
+                            *reinterpret_cast<uint4 *>(tile_piece(lane, 2 * q)) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4 *>(tile_piece(lane, 2 * q + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
                         }
-                        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at * D + 16 * q);
-                        o[0] = make_uint4(y[0], y[1], y[2], y[3]);
-                        o[1] = make_uint4(y[4], y[5], y[6], y[7]);
                     }
+                    __syncwarp();
+#pragma unroll 4
+                    for (int i = 0; i < kLanes; ++i) {
+                        const int r = i * kRowsAtOnce + sub, src = __shfl_sync(0xffffffffu, at_row, r);
+                        if (src < 0) continue;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(tile_piece(r, piece));
+                        uint4 *to_row = !whole  ? reinterpret_cast<uint4 *>(dst + (int64_t)(rr - lane + r) * D + c0)
+                                        : f32 ? reinterpret_cast<uint4 *>(static_cast<float *>(a.out) + (int64_t)src * D + c0)
+                                              : reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + (int64_t)src * D);
+                        to_row[piece] = v;
+                    }
+                    __syncwarp();
                 }
             }
             tc_fence_before();   // O may be written again once the next query is there
