@@ -26,10 +26,10 @@
 // results, at most two groups a CTA, which a last kernel joins.
 //
 // Three prompts' chunks of 500 to 4096 tokens onto caches of up to 8192, 64 query
-// heads on 8 of 128: 1350 us, 0.89 PFLOP/s, 46% of what a large library product
-// reaches; the tensor pipe is busy 43% of the time.  What bounds it is the way from
-// one half's S to its P (four rounds of load, exponentials, conversion, store: some
-// 3000 cycles of latency) against 1024 cycles of the other half's products: tensor
+// heads on 8 of 128: 1170 us, 1.03 PFLOP/s, 54% of what a large library product
+// reaches.  What bounds it is the way from one half's S to its P (four rounds of load,
+// exponentials, conversion, store: 2500 cycles, then 1400 of waiting for the next S)
+// against 1024 cycles of the other half's products: tensor
 // memory is full (two S of 128 columns, two O), so there is no third tile to work on
 // meanwhile.  (P in shared memory would free S sooner, but with both operands there
 // products of 128 columns read 128 bytes a clock, all that it has.)
@@ -37,7 +37,9 @@
 // Tiles of 64 tokens with two S each were slower (products of 64 columns take as long
 // as of 128: 1.50 ms for 1.36), and so were 16 softmax warps with half a row to a thread
 // (1.71: maxima and sums by shared memory); softmax in one piece of 128 columns
-// spilled and left the instruction cache (3.0 ms; loops of 32 columns 1.85).
+// spilled and left the instruction cache (3.0 ms; loops of 32 columns 1.85); largest
+// scores looked for only where the sum of 32 probabilities is large (1.28 for 1.195:
+// the sum is known last).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -57,7 +59,9 @@ constexpr int kSoftWarps = 8, kUnpackWarps = 4, kMmaWarp = kSoftWarps + kUnpackW
 constexpr int kWideThreads = (kMmaWarp + 1) * 32;
 constexpr int kStages = 2, kInfos = 4;
 constexpr int kTmemCols = 512;
-constexpr int kPieceTiles = 5;     // what the beginning and end of a piece cost, in tiles
+// What the beginning and end of a piece cost, in tiles (with 2, 3, 4 and 6: 1330, 1250,
+// 1194 and 1199 us where 4 and 6 tied).
+constexpr int kPieceTiles = 5;
 constexpr float kLazy = 8.0f;
 constexpr int kBias = 13;
 
@@ -371,19 +375,26 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             const int64_t at = (int64_t)(p.r.row0 + flat / a.G) * a.Hq + p.h * a.G + flat % a.G;
             const int at_row = there ? (int)at : -1;   // (rows times heads stay within 32 bits)
             float mult = 0.0f;
-            // The warp's 32 queries, fp16 times 2^up, by kLanes lanes to a row: eight loads of whole rows
-            // on their way.  (A thread to a row took 12000 cycles a piece: 16 bytes of each line at a time.)
-#pragma unroll 1
-            for (int i0 = 0; i0 < kLanes; i0 += 8) {
-                uint4 v[8];
+            // The warp's 32 queries, fp16 times 2^up, by kLanes lanes to a row: four loads of whole rows
+            // on their way.  (A thread to a row took 12000 cycles a piece: 16 bytes of each line at a time; 4000 so.)
+            uint4 next[4];
+            auto load = [&](int i0) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int src = __shfl_sync(0xffffffffu, at_row, (i0 + i) * kRowsAtOnce + sub);
-                    v[i] = src >= 0 ? __ldg(reinterpret_cast<const uint4 *>(a.q + (int64_t)src * D) + piece)
-                                    : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 4; ++i) {
+                    const int src = __shfl_sync(0xffffffffu, at_row, ((i0 + i) * kRowsAtOnce + sub) & 31);
+                    next[i] = src >= 0 && i0 < kLanes ? __ldg(reinterpret_cast<const uint4 *>(a.q + (int64_t)src * D) + piece)
+                                                      : make_uint4(0, 0, 0, 0);
                 }
+            };
+            load(0);
+#pragma unroll 1
+            for (int i0 = 0; i0 < kLanes; i0 += 4) {
+                uint4 v[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < 4; ++i) v[i] = next[i];
+                load(i0 + 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
                     const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                     uint32_t most = 0, y[4];   // of the magnitudes, as bf16 bits moved up
 #pragma unroll
@@ -569,20 +580,21 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             else if (there && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.69314718f;
             if (used) {
                 // By way of the queries' place (their products are done), so that rows leave whole; fp32 in
-                // two halves.  (A thread to a row: 8000 cycles a piece.)
+                // two halves.  (A thread to a row: 8000 cycles a piece, 5000 so.)
                 const bool f32 = !whole || !a.out_bf16;
                 const int cols = f32 ? D / 2 : D;
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += cols) {
+                    uint32_t r[16];
+                    tmem_ld16(to + c0, r);
 #pragma unroll 1
                     for (int q = 0; q < cols / 16; ++q) {
-                        uint32_t r[16];
-                        tmem_ld16(to + c0 + 16 * q, r);
                         tmem_wait_ld(r);
                         float x[16];
                         const bool gone = nans >> (8 * ((c0 + 16 * q) / 32)) & 1u;
 #pragma unroll
                         for (int i = 0; i < 16; ++i) x[i] = gone ? NAN : inv == 0.0f ? 0.0f : __uint_as_float(r[i]) * inv;
+                        if (q + 1 < cols / 16) tmem_ld16(to + c0 + 16 * q + 16, r);
                         if (f32) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
