@@ -57,6 +57,10 @@ __host__ __device__ constexpr int batch_tiles(int nq) { return 4 / nq; }
 constexpr int kScaleStrip = 32, kZeroStrip = 12;
 
 constexpr int kStages = 4;   // what 16 warps' rings, of two slices each, leave room for
+// Of the stages that are copied before the first products, those asked for before x is converted: with
+// 3, 2, 1 and 0 int4 of 7168 x 8192 and 16 rows took 17.5, 16.9, 17.6 and 17.8 us, MXFP4 and one row 9.9,
+// 9.8, 9.9 and 10.3 (copies and x come through the same queue).
+constexpr int kBefore = 2;
 
 // Kinds of weights: MXFP4, integers with one scale for a slice (groups of 128), with
 // more than one (32, 64)
@@ -295,7 +299,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
                     all[n][i][b] = __ldg(reinterpret_cast<const uint4 *>(a.x + (int64_t)t * a.K + k));
             }
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch();
+    for (int i = 0; i < kBefore; ++i) fetch();
     // Pieces behind N or K are never copied: their products are not used (rows) or
     // are with x of zero (columns; the ring's bits are finite numbers, and the scales
     // are taken as zero).
@@ -351,6 +355,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
             });
         }
     }
+#pragma unroll
+    for (int i = kBefore; i < kStages - 1; ++i) fetch();
     const int mrow = (lane & 7) + ((lane >> 3) & 1) * 8, mblk = lane >> 4;
 
     // (Not unrolled: with two tiles' code in line, the instruction cache was what 16 rows of x
