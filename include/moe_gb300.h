@@ -653,7 +653,7 @@ MOE_API int moe_cache_read(const moe_cache4 *cache, int32_t n, const int32_t *sl
  *   desc.max_len  the longest request: what the kernels and the workspace are
  *                 chosen by; larger ones on the device are computed all the same,
  *                 unless their units of work (128 tokens by 8 rows and more) pass
- *                 2^31 / requests: MOE_DEV_BAD_INDEX, and not computed
+ *                 2^30 / requests: MOE_DEV_BAD_INDEX, and not computed
  *   ws         moe_cache_attention_workspace_size bytes, 16-byte aligned; one call
  *              at a time; needs no initialisation
  * requests 0..4096, rows * q_heads below 2^31, q_heads a multiple of kv_heads. */

@@ -177,9 +177,9 @@ __device__ __forceinline__ void plan_units(const AttnArgs &a, int rows_at_once, 
             const AttnRequest r = attn_request(a, b);
             const int tiles = (int)(((int64_t)r.n * a.G + rows_at_once - 1) / rows_at_once);
             const int64_t want = (int64_t)a.Hk * tiles * (attn_chunks(r) + kPieceUnits);
-            // all requests together stay within 32 bits
+            // all requests together stay within 31 bits, and CTAs' shares of them within 32
             const bool few = (int64_t)r.n * a.G <= a.few_rows;   // else another kernel's
-            units = few && want <= INT32_MAX / a.B ? (int)want : 0;
+            units = few && want <= (1 << 30) / a.B ? (int)want : 0;
             if ((r.bad || (few && units != want)) && blockIdx.x == 0 && a.status) atomicOr(a.status, MOE_DEV_BAD_INDEX);
         }
         int v = units;
