@@ -232,3 +232,31 @@ def test_cached_keys_are_the_codes_of_exact_values(lib, style, D, R, norm):
             assert torch.equal(got, codes)
         else:
             assert int((got != codes).sum()) <= 2
+
+
+@pytest.mark.parametrize("new", [1, 2, 4, 5, 40])
+@pytest.mark.parametrize("D,Hk", [(128, 2), (64, 1)])
+def test_one_request_in_buffers_for_many_rows(lib, new, D, Hk):
+    """What a plan of many rows does with few, and the calls of fewer rows in its workspace."""
+    case = Case([333], [new], 8, Hk, D, 32, extra_rows=64 - new)
+    big = moe.CacheAttention(1, 64, 8, case.cache, case.table.shape[1], max_q=64, max_len=400)
+    for rows in sorted({64, new, 17}):
+        if rows < new:
+            continue
+        out = torch.full_like(case.q[:rows], 3.0)
+        lse = torch.full((rows, 8), 3.0, device="cuda")
+        big.of_rows(rows).forward(case.q[:rows], case.table, case.lengths, case.starts, out, lse=lse)
+        case.check(out, lse)
+        assert bool((out[new:] == 3.0).all()) and bool((lse[new:] == 3.0).all())
+
+
+@pytest.mark.parametrize("Hq,Hk", [(1, 1), (9, 1), (40, 2), (48, 1)])
+def test_a_workspace_holds_every_smaller_call(lib, Hq, Hk):
+    """Head layouts whose calls of 1, 2, 3 .. rows take different kernels."""
+    case = Case([70], [1], Hq, Hk, 64, 16, extra_rows=36)
+    for most in (1, 2, 3, 5, 37):
+        big = moe.CacheAttention(1, most, Hq, case.cache, case.table.shape[1], max_q=most, max_len=100)
+        for rows in range(1, most + 1, 2):
+            out = torch.empty_like(case.q[:rows])
+            big.of_rows(rows).forward(case.q[:rows], case.table, case.lengths, case.starts, out)
+            case.check(out)
