@@ -44,6 +44,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "attention4.cuh"
 #include "mx4.cuh"
@@ -648,12 +649,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             uint32_t kb[I], vb[I];   // scale bytes of this tile; 0 where there is nothing
             uint32_t kn[I], vn[I];   // of the next
             int64_t rows[2];         // of the next tile's keys for each 16 tokens: this lane's first; below 0: nothing
-            int ids[2];              // pages of the tile behind it; -2: nothing to see
+            int ids[2];              // pages of the tile behind it; -1: none, kHidden: nothing to see
+            constexpr int kHidden = INT_MIN;
             auto load_ids = [&](int c) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int t = p.g.lo + c * kTok + 32 * dw + 16 * i;
-                    ids[i] = c < p.c1 && t <= p.g.pos_hi ? __ldg(table + (t >> a.page_shift)) : -2;
+                    // (an id below zero is not kHidden, whatever it is)
+                    ids[i] = c < p.c1 && t <= p.g.pos_hi ? max(__ldg(table + (t >> a.page_shift)), -1) : kHidden;
                 }
             };
             // rounds of 16 / kRoundRows for each 16 tokens
@@ -679,7 +682,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                     rows[g] = -1;
                     if (ids[g] >= 0 && ids[g] < a.pages) {
                         rows[g] = (((int64_t)ids[g] * 2 * a.Hk + p.h) << a.page_shift) + ((t0 + 32 * dw + 16 * g + pr) & in_page);
-                    } else if (ids[g] != -2) {
+                    } else if (ids[g] != kHidden) {
                         next_lost |= 1u << (2 * dw + g);
                         if (a.status && lane == 0) atomicOr(a.status, MOE_DEV_BAD_INDEX);
                     }

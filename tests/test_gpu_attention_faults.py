@@ -1,0 +1,92 @@
+"""Attention over the four-bit cache where single entries of its inputs are out of the ordinary: page ids that
+are none, scales far apart, probabilities far apart, values that are NaN.  Against softmax in fp64, with a
+bound for each row and channel that knows only what that row sees.
+
+Tolerance.  Scores: as in test_gpu_attention.py, off by d <= 2^-19 sum |q k| scale, so a weight by
+exp(2 d) - 1 <= 4 d of itself (d small); 2^-16 for exponentials and sums.  Probabilities are rounded to fp16,
+2^-11 of themselves; below 2^-14 of the largest fp16 has steps of 2^-24 and they are off by half a step, 2^-25 of
+the largest, and by another half where they are scaled down with a maximum that rises: LEAST.  So a row's
+channel is off by sum_j |v_j| (w_j (2^-11 + 4 d + 2^-16) + LEAST max_i w_i), by 2^-24 of sum_j w_j |v_j| for the sum in
+fp32, and by half a step of the output's type; nothing that the row does not see adds to it."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import moe_expert_layer_07_gb300 as moe
+from _gpu_common import build_library
+from test_gpu_attention import Case
+
+pytestmark = pytest.mark.gpu
+I32, BF, F32 = torch.int32, torch.bfloat16, torch.float32
+LEAST = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    return build_library()
+
+
+def _i(v):
+    return torch.tensor(np.asarray(v), dtype=I32, device="cuda")
+
+
+def _strict(case, out, lse=None, window=0, lost=(), only=None):
+    """Every row and channel within the bound.  lost: (request, first token, end) that are not seen."""
+    c, at = case, 0
+    G, scale = c.Hq // c.Hk, c.D ** -0.5
+    half = 2.0 ** -8 if out.dtype == BF else 2.0 ** -24
+    for b, (L, n) in enumerate(zip(c.lens, c.news)):
+        rows, at = slice(at, at + n), at + n
+        if n == 0 or (only is not None and b not in only):
+            continue
+        k, v = c.values(b)
+        q = c.q[rows].double().reshape(n, c.Hk, G, c.D)
+        j, p = torch.arange(L, device="cuda"), torch.arange(L - n, L, device="cuda")[:, None]
+        seen = (j[None] <= p) & ((j[None] > p - window) if window else True)
+        for r, first, end in lost:
+            if r == b:
+                seen = seen & ~((j >= first) & (j < end))[None]
+        seen = seen[:, None, None]
+        x = torch.where(seen, torch.einsum("nhgd,hld->nhgl", q, k) * scale, -math.inf)
+        d = torch.where(seen, torch.einsum("nhgd,hld->nhgl", q.abs(), k.abs()) * scale * 2.0 ** -19, 0.0)
+        d = d.amax(-1, keepdim=True)
+        z = torch.logsumexp(x, -1, keepdim=True)
+        w = torch.exp(x - z)
+        off = w * (2.0 ** -11 + 4 * d + 2.0 ** -16 + 2.0 ** -24) + torch.where(seen, LEAST * w.amax(-1, keepdim=True), 0.0)
+        va = v.abs()
+        ref, bound = torch.einsum("nhgl,hld->nhgd", w, v), torch.einsum("nhgl,hld->nhgd", off, va)
+        got = out[rows].double().reshape(ref.shape)
+        err, bound = (got - ref).abs(), bound + ref.abs() * half
+        assert bool((err <= bound).all()), (b, float((err / bound.clamp(min=1e-300)).max()))
+        if lse is not None:
+            zz, gz = z[..., 0], lse[rows].double().reshape(z.shape[:-1])
+            assert bool(((gz - zz).abs() <= d[..., 0] + 2.0 ** -20 * (1 + zz.abs())).all())
+
+
+def _forward(case, dtype=F32, status=0, window=0, table=None):
+    out = torch.full(case.q.shape, 7.0, dtype=dtype, device="cuda")
+    lse = torch.full(case.q.shape[:2], 7.0, device="cuda")
+    word = _i([0])
+    case.plan(window=window).forward(case.q, case.table if table is None else table, case.lengths, case.starts, out,
+                                     lse=lse, status=word)
+    assert int(word) == status
+    return out, lse
+
+
+@pytest.mark.parametrize("news", [[2, 1], [40, 3], [3, 300]])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 16), (128, 64)])
+@pytest.mark.parametrize("bad", [-1, -2, -3, -2 ** 31, 2 ** 31 - 1, "pages"])
+def test_page_ids_that_are_none(lib, news, D, page, bad):
+    """Their tokens are not seen, whatever the id is, and the status says so."""
+    lens = [n + 150 for n in news]
+    c = Case(lens, news, 8, 2, D, page, seed=2)
+    table = c.table.clone()
+    table[0, 1] = table[1, 0] = c.cache.pages if bad == "pages" else bad
+    out, lse = _forward(c, status=moe.DEV_BAD_INDEX, table=table)
+    _strict(c, out, lse, lost=[(0, page, 2 * page), (1, 0, page)])
