@@ -4,19 +4,19 @@
 //
 // A CTA takes 256 rows (query heads of one KV head, query tokens one after the
 // other) as two tiles of 128, and passes over the keys and values in tiles of
-// 128 tokens.  tcgen05.mma (fp16 operands, fp32 in tensor memory): S from Q and
-// K in shared memory; O from P, which a tile's softmax leaves in tensor memory
+// 128 tokens.  tcgen05.mma (fp32 in tensor memory): S from Q and K in shared
+// memory, both bf16; O from P, fp16, which a tile's softmax leaves in tensor memory
 // where S was, and V in shared memory with channels contiguous.  While one
 // tile's softmax works on its S the products of the other are under way:
 //   QK0 QK1 | PV0 QK0 PV1 QK1 | PV0 QK0 PV1 QK1 ...
 // Warps 0-3 and 4-7 are the softmax of tile 0 and 1, a thread to a row; warps
 // 8-11 unpack keys and values; warp 12 issues the products.
 //
-// Four-bit codes become fp16 (cvt) times 2^(e - E + 13), E the largest exponent
-// of the tile's keys, or that the piece has met in its values; what lies 28
-// binades below E counts as zero.  Keys: 2^E goes into the row's factor.
-// Values: where E grows, O is scaled when P is made.  q is fp16 times a power of
-// two for each row.  m is raised only where a score passes it by 8 (in log2), so
+// A key's value, a code of two significant bits times a power of two, is a bf16 number
+// whatever its scale, and so is q: S has no error but its sum's.  Codes of values become
+// fp16 (cvt) times 2^(e - E + 13), E the largest exponent that the piece has met; what lies 28
+// binades below E counts as zero.  Where E grows, O is scaled when P is made.
+// m is raised only where a score passes it by 8 (in log2), so
 // S is read once and O hardly ever; it rises by whole powers of two.  A value that is
 // NaN counts as zero in the products; rows that give it weight remember its block.
 //
@@ -87,6 +87,17 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
     const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+__device__ __forceinline__ uint32_t mul_bf162(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// Pairs of e2m1 values from fp16 to bf16, times 2^-112: all bits move down by three (such a value has none
+// of the lowest three) and the sign goes back up, 2^12 + 7 2^12 = 2^15.
+__device__ __forceinline__ uint32_t bf16_of_half2(uint32_t h) {
+    const uint32_t t = h >> 3;
+    return t + 7u * (t & 0x10001000u);   // (an e2m1 value has none of the lowest three bits)
+}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -129,9 +140,9 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t bdes
         "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// fp16 operands, K-major; B with channels contiguous where `mn`
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool mn) {
-    return (1u << 4) | ((uint32_t)mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// fp16 operands, A K-major, B with channels contiguous
+__host__ __device__ constexpr uint32_t idesc_f16_mn(int M, int N) {
+    return (1u << 4) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // V: rows of 128 bytes (64 channels of a token), 128-byte swizzle; eight tokens 1024 bytes,
 // the next 64 channels kTok rows on
@@ -279,7 +290,6 @@ struct Walk {
 };
 
 struct Info {          // of a tile of tokens, from those who unpack it
-    float ek;          // 2^(E - 127 - kBias) of its keys
     float grown;       // what O is to be multiplied by before this tile
     float ev;          // 2^(E - 127 - kBias) of the values so far
     uint32_t bad;      // bit i: tokens 16 i .. are on a page that is not there
@@ -375,9 +385,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             const bool there = rr < p.g.nrows;
             const int64_t at = (int64_t)(p.r.row0 + flat / a.G) * a.Hq + p.h * a.G + flat % a.G;
             const int at_row = there ? (int)at : -1;   // (rows times heads stay within 32 bits)
-            float mult = 0.0f;
-            // The warp's 32 queries, fp16 times 2^up, by kLanes lanes to a row: four loads of whole rows
-            // on their way.  (A thread to a row took 12000 cycles a piece: 16 bytes of each line at a time; 4000 so.)
+            // The warp's 32 queries by kLanes lanes to a row: loads of whole rows, four on their way.
+            // (A thread to a row took 12000 cycles a piece, 16 bytes of each line at a time; 4000 so.)
             uint4 next[4];
             auto load = [&](int i0) {
 #pragma unroll
@@ -395,22 +404,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 for (int i = 0; i < 4; ++i) v[i] = next[i];
                 load(i0 + 4);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                    uint32_t most = 0, y[4];   // of the magnitudes, as bf16 bits moved up
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) most = max(most, max(x[j] << 16 & 0x7fff0000u, x[j] & 0x7fff0000u));
-#pragma unroll
-                    for (int o = kLanes / 2; o >= 1; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-                    const int up = 14 + 127 - min(max((int)(most >> 23), 27), 254);
-                    const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        y[j] = half2_of(__uint_as_float(x[j] << 16) * f, __uint_as_float(x[j] & 0xffff0000u) * f);
-                    *reinterpret_cast<uint4 *>(tile_piece((i0 + i) * kRowsAtOnce + sub, piece)) = make_uint4(y[0], y[1], y[2], y[3]);
-                    const int own = __shfl_sync(0xffffffffu, up, lane % kRowsAtOnce * kLanes);
-                    if (lane / kRowsAtOnce == i0 + i) mult = a.scale_log2 * __uint_as_float((uint32_t)(127 - own) << 23);
-                }
+                for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(tile_piece((i0 + i) * kRowsAtOnce + sub, piece)) = v[i];
             }
             fence_proxy_async_shared();
             __syncwarp();
@@ -431,7 +425,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 const int t0 = p.g.lo + c * kTok;
                 const bool edge = t0 + kTok - 1 > p.g.pos_lo || (a.window && t0 <= p.g.pos_hi - a.window) || info.bad;
                 const int upto = pos - t0, from = a.window ? pos - a.window - t0 : -1;   // columns from < i <= upto
-                const float xs = mult * info.ek;
                 float shrink = info.grown;
                 // 32 columns at a time (a small loop: unrolled, its code did not stay in the
                 // instruction cache): their P takes the place of S that has been read.
@@ -441,7 +434,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 F2 part[2] = {0ull, 0ull};
                 // scores of 32 columns from r, past m, hidden ones at minus infinity
                 auto scores = [&](int q, float (&x)[32]) {
-                    const F2 xs2 = pack2(__float_as_uint(xs), __float_as_uint(xs));
+                    const F2 xs2 = pack2(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
                     const F2 ref2 = pack2(__float_as_uint(-ref), __float_as_uint(-ref));
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
@@ -704,21 +697,21 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             int erun = 0;   // E of the values so far
             for (int c = p.c0; c < p.c1; ++c, ++tiles) {
                 const uint32_t stage = tiles % kStages, in = tiles % kInfos;
-                uint32_t bad = next_lost, nan = 0, mk = 0, mv = 0;   // of all the warp's tokens
+                uint32_t bad = next_lost, nan = 0, far = 0, mv = 0;   // of all the warp's tokens
 #pragma unroll
                 for (int i = 0; i < I; ++i) {
                     // rows behind the last token may hold anything
                     const bool seen = 32 * dw + kRoundRows * i + pr < next_seen;
                     kb[i] = seen ? kn[i] : 0u, vb[i] = seen ? vn[i] : 0u;
-                    if (kb[i] != 255u) mk = max(mk, kb[i]);
+                    far |= kb[i] > 142u;
                     if (vb[i] != 255u) mv = max(mv, vb[i]);
                     else nan = 1;
                 }
-                mk = __reduce_max_sync(0xffffffffu, mk);
                 mv = __reduce_max_sync(0xffffffffu, mv);
                 nan = __any_sync(0xffffffffu, nan);
+                far = __any_sync(0xffffffffu, far);
                 if (lane == 0) {
-                    s_e[tiles & 1][dw] = make_uint4(mk, mv, bad, nan);
+                    s_e[tiles & 1][dw] = make_uint4(mv, bad, nan, 0);
                     mbar_arrive(smem_u32(&e_full[tiles & 1]));
                 }
                 load_codes(vc, kv_rows);
@@ -726,17 +719,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 load_ids(c + 2);
                 ok = wait(e_full[tiles & 1], (tiles >> 1) & 1);
                 if (!ok) break;
-                int ek = 0, ev = erun;
+                int ev = erun;
 #pragma unroll
                 for (int x = 0; x < kUnpackWarps; ++x) {
                     const uint4 e = s_e[tiles & 1][x];
-                    ek = max(ek, (int)e.x), ev = max(ev, (int)e.y), bad |= e.z, nan |= e.w;
+                    ev = max(ev, (int)e.x), bad |= e.y, nan |= e.z;
                 }
                 ok = wait(k_empty[stage], ((tiles / kStages) & 1) ^ 1u);
                 if (!ok) break;
                 if (dw == 0 && lane == 0) {
                     Info info;
-                    info.ek = ex2w((float)(ek - 127 - kBias));
                     info.grown = ev == erun || c == p.c0 ? 1.0f : ex2w((float)(erun - ev));
                     info.ev = ex2w((float)(ev - 127 - kBias));
                     info.bad = bad, info.nan = nan;
@@ -751,11 +743,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                         if (kIn == 2) n[2] = 0;
                     }
                 erun = ev;
-                // codes of eight channels -> 16 bytes, times 2^(e - E + kBias)
-                auto widen = [&](const uint4 &codes, uint32_t byte, int e, uint8_t *dst, int t, bool keys) {
-                    uint32_t f = (uint32_t)max((int)byte - e + kBias + 15, 0) << 10;
-                    if (byte == 255u) f = keys ? 0x7e00u : 0u;
-                    f *= 0x10001u;
+                // codes of 32 channels (a lane's 16 bytes) of token t to shared memory, by `to16` of pairs
+                auto widen = [&](const uint4 &codes, uint8_t *dst, int t, auto to16) {
                     const uint32_t x[4] = {codes.x, codes.y, codes.z, codes.w};
                     uint8_t *rowp = dst + (pc >> 1) * S::kHalf + t * 128;
 #pragma unroll
@@ -763,12 +752,29 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                         uint32_t hv[4];
                         mx4_half8(x[j], hv);
                         *reinterpret_cast<uint4 *>(rowp + ((((pc & 1) * 4 + j) ^ (t & 7)) << 4)) =
-                            make_uint4(mul_half2(hv[0], f), mul_half2(hv[1], f), mul_half2(hv[2], f), mul_half2(hv[3], f));
+                            make_uint4(to16(hv[0]), to16(hv[1]), to16(hv[2]), to16(hv[3]));
                     }
                 };
+                // Keys: bf16, 2^(e - 127) by way of 2^-112 and 2^(e - 15); from 2^16 on that passes bf16's
+                // largest and is made of two
 #pragma unroll
-                for (int i = 0; i < I; ++i)
-                    widen(kc[i], kb[i], ek, smem + S::kK + stage * S::kTileBytes, 32 * dw + kRoundRows * i + pr, true);
+                for (int i = 0; i < I; ++i) {
+                    uint8_t *const dst = smem + S::kK + stage * S::kTileBytes;
+                    const int t = 32 * dw + kRoundRows * i + pr;
+                    const uint32_t f = (kb[i] == 255u ? 0x7fc0u : min(kb[i] + 112u, 254u) << 7) * 0x10001u;
+                    widen(kc[i], dst, t, [&](uint32_t h) { return mul_bf162(bf16_of_half2(h), f); });
+                }
+                if (far)   // (its own small loop: in line, it would be in the instruction cache's way)
+#pragma unroll 1
+                    for (int i = 0; i < 4 * I; ++i) {
+                        const int t = 32 * dw + kRoundRows * (i >> 2) + pr;
+                        const uint32_t byte = i < 4 ? kb[0] : i < 8 ? kb[1] : i < 12 ? kb[2 % I] : kb[3 % I];
+                        const uint32_t g = ((127u + max((int)byte - 142, 0)) << 7) * 0x10001u;
+                        uint4 *const at = reinterpret_cast<uint4 *>(smem + S::kK + stage * S::kTileBytes + (pc >> 1) * S::kHalf +
+                                                                    t * 128 + ((((pc & 1) * 4 + (i & 3)) ^ (t & 7)) << 4));
+                        const uint4 y = *at;
+                        *at = make_uint4(mul_bf162(y.x, g), mul_bf162(y.y, g), mul_bf162(y.z, g), mul_bf162(y.w, g));
+                    }
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) {
@@ -780,7 +786,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 if (!ok) break;
 #pragma unroll
                 for (int i = 0; i < I; ++i)
-                    widen(vc[i], vb[i], ev, smem + S::kV + stage * S::kTileBytes, 32 * dw + kRoundRows * i + pr, false);
+                {   // values: fp16, times 2^(e - E + kBias)
+                    const uint32_t f = vb[i] == 255u ? 0u : ((uint32_t)max((int)vb[i] - ev + kBias + 15, 0) << 10) * 0x10001u;
+                    widen(vc[i], smem + S::kV + stage * S::kTileBytes, 32 * dw + kRoundRows * i + pr,
+                          [&](uint32_t h) { return mul_half2(h, f); });
+                }
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&v_full[stage]));
@@ -789,7 +799,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
     } else {
         // ---- products ---------------------------------------------------------------------
         const bool elected = elect_one();
-        constexpr uint32_t kQK = idesc_f16(kM, kTok, false), kPV = idesc_f16(kM, D, true);
+        constexpr uint32_t kQK = idesc_bf16(kM, kTok), kPV = idesc_f16_mn(kM, D);
         uint32_t made[2] = {0, 0};   // P of each half that products have taken
         while (ok && walk.next(w, entries, p)) {
             if (p.c0 == p.c1) continue;

@@ -90,3 +90,40 @@ def test_page_ids_that_are_none(lib, news, D, page, bad):
     table[0, 1] = table[1, 0] = c.cache.pages if bad == "pages" else bad
     out, lse = _forward(c, status=moe.DEV_BAD_INDEX, table=table)
     _strict(c, out, lse, lost=[(0, page, 2 * page), (1, 0, page)])
+
+
+ROWS = [[3], [40], [300]]   # query tokens of a request: 12 rows of a head, many rows, rows of several groups
+
+
+@pytest.mark.parametrize("news", ROWS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("more", [27, 40, 100])
+@pytest.mark.parametrize("where", [0, 130, -2])
+def test_one_key_far_above_the_others(lib, news, D, more, where):
+    """A block of one key 2^more above the others: scores of the other keys are what they were, for rows that see
+    it and rows that stand before it."""
+    c = Case([news[0] + 200], news, 8, 2, D, 16, seed=more)
+    at = where % c.lens[0]
+    p, o = int(c.host_table[0, at // 16]), at % 16
+    c.cache.scales[p, 0, :, o, 1] += more
+    if where >= 0:
+        c.q[..., 32:64] = 0   # all rows see it; it gives scores of nothing
+    out, lse = _forward(c)
+    if where >= 0:
+        _strict(c, out, lse)
+    else:   # the last two rows' scores have no meaning beside 2^100; all rows before are as they were
+        c.lens, c.news = [at], [news[0] - 2]
+        _strict(c, out, lse)
+
+
+@pytest.mark.parametrize("news", ROWS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shift", [-100, -30, 14, 16, 18, 60, 100])
+def test_keys_of_any_size(lib, news, D, shift):
+    """Keys times 2^shift and queries times 2^-shift: the same scores."""
+    c = Case([news[0] + 77], news, 8, 2, D, 32, seed=shift + 100)
+    c.poison_stale()
+    scales = c.cache.scales[:, 0]
+    c.cache.scales[:, 0] = torch.where(scales == 255, 255, scales.int() + shift).to(torch.uint8)
+    c.q *= 2.0 ** -shift
+    _strict(c, *_forward(c))
