@@ -114,9 +114,9 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
 // Scale of a value that is NaN, for a start: minus zero.
 constexpr uint32_t kNan = 0x8000u;
 
-// Whether a pair of probabilities gives weight to a value that is NaN.
-__device__ __forceinline__ bool sees_nan(uint32_t p, uint32_t scales) {
-    return ((scales & 0xffffu) == kNan && (p & 0x7fffu)) || (scales >> 16 == kNan && (p & 0x7fff0000u));
+// Whether a row that sees a pair of tokens (seen: halves that are not zero) sees a value that is NaN.
+__device__ __forceinline__ bool sees_nan(uint32_t seen, uint32_t scales) {
+    return ((scales & 0xffffu) == kNan && (seen & 0xffffu)) || (scales >> 16 == kNan && seen >> 16);
 }
 
 // N words of shared memory, as bits or as floats.
@@ -630,18 +630,23 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
                         }
                     }
                 }
-                if (nans) {   // NaN for the rows that see it, in its block
+                if (nans) {   // NaN for the rows that see it (not by P, which fp16 may have made zero), in its block
 #pragma unroll
-                    for (int k = 0; k < kBlocks; ++k)
+                    for (int n = 0; n < NQ; ++n) {
+                        uint32_t seen[2];
 #pragma unroll
-                        for (int n = 0; n < NQ; ++n) {
-                            const bool hit = sees_nan(pt[n][0], vs0[k]) || sees_nan(pt[n][1], vs1[k]);
+                        for (int j = 0; j < 2; ++j)
+                            seen[j] = transposed8((s[u][n][2 * j] == -INFINITY ? 0u : 1u) | (s[u][n][2 * j + 1] == -INFINITY ? 0u : 1u << 16));
+#pragma unroll
+                        for (int k = 0; k < kBlocks; ++k) {
+                            const bool hit = sees_nan(seen[0], vs0[k]) || sees_nan(seen[1], vs1[k]);
                             const uint32_t lanes = __ballot_sync(0xffffffffu, hit);   // four lanes to row g
 #pragma unroll
                             for (int j = 0; j < 2; ++j)
                                 if (lanes >> (8 * c + 4 * j) & 15u)
                                     o[2 * k][n][j] = o[2 * k][n][j + 2] = o[2 * k + 1][n][j] = o[2 * k + 1][n][j + 2] = NAN;
                         }
+                    }
                 }
             }
         }

@@ -18,7 +18,7 @@
 // binades below E counts as zero.  Where E grows, O is scaled when P is made.
 // m is raised only where a score passes it by 8 (in log2), so
 // S is read once and O hardly ever; it rises by whole powers of two.  A value that is
-// NaN counts as zero in the products; rows that give it weight remember its block.
+// NaN counts as zero in the products; rows that see it remember its block.
 //
 // Work: one unit for each tile of tokens that a group of 256 rows sees (causal:
 // fewer for earlier rows) and some for its beginning and end; each CTA takes as
@@ -542,16 +542,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 tmem_wait_st();
                 if (info.nan) {
 #pragma unroll 1
-                    for (int q = 0; q < kTok / 32; ++q) {
-                        uint32_t r[16];
-                        tmem_ld16(ts + 16 * q, r);
-                        tmem_wait_ld(r);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const uint2 n8 = s_nan[in][16 * q + i];
-                            if (r[i] & 0x7fffu) nans |= n8.x;
-                            if (r[i] & 0x7fff0000u) nans |= n8.y;
-                        }
+                    for (int t = 0; t < kTok; t += 2) {   // (not by P, which fp16 may have made zero)
+                        const uint2 n8 = s_nan[in][t / 2];
+                        const bool there = !(info.bad >> (t >> 4) & 1u);
+                        if (there && t <= upto && t > from) nans |= n8.x;
+                        if (there && t + 1 <= upto && t + 1 > from) nans |= n8.y;
                     }
                 }
                 tc_fence_before();

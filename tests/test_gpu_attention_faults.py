@@ -127,3 +127,52 @@ def test_keys_of_any_size(lib, news, D, shift):
     c.cache.scales[:, 0] = torch.where(scales == 255, 255, scales.int() + shift).to(torch.uint8)
     c.q *= 2.0 ** -shift
     _strict(c, *_forward(c))
+
+
+@pytest.mark.parametrize("news", [[3], [60, 1], [300]])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 90])
+@pytest.mark.parametrize("light", [False, True])
+def test_a_value_that_is_nan(lib, news, D, window, light):
+    """Reaches the rows that see it, in its block of channels, also where its weight is next to nothing (2^-43 and
+    less); keys and queries that are NaN reach all of a row.  The others keep their bits."""
+    lens = [n + 250 for n in news]
+    c = Case(lens, news, 8, 2, D, 16, seed=3)
+    n, L, at = news[0], lens[0], lens[0] - 2 if news[0] < 60 else lens[0] - 50
+    p, o = int(c.host_table[0, at // 16]), at % 16
+    if light:   # every row's score there is 30 below zero, others' near it
+        c.q[..., :32] = 3.75 * D ** 0.5
+        c.q[..., 32:] *= 0.1
+        c.cache.scales[:, 0, :, :, 0] = 110
+        c.cache.codes[p, 0, :, o, :16] = 0x99   # -0.5 each
+        c.cache.scales[p, 0, :, o, 0] = 126
+    kw = dict(window=window)
+    clean, _ = _forward(c, **kw)
+    pos = torch.arange(L - n, L, device="cuda")
+    sees = (pos >= at) & ((pos - window < at) if window else True)
+    bad = torch.zeros_like(clean, dtype=torch.bool)
+    c.cache.scales[p, 1, 1, o, D // 32 - 1] = 255
+    c.cache.codes[p, 1, 1, o, D // 2 - 16:] = 0
+    bad[:n, 4:, D - 32:] = sees[:, None, None]
+    out, _ = _forward(c, **kw)
+    assert bool(torch.isnan(out[bad]).all()) and bool((out[~bad] == clean[~bad]).all())
+    c.cache.scales[p, 0, 0, o, 1] = 255
+    c.cache.codes[p, 0, 0, o, 16:32] = 0
+    bad[:n, :4] |= sees[:, None, None]
+    out, _ = _forward(c, **kw)
+    assert bool(torch.isnan(out[bad]).all()) and bool((out[~bad] == clean[~bad]).all())
+    c.q[n - 1, 2, 5] = float("nan")
+    bad[n - 1, 2] = True
+    out, _ = _forward(c, **kw)
+    assert bool(torch.isnan(out[bad]).all()) and bool((out[~bad] == clean[~bad]).all())
+
+
+def test_a_value_that_is_nan_in_requests_cut_between_ctas(lib):
+    for news in ([1], [40]):
+        c = Case([20001], news, 8, 1, 128, 64, seed=7)
+        clean, _ = _forward(c)
+        p, o = int(c.host_table[0, 9000 // 64]), 9000 % 64
+        c.cache.scales[p, 1, 0, o, 2], c.cache.codes[p, 1, 0, o, 32:48] = 255, 0
+        out, _ = _forward(c)
+        assert bool(torch.isnan(out[..., 64:96]).all())
+        assert bool((out[..., :64] == clean[..., :64]).all()) and bool((out[..., 96:] == clean[..., 96:]).all())
