@@ -10,13 +10,14 @@
 // there are eight.  tcgen05 would need both operands in shared memory, 16 bits
 // wide: 176 bytes a clock of an SM at the cache's full rate, where it has 128.
 //
-// Four-bit codes become fp16 with cvt (two an instruction), unscaled.  The
-// keys' scales are powers of two for 32 channels: they multiply the fp32
-// product of each block.  The values' scales multiply P: 2^(e - E + 7) with E
-// the largest exponent that the warp has met in the channel block, so that p up
-// to 2^8 times it fits fp16; what lies 22 binades below counts as zero.  m is
-// raised only when a score passes it by 8 (in log2), E when an exponent passes
-// it; then o is scaled.  q is fp16 times a power of two for each row: bf16
+// Four-bit codes become fp16 with cvt (two an instruction).  The keys' scales are
+// powers of two for 32 channels: they multiply the fp32 product of each block.
+// Values are fp16 numbers where their scale is 2^-23 to 2^13: one more product for
+// each pair of them.  (The scales times P instead, relative to the largest met, took less
+// and lost what lay 22 binades below it, also below tokens that a row does not see.)
+// A tile with other scales has them taken in bands of 37 binades, each with a
+// product of its own.  m is raised only when a score passes it by 8 (in log2);
+// then o is scaled.  q is fp16 times a power of two for each row: bf16
 // values have no more bits, and what is 2^-38 of the row's largest is lost.
 //
 // A warp works alone: it copies tiles of 16 tokens (keys, values and scales, 2176
@@ -54,7 +55,8 @@ constexpr int kThreads = kAttnWarps * 32;
 // to 16384 tokens 63.9, 58.4, 58.7, 60.0 and 62.0 us.
 constexpr int kPieceUnits = 4;
 constexpr float kLazy = 8.0f;      // how far scores may pass the maximum
-constexpr int kVBias = 7;          // P is scaled by 2^(e - E + kVBias)
+// Scale bytes with which every value is an fp16 number; others lie in bands of so many.
+constexpr int kLeastHalf = 104, kBand = 37;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -400,7 +402,6 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
         int last[NQ][2];   // position of this lane's two rows (columns of the products)
         float o[2 * kBlocks][NQ][4];
         float pass[NQ][2];         // what may pass m: kLazy, or nothing before there is an m
-        int vmax = 0;              // E of block lane % kBlocks
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -443,8 +444,18 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
             // Scales, each formed by one lane.  Keys: 2^(byte - 127) in fp32; byte 0 (2^-127) counts as
             // zero, 255 as infinity: its codes are zero, and zero times it NaN.
             const int vp = (lane / kBlocks) & 7, vk = lane % kBlocks;   // values: tokens 2 vp, 2 vp + 1 of block vk
-            uint32_t e[kTiles];
-            int emax = 0;
+            // (a tile's bytes for this lane's pair: what no row sees, written to or not, as any other)
+            auto value_bytes = [&](int u, uint32_t &e0, uint32_t &e1) {
+                const uint8_t *sv = ring + slot[u] + 2 * S::kCodes + S::kScales + 2 * vp * kBlocks + vk;
+                e0 = sv[0], e1 = sv[kBlocks];
+                if (edge) {
+                    const int t = t0 + u * kAttnChunk + 2 * vp, seen = a.window ? pos_lo - a.window : -1;
+                    const bool gone = !(have >> (kTiles - 1 - u) & 1u);
+                    if (gone || t > pos_hi || t <= seen) e0 = 127u;
+                    if (gone || t + 1 > pos_hi || t + 1 <= seen) e1 = 127u;
+                }
+            };
+            bool odd = false;   // a value's scale beyond fp16's
 #pragma unroll
             for (int u = 0; u < kTiles; ++u) {
                 const uint8_t *sc = ring + slot[u] + 2 * S::kCodes;
@@ -454,53 +465,23 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
                 } else {
                     s_ks[u * S::kScaleWords + lane] = __uint_as_float((uint32_t)sc[lane] << 23);
                 }
-                const uint8_t *sv = sc + S::kScales + 2 * vp * kBlocks + vk;
-                uint32_t e0 = sv[0], e1 = sv[kBlocks];
-                if (edge) {   // what no row sees, written to or not
-                    const int t = t0 + u * kAttnChunk + 2 * vp, seen = a.window ? pos_lo - a.window : -1;
-                    const bool gone = !(have >> (kTiles - 1 - u) & 1u);
-                    if (gone || t > pos_hi || t <= seen) e0 = 0;
-                    if (gone || t + 1 > pos_hi || t + 1 <= seen) e1 = 0;
-                }
-                e[u] = e0 | e1 << 16;
-                emax = max(emax, (int)max(e0, e1));
+                uint32_t e0, e1;
+                value_bytes(u, e0, e1);
+                odd |= e0 - kLeastHalf >= kBand || e1 - kLeastHalf >= kBand;
+                s_vs[u * S::kScaleWords + vp * kBlocks + vk] = half2_bits(__uint_as_float(e0 << 23), __uint_as_float(e1 << 23));
             }
-            bool nans = false;   // a value that is NaN, in these tiles
-            uint32_t nan_bits[kTiles];
-#pragma unroll
-            for (int u = 0; u < kTiles; ++u) nan_bits[u] = 0;
-            if (__any_sync(0xffffffffu, emax > vmax)) {
-                int v = vmax;
+            odd = __any_sync(0xffffffffu, odd);
+            // Band k: scale bytes kLeastHalf + k kBand .., as 2^(e - 127 - k kBand); 0 what is not in it
+            auto band_scale = [](uint32_t e, int k) {
+                const uint32_t from = e - (uint32_t)(kLeastHalf + k * kBand);
+                return e != 255u && from < kBand ? __uint_as_float((from + kLeastHalf) << 23) : 0.0f;
+            };
+            if (odd) {   // band 0 alone
 #pragma unroll
                 for (int u = 0; u < kTiles; ++u) {
-                    uint32_t e0 = e[u] & 0xffffu, e1 = e[u] >> 16;
-                    if (e0 == 255u) nan_bits[u] |= kNan, e0 = 0;
-                    if (e1 == 255u) nan_bits[u] |= kNan << 16, e1 = 0;
-                    nans |= nan_bits[u] != 0;
-                    e[u] = e0 | e1 << 16;
-                    v = max(v, (int)max(e0, e1));
-                }
-                nans = __any_sync(0xffffffffu, nans);
-#pragma unroll
-                for (int x = kBlocks; x <= 16; x <<= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, x));
-                const float f = ex2((float)(vmax - v));
-                vmax = v;
-#pragma unroll
-                for (int m = 0; m < kBlocks; ++m) {
-                    const float fm = __shfl_sync(0xffffffffu, f, m);
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) o[2 * m][n][j] *= fm, o[2 * m + 1][n][j] *= fm;
-                }
-            }
-            {
-                const uint32_t bias = (uint32_t)((15 + kVBias - vmax) & 0xffff) * 0x10001u;
-#pragma unroll
-                for (int u = 0; u < kTiles; ++u) {
-                    uint32_t f = __viaddmax_s16x2_relu(e[u], bias, 0u) << 10;
-                    if (nans) f = (f & ~((nan_bits[u] >> 15) * 0xffffu)) | nan_bits[u];
-                    s_vs[u * S::kScaleWords + vp * kBlocks + vk] = f;
+                    uint32_t e0, e1;
+                    value_bytes(u, e0, e1);
+                    s_vs[u * S::kScaleWords + vp * kBlocks + vk] = half2_bits(band_scale(e0, 0), band_scale(e1, 0));
                 }
             }
             __syncwarp();
@@ -605,31 +586,81 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
                     pt[n][0] = transposed8(half2_bits(p[0], p[1]));
                     pt[n][1] = transposed8(half2_bits(p[2], p[3]));
                 }
+                // Values of a tile, channel block k: of channels 4g .. 4g+3 of token 2c in the low half
+                // of the word, of token 2c + 1 in the high half (+ 8 in the second word)
+                auto values = [&](const uint32_t (&w)[4], int y, uint32_t f0, uint32_t f1, uint32_t (&v0)[4], uint32_t (&v1)[4]) {
+                    mx4_half8(token_pairs(w[2 * y]), v0);
+                    mx4_half8(token_pairs(w[2 * y + 1]), v1);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v0[j] = mul_half2(v0[j], f0), v1[j] = mul_half2(v1[j], f1);
+                };
+                const uint32_t values_at = ring_addr + slot[u] + S::kCodes + mrow * S::kRow;
                 // the values' scales of tokens 2c, 2c+1 and 2c+8, 2c+9
+                uint32_t *const scales = s_vs + u * S::kScaleWords;
                 uint32_t vs0[kBlocks], vs1[kBlocks];
-                load_blocks<kBlocks>(vs0, s_vs + u * S::kScaleWords + c * kBlocks);
-                load_blocks<kBlocks>(vs1, s_vs + u * S::kScaleWords + (c + 4) * kBlocks);
+                load_blocks<kBlocks>(vs0, scales + c * kBlocks);
+                load_blocks<kBlocks>(vs1, scales + (c + 4) * kBlocks);
                 // O^T += V^T P^T
 #pragma unroll
                 for (int x = 0; x < kBlocks / 2; ++x) {
                     uint32_t w[4];
-                    ldm4_trans(ring_addr + slot[u] + S::kCodes + mrow * S::kRow + swizzled<D>(mrow, 2 * x + mblk) * 16, w);
+                    ldm4_trans(values_at + swizzled<D>(mrow, 2 * x + mblk) * 16, w);
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const int k = 2 * x + y;
-                        // codes of channels 4g .. 4g+3 of block k: of token 2c in the low half
-                        // of the word, of token 2c + 1 in the high half (+ 8 in the second word)
                         uint32_t v0[4], v1[4];
-                        mx4_half8(token_pairs(w[2 * y]), v0);
-                        mx4_half8(token_pairs(w[2 * y + 1]), v1);
+                        values(w, y, vs0[k], vs1[k], v0, v1);
 #pragma unroll
                         for (int n = 0; n < NQ; ++n) {
-                            const uint32_t b0 = mul_half2(pt[n][0], vs0[k]), b1 = mul_half2(pt[n][1], vs1[k]);
-                            mma16816(o[2 * k][n], v0[0], v0[2], v1[0], v1[2], b0, b1);       // channels 4g, 4g + 1
-                            mma16816(o[2 * k + 1][n], v0[1], v0[3], v1[1], v1[3], b0, b1);   // 4g + 2, 4g + 3
+                            mma16816(o[2 * k][n], v0[0], v0[2], v1[0], v1[2], pt[n][0], pt[n][1]);       // channels 4g, 4g + 1
+                            mma16816(o[2 * k + 1][n], v0[1], v0[3], v1[1], v1[3], pt[n][0], pt[n][1]);   // 4g + 2, 4g + 3
                         }
                     }
                 }
+                if (!odd) continue;
+                uint32_t e0, e1;
+                value_bytes(u, e0, e1);
+#pragma unroll 1
+                for (int band = -3; band <= 4; ++band) {
+                    const float s0 = band_scale(e0, band), s1 = band_scale(e1, band);
+                    if (band == 0 || !__any_sync(0xffffffffu, s0 != 0.0f || s1 != 0.0f)) continue;
+                    __syncwarp();   // the scales before have been read
+                    scales[vp * kBlocks + vk] = half2_bits(s0, s1);
+                    __syncwarp();
+                    load_blocks<kBlocks>(vs0, scales + c * kBlocks);
+                    load_blocks<kBlocks>(vs1, scales + (c + 4) * kBlocks);
+                    // 2^(band kBand), which fp32 does not have for all bands: as two
+                    const float fa = __uint_as_float((uint32_t)(127 + band * (kBand / 2)) << 23);
+                    const float fb = __uint_as_float((uint32_t)(127 + band * (kBand - kBand / 2)) << 23);
+#pragma unroll
+                    for (int x = 0; x < kBlocks / 2; ++x) {
+                        uint32_t w[4];
+                        ldm4_trans(values_at + swizzled<D>(mrow, 2 * x + mblk) * 16, w);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int k = 2 * x + y;
+                            uint32_t v0[4], v1[4];
+                            values(w, y, vs0[k], vs1[k], v0, v1);
+#pragma unroll
+                            for (int n = 0; n < NQ; ++n) {
+                                float d0[4], d1[4];
+                                mma16816_first(d0, v0[0], v0[2], v1[0], v1[2], pt[n][0], pt[n][1]);
+                                mma16816_first(d1, v0[1], v0[3], v1[1], v1[3], pt[n][0], pt[n][1]);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    o[2 * k][n][j] += d0[j] * fa * fb, o[2 * k + 1][n][j] += d1[j] * fa * fb;
+                            }
+                        }
+                    }
+                }
+                // what is NaN: the scales' place has a mark for it now
+                const uint32_t marks = (e0 == 255u ? kNan : 0u) | (e1 == 255u ? kNan << 16 : 0u);
+                const bool nans = __any_sync(0xffffffffu, marks != 0);
+                __syncwarp();
+                scales[vp * kBlocks + vk] = marks;
+                __syncwarp();
+                load_blocks<kBlocks>(vs0, scales + c * kBlocks);
+                load_blocks<kBlocks>(vs1, scales + (c + 4) * kBlocks);
                 if (nans) {   // NaN for the rows that see it (not by P, which fp16 may have made zero), in its block
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
@@ -683,11 +714,9 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
                 const float mine = s_top[warp * S::kRows + rr], f = mine == m ? 1.0f : ex2(mine - m);
 #pragma unroll
                 for (int k = 0; k < kBlocks; ++k) {
-                    // 2^(E - 127 - kVBias)
-                    const float fe = f * (mx4_scale((uint32_t)__shfl_sync(0xffffffffu, vmax, k)) * exp2f(-kVBias));
                     *reinterpret_cast<float4 *>(s_o + ((warp * 8 + 2 * c + j) * D + 32 * k + 4 * g)) =
-                        make_float4(o[2 * k][n][j] * fe, o[2 * k][n][j + 2] * fe, o[2 * k + 1][n][j] * fe,
-                                    o[2 * k + 1][n][j + 2] * fe);
+                        make_float4(o[2 * k][n][j] * f, o[2 * k][n][j + 2] * f, o[2 * k + 1][n][j] * f,
+                                    o[2 * k + 1][n][j + 2] * f);
                 }
             }
             __syncthreads();

@@ -13,9 +13,9 @@
 // 8-11 unpack keys and values; warp 12 issues the products.
 //
 // A key's value, a code of two significant bits times a power of two, is a bf16 number
-// whatever its scale, and so is q: S has no error but its sum's.  Codes of values become
-// fp16 (cvt) times 2^(e - E + 13), E the largest exponent that the piece has met; what lies 28
-// binades below E counts as zero.  Where E grows, O is scaled when P is made.
+// whatever its scale, and so is q: S has no error but its sum's.  A value is an fp16 number where
+// its scale is 2^-23 to 2^13.  A tile that has others takes its values as bf16, and P as two bf16
+// numbers (16 bits) whose products follow one another: nothing depends on what a row does not see.
 // m is raised only where a score passes it by 8 (in log2), so
 // S is read once and O hardly ever; it rises by whole powers of two.  A value that is
 // NaN counts as zero in the products; rows that see it remember its block.
@@ -45,6 +45,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "attention4.cuh"
 #include "mx4.cuh"
@@ -64,7 +65,7 @@ constexpr int kTmemCols = 512;
 // 1194 and 1199 us where 4 and 6 tied).
 constexpr int kPieceTiles = 5;
 constexpr float kLazy = 8.0f;
-constexpr int kBias = 13;
+constexpr uint32_t kLeastHalf = 104, kMostHalf = 140;   // scale bytes with which every code is an fp16 number
 
 struct WideArgs {
     AttnArgs a;
@@ -82,6 +83,10 @@ __device__ __forceinline__ float ex2w(float x) {
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t bf162_of(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&b);
 }
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
     const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
@@ -140,9 +145,10 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t bdes
         "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// fp16 operands, A K-major, B with channels contiguous
-__host__ __device__ constexpr uint32_t idesc_f16_mn(int M, int N) {
-    return (1u << 4) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// fp16 or bf16 operands, A K-major, B with channels contiguous
+__host__ __device__ constexpr uint32_t idesc_mn(int M, int N, bool bf16) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (1u << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
 }
 // V: rows of 128 bytes (64 channels of a token), 128-byte swizzle; eight tokens 1024 bytes,
 // the next 64 channels kTok rows on
@@ -290,9 +296,8 @@ struct Walk {
 };
 
 struct Info {          // of a tile of tokens, from those who unpack it
-    float grown;       // what O is to be multiplied by before this tile
-    float ev;          // 2^(E - 127 - kBias) of the values so far
     uint32_t bad;      // bit i: tokens 16 i .. are on a page that is not there
+    uint32_t bf16;     // values are bf16, P is two numbers
     uint32_t nan;      // a value of the tile is NaN
 };
 
@@ -307,6 +312,60 @@ struct WideShape {
     static constexpr int kO = 2 * kTok;                    // columns: S of both halves, then O
 };
 
+// A row's maximum, what may pass it, its sum, and what O is to be multiplied by.
+struct RowState {
+    float ref, pass, sum, shrink;
+};
+
+// P of a tile (scores at ts, this row's columns from < t <= upto, but for bad pages) as two bf16 numbers
+// each: 16 columns become eight of the larger parts and eight of what they leave.  The largest score is
+// looked for first, so that nothing has to be scaled.  A function of its own: in line it slowed the
+// tiles that need none of it (prompts 1306 us for 1223; without any second way 1200).
+__device__ __noinline__ RowState two_bf16(uint32_t ts, int upto, int from, uint32_t bad, float scale_log2, RowState r) {
+    auto sixteen = [&](int k, float (&x)[16]) {
+        uint32_t y[16];
+        tmem_ld16(ts + 16 * k, y);
+        tmem_wait_ld(y);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int t = 16 * k + i;
+            x[i] = t <= upto && t > from && !(bad >> k & 1u) ? fmaf(__uint_as_float(y[i]), scale_log2, -r.ref) : -INFINITY;
+        }
+    };
+    float top = -INFINITY, x[16];
+#pragma unroll 1
+    for (int k = 0; k < kTok / 16; ++k) {
+        sixteen(k, x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, x[i]);
+    }
+    if (top > r.pass) {
+        const bool none = r.pass == -INFINITY;
+        const float rise = none ? ceilf(top) : fmaxf(ceilf(top), 0.0f), f = none ? 1.0f : ex2w(-rise);
+        r.pass = kLazy;
+        r.ref += rise;
+        r.sum *= f;
+        r.shrink *= f;
+    }
+    F2 part = 0ull;
+#pragma unroll 1
+    for (int k = 0; k < kTok / 16; ++k) {
+        uint32_t y[16];
+        sixteen(k, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float p0 = ex2w(x[2 * i]), p1 = ex2w(x[2 * i + 1]);
+            part = add2(part, pack2(__float_as_uint(p0), __float_as_uint(p1)));
+            y[i] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+            y[8 + i] = bf162_of(p0 - __uint_as_float(__float_as_uint(p0) & 0xffff0000u),
+                                p1 - __uint_as_float(__float_as_uint(p1) & 0xffff0000u));
+        }
+        tmem_st16(ts + 16 * k, y);
+    }
+    r.sum += __uint_as_float((uint32_t)part) + __uint_as_float((uint32_t)(part >> 32));
+    return r;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const WideArgs w) {
     using S = WideShape<D>;
@@ -317,7 +376,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
     __shared__ uint64_t e_full[2];
     __shared__ Info s_info[kInfos];
     __shared__ uint2 s_nan[kInfos][kTok / 2];        // a byte for each token and channel block
-    __shared__ uint4 s_e[2][kUnpackWarps];           // each warp's largest exponents, bad pages, NaN
+    __shared__ uint4 s_e[2][kUnpackWarps];           // each warp's bad pages, NaN, scales beyond fp16's
     __shared__ uint32_t tmem_slot;
     __shared__ int s_abort;
     const AttnArgs &a = w.a;
@@ -411,7 +470,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             if (lane == 0) mbar_arrive(smem_u32(&q_full));
             const int pos = p.r.len - p.r.n + (p.g.rowbase + min(rr, p.g.nrows - 1)) / a.G;
             const bool used = mt == 0 || p.g.nrows > kM;
-            float ref = 0.0f, pass = -INFINITY, sum = 0.0f, ev = 0.0f;
+            float ref = 0.0f, pass = -INFINITY, sum = 0.0f;
             uint32_t nans = 0;   // channel blocks that are NaN for this row
             for (int c = p.c0; c < p.c1; ++c, ++tiles) {
                 if (!used) continue;
@@ -421,17 +480,22 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 if (!ok) break;
                 tc_fence_after();
                 const Info info = s_info[in];
-                ev = info.ev;
                 const int t0 = p.g.lo + c * kTok;
                 const bool edge = t0 + kTok - 1 > p.g.pos_lo || (a.window && t0 <= p.g.pos_hi - a.window) || info.bad;
                 const int upto = pos - t0, from = a.window ? pos - a.window - t0 : -1;   // columns from < i <= upto
-                float shrink = info.grown;
+                float shrink = 1.0f;   // what O is to be multiplied by before this tile
+                F2 part[2] = {0ull, 0ull};
+                int q0 = 0;   // the first 32 columns to be taken here
+                if (info.bf16) {
+                    const RowState st = two_bf16(ts, upto, from, info.bad, a.scale_log2, {ref, pass, sum, shrink});
+                    ref = st.ref, pass = st.pass, sum = st.sum, shrink = st.shrink;
+                    q0 = kTok / 32;
+                }
                 // 32 columns at a time (a small loop: unrolled, its code did not stay in the
                 // instruction cache): their P takes the place of S that has been read.
                 uint32_t r[2][16];
                 tmem_ld16(ts, r[0]);
                 tmem_ld16(ts + 16, r[1]);
-                F2 part[2] = {0ull, 0ull};
                 // scores of 32 columns from r, past m, hidden ones at minus infinity
                 auto scores = [&](int q, float (&x)[32]) {
                     const F2 xs2 = pack2(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
@@ -464,7 +528,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                     return fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                 };
 #pragma unroll 1
-                for (int q = 0; q < kTok / 32; ++q) {
+                for (int q = q0; q < kTok / 32; ++q) {
                     float x[32];
                     uint32_t pk[16];
                     tmem_wait_ld(r[0]);
@@ -526,6 +590,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                     part[1] = add2(part[1], more[1]);
                     tmem_st16(ts + 16 * q, pk);
                 }
+                tmem_wait_ld(r[0]);   // (where the loop took none)
+                tmem_wait_ld(r[1]);
                 part[0] = add2(part[0], part[1]);
                 sum += __uint_as_float((uint32_t)part[0]) + __uint_as_float((uint32_t)(part[0] >> 32));
                 if (c > p.c0 && __any_sync(0xffffffffu, shrink != 1.0f)) {   // S was there: the products before it are done
@@ -564,7 +630,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 a.cuts[blockIdx.x] = cut;
             }
             float *dst = a.part + (int64_t)(2 * blockIdx.x + (p.c0 == 0)) * kWideRows * (D + 2);
-            const float inv = !whole ? ev : sum == 0.0f ? 0.0f : ev / sum;
+            const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
             if (!whole) dst[kWideRows * D + rr] = pass == -INFINITY ? -INFINITY : ref, dst[kWideRows * (D + 1) + rr] = sum;
             else if (there && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.69314718f;
             if (used) {
@@ -689,24 +755,23 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
             load_scales(p.c0);
             load_ids(p.c0 + 1);
             load_codes(kc, 0);
-            int erun = 0;   // E of the values so far
             for (int c = p.c0; c < p.c1; ++c, ++tiles) {
                 const uint32_t stage = tiles % kStages, in = tiles % kInfos;
-                uint32_t bad = next_lost, nan = 0, far = 0, mv = 0;   // of all the warp's tokens
+                uint32_t bad = next_lost, nan = 0, far = 0, odd = 0;   // of all the warp's tokens
 #pragma unroll
                 for (int i = 0; i < I; ++i) {
                     // rows behind the last token may hold anything
                     const bool seen = 32 * dw + kRoundRows * i + pr < next_seen;
                     kb[i] = seen ? kn[i] : 0u, vb[i] = seen ? vn[i] : 0u;
                     far |= kb[i] > 142u;
-                    if (vb[i] != 255u) mv = max(mv, vb[i]);
-                    else nan = 1;
+                    nan |= vb[i] == 255u;
+                    odd |= seen && vb[i] - kLeastHalf > kMostHalf - kLeastHalf && vb[i] != 255u;
                 }
-                mv = __reduce_max_sync(0xffffffffu, mv);
                 nan = __any_sync(0xffffffffu, nan);
                 far = __any_sync(0xffffffffu, far);
+                odd = __any_sync(0xffffffffu, odd);
                 if (lane == 0) {
-                    s_e[tiles & 1][dw] = make_uint4(mv, bad, nan, 0);
+                    s_e[tiles & 1][dw] = make_uint4(bad, nan, odd, 0);
                     mbar_arrive(smem_u32(&e_full[tiles & 1]));
                 }
                 load_codes(vc, kv_rows);
@@ -714,19 +779,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 load_ids(c + 2);
                 ok = wait(e_full[tiles & 1], (tiles >> 1) & 1);
                 if (!ok) break;
-                int ev = erun;
 #pragma unroll
                 for (int x = 0; x < kUnpackWarps; ++x) {
                     const uint4 e = s_e[tiles & 1][x];
-                    ev = max(ev, (int)e.x), bad |= e.y, nan |= e.z;
+                    bad |= e.x, nan |= e.y, odd |= e.z;
                 }
                 ok = wait(k_empty[stage], ((tiles / kStages) & 1) ^ 1u);
                 if (!ok) break;
                 if (dw == 0 && lane == 0) {
                     Info info;
-                    info.grown = ev == erun || c == p.c0 ? 1.0f : ex2w((float)(erun - ev));
-                    info.ev = ex2w((float)(ev - 127 - kBias));
-                    info.bad = bad, info.nan = nan;
+                    info.bad = bad, info.nan = nan, info.bf16 = odd;
                     s_info[in] = info;
                 }
                 if (nan)
@@ -737,7 +799,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                         n[0] = vb[i] == 255u;
                         if (kIn == 2) n[2] = 0;
                     }
-                erun = ev;
                 // codes of 32 channels (a lane's 16 bytes) of token t to shared memory, by `to16` of pairs
                 auto widen = [&](const uint4 &codes, uint8_t *dst, int t, auto to16) {
                     const uint32_t x[4] = {codes.x, codes.y, codes.z, codes.w};
@@ -750,6 +811,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                             make_uint4(to16(hv[0]), to16(hv[1]), to16(hv[2]), to16(hv[3]));
                     }
                 };
+                // where piece i of this lane's is, and what a scale has beyond bf16's one factor
+                auto piece_at = [&](uint8_t *dst, int i) {
+                    const int t = 32 * dw + kRoundRows * (i >> 2) + pr;
+                    return reinterpret_cast<uint4 *>(dst + (pc >> 1) * S::kHalf + t * 128 + ((((pc & 1) * 4 + (i & 3)) ^ (t & 7)) << 4));
+                };
+                auto beyond = [](uint32_t byte) { return ((127u + max((int)byte - 142, 0)) << 7) * 0x10001u; };
                 // Keys: bf16, 2^(e - 127) by way of 2^-112 and 2^(e - 15); from 2^16 on that passes bf16's
                 // largest and is made of two
 #pragma unroll
@@ -762,11 +829,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 if (far)   // (its own small loop: in line, it would be in the instruction cache's way)
 #pragma unroll 1
                     for (int i = 0; i < 4 * I; ++i) {
-                        const int t = 32 * dw + kRoundRows * (i >> 2) + pr;
-                        const uint32_t byte = i < 4 ? kb[0] : i < 8 ? kb[1] : i < 12 ? kb[2 % I] : kb[3 % I];
-                        const uint32_t g = ((127u + max((int)byte - 142, 0)) << 7) * 0x10001u;
-                        uint4 *const at = reinterpret_cast<uint4 *>(smem + S::kK + stage * S::kTileBytes + (pc >> 1) * S::kHalf +
-                                                                    t * 128 + ((((pc & 1) * 4 + (i & 3)) ^ (t & 7)) << 4));
+                        const uint32_t g = beyond(i < 4 ? kb[0] : i < 8 ? kb[1] : i < 12 ? kb[2 % I] : kb[3 % I]);
+                        uint4 *const at = piece_at(smem + S::kK + stage * S::kTileBytes, i);
                         const uint4 y = *at;
                         *at = make_uint4(mul_bf162(y.x, g), mul_bf162(y.y, g), mul_bf162(y.z, g), mul_bf162(y.w, g));
                     }
@@ -781,11 +845,21 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                 if (!ok) break;
 #pragma unroll
                 for (int i = 0; i < I; ++i)
-                {   // values: fp16, times 2^(e - E + kBias)
-                    const uint32_t f = vb[i] == 255u ? 0u : ((uint32_t)max((int)vb[i] - ev + kBias + 15, 0) << 10) * 0x10001u;
+                {   // values: fp16 times 2^(e - 127), or unscaled where the tile's are bf16
+                    const uint32_t f = odd ? 0x3c003c00u : vb[i] == 255u ? 0u : half2_of(__uint_as_float(vb[i] << 23), __uint_as_float(vb[i] << 23));
                     widen(vc[i], smem + S::kV + stage * S::kTileBytes, 32 * dw + kRoundRows * i + pr,
                           [&](uint32_t h) { return mul_half2(h, f); });
                 }
+                if (odd)   // to bf16, as keys
+#pragma unroll 1
+                    for (int i = 0; i < 4 * I; ++i) {
+                        const uint32_t byte = i < 4 ? vb[0] : i < 8 ? vb[1] : i < 12 ? vb[2 % I] : vb[3 % I];
+                        const uint32_t f = byte == 255u ? 0u : (min(byte + 112u, 254u) << 7) * 0x10001u, g = beyond(byte);
+                        uint4 *const at = piece_at(smem + S::kV + stage * S::kTileBytes, i);
+                        const uint4 y = *at;
+                        auto to16 = [&](uint32_t h) { return mul_bf162(mul_bf162(bf16_of_half2(h), f), g); };
+                        *at = make_uint4(to16(y.x), to16(y.y), to16(y.z), to16(y.w));
+                    }
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&v_full[stage]));
@@ -794,7 +868,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
     } else {
         // ---- products ---------------------------------------------------------------------
         const bool elected = elect_one();
-        constexpr uint32_t kQK = idesc_bf16(kM, kTok), kPV = idesc_f16_mn(kM, D);
+        constexpr uint32_t kQK = idesc_bf16(kM, kTok), kPV = idesc_mn(kM, D, false), kPV2 = idesc_mn(kM, D, true);
         uint32_t made[2] = {0, 0};   // P of each half that products have taken
         while (ok && walk.next(w, entries, p)) {
             if (p.c0 == p.c1) continue;
@@ -833,9 +907,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                     tc_fence_after();
                     if (elected) {
                         const uint64_t v = sdesc_mn_sw128(base + S::kV + stage * S::kTileBytes);
+                        const uint32_t p16 = tmem + mt * kTok, o = tmem + S::kO + mt * D;
+                        if (!s_info[tiles % kInfos].bf16) {
 #pragma unroll
-                        for (int s = 0; s < kTok / 16; ++s)
-                            mma_f16_ta(tmem + S::kO + mt * D, tmem + mt * kTok + 8 * s, v + s * (2048 >> 4), kPV, j > 0 || s > 0);
+                            for (int s = 0; s < kTok / 16; ++s)
+                                mma_f16_ta(o, p16 + 8 * s, v + s * (2048 >> 4), kPV, j > 0 || s > 0);
+                        } else {
+#pragma unroll 1
+                            for (int s = 0; s < kTok / 16; ++s) {
+                                const uint32_t at = p16 + 16 * s;
+                                mma_f16_ta(o, at, v + s * (2048 >> 4), kPV2, j > 0 || s > 0);
+                                mma_f16_ta(o, at + 8, v + s * (2048 >> 4), kPV2, 1);
+                            }
+                        }
                         if (mt == halves - 1) mma_commit(smem_u32(&v_empty[stage]));
                     }
                     __syncwarp();

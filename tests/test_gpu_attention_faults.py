@@ -176,3 +176,56 @@ def test_a_value_that_is_nan_in_requests_cut_between_ctas(lib):
         out, _ = _forward(c)
         assert bool(torch.isnan(out[..., 64:96]).all())
         assert bool((out[..., :64] == clean[..., :64]).all()) and bool((out[..., 96:] == clean[..., 96:]).all())
+
+
+@pytest.mark.parametrize("news", ROWS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("more", [20, 30, 90])
+@pytest.mark.parametrize("where", [0, 130, -2])
+def test_one_value_far_above_the_others(lib, news, D, more, where):
+    """A block of one value 2^more above the others: rows that stand before it and other channels are as they were."""
+    c = Case([news[0] + 200], news, 8, 2, D, 16, seed=more)
+    c.poison_stale()
+    at = where % c.lens[0]
+    p, o = int(c.host_table[0, at // 16]), at % 16
+    c.cache.scales[p, 1, :, o, 1] += more
+    _strict(c, *_forward(c))
+
+
+@pytest.mark.parametrize("news", ROWS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shift", [-110, -40, -28, 8, 12, 30, 90])
+def test_values_of_any_size(lib, news, D, shift):
+    """All values times 2^shift, with a token whose values are zero (its blocks' scale is 1) among them."""
+    c = Case([news[0] + 77], news, 8, 2, D, 32, seed=shift + 110)
+    c.poison_stale()
+    scales = c.cache.scales[:, 1]
+    c.cache.scales[:, 1] = torch.where(scales == 255, 255, scales.int() + shift).to(torch.uint8)
+    p = int(c.host_table[0, 1])
+    c.cache.scales[p, 1, :, 5], c.cache.codes[p, 1, :, 5] = 127, 0
+    _strict(c, *_forward(c))
+
+
+@pytest.mark.parametrize("news", [[3], [40], [300], [1, 70, 4]])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("share", [0.002, 0.05, 1.0])
+@pytest.mark.parametrize("window", [0, 150])
+def test_values_of_all_sizes_together(lib, news, D, share, window):
+    """Scale bytes of 2 to 220 for a share of the blocks: every row and channel to what its own terms allow."""
+    c = Case([n + 500 for n in news], news, 8, 2, D, 16, seed=D)
+    c.poison_stale()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    s = c.cache.scales[:, 1]
+    odd = (torch.rand(s.shape, device="cuda", generator=g) < share) & (s != 255)
+    c.cache.scales[:, 1] = torch.where(odd, torch.randint(2, 221, s.shape, device="cuda", generator=g).to(torch.uint8), s)
+    _strict(c, *_forward(c, window=window), window=window)
+
+
+def test_values_of_all_sizes_in_requests_cut_between_ctas(lib):
+    for news, D in (([1], 128), ([5], 64), ([40], 128)):
+        c = Case([30001], news, 8, 1, D, 64, seed=7)
+        g = torch.Generator(device="cuda").manual_seed(2)
+        s = c.cache.scales[:, 1]
+        odd = torch.rand(s.shape, device="cuda", generator=g) < 0.001
+        c.cache.scales[:, 1] = torch.where(odd, torch.randint(60, 180, s.shape, device="cuda", generator=g).to(torch.uint8), s)
+        _strict(c, *_forward(c))
