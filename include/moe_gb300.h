@@ -647,7 +647,9 @@ MOE_API int moe_cache_read(const moe_cache4 *cache, int32_t n, const int32_t *sl
  * ids outside [0, pages) set MOE_DEV_BAD_INDEX: such a request is not computed,
  * the tokens of such a page are not seen.
  * Scores and sums are fp32; probabilities are rounded to fp16 before the sum of
- * the values (relative 2^-11 each).  Keys and values count whatever their size:
+ * the values: each is off by 2^-11 of itself at most, or by 2^-36 of the row's
+ * largest where that is more (2^-30 where a request has more than 32 rows, of
+ * query tokens times heads of a KV head).  Keys and values count whatever their size:
  * nothing that a row does not see changes its result.
  *   desc.max_q    the most query rows of one request, and
  *   desc.max_len  the longest request: what the kernels and the workspace are

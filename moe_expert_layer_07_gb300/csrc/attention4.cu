@@ -2,7 +2,7 @@
 //   o = sum_j softmax_j(scale q . k_j) v_j
 //
 // One pass over the tokens with a running maximum m and sum l for each row:
-//   s = scale log2(e) q . k,  p = 2^(s - m),  l += p,  o += p v
+//   s = scale log2(e) q . k,  p = 2^(s - m + 11),  l += p,  o += p v
 // Rows are the query heads of one KV head, for one or more query tokens; 8, 16
 // or 32 of them are the N side of the tensor cores' mma.sync m16n8k16, tokens
 // (for S^T = K Q^T) and channels (for O^T = V^T P^T) the M side, so that a key
@@ -16,7 +16,7 @@
 // each pair of them.  (The scales times P instead, relative to the largest met, took less
 // and lost what lay 22 binades below it, also below tokens that a row does not see.)
 // A tile with other scales has them taken in bands of 37 binades, each with a
-// product of its own.  m is raised only when a score passes it by 8 (in log2);
+// product of its own.  m is raised only when a score passes it by 4 (in log2);
 // then o is scaled.  q is fp16 times a power of two for each row: bf16
 // values have no more bits, and what is 2^-38 of the row's largest is lost.
 //
@@ -54,7 +54,7 @@ constexpr int kThreads = kAttnWarps * 32;
 // way from memory, the warps' sums.  Measured with 3, 4, 5, 6 and 8: 48 requests of 64
 // to 16384 tokens 63.9, 58.4, 58.7, 60.0 and 62.0 us.
 constexpr int kPieceUnits = 4;
-constexpr float kLazy = 8.0f;      // how far scores may pass the maximum
+constexpr float kRest = 11.0f;     // where a raised maximum is put (log2)
 // Scale bytes with which every value is an fp16 number; others lie in bands of so many.
 constexpr int kLeastHalf = 104, kBand = 37;
 
@@ -398,10 +398,10 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
             for (int k = 0; k < D / 16; ++k)
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) qf[k][n] = s_q[(k * NQ + n) * 32 + lane];
-        float mult[NQ][2], ref[NQ][2], sum[NQ][2];   // ref: m, 0 before there is one
+        float mult[NQ][2], ref[NQ][2], sum[NQ][2];   // ref: m - 11, 0 before there is one
         int last[NQ][2];   // position of this lane's two rows (columns of the products)
         float o[2 * kBlocks][NQ][4];
-        float pass[NQ][2];         // what may pass m: kLazy, or nothing before there is an m
+        float pass[NQ][2];         // what may pass ref: kAttnTop, or nothing before there is an m
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -559,10 +559,10 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
 #pragma unroll
                         for (int x = 4; x <= 16; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
                         // how far m moves
-                        const float up = v == -INFINITY ? 0.0f : pass[n][j] == -INFINITY ? v : fmaxf(v, 0.0f);
+                        const float up = v == -INFINITY ? 0.0f : pass[n][j] == -INFINITY ? v - kRest : fmaxf(v - kRest, 0.0f);
                         // before there is an m there is nothing to scale
                         const float f = pass[n][j] == -INFINITY ? 1.0f : ex2(-up);
-                        if (v != -INFINITY) pass[n][j] = kLazy;
+                        if (v != -INFINITY) pass[n][j] = kAttnTop;
                         ref[n][j] += up;
                         sum[n][j] *= f;
 #pragma unroll

@@ -13,6 +13,12 @@ constexpr int kAttnTile = 16;      // tokens of a tile
 constexpr int kAttnWarps = 8;
 constexpr int kAttnChunk = kAttnTile * kAttnWarps;   // tokens of a unit of work
 
+// Probabilities are 2^(score - ref), fp16 in the products.  They may be up to 2^kAttnTop; where one passes
+// that, ref rises so that the largest is 2^11 (few rows) or 2^7 (many).  fp16 has all of its bits down to
+// 2^-14, 2^-25 and 2^-21 of the row's largest, and some down to 2^-24.  (With the largest at 2^0 tokens of
+// 2^-14 lost bits and of 2^-25 were gone: all of the result where the largest one's value is zero.)
+constexpr float kAttnTop = 15.0f;
+
 // What a CTA began and others went on with: `nrows` rows (0: nothing) from row rowbase
 // of a request whose query rows begin at row0, of the heads from head0, as far as CTA
 // `last`.
@@ -27,7 +33,7 @@ struct AttnArgs {
     void *out;
     float *lse;
     int32_t *status;
-    // partial results, two to a CTA: weighted sums [rows, D], then top and sum of each row
+    // partial results, two to a CTA: weighted sums [rows, D], then ref and sum of each row
     float *part;
     AttnCut *cuts;   // [CTAs]
     int B, rows, Hq, Hk, G, max_pages, pages, page_shift, window, out_bf16, ctas;

@@ -1,6 +1,6 @@
 // Attention of many query rows over the four-bit cache (chunks of prompts), on
 // the tensor cores' fifth-generation kinds:
-//   S = Q K^T,  P = 2^(S - m),  O += P V,  o = O / sum P
+//   S = Q K^T,  P = 2^(S - m + 7),  O += P V,  o = O / sum P
 //
 // A CTA takes 256 rows (query heads of one KV head, query tokens one after the
 // other) as two tiles of 128, and passes over the keys and values in tiles of
@@ -64,7 +64,9 @@ constexpr int kTmemCols = 512;
 // What the beginning and end of a piece cost, in tiles (with 2, 3, 4 and 6: 1330, 1250,
 // 1194 and 1199 us where 4 and 6 tied).
 constexpr int kPieceTiles = 5;
-constexpr float kLazy = 8.0f;
+// Where a raised maximum is put (log2).  Raising it scales O and is dear: chunks of 4096, 500 and 2000 onto 8192, 4096
+// and 6000 take 1179 us with scores of deviation 1, 1200 of 2 and 1374 of 4; with 11 instead 1208, 1388 and 1572.
+constexpr float kRest = 7.0f;
 constexpr uint32_t kLeastHalf = 104, kMostHalf = 140;   // scale bytes with which every code is an fp16 number
 
 struct WideArgs {
@@ -341,8 +343,8 @@ __device__ __noinline__ RowState two_bf16(uint32_t ts, int upto, int from, uint3
     }
     if (top > r.pass) {
         const bool none = r.pass == -INFINITY;
-        const float rise = none ? ceilf(top) : fmaxf(ceilf(top), 0.0f), f = none ? 1.0f : ex2w(-rise);
-        r.pass = kLazy;
+        const float rise = none ? ceilf(top) - kRest : fmaxf(ceilf(top) - kRest, 0.0f), f = none ? 1.0f : ex2w(-rise);
+        r.pass = kAttnTop;
         r.ref += rise;
         r.sum *= f;
         r.shrink *= f;
@@ -555,23 +557,32 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                         // m rises by whole powers of two, so that what is scaled stays exact
                         // before there is an m there is nothing to scale
                         const bool none = pass == -INFINITY;
-                        const float rise = top == -INFINITY ? 0.0f : none ? ceilf(top) : fmaxf(ceilf(top), 0.0f);
-                        if (top != -INFINITY) pass = kLazy;
+                        const float rise = top == -INFINITY ? 0.0f : none ? ceilf(top) - kRest : fmaxf(ceilf(top) - kRest, 0.0f);
+                        if (top != -INFINITY) pass = kAttnTop;
                         ref += rise;
                         const float f = none ? 1.0f : ex2w(-rise);
                         sum *= f;
                         shrink *= f;
 #pragma unroll
                         for (int i = 0; i < 2; ++i) part[i] = mul2(part[i], pack2(__float_as_uint(f), __float_as_uint(f)));
-                        const uint32_t f2 = half2_of(f, f);
                         tmem_wait_st();
+                        // P so far times f, at most 2^-14 at a time (fp16 has no 2^-25); below 2^-42 nothing is left
+                        float left = f;
 #pragma unroll 1
-                        for (int z = 0; z < 2 * q; ++z) {   // P so far
-                            uint32_t y[8];
-                            tmem_get8(ts + 8 * z, y);
+                        for (int times = 0; times < 3; ++times) {
+                            const float part16 = fmaxf(left, 0x1p-14f);
+                            const uint32_t f2 = half2_of(part16, part16);
+#pragma unroll 1
+                            for (int z = 0; z < 2 * q; ++z) {
+                                uint32_t y[8];
+                                tmem_get8(ts + 8 * z, y);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) y[i] = mul_half2(y[i], f2);
-                            tmem_st8(ts + 8 * z, y);
+                                for (int i = 0; i < 8; ++i) y[i] = mul_half2(y[i], f2);
+                                tmem_st8(ts + 8 * z, y);
+                            }
+                            if (!__any_sync(0xffffffffu, left < 0x1p-14f)) break;
+                            tmem_wait_st();
+                            left = left < 0x1p-14f ? left * 0x1p14f : 1.0f;
                         }
                         // these columns again, and the next ones' loads
                         tmem_ld16(ts + 32 * q, r[0]);

@@ -4,10 +4,12 @@ bound for each row and channel that knows only what that row sees.
 
 Tolerance.  Scores: as in test_gpu_attention.py, off by d <= 2^-19 sum |q k| scale, so a weight by
 exp(2 d) - 1 <= 4 d of itself (d small); 2^-16 for exponentials and sums.  Probabilities are rounded to fp16,
-2^-11 of themselves; below 2^-14 of the largest fp16 has steps of 2^-24 and they are off by half a step, 2^-25 of
-the largest, and by another half where they are scaled down with a maximum that rises: LEAST.  So a row's
-channel is off by sum_j |v_j| (w_j (2^-11 + 4 d + 2^-16) + LEAST max_i w_i), by 2^-24 of sum_j w_j |v_j| for the sum in
-fp32, and by half a step of the output's type; nothing that the row does not see adds to it."""
+2^-11 of themselves.  They are held as 2^(score - ref), a row's largest as 2^11 at least, or 2^6 with more than 32 rows
+(2^7, ref is whole there).  Where they fall below 2^-14 they are off by half of fp16's smallest step, 2^-25, and of many
+rows again wherever they are scaled down with ref, by 2 and more each time: 2^-25 / 2^11 = 2^-36 and 2 2^-25 / 2^6 = 2^-30 of
+the row's largest: least.  So a row's channel is off by sum_j |v_j| (w_j (2^-11 + 4 d + 2^-16) + least max_i w_i), by
+2^-24 of sum_j w_j |v_j| for the sum in fp32, and by half a step of the output's type; nothing that the row does not
+see adds to it."""
 from __future__ import annotations
 
 import math
@@ -22,7 +24,6 @@ from test_gpu_attention import Case
 
 pytestmark = pytest.mark.gpu
 I32, BF, F32 = torch.int32, torch.bfloat16, torch.float32
-LEAST = 2.0 ** -24
 
 
 @pytest.fixture(scope="module")
@@ -58,7 +59,8 @@ def _strict(case, out, lse=None, window=0, lost=(), only=None):
         d = d.amax(-1, keepdim=True)
         z = torch.logsumexp(x, -1, keepdim=True)
         w = torch.exp(x - z)
-        off = w * (2.0 ** -11 + 4 * d + 2.0 ** -16 + 2.0 ** -24) + torch.where(seen, LEAST * w.amax(-1, keepdim=True), 0.0)
+        least = 2.0 ** (-30 if n * G > 32 else -36)
+        off = w * (2.0 ** -11 + 4 * d + 2.0 ** -16 + 2.0 ** -24) + torch.where(seen, least * w.amax(-1, keepdim=True), 0.0)
         va = v.abs()
         ref, bound = torch.einsum("nhgl,hld->nhgd", w, v), torch.einsum("nhgl,hld->nhgd", off, va)
         got = out[rows].double().reshape(ref.shape)
@@ -229,3 +231,43 @@ def test_values_of_all_sizes_in_requests_cut_between_ctas(lib):
         odd = torch.rand(s.shape, device="cuda", generator=g) < 0.001
         c.cache.scales[:, 1] = torch.where(odd, torch.randint(60, 180, s.shape, device="cuda", generator=g).to(torch.uint8), s)
         _strict(c, *_forward(c))
+
+
+@pytest.mark.parametrize("news", ROWS + [[1, 50]])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("below", [8, 12, 15, 18])
+@pytest.mark.parametrize("where", [0, 8000])
+def test_results_of_probabilities_far_below_the_largest(lib, news, D, below, where):
+    """One key `below` natural logarithms above 8000 others, and its values zero: the others are the result."""
+    c = Case([8100 + n for n in news], news, 8, 2, D, 64, seed=below)
+    c.cache.scales[:, 0, :, :, 0] = 127
+    c.cache.codes[:, 0, :, :, :16] = 0xbb   # -1.5 each
+    c.q[..., :32] = below * D ** 0.5 / 96
+    c.q[..., 32:] *= 0.3
+    c.cache.codes[:, 1] &= 0x77   # no value below zero: nothing cancels
+    for b in range(len(news)):
+        p, o = int(c.host_table[b, where // 64]), where % 64
+        c.cache.codes[p, 0, :, o, :16] = 0x33   # 1.5
+        c.cache.codes[p, 1, :, o] = 0
+    _strict(c, *_forward(c))
+
+
+@pytest.mark.parametrize("news", ROWS)
+@pytest.mark.parametrize("step", [1, 3, 13, 40])
+def test_scores_that_rise_all_the_way(lib, news, step):
+    """Scores that grow by `step` (log2) every 32 or 16 tokens, so that the maximum rises within and between tiles."""
+    c = Case([900], news, 8, 2, 128, 16, seed=step)
+    c.cache.scales[:, 0, :, :, 0] = 127
+    c.cache.codes[:, 0, :, :, :16] = 0
+    tokens = np.arange(900)
+    page, off = c.host_table[0, tokens // 16], tokens % 16
+    # a channel of the first block for each bit of the count of 16 tokens: 1 or 0 there, 2^bit in q
+    codes = np.zeros((900, 16), np.uint8)
+    for bit in range(6):
+        codes[:, bit] = np.where((tokens // 16) >> bit & 1, 0x02, 0)
+    c.cache.codes[torch.tensor(page), 0, :, torch.tensor(off), :16] = torch.tensor(codes, device="cuda")[:, None]
+    c.q *= 0.1
+    c.q[..., :32] = 0
+    for bit in range(6):
+        c.q[..., 2 * bit] = step * 2.0 ** bit * 128 ** 0.5 * 0.6931
+    _strict(c, *_forward(c))
