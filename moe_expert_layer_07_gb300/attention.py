@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from . import OUT_BF16, OUT_F32, _check, _I, _P, _stream, lib
+from . import DEV_BAD_INDEX, OUT_BF16, OUT_F32, _check, _I, _P, _stream, lib
 from .block import _OUT, NORM_RMS, _dense, block_norm, mx4_grouped_gemm, mx4_quantize, pack_mx4_weights
 
 ROPE_HALVES, ROPE_PAIRS = 0, 1
@@ -405,13 +405,21 @@ class PageTables:
         cache_tables(self.lengths, new_tokens, self.free_pages, self.free_range, self.page, self.table,
                      self.lengths, self.starts, self.slots, self.positions, self.free_range, self.status, stream)
 
-    def release(self, request, length):
-        """Gives the pages of a request that holds `length` tokens back; it holds none then.  On the
-        current stream, between steps."""
-        n = -(-length // self.page)
-        at = (self.free_range[1] + torch.arange(n, device=self.free_pages.device)) % self.free_pages.shape[0]
-        self.free_pages[at] = self.table[request, :n]
+    def release(self, request, length=None):
+        """Gives the pages of a request back; it holds none then.  On the current stream, between steps, without
+        waiting for it: the pages are those of lengths[request].  length: what the caller takes it to hold; a
+        number that is not as many pages sets DEV_BAD_INDEX in status."""
+        if not 0 <= request < self.lengths.shape[0]:
+            raise IndexError(f"request {request} of {self.lengths.shape[0]}")
+        ring = self.free_pages.shape[0]
+        i = torch.arange(min(ring, self.table.shape[1]), device=self.free_pages.device)
+        n = (self.lengths[request] + (self.page - 1)) // self.page
+        if i.shape[0]:
+            at = (self.free_range[1] + i) % ring
+            self.free_pages[at] = torch.where(i < n, self.table[request, :i.shape[0]], self.free_pages[at])
         self.free_range[1] += n
+        if length is not None:
+            self.status |= (n != -(-length // self.page)).int() * DEV_BAD_INDEX
         self.lengths[request] = 0
 
 
