@@ -164,10 +164,11 @@ def qk_norm_rope(qkv, positions, cos_sin, q_heads, kv_heads, q_out, k_out=None, 
     """Norm (with w_q, w_k) and rotation of each head's queries and keys; keys to k_out, or with the
     values to `slots` of the cache, or both.
 
-    qkv bf16 [T, at least (q_heads + 2 kv_heads) dim] with any row stride, positions int32 [T], cos_sin
+    qkv bf16 [T, at least (q_heads + 2 kv_heads) dim], rows a multiple of 8 elements apart, positions int32 [T], cos_sin
     fp32 [positions, rope_dim] as rope_table gives it (None: no rotation), q_out bf16 [T, q_heads, dim],
     k_out bf16 [T, kv_heads, dim], w_* [dim] fp32 or bf16, slots int32 [T] (-1: nowhere)."""
     T, dim = qkv.shape[0], q_out.shape[-1]
+    width = (q_heads + 2 * kv_heads) * dim
     rot = 0 if cos_sin is None else cos_sin.shape[-1]
     param = w_q if w_q is not None else w_k
     pkind = OUT_BF16 if param is None else _OUT.get(param.dtype)
@@ -175,7 +176,7 @@ def qk_norm_rope(qkv, positions, cos_sin, q_heads, kv_heads, q_out, k_out=None, 
     dev = qkv.get_device()
     good = (pkind is not None and qkv.dtype is _BF16 and q_out.dtype is _BF16 and dev >= 0
             and q_out.get_device() == dev and dev == _current_device() and qkv.dim() == 2 and qkv.stride(1) == 1
-            and qkv.shape[1] >= (q_heads + 2 * kv_heads) * dim
+            and qkv.shape[1] >= width
             and q_out.shape == (T, q_heads, dim) and q_out.is_contiguous() and (cache is None) == (slots is None))
     for w in (w_q, w_k):
         if w is not None:
@@ -193,7 +194,7 @@ def qk_norm_rope(qkv, positions, cos_sin, q_heads, kv_heads, q_out, k_out=None, 
                 and slots.is_contiguous() and cache.device == dev)
     if not good:
         _refuse_rope(qkv, positions, cos_sin, rot, q_heads, kv_heads, q_out, k_out, w_q, w_k, param, pkind, cache, slots)
-    stride = qkv.stride(0) if T > 1 else qkv.shape[1]
+    stride = qkv.stride(0) if T > 1 else width   # (of one row it says nothing)
     key = (q_heads, kv_heads, dim, rot, style, pkind, cos_sin.shape[0] if rot else 0, stride, eps)
     d = _ROPES.get(key)   # descriptions are plain values: made once each
     if d is None:
