@@ -176,7 +176,7 @@ def qk_norm_rope(qkv, positions, cos_sin, q_heads, kv_heads, q_out, k_out=None, 
     dev = qkv.get_device()
     good = (pkind is not None and qkv.dtype is _BF16 and q_out.dtype is _BF16 and dev >= 0
             and q_out.get_device() == dev and dev == _current_device() and qkv.dim() == 2 and qkv.stride(1) == 1
-            and qkv.shape[1] >= width
+            and qkv.shape[1] >= width and (T < 2 or qkv.stride(0) < 2 ** 31)
             and q_out.shape == (T, q_heads, dim) and q_out.is_contiguous() and (cache is None) == (slots is None))
     for w in (w_q, w_k):
         if w is not None:
@@ -230,6 +230,8 @@ def _refuse_rope(qkv, positions, cos_sin, rot, q_heads, kv_heads, q_out, k_out, 
         raise ValueError("cache and slots go together")
     if slots is not None:
         _typed(slots, _I32, (T,), "slots")
+    if T > 1 and qkv.dim() == 2 and qkv.stride(0) >= 2 ** 31:
+        raise ValueError(f"qkv: rows are {qkv.stride(0)} elements apart, and 2^31 - 1 at most may be")
     if qkv.is_cuda and qkv.dim() == 2 and qkv.stride(1) == 1 and qkv.shape[1] >= (q_heads + 2 * kv_heads) * dim:
         raise ValueError(_ELSEWHERE)
     raise ValueError(f"qkv: expected CUDA rows of {q_heads} + 2 x {kv_heads} heads of {dim}, got {tuple(qkv.shape)}")

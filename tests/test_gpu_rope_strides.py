@@ -1,4 +1,4 @@
-"""Norm and rotation of rows that lie in larger tensors: one row of any width."""
+"""Norm and rotation of rows that lie in larger tensors: one row of any width, rows more than 2^31 elements apart."""
 from __future__ import annotations
 
 import pytest
@@ -33,3 +33,11 @@ def test_one_row_of_any_width(lib, more):
     want = _call(rows[:, :256], 2)
     for got, w in zip(_call(rows[:1, :256 + more], 1), want):
         assert torch.equal(got, w[:1])
+
+
+def test_rows_further_apart_than_a_stride_can_say_are_refused(lib):
+    """2^32 + 256 elements: in 32 bits that would be 256, rows of another place."""
+    far = 2 ** 32 + 256
+    qkv = torch.empty(far + 256, dtype=BF, device="cuda").as_strided((2, 256), (far, 1))
+    with pytest.raises(ValueError):
+        _call(qkv, 2)
