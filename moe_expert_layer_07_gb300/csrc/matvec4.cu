@@ -510,18 +510,20 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
     cp_async_wait<0>();
 }
 
-// Clusters of c that run at a time on the current device (asked for once each).
-int clusters_at_once(const void *kern, const cudaLaunchConfig_t &c, int ranks) {
-    static std::atomic<int> known[64][9];
+// Clusters of c that run at a time on the current device: asked for once each kernel, size of a cluster
+// and number of warps, which also say how much shared memory there is.
+template <int KIND, int NQ, int S>
+int clusters_at_once(const cudaLaunchConfig_t &c, int ranks, int warps) {
+    static std::atomic<int> known[16][9][kMaxWarps + 1];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-    if ((n = known[dev][ranks].load(std::memory_order_relaxed)) == 0) {
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &c) != cudaSuccess || n < 1) {
-            cudaGetLastError();
-            return 1;
-        }
-        known[dev][ranks].store(n, std::memory_order_relaxed);
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 1;
+    std::atomic<int> *const place = dev < 16 ? &known[dev][ranks][warps] : nullptr;
+    if (place && (n = place->load(std::memory_order_relaxed)) != 0) return n;
+    if (cudaOccupancyMaxActiveClusters(&n, matvec4_kernel<KIND, NQ, S>, &c) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return 1;
     }
+    if (place) place->store(n, std::memory_order_relaxed);
     return n;
 }
 
@@ -553,7 +555,7 @@ int launch(const MatvecArgs &a, int ranks, cudaStream_t s) {
     const int tiles = (int)ceil_div(a.N, kTileRows);
     int clusters = std::max(1, sm_count() / ranks);
     c.gridDim = dim3((unsigned)(ranks * clusters));
-    if (ranks > 2) clusters = std::min(clusters, clusters_at_once(reinterpret_cast<const void *>(kern), c, ranks));
+    if (ranks > 2) clusters = std::min(clusters, clusters_at_once<KIND, NQ, S>(c, ranks, a.warps));
     c.gridDim = dim3((unsigned)(ranks * std::min(tiles, clusters)));
     const cudaError_t e = cudaLaunchKernelEx(&c, kern, (const MatvecArgs)a);
     return e == cudaSuccess ? MOE_OK : cuda_fail("cudaLaunchKernelEx", e);
