@@ -49,6 +49,8 @@
 namespace moe {
 namespace {
 
+using namespace ptx;
+
 constexpr int kThreads = kAttnWarps * 32;
 // What the beginning and end of a piece cost, in units: queries, the first tiles'
 // way from memory, the warps' sums.  Measured with 3, 4, 5, 6 and 8: 48 requests of 64
@@ -58,62 +60,7 @@ constexpr float kRest = 11.0f;     // where a raised maximum is put (log2)
 // Scale bytes with which every value is an fp16 number; others lie in bands of so many.
 constexpr int kLeastHalf = 104, kBand = 37;
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src))
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void ldm4(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldm4_trans(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ uint32_t transposed8(uint32_t v) {
-    uint32_t r;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-    return r;
-}
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// d = the product alone
-__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-}
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
-    const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// Scale of a value that is NaN, for a start: minus zero.
+// Mark of a value that is NaN.
 constexpr uint32_t kNan = 0x8000u;
 
 // Whether a row that sees a pair of tokens (seen: halves that are not zero) sees a value that is NaN.
@@ -232,8 +179,8 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
     float *s_top = s_mult + S::kRows, *s_sum = s_top + kAttnWarps * S::kRows;  // [warp][rows]
     int *s_first = reinterpret_cast<int *>(smem + S::kSmem);                 // [requests + 1]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    ptx::pdl_launch_dependents();
-    ptx::pdl_wait();
+    pdl_launch_dependents();
+    pdl_wait();
     plan_units(a, S::kRows, s_first, s_warp);
     // (as many units as a warp's tiles at a time: fewer take as long)
     const int all = s_first[a.B], per = max(S::kTiles, (all + (int)gridDim.x - 1) / (int)gridDim.x);
@@ -241,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 4 ? 1 : 2) attention4_kernel(c
     int u = min(all, (int)blockIdx.x * per);
     const int u_end = min(all, u + per);
     uint8_t *ring = smem + warp * S::kStages * S::kStage;
-    const uint32_t ring_addr = ptx::smem_u32(ring);
+    const uint32_t ring_addr = smem_u32(ring);
 
     // The pieces of the CTA's units, one after the other: request b, KV head h, row group
     // qt, units c0 .. c1-1 of `chunks`.  Found by a search once: the code of a search, and
@@ -760,8 +707,8 @@ __global__ void __launch_bounds__(256, 3) attention4_join_kernel(const AttnArgs 
     constexpr int V = D / 32;   // channels of a lane
     __shared__ float s_top[8][kJoinRows], s_sum[8][kJoinRows];
     __shared__ __align__(16) float s_o[8][kJoinRows][D];
-    ptx::pdl_launch_dependents();
-    ptx::pdl_wait();
+    pdl_launch_dependents();
+    pdl_wait();
     const int k0 = blockIdx.x, r0 = blockIdx.y * kJoinRows, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const AttnCut cut = a.cuts[k0];
     if (r0 >= cut.nrows) return;

@@ -77,22 +77,9 @@ struct WideArgs {
     int32_t *entry_request, *first_entry;   // [entries], [requests + 1]
 };
 
-__device__ __forceinline__ float ex2w(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 __device__ __forceinline__ uint32_t bf162_of(float lo, float hi) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&b);
-}
-__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
-    const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&h);
 }
 __device__ __forceinline__ uint32_t mul_bf162(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -103,7 +90,7 @@ __device__ __forceinline__ uint32_t mul_bf162(uint32_t a, uint32_t b) {
 // of the lowest three) and the sign goes back up, 2^12 + 7 2^12 = 2^15.
 __device__ __forceinline__ uint32_t bf16_of_half2(uint32_t h) {
     const uint32_t t = h >> 3;
-    return t + 7u * (t & 0x10001000u);   // (an e2m1 value has none of the lowest three bits)
+    return t + 7u * (t & 0x10001000u);
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -128,16 +115,6 @@ __device__ __forceinline__ void tmem_get8(uint32_t addr, uint32_t (&r)[8]) {
         : "memory");
 }
 using F2 = uint64_t;   // two fp32 numbers
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 // D[tmem] (+)= A[tmem] * B[smem]
 __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -343,7 +320,7 @@ __device__ __noinline__ RowState two_bf16(uint32_t ts, int upto, int from, uint3
     }
     if (top > r.pass) {
         const bool none = r.pass == -INFINITY;
-        const float rise = none ? ceilf(top) - kRest : fmaxf(ceilf(top) - kRest, 0.0f), f = none ? 1.0f : ex2w(-rise);
+        const float rise = none ? ceilf(top) - kRest : fmaxf(ceilf(top) - kRest, 0.0f), f = none ? 1.0f : ex2(-rise);
         r.pass = kAttnTop;
         r.ref += rise;
         r.sum *= f;
@@ -356,7 +333,7 @@ __device__ __noinline__ RowState two_bf16(uint32_t ts, int upto, int from, uint3
         sixteen(k, x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float p0 = ex2w(x[2 * i]), p1 = ex2w(x[2 * i + 1]);
+            const float p0 = ex2(x[2 * i]), p1 = ex2(x[2 * i + 1]);
             part = add2(part, pack2(__float_as_uint(p0), __float_as_uint(p1)));
             y[i] = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
             y[8 + i] = bf162_of(p0 - __uint_as_float(__float_as_uint(p0) & 0xffff0000u),
@@ -546,10 +523,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                     auto exponentials = [&]() {
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
-                            x[i] = ex2w(x[i]);
-                            x[i + 1] = ex2w(x[i + 1]);
+                            x[i] = ex2(x[i]);
+                            x[i + 1] = ex2(x[i + 1]);
                             more[i >> 1 & 1] = add2(more[i >> 1 & 1], pack2(__float_as_uint(x[i]), __float_as_uint(x[i + 1])));
-                            pk[i / 2] = half2_of(x[i], x[i + 1]);
+                            pk[i / 2] = half2_bits(x[i], x[i + 1]);
                         }
                     };
                     exponentials();
@@ -560,7 +537,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
                         const float rise = top == -INFINITY ? 0.0f : none ? ceilf(top) - kRest : fmaxf(ceilf(top) - kRest, 0.0f);
                         if (top != -INFINITY) pass = kAttnTop;
                         ref += rise;
-                        const float f = none ? 1.0f : ex2w(-rise);
+                        const float f = none ? 1.0f : ex2(-rise);
                         sum *= f;
                         shrink *= f;
 #pragma unroll
@@ -571,7 +548,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
 #pragma unroll 1
                         for (int times = 0; times < 3; ++times) {
                             const float part16 = fmaxf(left, 0x1p-14f);
-                            const uint32_t f2 = half2_of(part16, part16);
+                            const uint32_t f2 = half2_bits(part16, part16);
 #pragma unroll 1
                             for (int z = 0; z < 2 * q; ++z) {
                                 uint32_t y[8];
@@ -857,7 +834,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention4_wide_kernel(const 
 #pragma unroll
                 for (int i = 0; i < I; ++i)
                 {   // values: fp16 times 2^(e - 127), or unscaled where the tile's are bf16
-                    const uint32_t f = odd ? 0x3c003c00u : vb[i] == 255u ? 0u : half2_of(__uint_as_float(vb[i] << 23), __uint_as_float(vb[i] << 23));
+                    const uint32_t f = odd ? 0x3c003c00u : vb[i] == 255u ? 0u : half2_bits(__uint_as_float(vb[i] << 23), __uint_as_float(vb[i] << 23));
                     widen(vc[i], smem + S::kV + stage * S::kTileBytes, 32 * dw + kRoundRows * i + pr,
                           [&](uint32_t h) { return mul_half2(h, f); });
                 }

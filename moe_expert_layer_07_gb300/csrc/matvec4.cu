@@ -47,6 +47,8 @@
 namespace moe {
 namespace {
 
+using namespace ptx;
+
 constexpr int kMaxWarps = 16;
 constexpr int kTileRows = 16, kSlice = 128;
 constexpr int kItemBytes = kTileRows * kSlice / 2;
@@ -80,36 +82,6 @@ struct MatvecArgs {
     int scale_row, scale_words, zero_words;   // bytes of a row's scales; words of a strip
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src))
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void ldm4(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// d = the product alone
-__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
                  : "memory");
@@ -173,18 +145,18 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
     constexpr int kStage = stage_bytes(INT, S), kStrips = S * kItemBytes;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    const int rank = ptx::cluster_rank();
+    const int rank = cluster_rank();
     const int ranks = a.slices > a.per_cta ? (a.slices + a.per_cta - 1) / a.per_cta : 1;
     const int cluster = blockIdx.x / ranks, clusters = gridDim.x / ranks;
     const int first_slice = rank * a.per_cta + warp * S, last_slice = min(a.slices, (rank + 1) * a.per_cta);
     const int tiles = (a.N + kTileRows - 1) / kTileRows;
     const int mine = cluster < tiles ? (tiles - cluster + clusters - 1) / clusters : 0;
     uint8_t *ring = smem + warp * kStages * kStage;
-    const uint32_t ring_addr = ptx::smem_u32(ring);
+    const uint32_t ring_addr = smem_u32(ring);
     float *s_part = reinterpret_cast<float *>(smem + a.warps * kStages * kStage);   // [warps][kBatch][kSums]
     float *s_hold = s_part + a.warps * kBatch * kSums;                                // [ranks][hold_tiles][kSums]
     const int hold_tiles = (kHold + ranks - 1) / ranks, inv_ranks = 256 / ranks + 1;   // exact below kHold, to 8 ranks
-    const uint32_t hold = ptx::smem_u32(s_hold);
+    const uint32_t hold = smem_u32(s_hold);
     // MXFP4: [slice][row][block]
     float *s_scale = s_hold + (ranks > 1 ? ranks * hold_tiles * kSums : 0) + warp * (S * 64);
     const int row_bytes = a.K >> 1, groups = a.K >> a.group_shift;
@@ -282,8 +254,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
     };
     const IntBits bits;
     if (ranks > 1) cluster_arrive_relaxed();
-    ptx::pdl_launch_dependents();
-    ptx::pdl_wait();
+    pdl_launch_dependents();
+    pdl_wait();
     uint32_t xf[S][8][NQ][2];   // slices, steps of 16, rows of x
     float down[NQ][2];          // what undoes the powers of two of rows 8 n + 2 c, + 1
     uint4 all[NQ][S][4];        // before W: its copies would be waited for in line
@@ -488,7 +460,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
             for (int q = 0; q < a.warps; ++q) v += p[q * kBatch * kSums];
             const int at = it0 + slot, held = at % kHold, share = held * inv_ranks >> 8;   // held / ranks
             if (ranks > 1)   // to the CTA that adds them up
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(ptx::cluster_map(
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(
                                  hold + 4 * ((rank * hold_tiles + share) * kSums + j), held - share * ranks)), "f"(v) : "memory");
             else write(a, t, (cluster + at * clusters) * kTileRows + row, v);
         }
@@ -496,7 +468,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) matvec4_kernel(const Matvec
         if (ranks > 1 && (it % kHold == kHold - 1 || it == mine - 1)) {
             // the CTAs' sums together: CTA r finishes tiles r, r + ranks .. of what is held
             const int held = it % kHold + 1, base = it - it % kHold, own = (held - rank + ranks - 1) / ranks;
-            ptx::cluster_sync();
+            cluster_sync();
             for (int i = tid; i < own << (4 + a.t_shift); i += a.warps * 32) {
                 const int t = i & ((1 << a.t_shift) - 1), row = i >> a.t_shift & 15, slot = i >> (4 + a.t_shift);
                 const float *p = s_hold + slot * kSums + row * 8 * NQ + t;

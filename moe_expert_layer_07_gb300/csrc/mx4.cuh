@@ -6,6 +6,16 @@
 
 namespace moe {
 
+// Pairs of fp16 numbers as words.
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+    const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
 // Scale byte of a block from its largest magnitude's fp32 bits (as unsigned
 // integers, magnitudes order like their values, infinities and NaN on top).
 // A subnormal number's biased exponent is 0, below every exponent the clamp

@@ -52,11 +52,7 @@ using F2 = uint64_t;
 __device__ __forceinline__ F2 pair(float lo, float hi) { return ptx::pack2(__float_as_uint(lo), __float_as_uint(hi)); }
 __device__ __forceinline__ float lo2(F2 v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float hi2(F2 v) { return __uint_as_float((uint32_t)(v >> 32)); }
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
+using ptx::mul2;
 
 __device__ __forceinline__ uint2 load_once(const uint16_t *p) {
     uint2 v;
