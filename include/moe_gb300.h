@@ -641,21 +641,24 @@ MOE_API int moe_cache_read(const moe_cache4 *cache, int32_t n, const int32_t *sl
  *              sum_j exp(scale q . k_j)
  *   table      int32 [requests, max_pages]; lengths int32 [requests];
  *              starts int32 [requests + 1] (moe_cache_tables' outputs)
- * A row that sees nothing (its position is negative) gets zeros and an lse of
- * -infinity.  Rows outside every request are left as they were.  starts that
+ * A row that sees nothing (its position is negative), or only scores of -infinity,
+ * gets zeros and an lse of -infinity.  Rows outside every request are left as they were.  starts that
  * decrease or leave [0, rows], lengths outside [0, max_pages * page] and page
  * ids outside [0, pages) set MOE_DEV_BAD_INDEX: such a request is not computed,
  * the tokens of such a page are not seen.
  * Scores and sums are fp32; probabilities are rounded to fp16 before the sum of
  * the values: each is off by 2^-11 of itself at most, or by 2^-36 of the row's
- * largest where that is more (2^-30 where a request has more than 32 rows, of
- * query tokens times heads of a KV head).  Keys and values count whatever their size:
- * nothing that a row does not see changes its result.
- *   desc.max_q    the most query rows of one request, and
- *   desc.max_len  the longest request: what the kernels and the workspace are
- *                 chosen by; larger ones on the device are computed all the same,
- *                 unless their units of work (128 tokens by 8 rows and more) pass
- *                 2^30 / requests: MOE_DEV_BAD_INDEX, and not computed
+ * largest where that is more (2^-30 where max_q query tokens are more than 32
+ * rows, query tokens times heads of a KV head).  Keys and values count
+ * whatever their size, up to 2^95 (sums may overflow beyond; a key block whose scale byte is 0,
+ * 2^-127, may count as zero): nothing that a row does not see changes its result.
+ *   desc.max_q    the most query tokens of one request: what the kernels and the
+ *                 workspace are chosen by.  With more than 32 rows the kernels for
+ *                 many rows are launched too, also for a step that has none for them.
+ *                 Requests of more are computed all the same (slowly, where max_q says that
+ *                 there are few), unless their units of work (128 tokens by 8
+ *                 rows and more) pass 2^30 / requests: MOE_DEV_BAD_INDEX, and not computed
+ *   desc.max_len  the longest request; has to be 0 or more, nothing is chosen by it
  *   ws         moe_cache_attention_workspace_size bytes, 16-byte aligned; one call
  *              at a time; needs no initialisation
  * requests 0..4096, rows * q_heads below 2^31, q_heads a multiple of kv_heads. */
@@ -677,7 +680,8 @@ MOE_API int moe_cache_attention(const moe_cache_attn *d, const moe_cache4 *cache
  *   MOE_W4_INT  W[n, k] = scale[n, k/group] (code - zero[n, k/group]), codes 0..15
  *               (even k in the low four bits), scales bf16 or fp32 (scale_dtype),
  *               zero points uint8 0..15 or NULL (8); group 32, 64 or 128
- * fp32 accumulation.  x is taken as fp16 times a power of two for each row
+ * fp32 accumulation; weights up to 2^96 (sums may overflow beyond), scale byte 0 (2^-127)
+ * counts as zero.  x is taken as fp16 times a power of two for each row
  * (and part of K): each value is off by 2^-29 of a row's largest at most.  n_out up to 2^30, k_dim a multiple of
  * the group (of 32 for MXFP4), at most 32768; x and codes 16-byte aligned. */
 enum { MOE_W4_MX = 0, MOE_W4_INT = 1 };

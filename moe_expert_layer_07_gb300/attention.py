@@ -268,9 +268,11 @@ class CacheAttention:
     """Attention of up to `rows` query rows of up to `requests` requests over a cache, with the
     workspace that it needs (one call at a time).
 
-    max_q: the most query rows of one request, max_len: the longest request, max_pages: columns of
-    the page table (these choose kernels; max_q and max_len are no limits).  window: how many tokens a
-    query sees, itself included (0: all)."""
+    max_q: the most query tokens of one request, max_pages: columns of the page table; max_len: the longest
+    request (nothing is chosen by it).  max_q chooses the kernels and is no limit: where max_q tokens have
+    more than 32 rows (tokens times heads of a KV head) the kernels for many rows are launched in every call, and
+    without that requests of many rows take several times as long.  window: how many tokens a query sees,
+    itself included (0: all)."""
 
     def __init__(self, requests, rows, q_heads, cache: Cache4, max_pages, max_q=1, max_len=None, window=0,
                  scale=None):
@@ -434,7 +436,10 @@ class AttentionBlock:
     w_qkv, w_o: MXFP4 (codes [N, K/2], scale bytes [N, K/32], row-major, as mx4_quantize gives them) of
     [(q_heads + 2 kv_heads) dim, hidden] and [hidden, q_heads dim].  Up to 16 rows are multiplied in bf16
     (w4_matvec); more, a prompt's, are quantised to MXFP4 themselves (mx4_grouped_gemm on packed
-    copies, made where max_rows is more than 16: both sizes then multiples of 128).  One call at a time."""
+    copies, made where max_rows is more than 16: both sizes then multiples of 128): from 17 rows on
+    projections carry the error of four bits on both sides.  max_q: the most tokens that one request gets in
+    any step, one choice for all of them (CacheAttention): max_rows for prompts, 1 where the block only decodes.
+    One call at a time."""
 
     def __init__(self, cache: Cache4, q_heads, hidden, w_qkv, w_o, cos_sin, requests, max_rows, max_pages, max_q=1,
                  max_len=None, w_q=None, w_k=None, w_pre=None, w_post=None, gate=None, residual_scale=1.0,

@@ -31,9 +31,9 @@
 // the requests' lengths.  A request that is cut between CTAs leaves partial
 // results in the workspace (at most two a CTA), which a second kernel joins.
 //
-// Measured (cold): 48 requests of 64 to 16384 tokens, 64 query heads on 8 of 128, 58.4 us (3.8 TB/s
-// of the cache); two of 131073 with three query tokens, 40 heads on 8, 97.6 (2.9 TB/s); one of
-// 4097 tokens 11.2, two thirds of it launches, the way to the first tokens and the join.
+// Measured (cold): 48 requests of 64 to 16384 tokens, 64 query heads on 8 of 128, 61.1 us (3.7 TB/s
+// of the cache; 58.4 with the scales times P); two of 131073 with three query tokens, 40 heads on 8, 94.5 (3.0
+// TB/s; 97.6); one of 4097 tokens 11.1, two thirds of it launches, the way to the first tokens and the join.
 // What bounds the large ones is the unpacking: 370 instructions a warp for 16 tokens
 // of 128 channels, three quarters of what an SM can issue while it streams (one CTA of an SM
 // is as fast alone as two are together), half of it on the integer pipe, which converts.
@@ -53,7 +53,7 @@ using namespace ptx;
 
 constexpr int kThreads = kAttnWarps * 32;
 // What the beginning and end of a piece cost, in units: queries, the first tiles'
-// way from memory, the warps' sums.  Measured with 3, 4, 5, 6 and 8: 48 requests of 64
+// way from memory, the warps' sums.  Measured with 3, 4, 5, 6 and 8 (the scales still times P): 48 requests of 64
 // to 16384 tokens 63.9, 58.4, 58.7, 60.0 and 62.0 us.
 constexpr int kPieceUnits = 4;
 constexpr float kRest = 11.0f;     // where a raised maximum is put (log2)
@@ -820,8 +820,8 @@ __global__ void __launch_bounds__(256, 3) attention4_join_kernel(const AttnArgs 
 
 // Requests of at most this many rows are this file's where the call also has larger
 // ones: up to there rows share a read of the cache here, and the other kernel's tiles
-// would be a quarter full.  (16 requests of 4096 tokens, 64 query heads on 8: 32 rows 60 us
-// here; 40 rows 103 here, 82 there; 128 rows 195 and 87.)
+// would be a quarter full.  (16 requests of 4096 tokens, 64 query heads on 8, cold, in a
+// graph: 32 rows 65 us here; 40 rows 107 here, 97 there; 128 rows 196 and 104.)
 constexpr int kFewRows = 32;
 
 int64_t most_rows(const moe_cache_attn *d, const moe_cache4 *cache) {

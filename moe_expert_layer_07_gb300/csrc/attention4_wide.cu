@@ -26,9 +26,11 @@
 // results, at most two groups a CTA, which a last kernel joins.
 //
 // Three prompts' chunks of 500 to 4096 tokens onto caches of up to 8192, 64 query
-// heads on 8 of 128: 1170 us, 1.03 PFLOP/s, 54% of what a large library product
-// reaches.  What bounds it is the way from one half's S to its P (four rounds of load,
-// exponentials, conversion, store: 2500 cycles, then 1400 of waiting for the next S)
+// heads on 8 of 128: 1242 us, 0.97 PFLOP/s, 51% of what a large library product
+// reaches.  (1170 with keys and values relative to the largest of a tile and a piece: keys as bf16 cost 30 us, the
+// second way for values and what P keeps where m rises 40, most of that by where code and registers
+// then lie.)  What bounds it is the way from one half's S to its P (four rounds of load,
+// exponentials, conversion, store: some 2500 cycles, then 1400 of waiting for the next S)
 // against 1024 cycles of the other half's products: tensor
 // memory is full (two S of 128 columns, two O), so there is no third tile to work on
 // meanwhile.  (P in shared memory would free S sooner, but with both operands there
@@ -45,7 +47,6 @@
 
 #include <algorithm>
 #include <climits>
-#include <type_traits>
 
 #include "attention4.cuh"
 #include "mx4.cuh"
