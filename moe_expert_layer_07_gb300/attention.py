@@ -486,14 +486,19 @@ class AttentionBlock:
 
     def forward(self, residual, x, y, tables: PageTables, w_next=None, x_next=None, stream=None):
         """residual fp32 or bf16 [T, hidden], updated in place; x bf16 [T, hidden] the normed input; y
-        bf16 [T, hidden] is scratch; tables: of this step, with at most T token rows (rows behind the
-        last token go nowhere; what their outputs hold means nothing).  With w_next the next block's
+        bf16 [T, hidden] is scratch; tables: of this step, for a cache of the same page size, with at most T
+        token rows (rows behind the last token go nowhere; what their outputs hold means nothing).  With w_next the next block's
         norm is part of the last pass, into x_next (may be x)."""
         T = x.shape[0]
         if T > self.max_rows:
             raise ValueError(f"{T} rows, and buffers for {self.max_rows}")
         if tables.slots.shape[0] < T:
             raise ValueError(f"{T} rows, and tables for {tables.slots.shape[0]}")
+        if tables.page != self.cache.page:
+            raise ValueError(f"a cache in pages of {self.cache.page}, and tables of pages of {tables.page}")
+        if tables.table.shape != (self.plan.d.requests, self.plan.d.max_pages):
+            raise ValueError(f"tables of {tuple(tables.table.shape)} requests and pages, and a block for "
+                             f"{(self.plan.d.requests, self.plan.d.max_pages)}")
         plan = self._plans.get(T)
         if plan is None:
             plan = self._plans[T] = self.plan.of_rows(T)

@@ -1,5 +1,8 @@
-"""PageTables.release: pages go back to the ring once each, as many as the request holds on the device."""
+"""PageTables.release: pages go back to the ring once each, as many as the request holds on the device.
+AttentionBlock takes tables of its own cache's form only."""
 from __future__ import annotations
+
+from types import SimpleNamespace as Some
 
 import pytest
 import torch
@@ -59,3 +62,16 @@ def test_a_request_that_is_none(request_):
     with pytest.raises(IndexError):
         t.release(request_, 20)
     assert t.lengths.tolist() == [33, 20] and t.free_range.tolist() == [0, 3]
+
+
+@pytest.mark.parametrize("page,requests,columns", [(32, 2, 4), (16, 3, 4), (16, 2, 5)])
+def test_a_block_refuses_tables_of_another_form(page, requests, columns):
+    """Before anything is computed or written: slots of other pages would be other tokens' places."""
+    block = moe.AttentionBlock.__new__(moe.AttentionBlock)
+    block.max_rows, block.cache = 8, Some(page=16)
+    block.plan = Some(d=Some(requests=2, max_pages=4), of_rows=lambda rows: pytest.fail("went on"))
+    block._plans = {}
+    tables = _tables([1] * requests, [[0] * columns] * requests, [1], [0, 1], page=page)
+    tables.slots = torch.zeros(8, dtype=I32)
+    with pytest.raises(ValueError):
+        block.forward(None, torch.zeros(1, 4), None, tables)
