@@ -597,7 +597,8 @@ MOE_API int moe_cache_tables(int32_t requests, int32_t page, const int32_t *held
  *   MOE_ROPE_PAIRS   channels 2i and 2i + 1
  *   a, b -> a cos_i - b sin_i, b cos_i + a sin_i
  * fp32 from load to store, each output rounded once; cached keys have the codes
- * of exact values (as fp64 would give them).
+ * of exact values (as fp64 would give them; sums of squares are fp32 numbers all
+ * the same, values of 2^60 and more may pass them).
  *   qkv         bf16 [T, qkv_stride]: q_heads, then kv_heads of keys, then
  *               kv_heads of values, `dim` channels each (dim 64 or 128;
  *               qkv_stride a multiple of 8)
